@@ -72,8 +72,15 @@ typedef enum {
 typedef enum {
   W4_OP_W4A8 = 0,           /* w4a8_gemm and w4a8_group_partials */
   W4_OP_W4AFP8_MOE = 1,     /* w4afp8_moe_grouped_gemm, w4afp8_moe_gemm_bf16in (M = R, the row count) */
-  W4_OP_MOE_ROUTE = 2       /* w4_moe_route (M = T tokens, N = E experts; K = 1, group ignored) */
+  W4_OP_MOE_ROUTE = 2,      /* w4_moe_route, w4_moe_route_grouped (M = T tokens, N = E experts; K = 1, group ignored) */
+  W4_OP_FP8_BLOCK = 3       /* w4_fp8_block_gemm_bf16in, w4_fp8_block_moe_gemm_bf16in (M = rows; N, group ignored) */
 } w4_op;
+
+/* Router scores of w4_moe_route_grouped. */
+typedef enum {
+  W4_SCORE_SIGMOID = 0,
+  W4_SCORE_SOFTMAX = 1
+} w4_scoring;
 
 /*
  * Bytes of device workspace an operation needs for M activation rows of
@@ -212,8 +219,8 @@ w4_status w4a8_gemm_bf16in(const void* x, const void* qweight, const void* w_sca
  * x or the bias, or writes y). So qweight, w_scale and zeros must not be
  * written by a kernel that runs immediately before on the same stream and
  * signals its dependents early; kernels that do not (every kernel of this
- * library except this one, and ordinary library kernels) are waited for in
- * full.
+ * library except this one and the per-block quantizers, and ordinary library
+ * kernels) are waited for in full.
  */
 w4_status w4a16_gemm(const void* x, const void* qweight, const void* w_scale, int32_t w_scale_dtype,
                      const void* zeros, int32_t group, const void* bias, void* y,
@@ -341,6 +348,115 @@ w4_status w4_moe_silu_mul_quant_fp8(const void* h, int64_t R, int64_t I, void* q
  */
 w4_status w4_moe_combine(const void* y, int64_t R, int64_t H, const float* topk_weights, const int32_t* row_of,
                          int64_t T, int32_t top_k, void* out, void* stream);
+
+/*
+ * w4_moe_route_grouped: routing with sigmoid or softmax scores, a balance bias
+ * and expert groups. Outputs, layouts and workspace as w4_moe_route, so every
+ * expert entry point takes its row order.
+ *
+ *   score[e]  sigmoid(logit) or softmax over all E experts (scoring)
+ *   key[e]    what the choice goes by: the logit itself (bias NULL), or
+ *             fl(score[e] + bias[e]) with bias fp32 [E]
+ *   groups    E / n_group consecutive experts each; a group's value is its
+ *             largest key (bias NULL), or the sum of its two largest keys (of
+ *             its one key, for groups of one). The topk_group best groups stay
+ *             open, equal values in ascending group order.
+ *   choice    the top_k largest keys of the open groups, largest first, equal
+ *             keys in ascending expert order
+ *   weight    score (without the bias), divided by the sum of the chosen
+ *             scores when renormalize != 0, times scale
+ * All in fp32. The steps a choice depends on are fixed: sigmoid is
+ * fl(1 / fl(1 + exp(-l))), and with a bias the softmax denominator is summed in
+ * fp64 and rounded once.
+ *
+ * 1 <= E <= 1024; n_group divides E (W4_ERR_GROUP), at most 32
+ * (W4_ERR_UNSUPPORTED); 1 <= topk_group <= n_group; 1 <= top_k <= min(64,
+ * topk_group * E / n_group). A logit of -inf scores 0 (a masked expert; it can
+ * still be chosen when nothing else is open). Where the chosen scores sum to 0,
+ * as in a row that is masked altogether, renormalized weights are 0. NaN logits
+ * count as -inf, +inf as the largest finite fp32. T == 0 launches nothing.
+ */
+w4_status w4_moe_route_grouped(const void* logits, int32_t logits_f32, const float* bias, int64_t T, int32_t E,
+                               int32_t top_k, int32_t n_group, int32_t topk_group, int32_t scoring,
+                               int32_t renormalize, float scale, int32_t* topk_ids, float* topk_weights,
+                               int32_t* offsets, int32_t* row_token, int32_t* row_of, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/*
+ * The fp8 block-scaled layer: e4m3 weights with one fp32 scale per 128 x 128
+ * block, e4m3 activations with one fp32 scale per token and 128 columns. [FP8]
+ * (W4AFP8Config) keeps every layer of the checkpoint but the routed experts in
+ * this form ("weight" e4m3 [N, K], "weight_scale_inv" [ceil(N/128),
+ * ceil(K/128)], dynamic activations); checkpoints whose experts were not
+ * converted to int4 keep those in it too.
+ *
+ * w4_quant_act_per_block: per row and block of 128 columns (the last one may be
+ * shorter) amax = max |x|, s = amax / 448 in fp32 (1 where amax is 0),
+ * q = e4m3(fl(x / s)), round to nearest even, saturating; the divides are IEEE.
+ *   x [M, K] bf16 or fp16 (x_dtype), 16-byte aligned; K % 8 == 0
+ *   q [M, K] e4m3 codes, 16-byte aligned; scale [M, ceil(K/128)] fp32
+ * May signal its programmatic dependents early (see w4a16_gemm).
+ */
+w4_status w4_quant_act_per_block(const void* x, int32_t x_dtype, int64_t M, int64_t K, void* q, float* scale,
+                                 void* stream);
+
+/*
+ * w4_silu_mul_quant_block: h [R, 2I] bf16 (gate columns first) -> the codes and
+ * scales of silu(gate) * up, quantized as by w4_quant_act_per_block. The product
+ * stays in fp32 up to its rounding to e4m3. q [R, I], scale [R, ceil(I/128)];
+ * I % 8 == 0; h and q 16-byte aligned.
+ */
+w4_status w4_silu_mul_quant_block(const void* h, int64_t R, int64_t I, void* q, float* scale, void* stream);
+
+/*
+ * w4_fp8_block_gemm:
+ *   y[m, n] = bf16( sum_b x_scale[m, b] * w_scale[n / 128, b] * P[m, b, n] + bias[n] ),
+ *   P[m, b, n] = sum over the 128 columns k of block b of qx[m, k] * qweight[n, k],
+ * everything after the e4m3 codes in fp32.
+ *   qx       [M, K] e4m3 codes        x_scale [M, ceil(K/128)] fp32
+ *   qweight  [N, K] e4m3 codes        w_scale [ceil(N/128), ceil(K/128)] fp32
+ *   bias     [N] bf16 or NULL         y       [M, N] bf16
+ * N % 8 == 0, K % 16 == 0 (a K that is a multiple of 8 only: W4_ERR_UNSUPPORTED);
+ * neither has to be a multiple of 128. Matrices and the bias are 16-byte aligned. Few
+ * rows take a form that streams the weights once for all of them; M == 1 is
+ * the decode call. Outputs do not depend on the number of SMs' timing: sums
+ * are taken in a fixed order.
+ */
+w4_status w4_fp8_block_gemm(const void* qx, const float* x_scale, const void* qweight, const float* w_scale,
+                            const void* bias, void* y, int64_t M, int64_t N, int64_t K, void* stream);
+
+/*
+ * w4_fp8_block_gemm_bf16in: w4_quant_act_per_block and w4_fp8_block_gemm in one
+ * call: x [M, K] bf16 or fp16 (x_dtype), its codes and scales in the workspace
+ * (at least w4_workspace_bytes(W4_OP_FP8_BLOCK, M, N, K, 0) bytes, 16-byte
+ * aligned). y equals the two calls' bit for bit. The product's weights start
+ * streaming while x is being quantized.
+ */
+w4_status w4_fp8_block_gemm_bf16in(const void* x, int32_t x_dtype, const void* qweight, const float* w_scale,
+                                   const void* bias, void* y, int64_t M, int64_t N, int64_t K, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/*
+ * w4_fp8_block_moe_grouped_gemm: the same product over expert-sorted rows, as
+ * w4afp8_moe_grouped_gemm takes them: rows [offsets[e], offsets[e+1]) of qx
+ * [R, K] times expert e of qweight [E, N, K], w_scale [E, ceil(N/128),
+ * ceil(K/128)] fp32; y [R, N] bf16. 1 <= E <= 1024. Offsets live on the device
+ * and are not validated; rows outside [0, R) are neither read nor written.
+ */
+w4_status w4_fp8_block_moe_grouped_gemm(const void* qx, const float* x_scale, const int32_t* expert_offsets, int32_t E,
+                                        const void* qweight, const float* w_scale, void* y, int64_t R, int64_t N,
+                                        int64_t K, void* stream);
+
+/*
+ * w4_fp8_block_moe_gemm_bf16in: row r is token row_token[r] of x [T, K] bf16
+ * (row_token NULL: R == T and row r is token r), quantized per block into the
+ * workspace (at least w4_workspace_bytes(W4_OP_FP8_BLOCK, R, N, K, 0) bytes),
+ * then w4_fp8_block_moe_grouped_gemm. A row_token entry outside [0, T) gives a
+ * zero row and sets W4_ERR_SHAPE in the device status word.
+ */
+w4_status w4_fp8_block_moe_gemm_bf16in(const void* x, int64_t T, const int32_t* row_token, const int32_t* expert_offsets,
+                                       int32_t E, const void* qweight, const float* w_scale, void* y, int64_t R,
+                                       int64_t N, int64_t K, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Weight-side tools (load time, not on the per-token path).

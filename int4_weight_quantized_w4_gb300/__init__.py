@@ -21,22 +21,26 @@ __all__ = [
     "w4a16_gemm_host", "w4afp8_moe_grouped_gemm", "w4_quantize_groupwise", "w4_repack_s4_to_uint4b8",
     "w4_embedding_gather", "w4_lm_head_gemv",
     "w4_moe_route", "w4_moe_gather_quant_fp8", "w4afp8_moe_gemm_bf16in", "w4_moe_silu_mul_quant_fp8",
-    "w4_moe_combine",
+    "w4_moe_combine", "w4_moe_route_grouped",
+    "w4_quant_act_per_block", "w4_silu_mul_quant_block", "w4_fp8_block_gemm", "w4_fp8_block_gemm_bf16in",
+    "w4_fp8_block_moe_grouped_gemm", "w4_fp8_block_moe_gemm_bf16in",
     "w4_device_status", "w4_selftest_bounded_wait", "apply_weights", "MIN_TOKENS_FOR_INT8",
     "W4_OK", "W4_ERR_NULL", "W4_ERR_ALIGN", "W4_ERR_GROUP", "W4_ERR_DTYPE",
     "W4_ERR_UNSUPPORTED", "W4_ERR_SHAPE", "W4_ERR_CUDA", "W4_ERR_TIMEOUT", "W4_ERR_WORKSPACE",
-    "W4_OP_W4A8", "W4_OP_W4AFP8_MOE", "W4_OP_MOE_ROUTE", "w4_workspace_bytes", "EXPORTED_SYMBOLS",
+    "W4_OP_W4A8", "W4_OP_W4AFP8_MOE", "W4_OP_MOE_ROUTE", "W4_OP_FP8_BLOCK", "w4_workspace_bytes", "EXPORTED_SYMBOLS",
 ]
 
 (W4_OK, W4_ERR_NULL, W4_ERR_ALIGN, W4_ERR_GROUP, W4_ERR_DTYPE, W4_ERR_UNSUPPORTED,
  W4_ERR_SHAPE, W4_ERR_CUDA, W4_ERR_TIMEOUT, W4_ERR_WORKSPACE) = range(10)
 W4_BF16, W4_FP16, W4_INT8, W4_FP8_E4M3 = range(4)
-W4_OP_W4A8, W4_OP_W4AFP8_MOE, W4_OP_MOE_ROUTE = range(3)
+W4_OP_W4A8, W4_OP_W4AFP8_MOE, W4_OP_MOE_ROUTE, W4_OP_FP8_BLOCK = range(4)
+W4_SCORE_SIGMOID, W4_SCORE_SOFTMAX = range(2)
 
 _DIR = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_DIR, "libw4.so")
 
 _P, _I32, _I64, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+_F = ctypes.c_float
 # name -> (restype, argtypes); mirrors include/w4.h
 _SIGNATURES = {
     "w4_quant_act_per_token": (_I32, [_P, _I32, _I64, _I64, _I32, _P, _P, _P]),
@@ -58,6 +62,14 @@ _SIGNATURES = {
                                       _P]),
     "w4_moe_silu_mul_quant_fp8": (_I32, [_P, _I64, _I64, _P, _P, _P, _P]),
     "w4_moe_combine": (_I32, [_P, _I64, _I64, _P, _P, _I64, _I32, _P, _P]),
+    "w4_moe_route_grouped": (_I32, [_P, _I32, _P, _I64, _I32, _I32, _I32, _I32, _I32, _I32, _F, _P, _P, _P, _P, _P, _P,
+                                    _SZ, _P]),
+    "w4_quant_act_per_block": (_I32, [_P, _I32, _I64, _I64, _P, _P, _P]),
+    "w4_silu_mul_quant_block": (_I32, [_P, _I64, _I64, _P, _P, _P]),
+    "w4_fp8_block_gemm": (_I32, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P]),
+    "w4_fp8_block_gemm_bf16in": (_I32, [_P, _I32, _P, _P, _P, _P, _I64, _I64, _I64, _P, _SZ, _P]),
+    "w4_fp8_block_moe_grouped_gemm": (_I32, [_P, _P, _P, _I32, _P, _P, _P, _I64, _I64, _I64, _P]),
+    "w4_fp8_block_moe_gemm_bf16in": (_I32, [_P, _I64, _P, _P, _I32, _P, _P, _P, _I64, _I64, _I64, _P, _SZ, _P]),
     "w4_last_error": (ctypes.c_char_p, []),
     "w4_status_string": (ctypes.c_char_p, [_I32]),
     "w4_device_status": (_I32, [_P]),
@@ -368,6 +380,173 @@ def w4_moe_route(logits, top_k: int, renormalize: bool = False, out=None, worksp
                                _ptr(ids), _ptr(wts), _ptr(off), _ptr(rt), _ptr(ro), _ptr(ws), wsb,
                                _stream(stream, dev)), "w4_moe_route")
     return out
+
+
+_SCORING = {"sigmoid": W4_SCORE_SIGMOID, "softmax": W4_SCORE_SOFTMAX}
+
+
+def w4_moe_route_grouped(logits, top_k: int, bias=None, n_group: int = 1, topk_group: int = 1,
+                         scoring: str = "sigmoid", renormalize: bool = True, scale: float = 1.0, out=None,
+                         workspace=None, stream=None):
+    """Top-k routing of router ``logits [T, E]`` (bf16 or fp32) with sigmoid or
+    softmax scores, an optional fp32 balance ``bias [E]`` that only moves the
+    choice, and the choice limited to the best ``topk_group`` of ``n_group``
+    groups of consecutive experts. Weights are the scores, renormalized over the
+    chosen if asked, times ``scale``. Returns (and takes as ``out``) the tuple of
+    ``w4_moe_route``: ``(topk_ids, topk_weights, offsets, row_token, row_of)``."""
+    _cuda2d(logits, "logits", (torch.bfloat16, torch.float32))
+    if scoring not in _SCORING:
+        raise ValueError("scoring must be 'sigmoid' or 'softmax'")
+    T, E = logits.shape
+    dev = logits.device
+    _expect(bias, "bias", (E,), _F32, dev, optional=True)
+    if out is None:
+        out = (torch.empty((T, top_k), dtype=torch.int32, device=dev),
+               torch.empty((T, top_k), dtype=torch.float32, device=dev),
+               (torch.empty if T else torch.zeros)((E + 1,), dtype=torch.int32, device=dev),
+               torch.empty((T * top_k,), dtype=torch.int32, device=dev),
+               torch.empty((T, top_k), dtype=torch.int32, device=dev))
+    ids, wts, off, rt, ro = out
+    _expect(ids, "topk_ids", (T, top_k), _I32T, dev)
+    _expect(wts, "topk_weights", (T, top_k), _F32, dev)
+    _expect(off, "offsets", (E + 1,), _I32T, dev)
+    _expect(rt, "row_token", (T * top_k,), _I32T, dev)
+    _expect(ro, "row_of", (T, top_k), _I32T, dev)
+    ws, wsb = _workspace(workspace, W4_OP_MOE_ROUTE, T, E, 1, 0, dev)
+    _check(load().w4_moe_route_grouped(_ptr(logits), int(logits.dtype == torch.float32), _ptr(bias), T, E, top_k,
+                                       n_group, topk_group, _SCORING[scoring], int(bool(renormalize)), scale,
+                                       _ptr(ids), _ptr(wts), _ptr(off), _ptr(rt), _ptr(ro), _ptr(ws), wsb,
+                                       _stream(stream, dev)), "w4_moe_route_grouped")
+    return out
+
+
+def w4_quant_act_per_block(x, q=None, scale=None, stream=None):
+    """e4m3 quantization of bf16 or fp16 ``x [M, K]`` with one scale per row and
+    128 columns; returns ``(q float8_e4m3fn [M, K], scale fp32 [M, ceil(K/128)])``."""
+    _cuda2d(x, "x", (torch.bfloat16, torch.float16))
+    M, K = x.shape
+    q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=x.device) if q is None else q
+    scale = torch.empty((M, _blocks(K)), dtype=torch.float32, device=x.device) if scale is None else scale
+    _expect(q, "q", (M, K), _FP8_T, x.device)
+    _expect(scale, "scale", (M, _blocks(K)), _F32, x.device)
+    _check(load().w4_quant_act_per_block(_ptr(x), _act_dtype(x), M, K, _ptr(q), _ptr(scale),
+                                         _stream(stream, x.device)), "w4_quant_act_per_block")
+    return q, scale
+
+
+def w4_silu_mul_quant_block(h, q=None, scale=None, stream=None):
+    """``silu(gate) * up`` of the bf16 gate_up output ``h [R, 2I]``, quantized to
+    e4m3 per row and 128 columns; returns ``(q [R, I], scale [R, ceil(I/128)])``."""
+    _cuda2d(h, "h", (torch.bfloat16,))
+    R, I2 = h.shape
+    if I2 % 2:
+        raise ValueError("h must hold gate and up halves of equal width")
+    I = I2 // 2
+    q = torch.empty((R, I), dtype=torch.float8_e4m3fn, device=h.device) if q is None else q
+    scale = torch.empty((R, _blocks(I)), dtype=torch.float32, device=h.device) if scale is None else scale
+    _expect(q, "q", (R, I), _FP8_T, h.device)
+    _expect(scale, "scale", (R, _blocks(I)), _F32, h.device)
+    _check(load().w4_silu_mul_quant_block(_ptr(h), R, I, _ptr(q), _ptr(scale), _stream(stream, h.device)),
+           "w4_silu_mul_quant_block")
+    return q, scale
+
+
+def _blocks(n):
+    return (n + 127) // 128
+
+
+def _act_dtype(x):
+    return W4_FP16 if x.dtype == torch.float16 else W4_BF16
+
+
+def _block_weight_args(what, qweight, w_scale, K, device, bias=None):
+    """e4m3 ``qweight [N, K]`` (float8_e4m3fn or uint8 codes) with fp32 ``w_scale
+    [ceil(N/128), ceil(K/128)]`` and optional bf16 ``bias [N]``; returns N."""
+    _cuda2d(qweight, "qweight", _FP8_T)
+    N = qweight.shape[0]
+    if qweight.shape[1] != K:
+        raise ValueError(f"inconsistent shapes for {what}")
+    _expect(qweight, "qweight", None, None, device)
+    _expect(w_scale, "w_scale", (_blocks(N), _blocks(K)), _F32, device)
+    _expect(bias, "bias", (N,), _BF16T, device, optional=True)
+    return N
+
+
+def _block_expert_args(what, qweight, w_scale, expert_offsets, K, device):
+    """e4m3 ``qweight [E, N, K]``, fp32 ``w_scale [E, ceil(N/128), ceil(K/128)]``
+    and int32 ``expert_offsets [E + 1]``; returns (E, N)."""
+    _expect(qweight, "qweight", None, _FP8_T, device)
+    if qweight.dim() != 3 or qweight.shape[2] != K:
+        raise ValueError(f"inconsistent shapes for {what}")
+    E, N = qweight.shape[0], qweight.shape[1]
+    _expect(w_scale, "w_scale", (E, _blocks(N), _blocks(K)), _F32, device)
+    _expect(expert_offsets, "expert_offsets", (E + 1,), _I32T, device)
+    return E, N
+
+
+def w4_fp8_block_gemm(qx, x_scale, qweight, w_scale, bias=None, y=None, stream=None):
+    """fp8 block-scaled linear: e4m3 ``qx [M, K]`` with fp32 ``x_scale [M,
+    ceil(K/128)]`` (from ``w4_quant_act_per_block``) times e4m3 ``qweight [N, K]``
+    with fp32 ``w_scale [ceil(N/128), ceil(K/128)]``; returns bf16 ``[M, N]``."""
+    _cuda2d(qx, "qx", _FP8_T)
+    M, K = qx.shape
+    N = _block_weight_args("w4_fp8_block_gemm", qweight, w_scale, K, qx.device, bias)
+    _expect(x_scale, "x_scale", (M, _blocks(K)), _F32, qx.device)
+    y = torch.empty((M, N), dtype=torch.bfloat16, device=qx.device) if y is None else y
+    _expect(y, "y", (M, N), _BF16T, qx.device)
+    _check(load().w4_fp8_block_gemm(_ptr(qx), _ptr(x_scale), _ptr(qweight), _ptr(w_scale), _ptr(bias), _ptr(y), M, N, K,
+                                    _stream(stream, qx.device)), "w4_fp8_block_gemm")
+    return y
+
+
+def w4_fp8_block_gemm_bf16in(x, qweight, w_scale, bias=None, y=None, workspace=None, stream=None):
+    """fp8 block-scaled linear from bf16 or fp16 ``x [M, K]``, quantized per block
+    inside the call; returns bf16 ``[M, N]``. One token is the decode call."""
+    _cuda2d(x, "x", (torch.bfloat16, torch.float16))
+    M, K = x.shape
+    N = _block_weight_args("w4_fp8_block_gemm_bf16in", qweight, w_scale, K, x.device, bias)
+    y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device) if y is None else y
+    _expect(y, "y", (M, N), _BF16T, x.device)
+    ws, wsb = _workspace(workspace, W4_OP_FP8_BLOCK, M, N, K, 0, x.device)
+    _check(load().w4_fp8_block_gemm_bf16in(_ptr(x), _act_dtype(x), _ptr(qweight), _ptr(w_scale), _ptr(bias), _ptr(y),
+                                           M, N, K, _ptr(ws), wsb, _stream(stream, x.device)),
+           "w4_fp8_block_gemm_bf16in")
+    return y
+
+
+def w4_fp8_block_moe_grouped_gemm(qx, x_scale, expert_offsets, qweight, w_scale, y=None, stream=None):
+    """Grouped expert linear on fp8 block-scaled weights: e4m3 ``qx [R, K]`` (rows
+    grouped by expert) with fp32 ``x_scale [R, ceil(K/128)]``, int32 device
+    ``expert_offsets [E+1]``, e4m3 ``qweight [E, N, K]``, fp32 ``w_scale [E,
+    ceil(N/128), ceil(K/128)]``; returns bf16 ``[R, N]``."""
+    _cuda2d(qx, "qx", _FP8_T)
+    R, K = qx.shape
+    E, N = _block_expert_args("w4_fp8_block_moe_grouped_gemm", qweight, w_scale, expert_offsets, K, qx.device)
+    _expect(x_scale, "x_scale", (R, _blocks(K)), _F32, qx.device)
+    y = torch.empty((R, N), dtype=torch.bfloat16, device=qx.device) if y is None else y
+    _expect(y, "y", (R, N), _BF16T, qx.device)
+    _check(load().w4_fp8_block_moe_grouped_gemm(_ptr(qx), _ptr(x_scale), _ptr(expert_offsets), E, _ptr(qweight),
+                                                _ptr(w_scale), _ptr(y), R, N, K, _stream(stream, qx.device)),
+           "w4_fp8_block_moe_grouped_gemm")
+    return y
+
+
+def w4_fp8_block_moe_gemm_bf16in(x, row_token, expert_offsets, qweight, w_scale, y=None, workspace=None, stream=None):
+    """``w4_fp8_block_moe_grouped_gemm`` from bf16 token rows: row r is
+    ``x[row_token[r]]`` (``row_token`` None: row r is token r), quantized per block
+    inside the call. Returns bf16 ``[R, N]``."""
+    _cuda2d(x, "x", (torch.bfloat16,))
+    T, K = x.shape
+    _expect(row_token, "row_token", None, _I32T, x.device, optional=True)
+    R = T if row_token is None else row_token.numel()
+    E, N = _block_expert_args("w4_fp8_block_moe_gemm_bf16in", qweight, w_scale, expert_offsets, K, x.device)
+    y = torch.empty((R, N), dtype=torch.bfloat16, device=x.device) if y is None else y
+    _expect(y, "y", (R, N), _BF16T, x.device)
+    ws, wsb = _workspace(workspace, W4_OP_FP8_BLOCK, R, N, K, 0, x.device)
+    _check(load().w4_fp8_block_moe_gemm_bf16in(_ptr(x), T, _ptr(row_token), _ptr(expert_offsets), E, _ptr(qweight),
+                                               _ptr(w_scale), _ptr(y), R, N, K, _ptr(ws), wsb,
+                                               _stream(stream, x.device)), "w4_fp8_block_moe_gemm_bf16in")
+    return y
 
 
 def w4_moe_gather_quant_fp8(x, row_token, q=None, scale=None, stream=None):

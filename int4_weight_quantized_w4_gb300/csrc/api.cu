@@ -129,6 +129,7 @@ size_t w4_workspace_bytes(int32_t op, int64_t M, int64_t N, int64_t K, int32_t g
     return w4::w4a8_workspace_bytes(M, K);
   }
   if (op == W4_OP_W4AFP8_MOE) return w4::w4a8_workspace_bytes(M, K);
+  if (op == W4_OP_FP8_BLOCK) return w4::fp8_block_workspace_bytes(M, K);
   if (op == W4_OP_MOE_ROUTE) return (N > 0 && N <= 1024) ? w4::moe_route_workspace_bytes(M, static_cast<int32_t>(N)) : 0;
   return 0;
 }
@@ -385,6 +386,165 @@ w4_status w4_moe_route(const void* logits, int32_t logits_f32, int64_t T, int32_
                                         topk_weights, offsets, row_token, row_of, workspace,
                                         static_cast<cudaStream_t>(stream)),
                    "moe route launch");
+}
+
+w4_status w4_moe_route_grouped(const void* logits, int32_t logits_f32, const float* bias, int64_t T, int32_t E,
+                               int32_t top_k, int32_t n_group, int32_t topk_group, int32_t scoring,
+                               int32_t renormalize, float scale, int32_t* topk_ids, float* topk_weights,
+                               int32_t* offsets, int32_t* row_token, int32_t* row_of, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  if (T < 0) return fail(W4_ERR_SHAPE, "T must be >= 0");
+  if (E < 1 || E > 1024) return fail(W4_ERR_UNSUPPORTED, "E must be in [1, 1024], got %d", E);
+  if (scoring != W4_SCORE_SIGMOID && scoring != W4_SCORE_SOFTMAX)
+    return fail(W4_ERR_DTYPE, "scoring must be W4_SCORE_SIGMOID or W4_SCORE_SOFTMAX");
+  if (n_group < 1 || E % n_group != 0) return fail(W4_ERR_GROUP, "n_group must be a positive divisor of E, got %d (E=%d)",
+                                                   n_group, E);
+  if (n_group > 32) return fail(W4_ERR_UNSUPPORTED, "n_group must be at most 32, got %d", n_group);
+  if (topk_group < 1 || topk_group > n_group)
+    return fail(W4_ERR_GROUP, "topk_group must be in [1, n_group], got %d (n_group=%d)", topk_group, n_group);
+  const int32_t open = topk_group * (E / n_group);
+  if (top_k < 1 || top_k > open || top_k > 64)
+    return fail(W4_ERR_SHAPE, "top_k must be in [1, min(64, experts of topk_group groups)], got %d (of %d)", top_k, open);
+  if (T > INT32_MAX / top_k) return fail(W4_ERR_UNSUPPORTED, "T * top_k rows must fit in int32");
+  if (T == 0) return ok();
+  if (!logits || !topk_ids || !topk_weights || !offsets || !row_token || !row_of)
+    return fail(W4_ERR_NULL, "logits and every output must be non-NULL");
+  if (!aligned(logits, logits_f32 ? 4 : 2) || !aligned(bias, 4) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4) ||
+      !aligned(offsets, 4) || !aligned(row_token, 4) || !aligned(row_of, 4))
+    return fail(W4_ERR_ALIGN, "route buffers must be aligned to their element size");
+  const size_t need = w4::moe_route_workspace_bytes(T, E);
+  if (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 4))
+    return fail(W4_ERR_WORKSPACE, "route workspace must be 4-byte aligned and at least %zu bytes (got %zu)", need,
+                workspace_bytes);
+  const w4::MoeRouteArgs a{logits,      bias,         T,       E,         top_k,  n_group,  topk_group, logits_f32 == 0,
+                           scoring == W4_SCORE_SOFTMAX, renormalize != 0, scale, topk_ids, topk_weights, offsets,
+                           row_token, row_of, workspace};
+  return from_cuda(w4::launch_moe_route_grouped(a, static_cast<cudaStream_t>(stream)), "moe grouped route launch");
+}
+
+w4_status w4_quant_act_per_block(const void* x, int32_t x_dtype, int64_t M, int64_t K, void* q, float* scale,
+                                 void* stream) {
+  if (M < 0 || K <= 0) return fail(W4_ERR_SHAPE, "sizes must be M >= 0, K > 0 (M=%lld K=%lld)", (long long)M, (long long)K);
+  if (x_dtype != W4_BF16 && x_dtype != W4_FP16) return fail(W4_ERR_DTYPE, "x_dtype must be W4_BF16 or W4_FP16");
+  if (K % 8 != 0) return fail(W4_ERR_ALIGN, "K must be a multiple of 8, got %lld", (long long)K);
+  if (M == 0) return ok();
+  if (!x || !q || !scale) return fail(W4_ERR_NULL, "x, q and scale must be non-NULL");
+  if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 4))
+    return fail(W4_ERR_ALIGN, "x and q must be 16-byte aligned, scale 4-byte aligned");
+  if (K > INT32_MAX / 2) return fail(W4_ERR_UNSUPPORTED, "K too large");
+  return from_cuda(w4::launch_quant_block(x, x_dtype == W4_FP16, false, M, K, nullptr, 0, q, scale, nullptr,
+                                          static_cast<cudaStream_t>(stream)),
+                   "w4_quant_act_per_block launch");
+}
+
+w4_status w4_silu_mul_quant_block(const void* h, int64_t R, int64_t I, void* q, float* scale, void* stream) {
+  if (R < 0 || I <= 0) return fail(W4_ERR_SHAPE, "sizes must be R >= 0, I > 0");
+  if (I % 8 != 0) return fail(W4_ERR_ALIGN, "I must be a multiple of 8, got %lld", (long long)I);
+  if (R == 0) return ok();
+  if (!h || !q || !scale) return fail(W4_ERR_NULL, "h, q and scale must be non-NULL");
+  if (!aligned(h, 16) || !aligned(q, 16) || !aligned(scale, 4))
+    return fail(W4_ERR_ALIGN, "h and q must be 16-byte aligned, scale 4-byte aligned");
+  if (I > INT32_MAX / 2) return fail(W4_ERR_UNSUPPORTED, "I too large");
+  return from_cuda(w4::launch_quant_block(h, false, true, R, I, nullptr, 0, q, scale, nullptr,
+                                          static_cast<cudaStream_t>(stream)),
+                   "w4_silu_mul_quant_block launch");
+}
+
+// Checks shared by the fp8 block-scaled products (E == 0: dense).
+static w4_status check_fp8_block(int64_t R, int64_t N, int64_t K, int32_t E, bool experts) {
+  if (R < 0 || N <= 0 || K <= 0) return fail(W4_ERR_SHAPE, "sizes must be M >= 0, N > 0, K > 0 (M=%lld N=%lld K=%lld)",
+                                             (long long)R, (long long)N, (long long)K);
+  if (experts && E <= 0) return fail(W4_ERR_SHAPE, "E must be > 0");
+  if (N % 8 != 0 || K % 8 != 0)
+    return fail(W4_ERR_ALIGN, "N and K must be multiples of 8, got N=%lld K=%lld", (long long)N, (long long)K);
+  if (K % 16 != 0) return fail(W4_ERR_UNSUPPORTED, "rows of e4m3 codes are copied 16 at a time: K=%lld", (long long)K);
+  if (experts && E > 1024) return fail(W4_ERR_UNSUPPORTED, "E must be at most 1024, got %d", E);
+  if (R > INT32_MAX / 2 || N > INT32_MAX / 2 || K > INT32_MAX / 2) return fail(W4_ERR_UNSUPPORTED, "M, N or K too large");
+  return W4_OK;
+}
+
+static w4_status check_block_workspace(void* ws, size_t bytes, int64_t rows, int64_t K) {
+  const size_t need = w4::fp8_block_workspace_bytes(rows, K);
+  if (ws == nullptr || bytes < need || !aligned(ws, 16))
+    return fail(W4_ERR_WORKSPACE, "workspace must be 16-byte aligned and at least %zu bytes (got %zu)", need, bytes);
+  return W4_OK;
+}
+
+static w4_status run_fp8_block(const void* qx, const float* x_scale, const int32_t* offsets, int32_t E,
+                               const void* qweight, const float* w_scale, const void* bias, void* y, int64_t R,
+                               int64_t N, int64_t K, void* stream) {
+  if (!qx || !x_scale || !qweight || !w_scale || !y) return fail(W4_ERR_NULL, "required pointer is NULL");
+  if (!aligned(qx, 16) || !aligned(qweight, 16) || !aligned(y, 16) || !aligned(x_scale, 4) || !aligned(w_scale, 4) ||
+      !aligned(offsets, 4) || !aligned(bias, 16))
+    return fail(W4_ERR_ALIGN, "matrices and the bias must be 16-byte aligned, scales and offsets 4-byte aligned");
+  unsigned int* status = nullptr;
+  cudaError_t e = status_ptr(&status);
+  if (e != cudaSuccess) return from_cuda(e, "device status word");
+  const w4::Fp8BlockArgs a{qx, x_scale, qweight, w_scale, bias, y, offsets, E, R, N, K, false, status};
+  return from_cuda(w4::launch_fp8_block(a, static_cast<cudaStream_t>(stream)), "fp8 block product launch");
+}
+
+// Quantizes rows of x (gathered by `rows` when given) into the workspace, then multiplies.
+static w4_status run_fp8_block_act(const void* x, bool f16, int64_t T, const int32_t* rows, const int32_t* offsets,
+                                   int32_t E, const void* qweight, const float* w_scale, const void* bias, void* y,
+                                   int64_t R, int64_t N, int64_t K, void* ws, size_t ws_bytes, void* stream) {
+  if (!x || !qweight || !w_scale || !y) return fail(W4_ERR_NULL, "required pointer is NULL");
+  if (!aligned(x, 16) || !aligned(qweight, 16) || !aligned(y, 16) || !aligned(w_scale, 4) || !aligned(offsets, 4) ||
+      !aligned(rows, 4) || !aligned(bias, 16))
+    return fail(W4_ERR_ALIGN, "matrices and the bias must be 16-byte aligned, scales, rows and offsets 4-byte aligned");
+  w4_status st = check_block_workspace(ws, ws_bytes, R, K);
+  if (st != W4_OK) return st;
+  unsigned int* status = nullptr;
+  cudaError_t e = status_ptr(&status);
+  if (e != cudaSuccess) return from_cuda(e, "device status word");
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  float* x_scale = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + static_cast<size_t>(R) * K);   // K % 16 == 0
+  e = w4::launch_quant_block(x, f16, false, R, K, rows, T, ws, x_scale, status, s);
+  if (e != cudaSuccess) return from_cuda(e, "block quant launch");
+  const w4::Fp8BlockArgs a{ws, x_scale, qweight, w_scale, bias, y, offsets, E, R, N, K, true, status};
+  return from_cuda(w4::launch_fp8_block(a, s), "fp8 block product launch");
+}
+
+w4_status w4_fp8_block_gemm(const void* qx, const float* x_scale, const void* qweight, const float* w_scale,
+                            const void* bias, void* y, int64_t M, int64_t N, int64_t K, void* stream) {
+  w4_status st = check_fp8_block(M, N, K, 1, false);
+  if (st != W4_OK) return st;
+  if (M == 0) return ok();
+  return run_fp8_block(qx, x_scale, nullptr, 1, qweight, w_scale, bias, y, M, N, K, stream);
+}
+
+w4_status w4_fp8_block_gemm_bf16in(const void* x, int32_t x_dtype, const void* qweight, const float* w_scale,
+                                   const void* bias, void* y, int64_t M, int64_t N, int64_t K, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  w4_status st = check_fp8_block(M, N, K, 1, false);
+  if (st != W4_OK) return st;
+  if (x_dtype != W4_BF16 && x_dtype != W4_FP16) return fail(W4_ERR_DTYPE, "x_dtype must be W4_BF16 or W4_FP16");
+  if (M == 0) return ok();
+  return run_fp8_block_act(x, x_dtype == W4_FP16, M, nullptr, nullptr, 1, qweight, w_scale, bias, y, M, N, K, workspace,
+                           workspace_bytes, stream);
+}
+
+w4_status w4_fp8_block_moe_grouped_gemm(const void* qx, const float* x_scale, const int32_t* expert_offsets, int32_t E,
+                                        const void* qweight, const float* w_scale, void* y, int64_t R, int64_t N,
+                                        int64_t K, void* stream) {
+  w4_status st = check_fp8_block(R, N, K, E, true);
+  if (st != W4_OK) return st;
+  if (R == 0) return ok();
+  if (!expert_offsets) return fail(W4_ERR_NULL, "expert_offsets must be non-NULL");
+  return run_fp8_block(qx, x_scale, expert_offsets, E, qweight, w_scale, nullptr, y, R, N, K, stream);
+}
+
+w4_status w4_fp8_block_moe_gemm_bf16in(const void* x, int64_t T, const int32_t* row_token, const int32_t* expert_offsets,
+                                       int32_t E, const void* qweight, const float* w_scale, void* y, int64_t R,
+                                       int64_t N, int64_t K, void* workspace, size_t workspace_bytes, void* stream) {
+  w4_status st = check_fp8_block(R, N, K, E, true);
+  if (st != W4_OK) return st;
+  if (T < 0) return fail(W4_ERR_SHAPE, "T must be >= 0");
+  if (row_token == nullptr && R != T) return fail(W4_ERR_SHAPE, "without row_token R must equal T");
+  if (R == 0) return ok();
+  if (!expert_offsets) return fail(W4_ERR_NULL, "expert_offsets must be non-NULL");
+  return run_fp8_block_act(x, false, T, row_token, expert_offsets, E, qweight, w_scale, nullptr, y, R, N, K, workspace,
+                           workspace_bytes, stream);
 }
 
 w4_status w4_moe_gather_quant_fp8(const void* x, int64_t T, int64_t K, const int32_t* row_token, int64_t R,

@@ -59,6 +59,13 @@ W4_DEV void fma2(float& d0, float& d1, float a, float b0, float b1) {
       : "+f"(d0), "+f"(d1) : "f"(a), "f"(b0), "f"(b1));
 }
 
+// d0 += a0 * b0 and d1 += a1 * b1, packed as fma2.
+W4_DEV void fma2v(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  asm("{.reg .b64 d, x, y; mov.b64 d, {%0, %1}; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; "
+      "fma.rn.f32x2 d, x, y, d; mov.b64 {%0, %1}, d;}"
+      : "+f"(d0), "+f"(d1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
 W4_DEV float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
 W4_DEV float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
 

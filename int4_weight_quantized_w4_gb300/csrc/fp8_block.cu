@@ -1,0 +1,669 @@
+// The fp8 block-scaled product on the 5th-generation tensor cores (tcgen05,
+// kind::f8f6f4, sm_103a), dense and over expert segments of rows:
+//
+//   y[r, n] = bf16( sum_b sx[r, b] sw[n / 128, b] P[r, b, n] + bias[n] ),
+//   P[r, b, n] = sum_{k in block b} q[r, k] w[n, k],
+//
+// q, w e4m3, blocks of 128 along k, fp32 scales. P is accumulated in fp32 by
+// the tensor core, one accumulation per block, because sx and sw are arbitrary
+// fp32 numbers; the sum over blocks is an fp32 FMA per element in registers.
+//
+// Two forms:
+//  * stream (few rows an expert or call): weights on the MMA's 128 rows (TMEM
+//    lane = output), NT tokens on its columns. Bound by the weight bytes.
+//  * tile (many rows): 128 tokens on the MMA's rows, 256 outputs on its
+//    columns, so that one scale sx * sw serves a thread's whole column strip.
+//    Bound by the tensor core and by the drain of one accumulator per block.
+#include <cuda.h>
+
+#include <cstring>
+
+#include "common.cuh"
+#include "launch.h"
+#include "tc.cuh"
+
+namespace w4 {
+namespace {
+
+constexpr int kBlk = 128;                     // k and weight rows per scale
+constexpr int kMaxExperts = 1024;
+constexpr uint64_t kWaitNs = 2000000000ull;   // 2 s per wait
+
+struct Params {
+  CUtensorMap tm_x;        // e4m3 codes [rows, K]
+  CUtensorMap tm_w;        // e4m3 codes [E, N, K]
+  const float* x_scale;    // [rows, KB]
+  const float* w_scale;    // [E, NB, KB]
+  const uint16_t* bias;    // bf16 [N] or null
+  uint16_t* y;             // bf16 [rows, N]
+  const int32_t* offsets;  // [E + 1], or null (dense: one segment of all rows)
+  int E, rows, N, K, KB, NB, n_tiles;
+  int split;               // stream form, dense: parts of the k blocks, one per CTA of a cluster
+  long long items;         // upper bound of (row tile, n tile) pairs
+  unsigned int* status;
+};
+
+W4_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+W4_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+W4_DEV uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// The float at shared address `a` of CTA `rank` of the cluster.
+W4_DEV float ld_cluster_f32(uint32_t a, uint32_t rank) {
+  float v;
+  asm volatile("{.reg .b32 t; mapa.shared::cluster.u32 t, %1, %2; ld.shared::cluster.f32 %0, [t];}"
+               : "=f"(v) : "r"(a), "r"(rank) : "memory");
+  return v;
+}
+W4_DEV void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// First row tile of every expert (tiles of `rows_per` rows), in shared memory:
+// starts[e], starts[E] = the total. All threads of the block take part; at
+// most kMaxExperts experts. A segment outside [0, rows) counts as clipped.
+W4_DEV void seg_bounds(const Params& p, int e, int& a, int& b) {
+  a = max(p.offsets[e], 0);
+  b = min(p.offsets[e + 1], p.rows);
+}
+template <int kThreads>
+W4_DEV void tile_starts(const Params& p, int rows_per, int32_t* starts, int32_t* warp_sum) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int carry = 0;
+  for (int e0 = 0; e0 < p.E; e0 += kThreads) {
+    const int e = e0 + threadIdx.x;
+    int n = 0;
+    if (e < p.E) {
+      int a, b;
+      seg_bounds(p, e, a, b);
+      n = b > a ? (b - a + rows_per - 1) / rows_per : 0;
+    }
+    int inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += t;
+    }
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    int before = carry, all = carry;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      const int s = warp_sum[w];
+      if (w < warp) before += s;
+      all += s;
+    }
+    if (e < p.E) starts[e] = before + inc - n;
+    carry = all;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) starts[p.E] = carry;
+}
+
+struct Tile {
+  int n0, row0, row_end, expert;
+};
+// Item `it` (n tiles fastest) as a tile of `rows_per` rows and `cols_per`
+// outputs; false when there are no more. `e` is the caller's cursor over the
+// experts: items come in increasing order.
+W4_DEV bool decode(const Params& p, long long it, int rows_per, int cols_per, const int32_t* starts, Tile& t, int& e) {
+  const int yt = static_cast<int>(it / p.n_tiles);
+  t.n0 = static_cast<int>(it - static_cast<long long>(yt) * p.n_tiles) * cols_per;
+  if (p.offsets == nullptr) {
+    t.expert = 0;
+    t.row0 = yt * rows_per;
+    t.row_end = min(t.row0 + rows_per, p.rows);
+    return t.row0 < p.rows;
+  }
+  if (yt >= starts[p.E]) return false;
+  while (starts[e + 1] <= yt) ++e;
+  int a, b;
+  seg_bounds(p, e, a, b);
+  t.expert = e;
+  t.row0 = a + (yt - starts[e]) * rows_per;
+  t.row_end = min(t.row0 + rows_per, b);
+  return true;
+}
+
+// e4m3 x e4m3, fp32 accumulator, both operands K-major: format codes 0.
+// One block of 128 k: four MMAs of 32 k, 32 bytes apart in the swizzle row.
+W4_DEV void mma_block(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) tc::mma_f8(d, a + 2 * j, b + 2 * j, idesc, j > 0 ? 1u : 0u);
+}
+
+// ---------------------------------------------------------------------------
+// stream form
+// ---------------------------------------------------------------------------
+
+template <int NT>
+struct Stream {
+  static constexpr int A_BYTES = kBlk * 128;             // 128 outputs x 128 k
+  static constexpr int B_BYTES = NT * 128;               // NT tokens x 128 k
+  static constexpr int CTAS = NT <= 64 ? 2 : 1;          // resident per SM
+  static constexpr int STAGES = NT <= 32 ? 5 : NT == 64 ? 4 : 6;
+  static constexpr int TMEM_COLS = CTAS == 2 ? 256 : 512;
+  static constexpr int ACCS = TMEM_COLS / NT > 8 ? 8 : TMEM_COLS / NT;
+  static constexpr int SC_SLOTS = 4;                     // scale slots of 4 blocks x NT tokens
+  static constexpr int SC_BYTES = SC_SLOTS * 4 * NT * 4;
+  static constexpr int SMEM = STAGES * (A_BYTES + B_BYTES) + SC_BYTES + 512 + (kMaxExperts + 1 + 8 + 7) / 4 * 16 + 1024;
+};
+static_assert(Stream<16>::SMEM * 2 + 2048 <= 233472 && Stream<32>::SMEM * 2 + 2048 <= 233472 &&
+                  Stream<64>::SMEM * 2 + 2048 <= 233472 && Stream<128>::SMEM <= 232448,
+              "shared memory per SM");
+
+// Warps 0-3 epilogue (warp w: TMEM lanes 32 w, outputs n0 + 32 w + lane), 4
+// weight copies, 5 activation copies, 6 MMA issuer and TMEM owner, 7 scales.
+constexpr int kSWarpA = 4, kSWarpB = 5, kSWarpMma = 6, kSWarpScale = 7;
+constexpr int kSThreads = 256;
+
+template <int NT>
+__global__ void __launch_bounds__(kSThreads, Stream<NT>::CTAS) stream_kernel(const __grid_constant__ Params p) {
+  using C = Stream<NT>;
+  extern __shared__ uint8_t smem_dyn[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
+  uint8_t* a_base = smem;
+  uint8_t* b_base = a_base + C::STAGES * C::A_BYTES;
+  float* sc_base = reinterpret_cast<float*>(b_base + C::STAGES * C::B_BYTES);
+  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(sc_base) + C::SC_BYTES);
+  uint64_t* empty = full + C::STAGES;
+  uint64_t* acc_full = empty + C::STAGES;
+  uint64_t* acc_empty = acc_full + C::ACCS;
+  uint64_t* sc_full = acc_empty + C::ACCS;
+  uint64_t* sc_empty = sc_full + C::SC_SLOTS;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sc_empty + C::SC_SLOTS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  int32_t* starts = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(full) + 512);
+  int32_t* warp_sum = starts + kMaxExperts + 1;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(&full[i], 2);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < C::ACCS; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 4);
+    }
+    for (int i = 0; i < C::SC_SLOTS; ++i) {
+      mbar_init(&sc_full[i], 1);
+      mbar_init(&sc_empty[i], 4);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kSWarpMma) tc::tmem_alloc(tmem_holder, C::TMEM_COLS);
+  if (warp == kSWarpA && lane == 0) tc::prefetch_tmap(&p.tm_w);
+  if (warp == kSWarpB && lane == 0) tc::prefetch_tmap(&p.tm_x);
+  if (p.offsets != nullptr) tile_starts<kSThreads>(p, NT, starts, warp_sum);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_holder;
+
+  // this CTA's part of the k blocks (the same for every item)
+  const int part = p.split > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int kb0 = static_cast<int>(static_cast<long long>(p.KB) * part / p.split);
+  const int kb1 = static_cast<int>(static_cast<long long>(p.KB) * (part + 1) / p.split);
+  const long long first = blockIdx.x / p.split, step = gridDim.x / p.split;
+
+  if (warp == kSWarpA) {
+    if (lane == 0) {
+      int st = 0, ph = 1, e = 0;
+      bool ok = true;
+      Tile t;
+      for (long long it = first; ok && it < p.items && decode(p, it, NT, kBlk, starts, t, e); it += step)
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!(ok = tc::wait(&empty[st], ph, abort_flag, p.status, kWaitNs))) break;
+          mbar_arrive_expect_tx(&full[st], C::A_BYTES);
+          tc::tma_load_3d(a_base + st * C::A_BYTES, &p.tm_w, &full[st], kb * kBlk, t.n0, t.expert);
+          if (++st == C::STAGES) st = 0, ph ^= 1;
+        }
+    }
+  } else if (warp == kSWarpB) {
+    if (lane == 0) {
+      grid_dependency_wait();   // the codes come from the kernel before
+      int st = 0, ph = 1, e = 0;
+      bool ok = true;
+      Tile t;
+      for (long long it = first; ok && it < p.items && decode(p, it, NT, kBlk, starts, t, e); it += step)
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!(ok = tc::wait(&empty[st], ph, abort_flag, p.status, kWaitNs))) break;
+          mbar_arrive_expect_tx(&full[st], C::B_BYTES);
+          tc::tma_load_2d(b_base + st * C::B_BYTES, &p.tm_x, &full[st], kb * kBlk, t.row0);
+          if (++st == C::STAGES) st = 0, ph ^= 1;
+        }
+    }
+  } else if (warp == kSWarpMma) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = tc::idesc_f16_f32(128, NT);
+      const uint64_t ad0 = tc::sdesc_sw128(smem_addr(a_base)), bd0 = tc::sdesc_sw128(smem_addr(b_base));
+      int st = 0, ph = 0, ac = 0, aph = 1, e = 0;
+      bool ok = true;
+      Tile t;
+      for (long long it = first; ok && it < p.items && decode(p, it, NT, kBlk, starts, t, e); it += step)
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!(ok = tc::wait(&acc_empty[ac], aph, abort_flag, p.status, kWaitNs))) break;
+          if (!(ok = tc::wait(&full[st], ph, abort_flag, p.status, kWaitNs, 200))) break;
+          tc::fence_after_sync();
+          mma_block(tmem + ac * NT, ad0 + static_cast<uint64_t>((st * C::A_BYTES) >> 4),
+                    bd0 + static_cast<uint64_t>((st * C::B_BYTES) >> 4), idesc);
+          tc::commit(&empty[st]);
+          tc::commit(&acc_full[ac]);
+          if (++st == C::STAGES) st = 0, ph ^= 1;
+          if (++ac == C::ACCS) ac = 0, aph ^= 1;
+        }
+    }
+    __syncwarp();
+  } else if (warp == kSWarpScale) {
+    // sx * sw of four blocks and NT tokens per slot
+    grid_dependency_wait();
+    int sl = 0, ph = 1, e = 0;
+    bool ok = true;
+    Tile t;
+    for (long long it = first; ok && it < p.items && decode(p, it, NT, kBlk, starts, t, e); it += step) {
+      const float* sw = p.w_scale + (static_cast<size_t>(t.expert) * p.NB + t.n0 / kBlk) * p.KB;
+      for (int kb = kb0; kb < kb1; kb += 4) {
+        float w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = kb + i < kb1 ? __ldg(sw + kb + i) : 0.f;
+        if (!(ok = tc::wait(&sc_empty[sl], ph, abort_flag, p.status, kWaitNs))) break;
+        float* sc = sc_base + sl * 4 * NT;
+#pragma unroll
+        for (int j0 = 0; j0 < NT; j0 += 32) {
+          const int j = j0 + lane, row = t.row0 + j;
+          if (NT % 32 == 0 || j < NT) {
+            const float* sx = p.x_scale + static_cast<size_t>(row) * p.KB + kb;
+            float x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = (row < t.row_end && kb + i < kb1) ? sx[i] : 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sc[i * NT + j] = x[i] * w[i];
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sc_full[sl]);
+        if (++sl == C::SC_SLOTS) sl = 0, ph ^= 1;
+      }
+    }
+  } else {
+    int ac = 0, aph = 0, sl = 0, sph = 0, e = 0;
+    bool ok = true;
+    Tile t;
+    for (long long it = first; ok && it < p.items && decode(p, it, NT, kBlk, starts, t, e); it += step) {
+      float T[NT];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) T[j] = 0.f;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        const int i = (kb - kb0) & 3;
+        if (i == 0 && !(ok = tc::wait(&sc_full[sl], sph, abort_flag, p.status, kWaitNs))) break;
+        if (!(ok = tc::wait(&acc_full[ac], aph, abort_flag, p.status, kWaitNs))) break;
+        tc::fence_after_sync();
+        const uint32_t ta = tmem + (static_cast<uint32_t>(32 * warp) << 16) + ac * NT;
+        const float* sc = sc_base + (sl * 4 + i) * NT;
+#pragma unroll
+        for (int c = 0; c < NT; c += 16) {
+          uint32_t v[16];
+          tc::tmem_ld16_async(ta + c, v);
+          tc::tmem_wait_ld(v);
+#pragma unroll
+          for (int j = 0; j < 16; j += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(sc + c + j);
+            fma2v(T[c + j], T[c + j + 1], f.x, f.y, __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+            fma2v(T[c + j + 2], T[c + j + 3], f.z, f.w, __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
+          }
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&acc_empty[ac]);
+          if (i == 3 || kb == kb1 - 1) mbar_arrive(&sc_empty[sl]);
+        }
+        if (++ac == C::ACCS) ac = 0, aph ^= 1;
+        if (i == 3 || kb == kb1 - 1) {
+          if (++sl == C::SC_SLOTS) sl = 0, sph ^= 1;
+        }
+      }
+      if (!ok) break;
+      const int o = 32 * warp + lane, n = t.n0 + o;
+      const int valid = t.row_end - t.row0;
+      if (p.split > 1) {
+        // every copy has landed and every MMA is done: the ring is free
+        float* mine = reinterpret_cast<float*>(smem);
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          if (j < valid) mine[j * kBlk + o] = T[j];
+      } else if (n < p.N) {
+        const float bs = p.bias != nullptr ? __uint_as_float(static_cast<uint32_t>(p.bias[n]) << 16) : 0.f;
+        uint16_t* yp = p.y + static_cast<size_t>(t.row0) * p.N + n;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          if (j < valid) yp[static_cast<size_t>(j) * p.N] = static_cast<uint16_t>(f32_to_bf16_bits(T[j] + bs));
+      }
+    }
+  }
+  __syncwarp();
+
+  if (p.split > 1) {
+    // one item per cluster: CTA r adds the parts of tokens r, r + split, ... in order of the parts
+    cluster_arrive();
+    cluster_wait();
+    int e = 0;
+    Tile t;
+    if (warp < 4 && decode(p, first, NT, kBlk, starts, t, e) && !*abort_flag) {
+      const int o = 32 * warp + lane, n = t.n0 + o;
+      if (n < p.N) {
+        const float bs = p.bias != nullptr ? __uint_as_float(static_cast<uint32_t>(p.bias[n]) << 16) : 0.f;
+        for (int j = part; j < t.row_end - t.row0; j += p.split) {
+          const uint32_t at = smem_addr(smem) + (j * kBlk + o) * 4;
+          float s = 0.f;
+          for (int r = 0; r < p.split; ++r) s += ld_cluster_f32(at, r);
+          p.y[static_cast<size_t>(t.row0 + j) * p.N + n] = static_cast<uint16_t>(f32_to_bf16_bits(s + bs));
+        }
+      }
+    }
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+  }
+
+  if (*abort_flag) {   // let copies and MMAs in flight land before the shared memory goes away
+    const uint64_t t0 = tc::globaltimer_ns();
+    while (tc::globaltimer_ns() - t0 < 1000000ull) {
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == kSWarpMma) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// tile form
+// ---------------------------------------------------------------------------
+
+constexpr int TM = 128, TN = 256;
+constexpr int T_A = TM * 128, T_B = TN * 128;
+constexpr int T_STAGES = 4;
+constexpr int T_SMEM = T_STAGES * (T_A + T_B) + 512 + (kMaxExperts + 1 + 12 + 3) / 4 * 16 + 1024;
+static_assert(T_SMEM <= 232448, "shared memory per CTA");
+// Warps 0-7 epilogue (warp w: TMEM lanes 32 (w % 4), outputs 128 (w / 4) ..),
+// 8 activation copies, 9 weight copies, 10 and 11 MMA issuers of the even and
+// odd blocks: a thread's MMAs queue behind its own commits, so with two
+// issuers one accumulates while the other's block completes.
+constexpr int kTEpi = 8, kTWarpA = 8, kTWarpB = 9, kTWarpMma = 10;
+constexpr int kTThreads = 384;
+
+__global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const __grid_constant__ Params p) {
+  extern __shared__ uint8_t smem_dyn[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
+  uint8_t* a_base = smem;
+  uint8_t* b_base = a_base + T_STAGES * T_A;
+  uint64_t* full = reinterpret_cast<uint64_t*>(b_base + T_STAGES * T_B);
+  uint64_t* done = full + T_STAGES;        // a block's MMAs: its stage is free and its accumulator complete
+  uint64_t* acc_empty = done + T_STAGES;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  int32_t* starts = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(full) + 512);
+  int32_t* warp_sum = starts + kMaxExperts + 1;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < T_STAGES; ++i) {
+      mbar_init(&full[i], 2);
+      mbar_init(&done[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) mbar_init(&acc_empty[i], kTEpi);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kTWarpMma) tc::tmem_alloc(tmem_holder, 2 * TN);
+  if (warp == kTWarpA && lane == 0) tc::prefetch_tmap(&p.tm_x);
+  if (warp == kTWarpB && lane == 0) tc::prefetch_tmap(&p.tm_w);
+  if (p.offsets != nullptr) tile_starts<kTThreads>(p, TM, starts, warp_sum);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_holder;
+  const int KB = p.KB;
+
+  if (warp >= kTEpi) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (lane == 0) {
+      if (warp == kTWarpA || warp == kTWarpB) {
+        if (warp == kTWarpA) grid_dependency_wait();
+        int st = 0, ph = 1, e = 0;
+        bool ok = true;
+        Tile t;
+        for (long long it = blockIdx.x; ok && it < p.items && decode(p, it, TM, TN, starts, t, e); it += gridDim.x)
+          for (int kb = 0; kb < KB; ++kb) {
+            if (!(ok = tc::wait(&done[st], ph, abort_flag, p.status, kWaitNs))) break;
+            if (warp == kTWarpA) {
+              mbar_arrive_expect_tx(&full[st], T_A);
+              tc::tma_load_2d(a_base + st * T_A, &p.tm_x, &full[st], kb * kBlk, t.row0);
+            } else {
+              mbar_arrive_expect_tx(&full[st], T_B);
+              tc::tma_load_3d(b_base + st * T_B, &p.tm_w, &full[st], kb * kBlk, t.n0, t.expert);
+            }
+            if (++st == T_STAGES) st = 0, ph ^= 1;
+          }
+      } else {
+        const int mine = warp - kTWarpMma;   // blocks and accumulators of this parity
+        constexpr uint32_t idesc = tc::idesc_f16_f32(TM, TN);
+        const uint64_t ad0 = tc::sdesc_sw128(smem_addr(a_base)), bd0 = tc::sdesc_sw128(smem_addr(b_base));
+        int st = 0, ph = 0, g = 0, aph = 1, e = 0;
+        bool ok = true;
+        Tile t;
+        for (long long it = blockIdx.x; ok && it < p.items && decode(p, it, TM, TN, starts, t, e); it += gridDim.x)
+          for (int kb = 0; kb < KB; ++kb, ++g) {
+            if ((g & 1) == mine) {
+              if (!(ok = tc::wait(&acc_empty[mine], aph, abort_flag, p.status, kWaitNs, 200))) break;
+              if (!(ok = tc::wait(&full[st], ph, abort_flag, p.status, kWaitNs, 200))) break;
+              tc::fence_after_sync();
+              mma_block(tmem + mine * TN, ad0 + static_cast<uint64_t>((st * T_A) >> 4),
+                        bd0 + static_cast<uint64_t>((st * T_B) >> 4), idesc);
+              tc::commit(&done[st]);
+              aph ^= 1;
+            }
+            if (++st == T_STAGES) st = 0, ph ^= 1;
+          }
+      }
+    }
+    __syncwarp();
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    grid_dependency_wait();
+    const int q = warp & 3, half = warp >> 2;
+    int st = 0, ph = 0, buf = 0, e = 0;
+    bool ok = true;
+    Tile t;
+    for (long long it = blockIdx.x; ok && it < p.items && decode(p, it, TM, TN, starts, t, e); it += gridDim.x) {
+      const int row = t.row0 + 32 * q + lane;
+      const bool r_ok = row < t.row_end;
+      const int n0 = t.n0 + 128 * half;
+      const bool n_any = n0 < p.N;
+      const float* sx = p.x_scale + static_cast<size_t>(r_ok ? row : t.row0) * KB;
+      const float* sw = p.w_scale + (static_cast<size_t>(t.expert) * p.NB + (n_any ? n0 / kBlk : 0)) * KB;
+      float T[128];
+#pragma unroll
+      for (int j = 0; j < 128; ++j) T[j] = 0.f;
+      // the scales of this block and the next three, loaded ahead
+      auto ld = [&](int kb) { return kb < KB ? sx[kb] * __ldg(sw + kb) : 0.f; };
+      float f0 = ld(0), f1 = ld(1), f2 = ld(2), f3 = ld(3);
+      for (int kb = 0; kb < KB; ++kb) {
+        const float f = f0;
+        f0 = f1, f1 = f2, f2 = f3, f3 = ld(kb + 4);
+        if (!(ok = tc::wait(&done[st], ph, abort_flag, p.status, kWaitNs))) break;
+        tc::fence_after_sync();
+        const uint32_t ta = tmem + (static_cast<uint32_t>(32 * q) << 16) + buf * TN + 128 * half;
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) {
+          uint32_t v[32];
+          tc::tmem_ld32(ta + c, v);
+#pragma unroll
+          for (int j = 0; j < 32; j += 2)
+            fma2(T[c + j], T[c + j + 1], f, __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[buf]);
+        buf ^= 1;
+        if (++st == T_STAGES) st = 0, ph ^= 1;
+      }
+      if (!ok) break;
+      if (r_ok) {
+        uint16_t* yp = p.y + static_cast<size_t>(row) * p.N + n0;
+#pragma unroll
+        for (int c = 0; c < 128; c += 8)
+          if (n0 + c < p.N) {   // N is a multiple of 8
+            float b[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (p.bias != nullptr) {
+              const uint4 bb = *reinterpret_cast<const uint4*>(p.bias + n0 + c);
+              b[0] = bf16_lo(bb.x), b[1] = bf16_hi(bb.x), b[2] = bf16_lo(bb.y), b[3] = bf16_hi(bb.y);
+              b[4] = bf16_lo(bb.z), b[5] = bf16_hi(bb.z), b[6] = bf16_lo(bb.w), b[7] = bf16_hi(bb.w);
+            }
+            *reinterpret_cast<uint4*>(yp + c) =
+                make_uint4(pack_bf16x2(T[c] + b[0], T[c + 1] + b[1]), pack_bf16x2(T[c + 2] + b[2], T[c + 3] + b[3]),
+                           pack_bf16x2(T[c + 4] + b[4], T[c + 5] + b[5]), pack_bf16x2(T[c + 6] + b[6], T[c + 7] + b[7]));
+          }
+      }
+    }
+  }
+
+  if (*abort_flag) {
+    const uint64_t t0 = tc::globaltimer_ns();
+    while (tc::globaltimer_ns() - t0 < 1000000ull) {
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == kTWarpMma) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 2 * TN);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+cudaError_t get_encoder(EncodeTiled* fn) {
+  static const EncodeTiled cached = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeTiled>(f);
+  }();
+  if (cached == nullptr) return cudaErrorNotSupported;
+  *fn = cached;
+  return cudaSuccess;
+}
+
+// e4m3 rows of K bytes in boxes of box_rows rows x 128 bytes, 128-byte swizzle;
+// rows and columns past the tensor arrive as zeros.
+cudaError_t encode(CUtensorMap* m, const void* base, int64_t K, int64_t rows, int64_t E, int box_rows) {
+  EncodeTiled fn = nullptr;
+  cudaError_t e = get_encoder(&fn);
+  if (e != cudaSuccess) return e;
+  const cuuint32_t rank = E > 0 ? 3 : 2;
+  const cuuint64_t dims[3] = {(cuuint64_t)K, (cuuint64_t)rows, (cuuint64_t)E};
+  const cuuint64_t strides[2] = {(cuuint64_t)K, (cuuint64_t)K * (cuuint64_t)rows};
+  const cuuint32_t box[3] = {128, (cuuint32_t)box_rows, 1}, estr[3] = {1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Row tiles of `per` rows that R rows in E segments can need at most.
+int64_t row_tiles(const Fp8BlockArgs& a, int per) {
+  const int64_t whole = (a.R + per - 1) / per;
+  return a.expert_offsets == nullptr ? whole : (a.R < whole + a.E ? a.R : whole + a.E);
+}
+
+cudaError_t start(void (*kernel)(Params), const Params& p, int64_t grid, int threads, int smem, int cluster, bool pdl,
+                  cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  int n = 0;
+  if (pdl) {
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster > 1) {
+    at[n].id = cudaLaunchAttributeClusterDimension;
+    at[n].val.clusterDim.x = cluster;
+    at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  cfg.attrs = at;
+  cfg.numAttrs = n;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <int NT>
+cudaError_t run_stream(const Fp8BlockArgs& a, Params& p, cudaStream_t s) {
+  using C = Stream<NT>;
+  cudaError_t e = encode(&p.tm_x, a.qx, a.K, a.R, 0, NT);
+  if (e != cudaSuccess) return e;
+  e = encode(&p.tm_w, a.qweight, a.K, a.N, a.E, kBlk);
+  if (e != cudaSuccess) return e;
+  p.n_tiles = static_cast<int>((a.N + kBlk - 1) / kBlk);
+  p.items = row_tiles(a, NT) * p.n_tiles;
+  const int64_t slots = static_cast<int64_t>(current_sm_count()) * C::CTAS;
+  p.split = 1;
+  if (a.expert_offsets == nullptr)
+    while (p.split < 8 && p.items * p.split * 2 <= slots && p.KB >= 4 * p.split) p.split *= 2;
+  const int64_t grid = p.split > 1 ? p.items * p.split : (p.items < slots ? p.items : slots);
+  return start(stream_kernel<NT>, p, grid, kSThreads, C::SMEM, p.split, a.pdl, s);
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_block(const Fp8BlockArgs& a, cudaStream_t s) {
+  Params p;
+  memset(&p, 0, sizeof(p));
+  p.x_scale = a.x_scale;
+  p.w_scale = a.w_scale;
+  p.bias = static_cast<const uint16_t*>(a.bias);
+  p.y = static_cast<uint16_t*>(a.y);
+  p.offsets = a.expert_offsets;
+  p.E = a.E;
+  p.rows = static_cast<int>(a.R);
+  p.N = static_cast<int>(a.N);
+  p.K = static_cast<int>(a.K);
+  p.KB = static_cast<int>((a.K + kBlk - 1) / kBlk);
+  p.NB = static_cast<int>((a.N + kBlk - 1) / kBlk);
+  p.split = 1;
+  p.status = a.status;
+  // rows a weight tile is used for, on average
+  const int64_t rows = a.expert_offsets == nullptr ? a.R : (a.R + a.E - 1) / a.E;
+  if (rows <= 16) return run_stream<16>(a, p, s);
+  if (rows <= 32) return run_stream<32>(a, p, s);
+  if (rows <= 64) return run_stream<64>(a, p, s);
+  if (rows <= 128) return run_stream<128>(a, p, s);
+  cudaError_t e = encode(&p.tm_x, a.qx, a.K, a.R, 0, TM);
+  if (e != cudaSuccess) return e;
+  e = encode(&p.tm_w, a.qweight, a.K, a.N, a.E, TN);
+  if (e != cudaSuccess) return e;
+  p.n_tiles = static_cast<int>((a.N + TN - 1) / TN);
+  p.items = row_tiles(a, TM) * p.n_tiles;
+  const int64_t sms = current_sm_count();
+  return start(tile_kernel, p, p.items < sms ? p.items : sms, kTThreads, T_SMEM, 1, a.pdl, s);
+}
+
+}  // namespace w4

@@ -97,10 +97,45 @@ size_t moe_route_workspace_bytes(int64_t T, int32_t E);
 cudaError_t launch_moe_route(const void* logits, bool bf16, int64_t T, int32_t E, int32_t k, bool renorm,
                              int32_t* ids, float* wts, int32_t* offsets, int32_t* row_token, int32_t* row_of,
                              void* workspace, cudaStream_t s);
+struct MoeRouteArgs {
+  const void* logits;      // [T, E], bf16 or fp32
+  const float* bias;       // [E] or null
+  int64_t T;
+  int32_t E, k, n_group, topk_group;
+  bool bf16, softmax, renorm;
+  float factor;
+  int32_t* ids;            // outputs as w4_moe_route
+  float* wts;
+  int32_t *offsets, *row_token, *row_of;
+  void* workspace;
+};
+cudaError_t launch_moe_route_grouped(const MoeRouteArgs& a, cudaStream_t s);
 cudaError_t launch_silu_mul_quant(const void* h, int64_t R, int64_t I, void* q, float* scale, void* act,
                                   cudaStream_t s);
 cudaError_t launch_moe_combine(const void* y, int64_t R, int64_t H, const float* w, const int32_t* row_of, int64_t T,
                                int32_t k, void* out, unsigned int* status, cudaStream_t s);
+// e4m3 codes and fp32 scales per row and 128 columns of x [*, K] (bf16, or fp16), or of silu(gate) * up of x
+// [*, 2K] (silu, bf16); gather (may be null): source row of each of the M output rows, checked against T.
+cudaError_t launch_quant_block(const void* x, bool f16, bool silu, int64_t M, int64_t K, const int32_t* gather,
+                               int64_t T, void* q, float* scale, unsigned int* status, cudaStream_t s);
+struct Fp8BlockArgs {
+  const void* qx;                 // e4m3 [R, K]
+  const float* x_scale;           // [R, ceil(K / 128)]
+  const void* qweight;            // e4m3 [E, N, K]
+  const float* w_scale;           // [E, ceil(N / 128), ceil(K / 128)]
+  const void* bias;               // bf16 [N] or null
+  void* y;                        // bf16 [R, N]
+  const int32_t* expert_offsets;  // device [E + 1], or null: dense, E = 1
+  int32_t E;
+  int64_t R, N, K;
+  bool pdl;                       // qx and x_scale come from the kernel launched just before, nothing else does
+  unsigned int* status;
+};
+// Quantized rows of the 16-bit-input forms: codes [R, K], then scales [R, ceil(K / 128)].
+inline size_t fp8_block_workspace_bytes(int64_t R, int64_t K) {
+  return static_cast<size_t>(R) * static_cast<size_t>(K) + static_cast<size_t>(R) * static_cast<size_t>((K + 127) / 128) * 4;
+}
+cudaError_t launch_fp8_block(const Fp8BlockArgs& a, cudaStream_t s);
 cudaError_t launch_bounded_wait_selftest(long long limit, unsigned int* status, cudaStream_t s);
 
 }  // namespace w4

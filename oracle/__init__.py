@@ -11,3 +11,4 @@ layer is also stated in plain C (``w4_oracle_c.c``, called through
 to the numpy statement.
 """
 from .w4_oracle import *  # noqa: F401,F403
+from .fp8_block_oracle import *  # noqa: F401,F403

@@ -1,0 +1,278 @@
+"""The fp8 block-scaled layer on the GPU against the oracle, through the C ABI:
+per-block quantization, silu * up requantization, the dense product in both its
+forms, and the product over expert segments."""
+import numpy as np
+import pytest
+import torch
+
+import int4_weight_quantized_w4_gb300 as w4
+import oracle as O
+import synthetic as S
+from _compare import check_bf16_output
+from _gpu import bf16, bits, requires_cuda, to_dev
+
+pytestmark = [pytest.mark.gpu, requires_cuda]
+
+
+def codes(t):
+    return t.view(torch.uint8).cpu().numpy()
+
+
+def fp8(a):
+    return to_dev(a).view(torch.float8_e4m3fn)
+
+
+def weights(N, K, seed=1, E=None):
+    """Random e4m3 codes of magnitude up to 1 and block scales around 0.02."""
+    lead = () if E is None else (E,)
+    q = S.fp8_codes(lead + (N, K), seed=seed)
+    q = (q & 0x80) | (q & 0x7F) % 0x39
+    s = S.scales_f16(lead + (-(-N // 128), -(-K // 128)), seed=seed + 1).astype(np.float32) * np.float32(1.0001)
+    return q.astype(np.uint8), s
+
+
+def rows(M, K, seed=0):
+    x = S.activations_bf16(M, K, seed=seed, outlier_frac=0.01)
+    q, s = O.quant_fp8_per_block(x)
+    return x, q, s
+
+
+# ---- quantizers -------------------------------------------------------------
+
+@pytest.mark.parametrize("M,K", [(1, 8), (3, 16), (1, 128), (2, 136), (7, 264), (5, 504), (129, 1408), (33, 4096),
+                                 (1, 8200), (1031, 520)])
+@pytest.mark.parametrize("f16", [False, True])
+def test_quant_per_block_bit_exact(M, K, f16):
+    """Codes and scales, with a zero row and a zero block among them."""
+    if f16:
+        x = S.bf16_bits_to_f32(S.activations_bf16(M, K, seed=K)).astype(np.float16)
+        x[M // 2, :128] = 0
+        t = to_dev(x)
+    else:
+        x = S.activations_bf16(M, K, seed=K, outlier_frac=0.02)
+        x[M // 2, :128] = 0
+        t = bf16(x)
+    q, s = w4.w4_quant_act_per_block(t)
+    torch.cuda.synchronize()
+    rq, rs = O.quant_fp8_per_block(x)
+    np.testing.assert_array_equal(s.cpu().numpy(), rs)
+    np.testing.assert_array_equal(codes(q), rq)
+
+
+def test_quant_per_block_extremes():
+    """Blocks of subnormals, of the largest bf16 values, and of equal magnitudes."""
+    x = np.zeros((4, 256), np.uint16)
+    x[0, :128] = S.raw_u64(3, 1, 128) % 128                      # bf16 subnormals
+    x[0, 128:] = 0x7F7F                                          # the largest finite value
+    x[1, :] = np.where(np.arange(256) % 2, 0x8001, 0x0001)       # the smallest subnormal, both signs
+    x[2, ::3] = 0x3F80
+    x[3, :] = S.activations_bf16(1, 256, seed=9, std=1e-30)[0]
+    q, s = w4.w4_quant_act_per_block(bf16(x))
+    torch.cuda.synchronize()
+    rq, rs = O.quant_fp8_per_block(x)
+    np.testing.assert_array_equal(s.cpu().numpy(), rs)
+    keep = rs.repeat(128, axis=1) > 0                            # a scale that underflowed to 0 divides by 0
+    np.testing.assert_array_equal(codes(q)[keep], rq[keep])
+
+
+@pytest.mark.parametrize("R,I", [(1, 8), (3, 128), (5, 200), (64, 1408), (1000, 136)])
+def test_silu_mul_quant_block(R, I):
+    """fp32 silu with the fast exponential is within 2^-19 of the definition
+    where it matters, so scales are within 2^-19 and a code moves by one step at
+    most, on few elements."""
+    h = S.activations_bf16(R, 2 * I, seed=R + I, std=3.0)
+    h[R // 2] = 0
+    q, s = w4.w4_silu_mul_quant_block(bf16(h))
+    torch.cuda.synchronize()
+    act = O.silu_mul_f64(h).astype(np.float32)
+    for b in range(-(-I // 128)):
+        c = slice(b * 128, min(I, (b + 1) * 128))
+        amax = np.abs(act[:, c]).max(axis=1)
+        rs = np.where(amax == 0, 1.0, amax.astype(np.float64) / 448)
+        np.testing.assert_allclose(s.cpu().numpy()[:, b], rs, rtol=2.0 ** -19)
+        ref = O.e4m3_encode(act[:, c].astype(np.float64) / rs[:, None]).astype(np.int64)
+        got = codes(q)[:, c].astype(np.int64)
+        same_sign = ((ref ^ got) & 0x80) == 0
+        step = np.abs((ref & 0x7F) - (got & 0x7F))
+        assert np.all((step <= 1) & (same_sign | (step + (ref & 0x7F) <= 1)))
+        assert np.mean(step == 0) >= 0.999 or step.sum() <= 1
+
+
+# ---- dense ------------------------------------------------------------------
+
+@pytest.mark.parametrize("M,N,K", [
+    (1, 8, 16), (1, 128, 128), (1, 136, 144), (1, 2056, 1408), (2, 264, 400), (5, 2048, 1408), (16, 520, 2064),
+    (17, 384, 1024), (31, 1000, 272), (33, 136, 1552), (64, 2056, 2048), (65, 264, 640), (100, 1032, 4112),
+    (128, 128, 128), (129, 8, 16), (129, 264, 144), (200, 520, 1408), (257, 1032, 272), (300, 776, 2064),
+    (513, 2056, 640), (1, 4096, 8208), (640, 10240, 256)])
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_gemm_matches_oracle(M, N, K, with_bias):
+    _, q, s = rows(M, K, seed=M + N)
+    qw, sw = weights(N, K, seed=K)
+    b = S.bias_bf16(N) if with_bias else None
+    y = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    w4.w4_fp8_block_gemm(fp8(q), to_dev(s), fp8(qw), to_dev(sw), bias=None if b is None else bf16(b), y=y)
+    torch.cuda.synchronize()
+    assert w4.w4_device_status() == w4.W4_OK
+    check_bf16_output(bits(y), O.fp8_block_linear(q, s, qw, sw, b), f"fp8 block gemm {M}x{N}x{K}")
+
+
+@pytest.mark.parametrize("M", [1, 15, 16, 32, 48, 64, 127, 128, 130, 383])
+def test_gemm_every_token_count(M):
+    """Each token-tile width and its edges, on one weight."""
+    N, K = 392, 1168
+    _, q, s = rows(M, K, seed=M)
+    qw, sw = weights(N, K, seed=3)
+    y = w4.w4_fp8_block_gemm(fp8(q), to_dev(s), fp8(qw), to_dev(sw))
+    torch.cuda.synchronize()
+    check_bf16_output(bits(y), O.fp8_block_linear(q, s, qw, sw), f"M={M}")
+
+
+@pytest.mark.parametrize("M,N,K,f16", [(1, 2056, 1408, False), (40, 1032, 2064, True), (300, 776, 1040, False)])
+def test_gemm_bf16in_equals_quant_then_gemm(M, N, K, f16):
+    x = S.activations_bf16(M, K, seed=M, outlier_frac=0.01)
+    t = to_dev(S.bf16_bits_to_f32(x).astype(np.float16)) if f16 else bf16(x)
+    qw, sw = weights(N, K, seed=5)
+    b = bf16(S.bias_bf16(N))
+    q, s = w4.w4_quant_act_per_block(t)
+    y2 = w4.w4_fp8_block_gemm(q, s, fp8(qw), to_dev(sw), bias=b)
+    first = w4.w4_fp8_block_gemm_bf16in(t, fp8(qw), to_dev(sw), bias=b)
+    for _ in range(5):     # back to back, into the same freshly freed memory: the quantizer of one call and the product of the last
+        y = w4.w4_fp8_block_gemm_bf16in(t, fp8(qw), to_dev(sw), bias=b)
+    torch.cuda.synchronize()
+    np.testing.assert_array_equal(bits(first), bits(y2))
+    np.testing.assert_array_equal(bits(y), bits(y2))
+    r = O.fp8_block_linear(codes(q), s.cpu().numpy(), qw, sw, S.bias_bf16(N))
+    check_bf16_output(bits(y), r, "bf16in")
+
+
+def test_gemm_infinite_and_nan_rows_stay_in_their_rows():
+    """A token whose codes are NaN gives NaN in its row only, in both forms."""
+    N, K = 264, 400
+    qw, sw = weights(N, K, seed=8)
+    for M in (20, 200):
+        _, q, s = rows(M, K, seed=M)
+        q[3, 5] = 0x7F
+        s[7, 1] = np.inf
+        y = w4.w4_fp8_block_gemm(fp8(q), to_dev(s), fp8(qw), to_dev(sw)).float().cpu().numpy()
+        assert np.isnan(y[3]).all() and not np.isfinite(y[7]).any()
+        good = [m for m in range(M) if m not in (3, 7)]
+        assert np.isfinite(y[good]).all()
+        r = O.fp8_block_linear(q[good], s[good], qw, sw)
+        np.testing.assert_allclose(y[good], r, rtol=8e-3, atol=8e-5 * np.sqrt(np.mean(r * r)) / 8e-3)
+
+
+def test_gemm_on_another_stream():
+    M, N, K = 24, 1032, 1408
+    x = S.activations_bf16(M, K, seed=11)
+    qw, sw = weights(N, K, seed=12)
+    t, qd, sd = bf16(x), fp8(qw), to_dev(sw)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    y = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty((w4.w4_workspace_bytes(w4.W4_OP_FP8_BLOCK, M, N, K, 0),), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    w4.w4_fp8_block_gemm_bf16in(t, qd, sd, y=y, workspace=ws, stream=st)
+    st.synchronize()
+    q, s = O.quant_fp8_per_block(x)
+    check_bf16_output(bits(y), O.fp8_block_linear(q, s, qw, sw), "side stream")
+
+
+def test_gemm_in_a_cuda_graph():
+    M, N, K = 4, 520, 1040
+    x = S.activations_bf16(M, K, seed=13)
+    qw, sw = weights(N, K, seed=14)
+    t, qd, sd = bf16(x), fp8(qw), to_dev(sw)
+    ref = w4.w4_fp8_block_gemm_bf16in(t, qd, sd)
+    y = torch.zeros_like(ref)
+    ws = torch.empty((w4.w4_workspace_bytes(w4.W4_OP_FP8_BLOCK, M, N, K, 0),), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        w4.w4_fp8_block_gemm_bf16in(t, qd, sd, y=y, workspace=ws)
+    for _ in range(3):
+        y.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        np.testing.assert_array_equal(bits(y), bits(ref))
+
+
+def test_gemm_empty():
+    qw, sw = weights(128, 128)
+    y = w4.w4_fp8_block_gemm_bf16in(torch.empty((0, 128), dtype=torch.bfloat16, device="cuda"), fp8(qw), to_dev(sw))
+    assert tuple(y.shape) == (0, 128)
+
+
+# ---- experts ----------------------------------------------------------------
+
+COUNTS = [
+    [1], [0, 3, 0], [16, 1, 0, 17, 5], [2] * 40 + [0] * 8, [40, 0, 25, 31], [70, 1, 64, 65], [128, 127, 129, 0, 3],
+    [300, 0, 1, 200], [0, 0, 700], [1000, 0, 0, 0, 0, 0, 0, 1], [0] * 100 + [5] + [0] * 899 + [260],
+]
+
+
+@pytest.mark.parametrize("counts", COUNTS, ids=lambda c: f"{len(c)}x{sum(c)}")
+@pytest.mark.parametrize("N,K", [(264, 400), (136, 16)])
+def test_grouped_matches_oracle(counts, N, K):
+    if len(counts) > 500 and K > 100:
+        N, K = 16, 144
+    off = S.offsets_from_counts(counts)
+    R, E = int(off[-1]), len(counts)
+    _, q, s = rows(R, K, seed=R)
+    qw, sw = weights(N, K, seed=E, E=E)
+    y = torch.full((R, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    w4.w4_fp8_block_moe_grouped_gemm(fp8(q), to_dev(s), to_dev(off), fp8(qw), to_dev(sw), y=y)
+    torch.cuda.synchronize()
+    assert w4.w4_device_status() == w4.W4_OK
+    check_bf16_output(bits(y), O.fp8_block_grouped_linear(q, s, off, qw, sw), f"{counts[:8]}")
+
+
+@pytest.mark.parametrize("R", [30, 700])
+def test_grouped_leaves_rows_outside_the_segments(R):
+    """Rows before the first and past the last offset keep what y held; offsets
+    past R are clipped."""
+    N, K, E = 136, 144, 2
+    _, q, s = rows(R, K, seed=R)
+    qw, sw = weights(N, K, seed=2, E=E)
+    for off in ([5, 9, R - 4], [5, 9, R + 100]):
+        off = np.array(off, np.int32)
+        y = torch.full((R, N), 7.0, dtype=torch.bfloat16, device="cuda")
+        w4.w4_fp8_block_moe_grouped_gemm(fp8(q), to_dev(s), to_dev(off), fp8(qw), to_dev(sw), y=y)
+        torch.cuda.synchronize()
+        end = min(int(off[-1]), R)
+        got = y.float().cpu().numpy()
+        assert np.all(got[:5] == 7) and np.all(got[end:] == 7)
+        off[-1] = end
+        check_bf16_output(bits(y)[5:end], O.fp8_block_grouped_linear(q, s, off, qw, sw)[5:end], "clipped")
+
+
+@pytest.mark.parametrize("T,E,k,N,K", [(1, 8, 2, 264, 256), (24, 64, 8, 136, 400), (300, 8, 4, 520, 272)])
+def test_grouped_bf16in_equals_gather_quant_gemm(T, E, k, N, K):
+    x = S.activations_bf16(T, K, seed=T)
+    _, _, off, rt, _ = w4.w4_moe_route(to_dev(S.router_logits(T, E, seed=E)), k)
+    qw, sw = weights(N, K, seed=7, E=E)
+    y = w4.w4_fp8_block_moe_gemm_bf16in(bf16(x), rt, off, fp8(qw), to_dev(sw))
+    g = bf16(x)[rt.long()].contiguous()
+    q, s = w4.w4_quant_act_per_block(g)
+    y2 = w4.w4_fp8_block_moe_grouped_gemm(q, s, off, fp8(qw), to_dev(sw))
+    torch.cuda.synchronize()
+    np.testing.assert_array_equal(bits(y), bits(y2))
+    r = O.fp8_block_grouped_linear(codes(q), s.cpu().numpy(), off.cpu().numpy(), qw, sw)
+    check_bf16_output(bits(y), r, "grouped bf16in")
+
+
+def test_grouped_bf16in_bad_row():
+    """A row_token entry outside [0, T) is a zero row and sets the status word."""
+    T, E, N, K = 6, 2, 136, 144
+    x = S.activations_bf16(T, K, seed=1)
+    qw, sw = weights(N, K, seed=7, E=E)
+    rt, off = np.array([0, 6, 3, -1, 5], np.int32), np.array([0, 2, 5], np.int32)
+    assert w4.w4_device_status() == w4.W4_OK
+    y = w4.w4_fp8_block_moe_gemm_bf16in(bf16(x), to_dev(rt), to_dev(off), fp8(qw), to_dev(sw))
+    assert w4.w4_device_status() == w4.W4_ERR_SHAPE
+    q, s = O.quant_fp8_per_block(x[[0, 0, 3, 0, 5]])
+    r = O.fp8_block_grouped_linear(q, s, off, qw, sw)
+    r[[1, 3]] = 0
+    got = bits(y)
+    assert not (got[[1, 3]] & 0x7FFF).any()
+    check_bf16_output(got, r, "bad rows")
