@@ -72,8 +72,9 @@ typedef enum {
 typedef enum {
   W4_OP_W4A8 = 0,           /* w4a8_gemm and w4a8_group_partials */
   W4_OP_W4AFP8_MOE = 1,     /* w4afp8_moe_grouped_gemm, w4afp8_moe_gemm_bf16in (M = R, the row count) */
-  W4_OP_MOE_ROUTE = 2,      /* w4_moe_route, w4_moe_route_grouped (M = T tokens, N = E experts; K = 1, group ignored) */
-  W4_OP_FP8_BLOCK = 3       /* w4_fp8_block_gemm_bf16in, w4_fp8_block_moe_gemm_bf16in (M = rows; N, group ignored) */
+  W4_OP_MOE_ROUTE = 2,      /* w4_moe_route (M = T tokens, N = E experts; K = 1, group ignored) */
+  W4_OP_MOE_ROUTE_GROUPED = 3, /* w4_moe_route_grouped (M = T tokens, N = E experts; K = 1, group ignored) */
+  W4_OP_FP8_BLOCK = 4       /* w4_fp8_block_gemm_bf16in (group ignored), w4_fp8_block_moe_gemm_bf16in (M = R rows, group = E) */
 } w4_op;
 
 /* Router scores of w4_moe_route_grouped. */
@@ -351,8 +352,10 @@ w4_status w4_moe_combine(const void* y, int64_t R, int64_t H, const float* topk_
 
 /*
  * w4_moe_route_grouped: routing with sigmoid or softmax scores, a balance bias
- * and expert groups. Outputs, layouts and workspace as w4_moe_route, so every
- * expert entry point takes its row order.
+ * and expert groups. Outputs and their layouts as w4_moe_route, so every expert
+ * entry point takes its row order. workspace: at least w4_workspace_bytes(
+ * W4_OP_MOE_ROUTE_GROUPED, T, E, 1, 0) bytes, 4-byte aligned (0 bytes for few
+ * tokens: it may then be NULL).
  *
  *   score[e]  sigmoid(logit) or softmax over all E experts (scoring)
  *   key[e]    what the choice goes by: the logit itself (bias NULL), or
@@ -429,8 +432,9 @@ w4_status w4_fp8_block_gemm(const void* qx, const float* x_scale, const void* qw
  * w4_fp8_block_gemm_bf16in: w4_quant_act_per_block and w4_fp8_block_gemm in one
  * call: x [M, K] bf16 or fp16 (x_dtype), its codes and scales in the workspace
  * (at least w4_workspace_bytes(W4_OP_FP8_BLOCK, M, N, K, 0) bytes, 16-byte
- * aligned). y equals the two calls' bit for bit. The product's weights start
- * streaming while x is being quantized.
+ * aligned; 0 bytes for few rows, where the product quantizes x itself and the
+ * workspace may be NULL). y equals the two calls' bit for bit. The product's
+ * weights start streaming while x is being quantized.
  */
 w4_status w4_fp8_block_gemm_bf16in(const void* x, int32_t x_dtype, const void* qweight, const float* w_scale,
                                    const void* bias, void* y, int64_t M, int64_t N, int64_t K, void* workspace,
@@ -450,7 +454,7 @@ w4_status w4_fp8_block_moe_grouped_gemm(const void* qx, const float* x_scale, co
 /*
  * w4_fp8_block_moe_gemm_bf16in: row r is token row_token[r] of x [T, K] bf16
  * (row_token NULL: R == T and row r is token r), quantized per block into the
- * workspace (at least w4_workspace_bytes(W4_OP_FP8_BLOCK, R, N, K, 0) bytes),
+ * workspace (at least w4_workspace_bytes(W4_OP_FP8_BLOCK, R, N, K, E) bytes),
  * then w4_fp8_block_moe_grouped_gemm. A row_token entry outside [0, T) gives a
  * zero row and sets W4_ERR_SHAPE in the device status word.
  */

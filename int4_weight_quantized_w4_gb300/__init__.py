@@ -27,13 +27,13 @@ __all__ = [
     "w4_device_status", "w4_selftest_bounded_wait", "apply_weights", "MIN_TOKENS_FOR_INT8",
     "W4_OK", "W4_ERR_NULL", "W4_ERR_ALIGN", "W4_ERR_GROUP", "W4_ERR_DTYPE",
     "W4_ERR_UNSUPPORTED", "W4_ERR_SHAPE", "W4_ERR_CUDA", "W4_ERR_TIMEOUT", "W4_ERR_WORKSPACE",
-    "W4_OP_W4A8", "W4_OP_W4AFP8_MOE", "W4_OP_MOE_ROUTE", "W4_OP_FP8_BLOCK", "w4_workspace_bytes", "EXPORTED_SYMBOLS",
+    "W4_OP_W4A8", "W4_OP_W4AFP8_MOE", "W4_OP_MOE_ROUTE", "W4_OP_MOE_ROUTE_GROUPED", "W4_OP_FP8_BLOCK", "w4_workspace_bytes", "EXPORTED_SYMBOLS",
 ]
 
 (W4_OK, W4_ERR_NULL, W4_ERR_ALIGN, W4_ERR_GROUP, W4_ERR_DTYPE, W4_ERR_UNSUPPORTED,
  W4_ERR_SHAPE, W4_ERR_CUDA, W4_ERR_TIMEOUT, W4_ERR_WORKSPACE) = range(10)
 W4_BF16, W4_FP16, W4_INT8, W4_FP8_E4M3 = range(4)
-W4_OP_W4A8, W4_OP_W4AFP8_MOE, W4_OP_MOE_ROUTE, W4_OP_FP8_BLOCK = range(4)
+W4_OP_W4A8, W4_OP_W4AFP8_MOE, W4_OP_MOE_ROUTE, W4_OP_MOE_ROUTE_GROUPED, W4_OP_FP8_BLOCK = range(5)
 W4_SCORE_SIGMOID, W4_SCORE_SOFTMAX = range(2)
 
 _DIR = os.path.dirname(os.path.abspath(__file__))
@@ -114,6 +114,16 @@ def _stream(stream, device):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _raw_stream(stream, device):
+    """The handle of ``stream``, or of the device's current stream (2 us less than
+    through a Stream object)."""
+    if stream is not None:
+        return stream.cuda_stream
+    if device.index is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -141,6 +151,27 @@ def _expect(t, name, shape, dtypes, device, optional=False):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if dtypes is not None and t.dtype not in dtypes:
         raise ValueError(f"{name} must have dtype in {dtypes}, got {t.dtype}")
+
+
+def _out(t, name, shape, dtype, dtypes, device):
+    """``t`` checked as by ``_expect``, or a new tensor when it is None."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _expect(t, name, shape, dtypes, device)
+    return t
+
+
+def _scratch(ws, op, M, N, K, group, device):
+    """A workspace for a call and its size; none (None, 0) where none is needed."""
+    if ws is None:
+        need = load().w4_workspace_bytes(op, M, N, K, group)
+        return (torch.empty(need, dtype=torch.uint8, device=device), need) if need else (None, 0)
+    _expect(ws, "workspace", None, None, device)   # the library checks its size in bytes
+    return ws, ws.numel() * ws.element_size()
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _groups(K, group):
@@ -383,6 +414,7 @@ def w4_moe_route(logits, top_k: int, renormalize: bool = False, out=None, worksp
 
 
 _SCORING = {"sigmoid": W4_SCORE_SIGMOID, "softmax": W4_SCORE_SOFTMAX}
+_LOGIT_T, _ACT_T = (torch.bfloat16, torch.float32), (torch.bfloat16, torch.float16)
 
 
 def w4_moe_route_grouped(logits, top_k: int, bias=None, n_group: int = 1, topk_group: int = 1,
@@ -394,61 +426,35 @@ def w4_moe_route_grouped(logits, top_k: int, bias=None, n_group: int = 1, topk_g
     groups of consecutive experts. Weights are the scores, renormalized over the
     chosen if asked, times ``scale``. Returns (and takes as ``out``) the tuple of
     ``w4_moe_route``: ``(topk_ids, topk_weights, offsets, row_token, row_of)``."""
-    _cuda2d(logits, "logits", (torch.bfloat16, torch.float32))
+    _cuda2d(logits, "logits", _LOGIT_T)
     if scoring not in _SCORING:
         raise ValueError("scoring must be 'sigmoid' or 'softmax'")
     T, E = logits.shape
     dev = logits.device
-    _expect(bias, "bias", (E,), _F32, dev, optional=True)
+    if bias is not None:
+        _expect(bias, "bias", (E,), _F32, dev)
     if out is None:
-        out = (torch.empty((T, top_k), dtype=torch.int32, device=dev),
-               torch.empty((T, top_k), dtype=torch.float32, device=dev),
-               (torch.empty if T else torch.zeros)((E + 1,), dtype=torch.int32, device=dev),
-               torch.empty((T * top_k,), dtype=torch.int32, device=dev),
-               torch.empty((T, top_k), dtype=torch.int32, device=dev))
-    ids, wts, off, rt, ro = out
-    _expect(ids, "topk_ids", (T, top_k), _I32T, dev)
-    _expect(wts, "topk_weights", (T, top_k), _F32, dev)
-    _expect(off, "offsets", (E + 1,), _I32T, dev)
-    _expect(rt, "row_token", (T * top_k,), _I32T, dev)
-    _expect(ro, "row_of", (T, top_k), _I32T, dev)
-    ws, wsb = _workspace(workspace, W4_OP_MOE_ROUTE, T, E, 1, 0, dev)
-    _check(load().w4_moe_route_grouped(_ptr(logits), int(logits.dtype == torch.float32), _ptr(bias), T, E, top_k,
-                                       n_group, topk_group, _SCORING[scoring], int(bool(renormalize)), scale,
-                                       _ptr(ids), _ptr(wts), _ptr(off), _ptr(rt), _ptr(ro), _ptr(ws), wsb,
-                                       _stream(stream, dev)), "w4_moe_route_grouped")
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+        wts = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+        off = (torch.empty if T else torch.zeros)(E + 1, dtype=torch.int32, device=dev)
+        rt = torch.empty(T * top_k, dtype=torch.int32, device=dev)
+        ro = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+        out = ids, wts, off, rt, ro
+    else:
+        ids, wts, off, rt, ro = out
+        _expect(ids, "topk_ids", (T, top_k), _I32T, dev)
+        _expect(wts, "topk_weights", (T, top_k), _F32, dev)
+        _expect(off, "offsets", (E + 1,), _I32T, dev)
+        _expect(rt, "row_token", (T * top_k,), _I32T, dev)
+        _expect(ro, "row_of", (T, top_k), _I32T, dev)
+    ws, wsb = _scratch(workspace, W4_OP_MOE_ROUTE_GROUPED, T, E, 1, 0, dev)
+    st = load().w4_moe_route_grouped(logits.data_ptr(), logits.dtype == torch.float32, _addr(bias), T, E, top_k, n_group,
+                                     topk_group, _SCORING[scoring], bool(renormalize), scale, ids.data_ptr(),
+                                     wts.data_ptr(), off.data_ptr(), rt.data_ptr(), ro.data_ptr(), _addr(ws), wsb,
+                                     _raw_stream(stream, dev))
+    if st:
+        _check(st, "w4_moe_route_grouped")
     return out
-
-
-def w4_quant_act_per_block(x, q=None, scale=None, stream=None):
-    """e4m3 quantization of bf16 or fp16 ``x [M, K]`` with one scale per row and
-    128 columns; returns ``(q float8_e4m3fn [M, K], scale fp32 [M, ceil(K/128)])``."""
-    _cuda2d(x, "x", (torch.bfloat16, torch.float16))
-    M, K = x.shape
-    q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=x.device) if q is None else q
-    scale = torch.empty((M, _blocks(K)), dtype=torch.float32, device=x.device) if scale is None else scale
-    _expect(q, "q", (M, K), _FP8_T, x.device)
-    _expect(scale, "scale", (M, _blocks(K)), _F32, x.device)
-    _check(load().w4_quant_act_per_block(_ptr(x), _act_dtype(x), M, K, _ptr(q), _ptr(scale),
-                                         _stream(stream, x.device)), "w4_quant_act_per_block")
-    return q, scale
-
-
-def w4_silu_mul_quant_block(h, q=None, scale=None, stream=None):
-    """``silu(gate) * up`` of the bf16 gate_up output ``h [R, 2I]``, quantized to
-    e4m3 per row and 128 columns; returns ``(q [R, I], scale [R, ceil(I/128)])``."""
-    _cuda2d(h, "h", (torch.bfloat16,))
-    R, I2 = h.shape
-    if I2 % 2:
-        raise ValueError("h must hold gate and up halves of equal width")
-    I = I2 // 2
-    q = torch.empty((R, I), dtype=torch.float8_e4m3fn, device=h.device) if q is None else q
-    scale = torch.empty((R, _blocks(I)), dtype=torch.float32, device=h.device) if scale is None else scale
-    _expect(q, "q", (R, I), _FP8_T, h.device)
-    _expect(scale, "scale", (R, _blocks(I)), _F32, h.device)
-    _check(load().w4_silu_mul_quant_block(_ptr(h), R, I, _ptr(q), _ptr(scale), _stream(stream, h.device)),
-           "w4_silu_mul_quant_block")
-    return q, scale
 
 
 def _blocks(n):
@@ -459,16 +465,48 @@ def _act_dtype(x):
     return W4_FP16 if x.dtype == torch.float16 else W4_BF16
 
 
-def _block_weight_args(what, qweight, w_scale, K, device, bias=None):
+def w4_quant_act_per_block(x, q=None, scale=None, stream=None):
+    """e4m3 quantization of bf16 or fp16 ``x [M, K]`` with one scale per row and
+    128 columns; returns ``(q float8_e4m3fn [M, K], scale fp32 [M, ceil(K/128)])``."""
+    _cuda2d(x, "x", _ACT_T)
+    M, K = x.shape
+    dev = x.device
+    q = _out(q, "q", (M, K), torch.float8_e4m3fn, _FP8_T, dev)
+    scale = _out(scale, "scale", (M, _blocks(K)), torch.float32, _F32, dev)
+    st = load().w4_quant_act_per_block(x.data_ptr(), _act_dtype(x), M, K, q.data_ptr(), scale.data_ptr(),
+                                       _raw_stream(stream, dev))
+    if st:
+        _check(st, "w4_quant_act_per_block")
+    return q, scale
+
+
+def w4_silu_mul_quant_block(h, q=None, scale=None, stream=None):
+    """``silu(gate) * up`` of the bf16 gate_up output ``h [R, 2I]``, quantized to
+    e4m3 per row and 128 columns; returns ``(q [R, I], scale [R, ceil(I/128)])``."""
+    _cuda2d(h, "h", _BF16T)
+    R, I2 = h.shape
+    if I2 % 2:
+        raise ValueError("h must hold gate and up halves of equal width")
+    I = I2 // 2
+    dev = h.device
+    q = _out(q, "q", (R, I), torch.float8_e4m3fn, _FP8_T, dev)
+    scale = _out(scale, "scale", (R, _blocks(I)), torch.float32, _F32, dev)
+    st = load().w4_silu_mul_quant_block(h.data_ptr(), R, I, q.data_ptr(), scale.data_ptr(), _raw_stream(stream, dev))
+    if st:
+        _check(st, "w4_silu_mul_quant_block")
+    return q, scale
+
+
+def _block_weight_args(what, qweight, w_scale, K, device, bias):
     """e4m3 ``qweight [N, K]`` (float8_e4m3fn or uint8 codes) with fp32 ``w_scale
     [ceil(N/128), ceil(K/128)]`` and optional bf16 ``bias [N]``; returns N."""
-    _cuda2d(qweight, "qweight", _FP8_T)
-    N = qweight.shape[0]
-    if qweight.shape[1] != K:
+    _expect(qweight, "qweight", None, _FP8_T, device)
+    if qweight.dim() != 2 or qweight.shape[1] != K:
         raise ValueError(f"inconsistent shapes for {what}")
-    _expect(qweight, "qweight", None, None, device)
+    N = qweight.shape[0]
     _expect(w_scale, "w_scale", (_blocks(N), _blocks(K)), _F32, device)
-    _expect(bias, "bias", (N,), _BF16T, device, optional=True)
+    if bias is not None:
+        _expect(bias, "bias", (N,), _BF16T, device)
     return N
 
 
@@ -490,27 +528,30 @@ def w4_fp8_block_gemm(qx, x_scale, qweight, w_scale, bias=None, y=None, stream=N
     with fp32 ``w_scale [ceil(N/128), ceil(K/128)]``; returns bf16 ``[M, N]``."""
     _cuda2d(qx, "qx", _FP8_T)
     M, K = qx.shape
-    N = _block_weight_args("w4_fp8_block_gemm", qweight, w_scale, K, qx.device, bias)
-    _expect(x_scale, "x_scale", (M, _blocks(K)), _F32, qx.device)
-    y = torch.empty((M, N), dtype=torch.bfloat16, device=qx.device) if y is None else y
-    _expect(y, "y", (M, N), _BF16T, qx.device)
-    _check(load().w4_fp8_block_gemm(_ptr(qx), _ptr(x_scale), _ptr(qweight), _ptr(w_scale), _ptr(bias), _ptr(y), M, N, K,
-                                    _stream(stream, qx.device)), "w4_fp8_block_gemm")
+    dev = qx.device
+    N = _block_weight_args("w4_fp8_block_gemm", qweight, w_scale, K, dev, bias)
+    _expect(x_scale, "x_scale", (M, _blocks(K)), _F32, dev)
+    y = _out(y, "y", (M, N), torch.bfloat16, _BF16T, dev)
+    st = load().w4_fp8_block_gemm(qx.data_ptr(), x_scale.data_ptr(), qweight.data_ptr(), w_scale.data_ptr(), _addr(bias),
+                                  y.data_ptr(), M, N, K, _raw_stream(stream, dev))
+    if st:
+        _check(st, "w4_fp8_block_gemm")
     return y
 
 
 def w4_fp8_block_gemm_bf16in(x, qweight, w_scale, bias=None, y=None, workspace=None, stream=None):
     """fp8 block-scaled linear from bf16 or fp16 ``x [M, K]``, quantized per block
     inside the call; returns bf16 ``[M, N]``. One token is the decode call."""
-    _cuda2d(x, "x", (torch.bfloat16, torch.float16))
+    _cuda2d(x, "x", _ACT_T)
     M, K = x.shape
-    N = _block_weight_args("w4_fp8_block_gemm_bf16in", qweight, w_scale, K, x.device, bias)
-    y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device) if y is None else y
-    _expect(y, "y", (M, N), _BF16T, x.device)
-    ws, wsb = _workspace(workspace, W4_OP_FP8_BLOCK, M, N, K, 0, x.device)
-    _check(load().w4_fp8_block_gemm_bf16in(_ptr(x), _act_dtype(x), _ptr(qweight), _ptr(w_scale), _ptr(bias), _ptr(y),
-                                           M, N, K, _ptr(ws), wsb, _stream(stream, x.device)),
-           "w4_fp8_block_gemm_bf16in")
+    dev = x.device
+    N = _block_weight_args("w4_fp8_block_gemm_bf16in", qweight, w_scale, K, dev, bias)
+    y = _out(y, "y", (M, N), torch.bfloat16, _BF16T, dev)
+    ws, wsb = _scratch(workspace, W4_OP_FP8_BLOCK, M, N, K, 0, dev)
+    st = load().w4_fp8_block_gemm_bf16in(x.data_ptr(), _act_dtype(x), qweight.data_ptr(), w_scale.data_ptr(),
+                                         _addr(bias), y.data_ptr(), M, N, K, _addr(ws), wsb, _raw_stream(stream, dev))
+    if st:
+        _check(st, "w4_fp8_block_gemm_bf16in")
     return y
 
 
@@ -521,13 +562,15 @@ def w4_fp8_block_moe_grouped_gemm(qx, x_scale, expert_offsets, qweight, w_scale,
     ceil(N/128), ceil(K/128)]``; returns bf16 ``[R, N]``."""
     _cuda2d(qx, "qx", _FP8_T)
     R, K = qx.shape
-    E, N = _block_expert_args("w4_fp8_block_moe_grouped_gemm", qweight, w_scale, expert_offsets, K, qx.device)
-    _expect(x_scale, "x_scale", (R, _blocks(K)), _F32, qx.device)
-    y = torch.empty((R, N), dtype=torch.bfloat16, device=qx.device) if y is None else y
-    _expect(y, "y", (R, N), _BF16T, qx.device)
-    _check(load().w4_fp8_block_moe_grouped_gemm(_ptr(qx), _ptr(x_scale), _ptr(expert_offsets), E, _ptr(qweight),
-                                                _ptr(w_scale), _ptr(y), R, N, K, _stream(stream, qx.device)),
-           "w4_fp8_block_moe_grouped_gemm")
+    dev = qx.device
+    E, N = _block_expert_args("w4_fp8_block_moe_grouped_gemm", qweight, w_scale, expert_offsets, K, dev)
+    _expect(x_scale, "x_scale", (R, _blocks(K)), _F32, dev)
+    y = _out(y, "y", (R, N), torch.bfloat16, _BF16T, dev)
+    st = load().w4_fp8_block_moe_grouped_gemm(qx.data_ptr(), x_scale.data_ptr(), expert_offsets.data_ptr(), E,
+                                              qweight.data_ptr(), w_scale.data_ptr(), y.data_ptr(), R, N, K,
+                                              _raw_stream(stream, dev))
+    if st:
+        _check(st, "w4_fp8_block_moe_grouped_gemm")
     return y
 
 
@@ -535,17 +578,19 @@ def w4_fp8_block_moe_gemm_bf16in(x, row_token, expert_offsets, qweight, w_scale,
     """``w4_fp8_block_moe_grouped_gemm`` from bf16 token rows: row r is
     ``x[row_token[r]]`` (``row_token`` None: row r is token r), quantized per block
     inside the call. Returns bf16 ``[R, N]``."""
-    _cuda2d(x, "x", (torch.bfloat16,))
+    _cuda2d(x, "x", _BF16T)
     T, K = x.shape
-    _expect(row_token, "row_token", None, _I32T, x.device, optional=True)
+    dev = x.device
+    _expect(row_token, "row_token", None, _I32T, dev, optional=True)
     R = T if row_token is None else row_token.numel()
-    E, N = _block_expert_args("w4_fp8_block_moe_gemm_bf16in", qweight, w_scale, expert_offsets, K, x.device)
-    y = torch.empty((R, N), dtype=torch.bfloat16, device=x.device) if y is None else y
-    _expect(y, "y", (R, N), _BF16T, x.device)
-    ws, wsb = _workspace(workspace, W4_OP_FP8_BLOCK, R, N, K, 0, x.device)
-    _check(load().w4_fp8_block_moe_gemm_bf16in(_ptr(x), T, _ptr(row_token), _ptr(expert_offsets), E, _ptr(qweight),
-                                               _ptr(w_scale), _ptr(y), R, N, K, _ptr(ws), wsb,
-                                               _stream(stream, x.device)), "w4_fp8_block_moe_gemm_bf16in")
+    E, N = _block_expert_args("w4_fp8_block_moe_gemm_bf16in", qweight, w_scale, expert_offsets, K, dev)
+    y = _out(y, "y", (R, N), torch.bfloat16, _BF16T, dev)
+    ws, wsb = _scratch(workspace, W4_OP_FP8_BLOCK, R, N, K, E, dev)
+    st = load().w4_fp8_block_moe_gemm_bf16in(x.data_ptr(), T, _addr(row_token), expert_offsets.data_ptr(), E,
+                                             qweight.data_ptr(), w_scale.data_ptr(), y.data_ptr(), R, N, K, _addr(ws),
+                                             wsb, _raw_stream(stream, dev))
+    if st:
+        _check(st, "w4_fp8_block_moe_gemm_bf16in")
     return y
 
 

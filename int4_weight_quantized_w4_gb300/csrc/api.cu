@@ -129,7 +129,9 @@ size_t w4_workspace_bytes(int32_t op, int64_t M, int64_t N, int64_t K, int32_t g
     return w4::w4a8_workspace_bytes(M, K);
   }
   if (op == W4_OP_W4AFP8_MOE) return w4::w4a8_workspace_bytes(M, K);
-  if (op == W4_OP_FP8_BLOCK) return w4::fp8_block_workspace_bytes(M, K);
+  if (op == W4_OP_MOE_ROUTE_GROUPED)
+    return (N > 0 && N <= 1024) ? w4::moe_route_grouped_workspace_bytes(M, static_cast<int32_t>(N)) : 0;
+  if (op == W4_OP_FP8_BLOCK) return w4::fp8_block_fuses(M, group > 0) ? 0 : w4::fp8_block_workspace_bytes(M, K);
   if (op == W4_OP_MOE_ROUTE) return (N > 0 && N <= 1024) ? w4::moe_route_workspace_bytes(M, static_cast<int32_t>(N)) : 0;
   return 0;
 }
@@ -412,8 +414,8 @@ w4_status w4_moe_route_grouped(const void* logits, int32_t logits_f32, const flo
   if (!aligned(logits, logits_f32 ? 4 : 2) || !aligned(bias, 4) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4) ||
       !aligned(offsets, 4) || !aligned(row_token, 4) || !aligned(row_of, 4))
     return fail(W4_ERR_ALIGN, "route buffers must be aligned to their element size");
-  const size_t need = w4::moe_route_workspace_bytes(T, E);
-  if (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 4))
+  const size_t need = w4::moe_route_grouped_workspace_bytes(T, E);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 4)))
     return fail(W4_ERR_WORKSPACE, "route workspace must be 4-byte aligned and at least %zu bytes (got %zu)", need,
                 workspace_bytes);
   const w4::MoeRouteArgs a{logits,      bias,         T,       E,         top_k,  n_group,  topk_group, logits_f32 == 0,
@@ -480,7 +482,7 @@ static w4_status run_fp8_block(const void* qx, const float* x_scale, const int32
   unsigned int* status = nullptr;
   cudaError_t e = status_ptr(&status);
   if (e != cudaSuccess) return from_cuda(e, "device status word");
-  const w4::Fp8BlockArgs a{qx, x_scale, qweight, w_scale, bias, y, offsets, E, R, N, K, false, status};
+  const w4::Fp8BlockArgs a{qx, x_scale, qweight, w_scale, bias, y, offsets, E, R, N, K, nullptr, false, false, status};
   return from_cuda(w4::launch_fp8_block(a, static_cast<cudaStream_t>(stream)), "fp8 block product launch");
 }
 
@@ -492,16 +494,21 @@ static w4_status run_fp8_block_act(const void* x, bool f16, int64_t T, const int
   if (!aligned(x, 16) || !aligned(qweight, 16) || !aligned(y, 16) || !aligned(w_scale, 4) || !aligned(offsets, 4) ||
       !aligned(rows, 4) || !aligned(bias, 16))
     return fail(W4_ERR_ALIGN, "matrices and the bias must be 16-byte aligned, scales, rows and offsets 4-byte aligned");
-  w4_status st = check_block_workspace(ws, ws_bytes, R, K);
+  const bool fused = w4::fp8_block_fuses(R, offsets != nullptr);   // few rows: the product quantizes, no workspace
+  w4_status st = fused ? W4_OK : check_block_workspace(ws, ws_bytes, R, K);
   if (st != W4_OK) return st;
   unsigned int* status = nullptr;
   cudaError_t e = status_ptr(&status);
   if (e != cudaSuccess) return from_cuda(e, "device status word");
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (fused) {
+    const w4::Fp8BlockArgs a{nullptr, nullptr, qweight, w_scale, bias, y, offsets, E, R, N, K, x, f16, false, status};
+    return from_cuda(w4::launch_fp8_block(a, s), "fp8 block product launch");
+  }
   float* x_scale = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + static_cast<size_t>(R) * K);   // K % 16 == 0
   e = w4::launch_quant_block(x, f16, false, R, K, rows, T, ws, x_scale, status, s);
   if (e != cudaSuccess) return from_cuda(e, "block quant launch");
-  const w4::Fp8BlockArgs a{ws, x_scale, qweight, w_scale, bias, y, offsets, E, R, N, K, true, status};
+  const w4::Fp8BlockArgs a{ws, x_scale, qweight, w_scale, bias, y, offsets, E, R, N, K, nullptr, false, true, status};
   return from_cuda(w4::launch_fp8_block(a, s), "fp8 block product launch");
 }
 

@@ -251,6 +251,23 @@ W4_DEV uint2 quant_e4m3_chunk(const uint4& v, const QuotientBracket& b) {
   return make_uint2(prmt(p[0], p[1], 0x5410u), prmt(p[2], p[3], 0x5410u));
 }
 
+// Per-block quantization: a half-warp holds a block of 128 columns of a row, one
+// chunk of 8 per lane. Scale fl(amax / 448), 1 for a block of zeros.
+W4_DEV float half_warp_max(float m) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+W4_DEV float block_scale(float amax) { return amax == 0.f ? 1.f : __fdiv_rn(amax, 448.f); }
+
+// This lane's e4m3 codes and the block's scale; every lane of the warp takes part.
+template <bool kF16>
+W4_DEV void quant_block_half_warp(const uint4& v, uint2& code, float& s) {
+  const uint32_t m2 = absmax2<kF16>(absmax2<kF16>(v.x, v.y), absmax2<kF16>(v.z, v.w));
+  s = block_scale(half_warp_max(fmaxf(fabsf(act_lo<kF16>(m2)), fabsf(act_hi<kF16>(m2)))));
+  code = quant_e4m3_chunk<kF16>(v, quotient_bracket(s));
+}
+
 // ---------------------------------------------------------------------------
 // global memory access
 // ---------------------------------------------------------------------------

@@ -10,7 +10,8 @@
 //
 // Two forms:
 //  * stream (few rows an expert or call): weights on the MMA's 128 rows (TMEM
-//    lane = output), NT tokens on its columns. Bound by the weight bytes.
+//    lane = output), NT tokens on its columns. Bound by the weight bytes. For up
+//    to kFuseRows dense rows the kernel quantizes 16-bit activations itself.
 //  * tile (many rows): 128 tokens on the MMA's rows, 256 outputs on its
 //    columns, so that one scale sx * sw serves a thread's whole column strip.
 //    Bound by the tensor core and by the drain of one accumulator per block.
@@ -27,12 +28,15 @@ namespace {
 
 constexpr int kBlk = 128;                     // k and weight rows per scale
 constexpr int kMaxExperts = 1024;
+constexpr int kFuseRows = 16;                 // up to this many dense rows the stream form quantizes
 constexpr uint64_t kWaitNs = 2000000000ull;   // 2 s per wait
 
 struct Params {
-  CUtensorMap tm_x;        // e4m3 codes [rows, K]
+  CUtensorMap tm_x;        // e4m3 codes [rows, K] (unused where the kernel quantizes)
   CUtensorMap tm_w;        // e4m3 codes [E, N, K]
   const float* x_scale;    // [rows, KB]
+  const uint4* x;          // 16-bit activations [rows, K] to quantize, or null
+  bool x_f16;
   const float* w_scale;    // [E, NB, KB]
   const uint16_t* bias;    // bf16 [N] or null
   uint16_t* y;             // bf16 [rows, N]
@@ -56,6 +60,11 @@ W4_DEV float ld_cluster_f32(uint32_t a, uint32_t rank) {
   asm volatile("{.reg .b32 t; mapa.shared::cluster.u32 t, %1, %2; ld.shared::cluster.f32 %0, [t];}"
                : "=f"(v) : "r"(a), "r"(rank) : "memory");
   return v;
+}
+// tc::wait by a whole warp with one answer: a warp whose lanes disagreed after a
+// time-out would not meet at its next warp-wide instruction.
+W4_DEV bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned int* status) {
+  return __all_sync(0xFFFFFFFFu, tc::wait(bar, parity, abort, status, kWaitNs));
 }
 W4_DEV void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
@@ -135,7 +144,7 @@ W4_DEV void mma_block(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
 // stream form
 // ---------------------------------------------------------------------------
 
-template <int NT>
+template <int NT, bool kQuant>
 struct Stream {
   static constexpr int A_BYTES = kBlk * 128;             // 128 outputs x 128 k
   static constexpr int B_BYTES = NT * 128;               // NT tokens x 128 k
@@ -143,22 +152,25 @@ struct Stream {
   static constexpr int STAGES = NT <= 32 ? 5 : NT == 64 ? 4 : 6;
   static constexpr int TMEM_COLS = CTAS == 2 ? 256 : 512;
   static constexpr int ACCS = TMEM_COLS / NT > 8 ? 8 : TMEM_COLS / NT;
-  static constexpr int SC_SLOTS = 4;                     // scale slots of 4 blocks x NT tokens
-  static constexpr int SC_BYTES = SC_SLOTS * 4 * NT * 4;
-  static constexpr int SMEM = STAGES * (A_BYTES + B_BYTES) + SC_BYTES + 512 + (kMaxExperts + 1 + 8 + 7) / 4 * 16 + 1024;
+  static constexpr int SC_PER = kQuant ? 1 : 4;          // blocks per scale slot (x NT tokens)
+  static constexpr int SC_SLOTS = kQuant ? 8 : 4;
+  static constexpr int SC_BYTES = SC_SLOTS * SC_PER * NT * 4;
+  static constexpr int THREADS = kQuant ? 320 : 256;
+  static constexpr int SMEM = STAGES * (A_BYTES + B_BYTES) + SC_BYTES + 512 + (kMaxExperts + 1 + 10 + 5) / 4 * 16 + 1024;
 };
-static_assert(Stream<16>::SMEM * 2 + 2048 <= 233472 && Stream<32>::SMEM * 2 + 2048 <= 233472 &&
-                  Stream<64>::SMEM * 2 + 2048 <= 233472 && Stream<128>::SMEM <= 232448,
+static_assert(Stream<16, true>::SMEM * 2 + 2048 <= 233472 && Stream<32, false>::SMEM * 2 + 2048 <= 233472 && Stream<64, false>::SMEM * 2 + 2048 <= 233472 &&
+                  Stream<128, false>::SMEM <= 232448,
               "shared memory per SM");
 
 // Warps 0-3 epilogue (warp w: TMEM lanes 32 w, outputs n0 + 32 w + lane), 4
-// weight copies, 5 activation copies, 6 MMA issuer and TMEM owner, 7 scales.
-constexpr int kSWarpA = 4, kSWarpB = 5, kSWarpMma = 6, kSWarpScale = 7;
-constexpr int kSThreads = 256;
+// weight copies, 5 MMA issuer and TMEM owner; then 6 activation copies and 7
+// scales, or (kQuant: dense, one row tile) 6-9 quantizers of alternate blocks.
+constexpr int kSWarpA = 4, kSWarpMma = 5, kSWarpB = 6, kSWarpScale = 7;
+constexpr int kQuantWarps = 4;
 
-template <int NT>
-__global__ void __launch_bounds__(kSThreads, Stream<NT>::CTAS) stream_kernel(const __grid_constant__ Params p) {
-  using C = Stream<NT>;
+template <int NT, bool kQuant>
+__global__ void __launch_bounds__(Stream<NT, kQuant>::THREADS, Stream<NT, kQuant>::CTAS) stream_kernel(const __grid_constant__ Params p) {
+  using C = Stream<NT, kQuant>;
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
   uint8_t* a_base = smem;
@@ -194,8 +206,8 @@ __global__ void __launch_bounds__(kSThreads, Stream<NT>::CTAS) stream_kernel(con
   }
   if (warp == kSWarpMma) tc::tmem_alloc(tmem_holder, C::TMEM_COLS);
   if (warp == kSWarpA && lane == 0) tc::prefetch_tmap(&p.tm_w);
-  if (warp == kSWarpB && lane == 0) tc::prefetch_tmap(&p.tm_x);
-  if (p.offsets != nullptr) tile_starts<kSThreads>(p, NT, starts, warp_sum);
+  if (!kQuant && warp == kSWarpB && lane == 0) tc::prefetch_tmap(&p.tm_x);
+  if (p.offsets != nullptr) tile_starts<C::THREADS>(p, NT, starts, warp_sum);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -219,6 +231,57 @@ __global__ void __launch_bounds__(kSThreads, Stream<NT>::CTAS) stream_kernel(con
           tc::tma_load_3d(a_base + st * C::A_BYTES, &p.tm_w, &full[st], kb * kBlk, t.n0, t.expert);
           if (++st == C::STAGES) st = 0, ph ^= 1;
         }
+    }
+  } else if (kQuant && warp >= kSWarpB) {
+    // Quantizer w takes blocks w, w + 4, ... of this CTA's sequence, a half-warp
+    // per row; the next block's rows are loaded before this one's are reduced.
+    if constexpr (kQuant) {
+      constexpr int RPH = NT / 2;                      // rows per half-warp
+      const int h = lane >> 4, l = lane & 15;
+      const int K8 = p.K >> 3, nkb = kb1 - kb0;
+      const long long items = first < p.items ? (p.items - first + step - 1) / step : 0;
+      const int total = static_cast<int>(items) * nkb;
+      auto load = [&](int g, uint4 (&v)[RPH]) {
+        const int c = (kb0 + g % nkb) * 16 + l;
+#pragma unroll
+        for (int i = 0; i < RPH; ++i) {
+          const int r = h + 2 * i;
+          v[i] = r < p.rows && c < K8 && g < total ? ld_nc_v4(p.x + static_cast<size_t>(r) * K8 + c) : make_uint4(0, 0, 0, 0);
+        }
+      };
+      uint4 cur[RPH], next[RPH];
+      load(warp - kSWarpB, cur);
+      for (int g = warp - kSWarpB; g < total; g += kQuantWarps) {
+        const int kb = kb0 + g % nkb;
+        const int nt = static_cast<int>((first + g / nkb * step) % p.n_tiles);
+        const float sw = __ldg(p.w_scale + static_cast<size_t>(nt) * p.KB + kb);
+        load(g + kQuantWarps, next);
+        const int st = g % C::STAGES, sl = g % C::SC_SLOTS;
+        if (!wait_warp(&empty[st], ((g / C::STAGES) & 1) ^ 1, abort_flag, p.status)) break;
+        if (!wait_warp(&sc_empty[sl], ((g / C::SC_SLOTS) & 1) ^ 1, abort_flag, p.status)) break;
+#pragma unroll
+        for (int i = 0; i < RPH; ++i) {
+          if (2 * i < p.rows) {          // the same for the whole warp
+            uint2 code;
+            float s;
+            if (p.x_f16)
+              quant_block_half_warp<true>(cur[i], code, s);
+            else
+              quant_block_half_warp<false>(cur[i], code, s);
+            const int r = h + 2 * i;     // a row past the last one fills a column that is never stored
+            *reinterpret_cast<uint2*>(b_base + st * C::B_BYTES + r * 128 + (((l >> 1) ^ (r & 7)) << 4) + (l & 1) * 8) = code;
+            if (l == 0) sc_base[sl * NT + r] = s * sw;
+          }
+        }
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&full[st]);
+          mbar_arrive(&sc_full[sl]);
+        }
+#pragma unroll
+        for (int i = 0; i < RPH; ++i) cur[i] = next[i];
+      }
     }
   } else if (warp == kSWarpB) {
     if (lane == 0) {
@@ -267,7 +330,7 @@ __global__ void __launch_bounds__(kSThreads, Stream<NT>::CTAS) stream_kernel(con
         float w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = kb + i < kb1 ? __ldg(sw + kb + i) : 0.f;
-        if (!(ok = tc::wait(&sc_empty[sl], ph, abort_flag, p.status, kWaitNs))) break;
+        if (!(ok = wait_warp(&sc_empty[sl], ph, abort_flag, p.status))) break;
         float* sc = sc_base + sl * 4 * NT;
 #pragma unroll
         for (int j0 = 0; j0 < NT; j0 += 32) {
@@ -295,12 +358,12 @@ __global__ void __launch_bounds__(kSThreads, Stream<NT>::CTAS) stream_kernel(con
 #pragma unroll
       for (int j = 0; j < NT; ++j) T[j] = 0.f;
       for (int kb = kb0; kb < kb1; ++kb) {
-        const int i = (kb - kb0) & 3;
-        if (i == 0 && !(ok = tc::wait(&sc_full[sl], sph, abort_flag, p.status, kWaitNs))) break;
-        if (!(ok = tc::wait(&acc_full[ac], aph, abort_flag, p.status, kWaitNs))) break;
+        const int i = (kb - kb0) & (C::SC_PER - 1);
+        if (i == 0 && !(ok = wait_warp(&sc_full[sl], sph, abort_flag, p.status))) break;
+        if (!(ok = wait_warp(&acc_full[ac], aph, abort_flag, p.status))) break;
         tc::fence_after_sync();
         const uint32_t ta = tmem + (static_cast<uint32_t>(32 * warp) << 16) + ac * NT;
-        const float* sc = sc_base + (sl * 4 + i) * NT;
+        const float* sc = sc_base + (sl * C::SC_PER + i) * NT;
 #pragma unroll
         for (int c = 0; c < NT; c += 16) {
           uint32_t v[16];
@@ -317,10 +380,10 @@ __global__ void __launch_bounds__(kSThreads, Stream<NT>::CTAS) stream_kernel(con
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&acc_empty[ac]);
-          if (i == 3 || kb == kb1 - 1) mbar_arrive(&sc_empty[sl]);
+          if (i == C::SC_PER - 1 || kb == kb1 - 1) mbar_arrive(&sc_empty[sl]);
         }
         if (++ac == C::ACCS) ac = 0, aph ^= 1;
-        if (i == 3 || kb == kb1 - 1) {
+        if (i == C::SC_PER - 1 || kb == kb1 - 1) {
           if (++sl == C::SC_SLOTS) sl = 0, sph ^= 1;
         }
       }
@@ -495,7 +558,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const __grid_constan
       for (int kb = 0; kb < KB; ++kb) {
         const float f = f0;
         f0 = f1, f1 = f2, f2 = f3, f3 = ld(kb + 4);
-        if (!(ok = tc::wait(&done[st], ph, abort_flag, p.status, kWaitNs))) break;
+        if (!(ok = wait_warp(&done[st], ph, abort_flag, p.status))) break;
         tc::fence_after_sync();
         const uint32_t ta = tmem + (static_cast<uint32_t>(32 * q) << 16) + buf * TN + 128 * half;
 #pragma unroll
@@ -615,10 +678,10 @@ cudaError_t start(void (*kernel)(Params), const Params& p, int64_t grid, int thr
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-template <int NT>
+template <int NT, bool kQuant>
 cudaError_t run_stream(const Fp8BlockArgs& a, Params& p, cudaStream_t s) {
-  using C = Stream<NT>;
-  cudaError_t e = encode(&p.tm_x, a.qx, a.K, a.R, 0, NT);
+  using C = Stream<NT, kQuant>;
+  cudaError_t e = kQuant ? cudaSuccess : encode(&p.tm_x, a.qx, a.K, a.R, 0, NT);
   if (e != cudaSuccess) return e;
   e = encode(&p.tm_w, a.qweight, a.K, a.N, a.E, kBlk);
   if (e != cudaSuccess) return e;
@@ -629,10 +692,12 @@ cudaError_t run_stream(const Fp8BlockArgs& a, Params& p, cudaStream_t s) {
   if (a.expert_offsets == nullptr)
     while (p.split < 8 && p.items * p.split * 2 <= slots && p.KB >= 4 * p.split) p.split *= 2;
   const int64_t grid = p.split > 1 ? p.items * p.split : (p.items < slots ? p.items : slots);
-  return start(stream_kernel<NT>, p, grid, kSThreads, C::SMEM, p.split, a.pdl, s);
+  return start(stream_kernel<NT, kQuant>, p, grid, C::THREADS, C::SMEM, p.split, a.pdl, s);
 }
 
 }  // namespace
+
+bool fp8_block_fuses(int64_t R, bool experts) { return !experts && R <= kFuseRows; }
 
 cudaError_t launch_fp8_block(const Fp8BlockArgs& a, cudaStream_t s) {
   Params p;
@@ -650,12 +715,14 @@ cudaError_t launch_fp8_block(const Fp8BlockArgs& a, cudaStream_t s) {
   p.NB = static_cast<int>((a.N + kBlk - 1) / kBlk);
   p.split = 1;
   p.status = a.status;
+  p.x = static_cast<const uint4*>(a.x);
+  p.x_f16 = a.x_f16;
   // rows a weight tile is used for, on average
-  const int64_t rows = a.expert_offsets == nullptr ? a.R : (a.R + a.E - 1) / a.E;
-  if (rows <= 16) return run_stream<16>(a, p, s);
-  if (rows <= 32) return run_stream<32>(a, p, s);
-  if (rows <= 64) return run_stream<64>(a, p, s);
-  if (rows <= 128) return run_stream<128>(a, p, s);
+  const int64_t rows = (a.R + a.E - 1) / a.E;
+  if (rows <= 16) return a.x != nullptr ? run_stream<16, true>(a, p, s) : run_stream<16, false>(a, p, s);
+  if (rows <= 32) return run_stream<32, false>(a, p, s);
+  if (rows <= 64) return run_stream<64, false>(a, p, s);
+  if (rows <= 128) return run_stream<128, false>(a, p, s);
   cudaError_t e = encode(&p.tm_x, a.qx, a.K, a.R, 0, TM);
   if (e != cudaSuccess) return e;
   e = encode(&p.tm_w, a.qweight, a.K, a.N, a.E, TN);

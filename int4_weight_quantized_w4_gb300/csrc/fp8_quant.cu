@@ -51,14 +51,6 @@ W4_DEV float silu_f32(float g) {
   return __fdividef(g >= 0.f ? g : g * t, 1.f + t);
 }
 
-W4_DEV float half_warp_max(float m) {
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  return m;
-}
-
-W4_DEV float block_scale(float amax) { return amax == 0.f ? 1.f : __fdiv_rn(amax, 448.f); }
-
 // x [*, K8 chunks], or with kSilu [*, 2 K8]; row r of the output comes from row
 // gather[r] (gather may be null: row r). An id outside [0, T) gives a zero row
 // with scales 1 and W4_ERR_SHAPE in the status word. KU = ceil(KB / kUnits).
@@ -106,9 +98,7 @@ __global__ void __launch_bounds__(kThreads) quant_block_kernel(const uint4* __re
       s = block_scale(half_warp_max(m));
       code = quant_e4m3_f32(a, quotient_bracket(s));
     } else {
-      const uint32_t m2 = absmax2<kF16>(absmax2<kF16>(v[i].x, v[i].y), absmax2<kF16>(v[i].z, v[i].w));
-      s = block_scale(half_warp_max(fmaxf(fabsf(act_lo<kF16>(m2)), fabsf(act_hi<kF16>(m2)))));
-      code = quant_e4m3_chunk<kF16>(v[i], quotient_bracket(s));
+      quant_block_half_warp<kF16>(v[i], code, s);
     }
     if (c < K8 && live) q[row * K8 + c] = code;
     if (l == 0 && live && b < KB) scale[row * KB + b] = s;

@@ -109,6 +109,7 @@ struct MoeRouteArgs {
   int32_t *offsets, *row_token, *row_of;
   void* workspace;
 };
+size_t moe_route_grouped_workspace_bytes(int64_t T, int32_t E);
 cudaError_t launch_moe_route_grouped(const MoeRouteArgs& a, cudaStream_t s);
 cudaError_t launch_silu_mul_quant(const void* h, int64_t R, int64_t I, void* q, float* scale, void* act,
                                   cudaStream_t s);
@@ -128,6 +129,8 @@ struct Fp8BlockArgs {
   const int32_t* expert_offsets;  // device [E + 1], or null: dense, E = 1
   int32_t E;
   int64_t R, N, K;
+  const void* x;                  // where fp8_block_fuses: 16-bit activations [R, K] in place of qx and x_scale
+  bool x_f16;
   bool pdl;                       // qx and x_scale come from the kernel launched just before, nothing else does
   unsigned int* status;
 };
@@ -135,6 +138,8 @@ struct Fp8BlockArgs {
 inline size_t fp8_block_workspace_bytes(int64_t R, int64_t K) {
   return static_cast<size_t>(R) * static_cast<size_t>(K) + static_cast<size_t>(R) * static_cast<size_t>((K + 127) / 128) * 4;
 }
+// Whether launch_fp8_block takes 16-bit activations.
+bool fp8_block_fuses(int64_t R, bool experts);
 cudaError_t launch_fp8_block(const Fp8BlockArgs& a, cudaStream_t s);
 cudaError_t launch_bounded_wait_selftest(long long limit, unsigned int* status, cudaStream_t s);
 

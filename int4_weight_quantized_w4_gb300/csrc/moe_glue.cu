@@ -364,199 +364,6 @@ __global__ void __launch_bounds__(256) combine_kernel(const uint4* __restrict__ 
                       pack_bf16x2(acc[6], acc[7]));
 }
 
-// Grouped routing, one warp per token. The choice goes by a key per expert:
-// the logit, or with a balance bias fl(score + bias), score = sigmoid or
-// softmax of the logit. Group values (the largest key, or with a bias the sum
-// of the two largest) pick the topk_group best of n_group groups of equal
-// size; the top_k largest keys of those are chosen, equal keys and groups in
-// ascending order. Weights are the scores, divided by their sum over the
-// chosen when renormalizing (0 where that sum is 0), times `factor`.
-//
-// Keys are compared as ordered integers (sign folded, -0 taken as +0), so a
-// warp maximum is one redux. The steps that decide a choice are fixed to the
-// bit: sigmoid = fl(1 / fl(1 + expf(-l))); softmax p = fl(expf(l - max) / S)
-// with S summed in fp64 and rounded once when keys depend on it, so that the
-// order of the sum cannot move a near-tie.
-struct RouteArgs {
-  const void* logits;
-  const float* bias;
-  int64_t T;
-  int E, k, n_group, topk_group;
-  bool bf16, softmax, renorm;
-  float factor;
-};
-
-W4_DEV uint32_t ordered_key(float f) {
-  const uint32_t u = __float_as_uint(f + 0.f);
-  return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
-}
-W4_DEV float key_value(uint32_t u) { return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xFFFFFFFFu)); }
-
-// A logit as the routing reads it: NaN counts as -inf, +inf as the largest finite number.
-W4_DEV float route_logit(const RouteArgs& a, int64_t i) {
-  const float v = a.bf16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(a.logits)[i]) << 16)
-                         : static_cast<const float*>(a.logits)[i];
-  return isnan(v) ? -INFINITY : fminf(v, 3.402823466e38f);
-}
-W4_DEV float sigmoid_f32(float v) { return __fdiv_rn(1.f, 1.f + expf(-v)); }
-
-constexpr uint32_t kNoKey = 0;   // below every key (the key of -inf is 0x007FFFFF)
-
-// kEPL experts per lane: lane l holds experts l, l + 32, ... keys: E + E / 32
-// words of shared memory per warp (padded: groups of 32 start in different banks).
-template <int kEPL>
-W4_DEV void route_token(const RouteArgs& a, int64_t t, uint32_t* keys, int32_t* __restrict__ ids,
-                        float* __restrict__ wts) {
-  const unsigned full = 0xFFFFFFFFu;
-  const int lane = threadIdx.x & 31;
-  const int E = a.E;
-  uint32_t key[kEPL];
-  float mx = -INFINITY, sum = 0.f;
-  {
-    float v[kEPL];
-#pragma unroll
-    for (int i = 0; i < kEPL; ++i) v[i] = lane + 32 * i < E ? route_logit(a, t * E + lane + 32 * i) : -INFINITY;
-    if (a.softmax) {
-#pragma unroll
-      for (int i = 0; i < kEPL; ++i) mx = fmaxf(mx, v[i]);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(full, mx, o));
-      if (a.bias != nullptr) {
-        double d = 0.0;
-#pragma unroll
-        for (int i = 0; i < kEPL; ++i)
-          if (v[i] != -INFINITY) d += static_cast<double>(expf(v[i] - mx));
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(full, d, o);
-        sum = static_cast<float>(d);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kEPL; ++i)
-          if (v[i] != -INFINITY) sum += expf(v[i] - mx);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(full, sum, o);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kEPL; ++i) {
-      const int e = lane + 32 * i;
-      float kv = v[i];
-      if (a.bias != nullptr && e < E) {
-        float s;
-        if (!a.softmax)
-          s = sigmoid_f32(v[i]);
-        else
-          s = v[i] != -INFINITY ? __fdiv_rn(expf(v[i] - mx), sum) : 0.f;
-        kv = s + a.bias[e];
-        if (isnan(kv)) kv = -INFINITY;
-      }
-      key[i] = e < E ? ordered_key(kv) : kNoKey;
-    }
-  }
-
-  if (a.topk_group < a.n_group) {
-    const int gs = E / a.n_group;
-#pragma unroll
-    for (int i = 0; i < kEPL; ++i) {
-      const int e = lane + 32 * i;
-      if (e < E) keys[e + (e >> 5)] = key[i];
-    }
-    __syncwarp();
-    // L lanes per group (a power of two): lane = group * L + part
-    int L = 1;
-    while (2 * L * a.n_group <= 32) L *= 2;
-    const int g = lane / L;
-    uint32_t m1 = kNoKey, m2 = kNoKey;       // the two largest keys of this lane's share
-    if (g < a.n_group)
-      for (int j = lane & (L - 1); j < gs; j += L) {
-        const int e = g * gs + j;
-        const uint32_t u = keys[e + (e >> 5)];
-        m2 = max(m2, min(m1, u));
-        m1 = max(m1, u);
-      }
-    for (int o = 1; o < L; o <<= 1) {
-      const uint32_t o1 = __shfl_xor_sync(full, m1, o), o2 = __shfl_xor_sync(full, m2, o);
-      m2 = max(max(m2, o2), min(m1, o1));
-      m1 = max(m1, o1);
-    }
-    float gv = key_value(m1);
-    if (a.bias != nullptr && gs > 1) gv += key_value(m2);
-    const uint32_t gk = ordered_key(isnan(gv) ? -INFINITY : gv);
-    int better = 0;
-    for (int o = 0; o < a.n_group; ++o) {
-      const uint32_t ok = __shfl_sync(full, gk, o * L);
-      better += ok > gk || (ok == gk && o < g);
-    }
-    const uint32_t kept = __ballot_sync(full, g < a.n_group && better < a.topk_group);   // bit g * L
-    const int magic = ((1 << 20) + gs - 1) / gs;   // e / gs = e * magic >> 20 for e < 1024
-#pragma unroll
-    for (int i = 0; i < kEPL; ++i) {
-      const int e = lane + 32 * i;
-      if (e < E && !((kept >> ((static_cast<uint32_t>(e) * magic >> 20) * L)) & 1u)) key[i] = kNoKey;
-    }
-    __syncwarp();
-  }
-
-  // k rounds of a warp maximum; the lane that holds the winner drops it
-  int mine[2] = {0, 0};              // choices lane and lane + 32
-  uint32_t best = kNoKey;
-  int at = 0;
-  auto rescan = [&]() {
-    best = kNoKey;
-    at = 0;
-#pragma unroll
-    for (int i = 0; i < kEPL; ++i)
-      if (key[i] > best) best = key[i], at = i;
-  };
-  rescan();
-  for (int j = 0; j < a.k; ++j) {
-    const uint32_t m = __reduce_max_sync(full, best);
-    const unsigned e = __reduce_min_sync(full, best == m ? static_cast<unsigned>(lane + 32 * at) : 0xFFFFu);
-    if (lane == static_cast<int>(e & 31)) {
-#pragma unroll
-      for (int i = 0; i < kEPL; ++i)
-        if (i == at) key[i] = kNoKey;
-      rescan();
-    }
-    if (lane == (j & 31)) mine[j >> 5] = static_cast<int>(e);
-  }
-  float w[2], total = 0.f;
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    w[s] = 0.f;
-    if (lane + 32 * s < a.k) {
-      const float v = route_logit(a, t * E + mine[s]);
-      if (!a.softmax)
-        w[s] = sigmoid_f32(v);
-      else
-        w[s] = v != -INFINITY ? __fdiv_rn(expf(v - mx), sum) : 0.f;
-    }
-    total += w[s];
-  }
-  if (a.renorm) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(full, total, o);
-#pragma unroll
-    for (int s = 0; s < 2; ++s) w[s] = total > 0.f ? __fdiv_rn(w[s], total) : 0.f;
-  }
-#pragma unroll
-  for (int s = 0; s < 2; ++s)
-    if (lane + 32 * s < a.k) {
-      ids[t * a.k + lane + 32 * s] = mine[s];
-      wts[t * a.k + lane + 32 * s] = w[s] * a.factor;
-    }
-}
-
-template <int kEPL>
-__global__ void __launch_bounds__(256) route_grouped_kernel(const RouteArgs a, int32_t* __restrict__ ids,
-                                                            float* __restrict__ wts) {
-  __shared__ uint32_t keys[8][kEPL * 33];
-  const int64_t nw = static_cast<int64_t>(gridDim.x) * 8;
-  const int warp = threadIdx.x >> 5;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + warp; t < a.T; t += nw)
-    route_token<kEPL>(a, t, keys[warp], ids, wts);
-}
-
 int sm_count_glue() { return current_sm_count(); }
 
 template <int kEPL>
@@ -570,10 +377,6 @@ cudaError_t launch_route_k(const void* logits, bool bf16, int64_t T, int E, int 
 }
 
 }  // namespace
-
-// The row order of chosen experts `ids` [T, k]: offsets, row_token, row_of.
-static cudaError_t launch_row_order(const int32_t* ids, int64_t T, int32_t E, int32_t k, int32_t* offsets,
-                                    int32_t* row_token, int32_t* row_of, void* workspace, cudaStream_t s);
 
 size_t moe_route_workspace_bytes(int64_t T, int32_t E) {
   const int64_t ntiles = (T + kTile - 1) / kTile;
@@ -597,16 +400,11 @@ cudaError_t launch_moe_route(const void* logits, bool bf16, int64_t T, int32_t E
   else
     e = launch_route_k<32>(logits, bf16, T, E, k, renorm, ids, wts, s);
   if (e != cudaSuccess) return e;
-  return launch_row_order(ids, T, E, k, offsets, row_token, row_of, workspace, s);
-}
-
-static cudaError_t launch_row_order(const int32_t* ids, int64_t T, int32_t E, int32_t k, int32_t* offsets,
-                                    int32_t* row_token, int32_t* row_of, void* workspace, cudaStream_t s) {
   const int ntiles = static_cast<int>((T + kTile - 1) / kTile);
   int32_t* tile_rows = static_cast<int32_t*>(workspace);
   const size_t smem_count = static_cast<size_t>(kTileWarps) * E * sizeof(uint32_t);
   const size_t smem_place = 2 * smem_count;
-  cudaError_t e = cudaFuncSetAttribute(tile_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  e = cudaFuncSetAttribute(tile_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(smem_count));
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(tile_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -620,27 +418,6 @@ static cudaError_t launch_row_order(const int32_t* ids, int64_t T, int32_t E, in
   if (e != cudaSuccess) return e;
   tile_kernel<true><<<ntiles, kTile, smem_place, s>>>(ids, T, k, E, tile_rows, row_token, row_of);
   return cudaGetLastError();
-}
-
-cudaError_t launch_moe_route_grouped(const MoeRouteArgs& r, cudaStream_t s) {
-  const RouteArgs a{r.logits, r.bias, r.T, r.E, r.k, r.n_group, r.topk_group, r.bf16, r.softmax, r.renorm, r.factor};
-  const int64_t want = (r.T + 7) / 8, cap = static_cast<int64_t>(sm_count_glue()) * 8;
-  const unsigned grid = static_cast<unsigned>(want < cap ? want : cap);
-  if (r.E <= 32)
-    route_grouped_kernel<1><<<grid, 256, 0, s>>>(a, r.ids, r.wts);
-  else if (r.E <= 64)
-    route_grouped_kernel<2><<<grid, 256, 0, s>>>(a, r.ids, r.wts);
-  else if (r.E <= 128)
-    route_grouped_kernel<4><<<grid, 256, 0, s>>>(a, r.ids, r.wts);
-  else if (r.E <= 256)
-    route_grouped_kernel<8><<<grid, 256, 0, s>>>(a, r.ids, r.wts);
-  else if (r.E <= 512)
-    route_grouped_kernel<16><<<grid, 256, 0, s>>>(a, r.ids, r.wts);
-  else
-    route_grouped_kernel<32><<<grid, 256, 0, s>>>(a, r.ids, r.wts);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  return launch_row_order(r.ids, r.T, r.E, r.k, r.offsets, r.row_token, r.row_of, r.workspace, s);
 }
 
 cudaError_t launch_silu_mul_quant(const void* h, int64_t R, int64_t I, void* q, float* scale, void* act,

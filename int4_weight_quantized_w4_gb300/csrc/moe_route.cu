@@ -1,0 +1,373 @@
+// Grouped routing: sigmoid or softmax scores, a balance bias, expert groups,
+// and the expert-sorted row order of the chosen (token, expert) pairs.
+//
+// The choice goes by a key per expert: the logit, or with a bias fl(score +
+// bias). Group values (the largest key, or with a bias the sum of the two
+// largest) pick the topk_group best of n_group groups of equal size; the top_k
+// largest keys of those are chosen, equal keys and groups in ascending order.
+// Weights are the scores, divided by their sum over the chosen when
+// renormalizing (0 where that sum is 0), times `factor`.
+//
+// The steps that decide a choice are fixed to the bit: sigmoid = fl(1 / fl(1 +
+// expf(-l))); softmax p = fl(expf(l - max) / S), with S summed in fp64 and
+// rounded once when keys depend on it, so that the order of the sum cannot move
+// a near-tie.
+//
+// A warp takes a token: lane l holds experts l, l + 32, ... as integer keys in
+// the order of their values (sign folded, -0 taken as +0), so that a warp
+// maximum is one redux. A CTA takes a tile of tokens and counts its rows per
+// expert; the place kernel, a CTA per tile, turns the counts of all tiles into
+// the tile's first row in every expert (each thread sums an expert's column, a
+// block scan adds the experts before) and ranks the tile's rows by token with
+// bit masks. At most kMaxTiles tiles: the count table that every place CTA
+// reads stays small. A call whose tokens fit one tile is one CTA and one
+// launch. Bound by instruction issue for many tokens, by latency for few.
+#include "common.cuh"
+#include "launch.h"
+
+namespace w4 {
+namespace {
+
+constexpr int kMaxTiles = 256;
+constexpr int kChunk = 128;             // tokens ranked at a time
+constexpr int kChunkWarps = kChunk / 32;
+constexpr uint32_t kNoKey = 0;          // below every key (the key of -inf is 0x007FFFFF)
+constexpr unsigned kFull = 0xFFFFFFFFu;
+
+W4_DEV uint32_t ordered_key(float f) {
+  const uint32_t u = __float_as_uint(f + 0.f);
+  return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+}
+W4_DEV float key_value(uint32_t u) { return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xFFFFFFFFu)); }
+
+// A logit as the routing reads it: NaN counts as -inf, +inf as the largest finite number.
+W4_DEV float route_logit(const MoeRouteArgs& a, int64_t i) {
+  const float v = a.bf16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(a.logits)[i]) << 16)
+                         : static_cast<const float*>(a.logits)[i];
+  return isnan(v) ? -INFINITY : fminf(v, 3.402823466e38f);
+}
+W4_DEV float sigmoid_f32(float v) { return __frcp_rn(1.f + expf(-v)); }   // 1 / x, correctly rounded
+
+// keys: kEPL * 33 words of shared memory of this warp (padded, so that groups
+// of 32 start in different banks). Chosen experts go to ids[0 .. k) and wts.
+template <int kEPL>
+W4_DEV void route_token(const MoeRouteArgs& a, int64_t t, uint32_t* keys, int (&mine)[2]) {
+  const int lane = threadIdx.x & 31;
+  const int E = a.E;
+  uint32_t key[kEPL];
+  float mx = -INFINITY, sum = 0.f;
+  {
+    float v[kEPL];
+#pragma unroll
+    for (int i = 0; i < kEPL; ++i) v[i] = lane + 32 * i < E ? route_logit(a, t * E + lane + 32 * i) : -INFINITY;
+    if (a.softmax) {
+#pragma unroll
+      for (int i = 0; i < kEPL; ++i) mx = fmaxf(mx, v[i]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+      float ex[kEPL];
+#pragma unroll
+      for (int i = 0; i < kEPL; ++i) ex[i] = v[i] != -INFINITY ? expf(v[i] - mx) : 0.f;
+      if (a.bias != nullptr) {
+        double d = 0.0;
+#pragma unroll
+        for (int i = 0; i < kEPL; ++i) d += static_cast<double>(ex[i]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(kFull, d, o);
+        sum = static_cast<float>(d);
+#pragma unroll
+        for (int i = 0; i < kEPL; ++i) v[i] = sum > 0.f ? __fdiv_rn(ex[i], sum) : 0.f;
+      } else {
+#pragma unroll
+        for (int i = 0; i < kEPL; ++i) sum += ex[i];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+      }
+    } else if (a.bias != nullptr) {
+#pragma unroll
+      for (int i = 0; i < kEPL; ++i) v[i] = sigmoid_f32(v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kEPL; ++i) {
+      const int e = lane + 32 * i;
+      float kv = v[i];
+      if (a.bias != nullptr && e < E) {
+        kv += __ldg(a.bias + e);
+        if (isnan(kv)) kv = -INFINITY;
+      }
+      key[i] = e < E ? ordered_key(kv) : kNoKey;
+    }
+  }
+
+  if (a.topk_group < a.n_group) {
+    const int gs = E / a.n_group;
+#pragma unroll
+    for (int i = 0; i < kEPL; ++i) keys[lane + 33 * i] = key[i];   // expert e at e + e / 32
+    __syncwarp();
+    // L lanes per group (a power of two): lane = group * L + part
+    int L = 1;
+    while (2 * L * a.n_group <= 32) L *= 2;
+    const int g = lane / L;
+    uint32_t m1 = kNoKey, m2 = kNoKey;       // the two largest keys of this lane's share
+    if (g < a.n_group)
+      for (int j = lane & (L - 1); j < gs; j += L) {
+        const int e = g * gs + j;
+        const uint32_t u = keys[e + (e >> 5)];
+        m2 = max(m2, min(m1, u));
+        m1 = max(m1, u);
+      }
+    for (int o = 1; o < L; o <<= 1) {
+      const uint32_t o1 = __shfl_xor_sync(kFull, m1, o), o2 = __shfl_xor_sync(kFull, m2, o);
+      m2 = max(max(m2, o2), min(m1, o1));
+      m1 = max(m1, o1);
+    }
+    float gv = key_value(m1);
+    if (a.bias != nullptr && gs > 1) gv += key_value(m2);
+    const uint32_t gk = ordered_key(isnan(gv) ? -INFINITY : gv);
+    int better = 0;
+    for (int o = 0; o < a.n_group; ++o) {
+      const uint32_t ok = __shfl_sync(kFull, gk, o * L);
+      better += ok > gk || (ok == gk && o < g);
+    }
+    const uint32_t kept = __ballot_sync(kFull, g < a.n_group && better < a.topk_group);   // bit g * L
+    const uint32_t magic = ((1u << 20) + gs - 1) / gs;   // e / gs = e * magic >> 20 for e < 1024
+#pragma unroll
+    for (int i = 0; i < kEPL; ++i) {
+      const uint32_t e = lane + 32 * i;
+      if (!((kept >> ((e * magic >> 20) * L & 31)) & 1u)) key[i] = kNoKey;
+    }
+    __syncwarp();
+  }
+
+  // k rounds of a warp maximum; the lane that holds the winner drops it
+  mine[0] = mine[1] = 0;             // choices lane and lane + 32
+  uint32_t best;
+  int at;
+  auto rescan = [&]() {
+    best = key[0];
+    at = 0;
+#pragma unroll
+    for (int i = 1; i < kEPL; ++i)
+      if (key[i] > best) best = key[i], at = i;
+  };
+  rescan();
+  for (int j = 0; j < a.k; ++j) {
+    const uint32_t m = __reduce_max_sync(kFull, best);
+    const unsigned e = __reduce_min_sync(kFull, best == m ? static_cast<unsigned>(lane + 32 * at) : 0xFFFFu);
+    if (lane == static_cast<int>(e & 31)) {
+#pragma unroll
+      for (int i = 0; i < kEPL; ++i)
+        if (i == at) key[i] = kNoKey;
+      rescan();
+    }
+    if (lane == (j & 31)) mine[j >> 5] = static_cast<int>(e);
+  }
+  float w[2], total = 0.f;
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    w[s] = 0.f;
+    if (lane + 32 * s < a.k) {
+      const float v = route_logit(a, t * E + mine[s]);
+      if (!a.softmax)
+        w[s] = sigmoid_f32(v);
+      else
+        w[s] = v != -INFINITY ? __fdiv_rn(expf(v - mx), sum) : 0.f;
+    }
+    total += w[s];
+  }
+  if (a.renorm) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kFull, total, o);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) w[s] = total > 0.f ? __fdiv_rn(w[s], total) : 0.f;
+  }
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+    if (lane + 32 * s < a.k) {
+      a.ids[t * a.k + lane + 32 * s] = mine[s];
+      a.wts[t * a.k + lane + 32 * s] = w[s] * a.factor;
+    }
+}
+
+// Rows of tokens [t0, t1) in order: base[e] is expert e's next row, moved on
+// past them. bits, first: [kChunkWarps][E]. All threads of the block take part.
+W4_DEV void place_tokens(const MoeRouteArgs& a, int64_t t0, int64_t t1, uint32_t* bits, int32_t* first, int32_t* base) {
+  const int E = a.E, k = a.k;
+  for (int64_t c0 = t0; c0 < t1; c0 += kChunk) {
+    const int n = static_cast<int>(t1 - c0 < kChunk ? t1 - c0 : kChunk) * k;   // pairs of the chunk
+    for (int i = threadIdx.x; i < kChunkWarps * E; i += blockDim.x) bits[i] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+      const int t = i / k;
+      atomicOr(&bits[(t >> 5) * E + a.ids[c0 * k + i]], 1u << (t & 31));
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+      int run = base[e];
+      for (int w = 0; w < kChunkWarps; ++w) {
+        first[w * E + e] = run;
+        run += __popc(bits[w * E + e]);
+      }
+      base[e] = run;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+      const int t = i / k, at = (t >> 5) * E + a.ids[c0 * k + i];
+      const int r = first[at] + __popc(bits[at] & ((1u << (t & 31)) - 1u));
+      a.row_token[r] = static_cast<int32_t>(c0 + t);
+      a.row_of[c0 * k + i] = r;
+    }
+    __syncthreads();
+  }
+}
+
+// base[e] (a count per expert) becomes base[e] + the totals of the experts
+// before e; total[e] the expert's rows. Writes offsets when `write`.
+W4_DEV void add_expert_starts(const MoeRouteArgs& a, const int32_t* total, int32_t* base, int32_t* part, bool write) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  int carry = 0;
+  for (int e0 = 0; e0 < a.E; e0 += blockDim.x) {
+    const int e = e0 + threadIdx.x;
+    const int n = e < a.E ? total[e] : 0;
+    int inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(kFull, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) part[warp] = inc;
+    __syncthreads();
+    int before = carry;
+    for (int w = 0; w < nw; ++w) {
+      const int v = part[w];
+      if (w < warp) before += v;
+      carry += v;
+    }
+    if (e < a.E) {
+      base[e] += before + inc - n;
+      if (write) a.offsets[e] = before + inc - n;
+    }
+    __syncthreads();
+  }
+  if (write && threadIdx.x == 0) a.offsets[a.E] = carry;
+}
+
+// Warps per CTA: the keys of all warps take 34 KB at most.
+template <int kEPL>
+constexpr int kRouteWarps = kEPL <= 8 ? 32 : 256 / kEPL;
+constexpr int kPlaceWords = (2 * kChunkWarps + 2) * 1024;   // bits, first, base, total for 1024 experts
+
+// Tokens [tile * per, ...) of this CTA: choices and weights, then the tile's
+// rows per expert into counts[tile][E], or (kWhole: the call is one tile) the
+// whole row order.
+template <int kEPL, bool kWhole>
+__global__ void __launch_bounds__(32 * kRouteWarps<kEPL>) route_tile_kernel(const MoeRouteArgs a, int per,
+                                                                           int32_t* __restrict__ counts) {
+  constexpr int kKeyWords = kRouteWarps<kEPL> * kEPL * 33;
+  __shared__ uint32_t buf[kWhole && kPlaceWords > kKeyWords ? kPlaceWords : kKeyWords];
+  __shared__ int32_t cnt[32 * kEPL];
+  __shared__ int32_t part[32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int e = threadIdx.x; e < 32 * kEPL; e += blockDim.x) cnt[e] = 0;
+  __syncthreads();
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * per, t1 = t0 + per < a.T ? t0 + per : a.T;
+  for (int64_t t = t0 + warp; t < t1; t += kRouteWarps<kEPL>) {
+    int mine[2];
+    route_token<kEPL>(a, t, buf + warp * kEPL * 33, mine);
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+      if (lane + 32 * s < a.k) atomicAdd(&cnt[mine[s]], 1);
+  }
+  __syncthreads();
+  if (!kWhole) {
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) counts[static_cast<int64_t>(blockIdx.x) * a.E + e] = cnt[e];
+    return;
+  }
+  int32_t* base = reinterpret_cast<int32_t*>(buf) + 2 * kChunkWarps * a.E;
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) base[e] = 0;
+  __syncthreads();
+  add_expert_starts(a, cnt, base, part, true);
+  place_tokens(a, t0, t1, buf, reinterpret_cast<int32_t*>(buf) + kChunkWarps * a.E, base);
+}
+
+constexpr int kPlaceThreads = 256;
+__global__ void __launch_bounds__(kPlaceThreads) place_kernel(const MoeRouteArgs a, int per,
+                                                              const int32_t* __restrict__ counts, int ntiles) {
+  extern __shared__ uint32_t sm[];
+  __shared__ int32_t part[kPlaceThreads / 32];
+  uint32_t* bits = sm;
+  int32_t* first = reinterpret_cast<int32_t*>(sm) + kChunkWarps * a.E;
+  int32_t* base = first + kChunkWarps * a.E;
+  int32_t* total = base + a.E;
+  const int tile = blockIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (int e = threadIdx.x; e < a.E; e += kPlaceThreads) {
+    int before = 0, after = 0;
+#pragma unroll 8
+    for (int i = 0; i < tile; ++i) before += counts[static_cast<int64_t>(i) * a.E + e];
+#pragma unroll 8
+    for (int i = tile; i < ntiles; ++i) after += counts[static_cast<int64_t>(i) * a.E + e];
+    base[e] = before;
+    total[e] = before + after;
+  }
+  __syncthreads();
+  add_expert_starts(a, total, base, part, tile == 0);
+  const int64_t t0 = static_cast<int64_t>(tile) * per, t1 = t0 + per < a.T ? t0 + per : a.T;
+  place_tokens(a, t0, t1, bits, first, base);
+}
+
+// Tokens per tile: one or two a warp while that makes at most kMaxTiles tiles.
+int64_t tile_tokens(int64_t T, int warps) {
+  int64_t per = warps;
+  while ((T + per - 1) / per > kMaxTiles) per *= 2;
+  return per;
+}
+int route_warps(int E) { return E <= 256 ? 32 : E <= 512 ? 16 : 8; }
+// One CTA does the whole call up to this many tokens: two per warp.
+bool one_tile(int64_t T, int E) { return T <= 2 * route_warps(E); }
+
+template <int kEPL>
+cudaError_t launch_k(const MoeRouteArgs& a, cudaStream_t s) {
+  constexpr int kThreads = 32 * kRouteWarps<kEPL>;
+  if (one_tile(a.T, a.E)) {
+    route_tile_kernel<kEPL, true><<<1, kThreads, 0, s>>>(a, static_cast<int>(a.T), nullptr);
+    return cudaGetLastError();
+  }
+  const int per = static_cast<int>(tile_tokens(a.T, kRouteWarps<kEPL>));
+  const int ntiles = static_cast<int>((a.T + per - 1) / per);
+  int32_t* counts = static_cast<int32_t*>(a.workspace);
+  route_tile_kernel<kEPL, false><<<ntiles, kThreads, 0, s>>>(a, per, counts);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ntiles);
+  cfg.blockDim = dim3(kPlaceThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(2 * kChunkWarps + 2) * a.E * 4;   // at most 40 KB
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, place_kernel, a, per, static_cast<const int32_t*>(counts), ntiles);
+}
+
+}  // namespace
+
+size_t moe_route_grouped_workspace_bytes(int64_t T, int32_t E) {
+  if (one_tile(T, E)) return 0;
+  const int64_t per = tile_tokens(T, route_warps(E));
+  return static_cast<size_t>((T + per - 1) / per) * static_cast<size_t>(E) * sizeof(int32_t);
+}
+
+cudaError_t launch_moe_route_grouped(const MoeRouteArgs& a, cudaStream_t s) {
+  if (a.E <= 32) return launch_k<1>(a, s);
+  if (a.E <= 64) return launch_k<2>(a, s);
+  if (a.E <= 128) return launch_k<4>(a, s);
+  if (a.E <= 256) return launch_k<8>(a, s);
+  if (a.E <= 512) return launch_k<16>(a, s);
+  return launch_k<32>(a, s);
+}
+
+}  // namespace w4
