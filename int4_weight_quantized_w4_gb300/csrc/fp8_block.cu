@@ -12,9 +12,9 @@
 //  * stream (few rows an expert or call): weights on the MMA's 128 rows (TMEM
 //    lane = output), NT tokens on its columns. Bound by the weight bytes. For up
 //    to kFuseRows dense rows the kernel quantizes 16-bit activations itself.
-//  * tile (many rows): 128 tokens on the MMA's rows, 256 outputs on its
-//    columns, so that one scale sx * sw serves a thread's whole column strip.
-//    Bound by the tensor core and by the drain of one accumulator per block.
+//  * tile (many rows): 128 tokens on the MMA's rows, 256 outputs on its columns,
+//    so that one scale sx * sw serves a thread's whole column strip. Bound by the
+//    hand-over and drain of one accumulator per block.
 #include <cuda.h>
 
 #include <cstring>
@@ -65,6 +65,13 @@ W4_DEV float ld_cluster_f32(uint32_t a, uint32_t rank) {
 // time-out would not meet at its next warp-wide instruction.
 W4_DEV bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned int* status) {
   return __all_sync(0xFFFFFFFFu, tc::wait(bar, parity, abort, status, kWaitNs));
+}
+// One lane of a converged warp. Loops that issue copies or MMAs run in the whole
+// warp with one lane issuing: descriptors and addresses stay in uniform registers.
+W4_DEV bool elect_one() {
+  uint32_t p;
+  asm volatile("{.reg .pred P; elect.sync _|P, 0xFFFFFFFF; selp.u32 %0, 1, 0, P;}" : "=r"(p));
+  return p != 0;
 }
 W4_DEV void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
@@ -447,16 +454,22 @@ __global__ void __launch_bounds__(Stream<NT, kQuant>::THREADS, Stream<NT, kQuant
 // tile form
 // ---------------------------------------------------------------------------
 
-constexpr int TM = 128, TN = 256;
+constexpr int TM = 128, TN = 256;             // rows and outputs of a tile
 constexpr int T_A = TM * 128, T_B = TN * 128;
 constexpr int T_STAGES = 4;
-constexpr int T_SMEM = T_STAGES * (T_A + T_B) + 512 + (kMaxExperts + 1 + 12 + 3) / 4 * 16 + 1024;
+constexpr int T_ACCS = 2;                      // accumulators of 256 columns: all 512 of tensor memory
+constexpr int T_SC_SLOTS = 3;                  // scale slots of 4 blocks x 2 output halves x 128 rows
+constexpr int T_SC_FLOATS = 4 * 2 * TM;
+constexpr int T_SC = T_SC_SLOTS * T_SC_FLOATS * 4;
+constexpr int T_SMEM = T_STAGES * (T_A + T_B) + T_SC + 512 + (kMaxExperts + 1 + 12 + 3) / 4 * 16 + 1024;
 static_assert(T_SMEM <= 232448, "shared memory per CTA");
+// Each issuer meets every phase of the stages and the accumulator that it waits on.
+static_assert(T_STAGES % 2 == 0 && T_ACCS == 2, "blocks of one parity keep their stages and accumulator");
 // Warps 0-7 epilogue (warp w: TMEM lanes 32 (w % 4), outputs 128 (w / 4) ..),
-// 8 activation copies, 9 weight copies, 10 and 11 MMA issuers of the even and
-// odd blocks: a thread's MMAs queue behind its own commits, so with two
-// issuers one accumulates while the other's block completes.
-constexpr int kTEpi = 8, kTWarpA = 8, kTWarpB = 9, kTWarpMma = 10;
+// 8 copies, 9 scales, 10 and 11 MMA issuers of the even and odd blocks: a
+// thread's MMAs queue behind its own commits, so with two issuers one
+// accumulates while the other's block completes.
+constexpr int kTEpi = 8, kTWarpLoad = 8, kTWarpScale = 9, kTWarpMma = 10;
 constexpr int kTThreads = 384;
 
 __global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const __grid_constant__ Params p) {
@@ -464,10 +477,13 @@ __global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const __grid_constan
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
   uint8_t* a_base = smem;
   uint8_t* b_base = a_base + T_STAGES * T_A;
-  uint64_t* full = reinterpret_cast<uint64_t*>(b_base + T_STAGES * T_B);
+  float* sc_base = reinterpret_cast<float*>(b_base + T_STAGES * T_B);
+  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(sc_base) + T_SC);
   uint64_t* done = full + T_STAGES;        // a block's MMAs: its stage is free and its accumulator complete
   uint64_t* acc_empty = done + T_STAGES;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  uint64_t* sc_full = acc_empty + T_ACCS;
+  uint64_t* sc_empty = sc_full + T_SC_SLOTS;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sc_empty + T_SC_SLOTS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int32_t* starts = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(full) + 512);
   int32_t* warp_sum = starts + kMaxExperts + 1;
@@ -475,16 +491,22 @@ __global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const __grid_constan
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < T_STAGES; ++i) {
-      mbar_init(&full[i], 2);
+      mbar_init(&full[i], 1);
       mbar_init(&done[i], 1);
     }
-    for (int i = 0; i < 2; ++i) mbar_init(&acc_empty[i], kTEpi);
+    for (int i = 0; i < T_ACCS; ++i) mbar_init(&acc_empty[i], kTEpi);
+    for (int i = 0; i < T_SC_SLOTS; ++i) {
+      mbar_init(&sc_full[i], 1);
+      mbar_init(&sc_empty[i], kTEpi);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kTWarpMma) tc::tmem_alloc(tmem_holder, 2 * TN);
-  if (warp == kTWarpA && lane == 0) tc::prefetch_tmap(&p.tm_x);
-  if (warp == kTWarpB && lane == 0) tc::prefetch_tmap(&p.tm_w);
+  if (warp == kTWarpMma) tc::tmem_alloc(tmem_holder, T_ACCS * TN);
+  if (warp == kTWarpLoad && lane == 0) {
+    tc::prefetch_tmap(&p.tm_x);
+    tc::prefetch_tmap(&p.tm_w);
+  }
   if (p.offsets != nullptr) tile_starts<kTThreads>(p, TM, starts, warp_sum);
   tc::fence_before_sync();
   __syncthreads();
@@ -494,89 +516,135 @@ __global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const __grid_constan
 
   if (warp >= kTEpi) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (lane == 0) {
-      if (warp == kTWarpA || warp == kTWarpB) {
-        if (warp == kTWarpA) grid_dependency_wait();
-        int st = 0, ph = 1, e = 0;
-        bool ok = true;
-        Tile t;
-        for (long long it = blockIdx.x; ok && it < p.items && decode(p, it, TM, TN, starts, t, e); it += gridDim.x)
-          for (int kb = 0; kb < KB; ++kb) {
-            if (!(ok = tc::wait(&done[st], ph, abort_flag, p.status, kWaitNs))) break;
-            if (warp == kTWarpA) {
-              mbar_arrive_expect_tx(&full[st], T_A);
-              tc::tma_load_2d(a_base + st * T_A, &p.tm_x, &full[st], kb * kBlk, t.row0);
-            } else {
-              mbar_arrive_expect_tx(&full[st], T_B);
-              tc::tma_load_3d(b_base + st * T_B, &p.tm_w, &full[st], kb * kBlk, t.n0, t.expert);
-            }
-            if (++st == T_STAGES) st = 0, ph ^= 1;
+    if (warp == kTWarpLoad) {
+      int st = 0, ph = 1, e = 0;
+      bool ok = true, waited = false;
+      Tile t;
+      for (long long it = blockIdx.x; ok && it < p.items && decode(p, it, TM, TN, starts, t, e); it += gridDim.x)
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!(ok = wait_warp(&done[st], ph, abort_flag, p.status))) break;
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&full[st], T_A + T_B);
+            tc::tma_load_3d(b_base + st * T_B, &p.tm_w, &full[st], kb * kBlk, t.n0, t.expert);
           }
-      } else {
-        const int mine = warp - kTWarpMma;   // blocks and accumulators of this parity
-        constexpr uint32_t idesc = tc::idesc_f16_f32(TM, TN);
-        const uint64_t ad0 = tc::sdesc_sw128(smem_addr(a_base)), bd0 = tc::sdesc_sw128(smem_addr(b_base));
-        int st = 0, ph = 0, g = 0, aph = 1, e = 0;
-        bool ok = true;
-        Tile t;
-        for (long long it = blockIdx.x; ok && it < p.items && decode(p, it, TM, TN, starts, t, e); it += gridDim.x)
-          for (int kb = 0; kb < KB; ++kb, ++g) {
-            if ((g & 1) == mine) {
-              if (!(ok = tc::wait(&acc_empty[mine], aph, abort_flag, p.status, kWaitNs, 200))) break;
-              if (!(ok = tc::wait(&full[st], ph, abort_flag, p.status, kWaitNs, 200))) break;
-              tc::fence_after_sync();
+          if (!waited) grid_dependency_wait();   // the codes come from the kernel before
+          waited = true;
+          if (elect_one()) tc::tma_load_2d(a_base + st * T_A, &p.tm_x, &full[st], kb * kBlk, t.row0);
+          if (++st == T_STAGES) st = 0, ph ^= 1;
+        }
+    } else if (warp == kTWarpScale) {
+      // sx * sw of four blocks, both output halves and the tile's 128 rows per slot
+      grid_dependency_wait();
+      int sl = 0, ph = 1, e = 0;
+      bool ok = true;
+      Tile t;
+      for (long long it = blockIdx.x; ok && it < p.items && decode(p, it, TM, TN, starts, t, e); it += gridDim.x) {
+        const int nb = t.n0 / kBlk;
+        const float* sw0 = p.w_scale + (static_cast<size_t>(t.expert) * p.NB + nb) * KB;
+        const float* sw1 = nb + 1 < p.NB ? sw0 + KB : sw0;
+        for (int kb = 0; kb < KB; kb += 4) {
+          float w0[4], w1[4], x[4][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            w0[i] = kb + i < KB ? __ldg(sw0 + kb + i) : 0.f;
+            w1[i] = kb + i < KB ? __ldg(sw1 + kb + i) : 0.f;
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int row = t.row0 + 32 * j + lane;
+            const float* sx = p.x_scale + static_cast<size_t>(row) * KB + kb;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[j][i] = (row < t.row_end && kb + i < KB) ? sx[i] : 0.f;
+          }
+          if (!(ok = wait_warp(&sc_empty[sl], ph, abort_flag, p.status))) break;
+          float* sc = sc_base + sl * T_SC_FLOATS + lane;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              sc[i * 2 * TM + 32 * j] = x[j][i] * w0[i];
+              sc[i * 2 * TM + TM + 32 * j] = x[j][i] * w1[i];
+            }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sc_full[sl]);
+          if (++sl == T_SC_SLOTS) sl = 0, ph ^= 1;
+        }
+      }
+    } else {
+      const int mine = warp - kTWarpMma;   // blocks and accumulator of this parity
+      constexpr uint32_t idesc = tc::idesc_f16_f32(TM, TN);
+      const uint64_t ad0 = tc::sdesc_sw128(smem_addr(a_base)), bd0 = tc::sdesc_sw128(smem_addr(b_base));
+      int st = 0, ph = 0, aph = 1, e = 0;
+      uint32_t g = 0;
+      bool ok = true;
+      Tile t;
+      for (long long it = blockIdx.x; ok && it < p.items && decode(p, it, TM, TN, starts, t, e); it += gridDim.x)
+        for (int kb = 0; kb < KB; ++kb, ++g) {
+          if (static_cast<int>(g & 1) == mine) {
+            if (!(ok = wait_warp(&acc_empty[mine], aph, abort_flag, p.status))) break;
+            if (!(ok = wait_warp(&full[st], ph, abort_flag, p.status))) break;
+            tc::fence_after_sync();
+            if (elect_one()) {
               mma_block(tmem + mine * TN, ad0 + static_cast<uint64_t>((st * T_A) >> 4),
                         bd0 + static_cast<uint64_t>((st * T_B) >> 4), idesc);
               tc::commit(&done[st]);
-              aph ^= 1;
             }
-            if (++st == T_STAGES) st = 0, ph ^= 1;
+            __syncwarp();
+            aph ^= 1;
           }
-      }
+          if (++st == T_STAGES) st = 0, ph ^= 1;
+        }
     }
     __syncwarp();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    grid_dependency_wait();
     const int q = warp & 3, half = warp >> 2;
-    int st = 0, ph = 0, buf = 0, e = 0;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * q) << 16) + 128 * half;
+    const float* sc_mine = sc_base + half * TM + 32 * q + lane;
+    int st = 0, ph = 0, buf = 0, sl = 0, sph = 0, e = 0;
     bool ok = true;
     Tile t;
     for (long long it = blockIdx.x; ok && it < p.items && decode(p, it, TM, TN, starts, t, e); it += gridDim.x) {
-      const int row = t.row0 + 32 * q + lane;
-      const bool r_ok = row < t.row_end;
-      const int n0 = t.n0 + 128 * half;
-      const bool n_any = n0 < p.N;
-      const float* sx = p.x_scale + static_cast<size_t>(r_ok ? row : t.row0) * KB;
-      const float* sw = p.w_scale + (static_cast<size_t>(t.expert) * p.NB + (n_any ? n0 / kBlk : 0)) * KB;
       float T[128];
 #pragma unroll
       for (int j = 0; j < 128; ++j) T[j] = 0.f;
-      // the scales of this block and the next three, loaded ahead
-      auto ld = [&](int kb) { return kb < KB ? sx[kb] * __ldg(sw + kb) : 0.f; };
-      float f0 = ld(0), f1 = ld(1), f2 = ld(2), f3 = ld(3);
       for (int kb = 0; kb < KB; ++kb) {
-        const float f = f0;
-        f0 = f1, f1 = f2, f2 = f3, f3 = ld(kb + 4);
+        const int i = kb & 3;
+        if (i == 0 && !(ok = wait_warp(&sc_full[sl], sph, abort_flag, p.status))) break;
+        const float f = sc_mine[sl * T_SC_FLOATS + i * 2 * TM];
         if (!(ok = wait_warp(&done[st], ph, abort_flag, p.status))) break;
         tc::fence_after_sync();
-        const uint32_t ta = tmem + (static_cast<uint32_t>(32 * q) << 16) + buf * TN + 128 * half;
+        const uint32_t ta = t_lane + buf * TN;
+        // 16 columns are multiplied while the next 16 load
+        uint32_t v[2][16];
+        tc::tmem_ld16_async(ta, v[0]);
 #pragma unroll
-        for (int c = 0; c < 128; c += 32) {
-          uint32_t v[32];
-          tc::tmem_ld32(ta + c, v);
+        for (int c = 0; c < 8; ++c) {
+          tc::tmem_wait_ld(v[c & 1]);
+          if (c < 7) {
+            tc::tmem_ld16_async(ta + 16 * (c + 1), v[(c + 1) & 1]);
+          } else {
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {   // the accumulator is in registers
+              mbar_arrive(&acc_empty[buf]);
+              if (i == 3 || kb == KB - 1) mbar_arrive(&sc_empty[sl]);
+            }
+          }
 #pragma unroll
-          for (int j = 0; j < 32; j += 2)
-            fma2(T[c + j], T[c + j + 1], f, __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+          for (int j = 0; j < 16; j += 2)
+            fma2(T[16 * c + j], T[16 * c + j + 1], f, __uint_as_float(v[c & 1][j]), __uint_as_float(v[c & 1][j + 1]));
         }
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&acc_empty[buf]);
         buf ^= 1;
         if (++st == T_STAGES) st = 0, ph ^= 1;
+        if (i == 3 || kb == KB - 1) {
+          if (++sl == T_SC_SLOTS) sl = 0, sph ^= 1;
+        }
       }
       if (!ok) break;
-      if (r_ok) {
+      const int row = t.row0 + 32 * q + lane;
+      const int n0 = t.n0 + 128 * half;
+      if (row < t.row_end) {
         uint16_t* yp = p.y + static_cast<size_t>(row) * p.N + n0;
 #pragma unroll
         for (int c = 0; c < 128; c += 8)
@@ -594,6 +662,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const __grid_constan
       }
     }
   }
+  __syncwarp();
 
   if (*abort_flag) {
     const uint64_t t0 = tc::globaltimer_ns();
@@ -604,7 +673,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const __grid_constan
   __syncthreads();
   if (warp == kTWarpMma) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, 2 * TN);
+    tc::tmem_dealloc(tmem, T_ACCS * TN);
   }
 }
 
