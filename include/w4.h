@@ -454,8 +454,9 @@ w4_status w4_fp8_block_moe_grouped_gemm(const void* qx, const float* x_scale, co
 /*
  * w4_fp8_block_moe_gemm_bf16in: row r is token row_token[r] of x [T, K] bf16
  * (row_token NULL: R == T and row r is token r), quantized per block into the
- * workspace (at least w4_workspace_bytes(W4_OP_FP8_BLOCK, R, N, K, E) bytes),
- * then w4_fp8_block_moe_grouped_gemm. A row_token entry outside [0, T) gives a
+ * workspace (w4_workspace_bytes(W4_OP_FP8_BLOCK, R, N, K, E) bytes; with only
+ * R * K + 4 * R * ceil(K/128) bytes, rounded up to 16, a token is quantized again for
+ * each of its rows), then w4_fp8_block_moe_grouped_gemm. A row_token entry outside [0, T) gives a
  * zero row and sets W4_ERR_SHAPE in the device status word.
  */
 w4_status w4_fp8_block_moe_gemm_bf16in(const void* x, int64_t T, const int32_t* row_token, const int32_t* expert_offsets,

@@ -131,7 +131,11 @@ size_t w4_workspace_bytes(int32_t op, int64_t M, int64_t N, int64_t K, int32_t g
   if (op == W4_OP_W4AFP8_MOE) return w4::w4a8_workspace_bytes(M, K);
   if (op == W4_OP_MOE_ROUTE_GROUPED)
     return (N > 0 && N <= 1024) ? w4::moe_route_grouped_workspace_bytes(M, static_cast<int32_t>(N)) : 0;
-  if (op == W4_OP_FP8_BLOCK) return w4::fp8_block_fuses(M, group > 0) ? 0 : w4::fp8_block_workspace_bytes(M, K);
+  if (op == W4_OP_FP8_BLOCK) {
+    if (w4::fp8_block_fuses(M, group > 0)) return 0;
+    // experts: the rows, and the tokens they come from when those are at most half as many
+    return w4::fp8_block_workspace_bytes(M, K) + (group > 0 ? w4::fp8_block_workspace_bytes(M / 2, K) : 0);
+  }
   if (op == W4_OP_MOE_ROUTE) return (N > 0 && N <= 1024) ? w4::moe_route_workspace_bytes(M, static_cast<int32_t>(N)) : 0;
   return 0;
 }
@@ -486,6 +490,8 @@ static w4_status run_fp8_block(const void* qx, const float* x_scale, const int32
   return from_cuda(w4::launch_fp8_block(a, static_cast<cudaStream_t>(stream)), "fp8 block product launch");
 }
 
+constexpr int64_t kCopyElements = int64_t{1} << 22;
+
 // Quantizes rows of x (gathered by `rows` when given) into the workspace, then multiplies.
 static w4_status run_fp8_block_act(const void* x, bool f16, int64_t T, const int32_t* rows, const int32_t* offsets,
                                    int32_t E, const void* qweight, const float* w_scale, const void* bias, void* y,
@@ -506,7 +512,18 @@ static w4_status run_fp8_block_act(const void* x, bool f16, int64_t T, const int
     return from_cuda(w4::launch_fp8_block(a, s), "fp8 block product launch");
   }
   float* x_scale = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + static_cast<size_t>(R) * K);   // K % 16 == 0
-  e = w4::launch_quant_block(x, f16, false, R, K, rows, T, ws, x_scale, status, s);
+  // Tokens that are rows of several experts are quantized once and their codes
+  // copied, when the workspace has room for the tokens' codes and the copy is
+  // worth a launch (32768 rows of 4096 tokens x 2048: see launch_gather_block_rows).
+  const size_t base = w4::fp8_block_workspace_bytes(R, K), tokens = w4::fp8_block_workspace_bytes(T, K);
+  if (rows != nullptr && 2 * T <= R && R * K >= kCopyElements && ws_bytes >= base + tokens) {
+    uint8_t* tq = static_cast<uint8_t*>(ws) + base;
+    float* ts = reinterpret_cast<float*>(tq + static_cast<size_t>(T) * K);
+    e = w4::launch_quant_block(x, f16, false, T, K, nullptr, 0, tq, ts, status, s);
+    if (e == cudaSuccess) e = w4::launch_gather_block_rows(tq, ts, T, K, rows, R, ws, x_scale, status, s);
+  } else {
+    e = w4::launch_quant_block(x, f16, false, R, K, rows, T, ws, x_scale, status, s);
+  }
   if (e != cudaSuccess) return from_cuda(e, "block quant launch");
   const w4::Fp8BlockArgs a{ws, x_scale, qweight, w_scale, bias, y, offsets, E, R, N, K, nullptr, false, true, status};
   return from_cuda(w4::launch_fp8_block(a, s), "fp8 block product launch");

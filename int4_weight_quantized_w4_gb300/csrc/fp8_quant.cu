@@ -9,12 +9,14 @@
 // would move a block's scale by up to 2^-8 whenever it moved its maximum).
 //
 // A block is 16 chunks of 8 elements: a half-warp holds it in registers, one
-// 16-byte load (two for gate and up) per lane, and its maximum is a 4-step
-// butterfly over the half-warp. No row-wide reduction exists, so a row is cut
-// into as many half-warps as it has blocks and one token fills several SMs.
-// Bound by HBM: 2 (or 4) bytes read and 1 + 4/128 written per element. Each
-// half-warp takes kUnits consecutive blocks of a row (one index division per
-// kUnits blocks) and loads them all before it reduces the first.
+// 16-byte load (two for gate and up) per lane. No row-wide reduction exists, so a
+// row is cut into as many half-warps as it has groups of kUnits blocks, and one
+// token fills several SMs. Bound by HBM (2 or 4 bytes read and 1 + 4/128 written
+// per element) once the instructions are few enough: the kUnits maxima of a
+// half-warp are reduced together, lanes trading one half of their values for the
+// other at each of the first steps, which leaves the maximum of unit l % kUnits
+// in lane l; each lane then divides once, for its unit, and the scales come back
+// by shuffles.
 #include "common.cuh"
 #include "launch.h"
 
@@ -23,6 +25,7 @@ namespace {
 
 constexpr int kBlk8 = 16;       // 8-element chunks per block of 128 columns
 constexpr int kThreads = 256;
+constexpr unsigned kFull = 0xFFFFFFFFu;
 
 // e4m3 codes of fl(x / s) for 8 fp32 values (the bracket of quant_e4m3_chunk
 // holds for any finite fp32 x).
@@ -51,57 +54,85 @@ W4_DEV float silu_f32(float g) {
   return __fdividef(g >= 0.f ? g : g * t, 1.f + t);
 }
 
+// The maximum over the half-warp of m[u] for u = lane % kUnits.
+template <int kUnits>
+W4_DEV float unit_max(const float (&m)[kUnits]) {
+  static_assert(kUnits == 2 || kUnits == 4, "one lane bit per halving");
+  const int lane = threadIdx.x & 31;
+  const bool b0 = lane & 1, b1 = lane & 2;
+  float z = fmaxf(b0 ? m[1] : m[0], __shfl_xor_sync(kFull, b0 ? m[0] : m[1], 1));
+  if constexpr (kUnits == 4) {
+    const float y = fmaxf(b0 ? m[3] : m[2], __shfl_xor_sync(kFull, b0 ? m[2] : m[3], 1));
+    z = fmaxf(b1 ? y : z, __shfl_xor_sync(kFull, b1 ? z : y, 2));
+  } else {
+    z = fmaxf(z, __shfl_xor_sync(kFull, z, 2));
+  }
+  z = fmaxf(z, __shfl_xor_sync(kFull, z, 4));
+  return fmaxf(z, __shfl_xor_sync(kFull, z, 8));
+}
+
 // x [*, K8 chunks], or with kSilu [*, 2 K8]; row r of the output comes from row
 // gather[r] (gather may be null: row r). An id outside [0, T) gives a zero row
 // with scales 1 and W4_ERR_SHAPE in the status word. KU = ceil(KB / kUnits).
 template <bool kF16, bool kSilu, int kUnits>
-__global__ void __launch_bounds__(kThreads) quant_block_kernel(const uint4* __restrict__ x, int64_t items, int K8,
-                                                               int KB, int KU, uint2* __restrict__ q,
+__global__ void __launch_bounds__(kThreads) quant_block_kernel(const uint4* __restrict__ x, uint32_t items, int K8,
+                                                               int KB, uint32_t KU, uint2* __restrict__ q,
                                                                float* __restrict__ scale,
                                                                const int32_t* __restrict__ gather, int64_t T,
                                                                unsigned int* status) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int l = threadIdx.x & (kBlk8 - 1);
-  const int64_t it = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / kBlk8;
+  const uint32_t it = blockIdx.x * (kThreads / kBlk8) + threadIdx.x / kBlk8;
   const bool live = it < items;                 // dead half-warps still take part in the shuffles
-  const int64_t row = live ? it / KU : 0;
-  const int b0 = live ? static_cast<int>(it - row * KU) * kUnits : KB;
+  const uint32_t row = it / KU;
+  const int b0 = static_cast<int>(it - row * KU) * kUnits;
   int64_t src = row;
   bool bad = false;
   if (gather != nullptr && live) {
     src = gather[row];
     bad = src < 0 || src >= T;
   }
+  const int c0 = live ? b0 * kBlk8 + l : K8;
   const uint4* xr = x + src * static_cast<int64_t>(kSilu ? 2 * K8 : K8);
   uint4 v[kUnits], u[kSilu ? kUnits : 1];
 #pragma unroll
   for (int i = 0; i < kUnits; ++i) {
-    const int c = (b0 + i) * kBlk8 + l;
-    const bool in = c < K8 && live && !bad;
+    const int c = c0 + i * kBlk8;
+    const bool in = c < K8 && !bad;
     v[i] = in ? ld_stream_v4(xr + c) : make_uint4(0, 0, 0, 0);
     if constexpr (kSilu) u[i] = in ? ld_stream_v4(xr + K8 + c) : make_uint4(0, 0, 0, 0);
   }
+  float m[kUnits], a[kSilu ? kUnits : 1][8];
 #pragma unroll
   for (int i = 0; i < kUnits; ++i) {
-    const int b = b0 + i, c = b * kBlk8 + l;
-    uint2 code;
-    float s;
     if constexpr (kSilu) {
       const uint32_t g[4] = {v[i].x, v[i].y, v[i].z, v[i].w}, w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-      float a[8], m = 0.f;
+      m[i] = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        a[2 * j] = silu_f32(bf16_lo(g[j])) * bf16_lo(w[j]);
-        a[2 * j + 1] = silu_f32(bf16_hi(g[j])) * bf16_hi(w[j]);
-        m = fmaxf(m, fmaxf(fabsf(a[2 * j]), fabsf(a[2 * j + 1])));
+        a[i][2 * j] = silu_f32(bf16_lo(g[j])) * bf16_lo(w[j]);
+        a[i][2 * j + 1] = silu_f32(bf16_hi(g[j])) * bf16_hi(w[j]);
+        m[i] = fmaxf(m[i], fmaxf(fabsf(a[i][2 * j]), fabsf(a[i][2 * j + 1])));
       }
-      s = block_scale(half_warp_max(m));
-      code = quant_e4m3_f32(a, quotient_bracket(s));
     } else {
-      quant_block_half_warp<kF16>(v[i], code, s);
+      const uint32_t m2 = absmax2<kF16>(absmax2<kF16>(v[i].x, v[i].y), absmax2<kF16>(v[i].z, v[i].w));
+      m[i] = fmaxf(fabsf(act_lo<kF16>(m2)), fabsf(act_hi<kF16>(m2)));
     }
-    if (c < K8 && live) q[row * K8 + c] = code;
-    if (l == 0 && live && b < KB) scale[row * KB + b] = s;
+  }
+  const QuotientBracket mine = quotient_bracket(block_scale(unit_max<kUnits>(m)));   // of block b0 + l % kUnits
+  if (l < kUnits && live && b0 + l < KB) scale[static_cast<size_t>(row) * KB + b0 + l] = mine.s;
+  uint2* qr = q + static_cast<size_t>(row) * K8;
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const QuotientBracket b{__shfl_sync(kFull, mine.s, i, kBlk8), __shfl_sync(kFull, mine.rlo, i, kBlk8),
+                            __shfl_sync(kFull, mine.rhi, i, kBlk8)};
+    const int c = c0 + i * kBlk8;
+    if (c < K8) {
+      if constexpr (kSilu)
+        qr[c] = quant_e4m3_f32(a[i], b);
+      else
+        qr[c] = quant_e4m3_chunk<kF16>(v[i], b);
+    }
   }
   if (bad && l == 0) report(status, W4_ERR_SHAPE);
 }
@@ -112,10 +143,48 @@ cudaError_t launch(const void* x, int64_t M, int64_t K, const int32_t* gather, i
   const int K8 = static_cast<int>(K / 8), KB = static_cast<int>((K + 127) / 128), KU = (KB + kUnits - 1) / kUnits;
   const int64_t items = M * KU;
   const int64_t blocks = (items * kBlk8 + kThreads - 1) / kThreads;
-  if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+  if (items > INT32_MAX) return cudaErrorInvalidConfiguration;
   quant_block_kernel<kF16, kSilu, kUnits><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(
-      static_cast<const uint4*>(x), items, K8, KB, KU, static_cast<uint2*>(q), scale, gather, T, status);
+      static_cast<const uint4*>(x), static_cast<uint32_t>(items), K8, KB, static_cast<uint32_t>(KU),
+      static_cast<uint2*>(q), scale, gather, T, status);
   return cudaGetLastError();
+}
+
+// Quantized rows copied to their places among the expert-sorted rows: row r of
+// (dst, dst_scale) is row gather[r] of (src, src_scale). A warp per row.
+__global__ void __launch_bounds__(kThreads) gather_rows_kernel(const uint4* __restrict__ src,
+                                                               const float* __restrict__ src_scale, int64_t T, int K16,
+                                                               int KB, const int32_t* __restrict__ gather, int64_t R,
+                                                               uint4* __restrict__ dst, float* __restrict__ dst_scale,
+                                                               unsigned int* status) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+  if (r >= R) return;
+  const int64_t t = gather[r];
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // src comes from the kernel before
+  uint4* d = dst + r * K16;
+  if (t < 0 || t >= T) {
+    for (int i = lane; i < K16; i += 32) d[i] = make_uint4(0, 0, 0, 0);
+    for (int i = lane; i < KB; i += 32) dst_scale[r * KB + i] = 1.f;
+    if (lane == 0) report(status, W4_ERR_SHAPE);
+    return;
+  }
+  const uint4* s = src + t * K16;
+  for (int i0 = 0; i0 < K16; i0 += 128) {
+    uint4 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = i0 + 32 * j + lane;
+      if (i < K16) v[j] = ld_cg_v4(s + i);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = i0 + 32 * j + lane;
+      if (i < K16) d[i] = v[j];
+    }
+  }
+  for (int i = lane; i < KB; i += 32) dst_scale[r * KB + i] = __ldcg(src_scale + t * KB + i);
 }
 
 }  // namespace
@@ -125,6 +194,23 @@ cudaError_t launch_quant_block(const void* x, bool f16, bool silu, int64_t M, in
   if (silu) return launch<false, true, 2>(x, M, K, gather, T, q, scale, status, s);
   return f16 ? launch<true, false, 4>(x, M, K, gather, T, q, scale, status, s)
              : launch<false, false, 4>(x, M, K, gather, T, q, scale, status, s);
+}
+
+cudaError_t launch_gather_block_rows(const void* src, const float* src_scale, int64_t T, int64_t K,
+                                     const int32_t* gather, int64_t R, void* dst, float* dst_scale,
+                                     unsigned int* status, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((R + kThreads / 32 - 1) / (kThreads / 32)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, gather_rows_kernel, static_cast<const uint4*>(src), src_scale, T,
+                            static_cast<int>(K / 16), static_cast<int>((K + 127) / 128), gather, R,
+                            static_cast<uint4*>(dst), dst_scale, status);
 }
 
 }  // namespace w4

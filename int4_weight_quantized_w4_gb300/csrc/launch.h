@@ -119,6 +119,10 @@ cudaError_t launch_moe_combine(const void* y, int64_t R, int64_t H, const float*
 // [*, 2K] (silu, bf16); gather (may be null): source row of each of the M output rows, checked against T.
 cudaError_t launch_quant_block(const void* x, bool f16, bool silu, int64_t M, int64_t K, const int32_t* gather,
                                int64_t T, void* q, float* scale, unsigned int* status, cudaStream_t s);
+// Rows gather[r] of quantized (src, src_scale) [T, K], which the kernel launched just before writes, as row r of (dst, dst_scale).
+cudaError_t launch_gather_block_rows(const void* src, const float* src_scale, int64_t T, int64_t K,
+                                     const int32_t* gather, int64_t R, void* dst, float* dst_scale,
+                                     unsigned int* status, cudaStream_t s);
 struct Fp8BlockArgs {
   const void* qx;                 // e4m3 [R, K]
   const float* x_scale;           // [R, ceil(K / 128)]
@@ -134,9 +138,10 @@ struct Fp8BlockArgs {
   bool pdl;                       // qx and x_scale come from the kernel launched just before, nothing else does
   unsigned int* status;
 };
-// Quantized rows of the 16-bit-input forms: codes [R, K], then scales [R, ceil(K / 128)].
+// Quantized rows of the 16-bit-input forms: codes [R, K], then scales [R, ceil(K / 128)], padded to 16 bytes.
 inline size_t fp8_block_workspace_bytes(int64_t R, int64_t K) {
-  return static_cast<size_t>(R) * static_cast<size_t>(K) + static_cast<size_t>(R) * static_cast<size_t>((K + 127) / 128) * 4;
+  const size_t n = static_cast<size_t>(R) * static_cast<size_t>(K) + static_cast<size_t>(R) * static_cast<size_t>((K + 127) / 128) * 4;
+  return (n + 15) / 16 * 16;
 }
 // Whether launch_fp8_block takes 16-bit activations.
 bool fp8_block_fuses(int64_t R, bool experts);
