@@ -260,12 +260,73 @@ W4_DEV float half_warp_max(float m) {
 }
 W4_DEV float block_scale(float amax) { return amax == 0.f ? 1.f : __fdiv_rn(amax, 448.f); }
 
+// (d0, d1) = (a0, a1) * b + (c0, c1), packed as fma2.
+W4_DEV void fma2c(float& d0, float& d1, float a0, float a1, float b, float c0, float c1) {
+  asm("{.reg .b64 d, x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %4}; mov.b64 z, {%5, %6}; "
+      "fma.rn.f32x2 d, x, y, z; mov.b64 {%0, %1}, d;}"
+      : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b), "f"(c0), "f"(c1));
+}
+
+// The e4m3 codes of the fp32 quotients fl(x0 / s), fl(x1 / s) in the low two
+// bytes, with r = fl(1 / s). Division by multiply-add refinement (P. Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor",
+// IBM J. Res. Dev. 34(1), 1990): with r the correctly rounded reciprocal and q
+// within one ulp of x / s, the remainder x - q s is exact in one FMA and
+// fl(q + remainder * r) is the correctly rounded quotient. fl(x r) is within 1.5
+// ulp; one step brings it within one, the second rounds it correctly. Holds while
+// the remainder does not underflow where it matters: a quotient below 2^-11 has
+// code 0 either way, and above that x is at least 2^-11 s and the remainder's last
+// bit 2^-48 x, so s >= kRefineMin = 2^-80 is ample. No branch: with the bracket of
+// quant_e4m3_chunk half of all warps met a tie of a bf16 ratio somewhere and paid
+// 8 divides (146 instructions a chunk, against 80).
+constexpr float kRefineMin = 8.27180613e-25f;
+W4_DEV uint32_t quotient2_e4m3(float x0, float x1, float s, float r) {
+  float q0, q1, e0, e1;
+  mul2(q0, q1, x0, x1, r);
+  fma2c(e0, e1, q0, q1, -s, x0, x1);
+  fma2c(q0, q1, e0, e1, r, q0, q1);
+  fma2c(e0, e1, q0, q1, -s, x0, x1);
+  fma2c(q0, q1, e0, e1, r, q0, q1);
+  return e4m3x2_rn(q0, q1);
+}
+
+// The codes of 8 values. s below kRefineMin (a block of values below 4e-22), or
+// not finite, takes the IEEE divide.
+W4_DEV uint2 quant_e4m3_block(const float (&x)[8], float s, float r) {
+  uint32_t p[4];
+  if (s >= kRefineMin && s < 1e37f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = quotient2_e4m3(x[2 * i], x[2 * i + 1], s, r);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = e4m3x2_rn(__fdiv_rn(x[2 * i], s), __fdiv_rn(x[2 * i + 1], s));
+  }
+  return make_uint2(prmt(p[0], p[1], 0x5410u), prmt(p[2], p[3], 0x5410u));
+}
+
+// A chunk's magnitude maximum, and its elements as fp32.
+template <bool kF16>
+W4_DEV float chunk_max(const uint4& v) {
+  const uint32_t m2 = absmax2<kF16>(absmax2<kF16>(v.x, v.y), absmax2<kF16>(v.z, v.w));
+  return fmaxf(fabsf(act_lo<kF16>(m2)), fabsf(act_hi<kF16>(m2)));
+}
+template <bool kF16>
+W4_DEV void chunk_f32(const uint4& v, float (&x)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = act_lo<kF16>(w[i]);
+    x[2 * i + 1] = act_hi<kF16>(w[i]);
+  }
+}
+
 // This lane's e4m3 codes and the block's scale; every lane of the warp takes part.
 template <bool kF16>
 W4_DEV void quant_block_half_warp(const uint4& v, uint2& code, float& s) {
-  const uint32_t m2 = absmax2<kF16>(absmax2<kF16>(v.x, v.y), absmax2<kF16>(v.z, v.w));
-  s = block_scale(half_warp_max(fmaxf(fabsf(act_lo<kF16>(m2)), fabsf(act_hi<kF16>(m2)))));
-  code = quant_e4m3_chunk<kF16>(v, quotient_bracket(s));
+  s = block_scale(half_warp_max(chunk_max<kF16>(v)));
+  float x[8];
+  chunk_f32<kF16>(v, x);
+  code = quant_e4m3_block(x, s, __frcp_rn(s));
 }
 
 // ---------------------------------------------------------------------------

@@ -28,7 +28,8 @@ namespace {
 
 constexpr int kBlk = 128;                     // k and weight rows per scale
 constexpr int kMaxExperts = 1024;
-constexpr int kFuseRows = 16;                 // up to this many dense rows the stream form quantizes
+constexpr int kMaxSplit = 8;                  // CTAs of a cluster that share a tile's k blocks
+constexpr int kFuseRows = 8;                 // up to this many dense rows the stream form quantizes
 constexpr uint64_t kWaitNs = 2000000000ull;   // 2 s per wait
 
 struct Params {
@@ -54,11 +55,11 @@ W4_DEV uint32_t cluster_rank() {
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-// The float at shared address `a` of CTA `rank` of the cluster.
-W4_DEV float ld_cluster_f32(uint32_t a, uint32_t rank) {
-  float v;
-  asm volatile("{.reg .b32 t; mapa.shared::cluster.u32 t, %1, %2; ld.shared::cluster.f32 %0, [t];}"
-               : "=f"(v) : "r"(a), "r"(rank) : "memory");
+// Four floats at shared address `a` of CTA `rank` of the cluster.
+W4_DEV float4 ld_cluster_f32x4(uint32_t a, uint32_t rank) {
+  float4 v;
+  asm volatile("{.reg .b32 t; mapa.shared::cluster.u32 t, %4, %5; ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [t];}"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a), "r"(rank) : "memory");
   return v;
 }
 // tc::wait by a whole warp with one answer: a warp whose lanes disagreed after a
@@ -243,7 +244,7 @@ __global__ void __launch_bounds__(Stream<NT, kQuant>::THREADS, Stream<NT, kQuant
     // Quantizer w takes blocks w, w + 4, ... of this CTA's sequence, a half-warp
     // per row; the next block's rows are loaded before this one's are reduced.
     if constexpr (kQuant) {
-      constexpr int RPH = NT / 2;                      // rows per half-warp
+      constexpr int RPH = kFuseRows / 2;               // rows per half-warp
       const int h = lane >> 4, l = lane & 15;
       const int K8 = p.K >> 3, nkb = kb1 - kb0;
       const long long items = first < p.items ? (p.items - first + step - 1) / step : 0;
@@ -415,20 +416,33 @@ __global__ void __launch_bounds__(Stream<NT, kQuant>::THREADS, Stream<NT, kQuant
   __syncwarp();
 
   if (p.split > 1) {
-    // one item per cluster: CTA r adds the parts of tokens r, r + split, ... in order of the parts
+    // One item per cluster: CTA r adds the parts of tokens r, r + split, ... in the
+    // order of the parts. A warp takes a token, 4 outputs a lane, with the loads of
+    // all parts in flight at once.
     cluster_arrive();
     cluster_wait();
     int e = 0;
     Tile t;
-    if (warp < 4 && decode(p, first, NT, kBlk, starts, t, e) && !*abort_flag) {
-      const int o = 32 * warp + lane, n = t.n0 + o;
+    if (decode(p, first, NT, kBlk, starts, t, e) && !*abort_flag) {
+      const int n = t.n0 + 4 * lane;
       if (n < p.N) {
-        const float bs = p.bias != nullptr ? __uint_as_float(static_cast<uint32_t>(p.bias[n]) << 16) : 0.f;
-        for (int j = part; j < t.row_end - t.row0; j += p.split) {
-          const uint32_t at = smem_addr(smem) + (j * kBlk + o) * 4;
-          float s = 0.f;
-          for (int r = 0; r < p.split; ++r) s += ld_cluster_f32(at, r);
-          p.y[static_cast<size_t>(t.row0 + j) * p.N + n] = static_cast<uint16_t>(f32_to_bf16_bits(s + bs));
+        float b[4] = {0.f, 0.f, 0.f, 0.f};
+        if (p.bias != nullptr) {
+          const uint2 bb = *reinterpret_cast<const uint2*>(p.bias + n);
+          b[0] = bf16_lo(bb.x), b[1] = bf16_hi(bb.x), b[2] = bf16_lo(bb.y), b[3] = bf16_hi(bb.y);
+        }
+        for (int j = part + warp * p.split; j < t.row_end - t.row0; j += C::THREADS / 32 * p.split) {
+          const uint32_t at = smem_addr(smem) + (j * kBlk + 4 * lane) * 4;
+          float4 v[kMaxSplit];
+#pragma unroll
+          for (int r = 0; r < kMaxSplit; ++r)
+            if (r < p.split) v[r] = ld_cluster_f32x4(at, r);
+          float4 s = v[0];
+#pragma unroll
+          for (int r = 1; r < kMaxSplit; ++r)
+            if (r < p.split) s.x += v[r].x, s.y += v[r].y, s.z += v[r].z, s.w += v[r].w;
+          *reinterpret_cast<uint2*>(p.y + static_cast<size_t>(t.row0 + j) * p.N + n) =
+              make_uint2(pack_bf16x2(s.x + b[0], s.y + b[1]), pack_bf16x2(s.z + b[2], s.w + b[3]));
         }
       }
     }
@@ -759,7 +773,7 @@ cudaError_t run_stream(const Fp8BlockArgs& a, Params& p, cudaStream_t s) {
   const int64_t slots = static_cast<int64_t>(current_sm_count()) * C::CTAS;
   p.split = 1;
   if (a.expert_offsets == nullptr)
-    while (p.split < 8 && p.items * p.split * 2 <= slots && p.KB >= 4 * p.split) p.split *= 2;
+    while (p.split < kMaxSplit && p.items * p.split * 2 <= slots && p.KB >= 4 * p.split) p.split *= 2;
   const int64_t grid = p.split > 1 ? p.items * p.split : (p.items < slots ? p.items : slots);
   return start(stream_kernel<NT, kQuant>, p, grid, C::THREADS, C::SMEM, p.split, a.pdl, s);
 }

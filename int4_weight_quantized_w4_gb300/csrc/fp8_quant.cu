@@ -27,31 +27,23 @@ constexpr int kBlk8 = 16;       // 8-element chunks per block of 128 columns
 constexpr int kThreads = 256;
 constexpr unsigned kFull = 0xFFFFFFFFu;
 
-// e4m3 codes of fl(x / s) for 8 fp32 values (the bracket of quant_e4m3_chunk
-// holds for any finite fp32 x).
-W4_DEV uint2 quant_e4m3_f32(const float (&x)[8], const QuotientBracket& b) {
-  uint32_t p[4];
-  uint32_t diff = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float l0, l1, h0, h1;
-    mul2(l0, l1, x[2 * i], x[2 * i + 1], b.rlo);
-    mul2(h0, h1, x[2 * i], x[2 * i + 1], b.rhi);
-    p[i] = e4m3x2_rn(l0, l1);
-    diff |= p[i] ^ e4m3x2_rn(h0, h1);
-  }
-  if (diff != 0) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = e4m3x2_rn(__fdiv_rn(x[2 * i], b.s), __fdiv_rn(x[2 * i + 1], b.s));
-  }
-  return make_uint2(prmt(p[0], p[1], 0x5410u), prmt(p[2], p[3], 0x5410u));
-}
-
-// silu(g) = g / (1 + e^-g) with the one exponential t = e^-|g| in (0, 1]: the
-// denominator stays in [1, 2], inside the fast divide's range for every g.
-W4_DEV float silu_f32(float g) {
-  const float t = __expf(-fabsf(g));
-  return __fdividef(g >= 0.f ? g : g * t, 1.f + t);
+// silu(g) * u of the bf16 pairs g and u. silu(g) = g / (1 + e^-g) with the one
+// exponential t = e^-|g| in (0, 1], as g / (1 + t), or g t / (1 + t) for g < 0: the
+// denominator stays in [1, 2], inside the fast reciprocal's range for every g. The
+// multiplications and additions go two at a time.
+W4_DEV void silu_mul2(uint32_t g, uint32_t u, float& a0, float& a1) {
+  const float g0 = bf16_lo(g), g1 = bf16_hi(g);
+  float t0, t1, d0, d1, n0, n1;
+  mul2(t0, t1, -fabsf(g0), -fabsf(g1), 1.44269504f);   // log2(e)
+  asm("ex2.approx.f32 %0, %1;" : "=f"(t0) : "f"(t0));
+  asm("ex2.approx.f32 %0, %1;" : "=f"(t1) : "f"(t1));
+  add2(d0, d1, t0, t1, 1.f);
+  n0 = g0 * t0;
+  n1 = g1 * t1;
+  n0 = g0 >= 0.f ? g0 : n0;
+  n1 = g1 >= 0.f ? g1 : n1;
+  a0 = __fdividef(n0, d0) * bf16_lo(u);
+  a1 = __fdividef(n1, d1) * bf16_hi(u);
 }
 
 // The maximum over the half-warp of m[u] for u = lane % kUnits.
@@ -110,28 +102,28 @@ __global__ void __launch_bounds__(kThreads) quant_block_kernel(const uint4* __re
       m[i] = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        a[i][2 * j] = silu_f32(bf16_lo(g[j])) * bf16_lo(w[j]);
-        a[i][2 * j + 1] = silu_f32(bf16_hi(g[j])) * bf16_hi(w[j]);
+        silu_mul2(g[j], w[j], a[i][2 * j], a[i][2 * j + 1]);
         m[i] = fmaxf(m[i], fmaxf(fabsf(a[i][2 * j]), fabsf(a[i][2 * j + 1])));
       }
     } else {
-      const uint32_t m2 = absmax2<kF16>(absmax2<kF16>(v[i].x, v[i].y), absmax2<kF16>(v[i].z, v[i].w));
-      m[i] = fmaxf(fabsf(act_lo<kF16>(m2)), fabsf(act_hi<kF16>(m2)));
+      m[i] = chunk_max<kF16>(v[i]);
     }
   }
-  const QuotientBracket mine = quotient_bracket(block_scale(unit_max<kUnits>(m)));   // of block b0 + l % kUnits
-  if (l < kUnits && live && b0 + l < KB) scale[static_cast<size_t>(row) * KB + b0 + l] = mine.s;
+  const float s_mine = block_scale(unit_max<kUnits>(m)), r_mine = __frcp_rn(s_mine);   // of block b0 + l % kUnits
+  if (l < kUnits && live && b0 + l < KB) scale[static_cast<size_t>(row) * KB + b0 + l] = s_mine;
   uint2* qr = q + static_cast<size_t>(row) * K8;
 #pragma unroll
   for (int i = 0; i < kUnits; ++i) {
-    const QuotientBracket b{__shfl_sync(kFull, mine.s, i, kBlk8), __shfl_sync(kFull, mine.rlo, i, kBlk8),
-                            __shfl_sync(kFull, mine.rhi, i, kBlk8)};
+    const float s = __shfl_sync(kFull, s_mine, i, kBlk8), r = __shfl_sync(kFull, r_mine, i, kBlk8);
     const int c = c0 + i * kBlk8;
     if (c < K8) {
-      if constexpr (kSilu)
-        qr[c] = quant_e4m3_f32(a[i], b);
-      else
-        qr[c] = quant_e4m3_chunk<kF16>(v[i], b);
+      if constexpr (kSilu) {
+        qr[c] = quant_e4m3_block(a[i], s, r);
+      } else {
+        float f[8];
+        chunk_f32<kF16>(v[i], f);
+        qr[c] = quant_e4m3_block(f, s, r);
+      }
     }
   }
   if (bad && l == 0) report(status, W4_ERR_SHAPE);
