@@ -220,8 +220,8 @@ w4_status w4a8_gemm_bf16in(const void* x, const void* qweight, const void* w_sca
  * x or the bias, or writes y). So qweight, w_scale and zeros must not be
  * written by a kernel that runs immediately before on the same stream and
  * signals its dependents early; kernels that do not (every kernel of this
- * library except this one and the per-block quantizers, and ordinary library
- * kernels) are waited for in full.
+ * library except this one and those of the fp8 block-scaled layer, and ordinary
+ * library kernels) are waited for in full.
  */
 w4_status w4a16_gemm(const void* x, const void* qweight, const void* w_scale, int32_t w_scale_dtype,
                      const void* zeros, int32_t group, const void* bias, void* y,
@@ -393,12 +393,18 @@ w4_status w4_moe_route_grouped(const void* logits, int32_t logits_f32, const flo
  * ceil(K/128)], dynamic activations); checkpoints whose experts were not
  * converted to int4 keep those in it too.
  *
+ * The entry points of this layer are launched with programmatic dependent launch,
+ * as w4a16_gemm is, and signal their own dependents early. They may start
+ * streaming qweight while the kernel before them on `stream` is finishing and wait
+ * for it before they touch anything else. So qweight must not be written by a
+ * kernel that runs immediately before on the same stream and signals its
+ * dependents early.
+ *
  * w4_quant_act_per_block: per row and block of 128 columns (the last one may be
  * shorter) amax = max |x|, s = amax / 448 in fp32 (1 where amax is 0),
  * q = e4m3(fl(x / s)), round to nearest even, saturating; the divides are IEEE.
  *   x [M, K] bf16 or fp16 (x_dtype), 16-byte aligned; K % 8 == 0
  *   q [M, K] e4m3 codes, 16-byte aligned; scale [M, ceil(K/128)] fp32
- * May signal its programmatic dependents early (see w4a16_gemm).
  */
 w4_status w4_quant_act_per_block(const void* x, int32_t x_dtype, int64_t M, int64_t K, void* q, float* scale,
                                  void* stream);

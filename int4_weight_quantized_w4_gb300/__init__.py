@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -161,10 +162,15 @@ def _out(t, name, shape, dtype, dtypes, device):
     return t
 
 
+@functools.lru_cache(maxsize=4096)
+def _scratch_bytes(lib, op, M, N, K, group):
+    return lib.w4_workspace_bytes(op, M, N, K, group)
+
+
 def _scratch(ws, op, M, N, K, group, device):
     """A workspace for a call and its size; none (None, 0) where none is needed."""
     if ws is None:
-        need = load().w4_workspace_bytes(op, M, N, K, group)
+        need = _scratch_bytes(load(), op, M, N, K, group)
         return (torch.empty(need, dtype=torch.uint8, device=device), need) if need else (None, 0)
     _expect(ws, "workspace", None, None, device)   # the library checks its size in bytes
     return ws, ws.numel() * ws.element_size()

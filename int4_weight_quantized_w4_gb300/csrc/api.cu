@@ -486,7 +486,7 @@ static w4_status run_fp8_block(const void* qx, const float* x_scale, const int32
   unsigned int* status = nullptr;
   cudaError_t e = status_ptr(&status);
   if (e != cudaSuccess) return from_cuda(e, "device status word");
-  const w4::Fp8BlockArgs a{qx, x_scale, qweight, w_scale, bias, y, offsets, E, R, N, K, nullptr, false, false, status};
+  const w4::Fp8BlockArgs a{qx, x_scale, qweight, w_scale, bias, y, offsets, E, R, N, K, nullptr, false, status};
   return from_cuda(w4::launch_fp8_block(a, static_cast<cudaStream_t>(stream)), "fp8 block product launch");
 }
 
@@ -508,7 +508,7 @@ static w4_status run_fp8_block_act(const void* x, bool f16, int64_t T, const int
   if (e != cudaSuccess) return from_cuda(e, "device status word");
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (fused) {
-    const w4::Fp8BlockArgs a{nullptr, nullptr, qweight, w_scale, bias, y, offsets, E, R, N, K, x, f16, false, status};
+    const w4::Fp8BlockArgs a{nullptr, nullptr, qweight, w_scale, bias, y, offsets, E, R, N, K, x, f16, status};
     return from_cuda(w4::launch_fp8_block(a, s), "fp8 block product launch");
   }
   float* x_scale = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + static_cast<size_t>(R) * K);   // K % 16 == 0
@@ -525,7 +525,7 @@ static w4_status run_fp8_block_act(const void* x, bool f16, int64_t T, const int
     e = w4::launch_quant_block(x, f16, false, R, K, rows, T, ws, x_scale, status, s);
   }
   if (e != cudaSuccess) return from_cuda(e, "block quant launch");
-  const w4::Fp8BlockArgs a{ws, x_scale, qweight, w_scale, bias, y, offsets, E, R, N, K, nullptr, false, true, status};
+  const w4::Fp8BlockArgs a{ws, x_scale, qweight, w_scale, bias, y, offsets, E, R, N, K, nullptr, false, status};
   return from_cuda(w4::launch_fp8_block(a, s), "fp8 block product launch");
 }
 

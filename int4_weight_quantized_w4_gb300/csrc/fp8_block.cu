@@ -15,8 +15,13 @@
 //  * tile (many rows): 128 tokens on the MMA's rows, 256 outputs on its columns,
 //    so that one scale sx * sw serves a thread's whole column strip. Bound by the
 //    hand-over and drain of one accumulator per block.
+//
+// Both are launched as programmatic dependents and let their own dependents go
+// early: the copies of weights start while the kernel before finishes, everything
+// else (activations, scales, bias, expert offsets, y) waits for it.
 #include <cuda.h>
 
+#include <atomic>
 #include <cstring>
 
 #include "common.cuh"
@@ -74,6 +79,7 @@ W4_DEV bool elect_one() {
   asm volatile("{.reg .pred P; elect.sync _|P, 0xFFFFFFFF; selp.u32 %0, 1, 0, P;}" : "=r"(p));
   return p != 0;
 }
+W4_DEV void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 W4_DEV void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // First row tile of every expert (tiles of `rows_per` rows), in shared memory:
@@ -215,10 +221,14 @@ __global__ void __launch_bounds__(Stream<NT, kQuant>::THREADS, Stream<NT, kQuant
   if (warp == kSWarpMma) tc::tmem_alloc(tmem_holder, C::TMEM_COLS);
   if (warp == kSWarpA && lane == 0) tc::prefetch_tmap(&p.tm_w);
   if (!kQuant && warp == kSWarpB && lane == 0) tc::prefetch_tmap(&p.tm_x);
-  if (p.offsets != nullptr) tile_starts<C::THREADS>(p, NT, starts, warp_sum);
+  if (p.offsets != nullptr) {
+    grid_dependency_wait();   // the routing may be running still
+    tile_starts<C::THREADS>(p, NT, starts, warp_sum);
+  }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
+  launch_dependents();
   const uint32_t tmem = *tmem_holder;
 
   // this CTA's part of the k blocks (the same for every item)
@@ -258,6 +268,7 @@ __global__ void __launch_bounds__(Stream<NT, kQuant>::THREADS, Stream<NT, kQuant
         }
       };
       uint4 cur[RPH], next[RPH];
+      grid_dependency_wait();   // x comes from the kernel before
       load(warp - kSWarpB, cur);
       for (int g = warp - kSWarpB; g < total; g += kQuantWarps) {
         const int kb = kb0 + g % nkb;
@@ -521,10 +532,14 @@ __global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const __grid_constan
     tc::prefetch_tmap(&p.tm_x);
     tc::prefetch_tmap(&p.tm_w);
   }
-  if (p.offsets != nullptr) tile_starts<kTThreads>(p, TM, starts, warp_sum);
+  if (p.offsets != nullptr) {
+    grid_dependency_wait();   // the routing may be running still
+    tile_starts<kTThreads>(p, TM, starts, warp_sum);
+  }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
+  launch_dependents();
   const uint32_t tmem = *tmem_holder;
   const int KB = p.KB;
 
@@ -735,30 +750,27 @@ int64_t row_tiles(const Fp8BlockArgs& a, int per) {
   return a.expert_offsets == nullptr ? whole : (a.R < whole + a.E ? a.R : whole + a.E);
 }
 
-cudaError_t start(void (*kernel)(Params), const Params& p, int64_t grid, int threads, int smem, int cluster, bool pdl,
-                  cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+// Lets a kernel use its dynamic shared memory: once per device, since the call
+// costs as much as the rest of the host path put together. A device reset takes
+// the setting back; the launch that then fails is repeated with it set again.
+template <void (*kKernel)(Params)>
+cudaError_t start(const Params& p, int64_t grid, int threads, int smem, int cluster, cudaStream_t s) {
+  static std::atomic<uint64_t> set{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[2];
-  int n = 0;
-  if (pdl) {
-    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[n++].val.programmaticStreamSerializationAllowed = 1;
+  const uint64_t bit = uint64_t{1} << (dev & 63);
+  PdlLaunch pl(static_cast<unsigned>(grid), threads, smem, s, cluster);
+  if (set.load(std::memory_order_relaxed) & bit) {
+    e = cudaLaunchKernelEx(&pl.cfg, kKernel, p);
+    if (e != cudaErrorInvalidValue) return e;
+    cudaGetLastError();
   }
-  if (cluster > 1) {
-    at[n].id = cudaLaunchAttributeClusterDimension;
-    at[n].val.clusterDim.x = cluster;
-    at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
-    ++n;
-  }
-  cfg.attrs = at;
-  cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  e = cudaLaunchKernelEx(&pl.cfg, kKernel, p);
+  if (e == cudaSuccess && dev < 64) set.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 template <int NT, bool kQuant>
@@ -775,7 +787,7 @@ cudaError_t run_stream(const Fp8BlockArgs& a, Params& p, cudaStream_t s) {
   if (a.expert_offsets == nullptr)
     while (p.split < kMaxSplit && p.items * p.split * 2 <= slots && p.KB >= 4 * p.split) p.split *= 2;
   const int64_t grid = p.split > 1 ? p.items * p.split : (p.items < slots ? p.items : slots);
-  return start(stream_kernel<NT, kQuant>, p, grid, C::THREADS, C::SMEM, p.split, a.pdl, s);
+  return start<stream_kernel<NT, kQuant>>(p, grid, C::THREADS, C::SMEM, p.split, s);
 }
 
 }  // namespace
@@ -813,7 +825,7 @@ cudaError_t launch_fp8_block(const Fp8BlockArgs& a, cudaStream_t s) {
   p.n_tiles = static_cast<int>((a.N + TN - 1) / TN);
   p.items = row_tiles(a, TM) * p.n_tiles;
   const int64_t sms = current_sm_count();
-  return start(tile_kernel, p, p.items < sms ? p.items : sms, kTThreads, T_SMEM, 1, a.pdl, s);
+  return start<tile_kernel>(p, p.items < sms ? p.items : sms, kTThreads, T_SMEM, 1, s);
 }
 
 }  // namespace w4

@@ -29,21 +29,19 @@ constexpr unsigned kFull = 0xFFFFFFFFu;
 
 // silu(g) * u of the bf16 pairs g and u. silu(g) = g / (1 + e^-g) with the one
 // exponential t = e^-|g| in (0, 1], as g / (1 + t), or g t / (1 + t) for g < 0: the
-// denominator stays in [1, 2], inside the fast reciprocal's range for every g. The
-// multiplications and additions go two at a time.
+// denominator stays in [1, 2], inside the fast reciprocal's range for every g. t
+// below 2^-126 (g < -87) counts as 0. Multiplications and additions go two at a time.
 W4_DEV void silu_mul2(uint32_t g, uint32_t u, float& a0, float& a1) {
   const float g0 = bf16_lo(g), g1 = bf16_hi(g);
-  float t0, t1, d0, d1, n0, n1;
+  float t0, t1, d0, d1;
   mul2(t0, t1, -fabsf(g0), -fabsf(g1), 1.44269504f);   // log2(e)
-  asm("ex2.approx.f32 %0, %1;" : "=f"(t0) : "f"(t0));
-  asm("ex2.approx.f32 %0, %1;" : "=f"(t1) : "f"(t1));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t0) : "f"(t0));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t1) : "f"(t1));
   add2(d0, d1, t0, t1, 1.f);
-  n0 = g0 * t0;
-  n1 = g1 * t1;
-  n0 = g0 >= 0.f ? g0 : n0;
-  n1 = g1 >= 0.f ? g1 : n1;
-  a0 = __fdividef(n0, d0) * bf16_lo(u);
-  a1 = __fdividef(n1, d1) * bf16_hi(u);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(d0) : "f"(d0));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(d1) : "f"(d1));
+  a0 = (g0 >= 0.f ? g0 : g0 * t0) * (d0 * bf16_lo(u));
+  a1 = (g1 >= 0.f ? g1 : g1 * t1) * (d1 * bf16_hi(u));
 }
 
 // The maximum over the half-warp of m[u] for u = lane % kUnits.
@@ -80,6 +78,9 @@ __global__ void __launch_bounds__(kThreads) quant_block_kernel(const uint4* __re
   const int b0 = static_cast<int>(it - row * KU) * kUnits;
   int64_t src = row;
   bool bad = false;
+  // The kernel before may still be running when this one starts (see launch): x and
+  // the row ids may come from it, and it may still be reading q.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (gather != nullptr && live) {
     src = gather[row];
     bad = src < 0 || src >= T;
@@ -136,10 +137,10 @@ cudaError_t launch(const void* x, int64_t M, int64_t K, const int32_t* gather, i
   const int64_t items = M * KU;
   const int64_t blocks = (items * kBlk8 + kThreads - 1) / kThreads;
   if (items > INT32_MAX) return cudaErrorInvalidConfiguration;
-  quant_block_kernel<kF16, kSilu, kUnits><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(
-      static_cast<const uint4*>(x), static_cast<uint32_t>(items), K8, KB, static_cast<uint32_t>(KU),
-      static_cast<uint2*>(q), scale, gather, T, status);
-  return cudaGetLastError();
+  PdlLaunch pl(static_cast<unsigned>(blocks), kThreads, 0, s);
+  return cudaLaunchKernelEx(&pl.cfg, quant_block_kernel<kF16, kSilu, kUnits>, static_cast<const uint4*>(x),
+                            static_cast<uint32_t>(items), K8, KB, static_cast<uint32_t>(KU), static_cast<uint2*>(q),
+                            scale, gather, T, status);
 }
 
 // Quantized rows copied to their places among the expert-sorted rows: row r of
@@ -191,16 +192,8 @@ cudaError_t launch_quant_block(const void* x, bool f16, bool silu, int64_t M, in
 cudaError_t launch_gather_block_rows(const void* src, const float* src_scale, int64_t T, int64_t K,
                                      const int32_t* gather, int64_t R, void* dst, float* dst_scale,
                                      unsigned int* status, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((R + kThreads / 32 - 1) / (kThreads / 32)));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gather_rows_kernel, static_cast<const uint4*>(src), src_scale, T,
+  PdlLaunch pl(static_cast<unsigned>((R + kThreads / 32 - 1) / (kThreads / 32)), kThreads, 0, s);
+  return cudaLaunchKernelEx(&pl.cfg, gather_rows_kernel, static_cast<const uint4*>(src), src_scale, T,
                             static_cast<int>(K / 16), static_cast<int>((K + 127) / 128), gather, R,
                             static_cast<uint4*>(dst), dst_scale, status);
 }

@@ -24,6 +24,30 @@ inline int current_sm_count() {
 // Polls a bounded wait makes before it gives up (about a second of spinning).
 constexpr long long kWaitLimit = 1LL << 24;
 
+// A launch that may start while the kernel before it on the stream finishes
+// (programmatic dependent launch): the kernel waits for it (griddepcontrol.wait)
+// before it reads anything that kernel writes or writes anything it reads. With
+// `cluster` > 1, in clusters of that many blocks.
+struct PdlLaunch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[2];
+  PdlLaunch(unsigned grid, unsigned block, size_t smem, cudaStream_t s, unsigned cluster = 1) {
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+  }
+  PdlLaunch(const PdlLaunch&) = delete;
+  PdlLaunch& operator=(const PdlLaunch&) = delete;
+};
+
 // status: the device status word (a timed-out wait records W4_ERR_TIMEOUT there).
 cudaError_t launch_quant_per_token(const void* x, bool x_f16, int64_t M, int64_t K, bool fp8, void* q,
                                    float* scale, unsigned int* status, cudaStream_t s);
@@ -135,7 +159,6 @@ struct Fp8BlockArgs {
   int64_t R, N, K;
   const void* x;                  // where fp8_block_fuses: 16-bit activations [R, K] in place of qx and x_scale
   bool x_f16;
-  bool pdl;                       // qx and x_scale come from the kernel launched just before, nothing else does
   unsigned int* status;
 };
 // Quantized rows of the 16-bit-input forms: codes [R, K], then scales [R, ceil(K / 128)], padded to 16 bytes.
