@@ -135,6 +135,10 @@ W4_DEV void mul2(float& d0, float& d1, float a0, float a1, float b) {
   asm("{.reg .b64 d, x, y; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %4}; mul.rn.f32x2 d, x, y; mov.b64 {%0, %1}, d;}"
       : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b));
 }
+W4_DEV void mul2v(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  asm("{.reg .b64 d, x, y; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mul.rn.f32x2 d, x, y; mov.b64 {%0, %1}, d;}"
+      : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
 W4_DEV void add2(float& d0, float& d1, float a0, float a1, float b) {
   asm("{.reg .b64 d, x, y; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %4}; add.rn.f32x2 d, x, y; mov.b64 {%0, %1}, d;}"
       : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b));

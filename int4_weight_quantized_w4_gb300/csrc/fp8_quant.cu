@@ -27,21 +27,22 @@ constexpr int kBlk8 = 16;       // 8-element chunks per block of 128 columns
 constexpr int kThreads = 256;
 constexpr unsigned kFull = 0xFFFFFFFFu;
 
-// silu(g) * u of the bf16 pairs g and u. silu(g) = g / (1 + e^-g) with the one
-// exponential t = e^-|g| in (0, 1], as g / (1 + t), or g t / (1 + t) for g < 0: the
-// denominator stays in [1, 2], inside the fast reciprocal's range for every g. t
-// below 2^-126 (g < -87) counts as 0. Multiplications and additions go two at a time.
+// silu(g) * u = g u / (1 + 2^(-g log2 e)) of the bf16 pairs g and u, with the fast
+// exponential and reciprocal (a few ulp). The exponent is held to 126, so that the
+// denominator stays a normal number and its reciprocal too: for g < -87 the
+// result is g u 2^-126 instead of a number smaller still. Multiplications and
+// additions go two at a time.
 W4_DEV void silu_mul2(uint32_t g, uint32_t u, float& a0, float& a1) {
   const float g0 = bf16_lo(g), g1 = bf16_hi(g);
-  float t0, t1, d0, d1;
-  mul2(t0, t1, -fabsf(g0), -fabsf(g1), 1.44269504f);   // log2(e)
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t0) : "f"(t0));
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t1) : "f"(t1));
-  add2(d0, d1, t0, t1, 1.f);
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(d0) : "f"(d0));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(d1) : "f"(d1));
-  a0 = (g0 >= 0.f ? g0 : g0 * t0) * (d0 * bf16_lo(u));
-  a1 = (g1 >= 0.f ? g1 : g1 * t1) * (d1 * bf16_hi(u));
+  float t0, t1;
+  mul2(t0, t1, g0, g1, -1.44269504f);   // -log2(e)
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t0) : "f"(fminf(t0, 126.f)));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t1) : "f"(fminf(t1, 126.f)));
+  add2(t0, t1, t0, t1, 1.f);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t0) : "f"(t0));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t1) : "f"(t1));
+  mul2v(a0, a1, g0, g1, bf16_lo(u), bf16_hi(u));
+  mul2v(a0, a1, a0, a1, t0, t1);
 }
 
 // The maximum over the half-warp of m[u] for u = lane % kUnits.
