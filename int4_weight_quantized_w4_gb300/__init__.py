@@ -4,14 +4,14 @@ A thin ctypes binding over the C ABI in ``include/w4.h`` (``libw4.so``). Each
 function has the name of the C entry point it calls and only marshals
 arguments: it checks tensor shapes and dtypes, allocates outputs with PyTorch
 when the caller passes none, and passes raw device pointers plus the current
-CUDA stream. Every step of the computation runs in the library's kernels;
+CUDA stream. The fp8 block-scaled layer and its router, whose decode calls are
+shorter than that work takes in Python, do it in a compiled module. Every step of the computation runs in the library's kernels;
 there is no fallback. If ``libw4.so`` has not been built the first call raises.
 """
 from __future__ import annotations
 
 import contextlib
 import ctypes
-import functools
 import os
 
 import torch
@@ -115,16 +115,6 @@ def _stream(stream, device):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
-def _raw_stream(stream, device):
-    """The handle of ``stream``, or of the device's current stream (2 us less than
-    through a Stream object)."""
-    if stream is not None:
-        return stream.cuda_stream
-    if device.index is None:
-        return torch.cuda.current_stream(device).cuda_stream
-    return torch._C._cuda_getCurrentRawStream(device.index)
-
-
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -152,32 +142,6 @@ def _expect(t, name, shape, dtypes, device, optional=False):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if dtypes is not None and t.dtype not in dtypes:
         raise ValueError(f"{name} must have dtype in {dtypes}, got {t.dtype}")
-
-
-def _out(t, name, shape, dtype, dtypes, device):
-    """``t`` checked as by ``_expect``, or a new tensor when it is None."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _expect(t, name, shape, dtypes, device)
-    return t
-
-
-@functools.lru_cache(maxsize=4096)
-def _scratch_bytes(lib, op, M, N, K, group):
-    return lib.w4_workspace_bytes(op, M, N, K, group)
-
-
-def _scratch(ws, op, M, N, K, group, device):
-    """A workspace for a call and its size; none (None, 0) where none is needed."""
-    if ws is None:
-        need = _scratch_bytes(load(), op, M, N, K, group)
-        return (torch.empty(need, dtype=torch.uint8, device=device), need) if need else (None, 0)
-    _expect(ws, "workspace", None, None, device)   # the library checks its size in bytes
-    return ws, ws.numel() * ws.element_size()
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
 
 
 def _groups(K, group):
@@ -420,7 +384,26 @@ def w4_moe_route(logits, top_k: int, renormalize: bool = False, out=None, worksp
 
 
 _SCORING = {"sigmoid": W4_SCORE_SIGMOID, "softmax": W4_SCORE_SOFTMAX}
-_LOGIT_T, _ACT_T = (torch.bfloat16, torch.float32), (torch.bfloat16, torch.float16)
+_binding_module = None
+
+
+def _native():
+    """The compiled half of the binding (``csrc/binding.cpp``): the functions below
+    check their tensors, allocate and call the library there."""
+    global _binding_module
+    if _binding_module is None:
+        load()
+        try:
+            from . import _binding as module
+        except ImportError as e:
+            raise RuntimeError(f"the compiled binding does not load ({e}): build it first "
+                               "(python -c 'import __graft_entry__ as g; g.build()')") from e
+        _binding_module = module
+    return _binding_module
+
+
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def w4_moe_route_grouped(logits, top_k: int, bias=None, n_group: int = 1, topk_group: int = 1,
@@ -432,133 +415,36 @@ def w4_moe_route_grouped(logits, top_k: int, bias=None, n_group: int = 1, topk_g
     groups of consecutive experts. Weights are the scores, renormalized over the
     chosen if asked, times ``scale``. Returns (and takes as ``out``) the tuple of
     ``w4_moe_route``: ``(topk_ids, topk_weights, offsets, row_token, row_of)``."""
-    _cuda2d(logits, "logits", _LOGIT_T)
     if scoring not in _SCORING:
         raise ValueError("scoring must be 'sigmoid' or 'softmax'")
-    T, E = logits.shape
-    dev = logits.device
-    if bias is not None:
-        _expect(bias, "bias", (E,), _F32, dev)
-    if out is None:
-        ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
-        wts = torch.empty((T, top_k), dtype=torch.float32, device=dev)
-        off = (torch.empty if T else torch.zeros)(E + 1, dtype=torch.int32, device=dev)
-        rt = torch.empty(T * top_k, dtype=torch.int32, device=dev)
-        ro = torch.empty((T, top_k), dtype=torch.int32, device=dev)
-        out = ids, wts, off, rt, ro
-    else:
-        ids, wts, off, rt, ro = out
-        _expect(ids, "topk_ids", (T, top_k), _I32T, dev)
-        _expect(wts, "topk_weights", (T, top_k), _F32, dev)
-        _expect(off, "offsets", (E + 1,), _I32T, dev)
-        _expect(rt, "row_token", (T * top_k,), _I32T, dev)
-        _expect(ro, "row_of", (T, top_k), _I32T, dev)
-    ws, wsb = _scratch(workspace, W4_OP_MOE_ROUTE_GROUPED, T, E, 1, 0, dev)
-    st = load().w4_moe_route_grouped(logits.data_ptr(), logits.dtype == torch.float32, _addr(bias), T, E, top_k, n_group,
-                                     topk_group, _SCORING[scoring], bool(renormalize), scale, ids.data_ptr(),
-                                     wts.data_ptr(), off.data_ptr(), rt.data_ptr(), ro.data_ptr(), _addr(ws), wsb,
-                                     _raw_stream(stream, dev))
-    if st:
-        _check(st, "w4_moe_route_grouped")
-    return out
-
-
-def _blocks(n):
-    return (n + 127) // 128
-
-
-def _act_dtype(x):
-    return W4_FP16 if x.dtype == torch.float16 else W4_BF16
+    return _native().route_grouped(logits, top_k, bias, n_group, topk_group, _SCORING[scoring], renormalize, scale, out,
+                                 workspace, _handle(stream))
 
 
 def w4_quant_act_per_block(x, q=None, scale=None, stream=None):
     """e4m3 quantization of bf16 or fp16 ``x [M, K]`` with one scale per row and
     128 columns; returns ``(q float8_e4m3fn [M, K], scale fp32 [M, ceil(K/128)])``."""
-    _cuda2d(x, "x", _ACT_T)
-    M, K = x.shape
-    dev = x.device
-    q = _out(q, "q", (M, K), torch.float8_e4m3fn, _FP8_T, dev)
-    scale = _out(scale, "scale", (M, _blocks(K)), torch.float32, _F32, dev)
-    st = load().w4_quant_act_per_block(x.data_ptr(), _act_dtype(x), M, K, q.data_ptr(), scale.data_ptr(),
-                                       _raw_stream(stream, dev))
-    if st:
-        _check(st, "w4_quant_act_per_block")
-    return q, scale
+    return _native().quant_block(x, q, scale, _handle(stream))
 
 
 def w4_silu_mul_quant_block(h, q=None, scale=None, stream=None):
     """``silu(gate) * up`` of the bf16 gate_up output ``h [R, 2I]``, quantized to
     e4m3 per row and 128 columns; returns ``(q [R, I], scale [R, ceil(I/128)])``."""
-    _cuda2d(h, "h", _BF16T)
-    R, I2 = h.shape
-    if I2 % 2:
-        raise ValueError("h must hold gate and up halves of equal width")
-    I = I2 // 2
-    dev = h.device
-    q = _out(q, "q", (R, I), torch.float8_e4m3fn, _FP8_T, dev)
-    scale = _out(scale, "scale", (R, _blocks(I)), torch.float32, _F32, dev)
-    st = load().w4_silu_mul_quant_block(h.data_ptr(), R, I, q.data_ptr(), scale.data_ptr(), _raw_stream(stream, dev))
-    if st:
-        _check(st, "w4_silu_mul_quant_block")
-    return q, scale
-
-
-def _block_weight_args(what, qweight, w_scale, K, device, bias):
-    """e4m3 ``qweight [N, K]`` (float8_e4m3fn or uint8 codes) with fp32 ``w_scale
-    [ceil(N/128), ceil(K/128)]`` and optional bf16 ``bias [N]``; returns N."""
-    _expect(qweight, "qweight", None, _FP8_T, device)
-    if qweight.dim() != 2 or qweight.shape[1] != K:
-        raise ValueError(f"inconsistent shapes for {what}")
-    N = qweight.shape[0]
-    _expect(w_scale, "w_scale", (_blocks(N), _blocks(K)), _F32, device)
-    if bias is not None:
-        _expect(bias, "bias", (N,), _BF16T, device)
-    return N
-
-
-def _block_expert_args(what, qweight, w_scale, expert_offsets, K, device):
-    """e4m3 ``qweight [E, N, K]``, fp32 ``w_scale [E, ceil(N/128), ceil(K/128)]``
-    and int32 ``expert_offsets [E + 1]``; returns (E, N)."""
-    _expect(qweight, "qweight", None, _FP8_T, device)
-    if qweight.dim() != 3 or qweight.shape[2] != K:
-        raise ValueError(f"inconsistent shapes for {what}")
-    E, N = qweight.shape[0], qweight.shape[1]
-    _expect(w_scale, "w_scale", (E, _blocks(N), _blocks(K)), _F32, device)
-    _expect(expert_offsets, "expert_offsets", (E + 1,), _I32T, device)
-    return E, N
+    return _native().silu_mul_quant_block(h, q, scale, _handle(stream))
 
 
 def w4_fp8_block_gemm(qx, x_scale, qweight, w_scale, bias=None, y=None, stream=None):
     """fp8 block-scaled linear: e4m3 ``qx [M, K]`` with fp32 ``x_scale [M,
     ceil(K/128)]`` (from ``w4_quant_act_per_block``) times e4m3 ``qweight [N, K]``
-    with fp32 ``w_scale [ceil(N/128), ceil(K/128)]``; returns bf16 ``[M, N]``."""
-    _cuda2d(qx, "qx", _FP8_T)
-    M, K = qx.shape
-    dev = qx.device
-    N = _block_weight_args("w4_fp8_block_gemm", qweight, w_scale, K, dev, bias)
-    _expect(x_scale, "x_scale", (M, _blocks(K)), _F32, dev)
-    y = _out(y, "y", (M, N), torch.bfloat16, _BF16T, dev)
-    st = load().w4_fp8_block_gemm(qx.data_ptr(), x_scale.data_ptr(), qweight.data_ptr(), w_scale.data_ptr(), _addr(bias),
-                                  y.data_ptr(), M, N, K, _raw_stream(stream, dev))
-    if st:
-        _check(st, "w4_fp8_block_gemm")
-    return y
+    (float8_e4m3fn or uint8 codes) with fp32 ``w_scale [ceil(N/128),
+    ceil(K/128)]`` and optional bf16 ``bias [N]``; returns bf16 ``[M, N]``."""
+    return _native().gemm(qx, x_scale, qweight, w_scale, bias, y, _handle(stream))
 
 
 def w4_fp8_block_gemm_bf16in(x, qweight, w_scale, bias=None, y=None, workspace=None, stream=None):
-    """fp8 block-scaled linear from bf16 or fp16 ``x [M, K]``, quantized per block
+    """``w4_fp8_block_gemm`` from bf16 or fp16 ``x [M, K]``, quantized per block
     inside the call; returns bf16 ``[M, N]``. One token is the decode call."""
-    _cuda2d(x, "x", _ACT_T)
-    M, K = x.shape
-    dev = x.device
-    N = _block_weight_args("w4_fp8_block_gemm_bf16in", qweight, w_scale, K, dev, bias)
-    y = _out(y, "y", (M, N), torch.bfloat16, _BF16T, dev)
-    ws, wsb = _scratch(workspace, W4_OP_FP8_BLOCK, M, N, K, 0, dev)
-    st = load().w4_fp8_block_gemm_bf16in(x.data_ptr(), _act_dtype(x), qweight.data_ptr(), w_scale.data_ptr(),
-                                         _addr(bias), y.data_ptr(), M, N, K, _addr(ws), wsb, _raw_stream(stream, dev))
-    if st:
-        _check(st, "w4_fp8_block_gemm_bf16in")
-    return y
+    return _native().gemm_act(x, qweight, w_scale, bias, y, workspace, _handle(stream))
 
 
 def w4_fp8_block_moe_grouped_gemm(qx, x_scale, expert_offsets, qweight, w_scale, y=None, stream=None):
@@ -566,38 +452,14 @@ def w4_fp8_block_moe_grouped_gemm(qx, x_scale, expert_offsets, qweight, w_scale,
     grouped by expert) with fp32 ``x_scale [R, ceil(K/128)]``, int32 device
     ``expert_offsets [E+1]``, e4m3 ``qweight [E, N, K]``, fp32 ``w_scale [E,
     ceil(N/128), ceil(K/128)]``; returns bf16 ``[R, N]``."""
-    _cuda2d(qx, "qx", _FP8_T)
-    R, K = qx.shape
-    dev = qx.device
-    E, N = _block_expert_args("w4_fp8_block_moe_grouped_gemm", qweight, w_scale, expert_offsets, K, dev)
-    _expect(x_scale, "x_scale", (R, _blocks(K)), _F32, dev)
-    y = _out(y, "y", (R, N), torch.bfloat16, _BF16T, dev)
-    st = load().w4_fp8_block_moe_grouped_gemm(qx.data_ptr(), x_scale.data_ptr(), expert_offsets.data_ptr(), E,
-                                              qweight.data_ptr(), w_scale.data_ptr(), y.data_ptr(), R, N, K,
-                                              _raw_stream(stream, dev))
-    if st:
-        _check(st, "w4_fp8_block_moe_grouped_gemm")
-    return y
+    return _native().moe_gemm(qx, x_scale, expert_offsets, qweight, w_scale, y, _handle(stream))
 
 
 def w4_fp8_block_moe_gemm_bf16in(x, row_token, expert_offsets, qweight, w_scale, y=None, workspace=None, stream=None):
     """``w4_fp8_block_moe_grouped_gemm`` from bf16 token rows: row r is
     ``x[row_token[r]]`` (``row_token`` None: row r is token r), quantized per block
     inside the call. Returns bf16 ``[R, N]``."""
-    _cuda2d(x, "x", _BF16T)
-    T, K = x.shape
-    dev = x.device
-    _expect(row_token, "row_token", None, _I32T, dev, optional=True)
-    R = T if row_token is None else row_token.numel()
-    E, N = _block_expert_args("w4_fp8_block_moe_gemm_bf16in", qweight, w_scale, expert_offsets, K, dev)
-    y = _out(y, "y", (R, N), torch.bfloat16, _BF16T, dev)
-    ws, wsb = _scratch(workspace, W4_OP_FP8_BLOCK, R, N, K, E, dev)
-    st = load().w4_fp8_block_moe_gemm_bf16in(x.data_ptr(), T, _addr(row_token), expert_offsets.data_ptr(), E,
-                                             qweight.data_ptr(), w_scale.data_ptr(), y.data_ptr(), R, N, K, _addr(ws),
-                                             wsb, _raw_stream(stream, dev))
-    if st:
-        _check(st, "w4_fp8_block_moe_gemm_bf16in")
-    return y
+    return _native().moe_gemm_act(x, row_token, expert_offsets, qweight, w_scale, y, workspace, _handle(stream))
 
 
 def w4_moe_gather_quant_fp8(x, row_token, q=None, scale=None, stream=None):

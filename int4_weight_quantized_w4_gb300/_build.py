@@ -2,7 +2,9 @@
 
 Each translation unit compiles in parallel to ``_obj/*.o``; the shared library
 links against the shared CUDA runtime (the same one PyTorch loads). A unit is
-rebuilt when it or any header is newer than its object file.
+rebuilt when it or any header is newer than its object file. ``binding.cpp``, the
+compiled half of the Python binding, becomes the extension module ``_binding``
+against PyTorch's headers and ``libw4.so``.
 """
 from __future__ import annotations
 
@@ -18,6 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJ = os.path.join(PKG, "_obj")
 LIB = os.path.join(PKG, "libw4.so")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-warn-spills",
@@ -43,6 +46,26 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _host_flags():
+    """g++ flags for the extension module: PyTorch's and CUDA's headers, Python's, and the C++ ABI PyTorch was built with."""
+    import sysconfig
+
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    dirs = [inc, os.path.join(inc, "torch", "csrc", "api", "include"), cuda, sysconfig.get_paths()["include"], INCLUDE]
+    return ["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] + \
+        [f for d in dirs for f in ("-isystem", d)]
+
+
+def _run(cmd, what: str, verbose: bool):
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+
 def build(verbose: bool = False, extra_flags=None) -> str:
     """Compile every kernel for sm_103a and link ``libw4.so``; return its path."""
     os.makedirs(OBJ, exist_ok=True)
@@ -64,8 +87,16 @@ def build(verbose: bool = False, extra_flags=None) -> str:
                 print(r.stdout + r.stderr, flush=True)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
+    host_src, host_obj = os.path.join(CSRC, "binding.cpp"), os.path.join(OBJ, "binding.o")
+
+    def compile_host():
+        if _stale(host_obj, [host_src] + headers):
+            _run(["g++"] + _host_flags() + ["-c", host_src, "-o", host_obj], "g++ on binding.cpp", verbose)
+
+    with cf.ThreadPoolExecutor(max_workers=min(12, os.cpu_count() or 1)) as ex:
+        host = ex.submit(compile_host)
         objs = list(ex.map(compile_one, sources))
+        host.result()
     if _stale(LIB, objs):
         tmp = LIB + ".tmp"
         cmd = [cc] + ARCH + ["-shared", "-cudart", "shared", "-o", tmp] + objs
@@ -75,6 +106,13 @@ def build(verbose: bool = False, extra_flags=None) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    if _stale(BINDING, [host_obj, LIB]):
+        import torch
+        tmp = BINDING + ".tmp"
+        _run(["g++", "-shared", "-o", tmp, host_obj, "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-lc10",
+              "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python", "-L", PKG, "-l:libw4.so",
+              "-Wl,-rpath,$ORIGIN"], "link of the binding", verbose)
+        os.replace(tmp, BINDING)
     return LIB
 
 
