@@ -15,20 +15,22 @@
 //
 // A warp takes a token: lane l holds experts l, l + 32, ... as integer keys in
 // the order of their values (sign folded, -0 taken as +0), so that a warp
-// maximum is one redux. A CTA takes a tile of tokens and counts its rows per
-// expert; the place kernel, a CTA per tile, turns the counts of all tiles into
-// the tile's first row in every expert (each thread sums an expert's column, a
-// block scan adds the experts before) and ranks the tile's rows by token with
-// bit masks. At most kMaxTiles tiles: the count table that every place CTA
-// reads stays small. A call whose tokens fit one tile is one CTA and one
-// launch. Bound by instruction issue for many tokens, by latency for few.
+// maximum is one redux. A lane keeps its two largest keys at hand and looks
+// through the others only when both are taken, which about one of eight choices
+// asks for. A CTA takes a tile of tokens and counts its rows per expert; the place
+// kernel, a CTA per tile, turns the counts of all tiles into the tile's first row
+// in every expert (column sums, then a block scan over the experts) and ranks the
+// tile's rows by token with bit masks. At most kMaxTiles tiles, one per SM: the
+// count table that every place CTA reads stays small. A call of up to a token per
+// warp of one CTA is one launch. Bound by instruction issue for many tokens, by
+// latency for few.
 #include "common.cuh"
 #include "launch.h"
 
 namespace w4 {
 namespace {
 
-constexpr int kMaxTiles = 256;
+constexpr int kMaxTiles = 152;
 constexpr int kChunk = 128;             // tokens ranked at a time
 constexpr int kChunkWarps = kChunk / 32;
 constexpr uint32_t kNoKey = 0;          // below every key (the key of -inf is 0x007FFFFF)
@@ -40,69 +42,85 @@ W4_DEV uint32_t ordered_key(float f) {
 }
 W4_DEV float key_value(uint32_t u) { return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xFFFFFFFFu)); }
 
-// A logit as the routing reads it: NaN counts as -inf, +inf as the largest finite number.
-W4_DEV float route_logit(const MoeRouteArgs& a, int64_t i) {
-  const float v = a.bf16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(a.logits)[i]) << 16)
-                         : static_cast<const float*>(a.logits)[i];
-  return isnan(v) ? -INFINITY : fminf(v, 3.402823466e38f);
-}
+constexpr float kMaxFinite = 3.402823466e38f;
 W4_DEV float sigmoid_f32(float v) { return __frcp_rn(1.f + expf(-v)); }   // 1 / x, correctly rounded
 
-// keys: kEPL * 33 words of shared memory of this warp (padded, so that groups
-// of 32 start in different banks). Chosen experts go to ids[0 .. k) and wts.
+// This lane's logits of token t; lanes and slots past E hold -inf. NaN counts as
+// -inf, +inf as the largest finite number.
 template <int kEPL>
-W4_DEV void route_token(const MoeRouteArgs& a, int64_t t, uint32_t* keys, int (&mine)[2]) {
+W4_DEV void load_logits(const MoeRouteArgs& a, int64_t t, float (&v)[kEPL]) {
+  const int lane = threadIdx.x & 31;
+  bool odd = false;
+  if (a.bf16) {
+    const uint16_t* p = static_cast<const uint16_t*>(a.logits) + t * a.E + lane;
+#pragma unroll
+    for (int i = 0; i < kEPL; ++i)
+      v[i] = lane + 32 * i < a.E ? __uint_as_float(static_cast<uint32_t>(p[32 * i]) << 16) : -INFINITY;
+  } else {
+    const float* p = static_cast<const float*>(a.logits) + t * a.E + lane;
+#pragma unroll
+    for (int i = 0; i < kEPL; ++i) v[i] = lane + 32 * i < a.E ? p[32 * i] : -INFINITY;
+  }
+#pragma unroll
+  for (int i = 0; i < kEPL; ++i) odd |= !(v[i] <= kMaxFinite);
+  if (odd) {
+#pragma unroll
+    for (int i = 0; i < kEPL; ++i) v[i] = isnan(v[i]) ? -INFINITY : fminf(v[i], kMaxFinite);
+  }
+}
+
+// Chooses for token t with logits v (overwritten). row: kEPL * 33 words of shared
+// memory of this warp (expert e at e + e / 32: groups of 32 start in different
+// banks). mine: choices lane and lane + 32.
+template <int kEPL>
+W4_DEV void route_token(const MoeRouteArgs& a, int64_t t, float (&v)[kEPL], uint32_t* row, int (&mine)[2]) {
   const int lane = threadIdx.x & 31;
   const int E = a.E;
   uint32_t key[kEPL];
-  float mx = -INFINITY, sum = 0.f;
-  {
-    float v[kEPL];
+  float sum = 0.f, mx = -INFINITY;
+  if (a.softmax) {
 #pragma unroll
-    for (int i = 0; i < kEPL; ++i) v[i] = lane + 32 * i < E ? route_logit(a, t * E + lane + 32 * i) : -INFINITY;
+    for (int i = 0; i < kEPL; ++i) mx = fmaxf(mx, v[i]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+  }
+  if (a.bias == nullptr) {
+#pragma unroll
+    for (int i = 0; i < kEPL; ++i) key[i] = lane + 32 * i < E ? ordered_key(v[i]) : kNoKey;
     if (a.softmax) {
 #pragma unroll
-      for (int i = 0; i < kEPL; ++i) mx = fmaxf(mx, v[i]);
+      for (int i = 0; i < kEPL; ++i) sum += v[i] != -INFINITY ? expf(v[i] - mx) : 0.f;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
-      float ex[kEPL];
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    }
+  } else {
+    if (a.softmax) {
+      double d = 0.0;
 #pragma unroll
-      for (int i = 0; i < kEPL; ++i) ex[i] = v[i] != -INFINITY ? expf(v[i] - mx) : 0.f;
-      if (a.bias != nullptr) {
-        double d = 0.0;
-#pragma unroll
-        for (int i = 0; i < kEPL; ++i) d += static_cast<double>(ex[i]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(kFull, d, o);
-        sum = static_cast<float>(d);
-#pragma unroll
-        for (int i = 0; i < kEPL; ++i) v[i] = sum > 0.f ? __fdiv_rn(ex[i], sum) : 0.f;
-      } else {
-#pragma unroll
-        for (int i = 0; i < kEPL; ++i) sum += ex[i];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+      for (int i = 0; i < kEPL; ++i) {
+        v[i] = v[i] != -INFINITY ? expf(v[i] - mx) : 0.f;
+        d += static_cast<double>(v[i]);
       }
-    } else if (a.bias != nullptr) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(kFull, d, o);
+      sum = static_cast<float>(d);
+#pragma unroll
+      for (int i = 0; i < kEPL; ++i) v[i] = sum > 0.f ? __fdiv_rn(v[i], sum) : 0.f;
+    } else {
 #pragma unroll
       for (int i = 0; i < kEPL; ++i) v[i] = sigmoid_f32(v[i]);
     }
 #pragma unroll
     for (int i = 0; i < kEPL; ++i) {
       const int e = lane + 32 * i;
-      float kv = v[i];
-      if (a.bias != nullptr && e < E) {
-        kv += __ldg(a.bias + e);
-        if (isnan(kv)) kv = -INFINITY;
-      }
-      key[i] = e < E ? ordered_key(kv) : kNoKey;
+      key[i] = e < E ? ordered_key(v[i] + __ldg(a.bias + e)) : kNoKey;
     }
   }
 
   if (a.topk_group < a.n_group) {
     const int gs = E / a.n_group;
 #pragma unroll
-    for (int i = 0; i < kEPL; ++i) keys[lane + 33 * i] = key[i];   // expert e at e + e / 32
+    for (int i = 0; i < kEPL; ++i) row[lane + 33 * i] = key[i];
     __syncwarp();
     // L lanes per group (a power of two): lane = group * L + part
     int L = 1;
@@ -112,7 +130,7 @@ W4_DEV void route_token(const MoeRouteArgs& a, int64_t t, uint32_t* keys, int (&
     if (g < a.n_group)
       for (int j = lane & (L - 1); j < gs; j += L) {
         const int e = g * gs + j;
-        const uint32_t u = keys[e + (e >> 5)];
+        const uint32_t u = row[e + (e >> 5)];
         m2 = max(m2, min(m1, u));
         m1 = max(m1, u);
       }
@@ -138,40 +156,56 @@ W4_DEV void route_token(const MoeRouteArgs& a, int64_t t, uint32_t* keys, int (&
     }
     __syncwarp();
   }
+  // the logits, or with a bias the scores, where a choice finds them by expert
+#pragma unroll
+  for (int i = 0; i < kEPL; ++i) row[lane + 33 * i] = __float_as_uint(v[i]);
+  __syncwarp();
 
-  // k rounds of a warp maximum; the lane that holds the winner drops it
-  mine[0] = mine[1] = 0;             // choices lane and lane + 32
-  uint32_t best;
-  int at;
-  auto rescan = [&]() {
-    best = key[0];
-    at = 0;
+  // k rounds of a warp maximum over every lane's best key. b1 and b2 are the
+  // lane's two largest, the lower expert first among equals.
+  mine[0] = mine[1] = 0;
+  uint32_t b1, b2;
+  int i1, i2;
+  auto scan = [&]() {
+    b1 = key[0], i1 = 0, b2 = kNoKey, i2 = 0;
 #pragma unroll
-    for (int i = 1; i < kEPL; ++i)
-      if (key[i] > best) best = key[i], at = i;
-  };
-  rescan();
-  for (int j = 0; j < a.k; ++j) {
-    const uint32_t m = __reduce_max_sync(kFull, best);
-    const unsigned e = __reduce_min_sync(kFull, best == m ? static_cast<unsigned>(lane + 32 * at) : 0xFFFFu);
-    if (lane == static_cast<int>(e & 31)) {
-#pragma unroll
-      for (int i = 0; i < kEPL; ++i)
-        if (i == at) key[i] = kNoKey;
-      rescan();
+    for (int i = 1; i < kEPL; ++i) {
+      const bool first = key[i] > b1, second = key[i] > b2;
+      b2 = first ? b1 : second ? key[i] : b2;
+      i2 = first ? i1 : second ? i : i2;
+      b1 = first ? key[i] : b1;
+      i1 = first ? i : i1;
     }
+  };
+  scan();
+  uint32_t taken = 0;
+  for (int j = 0; j < a.k; ++j) {
+    const uint32_t m = __reduce_max_sync(kFull, b1);
+    const unsigned e = __reduce_min_sync(kFull, b1 == m ? static_cast<unsigned>(lane + 32 * i1) : 0xFFFFu);
     if (lane == (j & 31)) mine[j >> 5] = static_cast<int>(e);
+    if (lane == static_cast<int>(e & 31)) {
+      taken |= 1u << i1;
+      b1 = b2, i1 = i2, b2 = kNoKey;
+      if (kEPL > 1 && b1 == kNoKey) {   // both are taken: look through the rest
+#pragma unroll
+        for (int i = 0; i < kEPL; ++i)
+          if ((taken >> i) & 1u) key[i] = kNoKey;
+        scan();
+      }
+    }
   }
   float w[2], total = 0.f;
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     w[s] = 0.f;
     if (lane + 32 * s < a.k) {
-      const float v = route_logit(a, t * E + mine[s]);
-      if (!a.softmax)
-        w[s] = sigmoid_f32(v);
+      const float x = __uint_as_float(row[mine[s] + (mine[s] >> 5)]);
+      if (a.bias != nullptr)
+        w[s] = x;
+      else if (!a.softmax)
+        w[s] = sigmoid_f32(x);
       else
-        w[s] = v != -INFINITY ? __fdiv_rn(expf(v - mx), sum) : 0.f;
+        w[s] = x != -INFINITY ? __fdiv_rn(expf(x - mx), sum) : 0.f;
     }
     total += w[s];
   }
@@ -187,6 +221,7 @@ W4_DEV void route_token(const MoeRouteArgs& a, int64_t t, uint32_t* keys, int (&
       a.ids[t * a.k + lane + 32 * s] = mine[s];
       a.wts[t * a.k + lane + 32 * s] = w[s] * a.factor;
     }
+  __syncwarp();   // row is free
 }
 
 // Rows of tokens [t0, t1) in order: base[e] is expert e's next row, moved on
@@ -252,7 +287,7 @@ W4_DEV void add_expert_starts(const MoeRouteArgs& a, const int32_t* total, int32
   if (write && threadIdx.x == 0) a.offsets[a.E] = carry;
 }
 
-// Warps per CTA: the keys of all warps take 34 KB at most.
+// Most warps per CTA: the rows of all warps take 34 KB at most.
 template <int kEPL>
 constexpr int kRouteWarps = kEPL <= 8 ? 32 : 256 / kEPL;
 constexpr int kPlaceWords = (2 * kChunkWarps + 2) * 1024;   // bits, first, base, total for 1024 experts
@@ -267,17 +302,25 @@ __global__ void __launch_bounds__(32 * kRouteWarps<kEPL>) route_tile_kernel(cons
   __shared__ uint32_t buf[kWhole && kPlaceWords > kKeyWords ? kPlaceWords : kKeyWords];
   __shared__ int32_t cnt[32 * kEPL];
   __shared__ int32_t part[32];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   for (int e = threadIdx.x; e < 32 * kEPL; e += blockDim.x) cnt[e] = 0;
   __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the kernel before writes the logits
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * per, t1 = t0 + per < a.T ? t0 + per : a.T;
-  for (int64_t t = t0 + warp; t < t1; t += kRouteWarps<kEPL>) {
+  float v[kEPL], next[kEPL];
+  if (t0 + warp < t1) load_logits<kEPL>(a, t0 + warp, v);
+  for (int64_t t = t0 + warp; t < t1; t += warps) {
+    if (!kWhole && t + warps < t1) load_logits<kEPL>(a, t + warps, next);
     int mine[2];
-    route_token<kEPL>(a, t, buf + warp * kEPL * 33, mine);
+    route_token<kEPL>(a, t, v, buf + warp * kEPL * 33, mine);
 #pragma unroll
     for (int s = 0; s < 2; ++s)
       if (lane + 32 * s < a.k) atomicAdd(&cnt[mine[s]], 1);
+    if (!kWhole) {
+#pragma unroll
+      for (int i = 0; i < kEPL; ++i) v[i] = next[i];
+    }
   }
   __syncthreads();
   if (!kWhole) {
@@ -291,7 +334,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps<kEPL>) route_tile_kernel(cons
   place_tokens(a, t0, t1, buf, reinterpret_cast<int32_t*>(buf) + kChunkWarps * a.E, base);
 }
 
-constexpr int kPlaceThreads = 256;
+constexpr int kPlaceThreads = 512;
 __global__ void __launch_bounds__(kPlaceThreads) place_kernel(const MoeRouteArgs a, int per,
                                                               const int32_t* __restrict__ counts, int ntiles) {
   extern __shared__ uint32_t sm[];
@@ -301,63 +344,65 @@ __global__ void __launch_bounds__(kPlaceThreads) place_kernel(const MoeRouteArgs
   int32_t* base = first + kChunkWarps * a.E;
   int32_t* total = base + a.E;
   const int tile = blockIdx.x;
+  for (int e = threadIdx.x; e < 2 * a.E; e += kPlaceThreads) base[e] = 0;   // and total
+  __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  for (int e = threadIdx.x; e < a.E; e += kPlaceThreads) {
-    int before = 0, after = 0;
-#pragma unroll 8
-    for (int i = 0; i < tile; ++i) before += counts[static_cast<int64_t>(i) * a.E + e];
-#pragma unroll 8
-    for (int i = tile; i < ntiles; ++i) after += counts[static_cast<int64_t>(i) * a.E + e];
-    base[e] = before;
-    total[e] = before + after;
-  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // column sums: as many threads per expert as there are, each over a share of the tiles
+  const int segs = a.E < kPlaceThreads ? kPlaceThreads / a.E : 1;
+  const int seg = a.E < kPlaceThreads ? threadIdx.x / a.E : 0;
+  if (seg < segs)
+    for (int e = threadIdx.x - seg * a.E; e < a.E; e += kPlaceThreads) {
+      const int i0 = ntiles * seg / segs, i1 = ntiles * (seg + 1) / segs;
+      int before = 0, all = 0;
+#pragma unroll 16
+      for (int i = i0; i < i1; ++i) {
+        const int c = __ldcg(counts + static_cast<int64_t>(i) * a.E + e);
+        all += c;
+        before += i < tile ? c : 0;
+      }
+      atomicAdd(&base[e], before);
+      atomicAdd(&total[e], all);
+    }
   __syncthreads();
   add_expert_starts(a, total, base, part, tile == 0);
   const int64_t t0 = static_cast<int64_t>(tile) * per, t1 = t0 + per < a.T ? t0 + per : a.T;
   place_tokens(a, t0, t1, bits, first, base);
 }
 
-// Tokens per tile: one or two a warp while that makes at most kMaxTiles tiles.
-int64_t tile_tokens(int64_t T, int warps) {
-  int64_t per = warps;
-  while ((T + per - 1) / per > kMaxTiles) per *= 2;
-  return per;
-}
 int route_warps(int E) { return E <= 256 ? 32 : E <= 512 ? 16 : 8; }
-// One CTA does the whole call up to this many tokens: two per warp.
-bool one_tile(int64_t T, int E) { return T <= 2 * route_warps(E); }
+// One CTA does the whole call up to a token per warp.
+bool one_tile(int64_t T, int E) { return T <= route_warps(E); }
+// Tokens per tile, at least 4 (a CTA of 4 warps).
+int64_t tile_tokens(int64_t T) {
+  const int64_t per = (T + kMaxTiles - 1) / kMaxTiles;
+  return per < 4 ? 4 : per;
+}
 
 template <int kEPL>
 cudaError_t launch_k(const MoeRouteArgs& a, cudaStream_t s) {
-  constexpr int kThreads = 32 * kRouteWarps<kEPL>;
   if (one_tile(a.T, a.E)) {
-    route_tile_kernel<kEPL, true><<<1, kThreads, 0, s>>>(a, static_cast<int>(a.T), nullptr);
-    return cudaGetLastError();
+    const int warps = a.T < 8 ? 8 : static_cast<int>(a.T);   // ranking and scanning take the whole CTA
+    PdlLaunch pl(1, 32 * warps, 0, s);
+    return cudaLaunchKernelEx(&pl.cfg, route_tile_kernel<kEPL, true>, a, static_cast<int>(a.T),
+                              static_cast<int32_t*>(nullptr));
   }
-  const int per = static_cast<int>(tile_tokens(a.T, kRouteWarps<kEPL>));
+  const int64_t per = tile_tokens(a.T);
   const int ntiles = static_cast<int>((a.T + per - 1) / per);
+  const int warps = static_cast<int>(per < kRouteWarps<kEPL> ? per : kRouteWarps<kEPL>);
   int32_t* counts = static_cast<int32_t*>(a.workspace);
-  route_tile_kernel<kEPL, false><<<ntiles, kThreads, 0, s>>>(a, per, counts);
-  cudaError_t e = cudaGetLastError();
+  PdlLaunch rl(ntiles, 32 * warps, 0, s);
+  cudaError_t e = cudaLaunchKernelEx(&rl.cfg, route_tile_kernel<kEPL, false>, a, static_cast<int>(per), counts);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ntiles);
-  cfg.blockDim = dim3(kPlaceThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(2 * kChunkWarps + 2) * a.E * 4;   // at most 40 KB
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, place_kernel, a, per, static_cast<const int32_t*>(counts), ntiles);
+  PdlLaunch pl(ntiles, kPlaceThreads, static_cast<size_t>(2 * kChunkWarps + 2) * a.E * 4, s);   // at most 40 KB
+  return cudaLaunchKernelEx(&pl.cfg, place_kernel, a, static_cast<int>(per), static_cast<const int32_t*>(counts), ntiles);
 }
 
 }  // namespace
 
 size_t moe_route_grouped_workspace_bytes(int64_t T, int32_t E) {
   if (one_tile(T, E)) return 0;
-  const int64_t per = tile_tokens(T, route_warps(E));
+  const int64_t per = tile_tokens(T);
   return static_cast<size_t>((T + per - 1) / per) * static_cast<size_t>(E) * sizeof(int32_t);
 }
 
