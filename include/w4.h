@@ -74,7 +74,8 @@ typedef enum {
   W4_OP_W4AFP8_MOE = 1,     /* w4afp8_moe_grouped_gemm, w4afp8_moe_gemm_bf16in (M = R, the row count) */
   W4_OP_MOE_ROUTE = 2,      /* w4_moe_route (M = T tokens, N = E experts; K = 1, group ignored) */
   W4_OP_MOE_ROUTE_GROUPED = 3, /* w4_moe_route_grouped (M = T tokens, N = E experts; K = 1, group ignored) */
-  W4_OP_FP8_BLOCK = 4       /* w4_fp8_block_gemm_bf16in (group ignored), w4_fp8_block_moe_gemm_bf16in (M = R rows, group = E) */
+  W4_OP_FP8_BLOCK = 4,      /* w4_fp8_block_gemm (group ignored) */
+  W4_OP_FP8_BLOCK_IN = 5    /* w4_fp8_block_gemm_bf16in (group = 0), w4_fp8_block_moe_gemm_bf16in (M = R rows, group = E) */
 } w4_op;
 
 /* Router scores of w4_moe_route_grouped. */
@@ -428,19 +429,23 @@ w4_status w4_silu_mul_quant_block(const void* h, int64_t R, int64_t I, void* q, 
  * N % 8 == 0, K % 16 == 0 (a K that is a multiple of 8 only: W4_ERR_UNSUPPORTED);
  * neither has to be a multiple of 128. Matrices and the bias are 16-byte aligned. Few
  * rows take a form that streams the weights once for all of them; M == 1 is
- * the decode call. Outputs do not depend on the number of SMs' timing: sums
- * are taken in a fixed order.
+ * the decode call. Sums are taken in a fixed order: a call's outputs are the same
+ * every time. workspace: w4_workspace_bytes(W4_OP_FP8_BLOCK, M, N, K, 0) bytes,
+ * 16-byte aligned, for the fp32 sums of tiles that are split along K (0 bytes
+ * where none is). NULL, or a smaller one: no tile is split.
  */
 w4_status w4_fp8_block_gemm(const void* qx, const float* x_scale, const void* qweight, const float* w_scale,
-                            const void* bias, void* y, int64_t M, int64_t N, int64_t K, void* stream);
+                            const void* bias, void* y, int64_t M, int64_t N, int64_t K, void* workspace,
+                            size_t workspace_bytes, void* stream);
 
 /*
  * w4_fp8_block_gemm_bf16in: w4_quant_act_per_block and w4_fp8_block_gemm in one
  * call: x [M, K] bf16 or fp16 (x_dtype), its codes and scales in the workspace
- * (at least w4_workspace_bytes(W4_OP_FP8_BLOCK, M, N, K, 0) bytes, 16-byte
+ * (at least w4_workspace_bytes(W4_OP_FP8_BLOCK_IN, M, N, K, 0) bytes, 16-byte
  * aligned; 0 bytes for few rows, where the product quantizes x itself and the
- * workspace may be NULL). y equals the two calls' bit for bit. The product's
- * weights start streaming while x is being quantized.
+ * workspace may be NULL; with only M * K + 4 * M * ceil(K/128) bytes, rounded up
+ * to 16, no tile is split). y equals the two calls' with their workspaces bit for
+ * bit. The product's weights start streaming while x is being quantized.
  */
 w4_status w4_fp8_block_gemm_bf16in(const void* x, int32_t x_dtype, const void* qweight, const float* w_scale,
                                    const void* bias, void* y, int64_t M, int64_t N, int64_t K, void* workspace,
@@ -460,7 +465,7 @@ w4_status w4_fp8_block_moe_grouped_gemm(const void* qx, const float* x_scale, co
 /*
  * w4_fp8_block_moe_gemm_bf16in: row r is token row_token[r] of x [T, K] bf16
  * (row_token NULL: R == T and row r is token r), quantized per block into the
- * workspace (w4_workspace_bytes(W4_OP_FP8_BLOCK, R, N, K, E) bytes; with only
+ * workspace (w4_workspace_bytes(W4_OP_FP8_BLOCK_IN, R, N, K, E) bytes; with only
  * R * K + 4 * R * ceil(K/128) bytes, rounded up to 16, a token is quantized again for
  * each of its rows), then w4_fp8_block_moe_grouped_gemm. A row_token entry outside [0, T) gives a
  * zero row and sets W4_ERR_SHAPE in the device status word.

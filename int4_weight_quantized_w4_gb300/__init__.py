@@ -28,13 +28,13 @@ __all__ = [
     "w4_device_status", "w4_selftest_bounded_wait", "apply_weights", "MIN_TOKENS_FOR_INT8",
     "W4_OK", "W4_ERR_NULL", "W4_ERR_ALIGN", "W4_ERR_GROUP", "W4_ERR_DTYPE",
     "W4_ERR_UNSUPPORTED", "W4_ERR_SHAPE", "W4_ERR_CUDA", "W4_ERR_TIMEOUT", "W4_ERR_WORKSPACE",
-    "W4_OP_W4A8", "W4_OP_W4AFP8_MOE", "W4_OP_MOE_ROUTE", "W4_OP_MOE_ROUTE_GROUPED", "W4_OP_FP8_BLOCK", "w4_workspace_bytes", "EXPORTED_SYMBOLS",
+    "W4_OP_W4A8", "W4_OP_W4AFP8_MOE", "W4_OP_MOE_ROUTE", "W4_OP_MOE_ROUTE_GROUPED", "W4_OP_FP8_BLOCK", "W4_OP_FP8_BLOCK_IN", "w4_workspace_bytes", "EXPORTED_SYMBOLS",
 ]
 
 (W4_OK, W4_ERR_NULL, W4_ERR_ALIGN, W4_ERR_GROUP, W4_ERR_DTYPE, W4_ERR_UNSUPPORTED,
  W4_ERR_SHAPE, W4_ERR_CUDA, W4_ERR_TIMEOUT, W4_ERR_WORKSPACE) = range(10)
 W4_BF16, W4_FP16, W4_INT8, W4_FP8_E4M3 = range(4)
-W4_OP_W4A8, W4_OP_W4AFP8_MOE, W4_OP_MOE_ROUTE, W4_OP_MOE_ROUTE_GROUPED, W4_OP_FP8_BLOCK = range(5)
+W4_OP_W4A8, W4_OP_W4AFP8_MOE, W4_OP_MOE_ROUTE, W4_OP_MOE_ROUTE_GROUPED, W4_OP_FP8_BLOCK, W4_OP_FP8_BLOCK_IN = range(6)
 W4_SCORE_SIGMOID, W4_SCORE_SOFTMAX = range(2)
 
 _DIR = os.path.dirname(os.path.abspath(__file__))
@@ -67,7 +67,7 @@ _SIGNATURES = {
                                     _SZ, _P]),
     "w4_quant_act_per_block": (_I32, [_P, _I32, _I64, _I64, _P, _P, _P]),
     "w4_silu_mul_quant_block": (_I32, [_P, _I64, _I64, _P, _P, _P]),
-    "w4_fp8_block_gemm": (_I32, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P]),
+    "w4_fp8_block_gemm": (_I32, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _SZ, _P]),
     "w4_fp8_block_gemm_bf16in": (_I32, [_P, _I32, _P, _P, _P, _P, _I64, _I64, _I64, _P, _SZ, _P]),
     "w4_fp8_block_moe_grouped_gemm": (_I32, [_P, _P, _P, _I32, _P, _P, _P, _I64, _I64, _I64, _P]),
     "w4_fp8_block_moe_gemm_bf16in": (_I32, [_P, _I64, _P, _P, _I32, _P, _P, _P, _I64, _I64, _I64, _P, _SZ, _P]),
@@ -433,12 +433,12 @@ def w4_silu_mul_quant_block(h, q=None, scale=None, stream=None):
     return _native().silu_mul_quant_block(h, q, scale, _handle(stream))
 
 
-def w4_fp8_block_gemm(qx, x_scale, qweight, w_scale, bias=None, y=None, stream=None):
+def w4_fp8_block_gemm(qx, x_scale, qweight, w_scale, bias=None, y=None, workspace=None, stream=None):
     """fp8 block-scaled linear: e4m3 ``qx [M, K]`` with fp32 ``x_scale [M,
     ceil(K/128)]`` (from ``w4_quant_act_per_block``) times e4m3 ``qweight [N, K]``
     (float8_e4m3fn or uint8 codes) with fp32 ``w_scale [ceil(N/128),
     ceil(K/128)]`` and optional bf16 ``bias [N]``; returns bf16 ``[M, N]``."""
-    return _native().gemm(qx, x_scale, qweight, w_scale, bias, y, _handle(stream))
+    return _native().gemm(qx, x_scale, qweight, w_scale, bias, y, workspace, _handle(stream))
 
 
 def w4_fp8_block_gemm_bf16in(x, qweight, w_scale, bias=None, y=None, workspace=None, stream=None):

@@ -131,10 +131,13 @@ size_t w4_workspace_bytes(int32_t op, int64_t M, int64_t N, int64_t K, int32_t g
   if (op == W4_OP_W4AFP8_MOE) return w4::w4a8_workspace_bytes(M, K);
   if (op == W4_OP_MOE_ROUTE_GROUPED)
     return (N > 0 && N <= 1024) ? w4::moe_route_grouped_workspace_bytes(M, static_cast<int32_t>(N)) : 0;
-  if (op == W4_OP_FP8_BLOCK) {
+  if ((op == W4_OP_FP8_BLOCK || op == W4_OP_FP8_BLOCK_IN) && N <= 0) return 0;
+  if (op == W4_OP_FP8_BLOCK) return w4::fp8_block_part_bytes(M, N, K);
+  if (op == W4_OP_FP8_BLOCK_IN) {
     if (w4::fp8_block_fuses(M, group > 0)) return 0;
-    // experts: the rows, and the tokens they come from when those are at most half as many
-    return w4::fp8_block_workspace_bytes(M, K) + (group > 0 ? w4::fp8_block_workspace_bytes(M / 2, K) : 0);
+    // the rows, and then: experts, the tokens they come from when those are at most half as many; dense, part sums
+    return w4::fp8_block_workspace_bytes(M, K) +
+           (group > 0 ? w4::fp8_block_workspace_bytes(M / 2, K) : w4::fp8_block_part_bytes(M, N, K));
   }
   if (op == W4_OP_MOE_ROUTE) return (N > 0 && N <= 1024) ? w4::moe_route_workspace_bytes(M, static_cast<int32_t>(N)) : 0;
   return 0;
@@ -478,15 +481,17 @@ static w4_status check_block_workspace(void* ws, size_t bytes, int64_t rows, int
 
 static w4_status run_fp8_block(const void* qx, const float* x_scale, const int32_t* offsets, int32_t E,
                                const void* qweight, const float* w_scale, const void* bias, void* y, int64_t R,
-                               int64_t N, int64_t K, void* stream) {
+                               int64_t N, int64_t K, void* ws, size_t ws_bytes, void* stream) {
   if (!qx || !x_scale || !qweight || !w_scale || !y) return fail(W4_ERR_NULL, "required pointer is NULL");
   if (!aligned(qx, 16) || !aligned(qweight, 16) || !aligned(y, 16) || !aligned(x_scale, 4) || !aligned(w_scale, 4) ||
       !aligned(offsets, 4) || !aligned(bias, 16))
     return fail(W4_ERR_ALIGN, "matrices and the bias must be 16-byte aligned, scales and offsets 4-byte aligned");
+  if (ws != nullptr && !aligned(ws, 16)) return fail(W4_ERR_WORKSPACE, "workspace must be 16-byte aligned");
   unsigned int* status = nullptr;
   cudaError_t e = status_ptr(&status);
   if (e != cudaSuccess) return from_cuda(e, "device status word");
-  const w4::Fp8BlockArgs a{qx, x_scale, qweight, w_scale, bias, y, offsets, E, R, N, K, nullptr, false, status};
+  const w4::Fp8BlockArgs a{qx, x_scale, qweight, w_scale, bias,  y,       offsets, E, R, N, K,
+                           nullptr, false, static_cast<float*>(ws), ws == nullptr ? 0 : ws_bytes, status};
   return from_cuda(w4::launch_fp8_block(a, static_cast<cudaStream_t>(stream)), "fp8 block product launch");
 }
 
@@ -508,7 +513,7 @@ static w4_status run_fp8_block_act(const void* x, bool f16, int64_t T, const int
   if (e != cudaSuccess) return from_cuda(e, "device status word");
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (fused) {
-    const w4::Fp8BlockArgs a{nullptr, nullptr, qweight, w_scale, bias, y, offsets, E, R, N, K, x, f16, status};
+    const w4::Fp8BlockArgs a{nullptr, nullptr, qweight, w_scale, bias, y, offsets, E, R, N, K, x, f16, nullptr, 0, status};
     return from_cuda(w4::launch_fp8_block(a, s), "fp8 block product launch");
   }
   float* x_scale = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + static_cast<size_t>(R) * K);   // K % 16 == 0
@@ -525,16 +530,20 @@ static w4_status run_fp8_block_act(const void* x, bool f16, int64_t T, const int
     e = w4::launch_quant_block(x, f16, false, R, K, rows, T, ws, x_scale, status, s);
   }
   if (e != cudaSuccess) return from_cuda(e, "block quant launch");
-  const w4::Fp8BlockArgs a{ws, x_scale, qweight, w_scale, bias, y, offsets, E, R, N, K, nullptr, false, status};
+  // dense: the part sums of split tiles follow the codes
+  const size_t extra = ws_bytes - base;
+  const w4::Fp8BlockArgs a{ws, x_scale, qweight, w_scale, bias, y, offsets, E, R, N, K, nullptr, false,
+                           reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + base), offsets == nullptr ? extra : 0, status};
   return from_cuda(w4::launch_fp8_block(a, s), "fp8 block product launch");
 }
 
 w4_status w4_fp8_block_gemm(const void* qx, const float* x_scale, const void* qweight, const float* w_scale,
-                            const void* bias, void* y, int64_t M, int64_t N, int64_t K, void* stream) {
+                            const void* bias, void* y, int64_t M, int64_t N, int64_t K, void* workspace,
+                            size_t workspace_bytes, void* stream) {
   w4_status st = check_fp8_block(M, N, K, 1, false);
   if (st != W4_OK) return st;
   if (M == 0) return ok();
-  return run_fp8_block(qx, x_scale, nullptr, 1, qweight, w_scale, bias, y, M, N, K, stream);
+  return run_fp8_block(qx, x_scale, nullptr, 1, qweight, w_scale, bias, y, M, N, K, workspace, workspace_bytes, stream);
 }
 
 w4_status w4_fp8_block_gemm_bf16in(const void* x, int32_t x_dtype, const void* qweight, const float* w_scale,
@@ -555,7 +564,7 @@ w4_status w4_fp8_block_moe_grouped_gemm(const void* qx, const float* x_scale, co
   if (st != W4_OK) return st;
   if (R == 0) return ok();
   if (!expert_offsets) return fail(W4_ERR_NULL, "expert_offsets must be non-NULL");
-  return run_fp8_block(qx, x_scale, expert_offsets, E, qweight, w_scale, nullptr, y, R, N, K, stream);
+  return run_fp8_block(qx, x_scale, expert_offsets, E, qweight, w_scale, nullptr, y, R, N, K, nullptr, 0, stream);
 }
 
 w4_status w4_fp8_block_moe_gemm_bf16in(const void* x, int64_t T, const int32_t* row_token, const int32_t* expert_offsets,

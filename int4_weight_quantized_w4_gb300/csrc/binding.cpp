@@ -259,18 +259,19 @@ PyObject* silu_mul_quant_block(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// qx, x_scale, qweight, w_scale, bias, y, stream
+// qx, x_scale, qweight, w_scale, bias, y, workspace, stream
 PyObject* gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  if (!count(n, 7)) return nullptr;
+  if (!count(n, 8)) return nullptr;
   const at::Tensor& x = ranked(a[0], "qx", kFp8, nullptr, 2);
   const at::Device dev = x.device();
   const int64_t M = x.size(0), K = x.size(1), N = dense_weights(a[2], a[3], a[4], K, dev);
   const at::Tensor& xs = tensor(a[1], "x_scale", kF32, dev, {M, blocks(K)});
   const c10::cuda::CUDAGuard guard(dev);
   const at::Tensor y = output(a[5], "y", {M, N}, ScalarType::BFloat16, kBf16, dev);
+  const Scratch s = scratch(a[6], W4_OP_FP8_BLOCK, M, N, K, 0, dev);
   if (failed(w4_fp8_block_gemm(x.data_ptr(), f32(xs), data(a[2]), static_cast<const float*>(data(a[3])), data(a[4]),
-                               y.data_ptr(), M, N, K, stream_of(a[6], dev)),
+                               y.data_ptr(), M, N, K, s.p, s.bytes, stream_of(a[7], dev)),
              "w4_fp8_block_gemm"))
     return nullptr;
   return THPVariable_Wrap(y);
@@ -286,7 +287,7 @@ PyObject* gemm_act(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t M = x.size(0), K = x.size(1), N = dense_weights(a[1], a[2], a[3], K, dev);
   const c10::cuda::CUDAGuard guard(dev);
   const at::Tensor y = output(a[4], "y", {M, N}, ScalarType::BFloat16, kBf16, dev);
-  const Scratch s = scratch(a[5], W4_OP_FP8_BLOCK, M, N, K, 0, dev);
+  const Scratch s = scratch(a[5], W4_OP_FP8_BLOCK_IN, M, N, K, 0, dev);
   if (failed(w4_fp8_block_gemm_bf16in(x.data_ptr(), act_dtype(x), data(a[1]), static_cast<const float*>(data(a[2])),
                                       data(a[3]), y.data_ptr(), M, N, K, s.p, s.bytes, stream_of(a[6], dev)),
              "w4_fp8_block_gemm_bf16in"))
@@ -326,7 +327,7 @@ PyObject* moe_gemm_act(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int32_t E = static_cast<int32_t>(THPVariable_Unpack(a[3]).size(0));
   const c10::cuda::CUDAGuard guard(dev);
   const at::Tensor y = output(a[5], "y", {R, N}, ScalarType::BFloat16, kBf16, dev);
-  const Scratch s = scratch(a[6], W4_OP_FP8_BLOCK, R, N, K, E, dev);
+  const Scratch s = scratch(a[6], W4_OP_FP8_BLOCK_IN, R, N, K, E, dev);
   if (failed(w4_fp8_block_moe_gemm_bf16in(x.data_ptr(), T, static_cast<const int32_t*>(data(a[1])),
                                           static_cast<const int32_t*>(data(a[2])), E, data(a[3]),
                                           static_cast<const float*>(data(a[4])), y.data_ptr(), R, N, K, s.p, s.bytes,

@@ -49,7 +49,12 @@ struct Params {
   const int32_t* offsets;  // [E + 1], or null (dense: one segment of all rows)
   int E, rows, N, K, KB, NB, n_tiles;
   int split;               // stream form, dense: parts of the k blocks, one per CTA of a cluster
-  long long items;         // upper bound of (row tile, n tile) pairs
+  long long items;         // upper bound of (row tile, n tile) pairs, or of the tile form's work items
+  // tile form, dense: items 0 .. full - 1 are whole tiles; item full + j is part
+  // j % parts of the k blocks of tile full + j / parts, summed into part_sums
+  long long full;
+  int parts;
+  float* part_sums;        // fp32 [tile - full][part][TM][TN]
   unsigned int* status;
 };
 
@@ -486,7 +491,8 @@ constexpr int T_ACCS = 2;                      // accumulators of 256 columns: a
 constexpr int T_SC_SLOTS = 3;                  // scale slots of 4 blocks x 2 output halves x 128 rows
 constexpr int T_SC_FLOATS = 4 * 2 * TM;
 constexpr int T_SC = T_SC_SLOTS * T_SC_FLOATS * 4;
-constexpr int T_SMEM = T_STAGES * (T_A + T_B) + T_SC + 512 + (kMaxExperts + 1 + 12 + 3) / 4 * 16 + 1024;
+constexpr int T_OUT = 8 * 32 * 64;             // per epilogue warp, 64 bytes of its 32 rows on their way out
+constexpr int T_SMEM = T_STAGES * (T_A + T_B) + T_SC + T_OUT + 512 + (kMaxExperts + 1 + 12 + 3) / 4 * 16 + 1024;
 static_assert(T_SMEM <= 232448, "shared memory per CTA");
 // Each issuer meets every phase of the stages and the accumulator that it waits on.
 static_assert(T_STAGES % 2 == 0 && T_ACCS == 2, "blocks of one parity keep their stages and accumulator");
@@ -497,13 +503,51 @@ static_assert(T_STAGES % 2 == 0 && T_ACCS == 2, "blocks of one parity keep their
 constexpr int kTEpi = 8, kTWarpLoad = 8, kTWarpScale = 9, kTWarpMma = 10;
 constexpr int kTThreads = 384;
 
+// 64 bytes of every lane's row (four 16-byte chunks) through `buf` (2 KB of this
+// warp): put(r, c, v) gets chunk c of row r, four lanes to a row and 8 rows an
+// instruction, where the lanes' own stores would touch 32 rows at 16 bytes each.
+template <class Put>
+W4_DEV void rows_out(uint4* buf, const uint4 (&v)[4], Put put) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) buf[lane * 4 + (c ^ ((lane >> 1) & 3))] = v[c];   // no two of 8 lanes in one bank
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + (lane >> 2), c = lane & 3;
+    put(r, c, buf[r * 4 + (c ^ ((r >> 1) & 3))]);
+  }
+  __syncwarp();
+}
+
+struct Work {
+  Tile t;
+  int kb0, kb1;
+  long long part;   // index of its part sums, or -1
+};
+W4_DEV bool decode_work(const Params& p, long long it, const int32_t* starts, Work& w, int& e) {
+  w.kb0 = 0;
+  w.kb1 = p.KB;
+  w.part = -1;
+  if (it >= p.full) {
+    const long long j = it - p.full, tile = j / p.parts;
+    const int part = static_cast<int>(j - tile * p.parts);
+    w.kb0 = static_cast<int>(static_cast<long long>(p.KB) * part / p.parts);
+    w.kb1 = static_cast<int>(static_cast<long long>(p.KB) * (part + 1) / p.parts);
+    w.part = j;
+    it = p.full + tile;
+  }
+  return decode(p, it, TM, TN, starts, w.t, e);
+}
+
 __global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
   uint8_t* a_base = smem;
   uint8_t* b_base = a_base + T_STAGES * T_A;
   float* sc_base = reinterpret_cast<float*>(b_base + T_STAGES * T_B);
-  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(sc_base) + T_SC);
+  uint4* out_base = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(sc_base) + T_SC);
+  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(out_base) + T_OUT);
   uint64_t* done = full + T_STAGES;        // a block's MMAs: its stage is free and its accumulator complete
   uint64_t* acc_empty = done + T_STAGES;
   uint64_t* sc_full = acc_empty + T_ACCS;
@@ -548,17 +592,17 @@ __global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const __grid_constan
     if (warp == kTWarpLoad) {
       int st = 0, ph = 1, e = 0;
       bool ok = true, waited = false;
-      Tile t;
-      for (long long it = blockIdx.x; ok && it < p.items && decode(p, it, TM, TN, starts, t, e); it += gridDim.x)
-        for (int kb = 0; kb < KB; ++kb) {
+      Work w;
+      for (long long it = blockIdx.x; ok && it < p.items && decode_work(p, it, starts, w, e); it += gridDim.x)
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
           if (!(ok = wait_warp(&done[st], ph, abort_flag, p.status))) break;
           if (elect_one()) {
             mbar_arrive_expect_tx(&full[st], T_A + T_B);
-            tc::tma_load_3d(b_base + st * T_B, &p.tm_w, &full[st], kb * kBlk, t.n0, t.expert);
+            tc::tma_load_3d(b_base + st * T_B, &p.tm_w, &full[st], kb * kBlk, w.t.n0, w.t.expert);
           }
           if (!waited) grid_dependency_wait();   // the codes come from the kernel before
           waited = true;
-          if (elect_one()) tc::tma_load_2d(a_base + st * T_A, &p.tm_x, &full[st], kb * kBlk, t.row0);
+          if (elect_one()) tc::tma_load_2d(a_base + st * T_A, &p.tm_x, &full[st], kb * kBlk, w.t.row0);
           if (++st == T_STAGES) st = 0, ph ^= 1;
         }
     } else if (warp == kTWarpScale) {
@@ -566,24 +610,25 @@ __global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const __grid_constan
       grid_dependency_wait();
       int sl = 0, ph = 1, e = 0;
       bool ok = true;
-      Tile t;
-      for (long long it = blockIdx.x; ok && it < p.items && decode(p, it, TM, TN, starts, t, e); it += gridDim.x) {
+      Work w;
+      for (long long it = blockIdx.x; ok && it < p.items && decode_work(p, it, starts, w, e); it += gridDim.x) {
+          const Tile& t = w.t;
         const int nb = t.n0 / kBlk;
         const float* sw0 = p.w_scale + (static_cast<size_t>(t.expert) * p.NB + nb) * KB;
         const float* sw1 = nb + 1 < p.NB ? sw0 + KB : sw0;
-        for (int kb = 0; kb < KB; kb += 4) {
+        for (int kb = w.kb0; kb < w.kb1; kb += 4) {
           float w0[4], w1[4], x[4][4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            w0[i] = kb + i < KB ? __ldg(sw0 + kb + i) : 0.f;
-            w1[i] = kb + i < KB ? __ldg(sw1 + kb + i) : 0.f;
+            w0[i] = kb + i < w.kb1 ? __ldg(sw0 + kb + i) : 0.f;
+            w1[i] = kb + i < w.kb1 ? __ldg(sw1 + kb + i) : 0.f;
           }
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int row = t.row0 + 32 * j + lane;
             const float* sx = p.x_scale + static_cast<size_t>(row) * KB + kb;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[j][i] = (row < t.row_end && kb + i < KB) ? sx[i] : 0.f;
+            for (int i = 0; i < 4; ++i) x[j][i] = (row < t.row_end && kb + i < w.kb1) ? sx[i] : 0.f;
           }
           if (!(ok = wait_warp(&sc_empty[sl], ph, abort_flag, p.status))) break;
           float* sc = sc_base + sl * T_SC_FLOATS + lane;
@@ -606,9 +651,9 @@ __global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const __grid_constan
       int st = 0, ph = 0, aph = 1, e = 0;
       uint32_t g = 0;
       bool ok = true;
-      Tile t;
-      for (long long it = blockIdx.x; ok && it < p.items && decode(p, it, TM, TN, starts, t, e); it += gridDim.x)
-        for (int kb = 0; kb < KB; ++kb, ++g) {
+      Work w;
+      for (long long it = blockIdx.x; ok && it < p.items && decode_work(p, it, starts, w, e); it += gridDim.x)
+        for (int kb = w.kb0; kb < w.kb1; ++kb, ++g) {
           if (static_cast<int>(g & 1) == mine) {
             if (!(ok = wait_warp(&acc_empty[mine], aph, abort_flag, p.status))) break;
             if (!(ok = wait_warp(&full[st], ph, abort_flag, p.status))) break;
@@ -632,13 +677,13 @@ __global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const __grid_constan
     const float* sc_mine = sc_base + half * TM + 32 * q + lane;
     int st = 0, ph = 0, buf = 0, sl = 0, sph = 0, e = 0;
     bool ok = true;
-    Tile t;
-    for (long long it = blockIdx.x; ok && it < p.items && decode(p, it, TM, TN, starts, t, e); it += gridDim.x) {
+    Work w;
+    for (long long it = blockIdx.x; ok && it < p.items && decode_work(p, it, starts, w, e); it += gridDim.x) {
       float T[128];
 #pragma unroll
       for (int j = 0; j < 128; ++j) T[j] = 0.f;
-      for (int kb = 0; kb < KB; ++kb) {
-        const int i = kb & 3;
+      for (int kb = w.kb0; kb < w.kb1; ++kb) {
+        const int i = (kb - w.kb0) & 3;
         if (i == 0 && !(ok = wait_warp(&sc_full[sl], sph, abort_flag, p.status))) break;
         const float f = sc_mine[sl * T_SC_FLOATS + i * 2 * TM];
         if (!(ok = wait_warp(&done[st], ph, abort_flag, p.status))) break;
@@ -657,7 +702,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const __grid_constan
             __syncwarp();
             if (lane == 0) {   // the accumulator is in registers
               mbar_arrive(&acc_empty[buf]);
-              if (i == 3 || kb == KB - 1) mbar_arrive(&sc_empty[sl]);
+              if (i == 3 || kb == w.kb1 - 1) mbar_arrive(&sc_empty[sl]);
             }
           }
 #pragma unroll
@@ -666,28 +711,49 @@ __global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const __grid_constan
         }
         buf ^= 1;
         if (++st == T_STAGES) st = 0, ph ^= 1;
-        if (i == 3 || kb == KB - 1) {
+        if (i == 3 || kb == w.kb1 - 1) {
           if (++sl == T_SC_SLOTS) sl = 0, sph ^= 1;
         }
       }
       if (!ok) break;
-      const int row = t.row0 + 32 * q + lane;
-      const int n0 = t.n0 + 128 * half;
-      if (row < t.row_end) {
-        uint16_t* yp = p.y + static_cast<size_t>(row) * p.N + n0;
+      const int row0 = w.t.row0 + 32 * q, n0 = w.t.n0 + 128 * half, row_end = w.t.row_end;
+      uint4* buf = out_base + warp * 128;
+      if (w.part >= 0) {
+        float* ps = p.part_sums + (w.part * TM + 32 * q) * TN + 128 * half;
 #pragma unroll
-        for (int c = 0; c < 128; c += 8)
-          if (n0 + c < p.N) {   // N is a multiple of 8
+        for (int c0 = 0; c0 < 128; c0 += 16) {
+          uint4 v[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            v[c] = make_uint4(__float_as_uint(T[c0 + 4 * c]), __float_as_uint(T[c0 + 4 * c + 1]),
+                              __float_as_uint(T[c0 + 4 * c + 2]), __float_as_uint(T[c0 + 4 * c + 3]));
+          rows_out(buf, v, [&](int r, int c, const uint4& x) {
+            if (row0 + r < row_end) *reinterpret_cast<uint4*>(ps + static_cast<size_t>(r) * TN + c0 + 4 * c) = x;
+          });
+        }
+      } else {
+        uint16_t* yp = p.y + static_cast<size_t>(row0) * p.N + n0;
+#pragma unroll
+        for (int c0 = 0; c0 < 128; c0 += 32) {
+          if (n0 + c0 >= p.N) break;
+          uint4 v[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float* x = T + c0 + 8 * c;
             float b[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (p.bias != nullptr) {
-              const uint4 bb = *reinterpret_cast<const uint4*>(p.bias + n0 + c);
+            if (p.bias != nullptr && n0 + c0 + 8 * c < p.N) {
+              const uint4 bb = *reinterpret_cast<const uint4*>(p.bias + n0 + c0 + 8 * c);
               b[0] = bf16_lo(bb.x), b[1] = bf16_hi(bb.x), b[2] = bf16_lo(bb.y), b[3] = bf16_hi(bb.y);
               b[4] = bf16_lo(bb.z), b[5] = bf16_hi(bb.z), b[6] = bf16_lo(bb.w), b[7] = bf16_hi(bb.w);
             }
-            *reinterpret_cast<uint4*>(yp + c) =
-                make_uint4(pack_bf16x2(T[c] + b[0], T[c + 1] + b[1]), pack_bf16x2(T[c + 2] + b[2], T[c + 3] + b[3]),
-                           pack_bf16x2(T[c + 4] + b[4], T[c + 5] + b[5]), pack_bf16x2(T[c + 6] + b[6], T[c + 7] + b[7]));
+            v[c] = make_uint4(pack_bf16x2(x[0] + b[0], x[1] + b[1]), pack_bf16x2(x[2] + b[2], x[3] + b[3]),
+                              pack_bf16x2(x[4] + b[4], x[5] + b[5]), pack_bf16x2(x[6] + b[6], x[7] + b[7]));
           }
+          rows_out(buf, v, [&](int r, int c, const uint4& x) {
+            if (row0 + r < row_end && n0 + c0 + 8 * c < p.N)   // N is a multiple of 8
+              *reinterpret_cast<uint4*>(yp + static_cast<size_t>(r) * p.N + c0 + 8 * c) = x;
+          });
+        }
       }
     }
   }
@@ -703,6 +769,33 @@ __global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const __grid_constan
   if (warp == kTWarpMma) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, T_ACCS * TN);
+  }
+}
+
+// y = bf16(part sums in order + bias) of the tiles that were split.
+__global__ void __launch_bounds__(256) join_parts_kernel(const float4* __restrict__ sums, int parts, int tiles,
+                                                         long long full, int n_tiles, int rows, int N,
+                                                         const uint16_t* __restrict__ bias, uint16_t* __restrict__ y) {
+  constexpr int kRow = TN / 4;
+  launch_dependents();
+  grid_dependency_wait();
+  const int total = tiles * TM * kRow;
+  for (int i = blockIdx.x * 256 + threadIdx.x; i < total; i += gridDim.x * 256) {
+    const int tile = i / (TM * kRow), r = i / kRow % TM, c4 = i % kRow;
+    const long long id = full + tile;
+    const int row = static_cast<int>(id / n_tiles) * TM + r, n = static_cast<int>(id % n_tiles) * TN + 4 * c4;
+    if (row >= rows || n >= N) continue;   // N is a multiple of 8
+    const float4* s = sums + (static_cast<size_t>(tile) * parts * TM + r) * kRow + c4;
+    float4 a = __ldcg(s);
+    for (int j = 1; j < parts; ++j) {
+      const float4 b = __ldcg(s + static_cast<size_t>(j) * TM * kRow);
+      a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+    }
+    if (bias != nullptr) {
+      const uint2 b = *reinterpret_cast<const uint2*>(bias + n);
+      a.x += bf16_lo(b.x), a.y += bf16_hi(b.x), a.z += bf16_lo(b.y), a.w += bf16_hi(b.y);
+    }
+    *reinterpret_cast<uint2*>(y + static_cast<size_t>(row) * N + n) = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
   }
 }
 
@@ -792,7 +885,36 @@ cudaError_t run_stream(const Fp8BlockArgs& a, Params& p, cudaStream_t s) {
 
 }  // namespace
 
+// The dense tile form's work: whole waves of whole tiles, and the r tiles of a
+// last, partly filled wave cut along k into as many parts as fit the SMs at once.
+// That takes KB - KB / s blocks of 0.54 us off the last wave and costs about
+// kSplitBlocks of them: the sums of 128 KB a part, written and read back, and the
+// join's launch. Measured whole / split: 517 x 11008 x 4096 (r = 63, two parts) 41.1
+// / 37.8 us, 300 x 2048 x 14336 (24, six) 56.4 / 23.0, 700 x 14336 x 8192 (32, four)
+// 108 / 89. More parts than SMs lose: 256 x 11008 x 4096 (86, three) 22.1 / 31.8.
+// The SM count is a GB300's whatever the device, so that the workspace is the same
+// everywhere.
+constexpr int kPlanSms = 152, kSplitBlocks = 12;
+struct Plan {
+  int64_t full, tail;
+  int parts;
+};
+static Plan tile_plan(int64_t R, int64_t N, int64_t K) {
+  const int64_t tiles = ((R + TM - 1) / TM) * ((N + TN - 1) / TN), r = tiles % kPlanSms, KB = (K + kBlk - 1) / kBlk;
+  if (r == 0) return {tiles, 0, 1};
+  int64_t s = kPlanSms / r;
+  if (s > 16) s = 16;
+  if (s < 2 || (KB + s - 1) / s + kSplitBlocks >= KB) return {tiles, 0, 1};
+  return {tiles - r, r, static_cast<int>(s)};
+}
+
 bool fp8_block_fuses(int64_t R, bool experts) { return !experts && R <= kFuseRows; }
+
+size_t fp8_block_part_bytes(int64_t R, int64_t N, int64_t K) {
+  if (R <= 128) return 0;   // stream form
+  const Plan p = tile_plan(R, N, K);
+  return p.parts > 1 ? static_cast<size_t>(p.tail) * p.parts * TM * TN * sizeof(float) : 0;
+}
 
 cudaError_t launch_fp8_block(const Fp8BlockArgs& a, cudaStream_t s) {
   Params p;
@@ -823,9 +945,22 @@ cudaError_t launch_fp8_block(const Fp8BlockArgs& a, cudaStream_t s) {
   e = encode(&p.tm_w, a.qweight, a.K, a.N, a.E, TN);
   if (e != cudaSuccess) return e;
   p.n_tiles = static_cast<int>((a.N + TN - 1) / TN);
-  p.items = row_tiles(a, TM) * p.n_tiles;
+  p.items = p.full = row_tiles(a, TM) * p.n_tiles;
+  p.parts = 1;
+  const Plan plan = a.expert_offsets == nullptr ? tile_plan(a.R, a.N, a.K) : Plan{0, 0, 1};
+  if (plan.parts > 1 && a.part_bytes >= fp8_block_part_bytes(a.R, a.N, a.K)) {
+    p.full = plan.full;
+    p.parts = plan.parts;
+    p.part_sums = a.part_sums;
+    p.items = plan.full + plan.tail * plan.parts;
+  }
   const int64_t sms = current_sm_count();
-  return start<tile_kernel>(p, p.items < sms ? p.items : sms, kTThreads, T_SMEM, 1, s);
+  e = start<tile_kernel>(p, p.items < sms ? p.items : sms, kTThreads, T_SMEM, 1, s);
+  if (e != cudaSuccess || p.parts == 1) return e;
+  const int64_t want = plan.tail * TM * (TN / 4) / 256, most = sms * 8;
+  PdlLaunch pl(static_cast<unsigned>(want < most ? want : most), 256, 0, s);
+  return cudaLaunchKernelEx(&pl.cfg, join_parts_kernel, reinterpret_cast<const float4*>(p.part_sums), p.parts,
+                            static_cast<int>(plan.tail), p.full, p.n_tiles, p.rows, p.N, p.bias, p.y);
 }
 
 }  // namespace w4

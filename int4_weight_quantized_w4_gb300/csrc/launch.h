@@ -159,8 +159,12 @@ struct Fp8BlockArgs {
   int64_t R, N, K;
   const void* x;                  // where fp8_block_fuses: 16-bit activations [R, K] in place of qx and x_scale
   bool x_f16;
+  float* part_sums;               // dense: at least fp8_block_part_bytes, 16-byte aligned (or null, 0: the product is not split along K)
+  size_t part_bytes;
   unsigned int* status;
 };
+// fp32 part sums of the dense product's split tiles.
+size_t fp8_block_part_bytes(int64_t R, int64_t N, int64_t K);
 // Quantized rows of the 16-bit-input forms: codes [R, K], then scales [R, ceil(K / 128)], padded to 16 bytes.
 inline size_t fp8_block_workspace_bytes(int64_t R, int64_t K) {
   const size_t n = static_cast<size_t>(R) * static_cast<size_t>(K) + static_cast<size_t>(R) * static_cast<size_t>((K + 127) / 128) * 4;

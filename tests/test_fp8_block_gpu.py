@@ -170,7 +170,7 @@ def test_gemm_on_another_stream():
     torch.cuda.synchronize()
     st = torch.cuda.Stream()
     y = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
-    ws = torch.empty((w4.w4_workspace_bytes(w4.W4_OP_FP8_BLOCK, M, N, K, 0),), dtype=torch.uint8, device="cuda")
+    ws = torch.empty((w4.w4_workspace_bytes(w4.W4_OP_FP8_BLOCK_IN, M, N, K, 0),), dtype=torch.uint8, device="cuda")
     torch.cuda.synchronize()
     w4.w4_fp8_block_gemm_bf16in(t, qd, sd, y=y, workspace=ws, stream=st)
     st.synchronize()
@@ -185,7 +185,7 @@ def test_gemm_in_a_cuda_graph():
     t, qd, sd = bf16(x), fp8(qw), to_dev(sw)
     ref = w4.w4_fp8_block_gemm_bf16in(t, qd, sd)
     y = torch.zeros_like(ref)
-    ws = torch.empty((w4.w4_workspace_bytes(w4.W4_OP_FP8_BLOCK, M, N, K, 0),), dtype=torch.uint8, device="cuda")
+    ws = torch.empty((w4.w4_workspace_bytes(w4.W4_OP_FP8_BLOCK_IN, M, N, K, 0),), dtype=torch.uint8, device="cuda")
     torch.cuda.synchronize()
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
