@@ -49,10 +49,10 @@ struct Params {
   const int32_t* offsets;  // [E + 1], or null (dense: one segment of all rows)
   int E, rows, N, K, KB, NB, n_tiles;
   int split;               // stream form, dense: parts of the k blocks, one per CTA of a cluster
-  long long items;         // upper bound of (row tile, n tile) pairs, or of the tile form's work items
+  int items;               // upper bound of (row tile, n tile) pairs, or of the tile form's work items
   // tile form, dense: items 0 .. full - 1 are whole tiles; item full + j is part
   // j % parts of the k blocks of tile full + j / parts, summed into part_sums
-  long long full;
+  int full;
   int parts;
   float* part_sums;        // fp32 [tile - full][part][TM][TN]
   unsigned int* status;
@@ -127,15 +127,18 @@ W4_DEV void tile_starts(const Params& p, int rows_per, int32_t* starts, int32_t*
   if (threadIdx.x == 0) starts[p.E] = carry;
 }
 
+// Where part `i` of `n` of KB blocks starts (KB, n below 2^15 and 2^5, or n = 1).
+W4_DEV int part_start(int KB, int i, int n) { return n == 1 ? i * KB : KB * i / n; }
+
 struct Tile {
   int n0, row0, row_end, expert;
 };
 // Item `it` (n tiles fastest) as a tile of `rows_per` rows and `cols_per`
 // outputs; false when there are no more. `e` is the caller's cursor over the
 // experts: items come in increasing order.
-W4_DEV bool decode(const Params& p, long long it, int rows_per, int cols_per, const int32_t* starts, Tile& t, int& e) {
-  const int yt = static_cast<int>(it / p.n_tiles);
-  t.n0 = static_cast<int>(it - static_cast<long long>(yt) * p.n_tiles) * cols_per;
+W4_DEV bool decode(const Params& p, int it, int rows_per, int cols_per, const int32_t* starts, Tile& t, int& e) {
+  const int yt = static_cast<int>(static_cast<unsigned>(it) / static_cast<unsigned>(p.n_tiles));
+  t.n0 = (it - yt * p.n_tiles) * cols_per;
   if (p.offsets == nullptr) {
     t.expert = 0;
     t.row0 = yt * rows_per;
@@ -238,16 +241,15 @@ __global__ void __launch_bounds__(Stream<NT, kQuant>::THREADS, Stream<NT, kQuant
 
   // this CTA's part of the k blocks (the same for every item)
   const int part = p.split > 1 ? static_cast<int>(cluster_rank()) : 0;
-  const int kb0 = static_cast<int>(static_cast<long long>(p.KB) * part / p.split);
-  const int kb1 = static_cast<int>(static_cast<long long>(p.KB) * (part + 1) / p.split);
-  const long long first = blockIdx.x / p.split, step = gridDim.x / p.split;
+  const int kb0 = part_start(p.KB, part, p.split), kb1 = part_start(p.KB, part + 1, p.split);
+  const int first = blockIdx.x / p.split, step = gridDim.x / p.split;
 
   if (warp == kSWarpA) {
     if (lane == 0) {
       int st = 0, ph = 1, e = 0;
       bool ok = true;
       Tile t;
-      for (long long it = first; ok && it < p.items && decode(p, it, NT, kBlk, starts, t, e); it += step)
+      for (int it = first; ok && it < p.items && decode(p, it, NT, kBlk, starts, t, e); it += step)
         for (int kb = kb0; kb < kb1; ++kb) {
           if (!(ok = tc::wait(&empty[st], ph, abort_flag, p.status, kWaitNs))) break;
           mbar_arrive_expect_tx(&full[st], C::A_BYTES);
@@ -262,8 +264,7 @@ __global__ void __launch_bounds__(Stream<NT, kQuant>::THREADS, Stream<NT, kQuant
       constexpr int RPH = kFuseRows / 2;               // rows per half-warp
       const int h = lane >> 4, l = lane & 15;
       const int K8 = p.K >> 3, nkb = kb1 - kb0;
-      const long long items = first < p.items ? (p.items - first + step - 1) / step : 0;
-      const int total = static_cast<int>(items) * nkb;
+      const int total = first < p.items ? (p.items - first + step - 1) / step * nkb : 0;
       auto load = [&](int g, uint4 (&v)[RPH]) {
         const int c = (kb0 + g % nkb) * 16 + l;
 #pragma unroll
@@ -277,7 +278,7 @@ __global__ void __launch_bounds__(Stream<NT, kQuant>::THREADS, Stream<NT, kQuant
       load(warp - kSWarpB, cur);
       for (int g = warp - kSWarpB; g < total; g += kQuantWarps) {
         const int kb = kb0 + g % nkb;
-        const int nt = static_cast<int>((first + g / nkb * step) % p.n_tiles);
+        const int nt = (first + g / nkb * step) % p.n_tiles;
         const float sw = __ldg(p.w_scale + static_cast<size_t>(nt) * p.KB + kb);
         load(g + kQuantWarps, next);
         const int st = g % C::STAGES, sl = g % C::SC_SLOTS;
@@ -313,7 +314,7 @@ __global__ void __launch_bounds__(Stream<NT, kQuant>::THREADS, Stream<NT, kQuant
       int st = 0, ph = 1, e = 0;
       bool ok = true;
       Tile t;
-      for (long long it = first; ok && it < p.items && decode(p, it, NT, kBlk, starts, t, e); it += step)
+      for (int it = first; ok && it < p.items && decode(p, it, NT, kBlk, starts, t, e); it += step)
         for (int kb = kb0; kb < kb1; ++kb) {
           if (!(ok = tc::wait(&empty[st], ph, abort_flag, p.status, kWaitNs))) break;
           mbar_arrive_expect_tx(&full[st], C::B_BYTES);
@@ -328,7 +329,7 @@ __global__ void __launch_bounds__(Stream<NT, kQuant>::THREADS, Stream<NT, kQuant
       int st = 0, ph = 0, ac = 0, aph = 1, e = 0;
       bool ok = true;
       Tile t;
-      for (long long it = first; ok && it < p.items && decode(p, it, NT, kBlk, starts, t, e); it += step)
+      for (int it = first; ok && it < p.items && decode(p, it, NT, kBlk, starts, t, e); it += step)
         for (int kb = kb0; kb < kb1; ++kb) {
           if (!(ok = tc::wait(&acc_empty[ac], aph, abort_flag, p.status, kWaitNs))) break;
           if (!(ok = tc::wait(&full[st], ph, abort_flag, p.status, kWaitNs, 200))) break;
@@ -348,7 +349,7 @@ __global__ void __launch_bounds__(Stream<NT, kQuant>::THREADS, Stream<NT, kQuant
     int sl = 0, ph = 1, e = 0;
     bool ok = true;
     Tile t;
-    for (long long it = first; ok && it < p.items && decode(p, it, NT, kBlk, starts, t, e); it += step) {
+    for (int it = first; ok && it < p.items && decode(p, it, NT, kBlk, starts, t, e); it += step) {
       const float* sw = p.w_scale + (static_cast<size_t>(t.expert) * p.NB + t.n0 / kBlk) * p.KB;
       for (int kb = kb0; kb < kb1; kb += 4) {
         float w[4];
@@ -377,7 +378,7 @@ __global__ void __launch_bounds__(Stream<NT, kQuant>::THREADS, Stream<NT, kQuant
     int ac = 0, aph = 0, sl = 0, sph = 0, e = 0;
     bool ok = true;
     Tile t;
-    for (long long it = first; ok && it < p.items && decode(p, it, NT, kBlk, starts, t, e); it += step) {
+    for (int it = first; ok && it < p.items && decode(p, it, NT, kBlk, starts, t, e); it += step) {
       float T[NT];
 #pragma unroll
       for (int j = 0; j < NT; ++j) T[j] = 0.f;
@@ -523,17 +524,16 @@ W4_DEV void rows_out(uint4* buf, const uint4 (&v)[4], Put put) {
 struct Work {
   Tile t;
   int kb0, kb1;
-  long long part;   // index of its part sums, or -1
+  int part;   // index of its part sums, or -1
 };
-W4_DEV bool decode_work(const Params& p, long long it, const int32_t* starts, Work& w, int& e) {
+W4_DEV bool decode_work(const Params& p, int it, const int32_t* starts, Work& w, int& e) {
   w.kb0 = 0;
   w.kb1 = p.KB;
   w.part = -1;
   if (it >= p.full) {
-    const long long j = it - p.full, tile = j / p.parts;
-    const int part = static_cast<int>(j - tile * p.parts);
-    w.kb0 = static_cast<int>(static_cast<long long>(p.KB) * part / p.parts);
-    w.kb1 = static_cast<int>(static_cast<long long>(p.KB) * (part + 1) / p.parts);
+    const int j = it - p.full, tile = j / p.parts, part = j - tile * p.parts;
+    w.kb0 = part_start(p.KB, part, p.parts);
+    w.kb1 = part_start(p.KB, part + 1, p.parts);
     w.part = j;
     it = p.full + tile;
   }
@@ -719,7 +719,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const __grid_constan
       const int row0 = w.t.row0 + 32 * q, n0 = w.t.n0 + 128 * half, row_end = w.t.row_end;
       uint4* buf = out_base + warp * 128;
       if (w.part >= 0) {
-        float* ps = p.part_sums + (w.part * TM + 32 * q) * TN + 128 * half;
+        float* ps = p.part_sums + (static_cast<size_t>(w.part) * TM + 32 * q) * TN + 128 * half;
 #pragma unroll
         for (int c0 = 0; c0 < 128; c0 += 16) {
           uint4 v[4];
@@ -774,7 +774,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const __grid_constan
 
 // y = bf16(part sums in order + bias) of the tiles that were split.
 __global__ void __launch_bounds__(256) join_parts_kernel(const float4* __restrict__ sums, int parts, int tiles,
-                                                         long long full, int n_tiles, int rows, int N,
+                                                         int full, int n_tiles, int rows, int N,
                                                          const uint16_t* __restrict__ bias, uint16_t* __restrict__ y) {
   constexpr int kRow = TN / 4;
   launch_dependents();
@@ -782,8 +782,7 @@ __global__ void __launch_bounds__(256) join_parts_kernel(const float4* __restric
   const int total = tiles * TM * kRow;
   for (int i = blockIdx.x * 256 + threadIdx.x; i < total; i += gridDim.x * 256) {
     const int tile = i / (TM * kRow), r = i / kRow % TM, c4 = i % kRow;
-    const long long id = full + tile;
-    const int row = static_cast<int>(id / n_tiles) * TM + r, n = static_cast<int>(id % n_tiles) * TN + 4 * c4;
+    const int id = full + tile, row = id / n_tiles * TM + r, n = id % n_tiles * TN + 4 * c4;
     if (row >= rows || n >= N) continue;   // N is a multiple of 8
     const float4* s = sums + (static_cast<size_t>(tile) * parts * TM + r) * kRow + c4;
     float4 a = __ldcg(s);
@@ -802,6 +801,8 @@ __global__ void __launch_bounds__(256) join_parts_kernel(const float4* __restric
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
+
+constexpr int64_t kMaxItems = int64_t{1} << 30;   // more tiles than any y that fits the device has
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -874,12 +875,14 @@ cudaError_t run_stream(const Fp8BlockArgs& a, Params& p, cudaStream_t s) {
   e = encode(&p.tm_w, a.qweight, a.K, a.N, a.E, kBlk);
   if (e != cudaSuccess) return e;
   p.n_tiles = static_cast<int>((a.N + kBlk - 1) / kBlk);
-  p.items = row_tiles(a, NT) * p.n_tiles;
+  const int64_t items = row_tiles(a, NT) * p.n_tiles;
+  if (items > kMaxItems) return cudaErrorInvalidConfiguration;
+  p.items = static_cast<int>(items);
   const int64_t slots = static_cast<int64_t>(current_sm_count()) * C::CTAS;
   p.split = 1;
   if (a.expert_offsets == nullptr)
-    while (p.split < kMaxSplit && p.items * p.split * 2 <= slots && p.KB >= 4 * p.split) p.split *= 2;
-  const int64_t grid = p.split > 1 ? p.items * p.split : (p.items < slots ? p.items : slots);
+    while (p.split < kMaxSplit && items * p.split * 2 <= slots && p.KB >= 4 * p.split) p.split *= 2;
+  const int64_t grid = p.split > 1 ? items * p.split : (items < slots ? items : slots);
   return start<stream_kernel<NT, kQuant>>(p, grid, C::THREADS, C::SMEM, p.split, s);
 }
 
@@ -945,14 +948,16 @@ cudaError_t launch_fp8_block(const Fp8BlockArgs& a, cudaStream_t s) {
   e = encode(&p.tm_w, a.qweight, a.K, a.N, a.E, TN);
   if (e != cudaSuccess) return e;
   p.n_tiles = static_cast<int>((a.N + TN - 1) / TN);
-  p.items = p.full = row_tiles(a, TM) * p.n_tiles;
+  const int64_t items = row_tiles(a, TM) * p.n_tiles;
+  if (items > kMaxItems) return cudaErrorInvalidConfiguration;
+  p.items = p.full = static_cast<int>(items);
   p.parts = 1;
   const Plan plan = a.expert_offsets == nullptr ? tile_plan(a.R, a.N, a.K) : Plan{0, 0, 1};
   if (plan.parts > 1 && a.part_bytes >= fp8_block_part_bytes(a.R, a.N, a.K)) {
-    p.full = plan.full;
+    p.full = static_cast<int>(plan.full);
     p.parts = plan.parts;
     p.part_sums = a.part_sums;
-    p.items = plan.full + plan.tail * plan.parts;
+    p.items = static_cast<int>(plan.full + plan.tail * plan.parts);
   }
   const int64_t sms = current_sm_count();
   e = start<tile_kernel>(p, p.items < sms ? p.items : sms, kTThreads, T_SMEM, 1, s);
