@@ -257,11 +257,6 @@ W4_DEV uint2 quant_e4m3_chunk(const uint4& v, const QuotientBracket& b) {
 
 // Per-block quantization: a half-warp holds a block of 128 columns of a row, one
 // chunk of 8 per lane. Scale fl(amax / 448), 1 for a block of zeros.
-W4_DEV float half_warp_max(float m) {
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  return m;
-}
 W4_DEV float block_scale(float amax) { return amax == 0.f ? 1.f : __fdiv_rn(amax, 448.f); }
 
 // (d0, d1) = (a0, a1) * b + (c0, c1), packed as fma2.
@@ -324,13 +319,53 @@ W4_DEV void chunk_f32(const uint4& v, float (&x)[8]) {
   }
 }
 
-// This lane's e4m3 codes and the block's scale; every lane of the warp takes part.
+// The maxima of kUnits blocks over the half-warp, reduced together: lanes trade one
+// half of their values for the other at each of the first steps, which leaves the
+// maximum of block u in the lanes with lane % kUnits == u.
+template <int kUnits>
+W4_DEV float unit_max(const float (&m)[kUnits]) {
+  static_assert(kUnits == 2 || kUnits == 4, "one lane bit per halving");
+  const int lane = threadIdx.x & 31;
+  const bool b0 = lane & 1, b1 = lane & 2;
+  float z = fmaxf(b0 ? m[1] : m[0], __shfl_xor_sync(0xffffffffu, b0 ? m[0] : m[1], 1));
+  if constexpr (kUnits == 4) {
+    const float y = fmaxf(b0 ? m[3] : m[2], __shfl_xor_sync(0xffffffffu, b0 ? m[2] : m[3], 1));
+    z = fmaxf(b1 ? y : z, __shfl_xor_sync(0xffffffffu, b1 ? z : y, 2));
+  } else {
+    z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 2));
+  }
+  z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 4));
+  return fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 8));
+}
+
+// This lane's codes and the scale of one block. Every lane of the warp takes part.
 template <bool kF16>
 W4_DEV void quant_block_half_warp(const uint4& v, uint2& code, float& s) {
-  s = block_scale(half_warp_max(chunk_max<kF16>(v)));
+  float m = chunk_max<kF16>(v);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  s = block_scale(m);
   float x[8];
   chunk_f32<kF16>(v, x);
   code = quant_e4m3_block(x, s, __frcp_rn(s));
+}
+
+// Four blocks of the half-warp at once, chunk v[u] of block u: this lane's codes
+// and (in lane l) the scale of block l % 4. Every lane of the warp takes part.
+template <bool kF16>
+W4_DEV float quant_blocks4(const uint4 (&v)[4], uint2 (&code)[4]) {
+  float m[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) m[u] = chunk_max<kF16>(v[u]);
+  const float s_mine = block_scale(unit_max<4>(m)), r_mine = __frcp_rn(s_mine);
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const float s = __shfl_sync(0xffffffffu, s_mine, u, 16), r = __shfl_sync(0xffffffffu, r_mine, u, 16);
+    float x[8];
+    chunk_f32<kF16>(v[u], x);
+    code[u] = quant_e4m3_block(x, s, r);
+  }
+  return s_mine;
 }
 
 // ---------------------------------------------------------------------------

@@ -45,23 +45,6 @@ W4_DEV void silu_mul2(uint32_t g, uint32_t u, float& a0, float& a1) {
   mul2v(a0, a1, a0, a1, t0, t1);
 }
 
-// The maximum over the half-warp of m[u] for u = lane % kUnits.
-template <int kUnits>
-W4_DEV float unit_max(const float (&m)[kUnits]) {
-  static_assert(kUnits == 2 || kUnits == 4, "one lane bit per halving");
-  const int lane = threadIdx.x & 31;
-  const bool b0 = lane & 1, b1 = lane & 2;
-  float z = fmaxf(b0 ? m[1] : m[0], __shfl_xor_sync(kFull, b0 ? m[0] : m[1], 1));
-  if constexpr (kUnits == 4) {
-    const float y = fmaxf(b0 ? m[3] : m[2], __shfl_xor_sync(kFull, b0 ? m[2] : m[3], 1));
-    z = fmaxf(b1 ? y : z, __shfl_xor_sync(kFull, b1 ? z : y, 2));
-  } else {
-    z = fmaxf(z, __shfl_xor_sync(kFull, z, 2));
-  }
-  z = fmaxf(z, __shfl_xor_sync(kFull, z, 4));
-  return fmaxf(z, __shfl_xor_sync(kFull, z, 8));
-}
-
 // x [*, K8 chunks], or with kSilu [*, 2 K8]; row r of the output comes from row
 // gather[r] (gather may be null: row r). An id outside [0, T) gives a zero row
 // with scales 1 and W4_ERR_SHAPE in the status word. KU = ceil(KB / kUnits).
