@@ -276,3 +276,162 @@ def test_grouped_bf16in_bad_row():
     got = bits(y)
     assert not (got[[1, 3]] & 0x7FFF).any()
     check_bf16_output(got, r, "bad rows")
+
+
+@pytest.mark.parametrize("R,T,bad", [(9000, 1000, False), (9000, 1000, True), (9000, 8000, False)])
+def test_grouped_bf16in_tokens_quantized_once(R, T, bad):
+    """Many rows of few tokens: the codes are copied from the tokens' (the last case
+    has too many tokens for that); with a workspace that only holds the rows they
+    are computed again, to the same bits. Rows of bad ids are zero."""
+    E, N, K = 4, 136, 528
+    x = S.activations_bf16(T, K, seed=5)
+    rt = (S.raw_u64(6, 1, R) % T).astype(np.int32)
+    if bad:
+        rt[[0, 4444, R - 1]] = [T, -1, 2 ** 31 - 1]
+    off = np.array([0, 2000, 2000, 5000, R], np.int32)
+    qw, sw = weights(N, K, seed=7, E=E)
+    args = bf16(x), to_dev(rt), to_dev(off), fp8(qw), to_dev(sw)
+    assert w4.w4_device_status() == w4.W4_OK
+    y = w4.w4_fp8_block_moe_gemm_bf16in(*args)
+    assert w4.w4_device_status() == (w4.W4_ERR_SHAPE if bad else w4.W4_OK)
+    rows_only = (R * K + R * 5 * 4 + 15) // 16 * 16
+    y2 = w4.w4_fp8_block_moe_gemm_bf16in(*args, workspace=torch.empty(rows_only, dtype=torch.uint8, device="cuda"))
+    assert w4.w4_device_status() == (w4.W4_ERR_SHAPE if bad else w4.W4_OK)
+    np.testing.assert_array_equal(bits(y), bits(y2))
+    ok = (rt >= 0) & (rt < T)
+    q, s = O.quant_fp8_per_block(x)
+    r = O.fp8_block_grouped_linear(q[np.where(ok, rt, 0)], s[np.where(ok, rt, 0)], off, qw, sw)
+    r[~ok] = 0
+    check_bf16_output(bits(y), r, "copied codes")
+
+
+@pytest.mark.parametrize("M,N,K,split", [(300, 4096, 2064, False), (700, 776, 4112, True), (2700, 2056, 1808, False),
+                                         (300, 4096, 4112, True), (2700, 2056, 4112, True)])
+def test_gemm_split_and_whole(M, N, K, split):
+    """The last wave's tiles cut along K where that pays, and the same call without
+    room for it."""
+    x, q, s = rows(M, K, seed=M)
+    qw, sw = weights(N, K, seed=4)
+    b = S.bias_bf16(N)
+    assert (w4.w4_workspace_bytes(w4.W4_OP_FP8_BLOCK, M, N, K, 0) > 0) == split
+    r = O.fp8_block_linear(q, s, qw, sw, b)
+    args = fp8(q), to_dev(s), fp8(qw), to_dev(sw)
+    y = w4.w4_fp8_block_gemm(*args, bias=bf16(b))
+    whole = w4.w4_fp8_block_gemm(*args, bias=bf16(b), workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    again = w4.w4_fp8_block_gemm(*args, bias=bf16(b))
+    act = w4.w4_fp8_block_gemm_bf16in(bf16(x), fp8(qw), to_dev(sw), bias=bf16(b))
+    torch.cuda.synchronize()
+    assert w4.w4_device_status() == w4.W4_OK
+    check_bf16_output(bits(y), r, "split")
+    check_bf16_output(bits(whole), r, "whole")
+    np.testing.assert_array_equal(bits(again), bits(y))
+    np.testing.assert_array_equal(bits(act), bits(y))
+
+
+def test_binding_refusals():
+    """Wrong shapes, types, layouts and missing tensors raise ValueError; what the
+    library refuses raises W4Error with its status."""
+    M, N, K, E = 4, 264, 256, 2
+    x, q, s = rows(M, K)
+    qw, sw = weights(N, K)
+    qe, se = weights(N, K, E=E)
+    X, Q, SX, W, WS = bf16(x), fp8(q), to_dev(s), fp8(qw), to_dev(sw)
+    WE, WSE, off = fp8(qe), to_dev(se), to_dev(np.array([0, 1, 4], np.int32))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    bad = [
+        lambda: w4.w4_quant_act_per_block(X.float()),
+        lambda: w4.w4_quant_act_per_block(X[0]),
+        lambda: w4.w4_quant_act_per_block(X[:, ::2]),
+        lambda: w4.w4_quant_act_per_block(X, q=torch.empty((M, K + 8), dtype=torch.uint8, device="cuda")),
+        lambda: w4.w4_quant_act_per_block(X, scale=torch.empty((M, 3), device="cuda")),
+        lambda: w4.w4_silu_mul_quant_block(X.half()),
+        lambda: w4.w4_silu_mul_quant_block(torch.zeros((2, 17), dtype=torch.bfloat16, device="cuda")),
+        lambda: w4.w4_fp8_block_gemm(X, SX, W, WS),
+        lambda: w4.w4_fp8_block_gemm(Q, SX[:, :1].contiguous(), W, WS),
+        lambda: w4.w4_fp8_block_gemm(Q, SX, W[:, :128].contiguous(), WS),
+        lambda: w4.w4_fp8_block_gemm(Q, SX, W, WS[:2].contiguous()),
+        lambda: w4.w4_fp8_block_gemm(Q, SX, W, WS.half()),
+        lambda: w4.w4_fp8_block_gemm(Q, SX, W.t(), WS),
+        lambda: w4.w4_fp8_block_gemm(Q, SX, W, WS, bias=torch.zeros(N, device="cuda")),
+        lambda: w4.w4_fp8_block_gemm(Q, SX, W, WS, bias=torch.zeros(N + 8, dtype=torch.bfloat16, device="cuda")),
+        lambda: w4.w4_fp8_block_gemm(Q, SX, W, WS, y=torch.empty((M, N), device="cuda")),
+        lambda: w4.w4_fp8_block_gemm(Q, SX, W, None),
+        lambda: w4.w4_fp8_block_gemm_bf16in(X.float(), W, WS),
+        lambda: w4.w4_fp8_block_gemm_bf16in(X, W, WS, workspace=torch.empty(64, dtype=torch.uint8)),
+        lambda: w4.w4_fp8_block_moe_grouped_gemm(Q, SX, off[:2].contiguous(), WE, WSE),
+        lambda: w4.w4_fp8_block_moe_grouped_gemm(Q, SX, off.long(), WE, WSE),
+        lambda: w4.w4_fp8_block_moe_grouped_gemm(Q, SX, off, W, WSE),
+        lambda: w4.w4_fp8_block_moe_grouped_gemm(Q, SX, off, WE, WSE[:1].contiguous()),
+        lambda: w4.w4_fp8_block_moe_gemm_bf16in(X.half(), None, off, WE, WSE),
+        lambda: w4.w4_fp8_block_moe_gemm_bf16in(X, torch.zeros(4, dtype=torch.int64, device="cuda"), off, WE, WSE),
+        lambda: w4.w4_moe_route_grouped(torch.zeros((2, 8), dtype=torch.float16, device="cuda"), 2),
+        lambda: w4.w4_moe_route_grouped(torch.zeros((2, 8), device="cuda"), 2, bias=torch.zeros(7, device="cuda")),
+        lambda: w4.w4_moe_route_grouped(torch.zeros((2, 8), device="cuda"), 2, out=(1, 2)),
+        lambda: w4.w4_moe_route_grouped(torch.zeros((2, 8), device="cuda"), 2, out=(
+            torch.empty((2, 2), **i32), torch.empty((2, 2), device="cuda"), torch.empty(8, **i32), torch.empty(4, **i32),
+            torch.empty((2, 2), **i32))),
+    ]
+    for i, call in enumerate(bad):
+        with pytest.raises(ValueError):
+            call()
+            pytest.fail(f"refusal {i} did not raise")
+    refused = [
+        (w4.W4_ERR_UNSUPPORTED, lambda: w4.w4_fp8_block_gemm(*(fp8(np.zeros((2, 24), np.uint8)), torch.ones((2, 1), device="cuda"),
+                                                               fp8(np.zeros((8, 24), np.uint8)), torch.ones((1, 1), device="cuda")))),
+        (w4.W4_ERR_ALIGN, lambda: w4.w4_quant_act_per_block(torch.zeros((2, 12), dtype=torch.bfloat16, device="cuda"))),
+        (w4.W4_ERR_GROUP, lambda: w4.w4_moe_route_grouped(torch.zeros((2, 8), device="cuda"), 2, n_group=3)),
+        (w4.W4_ERR_SHAPE, lambda: w4.w4_moe_route_grouped(torch.zeros((2, 8), device="cuda"), 9)),
+        (w4.W4_ERR_WORKSPACE, lambda: w4.w4_fp8_block_gemm_bf16in(
+            X.repeat(20, 1), W, WS, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))),
+    ]
+    for status, call in refused:
+        with pytest.raises(w4.W4Error) as e:
+            call()
+        assert e.value.status == status
+    assert w4.w4_device_status() == w4.W4_OK
+
+
+def test_uint8_codes_and_given_outputs():
+    """Codes as uint8 tensors are the same call; outputs are written in place."""
+    M, N, K = 20, 136, 272
+    _, q, s = rows(M, K, seed=2)
+    qw, sw = weights(N, K, seed=3)
+    a = w4.w4_fp8_block_gemm(fp8(q), to_dev(s), fp8(qw), to_dev(sw))
+    y = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+    b = w4.w4_fp8_block_gemm(to_dev(q), to_dev(s), to_dev(qw), to_dev(sw), y=y)
+    torch.cuda.synchronize()
+    assert b.data_ptr() == y.data_ptr()
+    np.testing.assert_array_equal(bits(a), bits(y))
+
+
+def test_offsets_past_32_bits():
+    """More than 2^32 bytes of weights, of activations and of outputs: the last
+    expert, the last rows."""
+    N, K, E = 8192, 16384, 34
+    qw = torch.zeros((E, N, K), dtype=torch.uint8, device="cuda")       # 4.6e9 codes
+    sw = torch.ones((E, N // 128, K // 128), device="cuda")
+    last_q, last_s = weights(N, K, seed=1)
+    qw[E - 1], sw[E - 1] = to_dev(last_q), to_dev(last_s)
+    for R in (3, 130):
+        _, q, s = rows(R, K, seed=R)
+        off = np.array([0] * E + [R], np.int32)
+        y = w4.w4_fp8_block_moe_grouped_gemm(fp8(q), to_dev(s), to_dev(off), qw, sw)
+        torch.cuda.synchronize()
+        pick = np.array([0, R - 1])
+        check_bf16_output(bits(y)[pick], O.fp8_block_linear(q[pick], s[pick], last_q, last_s), "last expert")
+    del qw, sw
+    M, K = 270000, 16384                                                # 4.4e9 codes
+    x = torch.zeros((M, K), dtype=torch.bfloat16, device="cuda")
+    xb = S.activations_bf16(2, K, seed=9)
+    x[M - 2:] = bf16(xb)
+    q, s = w4.w4_quant_act_per_block(x)
+    rq, rs = O.quant_fp8_per_block(xb)
+    np.testing.assert_array_equal(codes(q[M - 2:]), rq)
+    np.testing.assert_array_equal(s[M - 2:].cpu().numpy(), rs)
+    del x
+    Nw = 8200                                                           # y of 2.2e9 values, 4.4e9 bytes
+    w, ws = weights(Nw, 128, seed=3)
+    y = w4.w4_fp8_block_gemm(q[:, :128].contiguous(), s[:, :1].contiguous(), fp8(w), to_dev(ws))
+    torch.cuda.synchronize()
+    check_bf16_output(bits(y[M - 2:]), O.fp8_block_linear(rq[:, :128], rs[:, :1], w, ws), "last rows")
+    assert w4.w4_device_status() == w4.W4_OK
