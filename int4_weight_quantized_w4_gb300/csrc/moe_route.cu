@@ -225,17 +225,37 @@ W4_DEV void route_token(const MoeRouteArgs& a, int64_t t, float (&v)[kEPL], uint
 }
 
 // Rows of tokens [t0, t1) in order: base[e] is expert e's next row, moved on
-// past them. bits, first: [kChunkWarps][E]. All threads of the block take part.
-W4_DEV void place_tokens(const MoeRouteArgs& a, int64_t t0, int64_t t1, uint32_t* bits, int32_t* first, int32_t* base) {
+// past them. bits, first: [kChunkWarps][E]. All threads of the block take part; a
+// thread keeps the experts of its pairs (at most kPairs of a chunk's), `ids` being
+// those of the first chunk.
+constexpr int kPairs = 8;
+struct PairIds {
+  int e[kPairs];
+};
+W4_DEV PairIds load_ids(const MoeRouteArgs& a, int64_t c0, int64_t t1) {
+  const int n = static_cast<int>(t1 - c0 < kChunk ? t1 - c0 : kChunk) * a.k;   // pairs of the chunk
+  PairIds p;
+#pragma unroll
+  for (int j = 0; j < kPairs; ++j) {
+    const int i = threadIdx.x + j * blockDim.x;
+    p.e[j] = i < n ? __ldcg(a.ids + c0 * a.k + i) : -1;
+  }
+  return p;
+}
+W4_DEV void place_tokens(const MoeRouteArgs& a, int64_t t0, int64_t t1, PairIds ids, uint32_t* bits, int32_t* first,
+                         int32_t* base) {
   const int E = a.E, k = a.k;
   for (int64_t c0 = t0; c0 < t1; c0 += kChunk) {
-    const int n = static_cast<int>(t1 - c0 < kChunk ? t1 - c0 : kChunk) * k;   // pairs of the chunk
     for (int i = threadIdx.x; i < kChunkWarps * E; i += blockDim.x) bits[i] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-      const int t = i / k;
-      atomicOr(&bits[(t >> 5) * E + a.ids[c0 * k + i]], 1u << (t & 31));
-    }
+    int tok[kPairs];
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j)
+      if (ids.e[j] >= 0) {
+        tok[j] = static_cast<int>((threadIdx.x + j * blockDim.x) / static_cast<unsigned>(k));
+        ids.e[j] += (tok[j] >> 5) * E;
+        atomicOr(&bits[ids.e[j]], 1u << (tok[j] & 31));
+      }
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
       int run = base[e];
@@ -246,12 +266,14 @@ W4_DEV void place_tokens(const MoeRouteArgs& a, int64_t t0, int64_t t1, uint32_t
       base[e] = run;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-      const int t = i / k, at = (t >> 5) * E + a.ids[c0 * k + i];
-      const int r = first[at] + __popc(bits[at] & ((1u << (t & 31)) - 1u));
-      a.row_token[r] = static_cast<int32_t>(c0 + t);
-      a.row_of[c0 * k + i] = r;
-    }
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j)
+      if (ids.e[j] >= 0) {
+        const int r = first[ids.e[j]] + __popc(bits[ids.e[j]] & ((1u << (tok[j] & 31)) - 1u));
+        a.row_token[r] = static_cast<int32_t>(c0 + tok[j]);
+        a.row_of[c0 * k + threadIdx.x + j * blockDim.x] = r;
+      }
+    if (c0 + kChunk < t1) ids = load_ids(a, c0 + kChunk, t1);
     __syncthreads();
   }
 }
@@ -331,10 +353,13 @@ __global__ void __launch_bounds__(32 * kRouteWarps<kEPL>) route_tile_kernel(cons
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) base[e] = 0;
   __syncthreads();
   add_expert_starts(a, cnt, base, part, true);
-  place_tokens(a, t0, t1, buf, reinterpret_cast<int32_t*>(buf) + kChunkWarps * a.E, base);
+  place_tokens(a, t0, t1, load_ids(a, t0, t1), buf, reinterpret_cast<int32_t*>(buf) + kChunkWarps * a.E, base);
 }
 
-constexpr int kPlaceThreads = 512;
+// Threads of a place CTA: 1024 for tiles of 64 tokens and more, 512 below (333
+// tokens of 96 experts: 7.3 us against 10.5; 16384 of 256: 37 us against 32).
+constexpr int kPlaceThreads = 1024;
+static_assert(kChunk * 64 <= kPairs * kPlaceThreads && 64 * 64 <= kPairs * 512, "a chunk's pairs at the largest top_k");
 __global__ void __launch_bounds__(kPlaceThreads) place_kernel(const MoeRouteArgs a, int per,
                                                               const int32_t* __restrict__ counts, int ntiles) {
   extern __shared__ uint32_t sm[];
@@ -344,15 +369,18 @@ __global__ void __launch_bounds__(kPlaceThreads) place_kernel(const MoeRouteArgs
   int32_t* base = first + kChunkWarps * a.E;
   int32_t* total = base + a.E;
   const int tile = blockIdx.x;
-  for (int e = threadIdx.x; e < 2 * a.E; e += kPlaceThreads) base[e] = 0;   // and total
+  for (int e = threadIdx.x; e < 2 * a.E; e += blockDim.x) base[e] = 0;   // and total
   __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int64_t t0 = static_cast<int64_t>(tile) * per, t1 = t0 + per < a.T ? t0 + per : a.T;
+  const PairIds ids = load_ids(a, t0, t1);   // on their way during the sums
   // column sums: as many threads per expert as there are, each over a share of the tiles
-  const int segs = a.E < kPlaceThreads ? kPlaceThreads / a.E : 1;
-  const int seg = a.E < kPlaceThreads ? threadIdx.x / a.E : 0;
+  const int threads = blockDim.x;
+  const int segs = a.E < threads ? threads / a.E : 1;
+  const int seg = a.E < threads ? threadIdx.x / a.E : 0;
   if (seg < segs)
-    for (int e = threadIdx.x - seg * a.E; e < a.E; e += kPlaceThreads) {
+    for (int e = threadIdx.x - seg * a.E; e < a.E; e += threads) {
       const int i0 = ntiles * seg / segs, i1 = ntiles * (seg + 1) / segs;
       int before = 0, all = 0;
 #pragma unroll 16
@@ -366,8 +394,7 @@ __global__ void __launch_bounds__(kPlaceThreads) place_kernel(const MoeRouteArgs
     }
   __syncthreads();
   add_expert_starts(a, total, base, part, tile == 0);
-  const int64_t t0 = static_cast<int64_t>(tile) * per, t1 = t0 + per < a.T ? t0 + per : a.T;
-  place_tokens(a, t0, t1, bits, first, base);
+  place_tokens(a, t0, t1, ids, bits, first, base);
 }
 
 int route_warps(int E) { return E <= 256 ? 32 : E <= 512 ? 16 : 8; }
@@ -394,7 +421,7 @@ cudaError_t launch_k(const MoeRouteArgs& a, cudaStream_t s) {
   PdlLaunch rl(ntiles, 32 * warps, 0, s);
   cudaError_t e = cudaLaunchKernelEx(&rl.cfg, route_tile_kernel<kEPL, false>, a, static_cast<int>(per), counts);
   if (e != cudaSuccess) return e;
-  PdlLaunch pl(ntiles, kPlaceThreads, static_cast<size_t>(2 * kChunkWarps + 2) * a.E * 4, s);   // at most 40 KB
+  PdlLaunch pl(ntiles, per >= 64 ? kPlaceThreads : 512, static_cast<size_t>(2 * kChunkWarps + 2) * a.E * 4, s);   // at most 40 KB
   return cudaLaunchKernelEx(&pl.cfg, place_kernel, a, static_cast<int>(per), static_cast<const int32_t*>(counts), ntiles);
 }
 
