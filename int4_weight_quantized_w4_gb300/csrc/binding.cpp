@@ -81,6 +81,16 @@ at::Tensor empty(at::IntArrayRef shape, ScalarType type, const at::Device& dev) 
   return at::detail::empty_cuda(shape, type, dev, std::nullopt);
 }
 
+// `shape` of a 4-byte type at 4-byte word `at` of `base`'s storage: a view made
+// directly (through the dispatcher it costs what an allocation does).
+at::Tensor words_of(const at::Tensor& base, int64_t at, at::IntArrayRef shape, ScalarType type) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(base.storage()), base.key_set(),
+                                                          c10::scalarTypeToTypeMeta(type));
+  t.unsafeGetTensorImpl()->set_storage_offset(at);
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+  return t;
+}
+
 at::Tensor output(PyObject* o, const char* name, at::IntArrayRef shape, ScalarType type, const Types& types,
                   const at::Device& dev) {
   return o == Py_None ? empty(shape, type, dev) : tensor(o, name, types, dev, shape);
@@ -197,10 +207,17 @@ PyObject* route_grouped(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const char* names[5] = {"topk_ids", "topk_weights", "offsets", "row_token", "row_of"};
   if (a[8] != Py_None && (!PyTuple_Check(a[8]) || PyTuple_GET_SIZE(a[8]) != 5))
     value_error("out must be the tuple (topk_ids, topk_weights, offsets, row_token, row_of)");
+  // the five outputs share one allocation when none are given
+  const int64_t starts[5] = {0, T * k, 4 * T * k, 2 * T * k, 3 * T * k};
+  at::Tensor all;
+  if (a[8] == Py_None) all = empty({4 * T * k + E + 1}, ScalarType::Int, dev);
   for (int i = 0; i < 5; ++i) {
     const at::DimVector shape = i == 2 ? at::DimVector{E + 1} : i == 3 ? at::DimVector{T * k} : at::DimVector{T, k};
     const ScalarType type = i == 1 ? ScalarType::Float : ScalarType::Int;
-    o[i] = output(a[8] == Py_None ? Py_None : PyTuple_GET_ITEM(a[8], i), names[i], shape, type, i == 1 ? kF32 : kI32, dev);
+    if (a[8] == Py_None)
+      o[i] = words_of(all, starts[i], shape, type);
+    else
+      o[i] = tensor(PyTuple_GET_ITEM(a[8], i), names[i], i == 1 ? kF32 : kI32, dev, shape);
   }
   if (T == 0 && a[8] == Py_None) o[2].zero_();   // the library writes nothing
   const Scratch s = scratch(a[9], W4_OP_MOE_ROUTE_GROUPED, T, E, 1, 0, dev);

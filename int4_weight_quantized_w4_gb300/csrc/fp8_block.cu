@@ -658,6 +658,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const __grid_constan
         }
       }
     } else {
+      const bool leader = elect_one();
       const int mine = warp - kTWarpMma;   // blocks and accumulator of this parity
       constexpr uint32_t idesc = tc::idesc_f16_f32(TM, TN);
       const uint64_t ad0 = tc::sdesc_sw128(smem_addr(a_base)), bd0 = tc::sdesc_sw128(smem_addr(b_base));
@@ -668,12 +669,13 @@ __global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const __grid_constan
       for (long long it = blockIdx.x; ok && it < p.items && decode_work(p, it, starts, w, e); it += gridDim.x)
         for (int kb = w.kb0; kb < w.kb1; ++kb, ++g) {
           if (static_cast<int>(g & 1) == mine) {
-            if (!(ok = wait_warp(&acc_empty[mine], aph, abort_flag, p.status))) break;
+            const uint64_t ad = ad0 + static_cast<uint64_t>((st * T_A) >> 4), bd = bd0 + static_cast<uint64_t>((st * T_B) >> 4);
+            // the operands are there long before: the accumulator, waited for last, is what holds the MMAs up
             if (!(ok = wait_warp(&full[st], ph, abort_flag, p.status))) break;
+            if (!(ok = wait_warp(&acc_empty[mine], aph, abort_flag, p.status))) break;
             tc::fence_after_sync();
-            if (elect_one()) {
-              mma_block(tmem + mine * TN, ad0 + static_cast<uint64_t>((st * T_A) >> 4),
-                        bd0 + static_cast<uint64_t>((st * T_B) >> 4), idesc);
+            if (leader) {
+              mma_block(tmem + mine * TN, ad, bd, idesc);
               tc::commit(&done[st]);
             }
             __syncwarp();
