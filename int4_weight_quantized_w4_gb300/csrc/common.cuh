@@ -290,12 +290,22 @@ W4_DEV uint32_t quotient2_e4m3(float x0, float x1, float s, float r) {
 }
 
 // The codes of 8 values. s below kRefineMin (a block of values below 4e-22), or
-// not finite, takes the IEEE divide.
+// not finite, takes the IEEE divide. With kExact off the quotient is fl(x r), within
+// 1.5 ulp of x / s: for values that are known to a few ulp themselves.
+template <bool kExact = true>
 W4_DEV uint2 quant_e4m3_block(const float (&x)[8], float s, float r) {
   uint32_t p[4];
   if (s >= kRefineMin && s < 1e37f) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = quotient2_e4m3(x[2 * i], x[2 * i + 1], s, r);
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (kExact) {
+        p[i] = quotient2_e4m3(x[2 * i], x[2 * i + 1], s, r);
+      } else {
+        float q0, q1;
+        mul2(q0, q1, x[2 * i], x[2 * i + 1], r);
+        p[i] = e4m3x2_rn(q0, q1);
+      }
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) p[i] = e4m3x2_rn(__fdiv_rn(x[2 * i], s), __fdiv_rn(x[2 * i + 1], s));
