@@ -441,7 +441,7 @@ w4_status w4_quant_act_per_block(const void* x, int32_t x_dtype, int64_t M, int6
   if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 4))
     return fail(W4_ERR_ALIGN, "x and q must be 16-byte aligned, scale 4-byte aligned");
   if (K > INT32_MAX / 2) return fail(W4_ERR_UNSUPPORTED, "K too large");
-  return from_cuda(w4::launch_quant_block(x, x_dtype == W4_FP16, false, M, K, nullptr, 0, q, scale, nullptr,
+  return from_cuda(w4::launch_quant_block(x, x_dtype == W4_FP16, false, M, K, nullptr, 0, false, q, scale, nullptr,
                                           static_cast<cudaStream_t>(stream)),
                    "w4_quant_act_per_block launch");
 }
@@ -454,7 +454,7 @@ w4_status w4_silu_mul_quant_block(const void* h, int64_t R, int64_t I, void* q, 
   if (!aligned(h, 16) || !aligned(q, 16) || !aligned(scale, 4))
     return fail(W4_ERR_ALIGN, "h and q must be 16-byte aligned, scale 4-byte aligned");
   if (I > INT32_MAX / 2) return fail(W4_ERR_UNSUPPORTED, "I too large");
-  return from_cuda(w4::launch_quant_block(h, false, true, R, I, nullptr, 0, q, scale, nullptr,
+  return from_cuda(w4::launch_quant_block(h, false, true, R, I, nullptr, 0, false, q, scale, nullptr,
                                           static_cast<cudaStream_t>(stream)),
                    "w4_silu_mul_quant_block launch");
 }
@@ -491,7 +491,7 @@ static w4_status run_fp8_block(const void* qx, const float* x_scale, const int32
   cudaError_t e = status_ptr(&status);
   if (e != cudaSuccess) return from_cuda(e, "device status word");
   const w4::Fp8BlockArgs a{qx, x_scale, qweight, w_scale, bias,  y,       offsets, E, R, N, K,
-                           nullptr, false, static_cast<float*>(ws), ws == nullptr ? 0 : ws_bytes, status};
+                           nullptr, false, false, static_cast<float*>(ws), ws == nullptr ? 0 : ws_bytes, status};
   return from_cuda(w4::launch_fp8_block(a, static_cast<cudaStream_t>(stream)), "fp8 block product launch");
 }
 
@@ -513,7 +513,7 @@ static w4_status run_fp8_block_act(const void* x, bool f16, int64_t T, const int
   if (e != cudaSuccess) return from_cuda(e, "device status word");
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (fused) {
-    const w4::Fp8BlockArgs a{nullptr, nullptr, qweight, w_scale, bias, y, offsets, E, R, N, K, x, f16, nullptr, 0, status};
+    const w4::Fp8BlockArgs a{nullptr, nullptr, qweight, w_scale, bias, y, offsets, E, R, N, K, x, f16, false, nullptr, 0, status};
     return from_cuda(w4::launch_fp8_block(a, s), "fp8 block product launch");
   }
   float* x_scale = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + static_cast<size_t>(R) * K);   // K % 16 == 0
@@ -524,15 +524,15 @@ static w4_status run_fp8_block_act(const void* x, bool f16, int64_t T, const int
   if (rows != nullptr && 2 * T <= R && R * K >= kCopyElements && ws_bytes >= base + tokens) {
     uint8_t* tq = static_cast<uint8_t*>(ws) + base;
     float* ts = reinterpret_cast<float*>(tq + static_cast<size_t>(T) * K);
-    e = w4::launch_quant_block(x, f16, false, T, K, nullptr, 0, tq, ts, status, s);
+    e = w4::launch_quant_block(x, f16, false, T, K, nullptr, 0, false, tq, ts, status, s);
     if (e == cudaSuccess) e = w4::launch_gather_block_rows(tq, ts, T, K, rows, R, ws, x_scale, status, s);
   } else {
-    e = w4::launch_quant_block(x, f16, false, R, K, rows, T, ws, x_scale, status, s);
+    e = w4::launch_quant_block(x, f16, false, R, K, rows, T, offsets != nullptr, ws, x_scale, status, s);
   }
   if (e != cudaSuccess) return from_cuda(e, "block quant launch");
   // dense: the part sums of split tiles follow the codes
   const size_t extra = ws_bytes - base;
-  const w4::Fp8BlockArgs a{ws, x_scale, qweight, w_scale, bias, y, offsets, E, R, N, K, nullptr, false,
+  const w4::Fp8BlockArgs a{ws, x_scale, qweight, w_scale, bias, y, offsets, E, R, N, K, nullptr, false, offsets != nullptr,
                            reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + base), offsets == nullptr ? extra : 0, status};
   return from_cuda(w4::launch_fp8_block(a, s), "fp8 block product launch");
 }

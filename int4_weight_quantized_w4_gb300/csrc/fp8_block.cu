@@ -18,7 +18,9 @@
 //
 // Both are launched as programmatic dependents and let their own dependents go
 // early: the copies of weights start while the kernel before finishes, everything
-// else (activations, scales, bias, expert offsets, y) waits for it.
+// else (activations, scales, bias, y) waits for it, and so do the expert offsets
+// unless that kernel is the row quantizer, which starts this one only when all
+// before it is done.
 #include <cuda.h>
 
 #include <atomic>
@@ -47,6 +49,7 @@ struct Params {
   const uint16_t* bias;    // bf16 [N] or null
   uint16_t* y;             // bf16 [rows, N]
   const int32_t* offsets;  // [E + 1], or null (dense: one segment of all rows)
+  bool offsets_ready;      // whatever writes them is done when this kernel starts
   int E, rows, N, K, KB, NB, n_tiles;
   int split;               // stream form, dense: parts of the k blocks, one per CTA of a cluster
   int items;               // upper bound of (row tile, n tile) pairs, or of the tile form's work items
@@ -234,7 +237,7 @@ __global__ void __launch_bounds__(Stream<NT, kQuant>::THREADS, Stream<NT, kQuant
   if (warp == kSWarpA && lane == 0) tc::prefetch_tmap(&p.tm_w);
   if (!kQuant && warp == kSWarpB && lane == 0) tc::prefetch_tmap(&p.tm_x);
   if (p.offsets != nullptr) {
-    grid_dependency_wait();   // the routing may be running still
+    if (!p.offsets_ready) grid_dependency_wait();   // the routing may be running still
     tile_starts<C::THREADS>(p, NT, starts, warp_sum);
   }
   tc::fence_before_sync();
@@ -590,7 +593,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const __grid_constan
     tc::prefetch_tmap(&p.tm_w);
   }
   if (p.offsets != nullptr) {
-    grid_dependency_wait();   // the routing may be running still
+    if (!p.offsets_ready) grid_dependency_wait();   // the routing may be running still
     tile_starts<kTThreads>(p, TM, starts, warp_sum);
   }
   tc::fence_before_sync();
@@ -947,6 +950,7 @@ cudaError_t launch_fp8_block(const Fp8BlockArgs& a, cudaStream_t s) {
   p.bias = static_cast<const uint16_t*>(a.bias);
   p.y = static_cast<uint16_t*>(a.y);
   p.offsets = a.expert_offsets;
+  p.offsets_ready = a.offsets_ready;
   p.E = a.E;
   p.rows = static_cast<int>(a.R);
   p.N = static_cast<int>(a.N);

@@ -48,14 +48,15 @@ W4_DEV void silu_mul2(uint32_t g, uint32_t u, float& a0, float& a1) {
 
 // x [*, K8 chunks], or with kSilu [*, 2 K8]; row r of the output comes from row
 // gather[r] (gather may be null: row r). An id outside [0, T) gives a zero row
-// with scales 1 and W4_ERR_SHAPE in the status word. KU = ceil(KB / kUnits).
+// with scales 1 and W4_ERR_SHAPE in the status word. KU = ceil(KB / kUnits). late:
+// the next kernel starts only when every kernel before this one is done.
 template <bool kF16, bool kSilu, int kUnits>
 __global__ void __launch_bounds__(kThreads) quant_block_kernel(const uint4* __restrict__ x, uint32_t items, int K8,
                                                                int KB, uint32_t KU, uint2* __restrict__ q,
                                                                float* __restrict__ scale,
                                                                const int32_t* __restrict__ gather, int64_t T,
-                                                               unsigned int* status) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+                                                               bool late, unsigned int* status) {
+  if (!late) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int l = threadIdx.x & (kBlk8 - 1);
   const uint32_t it = blockIdx.x * (kThreads / kBlk8) + threadIdx.x / kBlk8;
   const bool live = it < items;                 // dead half-warps still take part in the shuffles
@@ -66,6 +67,7 @@ __global__ void __launch_bounds__(kThreads) quant_block_kernel(const uint4* __re
   // The kernel before may still be running when this one starts (see launch): x and
   // the row ids may come from it, and it may still be reading q.
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (late) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (gather != nullptr && live) {
     src = gather[row];
     bad = src < 0 || src >= T;
@@ -116,8 +118,8 @@ __global__ void __launch_bounds__(kThreads) quant_block_kernel(const uint4* __re
 }
 
 template <bool kF16, bool kSilu, int kUnits>
-cudaError_t launch(const void* x, int64_t M, int64_t K, const int32_t* gather, int64_t T, void* q, float* scale,
-                   unsigned int* status, cudaStream_t s) {
+cudaError_t launch(const void* x, int64_t M, int64_t K, const int32_t* gather, int64_t T, bool late, void* q,
+                   float* scale, unsigned int* status, cudaStream_t s) {
   const int K8 = static_cast<int>(K / 8), KB = static_cast<int>((K + 127) / 128), KU = (KB + kUnits - 1) / kUnits;
   const int64_t items = M * KU;
   const int64_t blocks = (items * kBlk8 + kThreads - 1) / kThreads;
@@ -125,22 +127,23 @@ cudaError_t launch(const void* x, int64_t M, int64_t K, const int32_t* gather, i
   PdlLaunch pl(static_cast<unsigned>(blocks), kThreads, 0, s);
   return cudaLaunchKernelEx(&pl.cfg, quant_block_kernel<kF16, kSilu, kUnits>, static_cast<const uint4*>(x),
                             static_cast<uint32_t>(items), K8, KB, static_cast<uint32_t>(KU), static_cast<uint2*>(q),
-                            scale, gather, T, status);
+                            scale, gather, T, late, status);
 }
 
 // Quantized rows copied to their places among the expert-sorted rows: row r of
-// (dst, dst_scale) is row gather[r] of (src, src_scale). A warp per row.
+// (dst, dst_scale) is row gather[r] of (src, src_scale). A warp per row. The next
+// kernel starts only when every kernel before this one is done.
 __global__ void __launch_bounds__(kThreads) gather_rows_kernel(const uint4* __restrict__ src,
                                                                const float* __restrict__ src_scale, int64_t T, int K16,
                                                                int KB, const int32_t* __restrict__ gather, int64_t R,
                                                                uint4* __restrict__ dst, float* __restrict__ dst_scale,
                                                                unsigned int* status) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31;
   const int64_t r = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // src comes from the kernel before
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (r >= R) return;
   const int64_t t = gather[r];
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // src comes from the kernel before
   uint4* d = dst + r * K16;
   if (t < 0 || t >= T) {
     for (int i = lane; i < K16; i += 32) d[i] = make_uint4(0, 0, 0, 0);
@@ -168,10 +171,10 @@ __global__ void __launch_bounds__(kThreads) gather_rows_kernel(const uint4* __re
 }  // namespace
 
 cudaError_t launch_quant_block(const void* x, bool f16, bool silu, int64_t M, int64_t K, const int32_t* gather,
-                               int64_t T, void* q, float* scale, unsigned int* status, cudaStream_t s) {
-  if (silu) return launch<false, true, 2>(x, M, K, gather, T, q, scale, status, s);
-  return f16 ? launch<true, false, 4>(x, M, K, gather, T, q, scale, status, s)
-             : launch<false, false, 4>(x, M, K, gather, T, q, scale, status, s);
+                               int64_t T, bool late, void* q, float* scale, unsigned int* status, cudaStream_t s) {
+  if (silu) return launch<false, true, 2>(x, M, K, gather, T, late, q, scale, status, s);
+  return f16 ? launch<true, false, 4>(x, M, K, gather, T, late, q, scale, status, s)
+             : launch<false, false, 4>(x, M, K, gather, T, late, q, scale, status, s);
 }
 
 cudaError_t launch_gather_block_rows(const void* src, const float* src_scale, int64_t T, int64_t K,

@@ -140,10 +140,12 @@ cudaError_t launch_silu_mul_quant(const void* h, int64_t R, int64_t I, void* q, 
 cudaError_t launch_moe_combine(const void* y, int64_t R, int64_t H, const float* w, const int32_t* row_of, int64_t T,
                                int32_t k, void* out, unsigned int* status, cudaStream_t s);
 // e4m3 codes and fp32 scales per row and 128 columns of x [*, K] (bf16, or fp16), or of silu(gate) * up of x
-// [*, 2K] (silu, bf16); gather (may be null): source row of each of the M output rows, checked against T.
+// [*, 2K] (silu, bf16); gather (may be null): source row of each of the M output rows, checked against T. late: a
+// programmatic dependent starts only when every kernel before this one is done.
 cudaError_t launch_quant_block(const void* x, bool f16, bool silu, int64_t M, int64_t K, const int32_t* gather,
-                               int64_t T, void* q, float* scale, unsigned int* status, cudaStream_t s);
-// Rows gather[r] of quantized (src, src_scale) [T, K], which the kernel launched just before writes, as row r of (dst, dst_scale).
+                               int64_t T, bool late, void* q, float* scale, unsigned int* status, cudaStream_t s);
+// Rows gather[r] of quantized (src, src_scale) [T, K], which the kernel launched just before writes, as row r of (dst, dst_scale);
+// late, as above.
 cudaError_t launch_gather_block_rows(const void* src, const float* src_scale, int64_t T, int64_t K,
                                      const int32_t* gather, int64_t R, void* dst, float* dst_scale,
                                      unsigned int* status, cudaStream_t s);
@@ -159,6 +161,7 @@ struct Fp8BlockArgs {
   int64_t R, N, K;
   const void* x;                  // where fp8_block_fuses: 16-bit activations [R, K] in place of qx and x_scale
   bool x_f16;
+  bool offsets_ready;             // experts: the kernel launched just before lets its dependents go late
   float* part_sums;               // dense: at least fp8_block_part_bytes, 16-byte aligned (or null, 0: the product is not split along K)
   size_t part_bytes;
   unsigned int* status;
