@@ -36,7 +36,7 @@ namespace {
 constexpr int kBlk = 128;                     // k and weight rows per scale
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxSplit = 8;                  // CTAs of a cluster that share a tile's k blocks
-constexpr int kFuseRows = 8;                 // up to this many dense rows the stream form quantizes
+constexpr int kFuseRows = 8;                  // up to this many dense rows the stream form quantizes
 constexpr uint64_t kWaitNs = 2000000000ull;   // 2 s per wait
 
 struct Params {
@@ -628,7 +628,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const __grid_constan
       bool ok = true;
       Work w;
       for (long long it = blockIdx.x; ok && it < p.items && decode_work(p, it, starts, w, e); it += gridDim.x) {
-          const Tile& t = w.t;
+        const Tile& t = w.t;
         const int nb = t.n0 / kBlk;
         const float* sw0 = p.w_scale + (static_cast<size_t>(t.expert) * p.NB + nb) * KB;
         const float* sw1 = nb + 1 < p.NB ? sw0 + KB : sw0;

@@ -28,22 +28,22 @@ constexpr int kBlk8 = 16;       // 8-element chunks per block of 128 columns
 constexpr int kThreads = 256;
 constexpr unsigned kFull = 0xFFFFFFFFu;
 
-// silu(g) * u = g u / (1 + 2^(-g log2 e)) of the bf16 pairs g and u, with the fast
-// exponential and reciprocal (a few ulp). The exponent is held to 126, so that the
-// denominator stays a normal number and its reciprocal too: for g < -87 the
-// result is g u 2^-126 instead of a number smaller still. Multiplications and
-// additions go two at a time.
+// silu(g) * u = g / (1 + 2^(-g log2 e)) * u of the bf16 pairs g and u, with the
+// fast exponential and reciprocal (a few ulp). The gate comes before u, so that only
+// the product itself can overflow. Gates below -87.3, whose reciprocal is no normal
+// number, give 0 (silu is above -1.1e-36 there). Multiplications and additions go
+// two at a time.
 W4_DEV void silu_mul2(uint32_t g, uint32_t u, float& a0, float& a1) {
   const float g0 = bf16_lo(g), g1 = bf16_hi(g);
   float t0, t1;
   mul2(t0, t1, g0, g1, -1.44269504f);   // -log2(e)
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t0) : "f"(fminf(t0, 126.f)));
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t1) : "f"(fminf(t1, 126.f)));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t0) : "f"(t0));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t1) : "f"(t1));
   add2(t0, t1, t0, t1, 1.f);
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t0) : "f"(t0));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t1) : "f"(t1));
-  mul2v(a0, a1, g0, g1, bf16_lo(u), bf16_hi(u));
-  mul2v(a0, a1, a0, a1, t0, t1);
+  mul2v(a0, a1, g0, g1, t0, t1);
+  mul2v(a0, a1, a0, a1, bf16_lo(u), bf16_hi(u));
 }
 
 // x [*, K8 chunks], or with kSilu [*, 2 K8]; row r of the output comes from row

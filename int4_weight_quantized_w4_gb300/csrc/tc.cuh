@@ -177,7 +177,7 @@ W4_DEV void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
       : "r"(taddr) : "memory");
 }
 
-// The same loads without the wait: 16 or 32 columns. tmem_wait_ld, given the
+// The same load of 16 columns without the wait. tmem_wait_ld, given the
 // registers, makes them usable (its operands keep the uses behind it).
 W4_DEV void tmem_ld16_async(uint32_t taddr, uint32_t (&v)[16]) {
   asm volatile(
@@ -192,66 +192,6 @@ W4_DEV void tmem_wait_ld(uint32_t (&v)[16]) {
                : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
                  "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
                :: "memory");
-}
-
-// ---------------------------------------------------------------------------
-// CTA pairs (two CTAs of a cluster, ranks 2i and 2i + 1): one MMA over both
-// SMs' shared memory and tensor memory. One warp of each CTA allocates and
-// frees; the MMAs are issued by the even CTA alone. Addresses in descriptors
-// and of accumulators are the same offsets in both CTAs.
-// ---------------------------------------------------------------------------
-
-W4_DEV void tmem_alloc_pair(uint32_t* dst, uint32_t ncols) {
-  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
-               :: "r"(smem_addr(dst)), "r"(ncols) : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-}
-W4_DEV void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
-  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(taddr), "r"(ncols) : "memory");
-}
-
-// M = 256: rows 0-127 of A and D in the even CTA, 128-255 in the odd one; the
-// first half of B's rows in the even CTA, the second in the odd one.
-W4_DEV void mma_f8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{.reg .pred p; setp.ne.b32 p, %4, 0; "
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;}"
-      :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
-}
-
-// Arrive (once) on `bar` of both CTAs when every pair MMA this thread issued so far is done.
-W4_DEV void commit_pair(uint64_t* bar) {
-  asm volatile(
-      "{.reg .b16 m; mov.b16 m, 3; "
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;}"
-      :: "r"(smem_addr(bar)) : "memory");
-}
-
-// The cluster address of `p` in CTA `rank` of the cluster.
-W4_DEV uint32_t cluster_addr(const void* p, uint32_t rank) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
-  return a;
-}
-// Arrive on a barrier of any CTA of the cluster. The default (CTA) release scope is
-// meant for handing over tensor memory, whose reads tcgen05.wait::ld and the
-// fence before it have finished; with .cluster scope the arrive first waits for
-// the thread's other memory traffic (about 0.5 us, measured in the fp8 block kernel).
-W4_DEV void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
-}
-
-// Tile copies into this CTA whose bytes count on a barrier of either CTA of the
-// pair (bar: a cluster address).
-W4_DEV void tma_load_2d_pair(void* smem_dst, const void* tmap, uint32_t bar, int c0, int c1) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
-      :: "r"(smem_addr(smem_dst)), "l"(tmap), "r"(bar), "r"(c0), "r"(c1) : "memory");
-}
-W4_DEV void tma_load_3d_pair(void* smem_dst, const void* tmap, uint32_t bar, int c0, int c1, int c2) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
-      :: "r"(smem_addr(smem_dst)), "l"(tmap), "r"(bar), "r"(c0), "r"(c1), "r"(c2) : "memory");
 }
 
 }  // namespace tc

@@ -98,6 +98,26 @@ def test_silu_mul_quant_block(R, I):
         assert np.mean(step == 0) >= 0.999 or step.sum() <= 1
 
 
+def test_silu_mul_quant_block_far_gates():
+    """Gates far below zero give 0, however large they or `up` are; only the
+    product itself overflows; NaN and infinite gates stay in their block."""
+    g = torch.tensor([-90.0, -1000.0, -1e30, -3e38, 1.0, 2.0, 0.0, -0.0]).repeat(32)
+    u = torch.tensor([1.0, 1e30, 3e38, 3e38, 448.0, -2.0, 5.0, 7.0]).repeat(32)
+    h = torch.cat([g, u]).bfloat16().cuda().repeat(3, 1)
+    h[1, 3], h[2, 129] = float("nan"), float("-inf")
+    q, s = w4.w4_silu_mul_quant_block(h)
+    torch.cuda.synchronize()
+    act = torch.nn.functional.silu(g.double()) * u.double()
+    c = codes(q).reshape(3, 32, 8)
+    np.testing.assert_allclose(s.cpu().numpy()[0], float(act[4]) / 448, rtol=2.0 ** -19)
+    assert (c[0][:, [0, 1, 2, 3, 6, 7]] & 0x7F == 0).all()
+    ref = O.e4m3_encode((act[4:6] / act[4] * 448).numpy())
+    assert (c[0][:, 4:6] == ref).all()
+    assert c[1][0, 3] & 0x7F == 0x7F and c[2].reshape(-1)[129] & 0x7F == 0x7F
+    np.testing.assert_array_equal(c[1][16:], c[0][16:])
+    np.testing.assert_array_equal(c[2][:16], c[0][:16])
+
+
 # ---- dense ------------------------------------------------------------------
 
 @pytest.mark.parametrize("M,N,K", [
