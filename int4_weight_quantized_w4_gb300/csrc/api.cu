@@ -495,7 +495,11 @@ static w4_status run_fp8_block(const void* qx, const float* x_scale, const int32
   return from_cuda(w4::launch_fp8_block(a, static_cast<cudaStream_t>(stream)), "fp8 block product launch");
 }
 
-constexpr int64_t kCopyElements = int64_t{1} << 22;
+// Codes of expert rows from which on tokens are quantized once and copied: the extra
+// launch costs 1 to 4 us, the rows' own quantization grows by 0.4 us a million (the
+// whole product, quantized by row / copied: 4 M codes 65.7 / 69.6 us, 14 M 42.6 /
+// 44.1, 16 M 147.1 / 146.5, 58 M 64.8 / 53.1, 67 M 241 / 227).
+constexpr int64_t kCopyElements = int64_t{1} << 24;
 
 // Quantizes rows of x (gathered by `rows` when given) into the workspace, then multiplies.
 static w4_status run_fp8_block_act(const void* x, bool f16, int64_t T, const int32_t* rows, const int32_t* offsets,
@@ -519,7 +523,7 @@ static w4_status run_fp8_block_act(const void* x, bool f16, int64_t T, const int
   float* x_scale = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + static_cast<size_t>(R) * K);   // K % 16 == 0
   // Tokens that are rows of several experts are quantized once and their codes
   // copied, when the workspace has room for the tokens' codes and the copy is
-  // worth a launch (32768 rows of 4096 tokens x 2048: see launch_gather_block_rows).
+  // worth a launch.
   const size_t base = w4::fp8_block_workspace_bytes(R, K), tokens = w4::fp8_block_workspace_bytes(T, K);
   if (rows != nullptr && 2 * T <= R && R * K >= kCopyElements && ws_bytes >= base + tokens) {
     uint8_t* tq = static_cast<uint8_t*>(ws) + base;

@@ -36,7 +36,10 @@ namespace {
 constexpr int kBlk = 128;                     // k and weight rows per scale
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxSplit = 8;                  // CTAs of a cluster that share a tile's k blocks
-constexpr int kFuseRows = 8;                  // up to this many dense rows the stream form quantizes
+// Up to this many dense rows the stream form quantizes: one launch less (fused / not:
+// 1 x 4096 x 4096 6.3 / 7.1 us, 8 x 4096 x 4096 7.0 / 7.6, 8 x 14336 x 4096 14.3 / 14.4). Every
+// CTA quantizes them again, so that at 16 rows the order turns (8.5 / 8.0).
+constexpr int kFuseRows = 8;
 constexpr uint64_t kWaitNs = 2000000000ull;   // 2 s per wait
 
 struct Params {
@@ -934,10 +937,23 @@ static Plan tile_plan(int64_t R, int64_t N, int64_t K) {
   return {tiles - r, r, static_cast<int>(s)};
 }
 
+// The tile form is for more rows per weight tile than the stream form takes at
+// once. Experts: above 56 rows an expert on average, where the stream form would have
+// to read many weight tiles twice (64 experts of 2816 x 2048, stream / tile: 48 rows
+// 69.9 / 72.5 us, 56 rows 73.0 / 73.0, 64 rows 81 / 74, 96 rows 106 / 79). Dense:
+// above 128 rows (4096 x 4096 at 129 rows 18.2 / 15.4 us, 11008 x 4096 41 / 21), or above
+// 64 where the N tiles alone fill more than half of the SMs, so that no cluster
+// shares their k (96 rows, stream / tile: 11008 x 4096 22.2 / 20.1, 131072 x 2048
+// 70 / 55, but 4096 x 4096 12.1 / 15.3 and 2048 x 8192 13.8 / 17.3).
+static bool tile_form(int64_t R, int64_t N, int64_t E, bool experts) {
+  if (experts) return R > 56 * E;
+  return R > 128 || (R > 64 && 2 * ((N + kBlk - 1) / kBlk) > kPlanSms);
+}
+
 bool fp8_block_fuses(int64_t R, bool experts) { return !experts && R <= kFuseRows; }
 
 size_t fp8_block_part_bytes(int64_t R, int64_t N, int64_t K) {
-  if (R <= 128) return 0;   // stream form
+  if (!tile_form(R, N, 1, false)) return 0;
   const Plan p = tile_plan(R, N, K);
   return p.parts > 1 ? static_cast<size_t>(p.tail) * p.parts * TM * TN * sizeof(float) : 0;
 }
@@ -961,12 +977,20 @@ cudaError_t launch_fp8_block(const Fp8BlockArgs& a, cudaStream_t s) {
   p.status = a.status;
   p.x = static_cast<const uint4*>(a.x);
   p.x_f16 = a.x_f16;
-  // rows a weight tile is used for, on average
-  const int64_t rows = (a.R + a.E - 1) / a.E;
-  if (rows <= 16) return a.x != nullptr ? run_stream<16, true>(a, p, s) : run_stream<16, false>(a, p, s);
-  if (rows <= 32) return run_stream<32, false>(a, p, s);
-  if (rows <= 64) return run_stream<64, false>(a, p, s);
-  if (rows <= 128) return run_stream<128, false>(a, p, s);
+  const bool experts = a.expert_offsets != nullptr;
+  if (!tile_form(a.R, a.N, a.E, experts)) {
+    // The smallest token tile that holds a call's rows, or an expert's on average: at
+    // 11008 x 4096 20 rows take 17.5 us in tiles of 16 and 12.1 in one of 32, 48
+    // rows 18.0 in tiles of 32 and 14.2 in one of 64, while 16 rows take 11.6 and 11.9,
+    // 33 rows 13.8 and (in one of 128) 21; 64 experts of 2816 x 2048 with 12 rows 63.5 in
+    // tiles of 16 and 64.6 of 32, with 20 rows 69.7 and 65.1, with 40 rows 77.7
+    // in tiles of 32 and 70.2 of 64.
+    const int64_t rows = (a.R + a.E - 1) / a.E;
+    if (rows <= 16) return a.x != nullptr ? run_stream<16, true>(a, p, s) : run_stream<16, false>(a, p, s);
+    if (rows <= 32) return run_stream<32, false>(a, p, s);
+    if (rows <= 64) return run_stream<64, false>(a, p, s);
+    return run_stream<128, false>(a, p, s);
+  }
   cudaError_t e = encode(&p.tm_x, a.qx, a.K, a.R, 0, TM);
   if (e != cudaSuccess) return e;
   e = encode(&p.tm_w, a.qweight, a.K, a.N, a.E, TN);
@@ -976,7 +1000,7 @@ cudaError_t launch_fp8_block(const Fp8BlockArgs& a, cudaStream_t s) {
   if (items > kMaxItems) return cudaErrorInvalidConfiguration;
   p.items = p.full = static_cast<int>(items);
   p.parts = 1;
-  const Plan plan = a.expert_offsets == nullptr ? tile_plan(a.R, a.N, a.K) : Plan{0, 0, 1};
+  const Plan plan = experts ? Plan{0, 0, 1} : tile_plan(a.R, a.N, a.K);
   if (plan.parts > 1 && a.part_bytes >= fp8_block_part_bytes(a.R, a.N, a.K)) {
     p.full = static_cast<int>(plan.full);
     p.parts = plan.parts;

@@ -124,7 +124,8 @@ def test_silu_mul_quant_block_far_gates():
     (1, 8, 16), (1, 128, 128), (1, 136, 144), (1, 2056, 1408), (2, 264, 400), (5, 2048, 1408), (16, 520, 2064),
     (17, 384, 1024), (31, 1000, 272), (33, 136, 1552), (64, 2056, 2048), (65, 264, 640), (100, 1032, 4112),
     (128, 128, 128), (129, 8, 16), (129, 264, 144), (200, 520, 1408), (257, 1032, 272), (300, 776, 2064),
-    (513, 2056, 640), (1, 4096, 8208), (640, 10240, 256)])
+    (513, 2056, 640), (1, 4096, 8208), (640, 10240, 256),
+    (64, 9736, 144), (65, 9728, 272), (65, 9736, 144), (128, 9864, 144)])
 @pytest.mark.parametrize("with_bias", [False, True])
 def test_gemm_matches_oracle(M, N, K, with_bias):
     _, q, s = rows(M, K, seed=M + N)
@@ -227,7 +228,7 @@ def test_gemm_empty():
 
 COUNTS = [
     [1], [0, 3, 0], [16, 1, 0, 17, 5], [2] * 40 + [0] * 8, [40, 0, 25, 31], [70, 1, 64, 65], [128, 127, 129, 0, 3],
-    [300, 0, 1, 200], [0, 0, 700], [1000, 0, 0, 0, 0, 0, 0, 1], [0] * 100 + [5] + [0] * 899 + [260],
+    [300, 0, 1, 200], [0, 0, 700], [1000, 0, 0, 0, 0, 0, 0, 1], [56, 56], [57, 56], [0, 113], [112, 0], [0] * 100 + [5] + [0] * 899 + [260],
 ]
 
 
@@ -298,10 +299,11 @@ def test_grouped_bf16in_bad_row():
     check_bf16_output(got, r, "bad rows")
 
 
-@pytest.mark.parametrize("R,T,bad", [(9000, 1000, False), (9000, 1000, True), (9000, 8000, False)])
+@pytest.mark.parametrize("R,T,bad", [(9000, 1000, False), (9000, 1000, True), (9000, 8000, False),
+                                     (33000, 1000, False), (33000, 1000, True), (33000, 16501, False)])
 def test_grouped_bf16in_tokens_quantized_once(R, T, bad):
-    """Many rows of few tokens: the codes are copied from the tokens' (the last case
-    has too many tokens for that); with a workspace that only holds the rows they
+    """Many rows of few tokens: at 33000 rows the codes are copied from the tokens' (the
+    last case has too many tokens for that); with a workspace that only holds the rows they
     are computed again, to the same bits. Rows of bad ids are zero."""
     E, N, K = 4, 136, 528
     x = S.activations_bf16(T, K, seed=5)
@@ -326,7 +328,8 @@ def test_grouped_bf16in_tokens_quantized_once(R, T, bad):
 
 
 @pytest.mark.parametrize("M,N,K,split", [(300, 4096, 2064, False), (700, 776, 4112, True), (2700, 2056, 1808, False),
-                                         (300, 4096, 4112, True), (2700, 2056, 4112, True)])
+                                         (300, 4096, 4112, True), (2700, 2056, 4112, True),
+                                         (65, 9736, 4112, True), (128, 9728, 4112, False)])
 def test_gemm_split_and_whole(M, N, K, split):
     """The last wave's tiles cut along K where that pays, and the same call without
     room for it."""
