@@ -14,7 +14,11 @@
 //    to kFuseRows dense rows the kernel quantizes 16-bit activations itself.
 //  * tile (many rows): 128 tokens on the MMA's rows, 256 outputs on its columns,
 //    so that one scale sx * sw serves a thread's whole column strip. Bound by the
-//    hand-over and drain of one accumulator per block.
+//    hand-over and drain of one accumulator per block: about 920 cycles a block,
+//    of which the barriers' round trip takes some 450, the FMAs 290 (256 are their
+//    issue time) and the reads of tensor memory 100, where its MMAs take 512 and its
+//    48 KB of operands 860; and by 1.8 us a tile in which all SMs write their
+//    outputs at once. 4096 x 11008 x 4096 takes 153 us after its quantizer, 2.4 PFLOP/s.
 //
 // Both are launched as programmatic dependents and let their own dependents go
 // early: the copies of weights start while the kernel before finishes, everything
@@ -81,7 +85,20 @@ W4_DEV float4 ld_cluster_f32x4(uint32_t a, uint32_t rank) {
 // tc::wait by a whole warp with one answer: a warp whose lanes disagreed after a
 // time-out would not meet at its next warp-wide instruction.
 W4_DEV bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned int* status) {
-  return __all_sync(0xFFFFFFFFu, tc::wait(bar, parity, abort, status, kWaitNs));
+  constexpr unsigned kAll = 0xFFFFFFFFu;
+  if (__all_sync(kAll, mbar_try_wait(bar, parity))) return true;
+  const uint64_t t0 = tc::globaltimer_ns();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i)
+      if (__all_sync(kAll, tc::try_wait_suspend(bar, parity, 1000))) return true;
+    if (__any_sync(kAll, *abort != 0)) return false;
+    if (__any_sync(kAll, tc::globaltimer_ns() - t0 > kWaitNs)) {
+      report(status, W4_ERR_TIMEOUT);
+      *abort = 1;
+      return false;
+    }
+  }
 }
 // One lane of a converged warp. Loops that issue copies or MMAs run in the whole
 // warp with one lane issuing: descriptors and addresses stay in uniform registers.
@@ -509,13 +526,18 @@ constexpr int T_A = TM * 128, T_B = TN * 128;
 constexpr int T_STAGES = 4;
 constexpr int T_ACCS = 2;                      // accumulators of 256 columns: all 512 of tensor memory
 constexpr int T_SC_SLOTS = 3;                  // scale slots of 4 blocks x 2 output halves x 128 rows
-constexpr int T_SC_FLOATS = 4 * 2 * TM;
+constexpr int T_SC_ROW = 2 * TM + 8;           // 8 rows x 4 blocks of a slot lie in 32 banks
+constexpr int T_SC_FLOATS = 4 * T_SC_ROW;
 constexpr int T_SC = T_SC_SLOTS * T_SC_FLOATS * 4;
 constexpr int T_OUT = 8 * 32 * 64;             // per epilogue warp, 64 bytes of its 32 rows on their way out
 constexpr int T_SMEM = T_STAGES * (T_A + T_B) + T_SC + T_OUT + 512 + (kMaxExperts + 1 + 12 + 3) / 4 * 16 + 1024;
 static_assert(T_SMEM <= 232448, "shared memory per CTA");
-// Each issuer meets every phase of the stages and the accumulator that it waits on.
-static_assert(T_STAGES % 2 == 0 && T_ACCS == 2, "blocks of one parity keep their stages and accumulator");
+// Blocks go in groups of four: block i of a group has stage i and accumulator i % 2,
+// so that the loops over a group know their barriers, and its scales are one slot. A
+// work item's last group is filled up with blocks that only pass the barriers
+// (counters in place of groups: 4096 x 11008 x 4096 171 us against 163). Every waiter
+// meets every phase of the barriers that it waits on.
+static_assert(T_STAGES == 4 && T_ACCS == 2, "a group of four blocks");
 // Warps 0-7 epilogue (warp w: TMEM lanes 32 (w % 4), outputs 128 (w / 4) ..),
 // 8 copies, 9 scales, 10 and 11 MMA issuers of the even and odd blocks: a
 // thread's MMAs queue behind its own commits, so with two issuers one
@@ -613,19 +635,25 @@ __global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const __grid_constan
       bool ok = true, waited = false;
       Work w;
       for (long long it = blockIdx.x; ok && it < p.items && decode_work(p, it, starts, w, e); it += gridDim.x)
-        for (int kb = w.kb0; kb < w.kb1; ++kb) {
+        for (int kb = w.kb0; kb < w.kb1 || st != 0; ++kb) {
           if (!(ok = wait_warp(&done[st], ph, abort_flag, p.status))) break;
-          if (elect_one()) {
-            mbar_arrive_expect_tx(&full[st], T_A + T_B);
-            tc::tma_load_3d(b_base + st * T_B, &p.tm_w, &full[st], kb * kBlk, w.t.n0, w.t.expert);
+          if (kb >= w.kb1) {
+            if (elect_one()) mbar_arrive(&full[st]);   // a filler
+          } else {
+            if (elect_one()) {
+              mbar_arrive_expect_tx(&full[st], T_A + T_B);
+              tc::tma_load_3d(b_base + st * T_B, &p.tm_w, &full[st], kb * kBlk, w.t.n0, w.t.expert);
+            }
+            if (!waited) grid_dependency_wait();   // the codes come from the kernel before
+            waited = true;
+            if (elect_one()) tc::tma_load_2d(a_base + st * T_A, &p.tm_x, &full[st], kb * kBlk, w.t.row0);
           }
-          if (!waited) grid_dependency_wait();   // the codes come from the kernel before
-          waited = true;
-          if (elect_one()) tc::tma_load_2d(a_base + st * T_A, &p.tm_x, &full[st], kb * kBlk, w.t.row0);
           if (++st == T_STAGES) st = 0, ph ^= 1;
         }
     } else if (warp == kTWarpScale) {
-      // sx * sw of four blocks, both output halves and the tile's 128 rows per slot
+      // sx * sw of four blocks, both output halves and the tile's 128 rows per slot. Lane
+      // l takes block l % 4 of rows l / 4 + 8 j, so that a load reads 8 rows' 16 bytes
+      // (with a lane to a row, 32 sectors: 4096 x 11008 x 4096 177 us against 171).
       grid_dependency_wait();
       int sl = 0, ph = 1, e = 0;
       bool ok = true;
@@ -633,31 +661,27 @@ __global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const __grid_constan
       for (long long it = blockIdx.x; ok && it < p.items && decode_work(p, it, starts, w, e); it += gridDim.x) {
         const Tile& t = w.t;
         const int nb = t.n0 / kBlk;
-        const float* sw0 = p.w_scale + (static_cast<size_t>(t.expert) * p.NB + nb) * KB;
+        const int i = lane & 3, r0 = lane >> 2;
+        const float* sw0 = p.w_scale + (static_cast<size_t>(t.expert) * p.NB + nb) * KB + i;
         const float* sw1 = nb + 1 < p.NB ? sw0 + KB : sw0;
+        const float* sx = p.x_scale + static_cast<size_t>(t.row0 + r0) * KB + i;
+        const int valid = t.row_end - t.row0 - r0;
         for (int kb = w.kb0; kb < w.kb1; kb += 4) {
-          float w0[4], w1[4], x[4][4];
+          const bool in = kb + i < w.kb1;
+          const float w0 = in ? __ldg(sw0 + kb) : 0.f, w1 = in ? __ldg(sw1 + kb) : 0.f;
+          float x[16];
+          const float* at = sx + kb;
+          int down = 8 * KB;
+          asm volatile("" : "+r"(down));   // 16 addresses kept over the loop would not fit the registers
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            w0[i] = kb + i < w.kb1 ? __ldg(sw0 + kb + i) : 0.f;
-            w1[i] = kb + i < w.kb1 ? __ldg(sw1 + kb + i) : 0.f;
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int row = t.row0 + 32 * j + lane;
-            const float* sx = p.x_scale + static_cast<size_t>(row) * KB + kb;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[j][i] = (row < t.row_end && kb + i < w.kb1) ? sx[i] : 0.f;
-          }
+          for (int j = 0; j < 16; ++j, at += down) x[j] = in && 8 * j < valid ? *at : 0.f;
           if (!(ok = wait_warp(&sc_empty[sl], ph, abort_flag, p.status))) break;
-          float* sc = sc_base + sl * T_SC_FLOATS + lane;
+          float* sc = sc_base + sl * T_SC_FLOATS + i * T_SC_ROW + r0;
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              sc[i * 2 * TM + 32 * j] = x[j][i] * w0[i];
-              sc[i * 2 * TM + TM + 32 * j] = x[j][i] * w1[i];
-            }
+          for (int j = 0; j < 16; ++j) {
+            sc[8 * j] = x[j] * w0;
+            sc[TM + 8 * j] = x[j] * w1;
+          }
           __syncwarp();
           if (lane == 0) mbar_arrive(&sc_full[sl]);
           if (++sl == T_SC_SLOTS) sl = 0, ph ^= 1;
@@ -668,26 +692,26 @@ __global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const __grid_constan
       const int mine = warp - kTWarpMma;   // blocks and accumulator of this parity
       constexpr uint32_t idesc = tc::idesc_f16_f32(TM, TN);
       const uint64_t ad0 = tc::sdesc_sw128(smem_addr(a_base)), bd0 = tc::sdesc_sw128(smem_addr(b_base));
-      int st = 0, ph = 0, aph = 1, e = 0;
-      uint32_t g = 0;
+      int ph = 0, e = 0;
       bool ok = true;
       Work w;
       for (long long it = blockIdx.x; ok && it < p.items && decode_work(p, it, starts, w, e); it += gridDim.x)
-        for (int kb = w.kb0; kb < w.kb1; ++kb, ++g) {
-          if (static_cast<int>(g & 1) == mine) {
-            const uint64_t ad = ad0 + static_cast<uint64_t>((st * T_A) >> 4), bd = bd0 + static_cast<uint64_t>((st * T_B) >> 4);
+        for (int kb = w.kb0 + mine; ok && kb < w.kb1 + mine; kb += 4) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int st = 2 * j + mine;
             // the operands are there long before: the accumulator, waited for last, is what holds the MMAs up
             if (!(ok = wait_warp(&full[st], ph, abort_flag, p.status))) break;
-            if (!(ok = wait_warp(&acc_empty[mine], aph, abort_flag, p.status))) break;
+            if (!(ok = wait_warp(&acc_empty[mine], j ^ 1, abort_flag, p.status))) break;
             tc::fence_after_sync();
             if (leader) {
-              mma_block(tmem + mine * TN, ad, bd, idesc);
+              if (kb + 2 * j < w.kb1)
+                mma_block(tmem + mine * TN, ad0 + static_cast<uint64_t>((st * T_A) >> 4), bd0 + static_cast<uint64_t>((st * T_B) >> 4), idesc);
               tc::commit(&done[st]);
             }
             __syncwarp();
-            aph ^= 1;
           }
-          if (++st == T_STAGES) st = 0, ph ^= 1;
+          ph ^= 1;
         }
     }
     __syncwarp();
@@ -696,45 +720,50 @@ __global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const __grid_constan
     const int q = warp & 3, half = warp >> 2;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * q) << 16) + 128 * half;
     const float* sc_mine = sc_base + half * TM + 32 * q + lane;
-    int st = 0, ph = 0, buf = 0, sl = 0, sph = 0, e = 0;
+    int ph = 0, sl = 0, sph = 0, e = 0;
     bool ok = true;
     Work w;
     for (long long it = blockIdx.x; ok && it < p.items && decode_work(p, it, starts, w, e); it += gridDim.x) {
       float T[128];
 #pragma unroll
       for (int j = 0; j < 128; ++j) T[j] = 0.f;
-      for (int kb = w.kb0; kb < w.kb1; ++kb) {
-        const int i = (kb - w.kb0) & 3;
-        if (i == 0 && !(ok = wait_warp(&sc_full[sl], sph, abort_flag, p.status))) break;
-        const float f = sc_mine[sl * T_SC_FLOATS + i * 2 * TM];
-        if (!(ok = wait_warp(&done[st], ph, abort_flag, p.status))) break;
-        tc::fence_after_sync();
-        const uint32_t ta = t_lane + buf * TN;
-        // 16 columns are multiplied while the next 16 load
-        uint32_t v[2][16];
-        tc::tmem_ld16_async(ta, v[0]);
+      for (int kb = w.kb0; ok && kb < w.kb1; kb += 4) {
+        if (!(ok = wait_warp(&sc_full[sl], sph, abort_flag, p.status))) break;
+        float f4[4];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          tc::tmem_wait_ld(v[c & 1]);
-          if (c < 7) {
-            tc::tmem_ld16_async(ta + 16 * (c + 1), v[(c + 1) & 1]);
-          } else {
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) {   // the accumulator is in registers
-              mbar_arrive(&acc_empty[buf]);
-              if (i == 3 || kb == w.kb1 - 1) mbar_arrive(&sc_empty[sl]);
-            }
+        for (int i = 0; i < 4; ++i) f4[i] = sc_mine[sl * T_SC_FLOATS + i * T_SC_ROW];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (!(ok = wait_warp(&done[i], ph, abort_flag, p.status))) break;
+          tc::fence_after_sync();
+          if (kb + i >= w.kb1) {
+            if (lane == 0) mbar_arrive(&acc_empty[i & 1]);   // a filler
+            continue;
           }
+          const uint32_t ta = t_lane + (i & 1) * TN;
+          const float f = f4[i];
+          // 16 columns are multiplied while the next 16 load
+          uint32_t v[2][16];
+          tc::tmem_ld16_async(ta, v[0]);
 #pragma unroll
-          for (int j = 0; j < 16; j += 2)
-            fma2(T[16 * c + j], T[16 * c + j + 1], f, __uint_as_float(v[c & 1][j]), __uint_as_float(v[c & 1][j + 1]));
+          for (int c = 0; c < 8; ++c) {
+            tc::tmem_wait_ld(v[c & 1]);
+            if (c < 7) {
+              tc::tmem_ld16_async(ta + 16 * (c + 1), v[(c + 1) & 1]);
+            } else {
+              tc::fence_before_sync();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&acc_empty[i & 1]);   // the accumulator is in registers
+            }
+#pragma unroll
+            for (int j = 0; j < 16; j += 2)
+              fma2(T[16 * c + j], T[16 * c + j + 1], f, __uint_as_float(v[c & 1][j]), __uint_as_float(v[c & 1][j + 1]));
+          }
         }
-        buf ^= 1;
-        if (++st == T_STAGES) st = 0, ph ^= 1;
-        if (i == 3 || kb == w.kb1 - 1) {
-          if (++sl == T_SC_SLOTS) sl = 0, sph ^= 1;
-        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sc_empty[sl]);
+        ph ^= 1;
+        if (++sl == T_SC_SLOTS) sl = 0, sph ^= 1;
       }
       if (!ok) break;
       const int row0 = w.t.row0 + 32 * q, n0 = w.t.n0 + 128 * half, row_end = w.t.row_end;
@@ -916,11 +945,11 @@ cudaError_t run_stream(const Fp8BlockArgs& a, Params& p, cudaStream_t s) {
 
 // The dense tile form's work: whole waves of whole tiles, and the r tiles of a
 // last, partly filled wave cut along k into as many parts as fit the SMs at once.
-// That takes KB - KB / s blocks of 0.54 us off the last wave and costs about
+// That takes KB - KB / s blocks of 0.48 us off the last wave and costs about
 // kSplitBlocks of them: the sums of 128 KB a part, written and read back, and the
-// join's launch. Measured whole / split: 517 x 11008 x 4096 (r = 63, two parts) 41.1
-// / 37.8 us, 300 x 2048 x 14336 (24, six) 56.4 / 23.0, 700 x 14336 x 8192 (32, four)
-// 108 / 89. More parts than SMs lose: 256 x 11008 x 4096 (86, three) 22.1 / 31.8.
+// join's launch. Measured whole / split: 517 x 11008 x 4096 (r = 63, two parts) 37.2
+// / 34.4 us, 300 x 2048 x 14336 (24, six) 52.2 / 22.6, 700 x 14336 x 8192 (32, four)
+// 99 / 84. More parts than SMs lose: 256 x 11008 x 4096 (86, three) 22.1 / 31.8.
 // The SM count is a GB300's whatever the device, so that the workspace is the same
 // everywhere.
 constexpr int kPlanSms = 152, kSplitBlocks = 12;
