@@ -199,7 +199,8 @@ struct Stream {
   static constexpr int ACCS = TMEM_COLS / NT > 8 ? 8 : TMEM_COLS / NT;
   static constexpr int SC_PER = kQuant ? 1 : 4;          // blocks per scale slot (x NT tokens)
   static constexpr int SC_SLOTS = kQuant ? 8 : 4;
-  static constexpr int SC_BYTES = SC_SLOTS * SC_PER * NT * 4;
+  static constexpr int SC_ROW = kQuant ? NT : NT + 8;    // 8 rows x 4 blocks of a slot lie in 32 banks
+  static constexpr int SC_BYTES = SC_SLOTS * SC_PER * SC_ROW * 4;
   static constexpr int THREADS = kQuant ? 320 : 256;
   static constexpr int SMEM = STAGES * (A_BYTES + B_BYTES) + SC_BYTES + 512 + (kMaxExperts + 1 + 10 + 5) / 4 * 16 + 1024;
 };
@@ -377,31 +378,27 @@ __global__ void __launch_bounds__(Stream<NT, kQuant>::THREADS, Stream<NT, kQuant
     }
     __syncwarp();
   } else if (warp == kSWarpScale) {
-    // sx * sw of four blocks and NT tokens per slot
+    // sx * sw of four blocks and NT tokens per slot; lane l takes block l % 4 of rows
+    // l / 4 + 8 j
     grid_dependency_wait();
     int sl = 0, ph = 1, e = 0;
     bool ok = true;
     Tile t;
     for (int it = first; ok && it < p.items && decode(p, it, NT, kBlk, starts, t, e); it += step) {
-      const float* sw = p.w_scale + (static_cast<size_t>(t.expert) * p.NB + t.n0 / kBlk) * p.KB;
+      const int i = lane & 3, r0 = lane >> 2;
+      const float* sw = p.w_scale + (static_cast<size_t>(t.expert) * p.NB + t.n0 / kBlk) * p.KB + i;
+      const float* sx = p.x_scale + static_cast<size_t>(t.row0 + r0) * p.KB + i;
+      const int valid = t.row_end - t.row0 - r0;
       for (int kb = kb0; kb < kb1; kb += 4) {
-        float w[4];
+        const bool in = kb + i < kb1;
+        const float w = in ? __ldg(sw + kb) : 0.f;
+        float x[NT / 8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = kb + i < kb1 ? __ldg(sw + kb + i) : 0.f;
+        for (int j = 0; j < NT / 8; ++j) x[j] = in && 8 * j < valid ? sx[static_cast<size_t>(8 * j) * p.KB + kb] : 0.f;
         if (!(ok = wait_warp(&sc_empty[sl], ph, abort_flag, p.status))) break;
-        float* sc = sc_base + sl * 4 * NT;
+        float* sc = sc_base + (sl * 4 + i) * C::SC_ROW + r0;
 #pragma unroll
-        for (int j0 = 0; j0 < NT; j0 += 32) {
-          const int j = j0 + lane, row = t.row0 + j;
-          if (NT % 32 == 0 || j < NT) {
-            const float* sx = p.x_scale + static_cast<size_t>(row) * p.KB + kb;
-            float x[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = (row < t.row_end && kb + i < kb1) ? sx[i] : 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sc[i * NT + j] = x[i] * w[i];
-          }
-        }
+        for (int j = 0; j < NT / 8; ++j) sc[8 * j] = x[j] * w;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sc_full[sl]);
         if (++sl == C::SC_SLOTS) sl = 0, ph ^= 1;
@@ -421,7 +418,7 @@ __global__ void __launch_bounds__(Stream<NT, kQuant>::THREADS, Stream<NT, kQuant
         if (!(ok = wait_warp(&acc_full[ac], aph, abort_flag, p.status))) break;
         tc::fence_after_sync();
         const uint32_t ta = tmem + (static_cast<uint32_t>(32 * warp) << 16) + ac * NT;
-        const float* sc = sc_base + (sl * C::SC_PER + i) * NT;
+        const float* sc = sc_base + (sl * C::SC_PER + i) * C::SC_ROW;
         // 16 columns are multiplied while the next 16 load
         uint32_t v[2][16];
         tc::tmem_ld16_async(ta, v[0]);
