@@ -278,34 +278,28 @@ W4_DEV void fma2c(float& d0, float& d1, float a0, float a1, float b, float c0, f
 // bit 2^-48 x, so s >= kRefineMin = 2^-80 is ample. No branch: with the bracket of
 // quant_e4m3_chunk half of all warps met a tie of a bf16 ratio somewhere and paid
 // 8 divides (146 instructions a chunk, against 80).
+// With kSteps = 1 the quotient is within one ulp: for values that are rounded themselves.
 constexpr float kRefineMin = 8.27180613e-25f;
+template <int kSteps>
 W4_DEV uint32_t quotient2_e4m3(float x0, float x1, float s, float r) {
   float q0, q1, e0, e1;
   mul2(q0, q1, x0, x1, r);
-  fma2c(e0, e1, q0, q1, -s, x0, x1);
-  fma2c(q0, q1, e0, e1, r, q0, q1);
-  fma2c(e0, e1, q0, q1, -s, x0, x1);
-  fma2c(q0, q1, e0, e1, r, q0, q1);
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    fma2c(e0, e1, q0, q1, -s, x0, x1);
+    fma2c(q0, q1, e0, e1, r, q0, q1);
+  }
   return e4m3x2_rn(q0, q1);
 }
 
 // The codes of 8 values. s below kRefineMin (a block of values below 4e-22), or
-// not finite, takes the IEEE divide. With kExact off the quotient is fl(x r), within
-// 1.5 ulp of x / s: for values that are known to a few ulp themselves.
-template <bool kExact = true>
+// not finite, takes the IEEE divide.
+template <int kSteps = 2>
 W4_DEV uint2 quant_e4m3_block(const float (&x)[8], float s, float r) {
   uint32_t p[4];
   if (s >= kRefineMin && s < 1e37f) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (kExact) {
-        p[i] = quotient2_e4m3(x[2 * i], x[2 * i + 1], s, r);
-      } else {
-        float q0, q1;
-        mul2(q0, q1, x[2 * i], x[2 * i + 1], r);
-        p[i] = e4m3x2_rn(q0, q1);
-      }
-    }
+    for (int i = 0; i < 4; ++i) p[i] = quotient2_e4m3<kSteps>(x[2 * i], x[2 * i + 1], s, r);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) p[i] = e4m3x2_rn(__fdiv_rn(x[2 * i], s), __fdiv_rn(x[2 * i + 1], s));
