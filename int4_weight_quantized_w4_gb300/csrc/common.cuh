@@ -255,6 +255,12 @@ W4_DEV uint2 quant_e4m3_chunk(const uint4& v, const QuotientBracket& b) {
   return make_uint2(prmt(p[0], p[1], 0x5410u), prmt(p[2], p[3], 0x5410u));
 }
 
+// (d0, d1) = (a0, a1) * (b0, b1) + (c0, c1), packed as fma2.
+W4_DEV void fma2x(float& d0, float& d1, float a0, float a1, float b0, float b1, float c0, float c1) {
+  asm("{.reg .b64 d, x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%6, %7}; "
+      "fma.rn.f32x2 d, x, y, z; mov.b64 {%0, %1}, d;}"
+      : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
 // Per-block quantization: a half-warp holds a block of 128 columns of a row, one
 // chunk of 8 per lane. Scale fl(amax / 448), 1 for a block of zeros.
 W4_DEV float block_scale(float amax) { return amax == 0.f ? 1.f : __fdiv_rn(amax, 448.f); }
@@ -292,12 +298,14 @@ W4_DEV uint32_t quotient2_e4m3(float x0, float x1, float s, float r) {
   return e4m3x2_rn(q0, q1);
 }
 
-// The codes of 8 values. s below kRefineMin (a block of values below 4e-22), or
-// not finite, takes the IEEE divide.
-template <int kSteps = 2>
+// The codes of 8 values x, or with kNegated of -x. s below kRefineMin (a block of
+// values below 4e-22), or not finite, takes the IEEE divide.
+template <int kSteps = 2, bool kNegated = false>
 W4_DEV uint2 quant_e4m3_block(const float (&x)[8], float s, float r) {
   uint32_t p[4];
-  if (s >= kRefineMin && s < 1e37f) {
+  const bool refine = s >= kRefineMin && s < 1e37f;
+  if (kNegated) s = -s, r = -r;
+  if (refine) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) p[i] = quotient2_e4m3<kSteps>(x[2 * i], x[2 * i + 1], s, r);
   } else {

@@ -6,11 +6,12 @@
 //   q = satfinite-rne_e4m3(fl(x / s)).
 // x is a bf16 or fp16 activation, or silu(gate) * up of a bf16 gate_up row,
 // which stays in fp32 up to its one rounding to e4m3 (a bf16 step in between
-// would move a block's scale by up to 2^-8 whenever it moved its maximum), and whose
-// quotient is within one ulp, as the product itself is within a few. Of 369 M codes of
-// normal gates and ups 151 were off where the same formula in IEEE fp32 steps gave
-// the one of fp64, and 121 the other way around; with fl(x r) as the quotient 241 and
-// 160 (2 us less of 40 at 32768 x 1408), with an IEEE-exact gate 63 and 48 (13 us more).
+// would move a block's scale by up to 2^-8 whenever it moved its maximum). The gate is
+// expf and a division that comes out as IEEE's but for rare last bits, and so does
+// x / s: of 369 M codes of normal gates and ups none differed from the formula's in IEEE
+// fp32 steps. Cheaper gates, at 32768 x 1408: ex2.approx in place of expf 48 us against
+// 55, with 48 codes wrong by fp64 where IEEE steps were right and 48 the other way
+// around; the quotient g r unrefined as well 40 us, 151 and 121.
 //
 // A block is 16 chunks of 8 elements: a half-warp holds it in registers, one
 // 16-byte load (two for gate and up) per lane. No row-wide reduction exists, so a
@@ -31,21 +32,22 @@ constexpr int kBlk8 = 16;       // 8-element chunks per block of 128 columns
 constexpr int kThreads = 256;
 constexpr unsigned kFull = 0xFFFFFFFFu;
 
-// silu(g) * u = g / (1 + 2^(-g log2 e)) * u of the bf16 pairs g and u, with the
-// fast exponential and reciprocal (a few ulp). The gate comes before u, so that only
-// the product itself can overflow. Gates below -87.3, whose reciprocal is no normal
-// number, give 0 (silu is above -1.1e-36 there). Multiplications and additions go
-// two at a time.
-W4_DEV void silu_mul2(uint32_t g, uint32_t u, float& a0, float& a1) {
+// -silu(g) * u = -g / (1 + exp(-g)) * u of the bf16 pairs g and u. With d the
+// denominator, r = -1/d approximately and q = g r, the remainder g + d q times r is what
+// q lacks: the quotient comes out within an ulp (the sign saves negations). The gate
+// comes before u, so that only the product itself can overflow. Gates below -87.3, whose
+// 1/d is no normal number, give 0 (silu is above -1.1e-36 there); the remainder's d
+// is held to 2^126, so that they do not meet inf * 0. Everything but exponential and
+// reciprocal goes two at a time.
+W4_DEV void neg_silu_mul2(uint32_t g, uint32_t u, float& a0, float& a1) {
   const float g0 = bf16_lo(g), g1 = bf16_hi(g);
-  float t0, t1;
-  mul2(t0, t1, g0, g1, -1.44269504f);   // -log2(e)
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t0) : "f"(t0));
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t1) : "f"(t1));
-  add2(t0, t1, t0, t1, 1.f);
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t0) : "f"(t0));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t1) : "f"(t1));
-  mul2v(a0, a1, g0, g1, t0, t1);
+  float d0, d1, r0, r1, e0, e1;
+  add2(d0, d1, expf(-g0), expf(-g1), 1.f);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(-d0));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(-d1));
+  mul2v(a0, a1, g0, g1, r0, r1);
+  fma2x(e0, e1, fminf(d0, 8.5070592e37f), fminf(d1, 8.5070592e37f), a0, a1, g0, g1);
+  fma2v(a0, a1, e0, e1, r0, r1);
   mul2v(a0, a1, a0, a1, bf16_lo(u), bf16_hi(u));
 }
 
@@ -53,8 +55,10 @@ W4_DEV void silu_mul2(uint32_t g, uint32_t u, float& a0, float& a1) {
 // gather[r] (gather may be null: row r). An id outside [0, T) gives a zero row
 // with scales 1 and W4_ERR_SHAPE in the status word. KU = ceil(KB / kUnits). late:
 // the next kernel starts only when every kernel before this one is done.
+// Seven silu blocks an SM: 54.6 us at 32768 x 1408, where the compiler's own choice of
+// registers leaves five and 59.8.
 template <bool kF16, bool kSilu, int kUnits>
-__global__ void __launch_bounds__(kThreads) quant_block_kernel(const uint4* __restrict__ x, uint32_t items, int K8,
+__global__ void __launch_bounds__(kThreads, kSilu ? 7 : 1) quant_block_kernel(const uint4* __restrict__ x, uint32_t items, int K8,
                                                                int KB, uint32_t KU, uint2* __restrict__ q,
                                                                float* __restrict__ scale,
                                                                const int32_t* __restrict__ gather, int64_t T,
@@ -93,7 +97,7 @@ __global__ void __launch_bounds__(kThreads) quant_block_kernel(const uint4* __re
       m[i] = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        silu_mul2(g[j], w[j], a[i][2 * j], a[i][2 * j + 1]);
+        neg_silu_mul2(g[j], w[j], a[i][2 * j], a[i][2 * j + 1]);
         m[i] = fmaxf(m[i], fmaxf(fabsf(a[i][2 * j]), fabsf(a[i][2 * j + 1])));
       }
     } else {
@@ -109,7 +113,7 @@ __global__ void __launch_bounds__(kThreads) quant_block_kernel(const uint4* __re
     const int c = c0 + i * kBlk8;
     if (c < K8) {
       if constexpr (kSilu) {
-        qr[c] = quant_e4m3_block<1>(a[i], s, r);
+        qr[c] = quant_e4m3_block<1, true>(a[i], s, r);
       } else {
         float f[8];
         chunk_f32<kF16>(v[i], f);
