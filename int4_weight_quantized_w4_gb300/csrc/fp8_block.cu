@@ -726,11 +726,10 @@ __global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const __grid_constan
       for (int j = 0; j < 128; ++j) T[j] = 0.f;
       for (int kb = w.kb0; ok && kb < w.kb1; kb += 4) {
         if (!(ok = wait_warp(&sc_full[sl], sph, abort_flag, p.status))) break;
-        float f4[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f4[i] = sc_mine[sl * T_SC_FLOATS + i * T_SC_ROW];
+        const float* sc_now = sc_mine + sl * T_SC_FLOATS;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
+          const float f = sc_now[i * T_SC_ROW];
           if (!(ok = wait_warp(&done[i], ph, abort_flag, p.status))) break;
           tc::fence_after_sync();
           if (kb + i >= w.kb1) {
@@ -738,7 +737,6 @@ __global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const __grid_constan
             continue;
           }
           const uint32_t ta = t_lane + (i & 1) * TN;
-          const float f = f4[i];
           // 16 columns are multiplied while the next 16 load
           uint32_t v[2][16];
           tc::tmem_ld16_async(ta, v[0]);
