@@ -912,6 +912,35 @@ cudaError_t start(const Params& p, int64_t grid, int threads, int smem, int clus
   return e;
 }
 
+// Clusters of n CTAs, one an SM, that the device holds at once: they do not cross a
+// group of SMs, so that this is less than the SMs divided by n. Asked once per device
+// and n (any stream kernel would do: the answer counts one CTA an SM for all of them).
+int one_cta_clusters(int n) {
+  using C = Stream<128, false>;
+  static std::atomic<int> known[64][kMaxSplit + 1];   // answer + 1
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return 0;
+  int v = known[dev][n].load(std::memory_order_relaxed);
+  if (v == 0) {
+    PdlLaunch pl(static_cast<unsigned>(n), C::THREADS, C::SMEM, nullptr, n);
+    if (cudaFuncSetAttribute(stream_kernel<128, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&v, stream_kernel<128, false>, &pl.cfg) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    known[dev][n].store(++v, std::memory_order_relaxed);
+  }
+  return v - 1;
+}
+// The same for `ctas` (1 or 2) an SM: with two, a group of S SMs holds 2S / n clusters
+// of n, at least as many as S / ceil(n / 2) and as twice S / n.
+int clusters_held(int n, int ctas) {
+  const int one = one_cta_clusters(n);
+  if (ctas == 1) return one;
+  const int half = n > 2 ? one_cta_clusters((n + 1) / 2) : 0;
+  return half > 2 * one ? half : 2 * one;
+}
+
 template <int NT, bool kQuant>
 cudaError_t run_stream(const Fp8BlockArgs& a, Params& p, cudaStream_t s) {
   using C = Stream<NT, kQuant>;
@@ -924,14 +953,13 @@ cudaError_t run_stream(const Fp8BlockArgs& a, Params& p, cudaStream_t s) {
   if (items > kMaxItems) return cudaErrorInvalidConfiguration;
   p.items = static_cast<int>(items);
   const int64_t slots = static_cast<int64_t>(current_sm_count()) * C::CTAS;
-  // The largest cluster that leaves every part 2.5 blocks on average and all CTAs resident at
-  // once. Clusters of more than 6 with a CTA per SM do not pack: at 128 x 2048 x 8192
-  // 16 of 8 took two rounds, 21.3 us against 13.5 for 16 of 6, while 8 of 8 (100 x
-  // 1024 x 4096) take 7.6 against 8.3.
+  // The largest cluster that leaves every part 2.5 blocks on average and all clusters
+  // resident at once: 16 x 4096 x 4096 takes 11.1 us in clusters of 2 and 8.0 of 8; 16 x
+  // 6144 x 4096 (48 items) 9.2 in clusters of 5, while 48 of 6 take two rounds and 15.9.
   p.split = 1;
   if (a.expert_offsets == nullptr)
     for (int n = kMaxSplit; n > 1 && p.split == 1; --n)
-      if (items * n <= (C::CTAS == 1 && n > 6 ? 96 : slots) && 2 * p.KB >= 5 * n) p.split = n;
+      if (2 * p.KB >= 5 * n && items <= clusters_held(n, C::CTAS)) p.split = n;
   const int64_t grid = p.split > 1 ? items * p.split : (items < slots ? items : slots);
   return start<stream_kernel<NT, kQuant>>(p, grid, C::THREADS, C::SMEM, p.split, s);
 }
@@ -1012,7 +1040,13 @@ cudaError_t launch_fp8_block(const Fp8BlockArgs& a, cudaStream_t s) {
     const int64_t rows = (a.R + a.E - 1) / a.E;
     if (rows <= 16) return a.x != nullptr ? run_stream<16, true>(a, p, s) : run_stream<16, false>(a, p, s);
     if (rows <= 32) return run_stream<32, false>(a, p, s);
-    if (rows <= 64) return run_stream<64, false>(a, p, s);
+    // Above 40 dense rows two tiles of 32, where clusters of 4 have room for them and the
+    // weights, read twice, are few: the join of wide tiles costs more. 64 x 4096 x 4096
+    // 10.1 us against 11.4, 64 x 2048 x 8192 11.0 / 12.2, 40 x 4096 x 4096 10.1 / 9.7, 64 x
+    // 6144 x 4096 (no room) 12.9 / 12.0, 64 x 4096 x 14336 (59 MB) 20.5 / 18.7.
+    const bool twice = !experts && rows > 40 && 2 * ((a.N + kBlk - 1) / kBlk) <= clusters_held(4, Stream<32, false>::CTAS) &&
+                       a.N * a.K <= int64_t{1} << 25;
+    if (rows <= 64) return twice ? run_stream<32, false>(a, p, s) : run_stream<64, false>(a, p, s);
     return run_stream<128, false>(a, p, s);
   }
   cudaError_t e = encode(&p.tm_x, a.qx, a.K, a.R, 0, TM);

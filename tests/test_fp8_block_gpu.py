@@ -125,7 +125,7 @@ def test_silu_mul_quant_block_far_gates():
     (17, 384, 1024), (31, 1000, 272), (33, 136, 1552), (64, 2056, 2048), (65, 264, 640), (100, 1032, 4112),
     (128, 128, 128), (129, 8, 16), (129, 264, 144), (200, 520, 1408), (257, 1032, 272), (300, 776, 2064),
     (513, 2056, 640), (1, 4096, 8208), (640, 10240, 256),
-    (64, 9736, 144), (65, 9728, 272), (65, 9736, 144), (128, 9864, 144)])
+    (64, 9736, 144), (41, 4104, 1408), (64, 1032, 2064), (16, 6144, 2064), (64, 5128, 2064), (65, 9728, 272), (65, 9736, 144), (128, 9864, 144)])
 @pytest.mark.parametrize("with_bias", [False, True])
 def test_gemm_matches_oracle(M, N, K, with_bias):
     _, q, s = rows(M, K, seed=M + N)
