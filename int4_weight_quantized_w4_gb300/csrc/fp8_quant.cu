@@ -9,8 +9,8 @@
 // would move a block's scale by up to 2^-8 whenever it moved its maximum). The gate is
 // expf and a division that comes out as IEEE's but for rare last bits, and so does
 // x / s: of 369 M codes of normal gates and ups none differed from the formula's in IEEE
-// fp32 steps. Cheaper gates, at 32768 x 1408: ex2.approx in place of expf 48 us against
-// 55, with 48 codes wrong by fp64 where IEEE steps were right and 48 the other way
+// fp32 steps. Cheaper gates, at 32768 x 1408 with two blocks a half-warp: ex2.approx in
+// place of expf 48 us against 55, with 48 codes wrong by fp64 where IEEE steps were right and 48 the other way
 // around; the quotient g r unrefined as well 40 us, 151 and 121.
 //
 // A block is 16 chunks of 8 elements: a half-warp holds it in registers, one
@@ -21,8 +21,8 @@
 // half-warp are reduced together, lanes trading one half of their values for the
 // other at each of the first steps, which leaves the maximum of unit l % kUnits
 // in lane l; each lane then divides once, for its unit, and the scales come back
-// by shuffles. 32768 x 2048 bf16 takes 34.5 us (0.86 of copy bandwidth), 4097 x 4096
-// 10.0 (0.74, of which 2 are the launch and the last wave); 32768 x 1408 silu 54.7,
+// by shuffles. 32768 x 2048 bf16 takes 33.8 us (0.88 of copy bandwidth), 4097 x 4096
+// 9.8 (0.76, of which 2 are the launch and the last wave); 32768 x 1408 silu 49.8,
 // bound by instruction issue.
 #include "common.cuh"
 #include "launch.h"
@@ -31,7 +31,7 @@ namespace w4 {
 namespace {
 
 constexpr int kBlk8 = 16;       // 8-element chunks per block of 128 columns
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;    // 4097 x 4096 9.8 us; blocks of 256 threads 10.1
 constexpr unsigned kFull = 0xFFFFFFFFu;
 
 // -silu(g) * u = -g / (1 + exp(-g)) * u of the bf16 pairs g and u. With d the
@@ -57,8 +57,9 @@ W4_DEV void neg_silu_mul2(uint32_t g, uint32_t u, float& a0, float& a1) {
 // gather[r] (gather may be null: row r). An id outside [0, T) gives a zero row
 // with scales 1 and W4_ERR_SHAPE in the status word. KU = ceil(KB / kUnits). late:
 // the next kernel starts only when every kernel before this one is done.
-// Seven silu blocks an SM: 54.6 us at 32768 x 1408, where the compiler's own choice of
-// registers leaves five and 59.8.
+// At least seven silu blocks an SM: 49.8 us at 32768 x 1408 (six 52.4, nine 51.6, ten 56.0,
+// by what the registers leave in flight). Four blocks of 128 columns a half-warp: with two,
+// silu takes 53.5, and the plain quantizer 42.0 at 32768 x 2048 against 34.5 (256 threads).
 template <bool kF16, bool kSilu, int kUnits>
 __global__ void __launch_bounds__(kThreads, kSilu ? 7 : 1) quant_block_kernel(const uint4* __restrict__ x, uint32_t items, int K8,
                                                                int KB, uint32_t KU, uint2* __restrict__ q,
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(kThreads) gather_rows_kernel(const uint4* __re
 
 cudaError_t launch_quant_block(const void* x, bool f16, bool silu, int64_t M, int64_t K, const int32_t* gather,
                                int64_t T, bool late, void* q, float* scale, unsigned int* status, cudaStream_t s) {
-  if (silu) return launch<false, true, 2>(x, M, K, gather, T, late, q, scale, status, s);
+  if (silu) return launch<false, true, 4>(x, M, K, gather, T, late, q, scale, status, s);
   return f16 ? launch<true, false, 4>(x, M, K, gather, T, late, q, scale, status, s)
              : launch<false, false, 4>(x, M, K, gather, T, late, q, scale, status, s);
 }
