@@ -407,6 +407,7 @@ __global__ void __launch_bounds__(Stream<NT, kQuant>::THREADS, Stream<NT, kQuant
       }
     }
   } else {
+    grid_dependency_wait();   // the kernels before may still use y
     int ac = 0, aph = 0, sl = 0, sph = 0, e = 0;
     bool ok = true;
     Tile t;
@@ -716,6 +717,9 @@ __global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const __grid_constan
     __syncwarp();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    // y and the part sums may still be in use by the kernels before: stores wait for
+    // them here, not only through the copies of the codes
+    grid_dependency_wait();
     const int q = warp & 3, half = warp >> 2;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * q) << 16) + 128 * half;
     const float* sc_mine = sc_base + half * TM + 32 * q + lane;
@@ -987,6 +991,7 @@ static Plan tile_plan(int64_t R, int64_t N, int64_t K) {
   if (r == 0) return {tiles, 0, 1};
   int64_t s = kPlanSms / r;
   if (s > 16) s = 16;
+  if (s > KB) s = KB;   // every part has a block
   if (s < 2 || (KB + s - 1) / s + kSplitBlocks >= KB) return {tiles, 0, 1};
   return {tiles - r, r, static_cast<int>(s)};
 }

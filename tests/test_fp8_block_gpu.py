@@ -458,3 +458,24 @@ def test_offsets_past_32_bits():
     torch.cuda.synchronize()
     check_bf16_output(bits(y[M - 2:]), O.fp8_block_linear(rq[:, :128], rs[:, :1], w, ws), "last rows")
     assert w4.w4_device_status() == w4.W4_OK
+
+
+@pytest.mark.parametrize("K", [1680, 1792, 1808, 1920, 2048])
+@pytest.mark.parametrize("N", [256, 1024, 1280])
+def test_gemm_split_into_as_many_parts_as_blocks(N, K):
+    """Few tiles and few blocks: every part holds a block. Two calls in a row share one
+    workspace, so that the second one's parts meet the first one's join."""
+    M = 256
+    _, q, s = rows(M, K, seed=N + K)
+    qw, sw = weights(N, K, seed=K)
+    need = w4.w4_workspace_bytes(w4.W4_OP_FP8_BLOCK, M, N, K, 0)
+    assert need > 0
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    args = fp8(q), to_dev(s), fp8(qw), to_dev(sw)
+    torch.cuda.synchronize()
+    ys = [w4.w4_fp8_block_gemm(*args, workspace=ws) for _ in range(8)]
+    torch.cuda.synchronize()
+    assert w4.w4_device_status() == w4.W4_OK
+    check_bf16_output(bits(ys[0]), O.fp8_block_linear(q, s, qw, sw), "parts")
+    for y in ys[1:]:
+        np.testing.assert_array_equal(bits(y), bits(ys[0]))

@@ -162,3 +162,21 @@ def test_binding_refuses_tensors_that_are_not_on_a_gpu(lib):
         w4.w4_quant_act_per_block(None)
     with pytest.raises(ValueError, match="scoring"):
         w4.w4_moe_route_grouped(t((2, 8)), 2, scoring="relu")
+
+
+def test_every_part_of_a_split_tile_has_a_block(lib):
+    """A tile is cut along K into at most as many parts as K has blocks of 128, over
+    every K up to 4096 and every count of tiles in the last wave."""
+    tile = 128 * 256 * 4
+    split = 0
+    for K in range(16, 4097, 16):
+        blocks = -(-K // 128)
+        for pairs in range(1, 77):
+            need = lib.w4_workspace_bytes(w4.W4_OP_FP8_BLOCK, 256, 256 * pairs, K, 0)
+            if need == 0:
+                continue
+            tiles = 2 * pairs % 152
+            parts, rest = divmod(need, tiles * tile)
+            assert rest == 0 and 2 <= parts <= min(16, blocks), (K, pairs, parts)
+            split += 1
+    assert split > 1000
