@@ -10,6 +10,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -77,6 +78,37 @@ const at::Tensor& ranked(PyObject* o, const char* name, const Types& types, cons
   return t;
 }
 
+// The stream of a call: the `stream` argument (a handle), or the current one of `dev`
+// for None. For as long as this lives `dev` is the current device and, where the two
+// streams differ, the call's is the current stream: memory allocated here belongs to
+// the stream that the kernels run on, so it is neither still in use by other work when
+// they write it nor handed to other work while they read it.
+class CallStream {
+ public:
+  CallStream(PyObject* o, const at::Device& dev) : device_(dev), caller_(c10::cuda::getCurrentCUDAStream(dev.index())) {
+    handle_ = caller_.stream();
+    if (o == Py_None) return;
+    cudaStream_t s = static_cast<cudaStream_t>(PyLong_AsVoidPtr(o));
+    if (s == nullptr && PyErr_Occurred()) throw python_error();
+    if (s == handle_) return;
+    handle_ = s;
+    stream_.reset_stream(c10::cuda::getStreamFromExternal(s, dev.index()));
+  }
+  cudaStream_t handle() const { return handle_; }
+  // Outputs are read on the caller's stream too (once it has waited): released there,
+  // they are not handed out again before that stream is done with them.
+  void keep_for_caller(const at::Tensor& t) const {
+    if (handle_ != caller_.stream() && t.nbytes() > 0)
+      c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), caller_);
+  }
+
+ private:
+  c10::cuda::CUDAGuard device_;
+  c10::cuda::OptionalCUDAStreamGuard stream_;
+  c10::cuda::CUDAStream caller_;
+  cudaStream_t handle_;
+};
+
 at::Tensor empty(at::IntArrayRef shape, ScalarType type, const at::Device& dev) {
   return at::detail::empty_cuda(shape, type, dev, std::nullopt);
 }
@@ -92,8 +124,11 @@ at::Tensor words_of(const at::Tensor& base, int64_t at, at::IntArrayRef shape, S
 }
 
 at::Tensor output(PyObject* o, const char* name, at::IntArrayRef shape, ScalarType type, const Types& types,
-                  const at::Device& dev) {
-  return o == Py_None ? empty(shape, type, dev) : tensor(o, name, types, dev, shape);
+                  const at::Device& dev, const CallStream& stream) {
+  if (o != Py_None) return tensor(o, name, types, dev, shape);
+  at::Tensor t = empty(shape, type, dev);
+  stream.keep_for_caller(t);
+  return t;
 }
 
 struct Scratch {
@@ -101,6 +136,7 @@ struct Scratch {
   void* p = nullptr;
   size_t bytes = 0;
 };
+// Allocated, where none is given, while the call's CallStream lives.
 Scratch scratch(PyObject* o, int32_t op, int64_t M, int64_t N, int64_t K, int32_t group, const at::Device& dev) {
   Scratch s;
   if (o == Py_None) {
@@ -115,13 +151,6 @@ Scratch scratch(PyObject* o, int32_t op, int64_t M, int64_t N, int64_t K, int32_
     s.bytes = s.t.nbytes();   // the library checks it
   }
   s.p = s.t.data_ptr();
-  return s;
-}
-
-void* stream_of(PyObject* o, const at::Device& dev) {
-  if (o == Py_None) return c10::cuda::getCurrentCUDAStream(dev.index()).stream();
-  void* s = PyLong_AsVoidPtr(o);
-  if (s == nullptr && PyErr_Occurred()) throw python_error();
   return s;
 }
 
@@ -202,7 +231,7 @@ PyObject* route_grouped(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const double scale = PyFloat_AsDouble(a[7]);
   if (scale == -1.0 && PyErr_Occurred()) return nullptr;
   if (a[2] != Py_None) tensor(a[2], "bias", kF32, dev, {E});
-  const c10::cuda::CUDAGuard guard(dev);
+  const CallStream stream(a[10], dev);
   at::Tensor o[5];
   const char* names[5] = {"topk_ids", "topk_weights", "offsets", "row_token", "row_of"};
   if (a[8] != Py_None && (!PyTuple_Check(a[8]) || PyTuple_GET_SIZE(a[8]) != 5))
@@ -210,7 +239,10 @@ PyObject* route_grouped(PyObject*, PyObject* const* a, Py_ssize_t n) {
   // the five outputs share one allocation when none are given
   const int64_t starts[5] = {0, T * k, 4 * T * k, 2 * T * k, 3 * T * k};
   at::Tensor all;
-  if (a[8] == Py_None) all = empty({4 * T * k + E + 1}, ScalarType::Int, dev);
+  if (a[8] == Py_None) {
+    all = empty({4 * T * k + E + 1}, ScalarType::Int, dev);
+    stream.keep_for_caller(all);
+  }
   for (int i = 0; i < 5; ++i) {
     const at::DimVector shape = i == 2 ? at::DimVector{E + 1} : i == 3 ? at::DimVector{T * k} : at::DimVector{T, k};
     const ScalarType type = i == 1 ? ScalarType::Float : ScalarType::Int;
@@ -225,7 +257,7 @@ PyObject* route_grouped(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                   static_cast<int32_t>(E), k, groups, keep, integer32(a[5], "scoring"),
                                   PyObject_IsTrue(a[6]), static_cast<float>(scale), i32(o[0]),
                                   static_cast<float*>(o[1].data_ptr()), i32(o[2]), i32(o[3]), i32(o[4]), s.p, s.bytes,
-                                  stream_of(a[10], dev)),
+                                  stream.handle()),
              "w4_moe_route_grouped"))
     return nullptr;
   if (a[8] != Py_None) {
@@ -246,11 +278,11 @@ PyObject* quant_block(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Tensor& x = ranked(a[0], "x", kAct, nullptr, 2);
   const at::Device dev = x.device();
   const int64_t M = x.size(0), K = x.size(1);
-  const c10::cuda::CUDAGuard guard(dev);
-  const at::Tensor q = output(a[1], "q", {M, K}, ScalarType::Float8_e4m3fn, kFp8, dev);
-  const at::Tensor s = output(a[2], "scale", {M, blocks(K)}, ScalarType::Float, kF32, dev);
+  const CallStream stream(a[3], dev);
+  const at::Tensor q = output(a[1], "q", {M, K}, ScalarType::Float8_e4m3fn, kFp8, dev, stream);
+  const at::Tensor s = output(a[2], "scale", {M, blocks(K)}, ScalarType::Float, kF32, dev, stream);
   if (failed(w4_quant_act_per_block(x.data_ptr(), act_dtype(x), M, K, q.data_ptr(), static_cast<float*>(s.data_ptr()),
-                                    stream_of(a[3], dev)),
+                                    stream.handle()),
              "w4_quant_act_per_block"))
     return nullptr;
   return pair(q, s);
@@ -265,11 +297,11 @@ PyObject* silu_mul_quant_block(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Device dev = h.device();
   if (h.size(1) % 2) value_error("h must hold gate and up halves of equal width");
   const int64_t R = h.size(0), I = h.size(1) / 2;
-  const c10::cuda::CUDAGuard guard(dev);
-  const at::Tensor q = output(a[1], "q", {R, I}, ScalarType::Float8_e4m3fn, kFp8, dev);
-  const at::Tensor s = output(a[2], "scale", {R, blocks(I)}, ScalarType::Float, kF32, dev);
+  const CallStream stream(a[3], dev);
+  const at::Tensor q = output(a[1], "q", {R, I}, ScalarType::Float8_e4m3fn, kFp8, dev, stream);
+  const at::Tensor s = output(a[2], "scale", {R, blocks(I)}, ScalarType::Float, kF32, dev, stream);
   if (failed(w4_silu_mul_quant_block(h.data_ptr(), R, I, q.data_ptr(), static_cast<float*>(s.data_ptr()),
-                                     stream_of(a[3], dev)),
+                                     stream.handle()),
              "w4_silu_mul_quant_block"))
     return nullptr;
   return pair(q, s);
@@ -284,11 +316,11 @@ PyObject* gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Device dev = x.device();
   const int64_t M = x.size(0), K = x.size(1), N = dense_weights(a[2], a[3], a[4], K, dev);
   const at::Tensor& xs = tensor(a[1], "x_scale", kF32, dev, {M, blocks(K)});
-  const c10::cuda::CUDAGuard guard(dev);
-  const at::Tensor y = output(a[5], "y", {M, N}, ScalarType::BFloat16, kBf16, dev);
+  const CallStream stream(a[7], dev);
+  const at::Tensor y = output(a[5], "y", {M, N}, ScalarType::BFloat16, kBf16, dev, stream);
   const Scratch s = scratch(a[6], W4_OP_FP8_BLOCK, M, N, K, 0, dev);
   if (failed(w4_fp8_block_gemm(x.data_ptr(), f32(xs), data(a[2]), static_cast<const float*>(data(a[3])), data(a[4]),
-                               y.data_ptr(), M, N, K, s.p, s.bytes, stream_of(a[7], dev)),
+                               y.data_ptr(), M, N, K, s.p, s.bytes, stream.handle()),
              "w4_fp8_block_gemm"))
     return nullptr;
   return THPVariable_Wrap(y);
@@ -302,11 +334,11 @@ PyObject* gemm_act(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Tensor& x = ranked(a[0], "x", kAct, nullptr, 2);
   const at::Device dev = x.device();
   const int64_t M = x.size(0), K = x.size(1), N = dense_weights(a[1], a[2], a[3], K, dev);
-  const c10::cuda::CUDAGuard guard(dev);
-  const at::Tensor y = output(a[4], "y", {M, N}, ScalarType::BFloat16, kBf16, dev);
+  const CallStream stream(a[6], dev);
+  const at::Tensor y = output(a[4], "y", {M, N}, ScalarType::BFloat16, kBf16, dev, stream);
   const Scratch s = scratch(a[5], W4_OP_FP8_BLOCK_IN, M, N, K, 0, dev);
   if (failed(w4_fp8_block_gemm_bf16in(x.data_ptr(), act_dtype(x), data(a[1]), static_cast<const float*>(data(a[2])),
-                                      data(a[3]), y.data_ptr(), M, N, K, s.p, s.bytes, stream_of(a[6], dev)),
+                                      data(a[3]), y.data_ptr(), M, N, K, s.p, s.bytes, stream.handle()),
              "w4_fp8_block_gemm_bf16in"))
     return nullptr;
   return THPVariable_Wrap(y);
@@ -321,12 +353,12 @@ PyObject* moe_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Device dev = x.device();
   const int64_t R = x.size(0), K = x.size(1), N = expert_weights(a[3], a[4], a[2], K, dev);
   const at::Tensor& xs = tensor(a[1], "x_scale", kF32, dev, {R, blocks(K)});
-  const c10::cuda::CUDAGuard guard(dev);
-  const at::Tensor y = output(a[5], "y", {R, N}, ScalarType::BFloat16, kBf16, dev);
+  const CallStream stream(a[6], dev);
+  const at::Tensor y = output(a[5], "y", {R, N}, ScalarType::BFloat16, kBf16, dev, stream);
   if (failed(w4_fp8_block_moe_grouped_gemm(x.data_ptr(), f32(xs), static_cast<const int32_t*>(data(a[2])),
                                            static_cast<int32_t>(THPVariable_Unpack(a[3]).size(0)), data(a[3]),
                                            static_cast<const float*>(data(a[4])), y.data_ptr(), R, N, K,
-                                           stream_of(a[6], dev)),
+                                           stream.handle()),
              "w4_fp8_block_moe_grouped_gemm"))
     return nullptr;
   return THPVariable_Wrap(y);
@@ -342,13 +374,13 @@ PyObject* moe_gemm_act(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t T = x.size(0), K = x.size(1), N = expert_weights(a[3], a[4], a[2], K, dev);
   const int64_t R = a[1] == Py_None ? T : tensor(a[1], "row_token", kI32, &dev).numel();
   const int32_t E = static_cast<int32_t>(THPVariable_Unpack(a[3]).size(0));
-  const c10::cuda::CUDAGuard guard(dev);
-  const at::Tensor y = output(a[5], "y", {R, N}, ScalarType::BFloat16, kBf16, dev);
+  const CallStream stream(a[7], dev);
+  const at::Tensor y = output(a[5], "y", {R, N}, ScalarType::BFloat16, kBf16, dev, stream);
   const Scratch s = scratch(a[6], W4_OP_FP8_BLOCK_IN, R, N, K, E, dev);
   if (failed(w4_fp8_block_moe_gemm_bf16in(x.data_ptr(), T, static_cast<const int32_t*>(data(a[1])),
                                           static_cast<const int32_t*>(data(a[2])), E, data(a[3]),
                                           static_cast<const float*>(data(a[4])), y.data_ptr(), R, N, K, s.p, s.bytes,
-                                          stream_of(a[7], dev)),
+                                          stream.handle()),
              "w4_fp8_block_moe_gemm_bf16in"))
     return nullptr;
   return THPVariable_Wrap(y);
