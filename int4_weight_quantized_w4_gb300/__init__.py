@@ -115,6 +115,37 @@ def _stream(stream, device):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _side(stream, device):
+    """``stream`` as a PyTorch stream where it is not the current one of ``device``, else None."""
+    if stream is None or stream.cuda_stream == torch.cuda.current_stream(device).cuda_stream:
+        return None
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    if not stream.cuda_stream:
+        return torch.cuda.default_stream(device)
+    return torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+
+
+def _on(side):
+    return contextlib.nullcontext() if side is None else torch.cuda.stream(side)
+
+
+def _empty(shape, dtype, device, stream, scratch=False, zero=False):
+    """Memory for a call on ``stream``. It belongs to that stream, so that it is neither
+    in use by other work when the call's kernels write it nor handed to other work while
+    they use it. An output (not ``scratch``) is read on the current stream too: released
+    there, it is not handed out again before that stream is done with it."""
+    make = torch.zeros if zero else torch.empty
+    side = _side(stream, device)
+    if side is None:
+        return make(shape, dtype=dtype, device=device)
+    with _on(side):
+        t = make(shape, dtype=dtype, device=device)
+    if not scratch:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -169,10 +200,10 @@ def w4_workspace_bytes(op: int, M: int, N: int, K: int, group: int) -> int:
     return int(load().w4_workspace_bytes(op, M, N, K, group))
 
 
-def _workspace(ws, op, M, N, K, group, device):
+def _workspace(ws, op, M, N, K, group, device, stream):
     need = w4_workspace_bytes(op, M, N, K, group)
     if ws is None:
-        ws = torch.empty((max(need, 16),), dtype=torch.uint8, device=device)
+        ws = _empty((max(need, 16),), torch.uint8, device, stream, scratch=True)
     _expect(ws, "workspace", None, None, device)   # the library checks its size in bytes
     return ws, ws.numel() * ws.element_size()
 
@@ -223,8 +254,8 @@ def w4_quant_act_per_token(x, q_dtype: str = "int8", q=None, scale=None, stream=
         qd, tdt = W4_FP8_E4M3, torch.float8_e4m3fn
     else:
         raise ValueError("q_dtype must be 'int8' or 'fp8'")
-    q = torch.empty((M, K), dtype=tdt, device=x.device) if q is None else q
-    scale = torch.empty((M,), dtype=torch.float32, device=x.device) if scale is None else scale
+    q = _empty((M, K), tdt, x.device, stream) if q is None else q
+    scale = _empty((M,), torch.float32, x.device, stream) if scale is None else scale
     _expect(q, "q", (M, K), (torch.int8,) if qd == W4_INT8 else _FP8_T, x.device)
     _expect(scale, "scale", (M,), _F32, x.device)
     xd = W4_FP16 if x.dtype == torch.float16 else W4_BF16
@@ -241,9 +272,9 @@ def w4a8_gemm(qx, x_scale, qweight, w_scale, group: int, bias=None, y=None, work
     M, K = qx.shape
     N = _dense_weight_args("w4a8_gemm", qweight, w_scale, K, group, qx.device, bias=bias)
     _expect(x_scale, "x_scale", (M,), _F32, qx.device)
-    y = torch.empty((M, N), dtype=torch.bfloat16, device=qx.device) if y is None else y
+    y = _empty((M, N), torch.bfloat16, qx.device, stream) if y is None else y
     _expect(y, "y", (M, N), _BF16T, qx.device)
-    ws, wsb = _workspace(workspace, W4_OP_W4A8, M, N, K, group, qx.device)
+    ws, wsb = _workspace(workspace, W4_OP_W4A8, M, N, K, group, qx.device, stream)
     _check(load().w4a8_gemm(_ptr(qx), _ptr(x_scale), _ptr(qweight), _ptr(w_scale), _scale_dtype(w_scale),
                             group, _ptr(bias), _ptr(y), M, N, K, _ptr(ws), wsb, _stream(stream, qx.device)),
            "w4a8_gemm")
@@ -256,11 +287,11 @@ def w4a8_gemm_bf16in(x, qweight, w_scale, group: int, bias=None, y=None, x_scale
     _cuda2d(x, "x", (torch.bfloat16,))
     M, K = x.shape
     N = _dense_weight_args("w4a8_gemm_bf16in", qweight, w_scale, K, group, x.device, bias=bias)
-    y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device) if y is None else y
-    x_scale = torch.empty((M,), dtype=torch.float32, device=x.device) if x_scale is None else x_scale
+    y = _empty((M, N), torch.bfloat16, x.device, stream) if y is None else y
+    x_scale = _empty((M,), torch.float32, x.device, stream) if x_scale is None else x_scale
     _expect(y, "y", (M, N), _BF16T, x.device)
     _expect(x_scale, "x_scale", (M,), _F32, x.device)
-    ws, wsb = _workspace(workspace, W4_OP_W4A8, M, N, K, group, x.device)
+    ws, wsb = _workspace(workspace, W4_OP_W4A8, M, N, K, group, x.device, stream)
     _check(load().w4a8_gemm_bf16in(_ptr(x), _ptr(qweight), _ptr(w_scale), _scale_dtype(w_scale), group, _ptr(bias),
                                    _ptr(y), _ptr(x_scale), M, N, K, _ptr(ws), wsb, _stream(stream, x.device)),
            "w4a8_gemm_bf16in")
@@ -276,7 +307,7 @@ def w4a8_gemm_noalloc(qx, x_scale, qweight, w_scale, group: int, bias=None, y=No
     M, K = qx.shape
     N = _dense_weight_args("w4a8_gemm_noalloc", qweight, w_scale, K, group, qx.device, bias=bias)
     _expect(x_scale, "x_scale", (M,), _F32, qx.device)
-    y = torch.empty((M, N), dtype=torch.bfloat16, device=qx.device) if y is None else y
+    y = _empty((M, N), torch.bfloat16, qx.device, stream) if y is None else y
     _expect(y, "y", (M, N), _BF16T, qx.device)
     # the built-in workspace is looked up on the current device: make qx's current
     with torch.cuda.device(qx.device) if qx.device.type == "cuda" else contextlib.nullcontext():
@@ -296,9 +327,9 @@ def w4a8_group_partials(qx, qweight, group: int, out=None, workspace=None, strea
         raise ValueError("inconsistent shapes for w4a8_group_partials")
     _expect(qweight, "qweight", None, None, qx.device)
     G = _groups(K, group)
-    out = torch.empty((M, G or 0, N), dtype=torch.int32, device=qx.device) if out is None else out
+    out = _empty((M, G or 0, N), torch.int32, qx.device, stream) if out is None else out
     _expect(out, "out", None if G is None else (M, G, N), _I32T, qx.device)
-    ws, wsb = _workspace(workspace, W4_OP_W4A8, M, N, K, group, qx.device)
+    ws, wsb = _workspace(workspace, W4_OP_W4A8, M, N, K, group, qx.device, stream)
     _check(load().w4a8_group_partials(_ptr(qx), _ptr(qweight), group, _ptr(out), M, N, K, _ptr(ws), wsb,
                                       _stream(stream, qx.device)), "w4a8_group_partials")
     return out
@@ -310,7 +341,7 @@ def w4a16_gemm(x, qweight, w_scale, group: int, zeros=None, bias=None, y=None, s
     _cuda2d(x, "x", (torch.bfloat16,))
     M, K = x.shape
     N = _dense_weight_args("w4a16_gemm", qweight, w_scale, K, group, x.device, zeros=zeros, bias=bias)
-    y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device) if y is None else y
+    y = _empty((M, N), torch.bfloat16, x.device, stream) if y is None else y
     _expect(y, "y", (M, N), _BF16T, x.device)
     _check(load().w4a16_gemm(_ptr(x), _ptr(qweight), _ptr(w_scale), _scale_dtype(w_scale), _ptr(zeros), group,
                              _ptr(bias), _ptr(y), M, N, K, _stream(stream, x.device)), "w4a16_gemm")
@@ -347,9 +378,9 @@ def w4afp8_moe_grouped_gemm(qx, x_scale, expert_offsets, qweight, w_scale, group
     R, K = qx.shape
     E, N = _expert_weight_args("w4afp8_moe_grouped_gemm", qweight, w_scale, expert_offsets, K, group, qx.device)
     _expect(x_scale, "x_scale", (R,), _F32, qx.device)
-    y = torch.empty((R, N), dtype=torch.bfloat16, device=qx.device) if y is None else y
+    y = _empty((R, N), torch.bfloat16, qx.device, stream) if y is None else y
     _expect(y, "y", (R, N), _BF16T, qx.device)
-    ws, wsb = _workspace(workspace, W4_OP_W4AFP8_MOE, R, N, K, group, qx.device)
+    ws, wsb = _workspace(workspace, W4_OP_W4AFP8_MOE, R, N, K, group, qx.device, stream)
     _check(load().w4afp8_moe_grouped_gemm(_ptr(qx), _ptr(x_scale), _ptr(expert_offsets), E, _ptr(qweight),
                                           _ptr(w_scale), _scale_dtype(w_scale), group, _ptr(y), R, N, K,
                                           _ptr(ws), wsb, _stream(stream, qx.device)), "w4afp8_moe_grouped_gemm")
@@ -365,18 +396,18 @@ def w4_moe_route(logits, top_k: int, renormalize: bool = False, out=None, worksp
     T, E = logits.shape
     dev = logits.device
     if out is None:
-        out = (torch.empty((T, top_k), dtype=torch.int32, device=dev),
-               torch.empty((T, top_k), dtype=torch.float32, device=dev),
-               torch.zeros((E + 1,), dtype=torch.int32, device=dev),
-               torch.empty((T * top_k,), dtype=torch.int32, device=dev),
-               torch.empty((T, top_k), dtype=torch.int32, device=dev))
+        out = (_empty((T, top_k), torch.int32, dev, stream),
+               _empty((T, top_k), torch.float32, dev, stream),
+               _empty((E + 1,), torch.int32, dev, stream, zero=True),
+               _empty((T * top_k,), torch.int32, dev, stream),
+               _empty((T, top_k), torch.int32, dev, stream))
     ids, wts, off, rt, ro = out
     _expect(ids, "topk_ids", (T, top_k), _I32T, dev)
     _expect(wts, "topk_weights", (T, top_k), _F32, dev)
     _expect(off, "offsets", (E + 1,), _I32T, dev)
     _expect(rt, "row_token", (T * top_k,), _I32T, dev)
     _expect(ro, "row_of", (T, top_k), _I32T, dev)
-    ws, wsb = _workspace(workspace, W4_OP_MOE_ROUTE, T, E, 1, 0, dev)
+    ws, wsb = _workspace(workspace, W4_OP_MOE_ROUTE, T, E, 1, 0, dev, stream)
     _check(load().w4_moe_route(_ptr(logits), int(logits.dtype == torch.float32), T, E, top_k, int(bool(renormalize)),
                                _ptr(ids), _ptr(wts), _ptr(off), _ptr(rt), _ptr(ro), _ptr(ws), wsb,
                                _stream(stream, dev)), "w4_moe_route")
@@ -469,8 +500,8 @@ def w4_moe_gather_quant_fp8(x, row_token, q=None, scale=None, stream=None):
     T, K = x.shape
     _expect(row_token, "row_token", None, _I32T, x.device)
     R = row_token.numel()
-    q = torch.empty((R, K), dtype=torch.float8_e4m3fn, device=x.device) if q is None else q
-    scale = torch.empty((R,), dtype=torch.float32, device=x.device) if scale is None else scale
+    q = _empty((R, K), torch.float8_e4m3fn, x.device, stream) if q is None else q
+    scale = _empty((R,), torch.float32, x.device, stream) if scale is None else scale
     _expect(q, "q", (R, K), _FP8_T, x.device)
     _expect(scale, "scale", (R,), _F32, x.device)
     _check(load().w4_moe_gather_quant_fp8(_ptr(x), T, K, _ptr(row_token), R, _ptr(q), _ptr(scale),
@@ -488,11 +519,11 @@ def w4afp8_moe_gemm_bf16in(x, row_token, expert_offsets, qweight, w_scale, group
     _expect(row_token, "row_token", None, _I32T, x.device, optional=True)
     R = T if row_token is None else row_token.numel()
     E, N = _expert_weight_args("w4afp8_moe_gemm_bf16in", qweight, w_scale, expert_offsets, K, group, x.device)
-    y = torch.empty((R, N), dtype=torch.bfloat16, device=x.device) if y is None else y
-    x_scale = torch.empty((R,), dtype=torch.float32, device=x.device) if x_scale is None else x_scale
+    y = _empty((R, N), torch.bfloat16, x.device, stream) if y is None else y
+    x_scale = _empty((R,), torch.float32, x.device, stream) if x_scale is None else x_scale
     _expect(y, "y", (R, N), _BF16T, x.device)
     _expect(x_scale, "x_scale", (R,), _F32, x.device)
-    ws, wsb = _workspace(workspace, W4_OP_W4AFP8_MOE, R, N, K, group, x.device)
+    ws, wsb = _workspace(workspace, W4_OP_W4AFP8_MOE, R, N, K, group, x.device, stream)
     _check(load().w4afp8_moe_gemm_bf16in(_ptr(x), T, _ptr(row_token), _ptr(expert_offsets), E, _ptr(qweight),
                                          _ptr(w_scale), _scale_dtype(w_scale), group, _ptr(y), _ptr(x_scale), R, N,
                                          K, _ptr(ws), wsb, _stream(stream, x.device)), "w4afp8_moe_gemm_bf16in")
@@ -508,8 +539,8 @@ def w4_moe_silu_mul_quant_fp8(h, q=None, scale=None, act=None, stream=None):
     if I2 % 2:
         raise ValueError("h must hold gate and up halves of equal width")
     I = I2 // 2
-    q = torch.empty((R, I), dtype=torch.float8_e4m3fn, device=h.device) if q is None else q
-    scale = torch.empty((R,), dtype=torch.float32, device=h.device) if scale is None else scale
+    q = _empty((R, I), torch.float8_e4m3fn, h.device, stream) if q is None else q
+    scale = _empty((R,), torch.float32, h.device, stream) if scale is None else scale
     _expect(q, "q", (R, I), _FP8_T, h.device)
     _expect(scale, "scale", (R,), _F32, h.device)
     _expect(act, "act", (R, I), _BF16T, h.device, optional=True)
@@ -527,7 +558,7 @@ def w4_moe_combine(y, topk_weights, row_of, out=None, stream=None):
     T, k = row_of.shape
     _expect(row_of, "row_of", None, None, y.device)
     _expect(topk_weights, "topk_weights", (T, k), _F32, y.device)
-    out = torch.empty((T, H), dtype=torch.bfloat16, device=y.device) if out is None else out
+    out = _empty((T, H), torch.bfloat16, y.device, stream) if out is None else out
     _expect(out, "out", (T, H), _BF16T, y.device)
     _check(load().w4_moe_combine(_ptr(y), R, H, _ptr(topk_weights), _ptr(row_of), T, k, _ptr(out),
                                  _stream(stream, y.device)), "w4_moe_combine")
@@ -540,9 +571,9 @@ def w4_quantize_groupwise(w, group: int, packed=None, scale=None, zero=None, str
     _cuda2d(w, "w", (torch.bfloat16, torch.float16))
     N, K = w.shape
     G = 1 if group == -1 else (K // group if group > 0 else 0)
-    packed = torch.empty((N, K // 2), dtype=torch.uint8, device=w.device) if packed is None else packed
-    scale = torch.empty((N, G), dtype=torch.float32, device=w.device) if scale is None else scale
-    zero = torch.empty((N, G), dtype=torch.float32, device=w.device) if zero is None else zero
+    packed = _empty((N, K // 2), torch.uint8, w.device, stream) if packed is None else packed
+    scale = _empty((N, G), torch.float32, w.device, stream) if scale is None else scale
+    zero = _empty((N, G), torch.float32, w.device, stream) if zero is None else zero
     _expect(packed, "packed", (N, K // 2), (torch.uint8,), w.device)
     gshape = (N, G) if _groups(K, group) is not None else None
     _expect(scale, "scale", gshape, _F32, w.device)
@@ -558,7 +589,7 @@ def w4_repack_s4_to_uint4b8(src, dst=None, stream=None):
     XOR 0x88 on every byte; ``dst`` may be ``src`` (in place)."""
     if not src.is_cuda or not src.is_contiguous():
         raise ValueError("src must be a contiguous CUDA tensor")
-    dst = torch.empty_like(src) if dst is None else dst
+    dst = _empty(src.shape, src.dtype, src.device, stream) if dst is None else dst
     n = src.numel() * src.element_size()
     if dst.numel() * dst.element_size() != n:
         raise ValueError("dst must hold as many bytes as src")
@@ -586,7 +617,7 @@ def w4_embedding_gather(ids, table, scale, zero, group: int, out=None, stream=No
     V, D = _table_args(table, scale, zero, group)
     _expect(ids, "ids", None, _I32T, table.device)
     T = ids.numel()
-    out = torch.empty((T, D), dtype=torch.bfloat16, device=table.device) if out is None else out
+    out = _empty((T, D), torch.bfloat16, table.device, stream) if out is None else out
     _expect(out, "out", (T, D), _BF16T, table.device)
     _check(load().w4_embedding_gather(_ptr(ids), T, _ptr(table), _ptr(scale), _ptr(zero), V, D, group, _ptr(out),
                                       _stream(stream, table.device)), "w4_embedding_gather")
@@ -602,7 +633,7 @@ def w4_lm_head_gemv(h, table, scale, zero, group: int, y=None, stream=None):
     if Dt != D:
         raise ValueError("table and h disagree on D")
     _expect(h, "h", None, None, table.device)
-    y = torch.empty((M, V), dtype=torch.bfloat16, device=h.device) if y is None else y
+    y = _empty((M, V), torch.bfloat16, h.device, stream) if y is None else y
     _expect(y, "y", (M, V), _BF16T, h.device)
     _check(load().w4_lm_head_gemv(_ptr(h), M, _ptr(table), _ptr(scale), _ptr(zero), V, D, group, _ptr(y),
                                   _stream(stream, h.device)), "w4_lm_head_gemv")
@@ -626,7 +657,8 @@ def apply_weights(x, qweight, w_scale, group: int, bias=None, zeros=None, stream
     zeros.
     """
     K = x.shape[-1]
-    x2 = x.reshape(-1, K)
+    with _on(_side(stream, x.device)):   # a copy, where x is not contiguous
+        x2 = x.reshape(-1, K)
     M = x2.shape[0]
     int8_path = x2.dtype == torch.float16 or (M >= MIN_TOKENS_FOR_INT8 and zeros is None
                                               and w_scale.dtype == torch.float16)

@@ -107,3 +107,39 @@ def test_outputs_of_a_call_on_another_stream_read_on_the_current_one():
         w4.w4_fp8_block_gemm_bf16in(b, wd, sd, stream=side)
     torch.cuda.synchronize()
     np.testing.assert_array_equal(bits(copy), bits(ref))
+
+
+def test_scratch_of_the_int4_layers_on_another_stream():
+    M, N, K, g, E = 300, 520, 1024, 128, 4
+    xb = S.activations_bf16(M, K, seed=1)
+    x = bf16(xb)
+    qw, sw = to_dev(S.random_words((K // 8, N), seed=2)), to_dev(S.scales_f16((K // g, N), seed=3))
+    qe, se = to_dev(S.random_words((E, N, K // 8), seed=4)), to_dev(S.scales_f16((E, N, K // g), seed=5))
+    off = to_dev(np.array([0, 100, 100, 290, M], np.int32))
+    lg = to_dev(S.router_logits(5000, 64, seed=6))
+    need = w4.w4_workspace_bytes(w4.W4_OP_W4A8, M, N, K, g)
+    ref, ref_s = w4.w4a8_gemm_bf16in(x, qw, sw, g)
+    y, s = on_side_stream(lambda st: w4.w4a8_gemm_bf16in(x, qw, sw, g, stream=st), [need, 2 * M * N, 4 * M])
+    np.testing.assert_array_equal(bits(y), bits(ref))
+    np.testing.assert_array_equal(s.cpu().numpy(), ref_s.cpu().numpy())
+    need = w4.w4_workspace_bytes(w4.W4_OP_W4AFP8_MOE, M, N, K, g)
+    ref, _ = w4.w4afp8_moe_gemm_bf16in(x, None, off, qe, se, g)
+    y, _ = on_side_stream(lambda st: w4.w4afp8_moe_gemm_bf16in(x, None, off, qe, se, g, stream=st), [need, 2 * M * N, 4 * M])
+    np.testing.assert_array_equal(bits(y), bits(ref))
+    need = w4.w4_workspace_bytes(w4.W4_OP_MOE_ROUTE, 5000, 64, 1, 0)
+    ref = w4.w4_moe_route(lg, 6)
+    out = on_side_stream(lambda st: w4.w4_moe_route(lg, 6, stream=st), [need, 4 * 5000 * 6, 4 * 65])
+    for a, b in zip(out, ref):
+        np.testing.assert_array_equal(a.cpu().numpy(), b.cpu().numpy())
+    # a layer whose activations are a transposed view of what the side stream makes
+    side = torch.cuda.Stream()
+    made = torch.zeros((2, M // 2, K), dtype=torch.bfloat16, device="cuda")
+    src = x.view(2, M // 2, K)
+    ref = w4.apply_weights(src.transpose(0, 1).contiguous(), qw, sw, g)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(int(40e6))
+        made.copy_(src)
+    y = w4.apply_weights(made.transpose(0, 1), qw, sw, g, stream=side)
+    torch.cuda.synchronize()
+    np.testing.assert_array_equal(bits(y), bits(ref))
