@@ -479,3 +479,37 @@ def test_gemm_split_into_as_many_parts_as_blocks(N, K):
     check_bf16_output(bits(ys[0]), O.fp8_block_linear(q, s, qw, sw), "parts")
     for y in ys[1:]:
         np.testing.assert_array_equal(bits(y), bits(ys[0]))
+
+
+@pytest.mark.parametrize("f16", [False, True])
+def test_quant_per_block_zeros_keep_their_sign(f16):
+    """-0 and +0 among ordinary values, alone in a block (scale 1), and beside values so
+    small that their block takes the divide."""
+    M, K = 6, 520
+    v = S.bf16_bits_to_f32(S.activations_bf16(M, K, seed=4)).astype(np.float32)
+    zero = S.raw_u64(5, 1, M * K).reshape(M, K) % 4
+    v[zero == 0], v[zero == 1] = -0.0, 0.0
+    v[2, 128:256] = -0.0
+    v[3, :128] = np.where(zero[3, :128] < 2, v[3, :128], np.float32(2.0 ** -24) if f16 else np.float32(1e-30))
+    v[4, 512:] = [-0.0, 1.0, -0.0, 0.0, -1.0, -0.0, 3.0, 0.0]
+    x = v.astype(np.float16) if f16 else S.to_bf16_bits(v)
+    q, s = w4.w4_quant_act_per_block(to_dev(x) if f16 else bf16(x))
+    torch.cuda.synchronize()
+    rq, rs = O.quant_fp8_per_block(x)
+    assert (rq == 0x80).sum() > M * K // 8 and (rq == 0).sum() > M * K // 8
+    np.testing.assert_array_equal(s.cpu().numpy(), rs)
+    np.testing.assert_array_equal(codes(q), rq)
+
+
+def test_silu_mul_quant_block_zeros_keep_their_sign():
+    """-0 and +0 as gates and as ups: the sign is the product's."""
+    g = np.array([-0.0, 0.0, 1.0, -1.0, -0.0, 0.0, 2.0, 1.0], np.float32)
+    u = np.array([1.0, -1.0, -0.0, 0.0, -1.0, 1.0, 0.5, 0.0], np.float32)
+    for scale in (1.0, 1e-30):                       # and in a block that takes the divide
+        h = np.concatenate([np.tile(g, 17), np.tile(u * np.float32(scale), 17)])[None]
+        q, _ = w4.w4_silu_mul_quant_block(bf16(S.to_bf16_bits(h)))
+        torch.cuda.synchronize()
+        got = codes(q).reshape(17, 8)
+        np.testing.assert_array_equal(got[:, [0, 1, 2, 3]], 0x80)
+        np.testing.assert_array_equal(got[:, [4, 5, 7]], 0)
+        np.testing.assert_array_equal(got[:, 6], 0x7E)
