@@ -413,9 +413,10 @@ w4_status w4_quant_act_per_block(const void* x, int32_t x_dtype, int64_t M, int6
 /*
  * w4_silu_mul_quant_block: h [R, 2I] bf16 (gate columns first) -> the codes and
  * scales of silu(gate) * up, quantized as by w4_quant_act_per_block. The product
- * stays in fp32 up to its rounding to e4m3, and each of its steps is within an fp32
- * ulp or two. Gates below -87.3 give 0. q [R, I], scale [R, ceil(I/128)];
- * I % 8 == 0; h and q 16-byte aligned.
+ * stays in fp32 up to its rounding to e4m3. It is within a few fp32 ulp of the
+ * definition as far as fp32 reaches (a gate of -100 times a large up is not 0), of a
+ * gate below -64 within 8. A gate of +inf gives an infinite product, -inf NaN.
+ * q [R, I], scale [R, ceil(I/128)]; I % 8 == 0; h and q 16-byte aligned.
  */
 w4_status w4_silu_mul_quant_block(const void* h, int64_t R, int64_t I, void* q, float* scale, void* stream);
 

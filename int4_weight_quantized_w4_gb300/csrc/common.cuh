@@ -309,20 +309,27 @@ W4_DEV uint32_t quotient2_e4m3(float x0, float x1, float s, float r) {
   return e4m3x2_rn(q0, q1);
 }
 
-// The codes of 8 values x, or with kNegated of -x. s below kRefineMin (a block of
-// values below 4e-22), or not finite, takes the IEEE divide.
+// Whether s takes the refinement: not below kRefineMin (a block of values below 4e-22), and finite.
+W4_DEV bool scale_refines(float s) { return s >= kRefineMin && s < 1e37f; }
+
+// The codes of 8 values x, or with kNegated of -x, where scale_refines(s).
+template <int kSteps = 2, bool kNegated = false>
+W4_DEV uint2 quant_e4m3_refined(const float (&x)[8], float s, float r) {
+  uint32_t p[4];
+  if (kNegated) s = -s, r = -r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p[i] = quotient2_e4m3<kSteps, kNegated>(x[2 * i], x[2 * i + 1], s, r);
+  return make_uint2(prmt(p[0], p[1], 0x5410u), prmt(p[2], p[3], 0x5410u));
+}
+
+// The same for any s: out of that range by the IEEE divide.
 template <int kSteps = 2, bool kNegated = false>
 W4_DEV uint2 quant_e4m3_block(const float (&x)[8], float s, float r) {
+  if (scale_refines(s)) return quant_e4m3_refined<kSteps, kNegated>(x, s, r);
+  if (kNegated) s = -s;
   uint32_t p[4];
-  const bool refine = s >= kRefineMin && s < 1e37f;
-  if (kNegated) s = -s, r = -r;
-  if (refine) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = quotient2_e4m3<kSteps, kNegated>(x[2 * i], x[2 * i + 1], s, r);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = e4m3x2_rn(__fdiv_rn(x[2 * i], s), __fdiv_rn(x[2 * i + 1], s));
-  }
+  for (int i = 0; i < 4; ++i) p[i] = e4m3x2_rn(__fdiv_rn(x[2 * i], s), __fdiv_rn(x[2 * i + 1], s));
   return make_uint2(prmt(p[0], p[1], 0x5410u), prmt(p[2], p[3], 0x5410u));
 }
 
@@ -342,23 +349,32 @@ W4_DEV void chunk_f32(const uint4& v, float (&x)[8]) {
   }
 }
 
+// The larger of two numbers; kNaN: NaN where either is (fmaxf drops it).
+template <bool kNaN>
+W4_DEV float max_of(float a, float b) {
+  if constexpr (!kNaN) return fmaxf(a, b);
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 // The maxima of kUnits blocks over the half-warp, reduced together: lanes trade one
 // half of their values for the other at each of the first steps, which leaves the
 // maximum of block u in the lanes with lane % kUnits == u.
-template <int kUnits>
+template <int kUnits, bool kNaN = false>
 W4_DEV float unit_max(const float (&m)[kUnits]) {
   static_assert(kUnits == 2 || kUnits == 4, "one lane bit per halving");
   const int lane = threadIdx.x & 31;
   const bool b0 = lane & 1, b1 = lane & 2;
-  float z = fmaxf(b0 ? m[1] : m[0], __shfl_xor_sync(0xffffffffu, b0 ? m[0] : m[1], 1));
+  float z = max_of<kNaN>(b0 ? m[1] : m[0], __shfl_xor_sync(0xffffffffu, b0 ? m[0] : m[1], 1));
   if constexpr (kUnits == 4) {
-    const float y = fmaxf(b0 ? m[3] : m[2], __shfl_xor_sync(0xffffffffu, b0 ? m[2] : m[3], 1));
-    z = fmaxf(b1 ? y : z, __shfl_xor_sync(0xffffffffu, b1 ? z : y, 2));
+    const float y = max_of<kNaN>(b0 ? m[3] : m[2], __shfl_xor_sync(0xffffffffu, b0 ? m[2] : m[3], 1));
+    z = max_of<kNaN>(b1 ? y : z, __shfl_xor_sync(0xffffffffu, b1 ? z : y, 2));
   } else {
-    z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 2));
+    z = max_of<kNaN>(z, __shfl_xor_sync(0xffffffffu, z, 2));
   }
-  z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 4));
-  return fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 8));
+  z = max_of<kNaN>(z, __shfl_xor_sync(0xffffffffu, z, 4));
+  return max_of<kNaN>(z, __shfl_xor_sync(0xffffffffu, z, 8));
 }
 
 // This lane's codes and the scale of one block. Every lane of the warp takes part.

@@ -9,9 +9,9 @@
 // would move a block's scale by up to 2^-8 whenever it moved its maximum). The gate is
 // expf and a division that comes out as IEEE's but for rare last bits, and so does
 // x / s: of 369 M codes of normal gates and ups none differed from the formula's in IEEE
-// fp32 steps. Cheaper gates, at 32768 x 1408 with two blocks a half-warp: ex2.approx in
-// place of expf 48 us against 55, with 48 codes wrong by fp64 where IEEE steps were right and 48 the other way
-// around; the quotient g r unrefined as well 40 us, 151 and 121.
+// fp32 steps. Cheaper gates measured 13 to 28% less time and made codes wrong by fp64
+// where IEEE steps were right (and as many the other way around): ex2.approx in place of
+// expf 48 of the 369 M, the quotient g r unrefined as well 151.
 //
 // A block is 16 chunks of 8 elements: a half-warp holds it in registers, one
 // 16-byte load (two for gate and up) per lane. No row-wide reduction exists, so a
@@ -22,7 +22,7 @@
 // other at each of the first steps, which leaves the maximum of unit l % kUnits
 // in lane l; each lane then divides once, for its unit, and the scales come back
 // by shuffles. 32768 x 2048 bf16 takes 33.8 us (0.88 of copy bandwidth), 4097 x 4096
-// 9.8 (0.76, of which 2 are the launch and the last wave); 32768 x 1408 silu 49.8,
+// 9.8 (0.76, of which 2 are the launch and the last wave); 32768 x 1408 silu 45.8,
 // bound by instruction issue.
 #include "common.cuh"
 #include "launch.h"
@@ -34,30 +34,43 @@ constexpr int kBlk8 = 16;       // 8-element chunks per block of 128 columns
 constexpr int kThreads = 128;    // 4097 x 4096 9.8 us; blocks of 256 threads 10.1
 constexpr unsigned kFull = 0xFFFFFFFFu;
 
-// -silu(g) * u = -g / (1 + exp(-g)) * u of the bf16 pairs g and u. With d the
-// denominator, r = -1/d approximately and q = g r, the remainder g + d q times r is what
-// q lacks: the quotient comes out within an ulp (the sign saves negations). The gate
-// comes before u, so that only the product itself can overflow. Gates below -87.3, whose
-// 1/d is no normal number, give 0 (silu is above -1.1e-36 there); the remainder's d
-// is held to 2^126, so that they do not meet inf * 0. Everything but exponential and
-// reciprocal goes two at a time.
-W4_DEV void neg_silu_mul2(uint32_t g, uint32_t u, float& a0, float& a1) {
+// -4 silu(g) * u = -g / D * u of the bf16 pairs g and u, D = (1 + exp(-g)) / 4: a
+// quarter, whose reciprocal is a normal number for every finite D. With r = -1/D
+// approximately and q = g r, the remainder g + D q times r is what q lacks: the quotient
+// comes out within an ulp (the signs save negations). The gate comes before u, so that
+// only the product itself can overflow. Where D is infinite (gates below -88.7) or the
+// gate is, the remainder is NaN, and a product beyond a quarter of the largest fp32 is
+// infinite or NaN: the caller sees that in the block's maximum. Everything but
+// exponential and reciprocal goes two at a time.
+W4_DEV void neg_silu4_mul2(uint32_t g, uint32_t u, float& a0, float& a1) {
   const float g0 = bf16_lo(g), g1 = bf16_hi(g);
   float d0, d1, r0, r1, e0, e1;
-  add2(d0, d1, expf(-g0), expf(-g1), 1.f);
+  fma2c(d0, d1, expf(-g0), expf(-g1), 0.25f, 0.25f, 0.25f);
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(-d0));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(-d1));
   mul2v(a0, a1, g0, g1, r0, r1);
-  fma2x(e0, e1, fminf(d0, 8.5070592e37f), fminf(d1, 8.5070592e37f), a0, a1, g0, g1);
+  fma2x(e0, e1, d0, d1, a0, a1, g0, g1);
   fma2v(a0, a1, e0, e1, r0, r1);
   mul2v(a0, a1, a0, a1, bf16_lo(u), bf16_hi(u));
+}
+// -silu(g) * u of any gate. Far below zero the denominator overflows long before the
+// product with a large u vanishes: there silu(g) = g exp(g), whose exponential is taken in
+// four factors, two on either side of u, so that an underflow before the end is one of the
+// product itself (gates down to -180 at the largest u; within 8 ulp). A gate of +inf
+// follows the formula, -inf gives NaN.
+W4_DEV float neg_silu_mul(float g, float u) {
+  if (g < -64.f) {
+    const float h = expf(0.25f * g);
+    return -(g * h * h * u * h * h);
+  }
+  return -(__fdiv_rn(g, 1.f + expf(-g)) * u);
 }
 
 // x [*, K8 chunks], or with kSilu [*, 2 K8]; row r of the output comes from row
 // gather[r] (gather may be null: row r). An id outside [0, T) gives a zero row
 // with scales 1 and W4_ERR_SHAPE in the status word. KU = ceil(KB / kUnits). late:
 // the next kernel starts only when every kernel before this one is done.
-// At least seven silu blocks an SM: 49.8 us at 32768 x 1408 (six 52.4, nine 51.6, ten 56.0,
+// At least seven silu blocks an SM: 45.8 us at 32768 x 1408 (six 47.0, eight 45.5,
 // by what the registers leave in flight). Four blocks of 128 columns a half-warp: with two,
 // silu takes 53.5, and the plain quantizer 42.0 at 32768 x 2048 against 34.5 (256 threads).
 template <bool kF16, bool kSilu, int kUnits>
@@ -100,27 +113,61 @@ __global__ void __launch_bounds__(kThreads, kSilu ? 7 : 1) quant_block_kernel(co
       m[i] = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        neg_silu_mul2(g[j], w[j], a[i][2 * j], a[i][2 * j + 1]);
-        m[i] = fmaxf(m[i], fmaxf(fabsf(a[i][2 * j]), fabsf(a[i][2 * j + 1])));
+        neg_silu4_mul2(g[j], w[j], a[i][2 * j], a[i][2 * j + 1]);
+        m[i] = max_of<true>(m[i], max_of<true>(fabsf(a[i][2 * j]), fabsf(a[i][2 * j + 1])));
       }
     } else {
       m[i] = chunk_max<kF16>(v[i]);
     }
   }
-  const float s_mine = block_scale(unit_max<kUnits>(m)), r_mine = __frcp_rn(s_mine);   // of block b0 + l % kUnits
-  if (l < kUnits && live && b0 + l < KB) scale[static_cast<size_t>(row) * KB + b0 + l] = s_mine;
   uint2* qr = q + static_cast<size_t>(row) * K8;
+  float* sr = scale + static_cast<size_t>(row) * KB + b0;
+  // lane l holds scale and reciprocal of block b0 + l % kUnits (silu: of four times its products)
+  const float amax = unit_max<kUnits, kSilu>(m);
+  const float s_mine = kSilu && amax == 0.f ? 4.f : block_scale(amax), r_mine = __frcp_rn(s_mine);
+  if (l < kUnits && live && b0 + l < KB) sr[l] = kSilu ? 0.25f * s_mine : s_mine;
 #pragma unroll
   for (int i = 0; i < kUnits; ++i) {
     const float s = __shfl_sync(kFull, s_mine, i, kBlk8), r = __shfl_sync(kFull, r_mine, i, kBlk8);
     const int c = c0 + i * kBlk8;
     if (c < K8) {
       if constexpr (kSilu) {
-        qr[c] = quant_e4m3_block<1, true>(a[i], s, r);
+        qr[c] = quant_e4m3_refined<1, true>(a[i], s, r);
       } else {
         float f[8];
         chunk_f32<kF16>(v[i], f);
         qr[c] = quant_e4m3_block(f, s, r);
+      }
+    }
+  }
+  if constexpr (kSilu) {
+    // A block whose scale is out of range (far or infinite gates, NaN, tiny or huge
+    // products) is rare: it is read, computed and written once more. Its branch stands
+    // apart, so that the arithmetic above overlaps as if it were not there (far gates
+    // looked for and mended between products and maximum 48.8 us, before the products 50.3).
+    const bool again = !scale_refines(s_mine);
+    if (__any_sync(kFull, again)) {
+#pragma unroll 1
+      for (int i = 0; i < kUnits; ++i) {
+        const int c = c0 + i * kBlk8;
+        const bool in = c < K8;
+        const uint4 gv = in ? ld_stream_v4(xr + c) : make_uint4(0, 0, 0, 0);
+        const uint4 uv = in ? ld_stream_v4(xr + K8 + c) : make_uint4(0, 0, 0, 0);
+        const uint32_t g[4] = {gv.x, gv.y, gv.z, gv.w}, w[4] = {uv.x, uv.y, uv.z, uv.w};
+        float f[8], fm = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          f[2 * j] = neg_silu_mul(bf16_lo(g[j]), bf16_lo(w[j]));
+          f[2 * j + 1] = neg_silu_mul(bf16_hi(g[j]), bf16_hi(w[j]));
+          fm = fmaxf(fm, fmaxf(fabsf(f[2 * j]), fabsf(f[2 * j + 1])));
+        }
+#pragma unroll
+        for (int o = kBlk8 / 2; o > 0; o >>= 1) fm = fmaxf(fm, __shfl_xor_sync(kFull, fm, o));
+        if (__shfl_sync(kFull, again, i, kBlk8) && in) {
+          const float s = block_scale(fm);
+          qr[c] = quant_e4m3_block<1, true>(f, s, __frcp_rn(s));
+          if (l == 0) sr[i] = s;
+        }
       }
     }
   }

@@ -513,3 +513,42 @@ def test_silu_mul_quant_block_zeros_keep_their_sign():
         np.testing.assert_array_equal(got[:, [0, 1, 2, 3]], 0x80)
         np.testing.assert_array_equal(got[:, [4, 5, 7]], 0)
         np.testing.assert_array_equal(got[:, 6], 0x7E)
+
+
+@pytest.mark.parametrize("up", [1e38, -3e38, 1e20])
+def test_silu_mul_quant_block_far_gates_times_large_ups(up):
+    """Products that fp32 holds although 1 + exp(-gate) overflows: scales within 2^-19 of the
+    definition's, codes at most a step off and almost all equal. Near and far gates share chunks."""
+    low = -175.0 if abs(up) > 1e30 else -130.0
+    g = np.linspace(low, -60.0, 1024).astype(np.float32)
+    g[5::16] = 3.0
+    h = S.to_bf16_bits(np.concatenate([g, np.full(1024, up, np.float32)])[None].repeat(2, 0))
+    h[1, :1024] = S.to_bf16_bits(np.linspace(low, -87.5, 1024).astype(np.float32))      # far ones alone
+    h[1, 1024:] = S.to_bf16_bits(np.full(1024, up, np.float32))
+    h[0, 1024 + 5:2048:16] = S.to_bf16_bits(np.float32([1.0]))[0]
+    act = O.silu_mul_f64(h)
+    q, s = w4.w4_silu_mul_quant_block(bf16(h))
+    torch.cuda.synchronize()
+    blocks = act.reshape(2, 8, 128)
+    rs = np.abs(blocks).max(axis=2) / 448
+    assert rs.min() > 1e-36
+    np.testing.assert_allclose(s.cpu().numpy(), rs, rtol=2.0 ** -19)
+    ref = O.e4m3_encode((blocks / rs[:, :, None]).reshape(2, 1024)).astype(np.int64)
+    got = codes(q).astype(np.int64)
+    step = np.abs((ref & 0x7F) - (got & 0x7F))
+    assert ((ref ^ got) & 0x80 == 0).all() and step.max() <= 1 and (step != 0).sum() <= 2
+
+
+def test_silu_mul_quant_block_infinite_gate():
+    """silu(inf) = inf: the block's scale is infinite, its finite products have code 0; other
+    blocks are as without it."""
+    h = S.activations_bf16(2, 512, seed=3)
+    h[1] = h[0]
+    h[1, 7], h[1, 256 + 7] = 0x7F80, 0x3F80
+    q, s = w4.w4_silu_mul_quant_block(bf16(h))
+    torch.cuda.synchronize()
+    c, s = codes(q), s.cpu().numpy()
+    assert np.isposinf(s[1, 0]) and c[1, 7] == 0x7F
+    assert (np.delete(c[1, :128], 7) & 0x7F == 0).all()
+    np.testing.assert_array_equal(c[1, 128:], c[0, 128:])
+    assert s[1, 1] == s[0, 1]
