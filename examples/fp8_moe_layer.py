@@ -67,8 +67,8 @@ def quantize_weight(w: torch.Tensor) -> Fp8Weight:
     p = torch.zeros((*lead, nb * 128, kb * 128), dtype=torch.float32, device=w.device)
     p[..., :N, :K] = w
     p = p.view(*lead, nb, 128, kb, 128)
-    amax = p.abs().amax(dim=(-3, -1))
-    s = torch.where(amax == 0, torch.ones_like(amax), amax / 448.0)
+    s = p.abs().amax(dim=(-3, -1)) / 448.0
+    s = torch.where(s == 0, torch.ones_like(s), s)
     q = (p / s[..., :, None, :, None]).clamp(-448.0, 448.0).to(torch.float8_e4m3fn)
     q = q.view(torch.uint8).reshape(*lead, nb * 128, kb * 128)[..., :N, :K].contiguous()
     return Fp8Weight(q.view(torch.float8_e4m3fn), s)

@@ -402,7 +402,7 @@ w4_status w4_moe_route_grouped(const void* logits, int32_t logits_f32, const flo
  * dependents early.
  *
  * w4_quant_act_per_block: per row and block of 128 columns (the last one may be
- * shorter) amax = max |x|, s = amax / 448 in fp32 (1 where amax is 0),
+ * shorter) amax = max |x|, s = amax / 448 in fp32 (1 where that is 0),
  * q = e4m3(fl(x / s)), round to nearest even, saturating; the divides are IEEE.
  *   x [M, K] bf16 or fp16 (x_dtype), 16-byte aligned; K % 8 == 0
  *   q [M, K] e4m3 codes, 16-byte aligned; scale [M, ceil(K/128)] fp32

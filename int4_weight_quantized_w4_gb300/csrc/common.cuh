@@ -262,8 +262,12 @@ W4_DEV void fma2x(float& d0, float& d1, float a0, float a1, float b0, float b1, 
       : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
 }
 // Per-block quantization: a half-warp holds a block of 128 columns of a row, one
-// chunk of 8 per lane. Scale fl(amax / 448), 1 for a block of zeros.
-W4_DEV float block_scale(float amax) { return amax == 0.f ? 1.f : __fdiv_rn(amax, 448.f); }
+// chunk of 8 per lane. Scale fl(amax / 448), 1 where that is 0: for a block of zeros,
+// and for fp32 values below 3e-43, whose zeros would give the code of 0 / 0.
+W4_DEV float block_scale(float amax) {
+  const float s = __fdiv_rn(amax, 448.f);
+  return s == 0.f ? 1.f : s;
+}
 
 // (d0, d1) = (a0, a1) * b + (c0, c1), packed as fma2; kDown: rounded down.
 template <bool kDown = false>

@@ -2,7 +2,7 @@
 // fp32 scale per row and 128 columns.
 //
 // Per row and block b of 128 columns (the last one may be shorter):
-//   amax = max |x|;  s = amax / 448 (IEEE fp32 divide; s = 1 where amax = 0);
+//   amax = max |x|;  s = amax / 448 (IEEE fp32 divide; s = 1 where that is 0);
 //   q = satfinite-rne_e4m3(fl(x / s)).
 // x is a bf16 or fp16 activation, or silu(gate) * up of a bf16 gate_up row,
 // which stays in fp32 up to its one rounding to e4m3 (a bf16 step in between
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, kSilu ? 7 : 1) quant_block_kernel(co
   float* sr = scale + static_cast<size_t>(row) * KB + b0;
   // lane l holds scale and reciprocal of block b0 + l % kUnits (silu: of four times its products)
   const float amax = unit_max<kUnits, kSilu>(m);
-  const float s_mine = kSilu && amax == 0.f ? 4.f : block_scale(amax), r_mine = __frcp_rn(s_mine);
+  const float s_mine = !kSilu ? block_scale(amax) : amax == 0.f ? 4.f : __fdiv_rn(amax, 448.f), r_mine = __frcp_rn(s_mine);
   if (l < kUnits && live && b0 + l < KB) sr[l] = kSilu ? 0.25f * s_mine : s_mine;
 #pragma unroll
   for (int i = 0; i < kUnits; ++i) {

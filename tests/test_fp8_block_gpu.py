@@ -552,3 +552,21 @@ def test_silu_mul_quant_block_infinite_gate():
     assert (np.delete(c[1, :128], 7) & 0x7F == 0).all()
     np.testing.assert_array_equal(c[1, 128:], c[0, 128:])
     assert s[1, 1] == s[0, 1]
+
+
+def test_silu_mul_quant_block_products_below_any_scale():
+    """A block whose largest product is not 0 but vanishes in fp32 when divided by 448 has
+    scale 1 and codes 0, zeros among its products too; a product with it stays finite."""
+    g = np.full((1, 256), -60.0, np.float32)
+    u = np.full((1, 256), 1e-20, np.float32)          # 60 exp(-60) 1e-20 = 5e-45
+    u[0, ::3] = 0.0
+    u[0, 128:] = 1.0                                  # a second, ordinary block
+    h = S.to_bf16_bits(np.concatenate([g, u], axis=1))
+    assert 0 < np.abs(O.silu_mul_f64(h)[0, :128]).max() / 448 < 2.0 ** -150
+    q, s = w4.w4_silu_mul_quant_block(bf16(h))
+    qw, sw = weights(136, 256, seed=1)
+    y = w4.w4_fp8_block_gemm(q, s, fp8(qw), to_dev(sw))
+    torch.cuda.synchronize()
+    assert s.cpu().numpy()[0, 0] == 1 and (codes(q)[0, :128] & 0x7F == 0).all()
+    assert (codes(q)[0, 128:] & 0x7F == 0x7E).all()
+    assert torch.isfinite(y).all()
