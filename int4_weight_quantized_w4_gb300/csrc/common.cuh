@@ -439,6 +439,16 @@ W4_DEV uint4 ld_cg_v4(const void* p) {
   return v;
 }
 
+// 16-byte streaming load that keeps nothing in L1, of data that another grid may have
+// written while this one was already running (the .nc loads above want data that
+// nothing writes for as long as the kernel runs).
+W4_DEV uint4 ld_once_v4(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+  return v;
+}
+
 W4_DEV uint2 ld_nc_v2(const void* p) {
   uint2 v;
   asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));

@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(Stream<NT, kQuant>::THREADS, Stream<NT, kQuant
       const int total = first < p.items ? (p.items - first + step - 1) / step * nkb : 0;
       auto load = [&](int g, int r) {
         const int c = (kb0 + g % nkb) * 16 + l;
-        return r < p.rows && c < K8 && g < total ? ld_nc_v4(p.x + static_cast<size_t>(r) * K8 + c) : make_uint4(0, 0, 0, 0);
+        return r < p.rows && c < K8 && g < total ? p.x[static_cast<size_t>(r) * K8 + c] : make_uint4(0, 0, 0, 0);
       };
       uint4 x[4];
       grid_dependency_wait();   // x comes from the kernel before
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(Stream<NT, kQuant>::THREADS, Stream<NT, kQuant
       for (int g = warp - kSWarpB; g < total; g += kQuantWarps) {
         const int kb = kb0 + g % nkb;
         const int nt = (first + g / nkb * step) % p.n_tiles;
-        const float sw = __ldg(p.w_scale + static_cast<size_t>(nt) * p.KB + kb);
+        const float sw = p.w_scale[static_cast<size_t>(nt) * p.KB + kb];
         const int st = g % C::STAGES, sl = g % C::SC_SLOTS;
         if (!wait_warp(&empty[st], ((g / C::STAGES) & 1) ^ 1, abort_flag, p.status)) break;
         if (!wait_warp(&sc_empty[sl], ((g / C::SC_SLOTS) & 1) ^ 1, abort_flag, p.status)) break;
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(Stream<NT, kQuant>::THREADS, Stream<NT, kQuant
       const int valid = t.row_end - t.row0 - r0;
       for (int kb = kb0; kb < kb1; kb += 4) {
         const bool in = kb + i < kb1;
-        const float w = in ? __ldg(sw + kb) : 0.f;
+        const float w = in ? sw[kb] : 0.f;
         float x[NT / 8];
 #pragma unroll
         for (int j = 0; j < NT / 8; ++j) x[j] = in && 8 * j < valid ? sx[static_cast<size_t>(8 * j) * p.KB + kb] : 0.f;
@@ -668,7 +668,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const __grid_constan
         const int valid = t.row_end - t.row0 - r0;
         for (int kb = w.kb0; kb < w.kb1; kb += 4) {
           const bool in = kb + i < w.kb1;
-          const float w0 = in ? __ldg(sw0 + kb) : 0.f, w1 = in ? __ldg(sw1 + kb) : 0.f;
+          const float w0 = in ? sw0[kb] : 0.f, w1 = in ? sw1[kb] : 0.f;
           float x[16];
           const float* at = sx + kb;
           int down = 8 * KB;
@@ -824,9 +824,9 @@ __global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const __grid_constan
 }
 
 // y = bf16(part sums in order + bias) of the tiles that were split.
-__global__ void __launch_bounds__(256) join_parts_kernel(const float4* __restrict__ sums, int parts, int tiles,
+__global__ void __launch_bounds__(256) join_parts_kernel(const float4* sums, int parts, int tiles,
                                                          int full, int n_tiles, int rows, int N,
-                                                         const uint16_t* __restrict__ bias, uint16_t* __restrict__ y) {
+                                                         const uint16_t* bias, uint16_t* __restrict__ y) {
   constexpr int kRow = TN / 4;
   launch_dependents();
   grid_dependency_wait();

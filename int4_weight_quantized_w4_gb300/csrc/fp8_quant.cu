@@ -74,10 +74,10 @@ W4_DEV float neg_silu_mul(float g, float u) {
 // by what the registers leave in flight). Four blocks of 128 columns a half-warp: with two,
 // silu takes 53.5, and the plain quantizer 42.0 at 32768 x 2048 against 34.5 (256 threads).
 template <bool kF16, bool kSilu, int kUnits>
-__global__ void __launch_bounds__(kThreads, kSilu ? 7 : 1) quant_block_kernel(const uint4* __restrict__ x, uint32_t items, int K8,
+__global__ void __launch_bounds__(kThreads, kSilu ? 7 : 1) quant_block_kernel(const uint4* x, uint32_t items, int K8,
                                                                int KB, uint32_t KU, uint2* __restrict__ q,
                                                                float* __restrict__ scale,
-                                                               const int32_t* __restrict__ gather, int64_t T,
+                                                               const int32_t* gather, int64_t T,
                                                                bool late, unsigned int* status) {
   if (!late) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int l = threadIdx.x & (kBlk8 - 1);
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kThreads, kSilu ? 7 : 1) quant_block_kernel(co
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (late) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (gather != nullptr && live) {
-    src = gather[row];
+    src = __ldcg(gather + row);
     bad = src < 0 || src >= T;
   }
   const int c0 = live ? b0 * kBlk8 + l : K8;
@@ -102,8 +102,8 @@ __global__ void __launch_bounds__(kThreads, kSilu ? 7 : 1) quant_block_kernel(co
   for (int i = 0; i < kUnits; ++i) {
     const int c = c0 + i * kBlk8;
     const bool in = c < K8 && !bad;
-    v[i] = in ? ld_stream_v4(xr + c) : make_uint4(0, 0, 0, 0);
-    if constexpr (kSilu) u[i] = in ? ld_stream_v4(xr + K8 + c) : make_uint4(0, 0, 0, 0);
+    v[i] = in ? ld_once_v4(xr + c) : make_uint4(0, 0, 0, 0);
+    if constexpr (kSilu) u[i] = in ? ld_once_v4(xr + K8 + c) : make_uint4(0, 0, 0, 0);
   }
   float m[kUnits], a[kSilu ? kUnits : 1][8];
 #pragma unroll
@@ -151,8 +151,8 @@ __global__ void __launch_bounds__(kThreads, kSilu ? 7 : 1) quant_block_kernel(co
       for (int i = 0; i < kUnits; ++i) {
         const int c = c0 + i * kBlk8;
         const bool in = c < K8;
-        const uint4 gv = in ? ld_stream_v4(xr + c) : make_uint4(0, 0, 0, 0);
-        const uint4 uv = in ? ld_stream_v4(xr + K8 + c) : make_uint4(0, 0, 0, 0);
+        const uint4 gv = in ? ld_once_v4(xr + c) : make_uint4(0, 0, 0, 0);
+        const uint4 uv = in ? ld_once_v4(xr + K8 + c) : make_uint4(0, 0, 0, 0);
         const uint32_t g[4] = {gv.x, gv.y, gv.z, gv.w}, w[4] = {uv.x, uv.y, uv.z, uv.w};
         float f[8], fm = 0.f;
 #pragma unroll
@@ -190,9 +190,9 @@ cudaError_t launch(const void* x, int64_t M, int64_t K, const int32_t* gather, i
 // Quantized rows copied to their places among the expert-sorted rows: row r of
 // (dst, dst_scale) is row gather[r] of (src, src_scale). A warp per row. The next
 // kernel starts only when every kernel before this one is done.
-__global__ void __launch_bounds__(kThreads) gather_rows_kernel(const uint4* __restrict__ src,
-                                                               const float* __restrict__ src_scale, int64_t T, int K16,
-                                                               int KB, const int32_t* __restrict__ gather, int64_t R,
+__global__ void __launch_bounds__(kThreads) gather_rows_kernel(const uint4* src,
+                                                               const float* src_scale, int64_t T, int K16,
+                                                               int KB, const int32_t* gather, int64_t R,
                                                                uint4* __restrict__ dst, float* __restrict__ dst_scale,
                                                                unsigned int* status) {
   const int lane = threadIdx.x & 31;
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kThreads) gather_rows_kernel(const uint4* __re
   asm volatile("griddepcontrol.wait;" ::: "memory");   // src comes from the kernel before
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (r >= R) return;
-  const int64_t t = gather[r];
+  const int64_t t = __ldcg(gather + r);
   uint4* d = dst + r * K16;
   if (t < 0 || t >= T) {
     for (int i = lane; i < K16; i += 32) d[i] = make_uint4(0, 0, 0, 0);

@@ -114,7 +114,7 @@ W4_DEV void route_token(const MoeRouteArgs& a, int64_t t, float (&v)[kEPL], uint
 #pragma unroll
     for (int i = 0; i < kEPL; ++i) {
       const int e = lane + 32 * i;
-      key[i] = e < E ? ordered_key(v[i] + __ldg(a.bias + e)) : kNoKey;
+      key[i] = e < E ? ordered_key(v[i] + a.bias[e]) : kNoKey;
     }
   }
 
@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps<kEPL>) route_tile_kernel(cons
 constexpr int kPlaceThreads = 1024;
 static_assert(kChunk * 64 <= kPairs * kPlaceThreads && 64 * 64 <= kPairs * 512, "a chunk's pairs at the largest top_k");
 __global__ void __launch_bounds__(kPlaceThreads) place_kernel(const MoeRouteArgs a, int per,
-                                                              const int32_t* __restrict__ counts, int ntiles) {
+                                                              const int32_t* counts, int ntiles) {
   extern __shared__ uint32_t sm[];
   __shared__ int32_t part[kPlaceThreads / 32];
   uint32_t* bits = sm;

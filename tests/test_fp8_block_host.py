@@ -2,6 +2,8 @@
 no GPU: argument validation through the C ABI, workspace sizes, and the compiled
 binding's refusals of tensors that are not on a GPU."""
 import ctypes
+import os
+import re
 
 import pytest
 import torch
@@ -180,3 +182,15 @@ def test_every_part_of_a_split_tile_has_a_block(lib):
             assert rest == 0 and 2 <= parts <= min(16, blocks), (K, pairs, parts)
             split += 1
     assert split > 1000
+
+
+@pytest.mark.parametrize("unit", ["fp8_block.cu", "fp8_quant.cu", "moe_route.cu"])
+def test_early_started_kernels_read_nothing_through_the_non_coherent_path(unit):
+    """These kernels start while the kernels before them still write what they read, so
+    none of their loads may be one that takes its data as constant for the whole kernel:
+    not spelled out, and not by a const __restrict__ pointer."""
+    with open(os.path.join(_build.CSRC, unit)) as f:
+        text = f.read()
+    assert "griddepcontrol.wait" in text
+    assert not re.findall(r"ld_nc_\w+|ld_stream_\w+|__ldg\b|\.nc\b", text)
+    assert not re.findall(r"const\s+\w+\s*\*\s*__restrict__", text)
