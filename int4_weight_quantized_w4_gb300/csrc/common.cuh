@@ -262,10 +262,13 @@ W4_DEV void fma2x(float& d0, float& d1, float a0, float a1, float b0, float b1, 
       : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
 }
 // Per-block quantization: a half-warp holds a block of 128 columns of a row, one
-// chunk of 8 per lane. Scale fl(amax / 448), 1 where that is 0: for a block of zeros,
-// and for fp32 values below 3e-43, whose zeros would give the code of 0 / 0.
-W4_DEV float block_scale(float amax) {
-  const float s = __fdiv_rn(amax, 448.f);
+// chunk of 8 per lane. Scale fl(amax / 448), 1 for a block of zeros (which the divide
+// would take a slow way through: 1 x 14336 x 4096 12.5 us against 12.4). The quotient of
+// a 16-bit amax is never 0; fp32 values below 3e-43 have block_scale_f32.
+W4_DEV float block_scale(float amax) { return amax == 0.f ? 1.f : __fdiv_rn(amax, 448.f); }
+// 1 also where the quotient is 0: the zeros of such a block would get the code of 0 / 0.
+W4_DEV float block_scale_f32(float amax) {
+  const float s = block_scale(amax);
   return s == 0.f ? 1.f : s;
 }
 

@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, kSilu ? 7 : 1) quant_block_kernel(co
   float* sr = scale + static_cast<size_t>(row) * KB + b0;
   // lane l holds scale and reciprocal of block b0 + l % kUnits (silu: of four times its products)
   const float amax = unit_max<kUnits, kSilu>(m);
-  const float s_mine = !kSilu ? block_scale(amax) : amax == 0.f ? 4.f : __fdiv_rn(amax, 448.f), r_mine = __frcp_rn(s_mine);
+  const float s_mine = kSilu && amax == 0.f ? 4.f : block_scale(amax), r_mine = __frcp_rn(s_mine);
   if (l < kUnits && live && b0 + l < KB) sr[l] = kSilu ? 0.25f * s_mine : s_mine;
 #pragma unroll
   for (int i = 0; i < kUnits; ++i) {
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, kSilu ? 7 : 1) quant_block_kernel(co
 #pragma unroll
         for (int o = kBlk8 / 2; o > 0; o >>= 1) fm = fmaxf(fm, __shfl_xor_sync(kFull, fm, o));
         if (__shfl_sync(kFull, again, i, kBlk8) && in) {
-          const float s = block_scale(fm);
+          const float s = block_scale_f32(fm);
           qr[c] = quant_e4m3_block<1, true>(f, s, __frcp_rn(s));
           if (l == 0) sr[i] = s;
         }
