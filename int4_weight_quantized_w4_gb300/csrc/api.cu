@@ -525,7 +525,7 @@ static w4_status run_fp8_block_act(const void* x, bool f16, int64_t T, const int
   // copied, when the workspace has room for the tokens' codes and the copy is
   // worth a launch.
   const size_t base = w4::fp8_block_workspace_bytes(R, K), tokens = w4::fp8_block_workspace_bytes(T, K);
-  if (rows != nullptr && 2 * T <= R && R * K >= kCopyElements && ws_bytes >= base + tokens) {
+  if (rows != nullptr && T > 0 && 2 * T <= R && R * K >= kCopyElements && ws_bytes >= base + tokens) {
     uint8_t* tq = static_cast<uint8_t*>(ws) + base;
     float* ts = reinterpret_cast<float*>(tq + static_cast<size_t>(T) * K);
     e = w4::launch_quant_block(x, f16, false, T, K, nullptr, 0, false, tq, ts, status, s);

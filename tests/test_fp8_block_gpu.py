@@ -1,6 +1,8 @@
 """The fp8 block-scaled layer on the GPU against the oracle, through the C ABI:
 per-block quantization, silu * up requantization, the dense product in both its
 forms, and the product over expert segments."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -570,3 +572,23 @@ def test_silu_mul_quant_block_products_below_any_scale():
     assert s.cpu().numpy()[0, 0] == 1 and (codes(q)[0, :128] & 0x7F == 0).all()
     assert (codes(q)[0, 128:] & 0x7F == 0x7E).all()
     assert torch.isfinite(y).all()
+
+
+@pytest.mark.parametrize("R", [6, 40000])
+def test_grouped_bf16in_of_no_tokens(R):
+    """T = 0: every row id is outside [0, T), few rows and many alike, so all rows are zero
+    and the status word says so. (The C entry point: an empty tensor has no address.)"""
+    N, K, E = 136, 528, 2
+    qw, sw = weights(N, K, seed=7, E=E)
+    off, rt = to_dev(np.array([0, R // 3, R], np.int32)), torch.zeros(R, dtype=torch.int32, device="cuda")
+    x, wd, sd = torch.empty((1, K), dtype=torch.bfloat16, device="cuda"), fp8(qw), to_dev(sw)
+    y = torch.full((R, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    need = w4.w4_workspace_bytes(w4.W4_OP_FP8_BLOCK_IN, R, N, K, E)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    assert w4.w4_device_status() == w4.W4_OK
+    p = lambda t: ctypes.c_void_p(t.data_ptr())
+    st = w4.load().w4_fp8_block_moe_gemm_bf16in(p(x), 0, p(rt), p(off), E, p(wd), p(sd), p(y), R, N, K, p(ws), need,
+                                                ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    assert st == w4.W4_OK
+    assert w4.w4_device_status() == w4.W4_ERR_SHAPE
+    assert not (bits(y) & 0x7FFF).any()
