@@ -130,17 +130,16 @@ def _on(side):
     return contextlib.nullcontext() if side is None else torch.cuda.stream(side)
 
 
-def _empty(shape, dtype, device, stream, scratch=False, zero=False):
+def _empty(shape, dtype, device, stream, scratch=False):
     """Memory for a call on ``stream``. It belongs to that stream, so that it is neither
     in use by other work when the call's kernels write it nor handed to other work while
     they use it. An output (not ``scratch``) is read on the current stream too: released
     there, it is not handed out again before that stream is done with it."""
-    make = torch.zeros if zero else torch.empty
     side = _side(stream, device)
     if side is None:
-        return make(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=device)
     with _on(side):
-        t = make(shape, dtype=dtype, device=device)
+        t = torch.empty(shape, dtype=dtype, device=device)
     if not scratch:
         t.record_stream(torch.cuda.current_stream(device))
     return t
@@ -398,7 +397,7 @@ def w4_moe_route(logits, top_k: int, renormalize: bool = False, out=None, worksp
     if out is None:
         out = (_empty((T, top_k), torch.int32, dev, stream),
                _empty((T, top_k), torch.float32, dev, stream),
-               _empty((E + 1,), torch.int32, dev, stream, zero=True),
+               _empty((E + 1,), torch.int32, dev, stream),
                _empty((T * top_k,), torch.int32, dev, stream),
                _empty((T, top_k), torch.int32, dev, stream))
     ids, wts, off, rt, ro = out
@@ -411,6 +410,9 @@ def w4_moe_route(logits, top_k: int, renormalize: bool = False, out=None, worksp
     _check(load().w4_moe_route(_ptr(logits), int(logits.dtype == torch.float32), T, E, top_k, int(bool(renormalize)),
                                _ptr(ids), _ptr(wts), _ptr(off), _ptr(rt), _ptr(ro), _ptr(ws), wsb,
                                _stream(stream, dev)), "w4_moe_route")
+    if T == 0:   # the library writes nothing
+        with _on(_side(stream, dev)):
+            off.zero_()
     return out
 
 

@@ -251,7 +251,6 @@ PyObject* route_grouped(PyObject*, PyObject* const* a, Py_ssize_t n) {
     else
       o[i] = tensor(PyTuple_GET_ITEM(a[8], i), names[i], i == 1 ? kF32 : kI32, dev, shape);
   }
-  if (T == 0 && a[8] == Py_None) o[2].zero_();   // the library writes nothing
   const Scratch s = scratch(a[9], W4_OP_MOE_ROUTE_GROUPED, T, E, 1, 0, dev);
   if (failed(w4_moe_route_grouped(x.data_ptr(), x.scalar_type() == ScalarType::Float, static_cast<float*>(data(a[2])), T,
                                   static_cast<int32_t>(E), k, groups, keep, integer32(a[5], "scoring"),
@@ -260,6 +259,7 @@ PyObject* route_grouped(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                   stream.handle()),
              "w4_moe_route_grouped"))
     return nullptr;
+  if (T == 0) o[2].zero_();   // the library writes nothing
   if (a[8] != Py_None) {
     Py_INCREF(a[8]);
     return a[8];

@@ -104,3 +104,19 @@ def test_route_grouped_many_tokens(T):
     order = np.argsort(ids.reshape(-1), kind="stable")
     np.testing.assert_array_equal(rt.cpu().numpy(), order // k)
     np.testing.assert_array_equal(ro.cpu().numpy().reshape(-1)[order], np.arange(T * k))
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_routes_of_no_tokens_have_empty_segments(given):
+    """T = 0: every offset is 0, in outputs of the caller's too (a reused buffer would
+    otherwise keep the segments of the call before)."""
+    E, k = 48, 4
+    lg = torch.empty((0, E), device="cuda")
+    for route in (w4.w4_moe_route_grouped, w4.w4_moe_route):
+        i32 = dict(dtype=torch.int32, device="cuda")
+        out = (torch.empty((0, k), **i32), torch.empty((0, k), device="cuda"), torch.full((E + 1,), 7, **i32),
+               torch.empty((0,), **i32), torch.empty((0, k), **i32)) if given else None
+        got = route(lg, k, out=out)
+        torch.cuda.synchronize()
+        assert not got[2].any() and got[2].shape == (E + 1,) and got[0].shape == (0, k)
+        assert not given or got[2].data_ptr() == out[2].data_ptr()
