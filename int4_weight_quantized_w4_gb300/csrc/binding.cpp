@@ -236,15 +236,19 @@ PyObject* route_grouped(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const char* names[5] = {"topk_ids", "topk_weights", "offsets", "row_token", "row_of"};
   if (a[8] != Py_None && (!PyTuple_Check(a[8]) || PyTuple_GET_SIZE(a[8]) != 5))
     value_error("out must be the tuple (topk_ids, topk_weights, offsets, row_token, row_of)");
-  // the five outputs share one allocation when none are given
-  const int64_t starts[5] = {0, T * k, 4 * T * k, 2 * T * k, 3 * T * k};
+  // the five outputs share one allocation when none are given; a top_k that the library
+  // refuses asks for no memory first
+  const int64_t n_out = a[8] == Py_None && (k > E || k > 64) ? 0 : k;
+  const int64_t starts[5] = {0, T * n_out, 4 * T * n_out, 2 * T * n_out, 3 * T * n_out};
   at::Tensor all;
   if (a[8] == Py_None) {
-    all = empty({4 * T * k + E + 1}, ScalarType::Int, dev);
+    all = empty({4 * T * n_out + E + 1}, ScalarType::Int, dev);
     stream.keep_for_caller(all);
   }
   for (int i = 0; i < 5; ++i) {
-    const at::DimVector shape = i == 2 ? at::DimVector{E + 1} : i == 3 ? at::DimVector{T * k} : at::DimVector{T, k};
+    const at::DimVector shape = i == 2   ? at::DimVector{E + 1}
+                                : i == 3 ? at::DimVector{T * n_out}
+                                         : at::DimVector{T, n_out};
     const ScalarType type = i == 1 ? ScalarType::Float : ScalarType::Int;
     if (a[8] == Py_None)
       o[i] = words_of(all, starts[i], shape, type);

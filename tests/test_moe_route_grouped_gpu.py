@@ -120,3 +120,15 @@ def test_routes_of_no_tokens_have_empty_segments(given):
         torch.cuda.synchronize()
         assert not got[2].any() and got[2].shape == (E + 1,) and got[0].shape == (0, k)
         assert not given or got[2].data_ptr() == out[2].data_ptr()
+
+
+@pytest.mark.parametrize("top_k", [65, 1 << 20, 2 ** 31 - 1])
+def test_refused_top_k_asks_for_no_memory(top_k):
+    """The library's refusal, not an allocation of T * top_k words that fails before it."""
+    lg = torch.zeros((100000, 64), device="cuda")
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    with pytest.raises(w4.W4Error) as e:
+        w4.w4_moe_route_grouped(lg, top_k)
+    assert e.value.status == w4.W4_ERR_SHAPE
+    assert torch.cuda.max_memory_allocated() - before < 1 << 20
