@@ -440,7 +440,7 @@ w4_status w4_quant_act_per_block(const void* x, int32_t x_dtype, int64_t M, int6
   if (!x || !q || !scale) return fail(W4_ERR_NULL, "x, q and scale must be non-NULL");
   if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 4))
     return fail(W4_ERR_ALIGN, "x and q must be 16-byte aligned, scale 4-byte aligned");
-  if (K > INT32_MAX / 2) return fail(W4_ERR_UNSUPPORTED, "K too large");
+  if (K > INT32_MAX / 2 || !w4::quant_block_fits(M, K)) return fail(W4_ERR_UNSUPPORTED, "M or K too large");
   return from_cuda(w4::launch_quant_block(x, x_dtype == W4_FP16, false, M, K, nullptr, 0, false, q, scale, nullptr,
                                           static_cast<cudaStream_t>(stream)),
                    "w4_quant_act_per_block launch");
@@ -453,7 +453,7 @@ w4_status w4_silu_mul_quant_block(const void* h, int64_t R, int64_t I, void* q, 
   if (!h || !q || !scale) return fail(W4_ERR_NULL, "h, q and scale must be non-NULL");
   if (!aligned(h, 16) || !aligned(q, 16) || !aligned(scale, 4))
     return fail(W4_ERR_ALIGN, "h and q must be 16-byte aligned, scale 4-byte aligned");
-  if (I > INT32_MAX / 2) return fail(W4_ERR_UNSUPPORTED, "I too large");
+  if (I > INT32_MAX / 2 || !w4::quant_block_fits(R, I)) return fail(W4_ERR_UNSUPPORTED, "R or I too large");
   return from_cuda(w4::launch_quant_block(h, false, true, R, I, nullptr, 0, false, q, scale, nullptr,
                                           static_cast<cudaStream_t>(stream)),
                    "w4_silu_mul_quant_block launch");
@@ -468,7 +468,7 @@ static w4_status check_fp8_block(int64_t R, int64_t N, int64_t K, int32_t E, boo
     return fail(W4_ERR_ALIGN, "N and K must be multiples of 8, got N=%lld K=%lld", (long long)N, (long long)K);
   if (K % 16 != 0) return fail(W4_ERR_UNSUPPORTED, "rows of e4m3 codes are copied 16 at a time: K=%lld", (long long)K);
   if (experts && E > 1024) return fail(W4_ERR_UNSUPPORTED, "E must be at most 1024, got %d", E);
-  if (R > INT32_MAX / 2 || N > INT32_MAX / 2 || K > INT32_MAX / 2) return fail(W4_ERR_UNSUPPORTED, "M, N or K too large");
+  if (R > INT32_MAX / 2 || N > INT32_MAX / 2 || K > INT32_MAX / 2 || !w4::quant_block_fits(R, K)) return fail(W4_ERR_UNSUPPORTED, "M, N or K too large");
   return W4_OK;
 }
 

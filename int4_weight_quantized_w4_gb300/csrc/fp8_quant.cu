@@ -180,7 +180,6 @@ cudaError_t launch(const void* x, int64_t M, int64_t K, const int32_t* gather, i
   const int K8 = static_cast<int>(K / 8), KB = static_cast<int>((K + 127) / 128), KU = (KB + kUnits - 1) / kUnits;
   const int64_t items = M * KU;
   const int64_t blocks = (items * kBlk8 + kThreads - 1) / kThreads;
-  if (items > INT32_MAX) return cudaErrorInvalidConfiguration;
   PdlLaunch pl(static_cast<unsigned>(blocks), kThreads, 0, s);
   return cudaLaunchKernelEx(&pl.cfg, quant_block_kernel<kF16, kSilu, kUnits>, static_cast<const uint4*>(x),
                             static_cast<uint32_t>(items), K8, KB, static_cast<uint32_t>(KU), static_cast<uint2*>(q),
@@ -226,6 +225,11 @@ __global__ void __launch_bounds__(kThreads) gather_rows_kernel(const uint4* src,
 }
 
 }  // namespace
+
+bool quant_block_fits(int64_t M, int64_t K) {
+  const int64_t per_row = (K + 511) / 512;   // half-warps
+  return M <= INT32_MAX / per_row;
+}
 
 cudaError_t launch_quant_block(const void* x, bool f16, bool silu, int64_t M, int64_t K, const int32_t* gather,
                                int64_t T, bool late, void* q, float* scale, unsigned int* status, cudaStream_t s) {

@@ -142,8 +142,10 @@ cudaError_t launch_moe_combine(const void* y, int64_t R, int64_t H, const float*
 // e4m3 codes and fp32 scales per row and 128 columns of x [*, K] (bf16, or fp16), or of silu(gate) * up of x
 // [*, 2K] (silu, bf16); gather (may be null): source row of each of the M output rows, checked against T. late: a
 // programmatic dependent starts only when every kernel before this one is done.
+// M rows of K fit one grid (quant_block_fits).
 cudaError_t launch_quant_block(const void* x, bool f16, bool silu, int64_t M, int64_t K, const int32_t* gather,
                                int64_t T, bool late, void* q, float* scale, unsigned int* status, cudaStream_t s);
+bool quant_block_fits(int64_t M, int64_t K);
 // Rows gather[r] of quantized (src, src_scale) [T, K], which the kernel launched just before writes, as row r of (dst, dst_scale);
 // late, as above.
 cudaError_t launch_gather_block_rows(const void* src, const float* src_scale, int64_t T, int64_t K,

@@ -194,3 +194,10 @@ def test_early_started_kernels_read_nothing_through_the_non_coherent_path(unit):
     assert "griddepcontrol.wait" in text
     assert not re.findall(r"ld_nc_\w+|ld_stream_\w+|__ldg\b|\.nc\b", text)
     assert not re.findall(r"const\s+\w+\s*\*\s*__restrict__", text)
+
+
+def test_block_quant_of_too_many_rows_is_unsupported(lib):
+    """Rows times blocks past what one grid numbers: refused as such, not by the launch."""
+    for M, K in ((1 << 31, 8), (1 << 31, 512), (1 << 30, 1032), (1 << 40, 128)):
+        assert lib.w4_quant_act_per_block(FAKE, w4.W4_BF16, M, K, FAKE, FAKE, None) == w4.W4_ERR_UNSUPPORTED
+        assert lib.w4_silu_mul_quant_block(FAKE, M, K, FAKE, FAKE, None) == w4.W4_ERR_UNSUPPORTED
