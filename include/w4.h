@@ -219,10 +219,12 @@ w4_status w4a8_gemm_bf16in(const void* x, const void* qweight, const void* w_sca
  * start streaming qweight with its scales and zeros, while the kernel before
  * it on `stream` is still finishing (it waits for that kernel before it reads
  * x or the bias, or writes y). So qweight, w_scale and zeros must not be
- * written by a kernel that runs immediately before on the same stream and
- * signals its dependents early; kernels that do not (every kernel of this
- * library except this one and those of the fp8 block-scaled layer, and ordinary
- * library kernels) are waited for in full.
+ * written by a kernel that signals its dependents early, unless a kernel that
+ * does not, or a synchronization, stands between the two on the stream (one
+ * early signaller after another lets this kernel start while the first still
+ * runs). Early signallers are this kernel and those of the fp8 block-scaled
+ * layer; every other kernel of this library, and ordinary library kernels, are
+ * waited for in full.
  */
 w4_status w4a16_gemm(const void* x, const void* qweight, const void* w_scale, int32_t w_scale_dtype,
                      const void* zeros, int32_t group, const void* bias, void* y,
@@ -375,10 +377,12 @@ w4_status w4_moe_combine(const void* y, int64_t R, int64_t H, const float* topk_
  *
  * 1 <= E <= 1024; n_group divides E (W4_ERR_GROUP), at most 32
  * (W4_ERR_UNSUPPORTED); 1 <= topk_group <= n_group; 1 <= top_k <= min(64,
- * topk_group * E / n_group). A logit of -inf scores 0 (a masked expert; it can
- * still be chosen when nothing else is open). Where the chosen scores sum to 0,
- * as in a row that is masked altogether, renormalized weights are 0. NaN logits
- * count as -inf, +inf as the largest finite fp32. T == 0 launches nothing.
+ * topk_group * E / n_group). A logit of -inf scores 0. Without a bias its key is
+ * -inf, so that it is chosen only when nothing else is open; with one its key is
+ * bias[e], which can beat another expert's (a bias of -inf closes an expert there).
+ * Where the chosen scores sum to 0, as in a row that is masked altogether,
+ * renormalized weights are 0. NaN logits count as -inf, +inf as the largest finite
+ * fp32; bias must not be NaN. T == 0 launches nothing.
  */
 w4_status w4_moe_route_grouped(const void* logits, int32_t logits_f32, const float* bias, int64_t T, int32_t E,
                                int32_t top_k, int32_t n_group, int32_t topk_group, int32_t scoring,
@@ -396,14 +400,17 @@ w4_status w4_moe_route_grouped(const void* logits, int32_t logits_f32, const flo
  *
  * The entry points of this layer are launched with programmatic dependent launch,
  * as w4a16_gemm is, and signal their own dependents early. They may start
- * streaming qweight while the kernel before them on `stream` is finishing and wait
- * for it before they touch anything else. So qweight must not be written by a
- * kernel that runs immediately before on the same stream and signals its
- * dependents early.
+ * streaming qweight while the kernels before them on `stream` are finishing and wait
+ * for those before they touch anything else. So qweight must not be written by a
+ * kernel that signals its dependents early (any of this layer, or w4a16_gemm), unless
+ * a kernel that does not, or a synchronization, stands between the two on the stream.
  *
  * w4_quant_act_per_block: per row and block of 128 columns (the last one may be
  * shorter) amax = max |x|, s = amax / 448 in fp32 (1 where that is 0),
- * q = e4m3(fl(x / s)), round to nearest even, saturating; the divides are IEEE.
+ * q = e4m3(fl(x / s)), round to nearest even, saturating; the divides are IEEE, and
+ * zeros keep their sign. NaN counts for nothing in amax and has a NaN code (a block of
+ * NaN alone a NaN scale); an infinity makes its block's scale infinite, its own code
+ * NaN and the block's other codes 0.
  *   x [M, K] bf16 or fp16 (x_dtype), 16-byte aligned; K % 8 == 0
  *   q [M, K] e4m3 codes, 16-byte aligned; scale [M, ceil(K/128)] fp32
  */

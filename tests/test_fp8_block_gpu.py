@@ -592,3 +592,27 @@ def test_grouped_bf16in_of_no_tokens(R):
     assert st == w4.W4_OK
     assert w4.w4_device_status() == w4.W4_ERR_SHAPE
     assert not (bits(y) & 0x7FFF).any()
+
+
+@pytest.mark.parametrize("f16", [False, True])
+def test_quant_per_block_nan_and_infinity(f16):
+    """NaN counts for nothing in the maximum and has a NaN code, a block of NaN a NaN scale;
+    an infinity makes its block's scale infinite. Other blocks are as without them."""
+    v = S.bf16_bits_to_f32(S.activations_bf16(2, 640, seed=4)).astype(np.float32)
+    v[1] = v[0]
+    v[1, 5], v[1, 128:256], v[1, 256 + 7], v[1, 384 + 9] = np.nan, np.nan, np.inf, -np.inf
+    x = v.astype(np.float16) if f16 else S.to_bf16_bits(v)
+    if not f16:
+        x[1, 5], x[1, 128:256] = 0x7FC0, 0x7FC0
+    q, s = w4.w4_quant_act_per_block(to_dev(x) if f16 else bf16(x))
+    torch.cuda.synchronize()
+    c, s = codes(q), s.cpu().numpy()
+    v[0, 5] = 0                                           # the first block's maximum without the NaN
+    assert s[1, 0] == np.float32(np.abs(v[0, :128]).max()) / np.float32(448)
+    assert c[1, 5] & 0x7F == 0x7F and (np.delete(c[1, :128], 5) & 0x7F != 0x7F).all()
+    assert np.isnan(s[1, 1]) and (c[1, 128:256] & 0x7F == 0x7F).all()
+    for b, at in ((2, 7), (3, 9)):
+        block = c[1, 128 * b:128 * b + 128] & 0x7F
+        assert np.isposinf(s[1, b]) and block[at] == 0x7F and (np.delete(block, at) == 0).all()
+    np.testing.assert_array_equal(c[1, 512:], c[0, 512:])
+    assert s[1, 4] == s[0, 4]

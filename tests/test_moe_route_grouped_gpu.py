@@ -132,3 +132,17 @@ def test_refused_top_k_asks_for_no_memory(top_k):
         w4.w4_moe_route_grouped(lg, top_k)
     assert e.value.status == w4.W4_ERR_SHAPE
     assert torch.cuda.max_memory_allocated() - before < 1 << 20
+
+
+@pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
+def test_masked_experts_with_and_without_a_bias(scoring):
+    """A logit of -inf is chosen last without a bias; with one its key is the bias alone. A
+    bias of -inf closes an expert."""
+    lg = np.full((1, 8), -2.0, np.float32)
+    lg[0, 3] = -np.inf
+    ids, _ = _check(lg, to_dev(lg), 8, None, scoring=scoring)
+    assert ids[0, -1] == 3
+    bias = np.zeros(8, np.float32)
+    bias[3], bias[5] = 1.0, -np.inf
+    ids, w = _check(lg, to_dev(lg), 8, bias, scoring=scoring, renormalize=False)
+    assert ids[0, 0] == 3 and w[0, 0] == 0 and ids[0, -1] == 5
