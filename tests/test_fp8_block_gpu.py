@@ -616,3 +616,27 @@ def test_quant_per_block_nan_and_infinity(f16):
         assert np.isposinf(s[1, b]) and block[at] == 0x7F and (np.delete(block, at) == 0).all()
     np.testing.assert_array_equal(c[1, 512:], c[0, 512:])
     assert s[1, 4] == s[0, 4]
+
+
+@pytest.mark.parametrize("M", [1, 2, 3, 5, 7, 8, 9])
+@pytest.mark.parametrize("f16", [False, True])
+@pytest.mark.parametrize("N,K", [(2056, 1456), (200, 272), (40008, 272), (5128, 2064)])
+def test_few_16_bit_rows(M, f16, N, K):
+    """Rows that the product quantizes itself (up to eight) and the first count that it does
+    not: K shared by a cluster and not, one item a CTA and several, ragged last blocks; equal
+    to quantizer and product bit for bit, and to the oracle."""
+    x = S.activations_bf16(M, K, seed=M + N, outlier_frac=0.01)
+    x = S.bf16_bits_to_f32(x).astype(np.float16) if f16 else x
+    t = to_dev(x) if f16 else bf16(x)
+    qw, sw = weights(N, K, seed=M)
+    b = S.bias_bf16(N)
+    wd, sd, bd = fp8(qw), to_dev(sw), bf16(b)
+    y = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    w4.w4_fp8_block_gemm_bf16in(t, wd, sd, bias=bd, y=y)
+    q, s = w4.w4_quant_act_per_block(t)
+    two = w4.w4_fp8_block_gemm(q, s, wd, sd, bias=bd)
+    torch.cuda.synchronize()
+    assert w4.w4_device_status() == w4.W4_OK
+    np.testing.assert_array_equal(bits(y), bits(two))
+    rq, rs = O.quant_fp8_per_block(x)
+    check_bf16_output(bits(y), O.fp8_block_linear(rq, rs, qw, sw, b), f"{M} rows")
