@@ -146,3 +146,15 @@ def test_masked_experts_with_and_without_a_bias(scoring):
     bias[3], bias[5] = 1.0, -np.inf
     ids, w = _check(lg, to_dev(lg), 8, bias, scoring=scoring, renormalize=False)
     assert ids[0, 0] == 3 and w[0, 0] == 0 and ids[0, -1] == 5
+
+
+@pytest.mark.parametrize("T,E,k,G,keep", [(5000, 256, 8, 8, 4), (16384, 256, 8, 8, 4), (2500, 512, 10, 2, 1),
+                                          (1300, 1024, 16, 32, 8), (5000, 64, 6, 1, 1), (10001, 33, 4, 3, 2)])
+@pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_route_grouped_more_tokens_than_warps(T, E, k, G, keep, scoring, with_bias):
+    """Tiles of more tokens than their CTA has warps: a warp routes several, the next one's
+    logits on their way meanwhile. Ids and weights of every token against the oracle."""
+    lg = S.router_logits(T, E, seed=T + k)
+    bias = (S.normal(T, 80, E) * 0.1).astype(np.float32) if with_bias else None
+    _check(lg, to_dev(lg), k, bias, n_group=G, topk_group=keep, scoring=scoring, renormalize=T % 2 == 0, scale=2.5)
