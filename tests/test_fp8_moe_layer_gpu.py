@@ -64,3 +64,16 @@ def test_layer_stage_by_stage(T):
     check_bf16_output(bits(shared), O.fp8_block_linear(codes(b), sb.cpu().numpy(), codes(layer.shared_down.codes),
                                                        layer.shared_down.scale.cpu().numpy()), "shared down")
     np.testing.assert_array_equal(bits(out), bits(routed + shared))
+
+
+@pytest.mark.parametrize("T", [1, 2, 7, 8, 9, 64])
+def test_shared_expert_of_the_layer(T):
+    """The shared expert's gate_up from 16-bit tokens, quantized in the product or before it."""
+    layer = example().random_layer(seed=T + 1)
+    g = torch.Generator().manual_seed(T)
+    x = torch.randn((T, layer.router.shape[1]), generator=g).to(torch.bfloat16).cuda()
+    h = w4.w4_fp8_block_gemm_bf16in(x, layer.shared_gate_up.codes, layer.shared_gate_up.scale)
+    torch.cuda.synchronize()
+    q, s = O.quant_fp8_per_block(bits(x))
+    check_bf16_output(bits(h), O.fp8_block_linear(q, s, codes(layer.shared_gate_up.codes),
+                                                  layer.shared_gate_up.scale.cpu().numpy()), "shared gate_up")
