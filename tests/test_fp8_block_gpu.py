@@ -640,3 +640,39 @@ def test_few_16_bit_rows(M, f16, N, K):
     np.testing.assert_array_equal(bits(y), bits(two))
     rq, rs = O.quant_fp8_per_block(x)
     check_bf16_output(bits(y), O.fp8_block_linear(rq, rs, qw, sw, b), f"{M} rows")
+
+
+@pytest.mark.parametrize("sweep", [False, True])
+def test_silu_mul_quant_block_against_the_fp32_formula(sweep):
+    """Codes and scales against fl(fl(g / fl(1 + fl(exp(-g)))) u), each step rounded once. A
+    product is off by a few fp32 ulp at most (exponential and quotient one each, and the
+    roundings), so by 2^-21; so is a scale. A quotient of the two crosses one of the code
+    boundaries, which are 2^-4 apart at least, for a share of at most 2^-15 of the elements
+    and by one step. Random gates, and every bf16 gate of magnitude up to 80."""
+    if sweep:
+        g = np.arange(1 << 16, dtype=np.uint16)
+        g = g[np.abs(np.nan_to_num(S.bf16_bits_to_f32(g), nan=1e9)) <= 80]
+        g = g[:g.size // 1024 * 1024].reshape(-1, 1024)
+        R, I = g.shape
+        h = np.concatenate([g, S.activations_bf16(R, I, seed=2, std=3.0)], axis=1)
+    else:
+        R, I = 512, 2048
+        h = S.activations_bf16(R, 2 * I, seed=1, std=3.0, outlier_frac=0.01)
+    q, s = w4.w4_silu_mul_quant_block(bf16(h))
+    torch.cuda.synchronize()
+    v = S.bf16_bits_to_f32(h)
+    g, u = v[:, :I], v[:, I:]
+    f32, f64 = np.float32, np.float64
+    with np.errstate(over="ignore", invalid="ignore", divide="ignore"):
+        d = (f32(1) + np.exp(-g.astype(f64)).astype(f32)).astype(f32)
+        p = ((g / d).astype(f32) * u).astype(f32).reshape(R, I // 128, 128)
+        rs = (np.abs(p).max(axis=2) / f32(448)).astype(f32)
+        ordinary = rs > 1e-30
+        quotient = (p / rs[:, :, None]).astype(f32)
+    assert ordinary.mean() > 0.5
+    np.testing.assert_allclose(s.cpu().numpy()[ordinary], rs[ordinary], rtol=2.0 ** -21)
+    ref = O.e4m3_encode(np.nan_to_num(quotient[ordinary]).astype(f64)).astype(np.int64)
+    got = codes(q).reshape(R, I // 128, 128)[ordinary].astype(np.int64)
+    step = np.abs((ref & 0x7F) - (got & 0x7F))
+    assert step.max() <= 1 and ((ref ^ got)[step == 0] == 0).all()
+    assert (step != 0).sum() <= step.size * 2.0 ** -15 + 1, (step != 0).sum()
