@@ -365,21 +365,16 @@ W4_DEV float max_of(float a, float b) {
   return d;
 }
 
-// The maxima of kUnits blocks over the half-warp, reduced together: lanes trade one
-// half of their values for the other at each of the first steps, which leaves the
-// maximum of block u in the lanes with lane % kUnits == u.
-template <int kUnits, bool kNaN = false>
-W4_DEV float unit_max(const float (&m)[kUnits]) {
-  static_assert(kUnits == 2 || kUnits == 4, "one lane bit per halving");
+// The maxima of four blocks over the half-warp, reduced together: lanes trade one
+// half of their values for the other at each of the first two steps, which leaves the
+// maximum of block u in the lanes with lane % 4 == u.
+template <bool kNaN>
+W4_DEV float unit_max(const float (&m)[4]) {
   const int lane = threadIdx.x & 31;
   const bool b0 = lane & 1, b1 = lane & 2;
-  float z = max_of<kNaN>(b0 ? m[1] : m[0], __shfl_xor_sync(0xffffffffu, b0 ? m[0] : m[1], 1));
-  if constexpr (kUnits == 4) {
-    const float y = max_of<kNaN>(b0 ? m[3] : m[2], __shfl_xor_sync(0xffffffffu, b0 ? m[2] : m[3], 1));
-    z = max_of<kNaN>(b1 ? y : z, __shfl_xor_sync(0xffffffffu, b1 ? z : y, 2));
-  } else {
-    z = max_of<kNaN>(z, __shfl_xor_sync(0xffffffffu, z, 2));
-  }
+  const float x = max_of<kNaN>(b0 ? m[1] : m[0], __shfl_xor_sync(0xffffffffu, b0 ? m[0] : m[1], 1));
+  const float y = max_of<kNaN>(b0 ? m[3] : m[2], __shfl_xor_sync(0xffffffffu, b0 ? m[2] : m[3], 1));
+  float z = max_of<kNaN>(b1 ? y : x, __shfl_xor_sync(0xffffffffu, b1 ? x : y, 2));
   z = max_of<kNaN>(z, __shfl_xor_sync(0xffffffffu, z, 4));
   return max_of<kNaN>(z, __shfl_xor_sync(0xffffffffu, z, 8));
 }
@@ -403,7 +398,7 @@ W4_DEV float quant_blocks4(const uint4 (&v)[4], uint2 (&code)[4]) {
   float m[4];
 #pragma unroll
   for (int u = 0; u < 4; ++u) m[u] = chunk_max<kF16>(v[u]);
-  const float s_mine = block_scale(unit_max<4>(m)), r_mine = __frcp_rn(s_mine);
+  const float s_mine = block_scale(unit_max<false>(m)), r_mine = __frcp_rn(s_mine);
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const float s = __shfl_sync(0xffffffffu, s_mine, u, 16), r = __shfl_sync(0xffffffffu, r_mine, u, 16);

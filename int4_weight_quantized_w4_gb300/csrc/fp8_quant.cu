@@ -31,6 +31,9 @@ namespace w4 {
 namespace {
 
 constexpr int kBlk8 = 16;       // 8-element chunks per block of 128 columns
+// Blocks of 128 columns a half-warp: with two, 32768 x 1408 silu took 53.5 us against 49.8,
+// and 32768 x 2048 bf16 42.0 against 34.5 (blocks of 256 threads).
+constexpr int kUnits = 4;
 constexpr int kThreads = 128;    // 4097 x 4096 9.8 us; blocks of 256 threads 10.1
 constexpr unsigned kFull = 0xFFFFFFFFu;
 
@@ -71,9 +74,8 @@ W4_DEV float neg_silu_mul(float g, float u) {
 // with scales 1 and W4_ERR_SHAPE in the status word. KU = ceil(KB / kUnits). late:
 // the next kernel starts only when every kernel before this one is done.
 // At least seven silu blocks an SM: 45.8 us at 32768 x 1408 (six 47.0, eight 45.5,
-// by what the registers leave in flight). Four blocks of 128 columns a half-warp: with two,
-// silu takes 53.5, and the plain quantizer 42.0 at 32768 x 2048 against 34.5 (256 threads).
-template <bool kF16, bool kSilu, int kUnits>
+// by what the registers leave in flight).
+template <bool kF16, bool kSilu>
 __global__ void __launch_bounds__(kThreads, kSilu ? 7 : 1) quant_block_kernel(const uint4* x, uint32_t items, int K8,
                                                                int KB, uint32_t KU, uint2* __restrict__ q,
                                                                float* __restrict__ scale,
@@ -123,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, kSilu ? 7 : 1) quant_block_kernel(co
   uint2* qr = q + static_cast<size_t>(row) * K8;
   float* sr = scale + static_cast<size_t>(row) * KB + b0;
   // lane l holds scale and reciprocal of block b0 + l % kUnits (silu: of four times its products)
-  const float amax = unit_max<kUnits, kSilu>(m);
+  const float amax = unit_max<kSilu>(m);
   const float s_mine = kSilu && amax == 0.f ? 4.f : block_scale(amax), r_mine = __frcp_rn(s_mine);
   if (l < kUnits && live && b0 + l < KB) sr[l] = kSilu ? 0.25f * s_mine : s_mine;
 #pragma unroll
@@ -174,14 +176,14 @@ __global__ void __launch_bounds__(kThreads, kSilu ? 7 : 1) quant_block_kernel(co
   if (bad && l == 0) report(status, W4_ERR_SHAPE);
 }
 
-template <bool kF16, bool kSilu, int kUnits>
+template <bool kF16, bool kSilu>
 cudaError_t launch(const void* x, int64_t M, int64_t K, const int32_t* gather, int64_t T, bool late, void* q,
                    float* scale, unsigned int* status, cudaStream_t s) {
   const int K8 = static_cast<int>(K / 8), KB = static_cast<int>((K + 127) / 128), KU = (KB + kUnits - 1) / kUnits;
   const int64_t items = M * KU;
   const int64_t blocks = (items * kBlk8 + kThreads - 1) / kThreads;
   PdlLaunch pl(static_cast<unsigned>(blocks), kThreads, 0, s);
-  return cudaLaunchKernelEx(&pl.cfg, quant_block_kernel<kF16, kSilu, kUnits>, static_cast<const uint4*>(x),
+  return cudaLaunchKernelEx(&pl.cfg, quant_block_kernel<kF16, kSilu>, static_cast<const uint4*>(x),
                             static_cast<uint32_t>(items), K8, KB, static_cast<uint32_t>(KU), static_cast<uint2*>(q),
                             scale, gather, T, late, status);
 }
@@ -233,9 +235,9 @@ bool quant_block_fits(int64_t M, int64_t K) {
 
 cudaError_t launch_quant_block(const void* x, bool f16, bool silu, int64_t M, int64_t K, const int32_t* gather,
                                int64_t T, bool late, void* q, float* scale, unsigned int* status, cudaStream_t s) {
-  if (silu) return launch<false, true, 4>(x, M, K, gather, T, late, q, scale, status, s);
-  return f16 ? launch<true, false, 4>(x, M, K, gather, T, late, q, scale, status, s)
-             : launch<false, false, 4>(x, M, K, gather, T, late, q, scale, status, s);
+  if (silu) return launch<false, true>(x, M, K, gather, T, late, q, scale, status, s);
+  return f16 ? launch<true, false>(x, M, K, gather, T, late, q, scale, status, s)
+             : launch<false, false>(x, M, K, gather, T, late, q, scale, status, s);
 }
 
 cudaError_t launch_gather_block_rows(const void* src, const float* src_scale, int64_t T, int64_t K,
