@@ -5,8 +5,14 @@ function has the name of the C entry point it calls and only marshals
 arguments: it checks tensor shapes and dtypes, allocates outputs with PyTorch
 when the caller passes none, and passes raw device pointers plus the current
 CUDA stream. The fp8 block-scaled layer and its router, whose decode calls are
-shorter than that work takes in Python, do it in a compiled module. Every step of the computation runs in the library's kernels;
-there is no fallback. If ``libw4.so`` has not been built the first call raises.
+shorter than that work takes in Python, do it in a compiled module. Every step of
+the computation runs in the library's kernels; there is no fallback. If
+``libw4.so`` has not been built the first call raises.
+
+With ``stream=`` a call runs on that stream, and outputs and workspace that it
+allocates belong to it, as if the call were made under ``torch.cuda.stream``. As
+there, inputs have to be ready on that stream and stay alive until it is done.
+Outputs may be read on the caller's current stream once that waits for it.
 """
 from __future__ import annotations
 

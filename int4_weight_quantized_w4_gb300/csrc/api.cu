@@ -496,8 +496,8 @@ static w4_status run_fp8_block(const void* qx, const float* x_scale, const int32
 }
 
 // Codes of expert rows from which on tokens are quantized once and copied: the extra
-// launch costs 1 to 4 us, the rows' own quantization grows by 0.4 us a million (the
-// whole product, quantized by row / copied: 4 M codes 65.7 / 69.6 us, 14 M 42.6 /
+// launch costs 1 to 4 us, the rows' own quantization grows by 0.4 us a million (GPU time of
+// the whole product in a CUDA graph, quantized by row / copied: 4 M codes 65.7 / 69.6 us, 14 M 42.6 /
 // 44.1, 16 M 147.1 / 146.5, 58 M 64.8 / 53.1, 67 M 241 / 227).
 constexpr int64_t kCopyElements = int64_t{1} << 24;
 

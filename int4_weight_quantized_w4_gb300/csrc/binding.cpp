@@ -5,7 +5,8 @@
 // Grace host, and take 1 to 3 us here. Each function has the arguments of the
 // Python function of the package that calls it, streams as handles (or None: the
 // current stream of the tensors' device); wrong tensors raise ValueError before
-// the library is called, a status other than W4_OK raises W4Error.
+// the library is called, a status other than W4_OK raises W4Error. What a call
+// allocates belongs to its stream.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>

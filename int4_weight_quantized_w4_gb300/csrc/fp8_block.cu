@@ -10,23 +10,29 @@
 //
 // Two forms:
 //  * stream (few rows an expert or call): weights on the MMA's 128 rows (TMEM
-//    lane = output), NT tokens on its columns. Bound by the weight bytes (0.93 of copy
-//    bandwidth at 1 x 131072 x 2048, 42 us) and some 3.5 us a call (0.71 at 1 x
-//    14336 x 4096, 12.2 us). For up
-//    to kFuseRows dense rows the kernel quantizes 16-bit activations itself.
+//    lane = output), NT tokens on its columns. Bound by the weight bytes (0.92 of copy
+//    bandwidth at 1 x 131072 x 2048, 43 us) and some 3.5 us a call (0.67 at 1 x
+//    14336 x 4096, 12.9 us). For up to kFuseRows dense rows the kernel quantizes 16-bit
+//    activations itself.
 //  * tile (many rows): 128 tokens on the MMA's rows, 256 outputs on its columns,
 //    so that one scale sx * sw serves a thread's whole column strip. Bound by the
 //    hand-over and drain of one accumulator per block: about 920 cycles a block,
 //    of which the barriers' round trip takes some 450, the FMAs 290 (256 are their
-//    issue time) and the reads of tensor memory 100, where its MMAs take 512 and its
-//    48 KB of operands 860; and by 1.7 us a tile for its outputs, in which the MMAs
-//    stand still. 4096 x 11008 x 4096 takes 152 us after its quantizer, 2.4 PFLOP/s.
+//    issue time) and what shows of the reads of tensor memory 100 (256 by themselves),
+//    where its MMAs take 512 and its 48 KB of operands 860; and by 1.7 us a tile for
+//    its outputs, in which the MMAs stand still. 4096 x 11008 x 4096 takes 165 us with
+//    its quantizer, and 153 alone on an idle card, 2.4 PFLOP/s.
+//
+// Times in this file are GPU times of a call in a CUDA graph of calls on inputs that
+// rotate past L2; a pair is the two sides measured in one run. Large products vary by
+// some 5% with what the card's power limit leaves, and a chain of calls from Python is
+// within 10% of a graph (173 to 176 us at 4096 x 11008 x 4096).
 //
 // Both are launched as programmatic dependents and let their own dependents go
-// early: the copies of weights start while the kernel before finishes, everything
-// else (activations, scales, bias, y) waits for it, and so do the expert offsets
-// unless that kernel is the row quantizer, which starts this one only when all
-// before it is done.
+// early: the copies of weights start while the kernels before finish, everything
+// else (activations, scales, bias, y) waits for them, and so do the expert offsets
+// unless the one before is the row quantizer, which starts this one only when all
+// before it are done.
 #include <cuda.h>
 
 #include <atomic>

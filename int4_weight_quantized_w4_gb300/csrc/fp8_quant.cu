@@ -9,9 +9,9 @@
 // would move a block's scale by up to 2^-8 whenever it moved its maximum). The gate is
 // expf and a division that comes out as IEEE's but for rare last bits, and so does
 // x / s: of 369 M codes of normal gates and ups none differed from the formula's in IEEE
-// fp32 steps. Cheaper gates measured 13 to 28% less time and made codes wrong by fp64
-// where IEEE steps were right (and as many the other way around): ex2.approx in place of
-// expf 48 of the 369 M, the quotient g r unrefined as well 151.
+// fp32 steps. Cheaper gates took 13 and 28% less time than the first form of these and made
+// codes wrong by fp64 where IEEE steps were right (and about as many the other way around):
+// ex2.approx in place of expf 48 of the 369 M, the quotient g r unrefined as well 151.
 //
 // A block is 16 chunks of 8 elements: a half-warp holds it in registers, one
 // 16-byte load (two for gate and up) per lane. No row-wide reduction exists, so a
@@ -21,9 +21,10 @@
 // half-warp are reduced together, lanes trading one half of their values for the
 // other at each of the first steps, which leaves the maximum of unit l % kUnits
 // in lane l; each lane then divides once, for its unit, and the scales come back
-// by shuffles. 32768 x 2048 bf16 takes 33.8 us (0.88 of copy bandwidth), 4097 x 4096
-// 9.8 (0.76, of which 2 are the launch and the last wave); 32768 x 1408 silu 45.8,
-// bound by instruction issue.
+// by shuffles. 32768 x 2048 bf16 takes 33.2 us a call (0.90 of copy bandwidth), 4097 x 4096
+// 9.5 (0.79, of which 2 are the launch and the last wave); 32768 x 1408 silu 45.8 on normal
+// gates and ups, 48.7 with a column in a hundred 20 times larger, bound by instruction issue
+// (26 instructions an element).
 #include "common.cuh"
 #include "launch.h"
 
@@ -34,7 +35,7 @@ constexpr int kBlk8 = 16;       // 8-element chunks per block of 128 columns
 // Blocks of 128 columns a half-warp: with two, 32768 x 1408 silu took 53.5 us against 49.8,
 // and 32768 x 2048 bf16 42.0 against 34.5 (blocks of 256 threads).
 constexpr int kUnits = 4;
-constexpr int kThreads = 128;    // 4097 x 4096 9.8 us; blocks of 256 threads 10.1
+constexpr int kThreads = 128;    // 4097 x 4096 9.8 us against 10.1 in blocks of 256 threads
 constexpr unsigned kFull = 0xFFFFFFFFu;
 
 // -4 silu(g) * u = -g / D * u of the bf16 pairs g and u, D = (1 + exp(-g)) / 4: a
@@ -73,8 +74,8 @@ W4_DEV float neg_silu_mul(float g, float u) {
 // gather[r] (gather may be null: row r). An id outside [0, T) gives a zero row
 // with scales 1 and W4_ERR_SHAPE in the status word. KU = ceil(KB / kUnits). late:
 // the next kernel starts only when every kernel before this one is done.
-// At least seven silu blocks an SM: 45.8 us at 32768 x 1408 (six 47.0, eight 45.5,
-// by what the registers leave in flight).
+// At least seven silu blocks an SM: 45.8 us at 32768 x 1408 (six 47.0, eight 45.5 in the
+// same run, by what the registers leave in flight).
 template <bool kF16, bool kSilu>
 __global__ void __launch_bounds__(kThreads, kSilu ? 7 : 1) quant_block_kernel(const uint4* x, uint32_t items, int K8,
                                                                int KB, uint32_t KU, uint2* __restrict__ q,

@@ -23,8 +23,9 @@
 // tile's rows by token with bit masks. At most kMaxTiles tiles, one per SM: the
 // count table that every place CTA reads stays small. A call of up to a token per
 // warp of one CTA is one launch. Bound by instruction issue for many tokens (1270
-// warp instructions a token of 256 experts; 16384 of them 32 us, a quarter of it the
-// place kernel), by latency for few (one token 3.9 us, 333 of 96 experts 7.6).
+// warp instructions a token of 256 experts; 16384 of them 33 us, a quarter of it the
+// place kernel), by latency for few (one token 3.9 us, 333 of 96 experts 8). Times are
+// GPU times in a CUDA graph of calls.
 #include "common.cuh"
 #include "launch.h"
 
