@@ -122,10 +122,12 @@ W4_DEV void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "me
 
 // First row tile of every expert (tiles of `rows_per` rows), in shared memory:
 // starts[e], starts[E] = the total. All threads of the block take part; at
-// most kMaxExperts experts. A segment outside [0, rows) counts as clipped.
+// most kMaxExperts experts. A segment outside [0, rows) counts as clipped. The offsets
+// are read from L2, where the kernel that wrote them left them: with offsets_ready this
+// one has not waited for the kernels before yet.
 W4_DEV void seg_bounds(const Params& p, int e, int& a, int& b) {
-  a = max(p.offsets[e], 0);
-  b = min(p.offsets[e + 1], p.rows);
+  a = max(__ldcg(p.offsets + e), 0);
+  b = min(__ldcg(p.offsets + e + 1), p.rows);
 }
 template <int kThreads>
 W4_DEV void tile_starts(const Params& p, int rows_per, int32_t* starts, int32_t* warp_sum) {

@@ -201,3 +201,13 @@ def test_block_quant_of_too_many_rows_is_unsupported(lib):
     for M, K in ((1 << 31, 8), (1 << 31, 512), (1 << 30, 1032), (1 << 40, 128)):
         assert lib.w4_quant_act_per_block(FAKE, w4.W4_BF16, M, K, FAKE, FAKE, None) == w4.W4_ERR_UNSUPPORTED
         assert lib.w4_silu_mul_quant_block(FAKE, M, K, FAKE, FAKE, None) == w4.W4_ERR_UNSUPPORTED
+
+
+def test_expert_offsets_are_read_from_l2():
+    """The expert products may read the offsets before they have waited for the kernels
+    before them (the quantizer starts them only when the routing is done), so that an L1 line
+    of an earlier routing must not answer."""
+    with open(os.path.join(_build.CSRC, "fp8_block.cu")) as f:
+        text = f.read()
+    assert "__ldcg(p.offsets" in text
+    assert not re.findall(r"p\.offsets\s*\[|\*\s*p\.offsets", text)
