@@ -75,8 +75,15 @@ typedef enum {
   W4_OP_MOE_ROUTE = 2,      /* w4_moe_route (M = T tokens, N = E experts; K = 1, group ignored) */
   W4_OP_MOE_ROUTE_GROUPED = 3, /* w4_moe_route_grouped (M = T tokens, N = E experts; K = 1, group ignored) */
   W4_OP_FP8_BLOCK = 4,      /* w4_fp8_block_gemm (group ignored) */
-  W4_OP_FP8_BLOCK_IN = 5    /* w4_fp8_block_gemm_bf16in (group = 0), w4_fp8_block_moe_gemm_bf16in (M = R rows, group = E) */
+  W4_OP_FP8_BLOCK_IN = 5,   /* w4_fp8_block_gemm_bf16in (group = 0), w4_fp8_block_moe_gemm_bf16in (M = R rows, group = E) */
+  W4_OP_FP4_IN = 6          /* w4_fp4_gemm_bf16in, w4_fp4_moe_gemm_bf16in (M = rows, group = 16 or 32: the format's block) */
 } w4_op;
+
+/* 4-bit weight formats. */
+typedef enum {
+  W4_FMT_MXFP4 = 0,  /* e2m1, a power of two (e8m0) per 32 columns */
+  W4_FMT_NVFP4 = 1   /* e2m1, an e4m3 scale per 16 columns, an fp32 scale per tensor */
+} w4_format;
 
 /* Router scores of w4_moe_route_grouped. */
 typedef enum {
@@ -222,9 +229,9 @@ w4_status w4a8_gemm_bf16in(const void* x, const void* qweight, const void* w_sca
  * written by a kernel that signals its dependents early, unless a kernel that
  * does not, or a synchronization, stands between the two on the stream (one
  * early signaller after another lets this kernel start while the first still
- * runs). Early signallers are this kernel and those of the fp8 block-scaled
- * layer; every other kernel of this library, and ordinary library kernels, are
- * waited for in full.
+ * runs). Early signallers are this kernel, those of the fp8 block-scaled
+ * layer and those of the 4-bit floating point products; every other kernel of this
+ * library, and ordinary library kernels, are waited for in full.
  */
 w4_status w4a16_gemm(const void* x, const void* qweight, const void* w_scale, int32_t w_scale_dtype,
                      const void* zeros, int32_t group, const void* bias, void* y,
@@ -482,6 +489,89 @@ w4_status w4_fp8_block_moe_grouped_gemm(const void* qx, const float* x_scale, co
 w4_status w4_fp8_block_moe_gemm_bf16in(const void* x, int64_t T, const int32_t* row_token, const int32_t* expert_offsets,
                                        int32_t E, const void* qweight, const float* w_scale, void* y, int64_t R,
                                        int64_t N, int64_t K, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Microscaled 4-bit floating point (no counterpart on the source pages). Codes are
+ * e2m1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and, with the high bit, their negatives; two codes a byte,
+ * the lower column in the low half. Every row has a scale per block of columns, in
+ * row-major order, as checkpoints hold them:
+ *     W4_FMT_MXFP4: blocks of 32, scale 2^(byte - 127) (e8m0; 255 is NaN);
+ *     W4_FMT_NVFP4: blocks of 16, scale e4m3 times an fp32 scale of the whole
+ *                   tensor, which is a device scalar (`global`; NULL: 1; must be NULL
+ *                   for mxfp4, else W4_ERR_UNSUPPORTED).
+ *
+ * w4_quant_fp4: x [M, K] bf16 or fp16 to codes q [M, K/2] bytes and scale [M, K/32]
+ * (mxfp4) or [M, K/16] (nvfp4) bytes, activations or weights alike. With amax
+ * the block's largest magnitude, every step in fp32 with IEEE rounding:
+ *     mxfp4: e = clamp(floor(log2 amax) - 2, -127, 127) (-127 for a block of zeros),
+ *            q = e2m1(x 2^-e);
+ *     nvfp4: s = e4m3(fl(fl(amax / 6) / global)), d = fl(s global), q = e2m1(fl(x / d)), 0 where d = 0;
+ * e2m1 and e4m3 round to nearest even and hold at the largest magnitude (6, 448). A
+ * block that holds a NaN or an infinity gets a NaN scale and codes 0, so that the row of
+ * a product is NaN. global must be positive and finite. K % 32 == 0 (W4_ERR_UNSUPPORTED
+ * for other multiples of 8); x and q 16-byte aligned, global 4-byte.
+ *
+ * w4_silu_mul_quant_fp4: the same of fl(fl(g / fl(1 + expf(-g))) u) for h [R, 2I] bf16, g its
+ * first I columns and u the others; I % 32 == 0.
+ *
+ * w4_dequant_fp4: out [M, K] (out_dtype W4_BF16 or W4_FP16) = code times scale (nvfp4: times
+ * fl(scale global)) in fp32, rounded once.
+ */
+w4_status w4_quant_fp4(const void* x, int32_t x_dtype, int32_t format, const float* global, int64_t M, int64_t K,
+                       void* q, void* scale, void* stream);
+w4_status w4_silu_mul_quant_fp4(const void* h, int32_t format, const float* global, int64_t R, int64_t I, void* q,
+                                void* scale, void* stream);
+w4_status w4_dequant_fp4(const void* q, const void* scale, int32_t format, const float* global, int64_t M, int64_t K,
+                         int32_t out_dtype, void* out, void* stream);
+
+/*
+ * w4_fp4_gemm: both operands in the same 4-bit format,
+ *     y[m, n] = bf16( x_global w_global sum_b x_scale[m, b] w_scale[n, b] sum_{k in b} qx[m, k] qw[n, k] + bias[n] ),
+ * products exact, sums in fp32 on the tensor cores.
+ *   qx       [M, K/2] bytes, x_scale [M, K/32 or K/16] bytes
+ *   qweight  [N, K/2] bytes, w_scale [N, K/32 or K/16] bytes
+ *   x_global, w_global  device fp32 scalars (nvfp4) or NULL
+ *   bias     [N] bf16 or NULL         y       [M, N] bf16
+ * N % 8 == 0; rows of scales are whole 32-bit words: K % 128 == 0 (mxfp4) or K % 64 == 0
+ * (nvfp4), else W4_ERR_UNSUPPORTED. Matrices and the bias are 16-byte aligned, scales
+ * 4-byte. Few rows take a form that streams the weights once; M == 1 is the decode call.
+ * Sums are taken in a fixed order: a call's outputs are the same every time.
+ *
+ * w4_fp4_gemm_bf16in: x [M, K] bf16 or fp16, quantized as w4_quant_fp4 does into the
+ * workspace (at least w4_workspace_bytes(W4_OP_FP4_IN, M, N, K, 16 or 32) bytes, 16-byte
+ * aligned), then w4_fp4_gemm; y equals the two calls' bit for bit.
+ *
+ * w4_fp4_moe_grouped_gemm: the product over expert-sorted rows, as
+ * w4afp8_moe_grouped_gemm takes them: rows [offsets[e], offsets[e+1]) of qx [R, K/2] times
+ * expert e of qweight [E, N, K/2], w_scale [E, N, K/32 or K/16]; w_global [E] or NULL; y [R, N]
+ * bf16. 1 <= E <= 1024. Offsets live on the device and are not validated; rows outside
+ * [0, R) and rows of no expert are not written.
+ *
+ * w4_fp4_moe_gemm_bf16in: row r is token row_token[r] of x [T, K] bf16 (row_token NULL: R
+ * == T and row r is token r), quantized into the workspace
+ * (w4_workspace_bytes(W4_OP_FP4_IN, R, N, K, 16 or 32) bytes), then
+ * w4_fp4_moe_grouped_gemm. A row_token entry outside [0, T) gives a zero row and sets
+ * W4_ERR_SHAPE in the device status word.
+ *
+ * The products are launched as programmatic dependents that start streaming weights and
+ * their scales early, and let their own dependents go early, as w4a16_gemm does; the rule
+ * given there for what may write weights holds for qweight, w_scale and w_global too.
+ * The quantizers above are waited for in full, so a weight may be quantized right before.
+ */
+w4_status w4_fp4_gemm(const void* qx, const void* x_scale, const float* x_global, const void* qweight,
+                      const void* w_scale, const float* w_global, int32_t format, const void* bias, void* y, int64_t M,
+                      int64_t N, int64_t K, void* stream);
+w4_status w4_fp4_gemm_bf16in(const void* x, int32_t x_dtype, const float* x_global, const void* qweight,
+                             const void* w_scale, const float* w_global, int32_t format, const void* bias, void* y,
+                             int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes, void* stream);
+w4_status w4_fp4_moe_grouped_gemm(const void* qx, const void* x_scale, const float* x_global,
+                                  const int32_t* expert_offsets, int32_t E, const void* qweight, const void* w_scale,
+                                  const float* w_global, int32_t format, void* y, int64_t R, int64_t N, int64_t K,
+                                  void* stream);
+w4_status w4_fp4_moe_gemm_bf16in(const void* x, int64_t T, const float* x_global, const int32_t* row_token,
+                                 const int32_t* expert_offsets, int32_t E, const void* qweight, const void* w_scale,
+                                 const float* w_global, int32_t format, void* y, int64_t R, int64_t N, int64_t K,
+                                 void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Weight-side tools (load time, not on the per-token path).

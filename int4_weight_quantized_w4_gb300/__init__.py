@@ -31,17 +31,20 @@ __all__ = [
     "w4_moe_combine", "w4_moe_route_grouped",
     "w4_quant_act_per_block", "w4_silu_mul_quant_block", "w4_fp8_block_gemm", "w4_fp8_block_gemm_bf16in",
     "w4_fp8_block_moe_grouped_gemm", "w4_fp8_block_moe_gemm_bf16in",
+    "w4_quant_fp4", "w4_silu_mul_quant_fp4", "w4_dequant_fp4", "w4_fp4_gemm", "w4_fp4_gemm_bf16in",
+    "w4_fp4_moe_grouped_gemm", "w4_fp4_moe_gemm_bf16in",
     "w4_device_status", "w4_selftest_bounded_wait", "apply_weights", "MIN_TOKENS_FOR_INT8",
     "W4_OK", "W4_ERR_NULL", "W4_ERR_ALIGN", "W4_ERR_GROUP", "W4_ERR_DTYPE",
     "W4_ERR_UNSUPPORTED", "W4_ERR_SHAPE", "W4_ERR_CUDA", "W4_ERR_TIMEOUT", "W4_ERR_WORKSPACE",
-    "W4_OP_W4A8", "W4_OP_W4AFP8_MOE", "W4_OP_MOE_ROUTE", "W4_OP_MOE_ROUTE_GROUPED", "W4_OP_FP8_BLOCK", "W4_OP_FP8_BLOCK_IN", "w4_workspace_bytes", "EXPORTED_SYMBOLS",
+    "W4_OP_W4A8", "W4_OP_W4AFP8_MOE", "W4_OP_MOE_ROUTE", "W4_OP_MOE_ROUTE_GROUPED", "W4_OP_FP8_BLOCK", "W4_OP_FP8_BLOCK_IN", "W4_OP_FP4_IN", "w4_workspace_bytes", "EXPORTED_SYMBOLS",
 ]
 
 (W4_OK, W4_ERR_NULL, W4_ERR_ALIGN, W4_ERR_GROUP, W4_ERR_DTYPE, W4_ERR_UNSUPPORTED,
  W4_ERR_SHAPE, W4_ERR_CUDA, W4_ERR_TIMEOUT, W4_ERR_WORKSPACE) = range(10)
 W4_BF16, W4_FP16, W4_INT8, W4_FP8_E4M3 = range(4)
-W4_OP_W4A8, W4_OP_W4AFP8_MOE, W4_OP_MOE_ROUTE, W4_OP_MOE_ROUTE_GROUPED, W4_OP_FP8_BLOCK, W4_OP_FP8_BLOCK_IN = range(6)
+W4_OP_W4A8, W4_OP_W4AFP8_MOE, W4_OP_MOE_ROUTE, W4_OP_MOE_ROUTE_GROUPED, W4_OP_FP8_BLOCK, W4_OP_FP8_BLOCK_IN, W4_OP_FP4_IN = range(7)
 W4_SCORE_SIGMOID, W4_SCORE_SOFTMAX = range(2)
+W4_FMT_MXFP4, W4_FMT_NVFP4 = range(2)
 
 _DIR = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_DIR, "libw4.so")
@@ -77,6 +80,13 @@ _SIGNATURES = {
     "w4_fp8_block_gemm_bf16in": (_I32, [_P, _I32, _P, _P, _P, _P, _I64, _I64, _I64, _P, _SZ, _P]),
     "w4_fp8_block_moe_grouped_gemm": (_I32, [_P, _P, _P, _I32, _P, _P, _P, _I64, _I64, _I64, _P]),
     "w4_fp8_block_moe_gemm_bf16in": (_I32, [_P, _I64, _P, _P, _I32, _P, _P, _P, _I64, _I64, _I64, _P, _SZ, _P]),
+    "w4_quant_fp4": (_I32, [_P, _I32, _I32, _P, _I64, _I64, _P, _P, _P]),
+    "w4_silu_mul_quant_fp4": (_I32, [_P, _I32, _P, _I64, _I64, _P, _P, _P]),
+    "w4_dequant_fp4": (_I32, [_P, _P, _I32, _P, _I64, _I64, _I32, _P, _P]),
+    "w4_fp4_gemm": (_I32, [_P, _P, _P, _P, _P, _P, _I32, _P, _P, _I64, _I64, _I64, _P]),
+    "w4_fp4_gemm_bf16in": (_I32, [_P, _I32, _P, _P, _P, _P, _I32, _P, _P, _I64, _I64, _I64, _P, _SZ, _P]),
+    "w4_fp4_moe_grouped_gemm": (_I32, [_P, _P, _P, _P, _I32, _P, _P, _P, _I32, _P, _I64, _I64, _I64, _P]),
+    "w4_fp4_moe_gemm_bf16in": (_I32, [_P, _I64, _P, _P, _P, _I32, _P, _P, _P, _I32, _P, _I64, _I64, _I64, _P, _SZ, _P]),
     "w4_last_error": (ctypes.c_char_p, []),
     "w4_status_string": (ctypes.c_char_p, [_I32]),
     "w4_device_status": (_I32, [_P]),
@@ -499,6 +509,76 @@ def w4_fp8_block_moe_gemm_bf16in(x, row_token, expert_offsets, qweight, w_scale,
     ``x[row_token[r]]`` (``row_token`` None: row r is token r), quantized per block
     inside the call. Returns bf16 ``[R, N]``."""
     return _native().moe_gemm_act(x, row_token, expert_offsets, qweight, w_scale, y, workspace, _handle(stream))
+
+
+_FORMATS = {"mxfp4": W4_FMT_MXFP4, "nvfp4": W4_FMT_NVFP4}
+
+
+def _fp4_format(name):
+    if name not in _FORMATS:
+        raise ValueError("format must be 'mxfp4' or 'nvfp4'")
+    return _FORMATS[name]
+
+
+def w4_quant_fp4(x, format: str, global_scale=None, q=None, scale=None, stream=None):
+    """Microscaled 4-bit floats of bf16 or fp16 ``x [M, K]`` (weights or activations):
+    ``(q uint8 [M, K/2], scale [M, K/32] or [M, K/16])``, two e2m1 codes a byte, the
+    lower column in the low half. ``format`` is ``"mxfp4"`` (a power of two,
+    float8_e8m0fnu, per 32 columns) or ``"nvfp4"`` (float8_e4m3fn per 16 columns, times
+    the fp32 ``global_scale`` of the whole tensor; None: 1). A calibrated
+    ``global_scale`` is the tensor's largest magnitude over 6 * 448."""
+    return _native().quant_fp4(x, _fp4_format(format), global_scale, q, scale, False, _handle(stream))
+
+
+def w4_silu_mul_quant_fp4(h, format: str, global_scale=None, q=None, scale=None, stream=None):
+    """``silu(gate) * up`` of the bf16 gate_up output ``h [R, 2I]`` as ``w4_quant_fp4``
+    quantizes it; returns ``(q [R, I/2], scale)``."""
+    return _native().quant_fp4(h, _fp4_format(format), global_scale, q, scale, True, _handle(stream))
+
+
+def w4_dequant_fp4(q, scale, format: str, global_scale=None, dtype=torch.bfloat16, out=None, stream=None):
+    """The values that 4-bit codes stand for, bf16 or fp16 ``[M, K]``."""
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("dtype must be torch.bfloat16 or torch.float16")
+    return _native().dequant_fp4(q, scale, _fp4_format(format), global_scale, dtype == torch.float16, out,
+                                 _handle(stream))
+
+
+def w4_fp4_gemm(qx, x_scale, qweight, w_scale, format: str, x_global=None, w_global=None, bias=None, y=None,
+                stream=None):
+    """4-bit floating point linear: ``qx [M, K/2]`` with ``x_scale`` times ``qweight [N,
+    K/2]`` with ``w_scale`` (both as ``w4_quant_fp4`` gives them), times the fp32 scalars
+    ``x_global`` and ``w_global`` (nvfp4), plus an optional bf16 ``bias [N]``; returns
+    bf16 ``[M, N]``."""
+    return _native().fp4_gemm(qx, x_scale, qweight, w_scale, _fp4_format(format), x_global, w_global, bias, y,
+                              _handle(stream))
+
+
+def w4_fp4_gemm_bf16in(x, qweight, w_scale, format: str, x_global=None, w_global=None, bias=None, y=None,
+                       workspace=None, stream=None):
+    """``w4_fp4_gemm`` from bf16 or fp16 ``x [M, K]``, quantized inside the call; returns
+    bf16 ``[M, N]``. One token is the decode call."""
+    return _native().fp4_gemm_act(x, qweight, w_scale, _fp4_format(format), x_global, w_global, bias, y, workspace,
+                                  _handle(stream))
+
+
+def w4_fp4_moe_grouped_gemm(qx, x_scale, expert_offsets, qweight, w_scale, format: str, x_global=None, w_global=None,
+                            y=None, stream=None):
+    """Grouped expert linear on 4-bit floating point weights: ``qx [R, K/2]`` (rows grouped
+    by expert) with ``x_scale``, int32 device ``expert_offsets [E+1]``, ``qweight [E, N,
+    K/2]`` with ``w_scale [E, N, K/block]`` and fp32 ``w_global [E]`` (nvfp4); returns bf16
+    ``[R, N]``."""
+    return _native().fp4_moe_gemm(qx, x_scale, expert_offsets, qweight, w_scale, _fp4_format(format), x_global,
+                                  w_global, y, _handle(stream))
+
+
+def w4_fp4_moe_gemm_bf16in(x, row_token, expert_offsets, qweight, w_scale, format: str, x_global=None, w_global=None,
+                           y=None, workspace=None, stream=None):
+    """``w4_fp4_moe_grouped_gemm`` from bf16 token rows: row r is ``x[row_token[r]]``
+    (``row_token`` None: row r is token r), quantized inside the call. Returns bf16
+    ``[R, N]``."""
+    return _native().fp4_moe_gemm_act(x, row_token, expert_offsets, qweight, w_scale, _fp4_format(format), x_global,
+                                      w_global, y, workspace, _handle(stream))
 
 
 def w4_moe_gather_quant_fp8(x, row_token, q=None, scale=None, stream=None):

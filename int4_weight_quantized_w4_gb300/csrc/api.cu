@@ -139,6 +139,7 @@ size_t w4_workspace_bytes(int32_t op, int64_t M, int64_t N, int64_t K, int32_t g
     return w4::fp8_block_workspace_bytes(M, K) +
            (group > 0 ? w4::fp8_block_workspace_bytes(M / 2, K) : w4::fp8_block_part_bytes(M, N, K));
   }
+  if (op == W4_OP_FP4_IN) return (group == 16 || group == 32) && K % group == 0 ? w4::fp4_workspace_bytes(M, K, group == 16) : 0;
   if (op == W4_OP_MOE_ROUTE) return (N > 0 && N <= 1024) ? w4::moe_route_workspace_bytes(M, static_cast<int32_t>(N)) : 0;
   return 0;
 }
@@ -582,6 +583,156 @@ w4_status w4_fp8_block_moe_gemm_bf16in(const void* x, int64_t T, const int32_t* 
   if (!expert_offsets) return fail(W4_ERR_NULL, "expert_offsets must be non-NULL");
   return run_fp8_block_act(x, false, T, row_token, expert_offsets, E, qweight, w_scale, nullptr, y, R, N, K, workspace,
                            workspace_bytes, stream);
+}
+
+// Checks shared by the 4-bit floating point calls.
+static w4_status check_fp4_format(int32_t format, const float* a, const float* b) {
+  if (format != W4_FMT_MXFP4 && format != W4_FMT_NVFP4) return fail(W4_ERR_DTYPE, "format must be W4_FMT_MXFP4 or W4_FMT_NVFP4");
+  if (format == W4_FMT_MXFP4 && (a != nullptr || b != nullptr)) return fail(W4_ERR_UNSUPPORTED, "mxfp4 has no scale per tensor");
+  if (!aligned(a, 4) || !aligned(b, 4)) return fail(W4_ERR_ALIGN, "scales per tensor must be 4-byte aligned");
+  return W4_OK;
+}
+static w4_status check_fp4_rows(int64_t M, int64_t K) {
+  if (M < 0 || K <= 0) return fail(W4_ERR_SHAPE, "sizes must be M >= 0, K > 0 (M=%lld K=%lld)", (long long)M, (long long)K);
+  if (K % 8 != 0) return fail(W4_ERR_ALIGN, "K must be a multiple of 8, got %lld", (long long)K);
+  if (K % 32 != 0) return fail(W4_ERR_UNSUPPORTED, "rows of 4-bit floats are multiples of 32: K=%lld", (long long)K);
+  if (K > INT32_MAX / 2 || !w4::quant_fp4_fits(M, K)) return fail(W4_ERR_UNSUPPORTED, "M or K too large");
+  return W4_OK;
+}
+
+w4_status w4_quant_fp4(const void* x, int32_t x_dtype, int32_t format, const float* global, int64_t M, int64_t K,
+                       void* q, void* scale, void* stream) {
+  if (x_dtype != W4_BF16 && x_dtype != W4_FP16) return fail(W4_ERR_DTYPE, "x_dtype must be W4_BF16 or W4_FP16");
+  w4_status st = check_fp4_format(format, global, nullptr);
+  if (st == W4_OK) st = check_fp4_rows(M, K);
+  if (st != W4_OK) return st;
+  if (M == 0) return ok();
+  if (!x || !q || !scale) return fail(W4_ERR_NULL, "x, q and scale must be non-NULL");
+  if (!aligned(x, 16) || !aligned(q, 16)) return fail(W4_ERR_ALIGN, "x and q must be 16-byte aligned");
+  const w4::QuantFp4Args a{x, format == W4_FMT_NVFP4, x_dtype == W4_FP16, false, M, K, global, nullptr, 0, false, q, scale, nullptr};
+  return from_cuda(w4::launch_quant_fp4(a, static_cast<cudaStream_t>(stream)), "w4_quant_fp4 launch");
+}
+
+w4_status w4_silu_mul_quant_fp4(const void* h, int32_t format, const float* global, int64_t R, int64_t I, void* q,
+                                void* scale, void* stream) {
+  w4_status st = check_fp4_format(format, global, nullptr);
+  if (st == W4_OK) st = check_fp4_rows(R, I);
+  if (st != W4_OK) return st;
+  if (R == 0) return ok();
+  if (!h || !q || !scale) return fail(W4_ERR_NULL, "h, q and scale must be non-NULL");
+  if (!aligned(h, 16) || !aligned(q, 16)) return fail(W4_ERR_ALIGN, "h and q must be 16-byte aligned");
+  const w4::QuantFp4Args a{h, format == W4_FMT_NVFP4, false, true, R, I, global, nullptr, 0, false, q, scale, nullptr};
+  return from_cuda(w4::launch_quant_fp4(a, static_cast<cudaStream_t>(stream)), "w4_silu_mul_quant_fp4 launch");
+}
+
+w4_status w4_dequant_fp4(const void* q, const void* scale, int32_t format, const float* global, int64_t M, int64_t K,
+                         int32_t out_dtype, void* out, void* stream) {
+  if (out_dtype != W4_BF16 && out_dtype != W4_FP16) return fail(W4_ERR_DTYPE, "out_dtype must be W4_BF16 or W4_FP16");
+  w4_status st = check_fp4_format(format, global, nullptr);
+  if (st == W4_OK) st = check_fp4_rows(M, K);
+  if (st != W4_OK) return st;
+  if (M == 0) return ok();
+  if (!q || !scale || !out) return fail(W4_ERR_NULL, "q, scale and out must be non-NULL");
+  if (!aligned(q, 16) || !aligned(out, 16)) return fail(W4_ERR_ALIGN, "q and out must be 16-byte aligned");
+  return from_cuda(w4::launch_dequant_fp4(q, scale, global, format == W4_FMT_NVFP4, out_dtype == W4_FP16, M, K, out,
+                                          static_cast<cudaStream_t>(stream)),
+                   "w4_dequant_fp4 launch");
+}
+
+// Checks shared by the 4-bit floating point products.
+static w4_status check_fp4_gemm(int32_t format, const float* x_global, const float* w_global, int64_t R, int64_t N,
+                                int64_t K, int32_t E, bool experts) {
+  w4_status st = check_fp4_format(format, x_global, w_global);
+  if (st != W4_OK) return st;
+  if (R < 0 || N <= 0 || K <= 0) return fail(W4_ERR_SHAPE, "sizes must be M >= 0, N > 0, K > 0 (M=%lld N=%lld K=%lld)",
+                                             (long long)R, (long long)N, (long long)K);
+  if (experts && E <= 0) return fail(W4_ERR_SHAPE, "E must be > 0");
+  if (N % 8 != 0 || K % 8 != 0)
+    return fail(W4_ERR_ALIGN, "N and K must be multiples of 8, got N=%lld K=%lld", (long long)N, (long long)K);
+  const int unit = format == W4_FMT_NVFP4 ? 64 : 128;
+  if (K % unit != 0) return fail(W4_ERR_UNSUPPORTED, "rows of scales are whole 32-bit words: K=%lld is not a multiple of %d", (long long)K, unit);
+  if (experts && E > 1024) return fail(W4_ERR_UNSUPPORTED, "E must be at most 1024, got %d", E);
+  if (R > INT32_MAX / 2 || N > INT32_MAX / 2 || K > INT32_MAX / 2 || !w4::quant_fp4_fits(R, K)) return fail(W4_ERR_UNSUPPORTED, "M, N or K too large");
+  return W4_OK;
+}
+
+static w4_status run_fp4(w4::Fp4Args a, void* stream) {
+  if (!a.qx || !a.x_scale || !a.qweight || !a.w_scale || !a.y) return fail(W4_ERR_NULL, "required pointer is NULL");
+  if (!aligned(a.qx, 16) || !aligned(a.qweight, 16) || !aligned(a.y, 16) || !aligned(a.x_scale, 4) || !aligned(a.w_scale, 4) ||
+      !aligned(a.expert_offsets, 4) || !aligned(a.bias, 16))
+    return fail(W4_ERR_ALIGN, "matrices and the bias must be 16-byte aligned, scales and offsets 4-byte aligned");
+  const cudaError_t e = status_ptr(&a.status);
+  if (e != cudaSuccess) return from_cuda(e, "device status word");
+  return from_cuda(w4::launch_fp4(a, static_cast<cudaStream_t>(stream)), "fp4 product launch");
+}
+
+// Quantizes rows of x (gathered by `rows` when given) into the workspace, then multiplies (a.qx, a.x_scale unset).
+static w4_status run_fp4_act(const void* x, bool f16, int64_t T, const int32_t* rows, w4::Fp4Args a, void* ws,
+                             size_t ws_bytes, void* stream) {
+  if (!x || !a.qweight || !a.w_scale || !a.y) return fail(W4_ERR_NULL, "required pointer is NULL");
+  if (!aligned(x, 16) || !aligned(rows, 4) || !aligned(a.qweight, 16) || !aligned(a.y, 16) || !aligned(a.w_scale, 4) ||
+      !aligned(a.expert_offsets, 4) || !aligned(a.bias, 16))
+    return fail(W4_ERR_ALIGN, "matrices and the bias must be 16-byte aligned, scales, rows and offsets 4-byte aligned");
+  const size_t need = w4::fp4_workspace_bytes(a.R, a.K, a.nv);
+  if (ws == nullptr || ws_bytes < need || !aligned(ws, 16))
+    return fail(W4_ERR_WORKSPACE, "workspace must be 16-byte aligned and at least %zu bytes (got %zu)", need, ws_bytes);
+  unsigned int* status = nullptr;
+  cudaError_t e = status_ptr(&status);
+  if (e != cudaSuccess) return from_cuda(e, "device status word");
+  uint8_t* scale = static_cast<uint8_t*>(ws) + w4::fp4_code_bytes(a.R, a.K);
+  const w4::QuantFp4Args q{x, a.nv, f16, false, a.R, a.K, a.x_global, rows, T, true, ws, scale, status};
+  e = w4::launch_quant_fp4(q, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return from_cuda(e, "fp4 quant launch");
+  a.qx = ws;
+  a.x_scale = scale;
+  return run_fp4(a, stream);
+}
+
+w4_status w4_fp4_gemm(const void* qx, const void* x_scale, const float* x_global, const void* qweight,
+                      const void* w_scale, const float* w_global, int32_t format, const void* bias, void* y, int64_t M,
+                      int64_t N, int64_t K, void* stream) {
+  w4_status st = check_fp4_gemm(format, x_global, w_global, M, N, K, 1, false);
+  if (st != W4_OK) return st;
+  if (M == 0) return ok();
+  return run_fp4({qx, x_scale, qweight, w_scale, format == W4_FMT_NVFP4, x_global, w_global, bias, y, nullptr, 1, M, N, K, nullptr}, stream);
+}
+
+w4_status w4_fp4_gemm_bf16in(const void* x, int32_t x_dtype, const float* x_global, const void* qweight,
+                             const void* w_scale, const float* w_global, int32_t format, const void* bias, void* y,
+                             int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes, void* stream) {
+  w4_status st = check_fp4_gemm(format, x_global, w_global, M, N, K, 1, false);
+  if (st != W4_OK) return st;
+  if (x_dtype != W4_BF16 && x_dtype != W4_FP16) return fail(W4_ERR_DTYPE, "x_dtype must be W4_BF16 or W4_FP16");
+  if (M == 0) return ok();
+  return run_fp4_act(x, x_dtype == W4_FP16, M, nullptr,
+                     {nullptr, nullptr, qweight, w_scale, format == W4_FMT_NVFP4, x_global, w_global, bias, y, nullptr, 1, M, N, K, nullptr},
+                     workspace, workspace_bytes, stream);
+}
+
+w4_status w4_fp4_moe_grouped_gemm(const void* qx, const void* x_scale, const float* x_global,
+                                  const int32_t* expert_offsets, int32_t E, const void* qweight, const void* w_scale,
+                                  const float* w_global, int32_t format, void* y, int64_t R, int64_t N, int64_t K,
+                                  void* stream) {
+  w4_status st = check_fp4_gemm(format, x_global, w_global, R, N, K, E, true);
+  if (st != W4_OK) return st;
+  if (R == 0) return ok();
+  if (!expert_offsets) return fail(W4_ERR_NULL, "expert_offsets must be non-NULL");
+  return run_fp4({qx, x_scale, qweight, w_scale, format == W4_FMT_NVFP4, x_global, w_global, nullptr, y, expert_offsets, E, R, N, K, nullptr}, stream);
+}
+
+w4_status w4_fp4_moe_gemm_bf16in(const void* x, int64_t T, const float* x_global, const int32_t* row_token,
+                                 const int32_t* expert_offsets, int32_t E, const void* qweight, const void* w_scale,
+                                 const float* w_global, int32_t format, void* y, int64_t R, int64_t N, int64_t K,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+  w4_status st = check_fp4_gemm(format, x_global, w_global, R, N, K, E, true);
+  if (st != W4_OK) return st;
+  if (T < 0) return fail(W4_ERR_SHAPE, "T must be >= 0");
+  if (row_token == nullptr && R != T) return fail(W4_ERR_SHAPE, "without row_token R must equal T");
+  if (R == 0) return ok();
+  if (!expert_offsets) return fail(W4_ERR_NULL, "expert_offsets must be non-NULL");
+  return run_fp4_act(x, false, T, row_token,
+                     {nullptr, nullptr, qweight, w_scale, format == W4_FMT_NVFP4, x_global, w_global, nullptr, y, expert_offsets, E, R, N, K, nullptr},
+                     workspace, workspace_bytes, stream);
 }
 
 w4_status w4_moe_gather_quant_fp8(const void* x, int64_t T, int64_t K, const int32_t* row_token, int64_t R,

@@ -1,5 +1,5 @@
-// Compiled half of the Python binding for the fp8 block-scaled layer and the
-// grouped router: checks the tensors, allocates outputs and workspace that were not
+// Compiled half of the Python binding for the fp8 block-scaled and 4-bit floating
+// point layers and the grouped router: checks the tensors, allocates outputs and workspace that were not
 // passed in, and calls the C entry points. A decode call's kernels take 5 to 15 us
 // on a GB300; the same checks and allocations in Python took 10 to 18 us on its
 // Grace host, and take 1 to 3 us here. Each function has the arguments of the
@@ -34,6 +34,9 @@ const Types kBf16 = {ScalarType::BFloat16};
 const Types kF32 = {ScalarType::Float};
 const Types kI32 = {ScalarType::Int};
 const Types kAct = {ScalarType::BFloat16, ScalarType::Half};
+const Types kByte = {ScalarType::Byte};
+const Types kScaleMx = {ScalarType::Float8_e8m0fnu, ScalarType::Byte};
+const Types kScaleNv = {ScalarType::Float8_e4m3fn, ScalarType::Byte};
 const Types kLogit = {ScalarType::BFloat16, ScalarType::Float};
 
 [[noreturn]] void value_error(const char* fmt, ...) {
@@ -392,10 +395,180 @@ PyObject* moe_gemm_act(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// ---- 4-bit floating point ----
+
+// W4_FMT_MXFP4 or W4_FMT_NVFP4, as the Python side checked it.
+struct Format {
+  int32_t id;
+  int64_t block;
+  const Types& scales;
+  ScalarType scale;
+};
+Format format(PyObject* o) {
+  const bool nv = integer(o) == W4_FMT_NVFP4;
+  return {nv ? W4_FMT_NVFP4 : W4_FMT_MXFP4, nv ? 16 : 32, nv ? kScaleNv : kScaleMx, nv ? ScalarType::Float8_e4m3fn : ScalarType::Float8_e8m0fnu};
+}
+const float* global_scale(PyObject* o, const char* name, int64_t n, const at::Device& dev) {
+  if (o == Py_None) return nullptr;
+  const at::Tensor& t = tensor(o, name, kF32, &dev);
+  if (t.numel() != n) value_error("%s must have %lld element(s), got %lld", name, (long long)n, (long long)t.numel());
+  return f32(t);
+}
+// Packed [.., N, K / 2] with [.., N, K / block] scales: N.
+int64_t fp4_weights(PyObject* w, PyObject* ws, int64_t dim, int64_t K, const Format& f, const at::Device& dev) {
+  const at::Tensor& q = ranked(w, "qweight", kByte, &dev, dim);
+  const int64_t N = q.size(dim - 2);
+  if (2 * q.size(dim - 1) != K) value_error("qweight must hold the %lld columns of the activations, two in a byte", (long long)K);
+  if (dim == 3) {
+    if (q.size(0) > INT32_MAX - 1) value_error("too many experts");
+    tensor(ws, "w_scale", f.scales, dev, {q.size(0), N, K / f.block});
+  } else {
+    tensor(ws, "w_scale", f.scales, dev, {N, K / f.block});
+  }
+  return N;
+}
+
+// x, format, global, q, scale, silu, stream
+PyObject* quant_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!count(n, 7)) return nullptr;
+  const bool silu = PyObject_IsTrue(a[5]);
+  const at::Tensor& x = ranked(a[0], silu ? "h" : "x", silu ? kBf16 : kAct, nullptr, 2);
+  const at::Device dev = x.device();
+  if (silu && x.size(1) % 2) value_error("h must hold gate and up halves of equal width");
+  const Format f = format(a[1]);
+  const int64_t M = x.size(0), K = silu ? x.size(1) / 2 : x.size(1);
+  const float* g = global_scale(a[2], "global_scale", 1, dev);
+  const CallStream stream(a[6], dev);
+  const at::Tensor q = output(a[3], "q", {M, K / 2}, ScalarType::Byte, kByte, dev, stream);
+  const at::Tensor s = output(a[4], "scale", {M, K / f.block}, f.scale, f.scales, dev, stream);
+  if (silu ? failed(w4_silu_mul_quant_fp4(x.data_ptr(), f.id, g, M, K, q.data_ptr(), s.data_ptr(), stream.handle()), "w4_silu_mul_quant_fp4")
+           : failed(w4_quant_fp4(x.data_ptr(), act_dtype(x), f.id, g, M, K, q.data_ptr(), s.data_ptr(), stream.handle()), "w4_quant_fp4"))
+    return nullptr;
+  return pair(q, s);
+  END_HANDLE_TH_ERRORS
+}
+
+// q, scale, format, global, fp16, out, stream
+PyObject* dequant_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!count(n, 7)) return nullptr;
+  const at::Tensor& q = ranked(a[0], "q", kByte, nullptr, 2);
+  const at::Device dev = q.device();
+  const Format f = format(a[2]);
+  const int64_t M = q.size(0), K = 2 * q.size(1);
+  const at::Tensor& s = tensor(a[1], "scale", f.scales, dev, {M, K / f.block});
+  const float* g = global_scale(a[3], "global_scale", 1, dev);
+  const bool half = PyObject_IsTrue(a[4]);
+  const CallStream stream(a[6], dev);
+  const ScalarType type = half ? ScalarType::Half : ScalarType::BFloat16;
+  const at::Tensor o = output(a[5], "out", {M, K}, type, {type}, dev, stream);
+  if (failed(w4_dequant_fp4(q.data_ptr(), s.data_ptr(), f.id, g, M, K, half ? W4_FP16 : W4_BF16, o.data_ptr(), stream.handle()),
+             "w4_dequant_fp4"))
+    return nullptr;
+  return THPVariable_Wrap(o);
+  END_HANDLE_TH_ERRORS
+}
+
+// qx, x_scale, qweight, w_scale, format, x_global, w_global, bias, y, stream
+PyObject* fp4_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!count(n, 10)) return nullptr;
+  const at::Tensor& x = ranked(a[0], "qx", kByte, nullptr, 2);
+  const at::Device dev = x.device();
+  const Format f = format(a[4]);
+  const int64_t M = x.size(0), K = 2 * x.size(1), N = fp4_weights(a[2], a[3], 2, K, f, dev);
+  const at::Tensor& xs = tensor(a[1], "x_scale", f.scales, dev, {M, K / f.block});
+  const float* xg = global_scale(a[5], "x_global", 1, dev);
+  const float* wg = global_scale(a[6], "w_global", 1, dev);
+  if (a[7] != Py_None) tensor(a[7], "bias", kBf16, dev, {N});
+  const CallStream stream(a[9], dev);
+  const at::Tensor y = output(a[8], "y", {M, N}, ScalarType::BFloat16, kBf16, dev, stream);
+  if (failed(w4_fp4_gemm(x.data_ptr(), xs.data_ptr(), xg, data(a[2]), data(a[3]), wg, f.id, data(a[7]), y.data_ptr(), M,
+                         N, K, stream.handle()),
+             "w4_fp4_gemm"))
+    return nullptr;
+  return THPVariable_Wrap(y);
+  END_HANDLE_TH_ERRORS
+}
+
+// x, qweight, w_scale, format, x_global, w_global, bias, y, workspace, stream
+PyObject* fp4_gemm_act(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!count(n, 10)) return nullptr;
+  const at::Tensor& x = ranked(a[0], "x", kAct, nullptr, 2);
+  const at::Device dev = x.device();
+  const Format f = format(a[3]);
+  const int64_t M = x.size(0), K = x.size(1), N = fp4_weights(a[1], a[2], 2, K, f, dev);
+  const float* xg = global_scale(a[4], "x_global", 1, dev);
+  const float* wg = global_scale(a[5], "w_global", 1, dev);
+  if (a[6] != Py_None) tensor(a[6], "bias", kBf16, dev, {N});
+  const CallStream stream(a[9], dev);
+  const at::Tensor y = output(a[7], "y", {M, N}, ScalarType::BFloat16, kBf16, dev, stream);
+  const Scratch s = scratch(a[8], W4_OP_FP4_IN, M, N, K, static_cast<int32_t>(f.block), dev);
+  if (failed(w4_fp4_gemm_bf16in(x.data_ptr(), act_dtype(x), xg, data(a[1]), data(a[2]), wg, f.id, data(a[6]),
+                                y.data_ptr(), M, N, K, s.p, s.bytes, stream.handle()),
+             "w4_fp4_gemm_bf16in"))
+    return nullptr;
+  return THPVariable_Wrap(y);
+  END_HANDLE_TH_ERRORS
+}
+
+// qx, x_scale, expert_offsets, qweight, w_scale, format, x_global, w_global, y, stream
+PyObject* fp4_moe_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!count(n, 10)) return nullptr;
+  const at::Tensor& x = ranked(a[0], "qx", kByte, nullptr, 2);
+  const at::Device dev = x.device();
+  const Format f = format(a[5]);
+  const int64_t R = x.size(0), K = 2 * x.size(1), N = fp4_weights(a[3], a[4], 3, K, f, dev);
+  const int64_t E = THPVariable_Unpack(a[3]).size(0);
+  const at::Tensor& xs = tensor(a[1], "x_scale", f.scales, dev, {R, K / f.block});
+  tensor(a[2], "expert_offsets", kI32, dev, {E + 1});
+  const float* xg = global_scale(a[6], "x_global", 1, dev);
+  const float* wg = global_scale(a[7], "w_global", E, dev);
+  const CallStream stream(a[9], dev);
+  const at::Tensor y = output(a[8], "y", {R, N}, ScalarType::BFloat16, kBf16, dev, stream);
+  if (failed(w4_fp4_moe_grouped_gemm(x.data_ptr(), xs.data_ptr(), xg, static_cast<const int32_t*>(data(a[2])),
+                                     static_cast<int32_t>(E), data(a[3]), data(a[4]), wg, f.id, y.data_ptr(), R, N, K,
+                                     stream.handle()),
+             "w4_fp4_moe_grouped_gemm"))
+    return nullptr;
+  return THPVariable_Wrap(y);
+  END_HANDLE_TH_ERRORS
+}
+
+// x, row_token, expert_offsets, qweight, w_scale, format, x_global, w_global, y, workspace, stream
+PyObject* fp4_moe_gemm_act(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!count(n, 11)) return nullptr;
+  const at::Tensor& x = ranked(a[0], "x", kBf16, nullptr, 2);
+  const at::Device dev = x.device();
+  const Format f = format(a[5]);
+  const int64_t T = x.size(0), K = x.size(1), N = fp4_weights(a[3], a[4], 3, K, f, dev);
+  const int64_t E = THPVariable_Unpack(a[3]).size(0);
+  tensor(a[2], "expert_offsets", kI32, dev, {E + 1});
+  const int64_t R = a[1] == Py_None ? T : tensor(a[1], "row_token", kI32, &dev).numel();
+  const float* xg = global_scale(a[6], "x_global", 1, dev);
+  const float* wg = global_scale(a[7], "w_global", E, dev);
+  const CallStream stream(a[10], dev);
+  const at::Tensor y = output(a[8], "y", {R, N}, ScalarType::BFloat16, kBf16, dev, stream);
+  const Scratch s = scratch(a[9], W4_OP_FP4_IN, R, N, K, static_cast<int32_t>(f.block), dev);
+  if (failed(w4_fp4_moe_gemm_bf16in(x.data_ptr(), T, xg, static_cast<const int32_t*>(data(a[1])),
+                                    static_cast<const int32_t*>(data(a[2])), static_cast<int32_t>(E), data(a[3]),
+                                    data(a[4]), wg, f.id, y.data_ptr(), R, N, K, s.p, s.bytes, stream.handle()),
+             "w4_fp4_moe_gemm_bf16in"))
+    return nullptr;
+  return THPVariable_Wrap(y);
+  END_HANDLE_TH_ERRORS
+}
+
 #define W4_METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {W4_METHOD(route_grouped), W4_METHOD(quant_block), W4_METHOD(silu_mul_quant_block),
                           W4_METHOD(gemm),          W4_METHOD(gemm_act),    W4_METHOD(moe_gemm),
-                          W4_METHOD(moe_gemm_act),  {nullptr, nullptr, 0, nullptr}};
+                          W4_METHOD(moe_gemm_act),  W4_METHOD(quant_fp4),   W4_METHOD(dequant_fp4),
+                          W4_METHOD(fp4_gemm),      W4_METHOD(fp4_gemm_act), W4_METHOD(fp4_moe_gemm),
+                          W4_METHOD(fp4_moe_gemm_act), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

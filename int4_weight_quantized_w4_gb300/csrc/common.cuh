@@ -113,6 +113,13 @@ W4_DEV uint32_t e4m3x2_to_f16x2(uint32_t two_codes) {
   return d;
 }
 
+// e2m1 codes n0..n7 (nibbles) -> fp16 pairs (n0,n1), (n2,n3), (n4,n5), (n6,n7), exactly.
+W4_DEV void e2m1x8_to_f16(uint32_t codes, uint32_t (&d)[4]) {
+  asm("{.reg .b8 a, b, c, d; mov.b32 {a, b, c, d}, %4; cvt.rn.f16x2.e2m1x2 %0, a; cvt.rn.f16x2.e2m1x2 %1, b; "
+      "cvt.rn.f16x2.e2m1x2 %2, c; cvt.rn.f16x2.e2m1x2 %3, d;}"
+      : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]) : "r"(codes));
+}
+
 // e4m3 codes b0..b7 -> fp16 (b0,b4,b1,b5,b2,b6,b3,b7), exactly.
 W4_DEV uint4 widen_e4m3(uint32_t u0, uint32_t u1) {
   const uint32_t a = prmt(u0, u1, 0x5140u), b = prmt(u0, u1, 0x7362u);

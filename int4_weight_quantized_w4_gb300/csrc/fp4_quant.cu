@@ -1,0 +1,240 @@
+// Microscaled 4-bit floats: e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+// negatives) with a scale per block of columns of a row.
+//
+//   mxfp4: blocks of 32; scale 2^e, e = clamp(floor(log2 amax) - 2, -127, 127), kept
+//          as e + 127 (e8m0); q = rne_e2m1(x 2^-e), held to +-6.
+//   nvfp4: blocks of 16 and an fp32 scale g of the whole tensor; s = rne_e4m3(fl(fl(amax
+//          / 6) / g)), held to 448; d = fl(s g); q = rne_e2m1(fl(x / d)), held to +-6 (0
+//          where d is 0).
+//
+// x is a bf16 or fp16 activation, or silu(gate) * up of a bf16 gate_up row, in IEEE
+// fp32 steps: fl(fl(g / fl(1 + expf(-g))) up). A block that holds a NaN or an infinity gets
+// a NaN scale, so that it shows in whatever is computed from it.
+//
+// K is a multiple of the block, so blocks of a row-major matrix follow one another
+// whatever the rows, and a thread takes 16 consecutive elements: an nvfp4 block, or
+// half an mxfp4 block whose other half is the neighbour lane's. No row-wide step
+// exists. Bound by HBM: 2 or 4 bytes read and 1/2 + 1/16 (1/32) written an element.
+#include "common.cuh"
+#include "launch.h"
+
+namespace w4 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr unsigned kFull = 0xFFFFFFFFu;
+constexpr uint32_t kInfBits = 0x7F800000u;
+
+// Eight e2m1 codes of eight floats (round to nearest even, held to +-6), element i in nibble i.
+W4_DEV uint32_t e2m1x8(const float (&x)[8]) {
+  uint32_t d;
+  asm("{.reg .b8 a, b, c, d; cvt.rn.satfinite.e2m1x2.f32 a, %2, %1; cvt.rn.satfinite.e2m1x2.f32 b, %4, %3; "
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5; cvt.rn.satfinite.e2m1x2.f32 d, %8, %7; mov.b32 %0, {a, b, c, d};}"
+      : "=r"(d) : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+  return d;
+}
+
+// Codes of fl(x / d), with r = fl(1 / d): the quotient by multiply-add refinement as
+// quotient2_e4m3, where d takes it (scale_refines). A quotient below 2^-3 has code 0 or -0
+// either way, so the bounds of the e4m3 form are ample.
+W4_DEV uint32_t quotients_e2m1(const float (&x)[8], float d, float r) {
+  float q[8];
+  if (scale_refines(d)) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      float q0, q1, e0, e1;
+      mul2(q0, q1, x[i], x[i + 1], r);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        fma2c<true>(e0, e1, q0, q1, -d, x[i], x[i + 1]);
+        fma2c(q0, q1, e0, e1, r, q0, q1);
+      }
+      q[i] = q0, q[i + 1] = q1;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(x[i], d);
+  }
+  return e2m1x8(q);
+}
+
+// Halfwise maximum of magnitude bits: NaNs are above infinities, those above numbers.
+W4_DEV uint32_t max_u16x2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
+
+// Scale byte and codes of 16 elements; bits: those of the block's largest magnitude.
+// kNv: the block is this thread's; else it is two lanes'.
+template <bool kNv>
+W4_DEV uint32_t block_codes(const float (&x)[2][8], uint32_t bits, float g, uint2& code) {
+  if constexpr (kNv) {
+    if (bits >= kInfBits) {
+      code = make_uint2(0, 0);
+      return 0x7F;
+    }
+    const float v = __fdiv_rn(__fdiv_rn(__uint_as_float(bits), 6.f), g);
+    const uint32_t s8 = e4m3x2_rn(v, 0.f) & 0xFFu;
+    const float s = half_bits_to_f32(e4m3x2_to_f16x2(s8) & 0xFFFFu);
+    const float d = s * g;
+    if (d > 0.f) {
+      const float r = __frcp_rn(d);
+      code.x = quotients_e2m1(x[0], d, r);
+      code.y = quotients_e2m1(x[1], d, r);
+    } else {
+      code = make_uint2(0, 0);
+    }
+    return s8;
+  } else {
+    if (bits >= kInfBits) {
+      code = make_uint2(0, 0);
+      return 0xFF;
+    }
+    const uint32_t b = max(static_cast<int>(bits >> 23) - 2, 0);   // floor(log2 amax) - 2 + 127
+    const float f = __uint_as_float((254u - b) << 23);
+    float y[8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) mul2(y[i], y[i + 1], x[h][i], x[h][i + 1], f);
+      (h ? code.y : code.x) = e2m1x8(y);
+    }
+    return b;
+  }
+}
+
+// Item i: 16 elements of the output. kSilu: columns c and K + c of the row's 2 K. gather
+// (may be null): source row of each output row; an id outside [0, T) gives a zero row and
+// W4_ERR_SHAPE in the status word. K16 = K / 16. signals: the next kernel may start once every
+// kernel before this one is done; else when this one is, which may have written weights.
+template <bool kNv, bool kF16, bool kSilu>
+__global__ void __launch_bounds__(kThreads) quant_fp4_kernel(const uint4* x, int64_t items, uint32_t K16,
+                                                             const float* global, const int32_t* gather, int64_t T,
+                                                             bool signals, uint2* __restrict__ q,
+                                                             uint8_t* __restrict__ scale, unsigned int* status) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  const bool live = i < items;   // an odd half of the last warp still takes part in the shuffles
+  int64_t at = i;
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // x may come from the kernel before, which may still read q
+  if (signals) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  bool bad = false;
+  if (live && (kSilu || gather != nullptr)) {
+    const int64_t row = i / K16;
+    const uint32_t c = static_cast<uint32_t>(i - row * K16);
+    int64_t src = row;
+    if (gather != nullptr) {
+      src = __ldcg(gather + row);
+      bad = src < 0 || src >= T;
+      if (bad && c == 0) report(status, W4_ERR_SHAPE);
+    }
+    at = src * (kSilu ? 2 * K16 : K16) + c;
+  }
+  uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+  float f[2][8];
+  uint32_t bits = 0;
+  if (live && !bad) {
+    v[0] = ld_once_v4(x + 2 * at);
+    v[1] = ld_once_v4(x + 2 * at + 1);
+  }
+  if constexpr (kSilu) {
+    uint4 u[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (live && !bad) {
+      u[0] = ld_once_v4(x + 2 * (at + K16));
+      u[1] = ld_once_v4(x + 2 * (at + K16) + 1);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float a[8];
+      chunk_f32<false>(v[h], a);
+      chunk_f32<false>(u[h], f[h]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        f[h][j] *= __fdiv_rn(a[j], 1.f + expf(-a[j]));
+        bits = max(bits, __float_as_uint(f[h][j]) & 0x7FFFFFFFu);
+      }
+    }
+  } else {
+    constexpr uint32_t kMag = 0x7FFF7FFFu;
+    uint32_t m = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      m = max_u16x2(max_u16x2(m, v[h].x & kMag), v[h].y & kMag);
+      m = max_u16x2(max_u16x2(m, v[h].z & kMag), v[h].w & kMag);
+      chunk_f32<kF16>(v[h], f[h]);
+    }
+    m = max(m & 0xFFFFu, m >> 16);
+    bits = __float_as_uint(act_lo<kF16>(m));   // fp16 infinities and NaNs become fp32's
+  }
+  if constexpr (!kNv) bits = max(bits, __shfl_xor_sync(kFull, bits, 1));
+  if (!live) return;
+  uint2 code;
+  const uint32_t s = block_codes<kNv>(f, bits, kNv && global != nullptr ? __ldcg(global) : 1.f, code);
+  q[i] = code;
+  if constexpr (kNv)
+    scale[i] = static_cast<uint8_t>(s);
+  else if ((i & 1) == 0)
+    scale[i >> 1] = static_cast<uint8_t>(s);
+}
+
+template <bool kNv, bool kF16, bool kSilu>
+cudaError_t launch(const QuantFp4Args& a, cudaStream_t s) {
+  const int64_t items = a.M * (a.K / 16);
+  PdlLaunch pl(static_cast<unsigned>((items + kThreads - 1) / kThreads), kThreads, 0, s);
+  return cudaLaunchKernelEx(&pl.cfg, quant_fp4_kernel<kNv, kF16, kSilu>, static_cast<const uint4*>(a.x), items,
+                            static_cast<uint32_t>(a.K / 16), a.global, a.gather, a.T, a.signals, static_cast<uint2*>(a.q),
+                            static_cast<uint8_t*>(a.scale), a.status);
+}
+
+// Values of 16 codes: rounded once, from fl(q d) with d = fl(s g), or from q 2^e.
+template <bool kNv, bool kF16>
+__global__ void __launch_bounds__(kThreads) dequant_fp4_kernel(const uint2* q, const uint8_t* scale,
+                                                               const float* global, int64_t items,
+                                                               uint4* __restrict__ out) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (i >= items) return;
+  const uint2 c = __ldcg(q + i);
+  const uint32_t s8 = __ldcg(scale + (kNv ? i : i >> 1));
+  float d;
+  if constexpr (kNv) {
+    d = half_bits_to_f32(e4m3x2_to_f16x2(s8) & 0xFFFFu) * (global != nullptr ? __ldcg(global) : 1.f);
+  } else {
+    d = __uint_as_float(s8 == 0 ? 1u << 22 : s8 == 255 ? 0x7FC00000u : s8 << 23);
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t w[4], o[4];
+    e2m1x8_to_f16(h ? c.y : c.x, w);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float lo, hi;
+      mul2(lo, hi, half_bits_to_f32(w[j] & 0xFFFFu), half_bits_to_f32(w[j] >> 16), d);
+      if constexpr (kF16)
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[j]) : "f"(hi), "f"(lo));
+      else
+        o[j] = pack_bf16x2(lo, hi);
+    }
+    out[2 * i + h] = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+}  // namespace
+
+bool quant_fp4_fits(int64_t M, int64_t K) {
+  return M <= static_cast<int64_t>(INT32_MAX) * kThreads / (K / 16);
+}
+
+cudaError_t launch_quant_fp4(const QuantFp4Args& a, cudaStream_t s) {
+  if (a.silu) return a.nv ? launch<true, false, true>(a, s) : launch<false, false, true>(a, s);
+  if (a.f16) return a.nv ? launch<true, true, false>(a, s) : launch<false, true, false>(a, s);
+  return a.nv ? launch<true, false, false>(a, s) : launch<false, false, false>(a, s);
+}
+
+cudaError_t launch_dequant_fp4(const void* q, const void* scale, const float* global, bool nv, bool f16, int64_t M,
+                               int64_t K, void* out, cudaStream_t s) {
+  const int64_t items = M * (K / 16);
+  PdlLaunch pl(static_cast<unsigned>((items + kThreads - 1) / kThreads), kThreads, 0, s);
+  auto* kernel = nv ? (f16 ? dequant_fp4_kernel<true, true> : dequant_fp4_kernel<true, false>)
+                    : (f16 ? dequant_fp4_kernel<false, true> : dequant_fp4_kernel<false, false>);
+  return cudaLaunchKernelEx(&pl.cfg, kernel, static_cast<const uint2*>(q), static_cast<const uint8_t*>(scale), global,
+                            items, static_cast<uint4*>(out));
+}
+
+}  // namespace w4

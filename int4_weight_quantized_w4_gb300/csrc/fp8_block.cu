@@ -30,31 +30,25 @@
 //
 // Both are launched as programmatic dependents and let their own dependents go
 // early: the copies of weights start while the kernels before finish, everything
-// else (activations, scales, bias, y) waits for them, and so do the expert offsets
+// else (activations, scales, bias, y) waits for them (griddepcontrol.wait), and so do the expert offsets
 // unless the one before is the row quantizer, which starts this one only when all
 // before it are done.
-#include <cuda.h>
-
 #include <atomic>
 #include <cstring>
 
 #include "common.cuh"
 #include "launch.h"
 #include "tc.cuh"
+#include "tiles.cuh"
 
 namespace w4 {
 namespace {
 
 constexpr int kBlk = 128;                     // k and weight rows per scale
-constexpr int kMaxExperts = 1024;
-constexpr int kMaxSplit = 8;                  // CTAs of a cluster that share a tile's k blocks
 // Up to this many dense rows the stream form quantizes: one launch less (fused / not:
 // 1 x 4096 x 4096 6.3 / 7.1 us, 8 x 4096 x 4096 7.0 / 7.6, 8 x 14336 x 4096 14.3 / 14.4). Every
 // CTA quantizes them again, so that at 16 rows the order turns (8.5 / 8.0).
 constexpr int kFuseRows = 8;
-// 2 s per wait. A warp that waits for what depends on the kernels before waits for these
-// first (griddepcontrol.wait, without a limit), so that their time does not count.
-constexpr uint64_t kWaitNs = 2000000000ull;
 
 struct Params {
   CUtensorMap tm_x;        // e4m3 codes [rows, K] (unused where the kernel quantizes)
@@ -78,117 +72,16 @@ struct Params {
   unsigned int* status;
 };
 
-W4_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-W4_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-W4_DEV uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-// Four floats at shared address `a` of CTA `rank` of the cluster.
-W4_DEV float4 ld_cluster_f32x4(uint32_t a, uint32_t rank) {
-  float4 v;
-  asm volatile("{.reg .b32 t; mapa.shared::cluster.u32 t, %4, %5; ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [t];}"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a), "r"(rank) : "memory");
-  return v;
-}
-// tc::wait by a whole warp with one answer: a warp whose lanes disagreed after a
-// time-out would not meet at its next warp-wide instruction.
-W4_DEV bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned int* status) {
-  constexpr unsigned kAll = 0xFFFFFFFFu;
-  if (__all_sync(kAll, mbar_try_wait(bar, parity))) return true;
-  const uint64_t t0 = tc::globaltimer_ns();
-  for (;;) {
-#pragma unroll 1
-    for (int i = 0; i < 8; ++i)
-      if (__all_sync(kAll, tc::try_wait_suspend(bar, parity, 1000))) return true;
-    if (__any_sync(kAll, *abort != 0)) return false;
-    if (__any_sync(kAll, tc::globaltimer_ns() - t0 > kWaitNs)) {
-      report(status, W4_ERR_TIMEOUT);
-      *abort = 1;
-      return false;
-    }
-  }
-}
-// One lane of a converged warp. Loops that issue copies or MMAs run in the whole
-// warp with one lane issuing: descriptors and addresses stay in uniform registers.
-W4_DEV bool elect_one() {
-  uint32_t p;
-  asm volatile("{.reg .pred P; elect.sync _|P, 0xFFFFFFFF; selp.u32 %0, 1, 0, P;}" : "=r"(p));
-  return p != 0;
-}
-W4_DEV void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-W4_DEV void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
-// First row tile of every expert (tiles of `rows_per` rows), in shared memory:
-// starts[e], starts[E] = the total. All threads of the block take part; at
-// most kMaxExperts experts. A segment outside [0, rows) counts as clipped. The offsets
+// Rows [a, b) of expert e; a segment outside [0, rows) counts as clipped. The offsets
 // are read from L2, where the kernel that wrote them left them: with offsets_ready this
 // one has not waited for the kernels before yet.
 W4_DEV void seg_bounds(const Params& p, int e, int& a, int& b) {
   a = max(__ldcg(p.offsets + e), 0);
   b = min(__ldcg(p.offsets + e + 1), p.rows);
 }
-template <int kThreads>
-W4_DEV void tile_starts(const Params& p, int rows_per, int32_t* starts, int32_t* warp_sum) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int carry = 0;
-  for (int e0 = 0; e0 < p.E; e0 += kThreads) {
-    const int e = e0 + threadIdx.x;
-    int n = 0;
-    if (e < p.E) {
-      int a, b;
-      seg_bounds(p, e, a, b);
-      n = b > a ? (b - a + rows_per - 1) / rows_per : 0;
-    }
-    int inc = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += t;
-    }
-    if (lane == 31) warp_sum[warp] = inc;
-    __syncthreads();
-    int before = carry, all = carry;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      const int s = warp_sum[w];
-      if (w < warp) before += s;
-      all += s;
-    }
-    if (e < p.E) starts[e] = before + inc - n;
-    carry = all;
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) starts[p.E] = carry;
-}
 
 // Where part `i` of `n` of KB blocks starts (KB, n below 2^15 and 2^5, or n = 1).
 W4_DEV int part_start(int KB, int i, int n) { return n == 1 ? i * KB : KB * i / n; }
-
-struct Tile {
-  int n0, row0, row_end, expert;
-};
-// Item `it` (n tiles fastest) as a tile of `rows_per` rows and `cols_per`
-// outputs; false when there are no more. `e` is the caller's cursor over the
-// experts: items come in increasing order.
-W4_DEV bool decode(const Params& p, int it, int rows_per, int cols_per, const int32_t* starts, Tile& t, int& e) {
-  const int yt = static_cast<int>(static_cast<unsigned>(it) / static_cast<unsigned>(p.n_tiles));
-  t.n0 = (it - yt * p.n_tiles) * cols_per;
-  if (p.offsets == nullptr) {
-    t.expert = 0;
-    t.row0 = yt * rows_per;
-    t.row_end = min(t.row0 + rows_per, p.rows);
-    return t.row0 < p.rows;
-  }
-  if (yt >= starts[p.E]) return false;
-  while (starts[e + 1] <= yt) ++e;
-  int a, b;
-  seg_bounds(p, e, a, b);
-  t.expert = e;
-  t.row0 = a + (yt - starts[e]) * rows_per;
-  t.row_end = min(t.row0 + rows_per, b);
-  return true;
-}
 
 // e4m3 x e4m3, fp32 accumulator, both operands K-major: format codes 0.
 // One block of 128 k: four MMAs of 32 k, 32 bytes apart in the swizzle row.
@@ -560,23 +453,6 @@ static_assert(T_STAGES == 4 && T_ACCS == 2, "a group of four blocks");
 constexpr int kTEpi = 8, kTWarpLoad = 8, kTWarpScale = 9, kTWarpMma = 10;
 constexpr int kTThreads = 384;
 
-// 64 bytes of every lane's row (four 16-byte chunks) through `buf` (2 KB of this
-// warp): put(r, c, v) gets chunk c of row r, four lanes to a row and 8 rows an
-// instruction, where the lanes' own stores would touch 32 rows at 16 bytes each.
-template <class Put>
-W4_DEV void rows_out(uint4* buf, const uint4 (&v)[4], Put put) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int c = 0; c < 4; ++c) buf[lane * 4 + (c ^ ((lane >> 1) & 3))] = v[c];   // no two of 8 lanes in one bank
-  __syncwarp();
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 8 * i + (lane >> 2), c = lane & 3;
-    put(r, c, buf[r * 4 + (c ^ ((r >> 1) & 3))]);
-  }
-  __syncwarp();
-}
-
 struct Work {
   Tile t;
   int kb0, kb1;
@@ -869,69 +745,10 @@ __global__ void __launch_bounds__(256) join_parts_kernel(const float4* sums, int
 // host side
 // ---------------------------------------------------------------------------
 
-constexpr int64_t kMaxItems = int64_t{1} << 30;   // more tiles than any y that fits the device has
-
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-cudaError_t get_encoder(EncodeTiled* fn) {
-  static const EncodeTiled cached = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return reinterpret_cast<EncodeTiled>(f);
-  }();
-  if (cached == nullptr) return cudaErrorNotSupported;
-  *fn = cached;
-  return cudaSuccess;
-}
-
-// e4m3 rows of K bytes in boxes of box_rows rows x 128 bytes, 128-byte swizzle;
-// rows and columns past the tensor arrive as zeros.
-cudaError_t encode(CUtensorMap* m, const void* base, int64_t K, int64_t rows, int64_t E, int box_rows) {
-  EncodeTiled fn = nullptr;
-  cudaError_t e = get_encoder(&fn);
-  if (e != cudaSuccess) return e;
-  const cuuint32_t rank = E > 0 ? 3 : 2;
-  const cuuint64_t dims[3] = {(cuuint64_t)K, (cuuint64_t)rows, (cuuint64_t)E};
-  const cuuint64_t strides[2] = {(cuuint64_t)K, (cuuint64_t)K * (cuuint64_t)rows};
-  const cuuint32_t box[3] = {128, (cuuint32_t)box_rows, 1}, estr[3] = {1, 1, 1};
-  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 // Row tiles of `per` rows that R rows in E segments can need at most.
 int64_t row_tiles(const Fp8BlockArgs& a, int per) {
   const int64_t whole = (a.R + per - 1) / per;
   return a.expert_offsets == nullptr ? whole : (a.R < whole + a.E ? a.R : whole + a.E);
-}
-
-// Lets a kernel use its dynamic shared memory: once per device, since the call
-// costs as much as the rest of the host path put together. A device reset takes
-// the setting back; the launch that then fails is repeated with it set again.
-template <void (*kKernel)(Params)>
-cudaError_t start(const Params& p, int64_t grid, int threads, int smem, int cluster, cudaStream_t s) {
-  static std::atomic<uint64_t> set{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = uint64_t{1} << (dev & 63);
-  PdlLaunch pl(static_cast<unsigned>(grid), threads, smem, s, cluster);
-  if (set.load(std::memory_order_relaxed) & bit) {
-    e = cudaLaunchKernelEx(&pl.cfg, kKernel, p);
-    if (e != cudaErrorInvalidValue) return e;
-    cudaGetLastError();
-  }
-  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  e = cudaLaunchKernelEx(&pl.cfg, kKernel, p);
-  if (e == cudaSuccess && dev < 64) set.fetch_or(bit, std::memory_order_relaxed);
-  return e;
 }
 
 // Clusters of n CTAs, one an SM, that the device holds at once: they do not cross a
@@ -954,6 +771,8 @@ int one_cta_clusters(int n) {
   }
   return v - 1;
 }
+}  // namespace
+
 // The same for `ctas` (1 or 2) an SM: with two, a group of S SMs holds 2S / n clusters
 // of n, at least as many as S / ceil(n / 2) and as twice S / n.
 int clusters_held(int n, int ctas) {
@@ -962,6 +781,8 @@ int clusters_held(int n, int ctas) {
   const int half = n > 2 ? one_cta_clusters((n + 1) / 2) : 0;
   return half > 2 * one ? half : 2 * one;
 }
+
+namespace {
 
 template <int NT, bool kQuant>
 cudaError_t run_stream(const Fp8BlockArgs& a, Params& p, cudaStream_t s) {

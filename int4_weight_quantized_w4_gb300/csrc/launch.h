@@ -178,6 +178,45 @@ inline size_t fp8_block_workspace_bytes(int64_t R, int64_t K) {
 // Whether launch_fp8_block takes 16-bit activations.
 bool fp8_block_fuses(int64_t R, bool experts);
 cudaError_t launch_fp8_block(const Fp8BlockArgs& a, cudaStream_t s);
+// Most clusters of n CTAs, `ctas` (1 or 2) an SM, that the current device holds at once.
+int clusters_held(int n, int ctas);
+
+// e2m1 codes and scales of x [*, K] (bf16, or fp16), or of silu(gate) * up of x [*, 2K] (silu, bf16): nvfp4 (nv), else
+// mxfp4. gather (may be null): source row of each of the M output rows, checked against T. quant_fp4_fits: one grid.
+struct QuantFp4Args {
+  const void* x;
+  bool nv, f16, silu;
+  int64_t M, K;
+  const float* global;       // nv: the tensor's scale, or null (1)
+  const int32_t* gather;
+  int64_t T;
+  bool signals;              // the next kernel may start once all before this one are done
+  void *q, *scale;
+  unsigned int* status;
+};
+bool quant_fp4_fits(int64_t M, int64_t K);
+cudaError_t launch_quant_fp4(const QuantFp4Args& a, cudaStream_t s);
+cudaError_t launch_dequant_fp4(const void* q, const void* scale, const float* global, bool nv, bool f16, int64_t M,
+                               int64_t K, void* out, cudaStream_t s);
+struct Fp4Args {
+  const void *qx, *x_scale;       // e2m1 [R, K/2 bytes] and its scales
+  const void *qweight, *w_scale;  // e2m1 [E, N, K/2 bytes] and its scales
+  bool nv;
+  const float *x_global, *w_global;  // fp32, [1] and [E], or null (1)
+  const void* bias;               // bf16 [N] or null
+  void* y;                        // bf16 [R, N]
+  const int32_t* expert_offsets;  // device [E + 1], or null: dense, E = 1
+  int32_t E;
+  int64_t R, N, K;
+  unsigned int* status;
+};
+inline int64_t fp4_block(bool nv) { return nv ? 16 : 32; }
+// Quantized rows of the 16-bit-input forms: codes [R, K/2], then scales, each padded to 16 bytes.
+inline size_t fp4_code_bytes(int64_t R, int64_t K) { return (static_cast<size_t>(R) * (K / 2) + 15) / 16 * 16; }
+inline size_t fp4_workspace_bytes(int64_t R, int64_t K, bool nv) {
+  return fp4_code_bytes(R, K) + (static_cast<size_t>(R) * (K / fp4_block(nv)) + 15) / 16 * 16;
+}
+cudaError_t launch_fp4(const Fp4Args& a, cudaStream_t s);
 cudaError_t launch_bounded_wait_selftest(long long limit, unsigned int* status, cudaStream_t s);
 
 }  // namespace w4

@@ -68,6 +68,14 @@ W4_DEV void tma_load_3d(void* smem_dst, const void* tmap, uint64_t* bar, int c0,
       :: "r"(smem_addr(smem_dst)), "l"(tmap), "r"(smem_addr(bar)), "r"(c0), "r"(c1), "r"(c2) : "memory");
 }
 
+// Asynchronous copy of 4 bytes, or zeros where `in` is false (then nothing is read).
+W4_DEV void copy4_async(uint32_t smem_dst, const void* src, bool in) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" :: "r"(smem_dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+}
+W4_DEV void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+W4_DEV void copy_async_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(kPending) : "memory"); }
+
 // Contiguous global -> shared copy of `bytes` (a multiple of 16; both
 // addresses 16-byte aligned), completion counted on `bar`.
 W4_DEV void bulk_load(void* smem_dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -154,6 +162,55 @@ W4_DEV void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t i
       "{.reg .pred p; setp.ne.b32 p, %4, 0; "
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;}"
       :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// block-scaled 4-bit MMA
+// ---------------------------------------------------------------------------
+
+// Instruction descriptor of the e2m1 x e2m1 block-scaled kinds (both operands
+// K-major, fp32 accumulator): scales e4m3 (kNv) or powers of two.
+template <bool kNv>
+constexpr uint32_t idesc_fp4(int M, int N) {
+  return (1u << 7) | (1u << 10)                   // A, B format: e2m1
+         | (static_cast<uint32_t>(N >> 3) << 17)  // N / 8
+         | ((kNv ? 0u : 1u) << 23)                // scale format
+         | (static_cast<uint32_t>(M >> 7) << 27); // M / 128
+}
+
+// M x N x 64 per instruction. Scales come from tensor memory, a 32-bit column word per
+// row: four e4m3 of 16 k each (kNv), or two powers of two of 32 k each in the half that
+// the descriptor's scale ids (bits 29 and 4, 0 or 2) name.
+template <bool kNv>
+W4_DEV void mma_fp4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                    uint32_t accumulate) {
+  if constexpr (kNv)
+    asm volatile(
+        "{.reg .pred p; setp.ne.b32 p, %6, 0; "
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;}"
+        :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
+  else
+    asm volatile(
+        "{.reg .pred p; setp.ne.b32 p, %6, 0; "
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;}"
+        :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
+}
+
+// Shared-memory descriptor of a scale atom: 32 rows of 16 bytes (four 32-bit words: rows r,
+// r + 32, r + 64, r + 96), no swizzle, 8-row groups 128 bytes apart.
+W4_DEV uint64_t sdesc_scales(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(1) << 16;
+  d |= static_cast<uint64_t>(128 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  return d;
+}
+
+// A scale atom into four columns of tensor memory, the same in all four lane quadrants.
+// It is executed in order with the MMAs that the thread issues.
+W4_DEV void copy_scales(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" :: "r"(taddr), "l"(sdesc) : "memory");
 }
 
 // Arrive (once) on `bar` when every tcgen05 op this thread issued so far is done.

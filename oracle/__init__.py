@@ -12,3 +12,4 @@ to the numpy statement.
 """
 from .w4_oracle import *  # noqa: F401,F403
 from .fp8_block_oracle import *  # noqa: F401,F403
+from .fp4_oracle import *  # noqa: F401,F403
