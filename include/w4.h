@@ -76,13 +76,15 @@ typedef enum {
   W4_OP_MOE_ROUTE_GROUPED = 3, /* w4_moe_route_grouped (M = T tokens, N = E experts; K = 1, group ignored) */
   W4_OP_FP8_BLOCK = 4,      /* w4_fp8_block_gemm (group ignored) */
   W4_OP_FP8_BLOCK_IN = 5,   /* w4_fp8_block_gemm_bf16in (group = 0), w4_fp8_block_moe_gemm_bf16in (M = R rows, group = E) */
-  W4_OP_FP4_IN = 6          /* w4_fp4_gemm_bf16in, w4_fp4_moe_gemm_bf16in (M = rows, group = 16 or 32: the format's block) */
+  W4_OP_FP4_IN = 6,         /* w4_fp4_gemm_bf16in, w4_fp4_moe_gemm_bf16in (M = rows, group = 16 or 32: the format's block) */
+  W4_OP_MOE_DECODE = 7      /* w4_moe_decode (M = T tokens, N = top_k, K = I; group ignored) */
 } w4_op;
 
 /* 4-bit weight formats. */
 typedef enum {
   W4_FMT_MXFP4 = 0,  /* e2m1, a power of two (e8m0) per 32 columns */
-  W4_FMT_NVFP4 = 1   /* e2m1, an e4m3 scale per 16 columns, an fp32 scale per tensor */
+  W4_FMT_NVFP4 = 1,  /* e2m1, an e4m3 scale per 16 columns, an fp32 scale per tensor */
+  W4_FMT_INT4 = 2    /* uint4b8 (q - 8), an fp16 scale per group of columns */
 } w4_format;
 
 /* Router scores of w4_moe_route_grouped. */
@@ -572,6 +574,38 @@ w4_status w4_fp4_moe_gemm_bf16in(const void* x, int64_t T, const float* x_global
                                  const int32_t* expert_offsets, int32_t E, const void* qweight, const void* w_scale,
                                  const float* w_global, int32_t format, void* y, int64_t R, int64_t N, int64_t K,
                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * w4_moe_decode: a whole routed MoE layer for a few tokens, in two kernels. From x [T, H]
+ * bf16 and router logits [T, E] (bf16, or fp32 where logits_f32 != 0),
+ *     experts e and weights w of token t as w4_moe_route_grouped gives them (bias,
+ *     top_k, n_group, topk_group, scoring, renormalize, scale as there);
+ *     h = gate_up[e] x_t;  a = silu(h[0 .. I)) h[I .. 2I);  y_t = bf16( sum_e w down[e] a ).
+ * Activations stay 16-bit (the W4A16 form of the experts); products are exact and sums
+ * are fp32. The activations in between are rounded once, to 11 bits (fp16 with an exponent
+ * of its own per eight columns). Outputs are the same every time.
+ *   format   W4_FMT_INT4: gate_up [E, 2I, H/8] int32, gate_up_scale [E, 2I, H/group] fp16
+ *            (the layout of w4afp8_moe_grouped_gemm); group: gate_up_group and
+ *            down_group, multiples of 32 that divide H and I, or -1;
+ *            W4_FMT_MXFP4, W4_FMT_NVFP4: gate_up [E, 2I, H/2] bytes, gate_up_scale [E, 2I,
+ *            H/32 or H/16] bytes as w4_quant_fp4 gives them (groups ignored)
+ *   gate_up_global, down_global  fp32 [E] (nvfp4) or NULL
+ *   down     [E, H, I/8] int32 or [E, H, I/2] bytes, down_scale alike
+ *   y        [T, H] bf16
+ * Limits (W4_ERR_UNSUPPORTED): T <= 16, E <= 256, top_k <= 32, H and I multiples of 64, and
+ * shared memory for T rows of x beside the copies in flight (H up to 4096 at 16 tokens,
+ * 8192 at 7). For more tokens w4_moe_route_grouped and the grouped products.
+ * Matrices, scales and the workspace are 16-byte aligned. workspace: at least
+ * w4_workspace_bytes(W4_OP_MOE_DECODE, T, top_k, I, 0) bytes. x, logits, bias and weights are
+ * read after the kernels before are done; its own dependents may start early, as those
+ * of w4a16_gemm.
+ */
+w4_status w4_moe_decode(const void* x, const void* logits, int32_t logits_f32, const float* bias, int64_t T, int32_t E,
+                        int32_t top_k, int32_t n_group, int32_t topk_group, int32_t scoring, int32_t renormalize,
+                        float scale, int32_t format, const void* gate_up, const void* gate_up_scale,
+                        const float* gate_up_global, int32_t gate_up_group, const void* down, const void* down_scale,
+                        const float* down_global, int32_t down_group, void* y, int64_t H, int64_t I, void* workspace,
+                        size_t workspace_bytes, void* stream);
 
 /*
  * Weight-side tools (load time, not on the per-token path).

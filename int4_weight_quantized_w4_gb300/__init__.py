@@ -32,19 +32,19 @@ __all__ = [
     "w4_quant_act_per_block", "w4_silu_mul_quant_block", "w4_fp8_block_gemm", "w4_fp8_block_gemm_bf16in",
     "w4_fp8_block_moe_grouped_gemm", "w4_fp8_block_moe_gemm_bf16in",
     "w4_quant_fp4", "w4_silu_mul_quant_fp4", "w4_dequant_fp4", "w4_fp4_gemm", "w4_fp4_gemm_bf16in",
-    "w4_fp4_moe_grouped_gemm", "w4_fp4_moe_gemm_bf16in",
+    "w4_fp4_moe_grouped_gemm", "w4_fp4_moe_gemm_bf16in", "w4_moe_decode",
     "w4_device_status", "w4_selftest_bounded_wait", "apply_weights", "MIN_TOKENS_FOR_INT8",
     "W4_OK", "W4_ERR_NULL", "W4_ERR_ALIGN", "W4_ERR_GROUP", "W4_ERR_DTYPE",
     "W4_ERR_UNSUPPORTED", "W4_ERR_SHAPE", "W4_ERR_CUDA", "W4_ERR_TIMEOUT", "W4_ERR_WORKSPACE",
-    "W4_OP_W4A8", "W4_OP_W4AFP8_MOE", "W4_OP_MOE_ROUTE", "W4_OP_MOE_ROUTE_GROUPED", "W4_OP_FP8_BLOCK", "W4_OP_FP8_BLOCK_IN", "W4_OP_FP4_IN", "w4_workspace_bytes", "EXPORTED_SYMBOLS",
+    "W4_OP_W4A8", "W4_OP_W4AFP8_MOE", "W4_OP_MOE_ROUTE", "W4_OP_MOE_ROUTE_GROUPED", "W4_OP_FP8_BLOCK", "W4_OP_FP8_BLOCK_IN", "W4_OP_FP4_IN", "W4_OP_MOE_DECODE", "w4_workspace_bytes", "EXPORTED_SYMBOLS",
 ]
 
 (W4_OK, W4_ERR_NULL, W4_ERR_ALIGN, W4_ERR_GROUP, W4_ERR_DTYPE, W4_ERR_UNSUPPORTED,
  W4_ERR_SHAPE, W4_ERR_CUDA, W4_ERR_TIMEOUT, W4_ERR_WORKSPACE) = range(10)
 W4_BF16, W4_FP16, W4_INT8, W4_FP8_E4M3 = range(4)
-W4_OP_W4A8, W4_OP_W4AFP8_MOE, W4_OP_MOE_ROUTE, W4_OP_MOE_ROUTE_GROUPED, W4_OP_FP8_BLOCK, W4_OP_FP8_BLOCK_IN, W4_OP_FP4_IN = range(7)
+W4_OP_W4A8, W4_OP_W4AFP8_MOE, W4_OP_MOE_ROUTE, W4_OP_MOE_ROUTE_GROUPED, W4_OP_FP8_BLOCK, W4_OP_FP8_BLOCK_IN, W4_OP_FP4_IN, W4_OP_MOE_DECODE = range(8)
 W4_SCORE_SIGMOID, W4_SCORE_SOFTMAX = range(2)
-W4_FMT_MXFP4, W4_FMT_NVFP4 = range(2)
+W4_FMT_MXFP4, W4_FMT_NVFP4, W4_FMT_INT4 = range(3)
 
 _DIR = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_DIR, "libw4.so")
@@ -87,6 +87,8 @@ _SIGNATURES = {
     "w4_fp4_gemm_bf16in": (_I32, [_P, _I32, _P, _P, _P, _P, _I32, _P, _P, _I64, _I64, _I64, _P, _SZ, _P]),
     "w4_fp4_moe_grouped_gemm": (_I32, [_P, _P, _P, _P, _I32, _P, _P, _P, _I32, _P, _I64, _I64, _I64, _P]),
     "w4_fp4_moe_gemm_bf16in": (_I32, [_P, _I64, _P, _P, _P, _I32, _P, _P, _P, _I32, _P, _I64, _I64, _I64, _P, _SZ, _P]),
+    "w4_moe_decode": (_I32, [_P, _P, _I32, _P, _I64, _I32, _I32, _I32, _I32, _I32, _I32, _F, _I32, _P, _P, _P, _I32, _P, _P,
+                             _P, _I32, _P, _I64, _I64, _P, _SZ, _P]),
     "w4_last_error": (ctypes.c_char_p, []),
     "w4_status_string": (ctypes.c_char_p, [_I32]),
     "w4_device_status": (_I32, [_P]),
@@ -579,6 +581,25 @@ def w4_fp4_moe_gemm_bf16in(x, row_token, expert_offsets, qweight, w_scale, forma
     ``[R, N]``."""
     return _native().fp4_moe_gemm_act(x, row_token, expert_offsets, qweight, w_scale, _fp4_format(format), x_global,
                                       w_global, y, workspace, _handle(stream))
+
+
+def w4_moe_decode(x, logits, gate_up, gate_up_scale, down, down_scale, top_k: int, format: str, gate_up_global=None,
+                  down_global=None, bias=None, n_group: int = 1, topk_group: int = 1, scoring: str = "sigmoid",
+                  renormalize: bool = True, scale: float = 1.0, y=None, workspace=None, stream=None):
+    """A whole routed MoE layer for up to 16 tokens: bf16 ``x [T, H]`` and router ``logits
+    [T, E]`` to bf16 ``[T, H]``. ``format`` of the weights: ``"int4"`` (``gate_up [E, 2I,
+    H/8]`` and ``down [E, H, I/8]`` int32 with fp16 scales ``[.., H/group]``, ``[..,
+    I/group]``, the group read off the shapes), ``"mxfp4"`` or ``"nvfp4"`` (uint8 ``[..,
+    K/2]`` and scales as ``w4_quant_fp4`` gives them, fp32 ``gate_up_global`` and
+    ``down_global [E]`` for nvfp4). Routing arguments as ``w4_moe_route_grouped``."""
+    if scoring not in _SCORING:
+        raise ValueError("scoring must be 'sigmoid' or 'softmax'")
+    fmt = W4_FMT_INT4 if format == "int4" else _FORMATS.get(format)
+    if fmt is None:
+        raise ValueError("format must be 'int4', 'mxfp4' or 'nvfp4'")
+    return _native().moe_decode(x, logits, gate_up, gate_up_scale, down, down_scale, top_k, fmt, gate_up_global,
+                                down_global, bias, n_group, topk_group, _SCORING[scoring], renormalize, scale, y,
+                                workspace, _handle(stream))
 
 
 def w4_moe_gather_quant_fp8(x, row_token, q=None, scale=None, stream=None):

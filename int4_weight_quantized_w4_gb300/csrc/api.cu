@@ -139,6 +139,7 @@ size_t w4_workspace_bytes(int32_t op, int64_t M, int64_t N, int64_t K, int32_t g
     return w4::fp8_block_workspace_bytes(M, K) +
            (group > 0 ? w4::fp8_block_workspace_bytes(M / 2, K) : w4::fp8_block_part_bytes(M, N, K));
   }
+  if (op == W4_OP_MOE_DECODE) return N > 0 ? w4::moe_decode_workspace_bytes(M, N, K) : 0;
   if (op == W4_OP_FP4_IN) return (group == 16 || group == 32) && K % group == 0 ? w4::fp4_workspace_bytes(M, K, group == 16) : 0;
   if (op == W4_OP_MOE_ROUTE) return (N > 0 && N <= 1024) ? w4::moe_route_workspace_bytes(M, static_cast<int32_t>(N)) : 0;
   return 0;
@@ -398,11 +399,9 @@ w4_status w4_moe_route(const void* logits, int32_t logits_f32, int64_t T, int32_
                    "moe route launch");
 }
 
-w4_status w4_moe_route_grouped(const void* logits, int32_t logits_f32, const float* bias, int64_t T, int32_t E,
-                               int32_t top_k, int32_t n_group, int32_t topk_group, int32_t scoring,
-                               int32_t renormalize, float scale, int32_t* topk_ids, float* topk_weights,
-                               int32_t* offsets, int32_t* row_token, int32_t* row_of, void* workspace,
-                               size_t workspace_bytes, void* stream) {
+// Which experts a grouped routing may choose.
+static w4_status check_route_choice(int64_t T, int32_t E, int32_t top_k, int32_t n_group, int32_t topk_group,
+                                    int32_t scoring) {
   if (T < 0) return fail(W4_ERR_SHAPE, "T must be >= 0");
   if (E < 1 || E > 1024) return fail(W4_ERR_UNSUPPORTED, "E must be in [1, 1024], got %d", E);
   if (scoring != W4_SCORE_SIGMOID && scoring != W4_SCORE_SOFTMAX)
@@ -415,6 +414,16 @@ w4_status w4_moe_route_grouped(const void* logits, int32_t logits_f32, const flo
   const int32_t open = topk_group * (E / n_group);
   if (top_k < 1 || top_k > open || top_k > 64)
     return fail(W4_ERR_SHAPE, "top_k must be in [1, min(64, experts of topk_group groups)], got %d (of %d)", top_k, open);
+  return W4_OK;
+}
+
+w4_status w4_moe_route_grouped(const void* logits, int32_t logits_f32, const float* bias, int64_t T, int32_t E,
+                               int32_t top_k, int32_t n_group, int32_t topk_group, int32_t scoring,
+                               int32_t renormalize, float scale, int32_t* topk_ids, float* topk_weights,
+                               int32_t* offsets, int32_t* row_token, int32_t* row_of, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  const w4_status st = check_route_choice(T, E, top_k, n_group, topk_group, scoring);
+  if (st != W4_OK) return st;
   if (T > INT32_MAX / top_k) return fail(W4_ERR_UNSUPPORTED, "T * top_k rows must fit in int32");
   if (T == 0) return ok();
   if (!logits || !topk_ids || !topk_weights || !offsets || !row_token || !row_of)
@@ -733,6 +742,55 @@ w4_status w4_fp4_moe_gemm_bf16in(const void* x, int64_t T, const float* x_global
   return run_fp4_act(x, false, T, row_token,
                      {nullptr, nullptr, qweight, w_scale, format == W4_FMT_NVFP4, x_global, w_global, nullptr, y, expert_offsets, E, R, N, K, nullptr},
                      workspace, workspace_bytes, stream);
+}
+
+w4_status w4_moe_decode(const void* x, const void* logits, int32_t logits_f32, const float* bias, int64_t T, int32_t E,
+                        int32_t top_k, int32_t n_group, int32_t topk_group, int32_t scoring, int32_t renormalize,
+                        float scale, int32_t format, const void* gate_up, const void* gate_up_scale,
+                        const float* gate_up_global, int32_t gate_up_group, const void* down, const void* down_scale,
+                        const float* down_global, int32_t down_group, void* y, int64_t H, int64_t I, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  w4_status st = check_route_choice(T, E, top_k, n_group, topk_group, scoring);
+  if (st != W4_OK) return st;
+  if (format != W4_FMT_INT4) {
+    st = check_fp4_format(format, gate_up_global, down_global);
+    if (st != W4_OK) return st;
+  } else if (gate_up_global != nullptr || down_global != nullptr) {
+    return fail(W4_ERR_UNSUPPORTED, "int4 has no scale per tensor");
+  }
+  if (H <= 0 || I <= 0) return fail(W4_ERR_SHAPE, "H and I must be > 0 (H=%lld I=%lld)", (long long)H, (long long)I);
+  if (H % 8 != 0 || I % 8 != 0) return fail(W4_ERR_ALIGN, "H and I must be multiples of 8, got H=%lld I=%lld", (long long)H, (long long)I);
+  if (H % 64 != 0 || I % 64 != 0 || H > INT32_MAX / 4 || I > INT32_MAX / 4)
+    return fail(W4_ERR_UNSUPPORTED, "H and I must be multiples of 64, got H=%lld I=%lld", (long long)H, (long long)I);
+  if (T > w4::kMoeDecodeTokens || E > w4::kMoeDecodeExperts || top_k > w4::kMoeDecodeTopK)
+    return fail(W4_ERR_UNSUPPORTED, "at most %d tokens, %d experts and top_k %d, got T=%lld E=%d top_k=%d", w4::kMoeDecodeTokens,
+                w4::kMoeDecodeExperts, w4::kMoeDecodeTopK, (long long)T, E, top_k);
+  if (format == W4_FMT_INT4) {
+    if (gate_up_group == -1) gate_up_group = static_cast<int32_t>(H);
+    if (down_group == -1) down_group = static_cast<int32_t>(I);
+    if (gate_up_group <= 0 || down_group <= 0 || H % gate_up_group != 0 || I % down_group != 0)
+      return fail(W4_ERR_GROUP, "groups must be -1 or positive divisors of H and I, got %d and %d", gate_up_group, down_group);
+    if (gate_up_group % 32 != 0 || down_group % 32 != 0)
+      return fail(W4_ERR_UNSUPPORTED, "groups must be multiples of 32, got %d and %d", gate_up_group, down_group);
+  }
+  const w4::MoeRouteArgs route{logits, bias, T, E, top_k, n_group, topk_group, logits_f32 == 0, scoring == W4_SCORE_SOFTMAX,
+                               renormalize != 0, scale, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr};
+  w4::MoeDecodeArgs a{route, x, format, gate_up_group, down_group, gate_up, gate_up_scale, gate_up_global, down, down_scale,
+                      down_global, H, I, y, workspace, nullptr};
+  if (!w4::moe_decode_fits(a))
+    return fail(W4_ERR_UNSUPPORTED, "T rows of x do not fit in shared memory (T=%lld H=%lld)", (long long)T, (long long)H);
+  if (T == 0) return ok();
+  if (!x || !logits || !gate_up || !gate_up_scale || !down || !down_scale || !y)
+    return fail(W4_ERR_NULL, "required pointer is NULL");
+  if (!aligned(x, 16) || !aligned(gate_up, 16) || !aligned(gate_up_scale, 16) || !aligned(down, 16) || !aligned(down_scale, 16) ||
+      !aligned(y, 16) || !aligned(logits, logits_f32 ? 4 : 2) || !aligned(bias, 4))
+    return fail(W4_ERR_ALIGN, "matrices and scales must be 16-byte aligned, logits and bias to their element size");
+  const size_t need = w4::moe_decode_workspace_bytes(T, top_k, I);
+  if (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 16))
+    return fail(W4_ERR_WORKSPACE, "workspace must be 16-byte aligned and at least %zu bytes (got %zu)", need, workspace_bytes);
+  const cudaError_t e = status_ptr(&a.status);
+  if (e != cudaSuccess) return from_cuda(e, "device status word");
+  return from_cuda(w4::launch_moe_decode(a, static_cast<cudaStream_t>(stream)), "moe decode launch");
 }
 
 w4_status w4_moe_gather_quant_fp8(const void* x, int64_t T, int64_t K, const int32_t* row_token, int64_t R,

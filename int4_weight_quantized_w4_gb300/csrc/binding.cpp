@@ -34,6 +34,7 @@ const Types kBf16 = {ScalarType::BFloat16};
 const Types kF32 = {ScalarType::Float};
 const Types kI32 = {ScalarType::Int};
 const Types kAct = {ScalarType::BFloat16, ScalarType::Half};
+const Types kHalf = {ScalarType::Half};
 const Types kByte = {ScalarType::Byte};
 const Types kScaleMx = {ScalarType::Float8_e8m0fnu, ScalarType::Byte};
 const Types kScaleNv = {ScalarType::Float8_e4m3fn, ScalarType::Byte};
@@ -563,12 +564,63 @@ PyObject* fp4_moe_gemm_act(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// x, logits, gate_up, gate_up_scale, down, down_scale, top_k, format, gate_up_global, down_global, bias, n_group,
+// topk_group, scoring, renormalize, scale, y, workspace, stream
+PyObject* moe_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!count(n, 19)) return nullptr;
+  const at::Tensor& x = ranked(a[0], "x", kBf16, nullptr, 2);
+  const at::Device dev = x.device();
+  const at::Tensor& logits = ranked(a[1], "logits", kLogit, &dev, 2);
+  const int64_t T = x.size(0), H = x.size(1), E = logits.size(1);
+  if (logits.size(0) != T) value_error("logits must have the %lld tokens of x", (long long)T);
+  if (E > INT32_MAX - 1) value_error("too many experts");
+  const int32_t k = integer32(a[6], "top_k"), fmt = integer32(a[7], "format");
+  const bool int4 = fmt == W4_FMT_INT4;
+  const int64_t per = int4 ? 8 : 2;   // columns in an element of the codes
+  const Types& codes = int4 ? kI32 : kByte;
+  const Types& scales = int4 ? kHalf : fmt == W4_FMT_NVFP4 ? kScaleNv : kScaleMx;
+  const at::Tensor& up = ranked(a[2], "gate_up", codes, &dev, 3);
+  if (up.size(0) != E || up.size(1) % 2 || up.size(2) * per != H) value_error("gate_up must hold E matrices of 2I rows of H columns");
+  const int64_t I = up.size(1) / 2;
+  const at::Tensor& down = tensor(a[4], "down", codes, dev, {E, H, I / per});
+  const at::Tensor& us = ranked(a[3], "gate_up_scale", scales, &dev, 3);
+  const at::Tensor& ds = ranked(a[5], "down_scale", scales, &dev, 3);
+  const int64_t block = int4 ? 0 : fmt == W4_FMT_NVFP4 ? 16 : 32;
+  auto group = [&](const at::Tensor& s, const char* name, int64_t rows, int64_t K) -> int32_t {
+    const int64_t G = s.size(2);
+    if (s.size(0) != E || s.size(1) != rows || G < 1 || (block ? G * block != K : K % G != 0))
+      value_error("%s does not match the weights: shape %s", name, shape_text(s.sizes()).c_str());
+    return static_cast<int32_t>(K / G);
+  };
+  const int32_t ug = group(us, "gate_up_scale", 2 * I, H), dg = group(ds, "down_scale", H, I);
+  const float* gu = global_scale(a[8], "gate_up_global", E, dev);
+  const float* gd = global_scale(a[9], "down_global", E, dev);
+  if (a[10] != Py_None) tensor(a[10], "bias", kF32, dev, {E});
+  const double scale = PyFloat_AsDouble(a[15]);
+  if (scale == -1.0 && PyErr_Occurred()) return nullptr;
+  const CallStream stream(a[18], dev);
+  const at::Tensor y = output(a[16], "y", {T, H}, ScalarType::BFloat16, kBf16, dev, stream);
+  // a call that the library refuses asks for no memory first
+  const bool small = T <= 16 && k >= 1 && k <= 32;
+  const Scratch s = scratch(a[17], W4_OP_MOE_DECODE, small ? T : 0, k, I, 0, dev);
+  if (failed(w4_moe_decode(x.data_ptr(), logits.data_ptr(), logits.scalar_type() == ScalarType::Float,
+                           static_cast<const float*>(data(a[10])), T, static_cast<int32_t>(E), k,
+                           integer32(a[11], "n_group"), integer32(a[12], "topk_group"), integer32(a[13], "scoring"),
+                           PyObject_IsTrue(a[14]), static_cast<float>(scale), fmt, up.data_ptr(), us.data_ptr(), gu, ug,
+                           down.data_ptr(), ds.data_ptr(), gd, dg, y.data_ptr(), H, I, s.p, s.bytes, stream.handle()),
+             "w4_moe_decode"))
+    return nullptr;
+  return THPVariable_Wrap(y);
+  END_HANDLE_TH_ERRORS
+}
+
 #define W4_METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {W4_METHOD(route_grouped), W4_METHOD(quant_block), W4_METHOD(silu_mul_quant_block),
                           W4_METHOD(gemm),          W4_METHOD(gemm_act),    W4_METHOD(moe_gemm),
                           W4_METHOD(moe_gemm_act),  W4_METHOD(quant_fp4),   W4_METHOD(dequant_fp4),
                           W4_METHOD(fp4_gemm),      W4_METHOD(fp4_gemm_act), W4_METHOD(fp4_moe_gemm),
-                          W4_METHOD(fp4_moe_gemm_act), {nullptr, nullptr, 0, nullptr}};
+                          W4_METHOD(fp4_moe_gemm_act), W4_METHOD(moe_decode), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

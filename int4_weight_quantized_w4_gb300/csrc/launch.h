@@ -217,6 +217,28 @@ inline size_t fp4_workspace_bytes(int64_t R, int64_t K, bool nv) {
   return fp4_code_bytes(R, K) + (static_cast<size_t>(R) * (K / fp4_block(nv)) + 15) / 16 * 16;
 }
 cudaError_t launch_fp4(const Fp4Args& a, cudaStream_t s);
+// Limits of the few-token expert layer.
+constexpr int kMoeDecodeTokens = 16, kMoeDecodeExperts = 256, kMoeDecodeTopK = 32;
+constexpr int kMoeDecodeSlots = 4;
+struct MoeDecodeArgs {
+  MoeRouteArgs route;           // logits [T, E] and how to choose; no outputs
+  const void* x;                // bf16 [T, H]
+  int32_t format, gate_up_group, down_group;   // groups: columns of an int4 scale
+  const void *gate_up, *gate_up_scale;   // [E, 2I, H/2 bytes], gate rows first
+  const float* gate_up_global;  // [E] or null
+  const void *down, *down_scale;         // [E, H, I/2 bytes]
+  const float* down_global;
+  int64_t H, I;
+  void* y;                      // bf16 [T, H]
+  void* workspace;              // moe_decode_workspace_bytes
+  unsigned int* status;
+};
+// fp16 activations of every chosen (token, expert) and an exponent per eight of them.
+inline size_t moe_decode_workspace_bytes(int64_t T, int64_t k, int64_t I) {
+  return (static_cast<size_t>(T * k) * static_cast<size_t>(2 * I + I / 8) + 15) / 16 * 16;
+}
+bool moe_decode_fits(const MoeDecodeArgs& a);
+cudaError_t launch_moe_decode(const MoeDecodeArgs& a, cudaStream_t s);
 cudaError_t launch_bounded_wait_selftest(long long limit, unsigned int* status, cudaStream_t s);
 
 }  // namespace w4

@@ -1,0 +1,615 @@
+// A whole mixture-of-experts layer for a few tokens, in two kernels: 4-bit weights
+// (int4 with fp16 group scales, mxfp4 or nvfp4), 16-bit activations.
+//
+//   route:  as route.cuh;
+//   up:     h = W_gu[e] x_t;  a = silu(h_gate) h_up            for every chosen (t, e)
+//   down:   y_t = bf16( sum_e w_te W_d[e] a_te ).
+//
+// The chosen experts' weights are nearly all there is to read, each weight once: bound by
+// HBM. Both kernels route for themselves (the logits are an input), so that the second
+// one's copies of weights can start while the first still computes, and no launch lies in
+// between.
+//
+// A unit of work is 16 weight rows of one expert: eight gate rows and their eight up rows
+// (up), or 16 output columns (down). Four warps take a unit together, each a quarter of
+// every 1024 columns, and add their sums in shared memory; a CTA has four such groups and
+// one warp that keeps every group's ring of row pieces full with bulk copies. The products
+// are mma.m16n8k16 in fp16 with fp32 sums: at 8 tokens an expert or fewer the tensor
+// core idles either way, and what counts is how few instructions turn a 32-bit word of
+// weights into operand registers. A word is 8 consecutive columns of a row, and a lane's
+// words are its operands as they lie: columns 8 c .. 8 c + 7 of 32 belong to lane c of a
+// quad for weights and activations alike, so that no shuffle is needed. int4 codes become
+// q - 8 by (q | 1024) - 1032 (exact in fp16, four words of five steps), e2m1 codes by the
+// conversion instruction; nvfp4 block scales are multiplied in (six mantissa bits, exact),
+// the others scale fp32 sums of their group.
+//
+// Activations are fp16 numbers times a power of two: x_t with its largest magnitude in
+// [2^14, 2^15) (a bf16 keeps all its bits down to 2^-29 of that), a_te the same over every
+// eight columns. Those exponents differ along k; a warp brings its columns to the
+// largest of them before it multiplies. fp16 rounds a to 11 bits where a bf16 step would
+// leave 8.
+//
+// Every sum has a fixed order: outputs are the same every time.
+#include "common.cuh"
+#include "launch.h"
+#include "route.cuh"
+#include "tc.cuh"
+#include "tiles.cuh"
+
+namespace w4 {
+namespace {
+
+constexpr int kGroups = 4, kGroupWarps = 4, kGroupThreads = 128;
+constexpr int kCompute = kGroups * kGroupThreads;    // threads that compute
+constexpr int kThreads = kCompute + 32;              // and the warp that copies
+constexpr int kChunkSteps = 32;                      // steps of 32 columns in a ring slot
+constexpr int kRowPitch = kChunkSteps * 16 + 16;     // bytes: eight rows start in different banks
+constexpr int kSlot = 16 * kRowPitch;
+constexpr int kMaxT = kMoeDecodeTokens, kMaxE = kMoeDecodeExperts, kMaxK = kMoeDecodeTopK, kMaxPairs = kMaxT * kMaxK;
+
+struct Params {
+  MoeRouteArgs route;      // ids and wts unset
+  const uint8_t* w;        // [E, rows, K/2 bytes]
+  const uint8_t* w_scale;  // [E, rows, scale_row bytes]
+  const float* w_global;   // [E] or null
+  const uint16_t* x;       // up: bf16 [T, H]
+  uint16_t* act;           // fp16 [pairs, I]
+  uint8_t* act_exp;        // [pairs, I / 8]: biased exponents
+  uint16_t* y;             // down: bf16 [T, H]
+  int H, I, K, rows;       // K: columns of w (up: H, down: I); rows an expert
+  int group_steps;         // int4: 32-column steps of a scale
+  int scale_row;           // bytes of a row's scales
+  int scale_pitch;         // the same in shared memory; scale_row: rows are copied as one block
+  int chunks, slots, scale_slots;
+  int split;               // down: CTAs of a cluster that share the experts of a slice
+  unsigned int* status;
+};
+
+// fp16 pairs of the 8 weights of a word; sc: the block's scale twice (nvfp4).
+// int4: columns (0,4), (1,5), (2,6), (3,7); else (0,1), (2,3), (4,5), (6,7).
+template <int kFmt>
+W4_DEV void widen(uint32_t w, uint32_t sc, uint32_t (&d)[4]) {
+  if constexpr (kFmt == W4_FMT_INT4) {
+    constexpr uint32_t k1024 = 0x64006400u, k1032 = 0x64086408u, kSixteenth = 0x2C002C00u, kMinus72 = 0xD480D480u;
+    const uint32_t v = w >> 8;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d[0]) : "r"(and_or(w, 0x000F000Fu, k1024)), "r"(k1032));
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d[1]) : "r"(and_or(w, 0x00F000F0u, k1024)), "r"(kSixteenth), "r"(kMinus72));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d[2]) : "r"(and_or(v, 0x000F000Fu, k1024)), "r"(k1032));
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d[3]) : "r"(and_or(v, 0x00F000F0u, k1024)), "r"(kSixteenth), "r"(kMinus72));
+  } else {
+    e2m1x8_to_f16(w, d);
+    if constexpr (kFmt == W4_FMT_NVFP4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(d[i]) : "r"(sc));
+    }
+  }
+}
+
+// Place of column i (of 8) in an activation's chunk, to match widen.
+template <int kFmt>
+W4_DEV int chunk_place(int i) {
+  return kFmt == W4_FMT_INT4 ? (i & 3) * 2 + (i >> 2) : i;
+}
+
+W4_DEV void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// What routing leaves in shared memory, the same in every CTA. Rows of the activations
+// are the chosen pairs by expert, then token.
+struct Routed {
+  uint32_t mask[kMaxE];        // tokens of an expert
+  int32_t ids[kMaxPairs];
+  float wts[kMaxPairs];
+  float weight[kMaxPairs];     // of a row
+  uint8_t token[kMaxPairs];    // of a row
+  int16_t expert[kMaxE];       // the chosen experts in ascending order
+  int16_t first[kMaxE + 1];    // their first rows
+  int32_t part[8];
+  int n;                       // how many
+  int x_exp[kMaxT];            // up: exponent taken out of x_t
+};
+
+W4_DEV void group_sync(int group) { asm volatile("bar.sync %0, %1;" :: "r"(group + 1), "r"(kGroupThreads) : "memory"); }
+
+// All threads. scratch: 16 x 8 x 33 words of shared memory. Warps call also(warp) on the way.
+template <class Also>
+W4_DEV void route_all(const Params& p, Routed& s, uint32_t* scratch, Also also) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int T = static_cast<int>(p.route.T), E = p.route.E, k = p.route.k;
+  for (int e = threadIdx.x; e < kMaxE; e += kThreads) s.mask[e] = 0;
+  __syncthreads();
+  if (warp < T) {
+    MoeRouteArgs a = p.route;
+    a.ids = s.ids;
+    a.wts = s.wts;
+    int mine[2];
+    if (E <= 64) {
+      float v[2];
+      load_logits<2>(a, warp, v);
+      route_token<2>(a, warp, v, scratch + warp * 8 * 33, mine);
+    } else {
+      float v[8];
+      load_logits<8>(a, warp, v);
+      route_token<8>(a, warp, v, scratch + warp * 8 * 33, mine);
+    }
+    if (lane < k) atomicOr(&s.mask[mine[0]], 1u << warp);
+  }
+  also(warp);
+  __syncthreads();
+  // the chosen experts and their first rows: a scan of (rows, experts) over 256 threads
+  int v = 0, inc = 0;
+  if (warp < 8) {
+    const uint32_t m = s.mask[threadIdx.x];
+    v = inc = m != 0 ? (__popc(m) << 16) | 1 : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(kFull, inc, o);
+      if (lane >= o) inc += u;
+    }
+    if (lane == 31) s.part[warp] = inc;
+  }
+  __syncthreads();
+  if (warp < 8) {
+    int before = inc - v;
+    for (int w = 0; w < warp; ++w) before += s.part[w];
+    if (v != 0) {
+      s.expert[before & 0xFFFF] = static_cast<int16_t>(threadIdx.x);
+      s.first[before & 0xFFFF] = static_cast<int16_t>(before >> 16);
+      s.mask[threadIdx.x] |= (before >> 16) << 16;   // first row beside the tokens, for the rows below
+    }
+    if (threadIdx.x == 255) {
+      s.n = (before + v) & 0xFFFF;
+      s.first[s.n] = static_cast<int16_t>((before + v) >> 16);
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < T * k; i += kThreads) {
+    const uint32_t m = s.mask[s.ids[i]];
+    const int t = i / k, r = static_cast<int>(m >> 16) + __popc(m & 0xFFFFu & ((1u << t) - 1u));
+    s.token[r] = static_cast<uint8_t>(t);
+    s.weight[r] = s.wts[i];
+  }
+  __syncthreads();
+}
+
+// x_t as fp16 times a power of two, by one warp; returns the exponent taken out.
+template <int kFmt>
+W4_DEV int widen_row(const Params& p, int t, uint8_t* to) {
+  const int lane = threadIdx.x & 31;
+  const uint4* xr = reinterpret_cast<const uint4*>(p.x) + static_cast<size_t>(t) * (p.H / 8);
+  uint32_t m = 0;
+  for (int i = lane; i < p.H / 8; i += 32) {
+    const uint4 v = ld_cg_v4(xr + i);
+    m = __vmaxu2(__vmaxu2(m, v.x & 0x7FFF7FFFu), v.y & 0x7FFF7FFFu);
+    m = __vmaxu2(__vmaxu2(m, v.z & 0x7FFF7FFFu), v.w & 0x7FFF7FFFu);
+  }
+  m = __reduce_max_sync(kFull, max(m & 0xFFFFu, m >> 16));
+  const int e = max(static_cast<int>(m >> 7), 15);   // biased exponent; factors are normal numbers
+  const float f = __uint_as_float(static_cast<uint32_t>(min(268 - e, 254)) << 23);   // 2^(14 - (e - 127))
+  for (int i = lane; i < p.H / 8; i += 32) {
+    const uint4 v = ld_cg_v4(xr + i);
+    float a[8];
+    chunk_f32<false>(v, a);
+    uint32_t h[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int lo = kFmt == W4_FMT_INT4 ? j : 2 * j, hi = kFmt == W4_FMT_INT4 ? j + 4 : 2 * j + 1;
+      asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[j]) : "f"(a[hi] * f), "f"(a[lo] * f));
+    }
+    *reinterpret_cast<uint4*>(to + i * 16) = make_uint4(h[0], h[1], h[2], h[3]);
+  }
+  return 127 - min(268 - e, 254);
+}
+
+// One unit's rows of weights: two blocks of eight rows.
+struct Unit {
+  int a;                 // index among the chosen experts
+  size_t row[2];         // first row of each block, over all experts
+};
+
+template <bool kDown>
+W4_DEV Unit unit_of(const Params& p, const Routed& s, int u) {
+  Unit t;
+  if constexpr (kDown) {
+    t.a = u;
+    const int n0 = static_cast<int>(blockIdx.x) / p.split * 16;
+    t.row[0] = static_cast<size_t>(s.expert[u]) * p.rows + n0;
+    t.row[1] = t.row[0] + 8;
+  } else {
+    const int per = p.I / 8;
+    t.a = u / per;
+    t.row[0] = static_cast<size_t>(s.expert[t.a]) * p.rows + (u - t.a * per) * 8;
+    t.row[1] = t.row[0] + p.I;
+  }
+  return t;
+}
+
+// Scale of row r, block b of the unit's scales in shared memory.
+template <int kFmt>
+W4_DEV uint32_t scale_f16x2(const uint8_t* row, int b) {
+  const uint32_t s8 = row[b];
+  return e4m3x2_to_f16x2(s8 * 0x0101u);
+}
+template <int kFmt>
+W4_DEV float scale_f32(const uint8_t* row, int b) {
+  if constexpr (kFmt == W4_FMT_INT4) {
+    return half_bits_to_f32(reinterpret_cast<const uint16_t*>(row)[b]);
+  } else {
+    const uint32_t s8 = row[b];
+    return __uint_as_float(s8 == 0 ? 1u << 22 : s8 == 255 ? 0x7FC00000u : s8 << 23);
+  }
+}
+
+// Adds this warp's steps [s0, s1) (of the whole row; the slot starts at step c0) to y: rows
+// lane / 4 and lane / 4 + 8 of the slot times the columns that b(step) gives. b: the lane's
+// 8 activations of step `step` (columns 32 step + 8 (lane % 4) ..) of token lane / 4.
+template <int kFmt, class B>
+W4_DEV void multiply(const Params& p, const uint8_t* slot, const uint8_t* scales, int c0, int s0, int s1, B b,
+                     float (&y)[4]) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const uint8_t* w0 = slot + g * kRowPitch + 4 * c - c0 * 16;
+  const uint8_t* sc0 = scales + g * p.scale_pitch;
+  const uint8_t* sc1 = sc0 + 8 * p.scale_pitch;
+  auto step = [&](int s, float (&d)[4]) {
+    const uint32_t wa = *reinterpret_cast<const uint32_t*>(w0 + s * 16);
+    const uint32_t wb = *reinterpret_cast<const uint32_t*>(w0 + 8 * kRowPitch + s * 16);
+    uint32_t fa = 0, fb = 0;
+    if constexpr (kFmt == W4_FMT_NVFP4) {
+      fa = scale_f16x2<kFmt>(sc0, 2 * s + (c >> 1));
+      fb = scale_f16x2<kFmt>(sc1, 2 * s + (c >> 1));
+    }
+    uint32_t ra[4], rb[4];
+    widen<kFmt>(wa, fa, ra);
+    widen<kFmt>(wb, fb, rb);
+    const uint4 v = b(s);
+    mma16816(d, ra[0], rb[0], ra[1], rb[1], v.x, v.y);
+    mma16816(d, ra[2], rb[2], ra[3], rb[3], v.z, v.w);
+  };
+  if constexpr (kFmt == W4_FMT_NVFP4) {
+#pragma unroll 4
+    for (int s = s0; s < s1; ++s) step(s, y);
+  } else if constexpr (kFmt == W4_FMT_MXFP4) {
+#pragma unroll 4
+    for (int s = s0; s < s1; ++s) {
+      float d[4] = {0.f, 0.f, 0.f, 0.f};
+      step(s, d);
+      const float fa = scale_f32<kFmt>(sc0, s), fb = scale_f32<kFmt>(sc1, s);
+      y[0] = fmaf(fa, d[0], y[0]), y[1] = fmaf(fa, d[1], y[1]);
+      y[2] = fmaf(fb, d[2], y[2]), y[3] = fmaf(fb, d[3], y[3]);
+    }
+  } else {
+    int grp = s0 / p.group_steps;
+    for (int s = s0; s < s1; ++grp) {
+      const int end = min(s1, (grp + 1) * p.group_steps);
+      const float fa = scale_f32<kFmt>(sc0, grp), fb = scale_f32<kFmt>(sc1, grp);
+      float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+      for (; s < end; ++s) step(s, d);
+      y[0] = fmaf(fa, d[0], y[0]), y[1] = fmaf(fa, d[1], y[1]);
+      y[2] = fmaf(fb, d[2], y[2]), y[3] = fmaf(fb, d[3], y[3]);
+    }
+  }
+}
+
+// Shared memory beyond Routed: barriers, sums of the groups' warps, then (dynamic) the rings
+// of row pieces and of scales, and up: x in fp16, down: each group's outputs.
+struct Common {
+  Routed r;
+  alignas(16) float red[kGroups][2][kGroupWarps][2][32][4];   // [group][alternating][warp][8 tokens][lane]
+  uint64_t full[kGroups][kMoeDecodeSlots], empty[kGroups][kMoeDecodeSlots];
+  int abort_flag;
+};
+
+template <int kFmt, bool kDown>
+__global__ void __launch_bounds__(kThreads, 1) moe_decode_kernel(const __grid_constant__ Params p) {
+  extern __shared__ uint8_t smem_dyn[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 127) & ~uintptr_t(127));
+  Common& c = *reinterpret_cast<Common*>(smem);
+  Routed& r = c.r;
+  uint8_t* ring = smem + (sizeof(Common) + 127) / 128 * 128;
+  uint8_t* scale_ring = ring + kGroups * p.slots * kSlot;
+  const int scale_slot = 16 * p.scale_pitch;
+  uint8_t* rest = scale_ring + kGroups * p.scale_slots * scale_slot;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int T = static_cast<int>(p.route.T);
+  volatile int* abort_flag = &c.abort_flag;
+
+  if (threadIdx.x == 0) {
+    for (int g = 0; g < kGroups; ++g)
+      for (int i = 0; i < p.slots; ++i) {
+        mbar_init(&c.full[g][i], 1);
+        mbar_init(&c.empty[g][i], kGroupWarps);
+      }
+    c.abort_flag = 0;
+    fence_mbar_init();
+  }
+  // down: the up kernel lets this one go when all before it are done, so the logits are there
+  if (!kDown) grid_dependency_wait();
+  launch_dependents();
+  const int x_pitch = 2 * p.H + 64;   // two tokens' pieces lie in different banks
+  route_all(p, r, reinterpret_cast<uint32_t*>(ring), [&](int w) {
+    const int t = T <= 8 ? w - 8 : w;   // by warps that route no token, where there are
+    if (!kDown && t >= 0 && t < T) {
+      const int e = widen_row<kFmt>(p, t, rest + t * x_pitch);
+      if (lane == 0) r.x_exp[t] = e;
+    }
+  });
+
+  // units of this CTA: up, a share of all (expert, eight columns) in order; down, every split-th expert
+  const int rank = kDown && p.split > 1 ? static_cast<int>(cluster_rank()) : 0;
+  int u0, u1, stride;
+  if constexpr (kDown) {
+    u0 = rank, u1 = r.n, stride = p.split;
+  } else {
+    const long long all = static_cast<long long>(r.n) * (p.I / 8);
+    u0 = static_cast<int>(all * blockIdx.x / gridDim.x);
+    u1 = static_cast<int>(all * (blockIdx.x + 1) / gridDim.x);
+    stride = 1;
+  }
+  const int steps = p.K / 32;
+
+  if (warp == kCompute / 32) {
+    // copies: a lane to a row; round by round, every group's unit
+    int count = 0, round = 0;
+    bool ok = true;
+    tc::fence_proxy_async_smem();   // the ring held the routing's scratch
+    for (int ub = u0; ok && ub < u1; ub += kGroups * stride, ++round)
+      for (int ch = 0; ok && ch < p.chunks; ++ch, ++count) {
+        const int slot = count % p.slots, ph = (count / p.slots & 1) ^ 1;
+        for (int g = 0; g < kGroups; ++g) {
+          const int u = ub + g * stride;
+          if (u >= u1) break;
+          if (!(ok = wait_warp(&c.empty[g][slot], ph, abort_flag, p.status))) break;
+          const Unit t = unit_of<kDown>(p, r, u);
+          const int s0 = ch * kChunkSteps, bytes = min(kChunkSteps, steps - s0) * 16;
+          const int blk = lane >> 3 & 1, i = lane & 7;
+          uint64_t* bar = &c.full[g][slot];
+          if (lane == 0) mbar_arrive_expect_tx(bar, 16 * bytes + (ch == 0 ? 16 * p.scale_row : 0));
+          __syncwarp();
+          if (lane < 16)
+            tc::bulk_load(ring + (g * p.slots + slot) * kSlot + lane * kRowPitch,
+                          p.w + (t.row[blk] + i) * (p.K / 2) + s0 * 16, bytes, bar);
+          if (ch == 0) {
+            uint8_t* to = scale_ring + (g * p.scale_slots + round % p.scale_slots) * scale_slot;
+            if (p.scale_pitch != p.scale_row) {
+              if (lane < 16) tc::bulk_load(to + lane * p.scale_pitch, p.w_scale + (t.row[blk] + i) * p.scale_row, p.scale_row, bar);
+            } else if (lane < 2) {
+              tc::bulk_load(to + lane * 8 * p.scale_pitch, p.w_scale + t.row[lane] * p.scale_row, 8 * p.scale_row, bar);
+            }
+          }
+        }
+      }
+  } else {
+    const int group = warp / kGroupWarps, w = warp % kGroupWarps, tid = threadIdx.x % kGroupThreads;
+    const int g = lane >> 2, q = lane & 3;
+    float* out = reinterpret_cast<float*>(rest) + group * T * 16;   // down: [T][16]
+    if constexpr (kDown) {
+      for (int i = tid; i < T * 16; i += kGroupThreads) out[i] = 0.f;
+      grid_dependency_wait();   // the activations, and y may still be read
+    }
+    int count = 0, round = 0;
+    bool ok = true;
+    for (int u = u0 + group * stride; u < u1; u += kGroups * stride, ++round) {
+      const Unit t = unit_of<kDown>(p, r, u);
+      const int first = r.first[t.a], tokens = r.first[t.a + 1] - first;
+      const uint8_t* scales = scale_ring + (group * p.scale_slots + round % p.scale_slots) * scale_slot;
+      float y[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      for (int ch = 0; ch < p.chunks; ++ch, ++count) {
+        const int slot = count % p.slots;
+        const int c0 = ch * kChunkSteps, n = min(kChunkSteps, steps - c0);
+        const int s0 = c0 + n * w / kGroupWarps, s1 = c0 + n * (w + 1) / kGroupWarps;
+        const uint8_t* piece = ring + (group * p.slots + slot) * kSlot;
+        // after a time-out the group goes on without waiting, so that its warps still meet
+        ok = ok && wait_warp(&c.full[group][slot], count / p.slots & 1, abort_flag, p.status);
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb) {
+          if (8 * nb >= tokens) break;
+          const int row = first + min(8 * nb + g, tokens - 1);   // columns past the last token repeat it
+          if constexpr (kDown) {
+            constexpr int kPer = kChunkSteps / kGroupWarps;
+            const uint16_t* ar = p.act + static_cast<size_t>(row) * p.K + 8 * q;
+            const uint8_t* er = p.act_exp + static_cast<size_t>(row) * (p.K / 8) + q;
+            uint4 v[kPer];
+            int e[kPer], top = 0;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+              if (s0 + i < s1) {
+                v[i] = ld_cg_v4(ar + 32 * (s0 + i));
+                e[i] = __ldcg(er + 4 * (s0 + i));
+              }
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+              if (s0 + i < s1) top = max(top, e[i]);
+            top = max(top, __shfl_xor_sync(kFull, top, 1));
+            top = max(top, __shfl_xor_sync(kFull, top, 2));
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+              if (s0 + i < s1) {
+                const float f = __uint_as_float(static_cast<uint32_t>(max(127 + e[i] - top, 0)) << 23);
+                uint32_t h;
+                asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(h) : "f"(f));
+                asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(v[i].x) : "r"(h));
+                asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(v[i].y) : "r"(h));
+                asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(v[i].z) : "r"(h));
+                asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(v[i].w) : "r"(h));
+              }
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+              if (s0 + i < s1) multiply<kFmt>(p, piece, scales, c0, s0 + i, s0 + i + 1, [&](int) { return v[i]; }, d);
+            // a factor 2^(top - 127 - 14) for this lane's two columns
+            const int t0 = __shfl_sync(kFull, top, 8 * q), t1 = __shfl_sync(kFull, top, 8 * q + 4);
+            const float f0 = ldexpf(1.f, t0 - 141), f1 = ldexpf(1.f, t1 - 141);
+            y[nb][0] = fmaf(d[0], f0, y[nb][0]), y[nb][1] = fmaf(d[1], f1, y[nb][1]);
+            y[nb][2] = fmaf(d[2], f0, y[nb][2]), y[nb][3] = fmaf(d[3], f1, y[nb][3]);
+          } else {
+            const uint8_t* xr = rest + r.token[row] * x_pitch + 16 * q;
+            multiply<kFmt>(p, piece, scales, c0, s0, s1,
+                           [&](int s) { return *reinterpret_cast<const uint4*>(xr + 64 * s); }, y[nb]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c.empty[group][slot]);
+      }
+      float (*red)[2][32][4] = c.red[group][round & 1];
+#pragma unroll
+      for (int nb = 0; nb < 2; ++nb)
+        if (8 * nb < tokens) *reinterpret_cast<float4*>(red[w][nb][lane]) = make_float4(y[nb][0], y[nb][1], y[nb][2], y[nb][3]);
+      group_sync(group);
+      const float gl = p.w_global != nullptr ? __ldcg(p.w_global + r.expert[t.a]) : 1.f;
+      if constexpr (kDown) {
+        for (int nb = 0; 8 * nb < tokens; ++nb) {
+          const int o = tid & 15, n = 8 * nb + (tid >> 4);
+          if (n < tokens) {
+            const int l = (o & 7) * 4 + (n & 7) / 2, j = (o >> 3) * 2 + (n & 1);
+            const float v = ((red[0][nb][l][j] + red[1][nb][l][j]) + red[2][nb][l][j]) + red[3][nb][l][j];
+            float& at = out[r.token[first + n] * 16 + o];
+            at = fmaf(v, gl * r.weight[first + n], at);
+          }
+        }
+      } else {
+        // thread: column tid % 8 of the unit, token tid / 8
+        const int i = tid & 7, n = tid >> 3, nb = n >> 3;
+        if (8 * (tid >> 6) < tokens) {   // whole warps: 64 threads for eight tokens
+          const int m = min(n, tokens - 1), l = i * 4 + (m & 7) / 2, j = m & 1, mb = m >> 3;
+          float gate = ((red[0][mb][l][j] + red[1][mb][l][j]) + red[2][mb][l][j]) + red[3][mb][l][j];
+          float up = ((red[0][mb][l][2 + j] + red[1][mb][l][2 + j]) + red[2][mb][l][2 + j]) + red[3][mb][l][2 + j];
+          const int e = r.x_exp[r.token[first + m]];
+          gate = ldexpf(gate, e) * gl;
+          up = ldexpf(up, e) * gl;
+          const float a = __fdiv_rn(gate, 1.f + expf(-gate)) * up;
+          uint32_t bits = __float_as_uint(a) & 0x7FFFFFFFu;
+          bits = max(bits, __shfl_xor_sync(kFull, bits, 1));
+          bits = max(bits, __shfl_xor_sync(kFull, bits, 2));
+          bits = max(bits, __shfl_xor_sync(kFull, bits, 4));
+          const uint32_t ex = max(bits >> 23, 14u);   // a 2^(14 - (ex - 127)): the largest in [2^14, 2^15)
+          if (n < tokens) {
+            const int i0 = static_cast<int>(t.row[0] - static_cast<size_t>(r.expert[t.a]) * p.rows);
+            uint16_t h;
+            asm("cvt.rn.f16.f32 %0, %1;" : "=h"(h) : "f"(a * __uint_as_float((268u - ex) << 23)));
+            p.act[static_cast<size_t>(first + n) * p.I + i0 + chunk_place<kFmt>(i)] = h;
+            if (i == 0) p.act_exp[static_cast<size_t>(first + n) * (p.I / 8) + i0 / 8] = static_cast<uint8_t>(ex);
+          }
+        }
+        (void)nb;
+      }
+    }
+  }
+
+  if constexpr (kDown) {
+    __syncthreads();
+    // the groups' outputs in order, then (split) the CTAs' of the cluster
+    float* sum = reinterpret_cast<float*>(rest);
+    for (int i = threadIdx.x; i < T * 16; i += kThreads) {
+      float v = sum[i];
+      for (int g = 1; g < kGroups; ++g) v += sum[g * T * 16 + i];
+      sum[i] = v;
+    }
+    if (p.split > 1) {
+      cluster_arrive();
+      cluster_wait();
+    } else {
+      __syncthreads();
+    }
+    const int n0 = static_cast<int>(blockIdx.x) / p.split * 16;
+    const int i = threadIdx.x * 4;
+    if (rank == 0 && i < T * 16) {
+      float4 v = *reinterpret_cast<const float4*>(sum + i);
+      for (int k = 1; k < p.split; ++k) {
+        const float4 o = ld_cluster_f32x4(smem_addr(sum + i), k);
+        v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+      }
+      *reinterpret_cast<uint2*>(p.y + static_cast<size_t>(i / 16) * p.H + n0 + i % 16) =
+          make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    }
+    if (p.split > 1) {
+      __syncwarp();
+      cluster_arrive();
+      cluster_wait();
+    }
+  }
+  if (*abort_flag) {   // let copies in flight land before the shared memory goes away
+    const uint64_t t0 = tc::globaltimer_ns();
+    while (tc::globaltimer_ns() - t0 < 1000000ull) {
+    }
+  }
+}
+
+// Bytes of a row's scales.
+int scale_row_bytes(const MoeDecodeArgs& a, bool down) {
+  const int64_t K = down ? a.I : a.H;
+  return static_cast<int>(a.format == W4_FMT_INT4 ? 2 * (K / (down ? a.down_group : a.gate_up_group)) : a.format == W4_FMT_NVFP4 ? K / 16 : K / 32);
+}
+
+template <int kFmt, bool kDown>
+cudaError_t run(const MoeDecodeArgs& a, cudaStream_t s) {
+  Params p = {};
+  p.route = a.route;
+  const int T = static_cast<int>(a.route.T);
+  p.w = static_cast<const uint8_t*>(kDown ? a.down : a.gate_up);
+  p.w_scale = static_cast<const uint8_t*>(kDown ? a.down_scale : a.gate_up_scale);
+  p.w_global = kDown ? a.down_global : a.gate_up_global;
+  p.x = static_cast<const uint16_t*>(a.x);
+  p.act = static_cast<uint16_t*>(a.workspace);
+  p.act_exp = reinterpret_cast<uint8_t*>(p.act + static_cast<size_t>(T) * a.route.k * a.I);
+  p.y = static_cast<uint16_t*>(a.y);
+  p.H = static_cast<int>(a.H);
+  p.I = static_cast<int>(a.I);
+  p.K = kDown ? p.I : p.H;
+  p.rows = kDown ? p.H : 2 * p.I;
+  p.group_steps = kFmt == W4_FMT_INT4 ? (kDown ? a.down_group : a.gate_up_group) / 32 : 1;
+  p.scale_row = scale_row_bytes(a, kDown);
+  // rows of whole 16 bytes are copied one by one to a pitch that spreads eight rows over the banks
+  p.scale_pitch = p.scale_row % 16 != 0 ? p.scale_row : p.scale_row % 32 == 0 ? p.scale_row + 16 : p.scale_row + 32;
+  p.chunks = (p.K / 32 + kChunkSteps - 1) / kChunkSteps;
+  p.status = a.status;
+  const int rest = kDown ? kGroups * T * 64 : T * (2 * p.H + 64);
+  const int base = 128 + (static_cast<int>(sizeof(Common)) + 127) / 128 * 128 + rest;
+  int smem = 0;
+  for (p.slots = kMoeDecodeSlots; p.slots >= 2; --p.slots) {
+    p.scale_slots = (p.slots + p.chunks - 1) / p.chunks + 1;
+    smem = base + kGroups * (p.slots * kSlot + p.scale_slots * 16 * p.scale_pitch);
+    if (smem <= 232448) break;
+  }
+  if (p.slots < 2) return cudaErrorInvalidConfiguration;   // refused before (moe_decode_fits)
+  p.split = 1;
+  int64_t grid = current_sm_count();
+  if (kDown) {
+    const int64_t slices = p.H / 16;
+    for (int n = kMaxSplit; n > 1 && p.split == 1; n /= 2)
+      if (slices * n <= grid && n <= a.route.k * T) p.split = n;
+    grid = slices * p.split;
+  }
+  return start<moe_decode_kernel<kFmt, kDown>>(p, grid, kThreads, smem, p.split, s);
+}
+
+template <int kFmt>
+cudaError_t run_both(const MoeDecodeArgs& a, cudaStream_t s) {
+  const cudaError_t e = run<kFmt, false>(a, s);
+  return e == cudaSuccess ? run<kFmt, true>(a, s) : e;
+}
+
+}  // namespace
+
+// Two ring slots a group beside the activations, for either kernel.
+bool moe_decode_fits(const MoeDecodeArgs& a) {
+  const int64_t common = 256 + static_cast<int64_t>(sizeof(Common));
+  for (bool down : {false, true}) {
+    const int64_t K = down ? a.I : a.H;
+    const int64_t chunks = (K / 32 + kChunkSteps - 1) / kChunkSteps;
+    const int64_t ring = kGroups * (2 * kSlot + ((2 + chunks - 1) / chunks + 1) * 16 * (static_cast<int64_t>(scale_row_bytes(a, down)) + 32));
+    const int64_t rest = down ? kGroups * a.route.T * 64 : a.route.T * (2 * a.H + 64);
+    if (common + ring + rest > 232448) return false;
+  }
+  return true;
+}
+
+cudaError_t launch_moe_decode(const MoeDecodeArgs& a, cudaStream_t s) {
+  if (a.format == W4_FMT_INT4) return run_both<W4_FMT_INT4>(a, s);
+  return a.format == W4_FMT_NVFP4 ? run_both<W4_FMT_NVFP4>(a, s) : run_both<W4_FMT_MXFP4>(a, s);
+}
+
+}  // namespace w4

@@ -108,3 +108,24 @@ def fp4_grouped_linear(qx, x_scale, offsets, qweight, w_scale, fmt, x_global=Non
             y[r] = fp4_linear(qx[r], x_scale[r], qweight[e], w_scale[e], fmt, x_global,
                               None if w_global is None else w_global[e])
     return y
+
+
+def moe_decode(x_bits, logits, gate_up, down, top_k, **route):
+    """A whole routed layer in float64. gate_up(e) [2I, H] and down(e) [H, I] give an expert's
+    weights as values. Returns ``(y [T, H], size [T, H])``: size is the sum of the
+    magnitudes that make up y, weight by weight and activation by activation."""
+    from .fp8_block_oracle import moe_route_grouped
+    from .w4_oracle import bf16_to_f64
+    x = bf16_to_f64(x_bits)
+    ids, wts, _ = moe_route_grouped(logits, top_k, **route)
+    y, size = np.zeros(x.shape), np.zeros(x.shape)
+    for e in sorted(set(ids.ravel().tolist())):
+        gu, d = gate_up(e), down(e)
+        for t, j in zip(*np.nonzero(ids == e)):
+            h = gu @ x[t]
+            I = h.size // 2
+            with np.errstate(over="ignore"):
+                a = h[:I] / (1.0 + np.exp(-h[:I])) * h[I:]
+            y[t] += wts[t, j] * (d @ a)
+            size[t] += wts[t, j] * (np.abs(d) @ np.abs(a))
+    return y, size
