@@ -10,10 +10,10 @@
 // one's copies of weights can start while the first still computes, and no launch lies in
 // between.
 //
-// A unit of work is 16 weight rows of one expert: eight gate rows and their eight up rows
-// (up), or 16 output columns (down). Four warps take a unit together, each a quarter of
-// every 1024 columns, and add their sums in shared memory; a CTA has four such groups and
-// one warp that keeps every group's ring of row pieces full with bulk copies. The products
+// A unit of work is 32 weight rows of one expert: 16 gate rows and their 16 up rows
+// (up), or 32 output columns (down). Four warps take a unit together, each a quarter of
+// every 512 columns, and add their sums in shared memory; a CTA has four such groups, each
+// with a ring of row pieces that TMA keeps full. The products
 // are mma.m16n8k16 in fp16 with fp32 sums: at 8 tokens an expert or fewer the tensor
 // core idles either way, and what counts is how few instructions turn a 32-bit word of
 // weights into operand registers. A word is 8 consecutive columns of a row, and a lane's
@@ -40,16 +40,17 @@ namespace w4 {
 namespace {
 
 constexpr int kGroups = 4, kGroupWarps = 4, kGroupThreads = 128;
-constexpr int kCompute = kGroups * kGroupThreads;    // threads that compute
-constexpr int kThreads = kCompute + 32;              // and the warp that copies
-constexpr int kChunkSteps = 32;                      // steps of 32 columns in a ring slot
-constexpr int kRowPitch = kChunkSteps * 16 + 16;     // bytes: eight rows start in different banks
-constexpr int kSlot = 16 * kRowPitch;
+constexpr int kThreads = kGroups * kGroupThreads;    // 16 warps leave a thread 128 registers, a 17th would leave 96
+constexpr int kChunkSteps = 16;                      // steps of 32 columns in a ring slot
+constexpr int kPer = kChunkSteps / kGroupWarps;      // a warp's of them
+constexpr int kRows = 32;                            // weight rows of a unit
+constexpr int kBox = kRows * 128;                    // 8 steps of them, 128-byte swizzle: 16-byte chunk c of row r at c ^ r % 8
+constexpr int kSlot = kChunkSteps / 8 * kBox;
 constexpr int kMaxT = kMoeDecodeTokens, kMaxE = kMoeDecodeExperts, kMaxK = kMoeDecodeTopK, kMaxPairs = kMaxT * kMaxK;
 
 struct Params {
+  CUtensorMap tm_w;        // up: [2E, I, K/2 bytes] in boxes of 16 rows of two matrices; down: [E, H, K/2 bytes], 32 rows
   MoeRouteArgs route;      // ids and wts unset
-  const uint8_t* w;        // [E, rows, K/2 bytes]
   const uint8_t* w_scale;  // [E, rows, scale_row bytes]
   const float* w_global;   // [E] or null
   const uint16_t* x;       // up: bf16 [T, H]
@@ -59,7 +60,7 @@ struct Params {
   int H, I, K, rows;       // K: columns of w (up: H, down: I); rows an expert
   int group_steps;         // int4: 32-column steps of a scale
   int scale_row;           // bytes of a row's scales
-  int scale_pitch;         // the same in shared memory; scale_row: rows are copied as one block
+  int scale_pitch;         // the same in shared memory
   int chunks, slots, scale_slots;
   int split;               // down: CTAs of a cluster that share the experts of a slice
   unsigned int* status;
@@ -92,7 +93,7 @@ W4_DEV int chunk_place(int i) {
 }
 
 W4_DEV void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -204,9 +205,10 @@ W4_DEV int widen_row(const Params& p, int t, uint8_t* to) {
   return 127 - min(268 - e, 254);
 }
 
-// One unit's rows of weights: two blocks of eight rows.
+// One unit's rows of weights: two blocks of 16, one behind the other (down) or gate and up.
 struct Unit {
   int a;                 // index among the chosen experts
+  int n0, mat;           // first row and matrix of its box
   size_t row[2];         // first row of each block, over all experts
 };
 
@@ -215,81 +217,130 @@ W4_DEV Unit unit_of(const Params& p, const Routed& s, int u) {
   Unit t;
   if constexpr (kDown) {
     t.a = u;
-    const int n0 = static_cast<int>(blockIdx.x) / p.split * 16;
-    t.row[0] = static_cast<size_t>(s.expert[u]) * p.rows + n0;
-    t.row[1] = t.row[0] + 8;
+    t.n0 = static_cast<int>(blockIdx.x) / p.split * kRows;
+    t.mat = s.expert[u];
+    t.row[0] = static_cast<size_t>(t.mat) * p.rows + t.n0;
+    t.row[1] = t.row[0] + 16;
   } else {
-    const int per = p.I / 8;
+    const int per = p.I / 16;
     t.a = u / per;
-    t.row[0] = static_cast<size_t>(s.expert[t.a]) * p.rows + (u - t.a * per) * 8;
+    t.n0 = (u - t.a * per) * 16;
+    t.mat = 2 * s.expert[t.a];
+    t.row[0] = static_cast<size_t>(s.expert[t.a]) * p.rows + t.n0;
     t.row[1] = t.row[0] + p.I;
   }
   return t;
 }
 
-// Scale of row r, block b of the unit's scales in shared memory.
-template <int kFmt>
-W4_DEV uint32_t scale_f16x2(const uint8_t* row, int b) {
-  const uint32_t s8 = row[b];
-  return e4m3x2_to_f16x2(s8 * 0x0101u);
-}
-template <int kFmt>
-W4_DEV float scale_f32(const uint8_t* row, int b) {
-  if constexpr (kFmt == W4_FMT_INT4) {
-    return half_bits_to_f32(reinterpret_cast<const uint16_t*>(row)[b]);
-  } else {
-    const uint32_t s8 = row[b];
-    return __uint_as_float(s8 == 0 ? 1u << 22 : s8 == 255 ? 0x7FC00000u : s8 << 23);
-  }
-}
+W4_DEV uint32_t e4m3_f16x2(uint32_t s8) { return e4m3x2_to_f16x2(s8 * 0x0101u); }   // twice
+W4_DEV float e8m0_f32(uint32_t s8) { return __uint_as_float(s8 << 23); }               // 0 for 2^-127, infinite for NaN
+W4_DEV float scale_int4(const uint8_t* row, int grp) { return half_bits_to_f32(reinterpret_cast<const uint16_t*>(row)[grp]); }
 
-// Adds this warp's steps [s0, s1) (of the whole row; the slot starts at step c0) to y: rows
-// lane / 4 and lane / 4 + 8 of the slot times the columns that b(step) gives. b: the lane's
-// 8 activations of step `step` (columns 32 step + 8 (lane % 4) ..) of token lane / 4.
-template <int kFmt, class B>
+// Where this lane's two MMA blocks find their rows: block m has rows r, r + 8 of the MMA from
+// rows at[m], at[m] + apart of the unit.
+template <bool kDown>
+struct RowsOf {
+  static constexpr int kApart = kDown ? 8 : 16;
+  W4_DEV static int first(int m) { return kDown ? 16 * m : 8 * m; }
+};
+
+// Adds this warp's steps [s0, s1), at most kPer, to y[block]; the slot starts at step c0. b(i)
+// are the lane's 8 activations of step s0 + i (columns 8 (lane % 4) ..) of token lane / 4.
+template <int kFmt, bool kDown, class B>
 W4_DEV void multiply(const Params& p, const uint8_t* slot, const uint8_t* scales, int c0, int s0, int s1, B b,
-                     float (&y)[4]) {
+                     float (&y)[2][4]) {
+  using R = RowsOf<kDown>;
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const uint8_t* w0 = slot + g * kRowPitch + 4 * c - c0 * 16;
-  const uint8_t* sc0 = scales + g * p.scale_pitch;
-  const uint8_t* sc1 = sc0 + 8 * p.scale_pitch;
-  auto step = [&](int s, float (&d)[4]) {
-    const uint32_t wa = *reinterpret_cast<const uint32_t*>(w0 + s * 16);
-    const uint32_t wb = *reinterpret_cast<const uint32_t*>(w0 + 8 * kRowPitch + s * 16);
-    uint32_t fa = 0, fb = 0;
-    if constexpr (kFmt == W4_FMT_NVFP4) {
-      fa = scale_f16x2<kFmt>(sc0, 2 * s + (c >> 1));
-      fb = scale_f16x2<kFmt>(sc1, 2 * s + (c >> 1));
+  const uint8_t* w0 = slot + g * 128 + 4 * c;
+  const uint32_t swz = static_cast<uint32_t>(g) << 4;
+  const uint8_t* sc[2][2];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) sc[m][h] = scales + (R::first(m) + h * R::kApart + g) * p.scale_pitch;
+  // one step: weights to operand registers, two products a block
+  auto step = [&](int s, const uint4& v, const uint32_t (&f)[2][2], float (&d)[2][4]) {
+    const uint8_t* w = w0 + ((s - c0) >> 3) * kBox + (((static_cast<uint32_t>(s) & 7u) << 4) ^ swz);
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      uint32_t ra[4], rb[4];
+      widen<kFmt>(*reinterpret_cast<const uint32_t*>(w + R::first(m) * 128), f[m][0], ra);
+      widen<kFmt>(*reinterpret_cast<const uint32_t*>(w + (R::first(m) + R::kApart) * 128), f[m][1], rb);
+      mma16816(d[m], ra[0], rb[0], ra[1], rb[1], v.x, v.y);
+      mma16816(d[m], ra[2], rb[2], ra[3], rb[3], v.z, v.w);
     }
-    uint32_t ra[4], rb[4];
-    widen<kFmt>(wa, fa, ra);
-    widen<kFmt>(wb, fb, rb);
-    const uint4 v = b(s);
-    mma16816(d, ra[0], rb[0], ra[1], rb[1], v.x, v.y);
-    mma16816(d, ra[2], rb[2], ra[3], rb[3], v.z, v.w);
+  };
+  auto add = [&](const float (&f)[2][2], const float (&d)[2][4]) {
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      y[m][0] = fmaf(f[m][0], d[m][0], y[m][0]), y[m][1] = fmaf(f[m][0], d[m][1], y[m][1]);
+      y[m][2] = fmaf(f[m][1], d[m][2], y[m][2]), y[m][3] = fmaf(f[m][1], d[m][3], y[m][3]);
+    }
   };
   if constexpr (kFmt == W4_FMT_NVFP4) {
-#pragma unroll 4
-    for (int s = s0; s < s1; ++s) step(s, y);
+    if (s1 - s0 == kPer && (s0 & 1) == 0) {   // scales of two steps are a word (a row's are multiples of 4 bytes)
+#pragma unroll
+      for (int i = 0; i < kPer; i += 2) {
+        uint32_t word[2][2];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) word[m][h] = reinterpret_cast<const uint32_t*>(sc[m][h])[(s0 + i) >> 1];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          uint32_t f[2][2];
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) f[m][h] = e4m3x2_to_f16x2(prmt(word[m][h], 0, (c >> 1) * 0x11 + j * 0x22 + 0x4400));
+          step(s0 + i + j, b(i + j), f, y);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        if (s0 + i >= s1) break;
+        uint32_t f[2][2];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) f[m][h] = e4m3_f16x2(sc[m][h][2 * (s0 + i) + (c >> 1)]);
+        step(s0 + i, b(i), f, y);
+      }
+    }
   } else if constexpr (kFmt == W4_FMT_MXFP4) {
-#pragma unroll 4
-    for (int s = s0; s < s1; ++s) {
-      float d[4] = {0.f, 0.f, 0.f, 0.f};
-      step(s, d);
-      const float fa = scale_f32<kFmt>(sc0, s), fb = scale_f32<kFmt>(sc1, s);
-      y[0] = fmaf(fa, d[0], y[0]), y[1] = fmaf(fa, d[1], y[1]);
-      y[2] = fmaf(fb, d[2], y[2]), y[3] = fmaf(fb, d[3], y[3]);
+    const uint32_t none[2][2] = {};
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (s0 + i >= s1) break;
+      float d[2][4] = {}, f[2][2];
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) f[m][h] = e8m0_f32(sc[m][h][s0 + i]);
+      step(s0 + i, b(i), none, d);
+      add(f, d);
     }
   } else {
-    int grp = s0 / p.group_steps;
-    for (int s = s0; s < s1; ++grp) {
-      const int end = min(s1, (grp + 1) * p.group_steps);
-      const float fa = scale_f32<kFmt>(sc0, grp), fb = scale_f32<kFmt>(sc1, grp);
-      float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-      for (; s < end; ++s) step(s, d);
-      y[0] = fmaf(fa, d[0], y[0]), y[1] = fmaf(fa, d[1], y[1]);
-      y[2] = fmaf(fb, d[2], y[2]), y[3] = fmaf(fb, d[3], y[3]);
+    const uint32_t none[2][2] = {};
+    int grp = s0 / p.group_steps, left = (grp + 1) * p.group_steps - s0;
+    float d[2][4] = {};
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (s0 + i >= s1) break;
+      step(s0 + i, b(i), none, d);
+      if (--left == 0 || s0 + i + 1 == s1) {   // the end of a scale's columns, or of this warp's
+        float f[2][2];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) f[m][h] = scale_int4(sc[m][h], grp);
+        add(f, d);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[j >> 2][j & 3] = 0.f;
+        ++grp;
+        left = p.group_steps;
+      }
     }
   }
 }
@@ -298,20 +349,21 @@ W4_DEV void multiply(const Params& p, const uint8_t* slot, const uint8_t* scales
 // of row pieces and of scales, and up: x in fp16, down: each group's outputs.
 struct Common {
   Routed r;
-  alignas(16) float red[kGroups][2][kGroupWarps][2][32][4];   // [group][alternating][warp][8 tokens][lane]
-  uint64_t full[kGroups][kMoeDecodeSlots], empty[kGroups][kMoeDecodeSlots];
+  alignas(16) float red[kGroups][kGroupWarps][2][32][4];   // [group][warp][block][lane]
+  uint64_t full[kGroups][kMoeDecodeSlots];
+  unsigned int done[kGroups][kMoeDecodeSlots];   // warps that are done with a slot, ever
   int abort_flag;
 };
 
 template <int kFmt, bool kDown>
 __global__ void __launch_bounds__(kThreads, 1) moe_decode_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_dyn[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 127) & ~uintptr_t(127));
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
   Common& c = *reinterpret_cast<Common*>(smem);
   Routed& r = c.r;
-  uint8_t* ring = smem + (sizeof(Common) + 127) / 128 * 128;
+  uint8_t* ring = smem + (sizeof(Common) + 1023) / 1024 * 1024;
   uint8_t* scale_ring = ring + kGroups * p.slots * kSlot;
-  const int scale_slot = 16 * p.scale_pitch;
+  const int scale_slot = kRows * p.scale_pitch;
   uint8_t* rest = scale_ring + kGroups * p.scale_slots * scale_slot;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int T = static_cast<int>(p.route.T);
@@ -320,8 +372,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_decode_kernel(const __grid_co
   if (threadIdx.x == 0) {
     for (int g = 0; g < kGroups; ++g)
       for (int i = 0; i < p.slots; ++i) {
-        mbar_init(&c.full[g][i], 1);
-        mbar_init(&c.empty[g][i], kGroupWarps);
+        mbar_init(&c.full[g][i], 1 + 32);   // the weights; every lane's copies of scales
+        c.done[g][i] = 0;
       }
     c.abort_flag = 0;
     fence_mbar_init();
@@ -338,56 +390,56 @@ __global__ void __launch_bounds__(kThreads, 1) moe_decode_kernel(const __grid_co
     }
   });
 
-  // units of this CTA: up, a share of all (expert, eight columns) in order; down, every split-th expert
+  // units of this CTA: up, a share of all (expert, 16 columns) in order; down, every split-th expert
   const int rank = kDown && p.split > 1 ? static_cast<int>(cluster_rank()) : 0;
   int u0, u1, stride;
   if constexpr (kDown) {
     u0 = rank, u1 = r.n, stride = p.split;
   } else {
-    const long long all = static_cast<long long>(r.n) * (p.I / 8);
+    const long long all = static_cast<long long>(r.n) * (p.I / 16);
     u0 = static_cast<int>(all * blockIdx.x / gridDim.x);
     u1 = static_cast<int>(all * (blockIdx.x + 1) / gridDim.x);
     stride = 1;
   }
   const int steps = p.K / 32;
 
-  if (warp == kCompute / 32) {
-    // copies: a lane to a row; round by round, every group's unit
-    int count = 0, round = 0;
-    bool ok = true;
-    tc::fence_proxy_async_smem();   // the ring held the routing's scratch
-    for (int ub = u0; ok && ub < u1; ub += kGroups * stride, ++round)
-      for (int ch = 0; ok && ch < p.chunks; ++ch, ++count) {
-        const int slot = count % p.slots, ph = (count / p.slots & 1) ^ 1;
-        for (int g = 0; g < kGroups; ++g) {
-          const int u = ub + g * stride;
-          if (u >= u1) break;
-          if (!(ok = wait_warp(&c.empty[g][slot], ph, abort_flag, p.status))) break;
-          const Unit t = unit_of<kDown>(p, r, u);
-          const int s0 = ch * kChunkSteps, bytes = min(kChunkSteps, steps - s0) * 16;
-          const int blk = lane >> 3 & 1, i = lane & 7;
-          uint64_t* bar = &c.full[g][slot];
-          if (lane == 0) mbar_arrive_expect_tx(bar, 16 * bytes + (ch == 0 ? 16 * p.scale_row : 0));
-          __syncwarp();
-          if (lane < 16)
-            tc::bulk_load(ring + (g * p.slots + slot) * kSlot + lane * kRowPitch,
-                          p.w + (t.row[blk] + i) * (p.K / 2) + s0 * 16, bytes, bar);
-          if (ch == 0) {
-            uint8_t* to = scale_ring + (g * p.scale_slots + round % p.scale_slots) * scale_slot;
-            if (p.scale_pitch != p.scale_row) {
-              if (lane < 16) tc::bulk_load(to + lane * p.scale_pitch, p.w_scale + (t.row[blk] + i) * p.scale_row, p.scale_row, bar);
-            } else if (lane < 2) {
-              tc::bulk_load(to + lane * 8 * p.scale_pitch, p.w_scale + t.row[lane] * p.scale_row, 8 * p.scale_row, bar);
-            }
-          }
-        }
-      }
-  } else {
+  {
     const int group = warp / kGroupWarps, w = warp % kGroupWarps, tid = threadIdx.x % kGroupThreads;
     const int g = lane >> 2, q = lane & 3;
-    float* out = reinterpret_cast<float*>(rest) + group * T * 16;   // down: [T][16]
+    // A whole warp: starts the copies of the group's piece number `count`, its unit's scales
+    // with the first piece of the unit.
+    auto fill = [&](int count) {
+      const int round = count / p.chunks, ch = count - round * p.chunks;
+      const int u = u0 + (group + kGroups * round) * stride;
+      if (u >= u1) return;
+      const Unit t = unit_of<kDown>(p, r, u);
+      const int slot = count % p.slots, s0 = ch * kChunkSteps, boxes = (min(kChunkSteps, steps - s0) + 7) / 8;
+      uint64_t* bar = &c.full[group][slot];
+      if (elect_one()) {
+        mbar_arrive_expect_tx(bar, boxes * kBox);
+        for (int i = 0; i < boxes; ++i)
+          tc::tma_load_3d(ring + (group * p.slots + slot) * kSlot + i * kBox, &p.tm_w, bar, (s0 + 8 * i) * 16, t.n0, t.mat);
+      }
+      __syncwarp();
+      if (ch == 0) {
+        // two blocks of 16 rows, 16 bytes at a time; rows of whole 16 bytes go to their pitch
+        const uint32_t to = smem_addr(scale_ring + (group * p.scale_slots + round % p.scale_slots) * scale_slot);
+        const bool pitched = p.scale_pitch != p.scale_row;
+        const int per = p.scale_row / 16;
+        for (int i = lane; i < 2 * p.scale_row; i += 32) {   // 16 rows are scale_row pieces of 16 bytes
+          const int blk = i >= p.scale_row, j = i - blk * p.scale_row;
+          const int row = pitched ? j / per : 0;
+          tc::copy16_async(to + blk * 16 * p.scale_pitch + (pitched ? row * (p.scale_pitch - p.scale_row) : 0) + j * 16,
+                           p.w_scale + t.row[blk] * p.scale_row + j * 16);
+        }
+      }
+      tc::copy_async_arrive(bar);
+    };
+    tc::fence_proxy_async_smem();   // the ring held the routing's scratch
+    if (w < p.slots) fill(w);
+    float* out = reinterpret_cast<float*>(rest) + group * T * kRows;   // down: [T][32]
     if constexpr (kDown) {
-      for (int i = tid; i < T * 16; i += kGroupThreads) out[i] = 0.f;
+      for (int i = tid; i < T * kRows; i += kGroupThreads) out[i] = 0.f;
       grid_dependency_wait();   // the activations, and y may still be read
     }
     int count = 0, round = 0;
@@ -396,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_decode_kernel(const __grid_co
       const Unit t = unit_of<kDown>(p, r, u);
       const int first = r.first[t.a], tokens = r.first[t.a + 1] - first;
       const uint8_t* scales = scale_ring + (group * p.scale_slots + round % p.scale_slots) * scale_slot;
-      float y[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      float y[2][2][4] = {};   // [eight tokens][block]
       for (int ch = 0; ch < p.chunks; ++ch, ++count) {
         const int slot = count % p.slots;
         const int c0 = ch * kChunkSteps, n = min(kChunkSteps, steps - c0);
@@ -409,7 +461,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_decode_kernel(const __grid_co
           if (8 * nb >= tokens) break;
           const int row = first + min(8 * nb + g, tokens - 1);   // columns past the last token repeat it
           if constexpr (kDown) {
-            constexpr int kPer = kChunkSteps / kGroupWarps;
             const uint16_t* ar = p.act + static_cast<size_t>(row) * p.K + 8 * q;
             const uint8_t* er = p.act_exp + static_cast<size_t>(row) * (p.K / 8) + q;
             uint4 v[kPer];
@@ -436,50 +487,59 @@ __global__ void __launch_bounds__(kThreads, 1) moe_decode_kernel(const __grid_co
                 asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(v[i].z) : "r"(h));
                 asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(v[i].w) : "r"(h));
               }
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-              if (s0 + i < s1) multiply<kFmt>(p, piece, scales, c0, s0 + i, s0 + i + 1, [&](int) { return v[i]; }, d);
+            float d[2][4] = {};
+            multiply<kFmt, kDown>(p, piece, scales, c0, s0, s1, [&](int i) { return v[i]; }, d);
             // a factor 2^(top - 127 - 14) for this lane's two columns
             const int t0 = __shfl_sync(kFull, top, 8 * q), t1 = __shfl_sync(kFull, top, 8 * q + 4);
             const float f0 = ldexpf(1.f, t0 - 141), f1 = ldexpf(1.f, t1 - 141);
-            y[nb][0] = fmaf(d[0], f0, y[nb][0]), y[nb][1] = fmaf(d[1], f1, y[nb][1]);
-            y[nb][2] = fmaf(d[2], f0, y[nb][2]), y[nb][3] = fmaf(d[3], f1, y[nb][3]);
-          } else {
-            const uint8_t* xr = rest + r.token[row] * x_pitch + 16 * q;
-            multiply<kFmt>(p, piece, scales, c0, s0, s1,
-                           [&](int s) { return *reinterpret_cast<const uint4*>(xr + 64 * s); }, y[nb]);
-          }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c.empty[group][slot]);
-      }
-      float (*red)[2][32][4] = c.red[group][round & 1];
 #pragma unroll
-      for (int nb = 0; nb < 2; ++nb)
-        if (8 * nb < tokens) *reinterpret_cast<float4*>(red[w][nb][lane]) = make_float4(y[nb][0], y[nb][1], y[nb][2], y[nb][3]);
-      group_sync(group);
-      const float gl = p.w_global != nullptr ? __ldcg(p.w_global + r.expert[t.a]) : 1.f;
-      if constexpr (kDown) {
-        for (int nb = 0; 8 * nb < tokens; ++nb) {
-          const int o = tid & 15, n = 8 * nb + (tid >> 4);
-          if (n < tokens) {
-            const int l = (o & 7) * 4 + (n & 7) / 2, j = (o >> 3) * 2 + (n & 1);
-            const float v = ((red[0][nb][l][j] + red[1][nb][l][j]) + red[2][nb][l][j]) + red[3][nb][l][j];
-            float& at = out[r.token[first + n] * 16 + o];
-            at = fmaf(v, gl * r.weight[first + n], at);
+            for (int m = 0; m < 2; ++m) {
+              y[nb][m][0] = fmaf(d[m][0], f0, y[nb][m][0]), y[nb][m][1] = fmaf(d[m][1], f1, y[nb][m][1]);
+              y[nb][m][2] = fmaf(d[m][2], f0, y[nb][m][2]), y[nb][m][3] = fmaf(d[m][3], f1, y[nb][m][3]);
+            }
+          } else {
+            const uint8_t* xr = rest + r.token[row] * x_pitch + 64 * s0 + 16 * q;
+            multiply<kFmt, kDown>(p, piece, scales, c0, s0, s1,
+                           [&](int i) { return *reinterpret_cast<const uint4*>(xr + 64 * i); }, y[nb]);
           }
         }
-      } else {
-        // thread: column tid % 8 of the unit, token tid / 8
-        const int i = tid & 7, n = tid >> 3, nb = n >> 3;
-        if (8 * (tid >> 6) < tokens) {   // whole warps: 64 threads for eight tokens
-          const int m = min(n, tokens - 1), l = i * 4 + (m & 7) / 2, j = m & 1, mb = m >> 3;
-          float gate = ((red[0][mb][l][j] + red[1][mb][l][j]) + red[2][mb][l][j]) + red[3][mb][l][j];
-          float up = ((red[0][mb][l][2 + j] + red[1][mb][l][2 + j]) + red[2][mb][l][2 + j]) + red[3][mb][l][2 + j];
-          const int e = r.x_exp[r.token[first + m]];
-          gate = ldexpf(gate, e) * gl;
-          up = ldexpf(up, e) * gl;
+        // the last of the four warps to be done with the piece starts the copy of the next one into its place
+        __syncwarp();
+        int before = 0;
+        if (lane == 0) {
+          __threadfence_block();
+          before = atomicAdd(&c.done[group][slot], 1);
+          __threadfence_block();
+        }
+        if ((__shfl_sync(kFull, before, 0) & (kGroupWarps - 1)) == kGroupWarps - 1) fill(count + p.slots);
+      }
+      const float gl = p.w_global != nullptr ? __ldcg(p.w_global + r.expert[t.a]) : 1.f;
+#pragma unroll
+      for (int nb = 0; nb < 2; ++nb) {
+        if (8 * nb >= tokens) break;
+        float (*red)[2][32][4] = c.red[group];
+        if (round > 0 || nb > 0) group_sync(group);   // the sums before have been read
+#pragma unroll
+        for (int m = 0; m < 2; ++m) *reinterpret_cast<float4*>(red[w][m][lane]) = make_float4(y[nb][m][0], y[nb][m][1], y[nb][m][2], y[nb][m][3]);
+        group_sync(group);
+        auto sum = [&](int m, int l, int j) { return ((red[0][m][l][j] + red[1][m][l][j]) + red[2][m][l][j]) + red[3][m][l][j]; };
+        if constexpr (kDown) {
+          const int o = tid & 31;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int n = 8 * nb + 4 * k + (tid >> 5);
+            if (n < tokens) {
+              const float v = sum(o >> 4, (o & 7) * 4 + (n & 7) / 2, (o >> 3 & 1) * 2 + (n & 1));
+              float& at = out[r.token[first + n] * kRows + o];
+              at = fmaf(v, gl * r.weight[first + n], at);
+            }
+          }
+        } else {
+          // thread: column tid % 16 of the unit, token tid / 16
+          const int i = tid & 15, n = 8 * nb + (tid >> 4);
+          const int k = min(n, tokens - 1), l = (i & 7) * 4 + (k & 7) / 2, j = k & 1;
+          const int e = r.x_exp[r.token[first + k]];
+          const float gate = ldexpf(sum(i >> 3, l, j), e) * gl, up = ldexpf(sum(i >> 3, l, 2 + j), e) * gl;
           const float a = __fdiv_rn(gate, 1.f + expf(-gate)) * up;
           uint32_t bits = __float_as_uint(a) & 0x7FFFFFFFu;
           bits = max(bits, __shfl_xor_sync(kFull, bits, 1));
@@ -487,14 +547,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_decode_kernel(const __grid_co
           bits = max(bits, __shfl_xor_sync(kFull, bits, 4));
           const uint32_t ex = max(bits >> 23, 14u);   // a 2^(14 - (ex - 127)): the largest in [2^14, 2^15)
           if (n < tokens) {
-            const int i0 = static_cast<int>(t.row[0] - static_cast<size_t>(r.expert[t.a]) * p.rows);
             uint16_t h;
             asm("cvt.rn.f16.f32 %0, %1;" : "=h"(h) : "f"(a * __uint_as_float((268u - ex) << 23)));
-            p.act[static_cast<size_t>(first + n) * p.I + i0 + chunk_place<kFmt>(i)] = h;
-            if (i == 0) p.act_exp[static_cast<size_t>(first + n) * (p.I / 8) + i0 / 8] = static_cast<uint8_t>(ex);
+            p.act[static_cast<size_t>(first + n) * p.I + t.n0 + (i & 8) + chunk_place<kFmt>(i & 7)] = h;
+            if ((i & 7) == 0) p.act_exp[static_cast<size_t>(first + n) * (p.I / 8) + (t.n0 + i) / 8] = static_cast<uint8_t>(ex);
           }
         }
-        (void)nb;
       }
     }
   }
@@ -503,9 +561,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_decode_kernel(const __grid_co
     __syncthreads();
     // the groups' outputs in order, then (split) the CTAs' of the cluster
     float* sum = reinterpret_cast<float*>(rest);
-    for (int i = threadIdx.x; i < T * 16; i += kThreads) {
+    for (int i = threadIdx.x; i < T * kRows; i += kThreads) {
       float v = sum[i];
-      for (int g = 1; g < kGroups; ++g) v += sum[g * T * 16 + i];
+      for (int g = 1; g < kGroups; ++g) v += sum[g * T * kRows + i];
       sum[i] = v;
     }
     if (p.split > 1) {
@@ -514,15 +572,15 @@ __global__ void __launch_bounds__(kThreads, 1) moe_decode_kernel(const __grid_co
     } else {
       __syncthreads();
     }
-    const int n0 = static_cast<int>(blockIdx.x) / p.split * 16;
+    const int n0 = static_cast<int>(blockIdx.x) / p.split * kRows;
     const int i = threadIdx.x * 4;
-    if (rank == 0 && i < T * 16) {
+    if (rank == 0 && i < T * kRows) {
       float4 v = *reinterpret_cast<const float4*>(sum + i);
       for (int k = 1; k < p.split; ++k) {
         const float4 o = ld_cluster_f32x4(smem_addr(sum + i), k);
         v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
       }
-      *reinterpret_cast<uint2*>(p.y + static_cast<size_t>(i / 16) * p.H + n0 + i % 16) =
+      *reinterpret_cast<uint2*>(p.y + static_cast<size_t>(i / kRows) * p.H + n0 + i % kRows) =
           make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
     }
     if (p.split > 1) {
@@ -549,7 +607,8 @@ cudaError_t run(const MoeDecodeArgs& a, cudaStream_t s) {
   Params p = {};
   p.route = a.route;
   const int T = static_cast<int>(a.route.T);
-  p.w = static_cast<const uint8_t*>(kDown ? a.down : a.gate_up);
+  cudaError_t e = kDown ? encode(&p.tm_w, a.down, a.I / 2, a.H, a.route.E, kRows) : encode(&p.tm_w, a.gate_up, a.H / 2, a.I, 2 * a.route.E, kRows / 2, 2);
+  if (e != cudaSuccess) return e;
   p.w_scale = static_cast<const uint8_t*>(kDown ? a.down_scale : a.gate_up_scale);
   p.w_global = kDown ? a.down_global : a.gate_up_global;
   p.x = static_cast<const uint16_t*>(a.x);
@@ -566,19 +625,19 @@ cudaError_t run(const MoeDecodeArgs& a, cudaStream_t s) {
   p.scale_pitch = p.scale_row % 16 != 0 ? p.scale_row : p.scale_row % 32 == 0 ? p.scale_row + 16 : p.scale_row + 32;
   p.chunks = (p.K / 32 + kChunkSteps - 1) / kChunkSteps;
   p.status = a.status;
-  const int rest = kDown ? kGroups * T * 64 : T * (2 * p.H + 64);
-  const int base = 128 + (static_cast<int>(sizeof(Common)) + 127) / 128 * 128 + rest;
+  const int rest = kDown ? kGroups * T * kRows * 4 : T * (2 * p.H + 64);
+  const int base = 1024 + (static_cast<int>(sizeof(Common)) + 1023) / 1024 * 1024 + rest;
   int smem = 0;
   for (p.slots = kMoeDecodeSlots; p.slots >= 2; --p.slots) {
     p.scale_slots = (p.slots + p.chunks - 1) / p.chunks + 1;
-    smem = base + kGroups * (p.slots * kSlot + p.scale_slots * 16 * p.scale_pitch);
+    smem = base + kGroups * (p.slots * kSlot + p.scale_slots * kRows * p.scale_pitch);
     if (smem <= 232448) break;
   }
   if (p.slots < 2) return cudaErrorInvalidConfiguration;   // refused before (moe_decode_fits)
   p.split = 1;
   int64_t grid = current_sm_count();
   if (kDown) {
-    const int64_t slices = p.H / 16;
+    const int64_t slices = p.H / kRows;
     for (int n = kMaxSplit; n > 1 && p.split == 1; n /= 2)
       if (slices * n <= grid && n <= a.route.k * T) p.split = n;
     grid = slices * p.split;
@@ -596,12 +655,12 @@ cudaError_t run_both(const MoeDecodeArgs& a, cudaStream_t s) {
 
 // Two ring slots a group beside the activations, for either kernel.
 bool moe_decode_fits(const MoeDecodeArgs& a) {
-  const int64_t common = 256 + static_cast<int64_t>(sizeof(Common));
+  const int64_t common = 1024 + (static_cast<int64_t>(sizeof(Common)) + 1023) / 1024 * 1024;
   for (bool down : {false, true}) {
     const int64_t K = down ? a.I : a.H;
     const int64_t chunks = (K / 32 + kChunkSteps - 1) / kChunkSteps;
-    const int64_t ring = kGroups * (2 * kSlot + ((2 + chunks - 1) / chunks + 1) * 16 * (static_cast<int64_t>(scale_row_bytes(a, down)) + 32));
-    const int64_t rest = down ? kGroups * a.route.T * 64 : a.route.T * (2 * a.H + 64);
+    const int64_t ring = kGroups * (2 * kSlot + ((2 + chunks - 1) / chunks + 1) * kRows * (static_cast<int64_t>(scale_row_bytes(a, down)) + 32));
+    const int64_t rest = down ? kGroups * a.route.T * kRows * 4 : a.route.T * (2 * a.H + 64);
     if (common + ring + rest > 232448) return false;
   }
   return true;

@@ -72,6 +72,13 @@ W4_DEV void tma_load_3d(void* smem_dst, const void* tmap, uint64_t* bar, int c0,
 W4_DEV void copy4_async(uint32_t smem_dst, const void* src, bool in) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" :: "r"(smem_dst), "l"(src), "r"(in ? 4 : 0) : "memory");
 }
+W4_DEV void copy16_async(uint32_t smem_dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(smem_dst), "l"(src) : "memory");
+}
+// Arrives on `bar`, which counts it, when this thread's copies so far have landed.
+W4_DEV void copy_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" :: "r"(smem_addr(bar)) : "memory");
+}
 W4_DEV void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kPending>
 W4_DEV void copy_async_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(kPending) : "memory"); }
