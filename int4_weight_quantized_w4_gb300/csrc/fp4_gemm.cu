@@ -10,18 +10,21 @@
 // all of k and the epilogue is a multiply-add and one rounding.
 //
 // Operands come by TMA, 256 columns (128 bytes a row) a stage. Scales are row-major in
-// memory, as checkpoints hold them; the MMA wants them in tensor memory with 128 rows'
-// words in four columns. Scale warps copy a row's words of a stage (16 bytes nvfp4, 8
-// mxfp4) asynchronously to their places in shared memory, and the MMA warp sends each
-// 512-byte atom on to tensor memory ahead of the MMAs that use it.
+// memory, as checkpoints hold them; the MMA wants them in tensor memory, 128 rows' 32-bit
+// words in four columns. They are copied 32 bytes a row at a time (two stages' nvfp4 scales,
+// four stages' mxfp4), a warp per 128 rows transposes a stage's words in registers, and the
+// MMA warp sends each 512-byte atom on to tensor memory ahead of the MMAs that use it.
 //
-// Two forms:
-//  * stream (few rows): weights on the MMA's 128 rows, NT tokens on its columns; dense
+// Three forms:
+//  * stream (few rows): weights on the MMA's 128 rows, X tokens on its columns; dense
 //    products share a tile's k among the CTAs of a cluster. Bound by the weight bytes.
-//  * tile (many rows): 128 tokens on the MMA's rows, 192 outputs on its columns, with
-//    two accumulators, so that the MMAs of a tile run while the one before leaves.
+//  * tile: 128 tokens on the MMA's rows, 192 outputs on its columns, with two
+//    accumulators, so that the MMAs of a tile run while the one before leaves.
+//  * pair (many rows): two CTAs share a tile of 256 tokens and 192 outputs (cta_group::2):
+//    each copies its 128 tokens and half of the weights. What an SM takes in is what
+//    bounds tiles of 4-bit operands, and a CTA of a pair takes in 33 KB a stage, one alone 45.
 //
-// Both are launched as programmatic dependents and let their own dependents go early: the
+// All are launched as programmatic dependents and let their own dependents go early: the
 // weights and their scales start while the kernels before finish, everything else waits.
 #include <cstring>
 
@@ -36,17 +39,22 @@ namespace {
 constexpr int kStageK = 256;                  // columns of a stage
 constexpr int kStageBytes = kStageK / 2;
 
+enum Form { kStream, kTile, kPair };
+
 struct Params {
   CUtensorMap tm_x;        // codes [rows, K/2 bytes]
   CUtensorMap tm_w;        // codes [E, N, K/2 bytes]
-  const uint8_t* x_scale;  // [rows, SB]
-  const uint8_t* w_scale;  // [E, N, SB]
+  CUtensorMap tm_xs;       // scales [rows, SB], [E, N, SB], where tma_scales
+  CUtensorMap tm_ws;
+  const uint8_t* x_scale;
+  const uint8_t* w_scale;
   const float* x_global;   // or null
   const float* w_global;   // [E], or null
   const uint16_t* bias;    // bf16 [N] or null
   uint16_t* y;             // bf16 [rows, N]
   const int32_t* offsets;  // [E + 1], or null (dense: one segment of all rows)
   int E, rows, N, K, SB, KS, n_tiles;   // SB: scale bytes a row, KS: stages over k
+  bool tma_scales;         // rows of scales are 16-byte aligned; else words are copied one by one
   int split;               // stream form, dense: parts of the stages, one per CTA of a cluster
   int items;
   unsigned int* status;
@@ -59,100 +67,107 @@ W4_DEV void seg_bounds(const Params& p, int e, int& a, int& b) {
   b = min(__ldcg(p.offsets + e + 1), p.rows);
 }
 
-// W: weight rows of a tile, X: tokens of a tile; the one on the MMA's rows is 128.
-template <int W, int X, bool kNv, bool kTile>
+// W: weight rows of a tile, X: tokens of a CTA's tile.
+template <int W, int X, bool kNv, Form kForm>
 struct Shape {
+  static constexpr bool PAIR = kForm == kPair;
   static constexpr int WORDS = kNv ? 4 : 2;                    // 32-bit scale words of a row's stage
-  static constexpr int N = kTile ? W : X;                      // MMA columns
-  static constexpr int ATOMS_W = (W + 127) / 128, ATOMS_X = (X + 127) / 128;
-  static constexpr int W_BYTES = W * kStageBytes, X_BYTES = X * kStageBytes;
-  static constexpr int SW_BYTES = ATOMS_W * WORDS * 512, SX_BYTES = ATOMS_X * WORDS * 512;
+  static constexpr int SUPER = 8 / WORDS;                      // stages of a row's 32 bytes of scales
+  static constexpr int N = kForm == kStream ? X : W;           // MMA columns
+  static constexpr int W_LOAD = PAIR ? W / 2 : W;              // weight rows that this CTA copies
+  static constexpr int AW = (W + 127) / 128, AX = (X + 127) / 128;   // atoms of 128 rows
+  static constexpr int W_BYTES = W_LOAD * kStageBytes, X_BYTES = X * kStageBytes;
   static constexpr int STAGE = W_BYTES + X_BYTES;
-  static constexpr int SSTAGE = SW_BYTES + SX_BYTES;
-  static constexpr int CTAS = kTile || X > 64 ? 1 : 2;         // resident per SM
-  static constexpr int STAGES = CTAS == 2 ? (X == 64 ? 3 : 4) : kTile ? 4 : 5;
-  static constexpr int AHEAD = STAGES - 2;                     // stages of scale copies in flight (reported before the ring is full)
+  static constexpr int SW_BYTES = AW * WORDS * 512, SSTAGE = SW_BYTES + AX * WORDS * 512;
+  static constexpr int RAW_W = 128 * AW * 32, RAW = RAW_W + (X + 31) / 32 * 32 * 32;   // scales as they are in memory
+  static constexpr int CTAS = kForm != kStream || X > 64 ? 1 : 2;   // resident per SM
+  static constexpr int STAGES = CTAS == 2 ? (X == 64 ? 3 : 4) : kForm == kTile ? 4 : 5;
+  static constexpr int RAWS = kForm == kTile || X == 32 ? 2 : 3;
   static constexpr int ACCS = 2;
-  static constexpr int S_COLS = 4 * WORDS * (ATOMS_W + ATOMS_X);   // tensor memory columns of a stage's scales
+  static constexpr int S_COLS = 4 * WORDS * (AW + AX);         // tensor memory columns of a stage's scales
   static constexpr int USED = ACCS * N + 2 * S_COLS;
   static constexpr int TMEM_COLS = USED <= 128 ? 128 : USED <= 256 ? 256 : 512;
-  // warps: 4 epilogue, the MMA issuer, then those that copy weights and their scales, then the activations'
-  static constexpr int WW = W / 32 > 4 ? 4 : W / 32, XW = X / 32 > 4 ? 4 : X < 32 ? 1 : X / 32;
-  static constexpr int THREADS = 32 * (5 + WW + XW);
-  static constexpr int OUT = kTile ? 4 * 2048 : 0;
-  static constexpr int SMEM = STAGES * (STAGE + SSTAGE) + OUT + 256 + (kMaxExperts + 1 + 16 + 3) / 4 * 16 + 1024;
+  static constexpr int THREADS = 32 * (7 + AW + AX);
+  static constexpr int OUT = kForm != kStream ? 4 * 2048 : 0;
+  static constexpr int BARS = 2 * STAGES + 2 * RAWS + 2 * ACCS;
+  static constexpr int SMEM = STAGES * (STAGE + SSTAGE) + RAWS * RAW + OUT + 256 + (kMaxExperts + 1 + 16 + 3) / 4 * 16 + 1024;
   static_assert(USED <= 512 && CTAS * TMEM_COLS <= 512, "tensor memory");
   static_assert(SMEM <= 232448 && CTAS * SMEM + CTAS * 1024 <= 233472, "shared memory");
-  static_assert((2 * STAGES + 2 * ACCS) * 8 + 8 <= 256, "barriers");
+  static_assert(BARS * 8 + 8 <= 256, "barriers");
   static_assert(STAGE % 1024 == 0 && W_BYTES % 1024 == 0, "swizzle atoms");
-  static_assert(kTile || X * 512 <= STAGES * STAGE, "part sums of a cluster fit the ring");
+  static_assert(kForm != kStream || X * 512 <= STAGES * STAGE, "part sums of a cluster fit the ring");
 };
 
-// Scale words of `ROWS` rows from row0 on (those below `valid` exist), stage ks, by warps
-// of which this one is number `w` of `kWarps`: word j of row r to atom j * ATOMS + r / 128,
-// at 16 (r % 32) + 4 (r / 32 % 4). Words past the row's end are zeros.
-template <int ROWS, int WORDS, int kWarps>
-W4_DEV void load_scales(uint32_t to, const uint8_t* src, int SB, int ks, int valid, int w) {
-  constexpr int ATOMS = (ROWS + 127) / 128;
-  const int lane = threadIdx.x & 31;
-  const int at = ks * WORDS * 4;
-#pragma unroll
-  for (int r0 = 0; r0 < ROWS; r0 += 32 * kWarps) {
-    const int r = r0 + 32 * w + lane;
-    if (r0 + 32 * kWarps <= ROWS || r < ROWS) {
-      const uint32_t d = to + (r >> 7) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4;
-      const bool in = r < valid;
-      const uint8_t* s = src + static_cast<size_t>(in ? r : 0) * SB + at;
-#pragma unroll
-      for (int j = 0; j < WORDS; ++j) {
-        const bool word = in && at + 4 * j < SB;
-        tc::copy4_async(d + j * ATOMS * 512, word ? s + 4 * j : src, word);
-      }
-    }
+// By all lanes: 32 bytes of scales of `rows` rows from byte `at` of the row on, those below
+// `valid` and SB; zeros elsewhere.
+W4_DEV void copy_scale_words(uint32_t to, const uint8_t* src, int SB, int at, int rows, int valid) {
+  for (int i = threadIdx.x & 31; i < rows * 8; i += 32) {
+    const int r = i >> 3, b = at + 4 * (i & 7);
+    const bool in = r < valid && b < SB;
+    tc::copy4_async(to + i * 4, in ? src + static_cast<size_t>(r) * SB + b : src, in);
   }
 }
 
-template <int W, int X, bool kNv, bool kTile>
-__global__ void __launch_bounds__(Shape<W, X, kNv, kTile>::THREADS, Shape<W, X, kNv, kTile>::CTAS)
+template <int W, int X, bool kNv, Form kForm>
+__global__ void __launch_bounds__(Shape<W, X, kNv, kForm>::THREADS, Shape<W, X, kNv, kForm>::CTAS)
 fp4_kernel(const __grid_constant__ Params p) {
-  using C = Shape<W, X, kNv, kTile>;
-  constexpr int kMma = 4, kW0 = 5, kX0 = 5 + C::WW;
+  using C = Shape<W, X, kNv, kForm>;
+  constexpr int kMma = 4, kLoadW = 5, kLoadX = 6, kTurn = 7;   // warps; 0 to 3: epilogue; kTurn ..: scales
+  constexpr bool P = C::PAIR;
+  constexpr int kRowsPer = P ? 2 * X : X;
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
   uint8_t* ring = smem;                               // per stage: weights, activations
   uint8_t* scales = ring + C::STAGES * C::STAGE;      // per stage: weights', activations'
-  uint4* out_base = reinterpret_cast<uint4*>(scales + C::STAGES * C::SSTAGE);
-  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(out_base) + C::OUT);
+  uint8_t* raw = scales + C::STAGES * C::SSTAGE;      // per slot: weights', activations'
+  uint4* out_base = reinterpret_cast<uint4*>(raw + C::RAWS * C::RAW);
+  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(out_base) + C::OUT);   // pair: the first CTA's
   uint64_t* empty = full + C::STAGES;
-  uint64_t* acc_full = empty + C::STAGES;
-  uint64_t* acc_empty = acc_full + C::ACCS;
+  uint64_t* raw_full = empty + C::STAGES;
+  uint64_t* raw_empty = raw_full + C::RAWS;
+  uint64_t* acc_full = raw_empty + C::RAWS;
+  uint64_t* acc_empty = acc_full + C::ACCS;                                                      // pair: the first CTA's
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(acc_empty + C::ACCS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int32_t* starts = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(full) + 256);
   int32_t* warp_sum = starts + kMaxExperts + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = P ? cluster_rank() : 0;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
-      mbar_init(&full[i], 2 + C::WW + C::XW);   // two copies by TMA, the scale warps
+      mbar_init(&full[i], (2 + C::AW + C::AX) * (P ? 2 : 1));   // a CTA's two operands, its scale warps
       mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < C::RAWS; ++i) {
+      mbar_init(&raw_full[i], p.tma_scales ? 2 : 64);
+      mbar_init(&raw_empty[i], C::AW + C::AX);
     }
     for (int i = 0; i < C::ACCS; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 4);
+      mbar_init(&acc_empty[i], P ? 8 : 4);
     }
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kMma) tc::tmem_alloc(tmem_holder, C::TMEM_COLS);
-  if (warp == kW0 && lane == 0) tc::prefetch_tmap(&p.tm_w);
-  if (warp == kX0 && lane == 0) tc::prefetch_tmap(&p.tm_x);
+  if (warp == kMma) {
+    if constexpr (P)
+      tc::tmem_alloc_pair(tmem_holder, C::TMEM_COLS);
+    else
+      tc::tmem_alloc(tmem_holder, C::TMEM_COLS);
+  }
+  if (warp == kLoadW && lane == 0) tc::prefetch_tmap(&p.tm_w);
+  if (warp == kLoadX && lane == 0) tc::prefetch_tmap(&p.tm_x);
   if (p.offsets != nullptr) {
     grid_dependency_wait();   // the routing may be running still
-    tile_starts<C::THREADS>(p, X, starts, warp_sum);
+    tile_starts<C::THREADS>(p, kRowsPer, starts, warp_sum);
   }
   tc::fence_before_sync();
   __syncthreads();
+  if constexpr (P) {   // the other CTA's barriers are set up
+    cluster_arrive();
+    cluster_wait();
+  }
   tc::fence_after_sync();
   launch_dependents();
   const uint32_t tmem = *tmem_holder;
@@ -160,101 +175,166 @@ fp4_kernel(const __grid_constant__ Params p) {
   // this CTA's part of the stages (the same for every item)
   const int part = p.split > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int ks0 = p.KS * part / p.split, ks1 = p.KS * (part + 1) / p.split;
-  const int first = blockIdx.x / p.split, step = gridDim.x / p.split;
+  const int ctas = P ? 2 : p.split;   // of one item
+  const int first = blockIdx.x / ctas, step = gridDim.x / ctas;
 
-  if (warp >= kW0) {
-    // Copies of weights (kW0 ..) or activations (kX0 ..): a whole warp walks the ring, its
-    // lanes copy scales, lane 0 of the first warp the operand. A stage's scales are
-    // reported full AHEAD stages later, when their copies have landed.
-    const bool mine_w = warp < kX0;
-    const int w = mine_w ? warp - kW0 : warp - kX0;
-    int st = 0, ph = 1, e = 0, g = 0;
-    bool ok = true, waited = false;
+  if (warp == kLoadW || warp == kLoadX) {
+    // An operand and its scales, by lane 0; scales that TMA cannot copy by all lanes.
+    const bool is_w = warp == kLoadW;
+    int st = 0, ph = 1, rs = 0, rph = 1, e = 0;
+    bool ok = true, waited = !is_w;
     Tile t;
-    if (!mine_w) grid_dependency_wait();   // the codes come from the kernel before
-    auto landed = [&](int stage) {
-      tc::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&full[stage]);
-    };
-    for (int it = first; ok && it < p.items && decode(p, it, X, W, starts, t, e); it += step)
+    if (!is_w) grid_dependency_wait();   // the codes come from the kernel before
+    for (int it = first; ok && it < p.items && decode(p, it, kRowsPer, W, starts, t, e); it += step) {
+      const int row0 = t.row0 + static_cast<int>(rank) * X;
       for (int ks = ks0; ks < ks1; ++ks) {
-        if (mine_w && ph == 0 && !waited) {   // the ring is full, and is emptied only after the kernels before
+        if (!waited && (ph == 0 || rph == 0)) {   // a ring is full, and is emptied only after the kernels before
           grid_dependency_wait();
           waited = true;
         }
-        if (!(ok = wait_warp(&empty[st], ph, abort_flag, p.status))) break;
-        uint8_t* to = ring + st * C::STAGE;
-        const uint32_t sc = smem_addr(scales + st * C::SSTAGE);
-        if (mine_w) {
-          if (w == 0 && lane == 0) {
-            mbar_arrive_expect_tx(&full[st], C::W_BYTES);
-            tc::tma_load_3d(to, &p.tm_w, &full[st], ks * kStageBytes, t.n0, t.expert);
-          }
-          load_scales<W, C::WORDS, C::WW>(sc, p.w_scale + (static_cast<size_t>(t.expert) * p.N + t.n0) * p.SB, p.SB, ks,
-                                          p.N - t.n0, w);
-        } else {
-          if (w == 0 && lane == 0) {
-            mbar_arrive_expect_tx(&full[st], C::X_BYTES);
-            tc::tma_load_2d(to + C::W_BYTES, &p.tm_x, &full[st], ks * kStageBytes, t.row0);
-          }
-          load_scales<X, C::WORDS, C::XW>(sc + C::SW_BYTES, p.x_scale + static_cast<size_t>(t.row0) * p.SB, p.SB, ks,
-                                          t.row_end - t.row0, w);
-        }
-        tc::copy_async_commit();
-        if (g >= C::AHEAD) {
-          tc::copy_async_wait<C::AHEAD>();
-          landed(st >= C::AHEAD ? st - C::AHEAD : st - C::AHEAD + C::STAGES);
-        }
-        ++g;
-        if (++st == C::STAGES) st = 0, ph ^= 1;
-      }
-    tc::copy_async_wait<0>();
-    if (ok)
-      for (int i = g < C::AHEAD ? g : C::AHEAD; i > 0; --i) landed(st >= i ? st - i : st - i + C::STAGES);
-  } else if (warp == kMma) {
-    grid_dependency_wait();
-    constexpr uint32_t idesc = tc::idesc_fp4<kNv>(128, C::N);
-    const bool leader = elect_one();
-    const uint64_t wd0 = tc::sdesc_sw128(smem_addr(ring)), xd0 = wd0 + (C::W_BYTES >> 4);
-    const uint64_t sd0 = tc::sdesc_scales(smem_addr(scales));
-    int st = 0, ph = 0, ac = 0, aph = 1, e = 0, buf = 0;
-    bool ok = true;
-    Tile t;
-    for (int it = first; ok && it < p.items && decode(p, it, X, W, starts, t, e); it += step) {
-      if (!(ok = wait_warp(&acc_empty[ac], aph, abort_flag, p.status))) break;
-      for (int ks = ks0; ks < ks1; ++ks) {
-        if (!(ok = wait_warp(&full[st], ph, abort_flag, p.status))) break;
-        tc::fence_after_sync();
-        if (leader) {
-          // weights' scales, then the activations': [word][atom][4 columns] each
-          const uint32_t sw = tmem + C::ACCS * C::N + buf * C::S_COLS, sx = sw + 4 * C::WORDS * C::ATOMS_W;
-          const uint64_t sd = sd0 + static_cast<uint64_t>((st * C::SSTAGE) >> 4);
-#pragma unroll
-          for (int i = 0; i < C::WORDS * (C::ATOMS_W + C::ATOMS_X); ++i) tc::copy_scales(sw + 4 * i, sd + 32 * i);
-          const uint64_t wd = wd0 + static_cast<uint64_t>((st * C::STAGE) >> 4);
-          const uint64_t xd = xd0 + static_cast<uint64_t>((st * C::STAGE) >> 4);
-          const int left = p.K - ks * kStageK;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {   // 64 columns, 32 bytes, at a time
-            if (64 * j >= left) break;
-            const int word = kNv ? j : j >> 1;
-            const uint32_t id = idesc | (kNv || !(j & 1) ? 0u : (2u << 29) | (2u << 4));
-            const uint32_t fw = sw + 4 * C::ATOMS_W * word, fx = sx + 4 * C::ATOMS_X * word;
-            const uint32_t acc = ks > ks0 || j > 0 ? 1u : 0u;
-            if constexpr (kTile)
-              tc::mma_fp4<kNv>(tmem + ac * C::N, xd + 2 * j, wd + 2 * j, id, fx, fw, acc);
+        if (ks == ks0 || ks % C::SUPER == 0) {
+          if (!(ok = wait_warp(&raw_empty[rs], rph, abort_flag, p.status))) break;
+          uint8_t* to = raw + rs * C::RAW + (is_w ? 0 : C::RAW_W);
+          const int at = ks / C::SUPER * 32;
+          if (p.tma_scales) {
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&raw_full[rs], 32 * (is_w ? W : X));
+              if (is_w)
+                tc::tma_load_3d(to, &p.tm_ws, &raw_full[rs], at, t.n0, t.expert);
+              else
+                tc::tma_load_2d(to, &p.tm_xs, &raw_full[rs], at, row0);
+            }
+          } else {
+            if (is_w)
+              copy_scale_words(smem_addr(to), p.w_scale + (static_cast<size_t>(t.expert) * p.N + t.n0) * p.SB, p.SB, at, W, p.N - t.n0);
             else
-              tc::mma_fp4<kNv>(tmem + ac * C::N, wd + 2 * j, xd + 2 * j, id, fw, fx, acc);
+              copy_scale_words(smem_addr(to), p.x_scale + static_cast<size_t>(row0 < t.row_end ? row0 : t.row0) * p.SB, p.SB, at, X, t.row_end - row0);
+            tc::copy_async_arrive(&raw_full[rs]);
           }
-          tc::commit(&empty[st]);
-          if (ks == ks1 - 1) tc::commit(&acc_full[ac]);
+          if (++rs == C::RAWS) rs = 0, rph ^= 1;
+        }
+        if (!(ok = wait_warp(&empty[st], ph, abort_flag, p.status))) break;
+        if (lane == 0) {
+          uint8_t* to = ring + st * C::STAGE + (is_w ? 0 : C::W_BYTES);
+          if constexpr (P) {
+            const uint32_t bar = tc::cluster_addr(&full[st], 0);
+            tc::cluster_arrive_expect_tx(bar, is_w ? C::W_BYTES : C::X_BYTES);
+            if (is_w)
+              tc::tma_load_3d_pair(to, &p.tm_w, bar, ks * kStageBytes, t.n0 + static_cast<int>(rank) * C::W_LOAD, t.expert);
+            else
+              tc::tma_load_2d_pair(to, &p.tm_x, bar, ks * kStageBytes, row0);
+          } else {
+            mbar_arrive_expect_tx(&full[st], is_w ? C::W_BYTES : C::X_BYTES);
+            if (is_w)
+              tc::tma_load_3d(to, &p.tm_w, &full[st], ks * kStageBytes, t.n0, t.expert);
+            else
+              tc::tma_load_2d(to, &p.tm_x, &full[st], ks * kStageBytes, t.row0);
+          }
         }
         __syncwarp();
-        buf ^= 1;
         if (++st == C::STAGES) st = 0, ph ^= 1;
       }
-      if (++ac == C::ACCS) ac = 0, aph ^= 1;
+    }
+  } else if (warp >= kTurn) {
+    // Lane l holds the words of rows l, l + 32, l + 64 and l + 96 of this warp's 128.
+    const int a = warp - kTurn;
+    const bool is_w = a < C::AW;
+    constexpr int kBlocksX = X < 128 ? (X + 31) / 32 : 4;
+    const int blocks = is_w ? 4 : kBlocksX;
+    const uint8_t* from = raw + (is_w ? a * 4096 : C::RAW_W + (a - C::AW) * 4096) + lane * 32;
+    uint8_t* to = scales + (is_w ? a * 512 : C::SW_BYTES + (a - C::AW) * 512) + lane * 16;
+    const int pitch = (is_w ? C::AW : C::AX) * 512;   // from word to word
+    int st = 0, ph = 1, rs = 0, rph = 0, e = 0;
+    bool ok = true;
+    grid_dependency_wait();   // what it waits for depends on the kernels before
+    Tile t;
+    for (int it = first; ok && it < p.items && decode(p, it, kRowsPer, W, starts, t, e); it += step)
+      for (int ks = ks0; ks < ks1; ++ks) {
+        const int sub = ks % C::SUPER;
+        if (ks == ks0 || sub == 0) {
+          if (!(ok = wait_warp(&raw_full[rs], rph, abort_flag, p.status))) break;
+        }
+        uint32_t v[4][C::WORDS];
+        const uint8_t* f = from + rs * C::RAW + sub * C::WORDS * 4;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          if constexpr (kNv) {
+            const uint4 x = b < blocks ? *reinterpret_cast<const uint4*>(f + b * 1024) : make_uint4(0, 0, 0, 0);
+            v[b][0] = x.x, v[b][1] = x.y, v[b][2] = x.z, v[b][3] = x.w;
+          } else {
+            const uint2 x = b < blocks ? *reinterpret_cast<const uint2*>(f + b * 1024) : make_uint2(0, 0);
+            v[b][0] = x.x, v[b][1] = x.y;
+          }
+        }
+        if (ks == ks1 - 1 || sub == C::SUPER - 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&raw_empty[rs]);
+          if (++rs == C::RAWS) rs = 0, rph ^= 1;
+        }
+        if (!(ok = wait_warp(&empty[st], ph, abort_flag, p.status))) break;
+#pragma unroll
+        for (int j = 0; j < C::WORDS; ++j)
+          *reinterpret_cast<uint4*>(to + st * C::SSTAGE + j * pitch) = make_uint4(v[0][j], v[1][j], v[2][j], v[3][j]);
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (P)
+            tc::cluster_arrive_on(tc::cluster_addr(&full[st], 0));
+          else
+            mbar_arrive(&full[st]);
+        }
+        if (++st == C::STAGES) st = 0, ph ^= 1;
+      }
+  } else if (warp == kMma) {
+    grid_dependency_wait();
+    if (rank == 0) {
+      constexpr uint32_t idesc = tc::idesc_fp4<kNv>(P ? 256 : 128, C::N);
+      const bool leader = elect_one();
+      const uint64_t wd0 = tc::sdesc_sw128(smem_addr(ring)), xd0 = wd0 + (C::W_BYTES >> 4);
+      const uint64_t sd0 = tc::sdesc_scales(smem_addr(scales));
+      int st = 0, ph = 0, ac = 0, aph = 1, e = 0, buf = 0;
+      bool ok = true;
+      Tile t;
+      for (int it = first; ok && it < p.items && decode(p, it, kRowsPer, W, starts, t, e); it += step) {
+        if (!(ok = wait_warp(&acc_empty[ac], aph, abort_flag, p.status))) break;
+        for (int ks = ks0; ks < ks1; ++ks) {
+          if (!(ok = wait_warp(&full[st], ph, abort_flag, p.status))) break;
+          tc::fence_after_sync();
+          if (leader) {
+            // weights' scales, then the activations': [word][atom][4 columns] each
+            const uint32_t sw = tmem + C::ACCS * C::N + buf * C::S_COLS, sx = sw + 4 * C::WORDS * C::AW;
+            const uint64_t sd = sd0 + static_cast<uint64_t>((st * C::SSTAGE) >> 4);
+#pragma unroll
+            for (int i = 0; i < C::WORDS * (C::AW + C::AX); ++i) tc::copy_scales<P>(sw + 4 * i, sd + 32 * i);
+            const uint64_t wd = wd0 + static_cast<uint64_t>((st * C::STAGE) >> 4);
+            const uint64_t xd = xd0 + static_cast<uint64_t>((st * C::STAGE) >> 4);
+            const int left = p.K - ks * kStageK;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {   // 64 columns, 32 bytes, at a time
+              if (64 * j >= left) break;
+              const int word = kNv ? j : j >> 1;
+              const uint32_t id = idesc | (kNv || !(j & 1) ? 0u : (2u << 29) | (2u << 4));
+              const uint32_t fw = sw + 4 * C::AW * word, fx = sx + 4 * C::AX * word;
+              const uint32_t acc = ks > ks0 || j > 0 ? 1u : 0u;
+              if constexpr (kForm != kStream)
+                tc::mma_fp4<kNv, P>(tmem + ac * C::N, xd + 2 * j, wd + 2 * j, id, fx, fw, acc);
+              else
+                tc::mma_fp4<kNv, P>(tmem + ac * C::N, wd + 2 * j, xd + 2 * j, id, fw, fx, acc);
+            }
+            if constexpr (P) {
+              tc::commit_pair(&empty[st]);
+              if (ks == ks1 - 1) tc::commit_pair(&acc_full[ac]);
+            } else {
+              tc::commit(&empty[st]);
+              if (ks == ks1 - 1) tc::commit(&acc_full[ac]);
+            }
+          }
+          __syncwarp();
+          buf ^= 1;
+          if (++st == C::STAGES) st = 0, ph ^= 1;
+        }
+        if (++ac == C::ACCS) ac = 0, aph ^= 1;
+      }
     }
     __syncwarp();
   } else {
@@ -263,45 +343,50 @@ fp4_kernel(const __grid_constant__ Params p) {
     int ac = 0, aph = 0, e = 0;
     bool ok = true;
     Tile t;
-    for (int it = first; ok && it < p.items && decode(p, it, X, W, starts, t, e); it += step) {
+    auto hand_back = [&](int acc) {   // the accumulator is read
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (P)
+          tc::cluster_arrive_on(tc::cluster_addr(&acc_empty[acc], 0));
+        else
+          mbar_arrive(&acc_empty[acc]);
+      }
+    };
+    for (int it = first; ok && it < p.items && decode(p, it, kRowsPer, W, starts, t, e); it += step) {
       const float alpha = p.w_global != nullptr ? gx * __ldcg(p.w_global + t.expert) : gx;
       if (!(ok = wait_warp(&acc_full[ac], aph, abort_flag, p.status))) break;
       tc::fence_after_sync();
       const uint32_t ta = tmem + (static_cast<uint32_t>(32 * warp) << 16) + ac * C::N;
-      if constexpr (kTile) {
-        const int row0 = t.row0 + 32 * warp;
+      if constexpr (kForm != kStream) {
+        const int row0 = t.row0 + static_cast<int>(rank) * X + 32 * warp;
         uint4* buf = out_base + warp * 128;
         uint16_t* yp = p.y + static_cast<size_t>(row0) * p.N + t.n0;
 #pragma unroll 1
         for (int c0 = 0; c0 < C::N; c0 += 32) {
           uint32_t v[32];
           tc::tmem_ld32(ta + c0, v);
-          if (c0 + 32 == C::N) {
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_empty[ac]);
-          }
-          if (t.n0 + c0 < p.N) {
-            uint4 o[4];
+          if (c0 + 32 == C::N) hand_back(ac);
+          if (t.n0 + c0 >= p.N) continue;
+          uint4 o[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              float b[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-              if (p.bias != nullptr && t.n0 + c0 + 8 * c < p.N) {
-                const uint4 bb = *reinterpret_cast<const uint4*>(p.bias + t.n0 + c0 + 8 * c);
-                b[0] = bf16_lo(bb.x), b[1] = bf16_hi(bb.x), b[2] = bf16_lo(bb.y), b[3] = bf16_hi(bb.y);
-                b[4] = bf16_lo(bb.z), b[5] = bf16_hi(bb.z), b[6] = bf16_lo(bb.w), b[7] = bf16_hi(bb.w);
-              }
-              float f[8];
-#pragma unroll
-              for (int j = 0; j < 8; ++j) f[j] = fmaf(__uint_as_float(v[8 * c + j]), alpha, b[j]);
-              o[c] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                                pack_bf16x2(f[6], f[7]));
+          for (int c = 0; c < 4; ++c) {
+            float b[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (p.bias != nullptr && t.n0 + c0 + 8 * c < p.N) {
+              const uint4 bb = *reinterpret_cast<const uint4*>(p.bias + t.n0 + c0 + 8 * c);
+              b[0] = bf16_lo(bb.x), b[1] = bf16_hi(bb.x), b[2] = bf16_lo(bb.y), b[3] = bf16_hi(bb.y);
+              b[4] = bf16_lo(bb.z), b[5] = bf16_hi(bb.z), b[6] = bf16_lo(bb.w), b[7] = bf16_hi(bb.w);
             }
-            rows_out(buf, o, [&](int r, int c, const uint4& x) {
-              if (row0 + r < t.row_end && t.n0 + c0 + 8 * c < p.N)   // N is a multiple of 8
-                *reinterpret_cast<uint4*>(yp + static_cast<size_t>(r) * p.N + c0 + 8 * c) = x;
-            });
+            float f[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = fmaf(__uint_as_float(v[8 * c + j]), alpha, b[j]);
+            o[c] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                              pack_bf16x2(f[6], f[7]));
           }
+          rows_out(buf, o, [&](int r, int c, const uint4& x) {
+            if (row0 + r < t.row_end && t.n0 + c0 + 8 * c < p.N)   // N is a multiple of 8
+              *reinterpret_cast<uint4*>(yp + static_cast<size_t>(r) * p.N + c0 + 8 * c) = x;
+          });
         }
       } else {
         const int o = 32 * warp + lane, n = t.n0 + o, valid = t.row_end - t.row0;
@@ -323,16 +408,14 @@ fp4_kernel(const __grid_constant__ Params p) {
               yp[static_cast<size_t>(c0 + j) * p.N] = static_cast<uint16_t>(f32_to_bf16_bits(fmaf(__uint_as_float(v[j]), alpha, b)));
           }
         }
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&acc_empty[ac]);
+        hand_back(ac);
       }
       if (++ac == C::ACCS) ac = 0, aph ^= 1;
     }
   }
   __syncwarp();
 
-  if constexpr (!kTile) {
+  if constexpr (kForm == kStream) {
     if (p.split > 1) {
       // One item per cluster: CTA r adds the parts of tokens r, r + split, ... in the order
       // of the parts. A warp takes a token, 4 outputs a lane.
@@ -378,9 +461,16 @@ fp4_kernel(const __grid_constant__ Params p) {
   }
   tc::fence_before_sync();
   __syncthreads();
+  if constexpr (P) {   // nothing of the other CTA's is on its way here any more
+    cluster_arrive();
+    cluster_wait();
+  }
   if (warp == kMma) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, C::TMEM_COLS);
+    if constexpr (P)
+      tc::tmem_dealloc_pair(tmem, C::TMEM_COLS);
+    else
+      tc::tmem_dealloc(tmem, C::TMEM_COLS);
   }
 }
 
@@ -394,35 +484,42 @@ int64_t row_tiles(const Fp4Args& a, int per) {
   return a.expert_offsets == nullptr ? whole : (a.R < whole + a.E ? a.R : whole + a.E);
 }
 
-template <int W, int X, bool kNv, bool kTile>
+template <int W, int X, bool kNv, Form kForm>
 cudaError_t run(const Fp4Args& a, Params& p, cudaStream_t s) {
-  using C = Shape<W, X, kNv, kTile>;
+  using C = Shape<W, X, kNv, kForm>;
   cudaError_t e = encode(&p.tm_x, a.qx, a.K / 2, a.R, 0, X);
-  if (e != cudaSuccess) return e;
-  e = encode(&p.tm_w, a.qweight, a.K / 2, a.N, a.E, W);
+  if (e == cudaSuccess) e = encode(&p.tm_w, a.qweight, a.K / 2, a.N, a.E, C::W_LOAD);
+  if (e == cudaSuccess && p.tma_scales) e = encode(&p.tm_xs, a.x_scale, p.SB, a.R, 0, X, 1, 32);
+  if (e == cudaSuccess && p.tma_scales) e = encode(&p.tm_ws, a.w_scale, p.SB, a.N, a.E, W, 1, 32);
   if (e != cudaSuccess) return e;
   p.n_tiles = static_cast<int>((a.N + W - 1) / W);
-  const int64_t items = row_tiles(a, X) * p.n_tiles;
+  const int64_t items = row_tiles(a, C::PAIR ? 2 * X : X) * p.n_tiles;
   if (items > kMaxItems) return cudaErrorInvalidConfiguration;
   p.items = static_cast<int>(items);
-  const int64_t slots = static_cast<int64_t>(current_sm_count()) * C::CTAS;
   p.split = 1;
-  if (!kTile && a.expert_offsets == nullptr)
+  if (C::PAIR) {
+    const int64_t pairs = clusters_held(2, 1);
+    if (pairs < 1) return cudaErrorInvalidConfiguration;
+    return start<fp4_kernel<W, X, kNv, kForm>>(p, 2 * (items < pairs ? items : pairs), C::THREADS, C::SMEM, 2, s);
+  }
+  const int64_t slots = static_cast<int64_t>(current_sm_count()) * C::CTAS;
+  if (kForm == kStream && a.expert_offsets == nullptr)
     for (int n = kMaxSplit; n > 1 && p.split == 1; --n)
       if (p.KS >= 2 * n && items <= clusters_held(n, C::CTAS)) p.split = n;
   const int64_t grid = p.split > 1 ? items * p.split : (items < slots ? items : slots);
-  return start<fp4_kernel<W, X, kNv, kTile>>(p, grid, C::THREADS, C::SMEM, p.split, s);
+  return start<fp4_kernel<W, X, kNv, kForm>>(p, grid, C::THREADS, C::SMEM, p.split, s);
 }
 
 template <bool kNv>
 cudaError_t launch(const Fp4Args& a, Params& p, cudaStream_t s) {
   const bool experts = a.expert_offsets != nullptr;
   const int64_t rows = (a.R + a.E - 1) / a.E;
-  if (rows <= 16) return run<128, 16, kNv, false>(a, p, s);
-  if (rows <= 32) return run<128, 32, kNv, false>(a, p, s);
-  if (rows <= 64) return run<128, 64, kNv, false>(a, p, s);
-  if (!experts && rows <= 128) return run<128, 128, kNv, false>(a, p, s);
-  return run<192, 128, kNv, true>(a, p, s);
+  if (rows <= 16) return run<128, 16, kNv, kStream>(a, p, s);
+  if (rows <= 32) return run<128, 32, kNv, kStream>(a, p, s);
+  if (rows <= 64) return run<128, 64, kNv, kStream>(a, p, s);
+  if (!experts && rows <= 128) return run<128, 128, kNv, kStream>(a, p, s);
+  if (rows <= 192) return run<192, 128, kNv, kTile>(a, p, s);
+  return run<192, 128, kNv, kPair>(a, p, s);
 }
 
 }  // namespace
@@ -443,6 +540,8 @@ cudaError_t launch_fp4(const Fp4Args& a, cudaStream_t s) {
   p.K = static_cast<int>(a.K);
   p.SB = static_cast<int>(a.K / fp4_block(a.nv));
   p.KS = static_cast<int>((a.K + kStageK - 1) / kStageK);
+  // rows of scales that TMA takes; words one by one otherwise
+  p.tma_scales = p.SB % 16 == 0 && ((reinterpret_cast<uintptr_t>(a.x_scale) | reinterpret_cast<uintptr_t>(a.w_scale)) & 15) == 0;
   p.status = a.status;
   return a.nv ? launch<true>(a, p, s) : launch<false>(a, p, s);
 }

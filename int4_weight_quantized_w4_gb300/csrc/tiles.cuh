@@ -168,16 +168,18 @@ cudaError_t get_encoder(EncodeTiled* fn) {
 
 // Rows of K bytes in boxes of box_rows rows x 128 bytes (of box_mats matrices), 128-byte
 // swizzle; rows and columns past the tensor arrive as zeros.
-cudaError_t encode(CUtensorMap* m, const void* base, int64_t K, int64_t rows, int64_t E, int box_rows, int box_mats = 1) {
+// With `plain` bytes given, boxes of that many bytes a row without a swizzle.
+cudaError_t encode(CUtensorMap* m, const void* base, int64_t K, int64_t rows, int64_t E, int box_rows, int box_mats = 1,
+                   int plain = 0) {
   EncodeTiled fn = nullptr;
   cudaError_t e = get_encoder(&fn);
   if (e != cudaSuccess) return e;
   const cuuint32_t rank = E > 0 ? 3 : 2;
   const cuuint64_t dims[3] = {(cuuint64_t)K, (cuuint64_t)rows, (cuuint64_t)E};
   const cuuint64_t strides[2] = {(cuuint64_t)K, (cuuint64_t)K * (cuuint64_t)rows};
-  const cuuint32_t box[3] = {128, (cuuint32_t)box_rows, (cuuint32_t)box_mats}, estr[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {plain > 0 ? (cuuint32_t)plain : 128, (cuuint32_t)box_rows, (cuuint32_t)box_mats}, estr[3] = {1, 1, 1};
   CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, plain > 0 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
