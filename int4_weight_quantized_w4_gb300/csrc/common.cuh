@@ -292,6 +292,26 @@ W4_DEV void fma2c(float& d0, float& d1, float a0, float a1, float b, float c0, f
         : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b), "f"(c0), "f"(c1));
 }
 
+// -4 silu(g) * u = -g / D * u of the bf16 pairs g and u, D = (1 + exp(-g)) / 4: a
+// quarter, whose reciprocal is a normal number for every finite D. With r = -1/D
+// approximately and q = g r, the remainder g + D q times r is what q lacks: the quotient
+// comes out within an ulp (the signs save negations). The gate comes before u, so that
+// only the product itself can overflow. Where D is infinite (gates below -88.7) or the
+// gate is, the remainder is NaN, and a product beyond a quarter of the largest fp32 is
+// infinite or NaN: the caller sees that in the block's maximum. Everything but
+// exponential and reciprocal goes two at a time.
+W4_DEV void neg_silu4_mul2(uint32_t g, uint32_t u, float& a0, float& a1) {
+  const float g0 = bf16_lo(g), g1 = bf16_hi(g);
+  float d0, d1, r0, r1, e0, e1;
+  fma2c(d0, d1, expf(-g0), expf(-g1), 0.25f, 0.25f, 0.25f);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(-d0));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(-d1));
+  mul2v(a0, a1, g0, g1, r0, r1);
+  fma2x(e0, e1, d0, d1, a0, a1, g0, g1);
+  fma2v(a0, a1, e0, e1, r0, r1);
+  mul2v(a0, a1, a0, a1, bf16_lo(u), bf16_hi(u));
+}
+
 // The e4m3 codes of the fp32 quotients fl(x0 / s), fl(x1 / s) in the low two
 // bytes, with r = fl(1 / s). Division by multiply-add refinement (P. Markstein,
 // "Computation of elementary functions on the IBM RISC System/6000 processor",
@@ -452,6 +472,17 @@ W4_DEV uint4 ld_once_v4(const void* p) {
   asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
   return v;
+}
+
+// 32 bytes in one access, for 32-byte aligned addresses: a lane's two 16-byte loads would
+// each ask for the whole sector.
+W4_DEV void ld_once_v8(const void* p, uint4& a, uint4& b) {
+  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w) : "l"(p) : "memory");
+}
+W4_DEV void st_v8(void* p, const uint4& a, const uint4& b) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+               :: "l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w) : "memory");
 }
 
 W4_DEV uint2 ld_nc_v2(const void* p) {

@@ -7,8 +7,8 @@
 //          / 6) / g)), held to 448; d = fl(s g); q = rne_e2m1(fl(x / d)), held to +-6 (0
 //          where d is 0).
 //
-// x is a bf16 or fp16 activation, or silu(gate) * up of a bf16 gate_up row, in IEEE
-// fp32 steps: fl(fl(g / fl(1 + expf(-g))) up). A block that holds a NaN or an infinity gets
+// x is a bf16 or fp16 activation, or silu(gate) * up of a bf16 gate_up row, in fp32 steps:
+// fl(fl(g / fl(1 + expf(-g))) up), the quotient within an ulp of IEEE's. A block that holds a NaN or an infinity gets
 // a NaN scale, so that it shows in whatever is computed from it.
 //
 // K is a multiple of the block, so blocks of a row-major matrix follow one another
@@ -21,7 +21,7 @@
 namespace w4 {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr uint32_t kInfBits = 0x7F800000u;
 
@@ -61,6 +61,22 @@ W4_DEV uint32_t quotients_e2m1(const float (&x)[8], float d, float r) {
 // Halfwise maximum of magnitude bits: NaNs are above infinities, those above numbers.
 W4_DEV uint32_t max_u16x2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
 
+// fl(fl(a / 6) / g) up to what e4m3 makes of it, by multiply-add refinement (as
+// quotient2_e4m3) where no remainder can underflow or overflow; else by IEEE divides.
+W4_DEV float block_quotient(float a, float g) {
+  constexpr float kSixth = 0.166666672f;   // fl(1 / 6)
+  if (!(a > 1e-25f && a < 1e30f && scale_refines(g))) return __fdiv_rn(__fdiv_rn(a, 6.f), g);
+  float v = a * kSixth;
+  v = fmaf(fmaf(v, -6.f, a), kSixth, v);
+  const float r = __frcp_rn(g);
+  float q = v * r;
+  if (q < 4096.f) {   // others are held at 448
+    q = fmaf(fmaf(q, -g, v), r, q);
+    q = fmaf(fmaf(q, -g, v), r, q);
+  }
+  return q;
+}
+
 // Scale byte and codes of 16 elements; bits: those of the block's largest magnitude.
 // kNv: the block is this thread's; else it is two lanes'.
 template <bool kNv>
@@ -70,7 +86,7 @@ W4_DEV uint32_t block_codes(const float (&x)[2][8], uint32_t bits, float g, uint
       code = make_uint2(0, 0);
       return 0x7F;
     }
-    const float v = __fdiv_rn(__fdiv_rn(__uint_as_float(bits), 6.f), g);
+    const float v = block_quotient(__uint_as_float(bits), g);
     const uint32_t s8 = e4m3x2_rn(v, 0.f) & 0xFFu;
     const float s = half_bits_to_f32(e4m3x2_to_f16x2(s8) & 0xFFFFu);
     const float d = s * g;
@@ -100,14 +116,23 @@ W4_DEV uint32_t block_codes(const float (&x)[2][8], uint32_t bits, float g, uint
   }
 }
 
+W4_DEV void load32(const uint4* p, bool wide, uint4 (&v)[2]) {
+  if (wide) {
+    ld_once_v8(p, v[0], v[1]);
+  } else {
+    v[0] = ld_once_v4(p);
+    v[1] = ld_once_v4(p + 1);
+  }
+}
+
 // Item i: 16 elements of the output. kSilu: columns c and K + c of the row's 2 K. gather
 // (may be null): source row of each output row; an id outside [0, T) gives a zero row and
-// W4_ERR_SHAPE in the status word. K16 = K / 16. signals: the next kernel may start once every
+// W4_ERR_SHAPE in the status word. K16 = K / 16. wide: x is 32-byte aligned. signals: the next kernel may start once every
 // kernel before this one is done; else when this one is, which may have written weights.
 template <bool kNv, bool kF16, bool kSilu>
 __global__ void __launch_bounds__(kThreads) quant_fp4_kernel(const uint4* x, int64_t items, uint32_t K16,
                                                              const float* global, const int32_t* gather, int64_t T,
-                                                             bool signals, uint2* __restrict__ q,
+                                                             bool signals, bool wide, uint2* __restrict__ q,
                                                              uint8_t* __restrict__ scale, unsigned int* status) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
   const bool live = i < items;   // an odd half of the last warp still takes part in the shuffles
@@ -130,24 +155,38 @@ __global__ void __launch_bounds__(kThreads) quant_fp4_kernel(const uint4* x, int
   float f[2][8];
   uint32_t bits = 0;
   if (live && !bad) {
-    v[0] = ld_once_v4(x + 2 * at);
-    v[1] = ld_once_v4(x + 2 * at + 1);
+    load32(x + 2 * at, wide, v);
   }
   if constexpr (kSilu) {
     uint4 u[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
     if (live && !bad) {
-      u[0] = ld_once_v4(x + 2 * (at + K16));
-      u[1] = ld_once_v4(x + 2 * (at + K16) + 1);
+      load32(x + 2 * (at + K16), wide, u);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      float a[8];
-      chunk_f32<false>(v[h], a);
-      chunk_f32<false>(u[h], f[h]);
+      const uint32_t gw[4] = {v[h].x, v[h].y, v[h].z, v[h].w}, uw[4] = {u[h].x, u[h].y, u[h].z, u[h].w};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        f[h][j] *= __fdiv_rn(a[j], 1.f + expf(-a[j]));
-        bits = max(bits, __float_as_uint(f[h][j]) & 0x7FFFFFFFu);
+      for (int j = 0; j < 4; ++j) {
+        float a0, a1;
+        neg_silu4_mul2(gw[j], uw[j], a0, a1);
+        mul2(f[h][2 * j], f[h][2 * j + 1], a0, a1, -0.25f);
+        bits = max(bits, max(__float_as_uint(f[h][2 * j]) & 0x7FFFFFFFu, __float_as_uint(f[h][2 * j + 1]) & 0x7FFFFFFFu));
+      }
+    }
+    // far or infinite gates and products beyond a quarter of the largest number show as
+    // infinities or NaN there; products below 2^-120 have lost bits: by the formula's steps
+    if (bits >= kInfBits || bits < (7u << 23)) {
+      bits = 0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float a[8];
+        chunk_f32<false>(v[h], a);
+        chunk_f32<false>(u[h], f[h]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          f[h][j] *= __fdiv_rn(a[j], 1.f + expf(-a[j]));
+          bits = max(bits, __float_as_uint(f[h][j]) & 0x7FFFFFFFu);
+        }
       }
     }
   } else {
@@ -165,7 +204,7 @@ __global__ void __launch_bounds__(kThreads) quant_fp4_kernel(const uint4* x, int
   if constexpr (!kNv) bits = max(bits, __shfl_xor_sync(kFull, bits, 1));
   if (!live) return;
   uint2 code;
-  const uint32_t s = block_codes<kNv>(f, bits, kNv && global != nullptr ? __ldcg(global) : 1.f, code);
+  const uint32_t s = block_codes<kNv>(f, bits, kNv && global != nullptr ? *global : 1.f, code);
   q[i] = code;
   if constexpr (kNv)
     scale[i] = static_cast<uint8_t>(s);
@@ -178,14 +217,14 @@ cudaError_t launch(const QuantFp4Args& a, cudaStream_t s) {
   const int64_t items = a.M * (a.K / 16);
   PdlLaunch pl(static_cast<unsigned>((items + kThreads - 1) / kThreads), kThreads, 0, s);
   return cudaLaunchKernelEx(&pl.cfg, quant_fp4_kernel<kNv, kF16, kSilu>, static_cast<const uint4*>(a.x), items,
-                            static_cast<uint32_t>(a.K / 16), a.global, a.gather, a.T, a.signals, static_cast<uint2*>(a.q),
+                            static_cast<uint32_t>(a.K / 16), a.global, a.gather, a.T, a.signals, (reinterpret_cast<uintptr_t>(a.x) & 31) == 0, static_cast<uint2*>(a.q),
                             static_cast<uint8_t*>(a.scale), a.status);
 }
 
 // Values of 16 codes: rounded once, from fl(q d) with d = fl(s g), or from q 2^e.
 template <bool kNv, bool kF16>
 __global__ void __launch_bounds__(kThreads) dequant_fp4_kernel(const uint2* q, const uint8_t* scale,
-                                                               const float* global, int64_t items,
+                                                               const float* global, int64_t items, bool wide,
                                                                uint4* __restrict__ out) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -194,10 +233,11 @@ __global__ void __launch_bounds__(kThreads) dequant_fp4_kernel(const uint2* q, c
   const uint32_t s8 = __ldcg(scale + (kNv ? i : i >> 1));
   float d;
   if constexpr (kNv) {
-    d = half_bits_to_f32(e4m3x2_to_f16x2(s8) & 0xFFFFu) * (global != nullptr ? __ldcg(global) : 1.f);
+    d = half_bits_to_f32(e4m3x2_to_f16x2(s8) & 0xFFFFu) * (global != nullptr ? *global : 1.f);   // from L1: one L2 line for every warp took 36 us in place of 23
   } else {
     d = __uint_as_float(s8 == 0 ? 1u << 22 : s8 == 255 ? 0x7FC00000u : s8 << 23);
   }
+  uint4 v[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     uint32_t w[4], o[4];
@@ -211,7 +251,13 @@ __global__ void __launch_bounds__(kThreads) dequant_fp4_kernel(const uint2* q, c
       else
         o[j] = pack_bf16x2(lo, hi);
     }
-    out[2 * i + h] = make_uint4(o[0], o[1], o[2], o[3]);
+    v[h] = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+  if (wide) {
+    st_v8(out + 2 * i, v[0], v[1]);
+  } else {
+    out[2 * i] = v[0];
+    out[2 * i + 1] = v[1];
   }
 }
 
@@ -234,7 +280,7 @@ cudaError_t launch_dequant_fp4(const void* q, const void* scale, const float* gl
   auto* kernel = nv ? (f16 ? dequant_fp4_kernel<true, true> : dequant_fp4_kernel<true, false>)
                     : (f16 ? dequant_fp4_kernel<false, true> : dequant_fp4_kernel<false, false>);
   return cudaLaunchKernelEx(&pl.cfg, kernel, static_cast<const uint2*>(q), static_cast<const uint8_t*>(scale), global,
-                            items, static_cast<uint4*>(out));
+                            items, (reinterpret_cast<uintptr_t>(out) & 31) == 0, static_cast<uint4*>(out));
 }
 
 }  // namespace w4

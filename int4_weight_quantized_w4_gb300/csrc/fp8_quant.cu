@@ -38,25 +38,6 @@ constexpr int kUnits = 4;
 constexpr int kThreads = 128;    // 4097 x 4096 9.8 us against 10.1 in blocks of 256 threads
 constexpr unsigned kFull = 0xFFFFFFFFu;
 
-// -4 silu(g) * u = -g / D * u of the bf16 pairs g and u, D = (1 + exp(-g)) / 4: a
-// quarter, whose reciprocal is a normal number for every finite D. With r = -1/D
-// approximately and q = g r, the remainder g + D q times r is what q lacks: the quotient
-// comes out within an ulp (the signs save negations). The gate comes before u, so that
-// only the product itself can overflow. Where D is infinite (gates below -88.7) or the
-// gate is, the remainder is NaN, and a product beyond a quarter of the largest fp32 is
-// infinite or NaN: the caller sees that in the block's maximum. Everything but
-// exponential and reciprocal goes two at a time.
-W4_DEV void neg_silu4_mul2(uint32_t g, uint32_t u, float& a0, float& a1) {
-  const float g0 = bf16_lo(g), g1 = bf16_hi(g);
-  float d0, d1, r0, r1, e0, e1;
-  fma2c(d0, d1, expf(-g0), expf(-g1), 0.25f, 0.25f, 0.25f);
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(-d0));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(-d1));
-  mul2v(a0, a1, g0, g1, r0, r1);
-  fma2x(e0, e1, d0, d1, a0, a1, g0, g1);
-  fma2v(a0, a1, e0, e1, r0, r1);
-  mul2v(a0, a1, a0, a1, bf16_lo(u), bf16_hi(u));
-}
 // -silu(g) * u of any gate. Far below zero the denominator overflows long before the
 // product with a large u vanishes: there silu(g) = g exp(g), whose exponential is taken in
 // four factors, two on either side of u, so that an underflow before the end is one of the
