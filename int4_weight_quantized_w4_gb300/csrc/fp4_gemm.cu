@@ -87,7 +87,7 @@ struct Shape {
   static constexpr int S_COLS = 4 * WORDS * (AW + AX);         // tensor memory columns of a stage's scales
   static constexpr int USED = ACCS * N + 2 * S_COLS;
   static constexpr int TMEM_COLS = USED <= 128 ? 128 : USED <= 256 ? 256 : 512;
-  static constexpr int THREADS = 32 * (7 + AW + AX);
+  static constexpr int THREADS = 32 * (8 + AW + AX);
   static constexpr int OUT = kForm != kStream ? 4 * 2048 : 0;
   static constexpr int BARS = 2 * STAGES + 2 * RAWS + 2 * ACCS;
   static constexpr int SMEM = STAGES * (STAGE + SSTAGE) + RAWS * RAW + OUT + 256 + (kMaxExperts + 1 + 16 + 3) / 4 * 16 + 1024;
@@ -112,7 +112,7 @@ template <int W, int X, bool kNv, Form kForm>
 __global__ void __launch_bounds__(Shape<W, X, kNv, kForm>::THREADS, Shape<W, X, kNv, kForm>::CTAS)
 fp4_kernel(const __grid_constant__ Params p) {
   using C = Shape<W, X, kNv, kForm>;
-  constexpr int kMma = 4, kLoadW = 5, kLoadX = 6, kTurn = 7;   // warps; 0 to 3: epilogue; kTurn ..: scales
+  constexpr int kMma = 4, kLoadW = 5, kLoadX = 6, kLoadS = 7, kTurn = 8;   // warps; 0 to 3: epilogue; kTurn ..: a warp per scale atom
   constexpr bool P = C::PAIR;
   constexpr int kRowsPer = P ? 2 * X : X;
   extern __shared__ uint8_t smem_dyn[];
@@ -136,11 +136,11 @@ fp4_kernel(const __grid_constant__ Params p) {
   const uint32_t rank = P ? cluster_rank() : 0;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
-      mbar_init(&full[i], (2 + C::AW + C::AX) * (P ? 2 : 1));   // a CTA's two operands, its scale warps
+      mbar_init(&full[i], P ? 1 + 2 * (C::AW + C::AX) : 2 + C::AW + C::AX);   // operands; scale warps
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < C::RAWS; ++i) {
-      mbar_init(&raw_full[i], p.tma_scales ? 2 : 64);
+      mbar_init(&raw_full[i], p.tma_scales ? 1 : 32);
       mbar_init(&raw_empty[i], C::AW + C::AX);
     }
     for (int i = 0; i < C::ACCS; ++i) {
@@ -158,6 +158,10 @@ fp4_kernel(const __grid_constant__ Params p) {
   }
   if (warp == kLoadW && lane == 0) tc::prefetch_tmap(&p.tm_w);
   if (warp == kLoadX && lane == 0) tc::prefetch_tmap(&p.tm_x);
+  if (warp == kLoadS && lane == 0 && p.tma_scales) {
+    tc::prefetch_tmap(&p.tm_ws);
+    tc::prefetch_tmap(&p.tm_xs);
+  }
   if (p.offsets != nullptr) {
     grid_dependency_wait();   // the routing may be running still
     tile_starts<C::THREADS>(p, kRowsPer, starts, warp_sum);
@@ -179,50 +183,30 @@ fp4_kernel(const __grid_constant__ Params p) {
   const int first = blockIdx.x / ctas, step = gridDim.x / ctas;
 
   if (warp == kLoadW || warp == kLoadX) {
-    // An operand and its scales, by lane 0; scales that TMA cannot copy by all lanes.
+    // An operand. Pair: all four copies of a stage count on the first CTA's barrier, and its
+    // weights' warp announces them.
     const bool is_w = warp == kLoadW;
-    int st = 0, ph = 1, rs = 0, rph = 1, e = 0;
+    int st = 0, ph = 1, e = 0;
     bool ok = true, waited = !is_w;
     Tile t;
     if (!is_w) grid_dependency_wait();   // the codes come from the kernel before
-    for (int it = first; ok && it < p.items && decode(p, it, kRowsPer, W, starts, t, e); it += step) {
-      const int row0 = t.row0 + static_cast<int>(rank) * X;
+    for (int it = first; ok && it < p.items && decode(p, it, kRowsPer, W, starts, t, e); it += step)
       for (int ks = ks0; ks < ks1; ++ks) {
-        if (!waited && (ph == 0 || rph == 0)) {   // a ring is full, and is emptied only after the kernels before
+        if (!waited && ph == 0) {   // the ring is full, and is emptied only after the kernels before
           grid_dependency_wait();
           waited = true;
         }
-        if (ks == ks0 || ks % C::SUPER == 0) {
-          if (!(ok = wait_warp(&raw_empty[rs], rph, abort_flag, p.status))) break;
-          uint8_t* to = raw + rs * C::RAW + (is_w ? 0 : C::RAW_W);
-          const int at = ks / C::SUPER * 32;
-          if (p.tma_scales) {
-            if (lane == 0) {
-              mbar_arrive_expect_tx(&raw_full[rs], 32 * (is_w ? W : X));
-              if (is_w)
-                tc::tma_load_3d(to, &p.tm_ws, &raw_full[rs], at, t.n0, t.expert);
-              else
-                tc::tma_load_2d(to, &p.tm_xs, &raw_full[rs], at, row0);
-            }
-          } else {
-            if (is_w)
-              copy_scale_words(smem_addr(to), p.w_scale + (static_cast<size_t>(t.expert) * p.N + t.n0) * p.SB, p.SB, at, W, p.N - t.n0);
-            else
-              copy_scale_words(smem_addr(to), p.x_scale + static_cast<size_t>(row0 < t.row_end ? row0 : t.row0) * p.SB, p.SB, at, X, t.row_end - row0);
-            tc::copy_async_arrive(&raw_full[rs]);
-          }
-          if (++rs == C::RAWS) rs = 0, rph ^= 1;
-        }
         if (!(ok = wait_warp(&empty[st], ph, abort_flag, p.status))) break;
-        if (lane == 0) {
+        if (elect_one()) {
           uint8_t* to = ring + st * C::STAGE + (is_w ? 0 : C::W_BYTES);
           if constexpr (P) {
             const uint32_t bar = tc::cluster_addr(&full[st], 0);
-            tc::cluster_arrive_expect_tx(bar, is_w ? C::W_BYTES : C::X_BYTES);
-            if (is_w)
+            if (is_w) {
+              if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * C::STAGE);
               tc::tma_load_3d_pair(to, &p.tm_w, bar, ks * kStageBytes, t.n0 + static_cast<int>(rank) * C::W_LOAD, t.expert);
-            else
-              tc::tma_load_2d_pair(to, &p.tm_x, bar, ks * kStageBytes, row0);
+            } else {
+              tc::tma_load_2d_pair(to, &p.tm_x, bar, ks * kStageBytes, t.row0 + static_cast<int>(rank) * X);
+            }
           } else {
             mbar_arrive_expect_tx(&full[st], is_w ? C::W_BYTES : C::X_BYTES);
             if (is_w)
@@ -233,6 +217,37 @@ fp4_kernel(const __grid_constant__ Params p) {
         }
         __syncwarp();
         if (++st == C::STAGES) st = 0, ph ^= 1;
+      }
+  } else if (warp == kLoadS) {
+    // Both operands' scales, 32 bytes a row; those that TMA cannot copy by all lanes.
+    int rs = 0, rph = 1, e = 0;
+    bool ok = true, waited = false;
+    Tile t;
+    for (int it = first; ok && it < p.items && decode(p, it, kRowsPer, W, starts, t, e); it += step) {
+      const int row0 = t.row0 + static_cast<int>(rank) * X;
+      for (int ks = ks0; ks < ks1; ks = (ks / C::SUPER + 1) * C::SUPER) {
+        if (!(ok = wait_warp(&raw_empty[rs], rph, abort_flag, p.status))) break;
+        uint8_t* to = raw + rs * C::RAW;
+        const int at = ks / C::SUPER * 32;
+        if (p.tma_scales) {
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&raw_full[rs], 32 * (W + X));
+            tc::tma_load_3d(to, &p.tm_ws, &raw_full[rs], at, t.n0, t.expert);
+          }
+          __syncwarp();
+        } else {
+          copy_scale_words(smem_addr(to), p.w_scale + (static_cast<size_t>(t.expert) * p.N + t.n0) * p.SB, p.SB, at, W, p.N - t.n0);
+        }
+        if (!waited) grid_dependency_wait();   // the activations' come from the kernel before
+        waited = true;
+        if (p.tma_scales) {
+          if (elect_one()) tc::tma_load_2d(to + C::RAW_W, &p.tm_xs, &raw_full[rs], at, row0);
+          __syncwarp();
+        } else {
+          copy_scale_words(smem_addr(to + C::RAW_W), p.x_scale + static_cast<size_t>(row0 < t.row_end ? row0 : t.row0) * p.SB, p.SB, at, X, t.row_end - row0);
+          tc::copy_async_arrive(&raw_full[rs]);
+        }
+        if (++rs == C::RAWS) rs = 0, rph ^= 1;
       }
     }
   } else if (warp >= kTurn) {

@@ -78,14 +78,11 @@ W4_DEV uint32_t cluster_addr(const void* p, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
   return a;
 }
-// Arrivals on a barrier of any CTA of the cluster, given by cluster_addr. They order what a
-// thread did for its own CTA (with release at cluster scope one takes some 1500 cycles): the
+// Arrival on a barrier of any CTA of the cluster, given by cluster_addr. It orders what a
+// thread did for its own CTA (with release at cluster scope it takes some 1500 cycles): the
 // one that waits issues MMAs, whose reads of either CTA's shared memory are its own SM's.
 W4_DEV void cluster_arrive_on(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
-}
-W4_DEV void cluster_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" :: "r"(bar), "r"(bytes) : "memory");
 }
 // Copies into this CTA's shared memory whose bytes count on a barrier of either CTA.
 W4_DEV void tma_load_2d_pair(void* smem_dst, const void* tmap, uint32_t bar, int c0, int c1) {
