@@ -76,8 +76,9 @@ typedef enum {
   W4_OP_MOE_ROUTE_GROUPED = 3, /* w4_moe_route_grouped (M = T tokens, N = E experts; K = 1, group ignored) */
   W4_OP_FP8_BLOCK = 4,      /* w4_fp8_block_gemm (group ignored) */
   W4_OP_FP8_BLOCK_IN = 5,   /* w4_fp8_block_gemm_bf16in (group = 0), w4_fp8_block_moe_gemm_bf16in (M = R rows, group = E) */
-  W4_OP_FP4_IN = 6,         /* w4_fp4_gemm_bf16in, w4_fp4_moe_gemm_bf16in (M = rows, group = 16 or 32: the format's block) */
-  W4_OP_MOE_DECODE = 7      /* w4_moe_decode (M = T tokens, N = top_k, K = I; group ignored) */
+  W4_OP_FP4_IN = 6,         /* w4_fp4_gemm_bf16in (M = rows, group = 16 or 32: the format's block) */
+  W4_OP_MOE_DECODE = 7,     /* w4_moe_decode (M = T tokens, N = top_k, K = I; group ignored) */
+  W4_OP_FP4_MOE_IN = 8      /* w4_fp4_moe_gemm_bf16in (M = R rows, group = 16 or 32) */
 } w4_op;
 
 /* 4-bit weight formats. */
@@ -551,7 +552,8 @@ w4_status w4_dequant_fp4(const void* q, const void* scale, int32_t format, const
  *
  * w4_fp4_moe_gemm_bf16in: row r is token row_token[r] of x [T, K] bf16 (row_token NULL: R
  * == T and row r is token r), quantized into the workspace
- * (w4_workspace_bytes(W4_OP_FP4_IN, R, N, K, 16 or 32) bytes), then
+ * (w4_workspace_bytes(W4_OP_FP4_MOE_IN, R, N, K, 16 or 32) bytes; with only those of
+ * W4_OP_FP4_IN a token is quantized again for each of its rows), then
  * w4_fp4_moe_grouped_gemm. A row_token entry outside [0, T) gives a zero row and sets
  * W4_ERR_SHAPE in the device status word.
  *

@@ -140,7 +140,11 @@ size_t w4_workspace_bytes(int32_t op, int64_t M, int64_t N, int64_t K, int32_t g
            (group > 0 ? w4::fp8_block_workspace_bytes(M / 2, K) : w4::fp8_block_part_bytes(M, N, K));
   }
   if (op == W4_OP_MOE_DECODE) return N > 0 ? w4::moe_decode_workspace_bytes(M, N, K) : 0;
-  if (op == W4_OP_FP4_IN) return (group == 16 || group == 32) && K % group == 0 ? w4::fp4_workspace_bytes(M, K, group == 16) : 0;
+  if (op == W4_OP_FP4_IN || op == W4_OP_FP4_MOE_IN) {
+    if ((group != 16 && group != 32) || K % group != 0) return 0;
+    // the rows, and for experts the tokens they come from when those are at most half as many
+    return w4::fp4_workspace_bytes(M, K, group == 16) + (op == W4_OP_FP4_MOE_IN ? w4::fp4_workspace_bytes(M / 2, K, group == 16) : 0);
+  }
   if (op == W4_OP_MOE_ROUTE) return (N > 0 && N <= 1024) ? w4::moe_route_workspace_bytes(M, static_cast<int32_t>(N)) : 0;
   return 0;
 }
@@ -675,6 +679,10 @@ static w4_status run_fp4(w4::Fp4Args a, void* stream) {
   return from_cuda(w4::launch_fp4(a, static_cast<cudaStream_t>(stream)), "fp4 product launch");
 }
 
+// Elements of expert rows from which on tokens are quantized once and their codes copied, as
+// kCopyElements.
+constexpr int64_t kCopyFp4 = int64_t{1} << 23;
+
 // Quantizes rows of x (gathered by `rows` when given) into the workspace, then multiplies (a.qx, a.x_scale unset).
 static w4_status run_fp4_act(const void* x, bool f16, int64_t T, const int32_t* rows, w4::Fp4Args a, void* ws,
                              size_t ws_bytes, void* stream) {
@@ -688,9 +696,18 @@ static w4_status run_fp4_act(const void* x, bool f16, int64_t T, const int32_t* 
   unsigned int* status = nullptr;
   cudaError_t e = status_ptr(&status);
   if (e != cudaSuccess) return from_cuda(e, "device status word");
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t* scale = static_cast<uint8_t*>(ws) + w4::fp4_code_bytes(a.R, a.K);
-  const w4::QuantFp4Args q{x, a.nv, f16, false, a.R, a.K, a.x_global, rows, T, true, ws, scale, status};
-  e = w4::launch_quant_fp4(q, static_cast<cudaStream_t>(stream));
+  if (rows != nullptr && T > 0 && 2 * T <= a.R && a.R * a.K >= kCopyFp4 && ws_bytes >= need + w4::fp4_workspace_bytes(T, a.K, a.nv)) {
+    uint8_t* tq = static_cast<uint8_t*>(ws) + need;
+    uint8_t* ts = tq + w4::fp4_code_bytes(T, a.K);
+    const w4::QuantFp4Args q{x, a.nv, f16, false, T, a.K, a.x_global, nullptr, 0, true, tq, ts, status};
+    e = w4::launch_quant_fp4(q, s);
+    if (e == cudaSuccess) e = w4::launch_gather_fp4_rows(tq, ts, T, a.K, a.nv, rows, a.R, ws, scale, status, s);
+  } else {
+    const w4::QuantFp4Args q{x, a.nv, f16, false, a.R, a.K, a.x_global, rows, T, true, ws, scale, status};
+    e = w4::launch_quant_fp4(q, s);
+  }
   if (e != cudaSuccess) return from_cuda(e, "fp4 quant launch");
   a.qx = ws;
   a.x_scale = scale;

@@ -554,7 +554,7 @@ PyObject* fp4_moe_gemm_act(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const float* wg = global_scale(a[7], "w_global", E, dev);
   const CallStream stream(a[10], dev);
   const at::Tensor y = output(a[8], "y", {R, N}, ScalarType::BFloat16, kBf16, dev, stream);
-  const Scratch s = scratch(a[9], W4_OP_FP4_IN, R, N, K, static_cast<int32_t>(f.block), dev);
+  const Scratch s = scratch(a[9], W4_OP_FP4_MOE_IN, R, N, K, static_cast<int32_t>(f.block), dev);
   if (failed(w4_fp4_moe_gemm_bf16in(x.data_ptr(), T, xg, static_cast<const int32_t*>(data(a[1])),
                                     static_cast<const int32_t*>(data(a[2])), static_cast<int32_t>(E), data(a[3]),
                                     data(a[4]), wg, f.id, y.data_ptr(), R, N, K, s.p, s.bytes, stream.handle()),

@@ -60,11 +60,17 @@ struct Params {
   unsigned int* status;
 };
 
-// Rows [a, b) of expert e; a segment outside [0, rows) counts as clipped. The offsets
-// are read from L2, where the kernel that wrote them left them.
-W4_DEV void seg_bounds(const Params& p, int e, int& a, int& b) {
-  a = max(__ldcg(p.offsets + e), 0);
-  b = min(__ldcg(p.offsets + e + 1), p.rows);
+// What a call's tiles follow from (tiles.cuh). offsets: a copy in shared memory where there
+// is room, because every warp looks them up for every tile (from L2, 1300 cycles in which
+// the MMAs of a 4096-token gate_up stood still).
+struct Segments {
+  const int32_t* offsets;
+  int E, rows, n_tiles;
+};
+// Rows [a, b) of expert e; a segment outside [0, rows) counts as clipped.
+W4_DEV void seg_bounds(const Segments& p, int e, int& a, int& b) {
+  a = max(p.offsets[e], 0);
+  b = min(p.offsets[e + 1], p.rows);
 }
 
 // W: weight rows of a tile, X: tokens of a CTA's tile.
@@ -82,15 +88,17 @@ struct Shape {
   static constexpr int RAW_W = 128 * AW * 32, RAW = RAW_W + (X + 31) / 32 * 32 * 32;   // scales as they are in memory
   static constexpr int CTAS = kForm != kStream || X > 64 ? 1 : 2;   // resident per SM
   static constexpr int STAGES = CTAS == 2 ? (X == 64 ? 3 : 4) : kForm == kTile ? 4 : 5;
-  static constexpr int RAWS = kForm == kTile || X == 32 ? 2 : 3;
+  static constexpr int RAWS = kForm != kStream || X == 32 ? 2 : 3;
   static constexpr int ACCS = 2;
   static constexpr int S_COLS = 4 * WORDS * (AW + AX);         // tensor memory columns of a stage's scales
   static constexpr int USED = ACCS * N + 2 * S_COLS;
   static constexpr int TMEM_COLS = USED <= 128 ? 128 : USED <= 256 ? 256 : 512;
-  static constexpr int THREADS = 32 * (8 + AW + AX);
-  static constexpr int OUT = kForm != kStream ? 4 * 2048 : 0;
+  static constexpr int EPI = PAIR ? 8 : 4;                     // epilogue warps: a quarter of the lanes, a half or all of the columns
+  static constexpr int THREADS = 32 * (EPI + 4 + AW + AX);
+  static constexpr int OUT = kForm != kStream ? EPI * 2048 : 0;
   static constexpr int BARS = 2 * STAGES + 2 * RAWS + 2 * ACCS;
-  static constexpr int SMEM = STAGES * (STAGE + SSTAGE) + RAWS * RAW + OUT + 256 + (kMaxExperts + 1 + 16 + 3) / 4 * 16 + 1024;
+  static constexpr int STARTS = (kForm != kStream ? 2 : 1) * (kMaxExperts + 1) + 16;   // words
+  static constexpr int SMEM = STAGES * (STAGE + SSTAGE) + RAWS * RAW + OUT + 256 + (STARTS + 3) / 4 * 16 + 1024;
   static_assert(USED <= 512 && CTAS * TMEM_COLS <= 512, "tensor memory");
   static_assert(SMEM <= 232448 && CTAS * SMEM + CTAS * 1024 <= 233472, "shared memory");
   static_assert(BARS * 8 + 8 <= 256, "barriers");
@@ -112,7 +120,8 @@ template <int W, int X, bool kNv, Form kForm>
 __global__ void __launch_bounds__(Shape<W, X, kNv, kForm>::THREADS, Shape<W, X, kNv, kForm>::CTAS)
 fp4_kernel(const __grid_constant__ Params p) {
   using C = Shape<W, X, kNv, kForm>;
-  constexpr int kMma = 4, kLoadW = 5, kLoadX = 6, kLoadS = 7, kTurn = 8;   // warps; 0 to 3: epilogue; kTurn ..: a warp per scale atom
+  // warps; below kMma: epilogue; kTurn ..: a warp per scale atom
+  constexpr int kMma = C::EPI, kLoadW = kMma + 1, kLoadX = kMma + 2, kLoadS = kMma + 3, kTurn = kMma + 4;
   constexpr bool P = C::PAIR;
   constexpr int kRowsPer = P ? 2 * X : X;
   extern __shared__ uint8_t smem_dyn[];
@@ -131,6 +140,7 @@ fp4_kernel(const __grid_constant__ Params p) {
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int32_t* starts = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(full) + 256);
   int32_t* warp_sum = starts + kMaxExperts + 1;
+  int32_t* offsets = warp_sum + 16;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = P ? cluster_rank() : 0;
@@ -145,7 +155,7 @@ fp4_kernel(const __grid_constant__ Params p) {
     }
     for (int i = 0; i < C::ACCS; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], P ? 8 : 4);
+      mbar_init(&acc_empty[i], P ? 2 * C::EPI : C::EPI);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -162,9 +172,15 @@ fp4_kernel(const __grid_constant__ Params p) {
     tc::prefetch_tmap(&p.tm_ws);
     tc::prefetch_tmap(&p.tm_xs);
   }
+  Segments seg{p.offsets, p.E, p.rows, p.n_tiles};
   if (p.offsets != nullptr) {
     grid_dependency_wait();   // the routing may be running still
-    tile_starts<C::THREADS>(p, kRowsPer, starts, warp_sum);
+    if constexpr (kForm != kStream) {
+      for (int i = threadIdx.x; i <= p.E; i += C::THREADS) offsets[i] = p.offsets[i];
+      seg.offsets = offsets;
+      __syncthreads();
+    }
+    tile_starts<C::THREADS>(seg, kRowsPer, starts, warp_sum);
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -181,6 +197,7 @@ fp4_kernel(const __grid_constant__ Params p) {
   const int ks0 = p.KS * part / p.split, ks1 = p.KS * (part + 1) / p.split;
   const int ctas = P ? 2 : p.split;   // of one item
   const int first = blockIdx.x / ctas, step = gridDim.x / ctas;
+  const int items = p.offsets == nullptr ? p.items : min(p.items, starts[p.E] * p.n_tiles);
 
   if (warp == kLoadW || warp == kLoadX) {
     // An operand. Pair: all four copies of a stage count on the first CTA's barrier, and its
@@ -190,7 +207,7 @@ fp4_kernel(const __grid_constant__ Params p) {
     bool ok = true, waited = !is_w;
     Tile t;
     if (!is_w) grid_dependency_wait();   // the codes come from the kernel before
-    for (int it = first; ok && it < p.items && decode(p, it, kRowsPer, W, starts, t, e); it += step)
+    for (int it = first; ok && it < items && decode(seg, it, kRowsPer, W, starts, t, e); it += step)
       for (int ks = ks0; ks < ks1; ++ks) {
         if (!waited && ph == 0) {   // the ring is full, and is emptied only after the kernels before
           grid_dependency_wait();
@@ -223,7 +240,7 @@ fp4_kernel(const __grid_constant__ Params p) {
     int rs = 0, rph = 1, e = 0;
     bool ok = true, waited = false;
     Tile t;
-    for (int it = first; ok && it < p.items && decode(p, it, kRowsPer, W, starts, t, e); it += step) {
+    for (int it = first; ok && it < items && decode(seg, it, kRowsPer, W, starts, t, e); it += step) {
       const int row0 = t.row0 + static_cast<int>(rank) * X;
       for (int ks = ks0; ks < ks1; ks = (ks / C::SUPER + 1) * C::SUPER) {
         if (!(ok = wait_warp(&raw_empty[rs], rph, abort_flag, p.status))) break;
@@ -263,7 +280,7 @@ fp4_kernel(const __grid_constant__ Params p) {
     bool ok = true;
     grid_dependency_wait();   // what it waits for depends on the kernels before
     Tile t;
-    for (int it = first; ok && it < p.items && decode(p, it, kRowsPer, W, starts, t, e); it += step)
+    for (int it = first; ok && it < items && decode(seg, it, kRowsPer, W, starts, t, e); it += step)
       for (int ks = ks0; ks < ks1; ++ks) {
         const int sub = ks % C::SUPER;
         if (ks == ks0 || sub == 0) {
@@ -304,18 +321,16 @@ fp4_kernel(const __grid_constant__ Params p) {
     grid_dependency_wait();
     if (rank == 0) {
       constexpr uint32_t idesc = tc::idesc_fp4<kNv>(P ? 256 : 128, C::N);
-      const bool leader = elect_one();
       const uint64_t wd0 = tc::sdesc_sw128(smem_addr(ring)), xd0 = wd0 + (C::W_BYTES >> 4);
       const uint64_t sd0 = tc::sdesc_scales(smem_addr(scales));
-      int st = 0, ph = 0, ac = 0, aph = 1, e = 0, buf = 0;
+      int st = 0, ph = 0, ac = 0, aph = 1, buf = 0;
       bool ok = true;
-      Tile t;
-      for (int it = first; ok && it < p.items && decode(p, it, kRowsPer, W, starts, t, e); it += step) {
+      for (int it = first; ok && it < items; it += step) {
         if (!(ok = wait_warp(&acc_empty[ac], aph, abort_flag, p.status))) break;
         for (int ks = ks0; ks < ks1; ++ks) {
           if (!(ok = wait_warp(&full[st], ph, abort_flag, p.status))) break;
           tc::fence_after_sync();
-          if (leader) {
+          if (elect_one()) {
             // weights' scales, then the activations': [word][atom][4 columns] each
             const uint32_t sw = tmem + C::ACCS * C::N + buf * C::S_COLS, sx = sw + 4 * C::WORDS * C::AW;
             const uint64_t sd = sd0 + static_cast<uint64_t>((st * C::SSTAGE) >> 4);
@@ -368,20 +383,23 @@ fp4_kernel(const __grid_constant__ Params p) {
           mbar_arrive(&acc_empty[acc]);
       }
     };
-    for (int it = first; ok && it < p.items && decode(p, it, kRowsPer, W, starts, t, e); it += step) {
+    for (int it = first; ok && it < items && decode(seg, it, kRowsPer, W, starts, t, e); it += step) {
       const float alpha = p.w_global != nullptr ? gx * __ldcg(p.w_global + t.expert) : gx;
       if (!(ok = wait_warp(&acc_full[ac], aph, abort_flag, p.status))) break;
       tc::fence_after_sync();
-      const uint32_t ta = tmem + (static_cast<uint32_t>(32 * warp) << 16) + ac * C::N;
+      const int q = warp & 3;
+      const uint32_t ta = tmem + (static_cast<uint32_t>(32 * q) << 16) + ac * C::N;
       if constexpr (kForm != kStream) {
-        const int row0 = t.row0 + static_cast<int>(rank) * X + 32 * warp;
+        constexpr int kCols = C::N / (C::EPI / 4);   // of a warp
+        const int col0 = (warp >> 2) * kCols;
+        const int row0 = t.row0 + static_cast<int>(rank) * X + 32 * q;
         uint4* buf = out_base + warp * 128;
         uint16_t* yp = p.y + static_cast<size_t>(row0) * p.N + t.n0;
 #pragma unroll 1
-        for (int c0 = 0; c0 < C::N; c0 += 32) {
+        for (int c0 = col0; c0 < col0 + kCols; c0 += 32) {
           uint32_t v[32];
           tc::tmem_ld32(ta + c0, v);
-          if (c0 + 32 == C::N) hand_back(ac);
+          if (c0 + 32 == col0 + kCols) hand_back(ac);
           if (t.n0 + c0 >= p.N) continue;
           uint4 o[4];
 #pragma unroll
@@ -438,7 +456,7 @@ fp4_kernel(const __grid_constant__ Params p) {
       cluster_wait();
       int e = 0;
       Tile t;
-      if (decode(p, first, X, W, starts, t, e) && !*abort_flag) {
+      if (decode(seg, first, X, W, starts, t, e) && !*abort_flag) {
         const int n = t.n0 + 4 * lane;
         if (n < p.N) {
           const float alpha = (p.x_global != nullptr ? __ldcg(p.x_global) : 1.f) * (p.w_global != nullptr ? __ldcg(p.w_global) : 1.f);

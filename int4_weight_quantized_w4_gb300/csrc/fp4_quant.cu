@@ -261,6 +261,45 @@ __global__ void __launch_bounds__(kThreads) dequant_fp4_kernel(const uint2* q, c
   }
 }
 
+// Quantized rows copied to their places among the expert-sorted rows: row r of (dst,
+// dst_scale) is row gather[r] of (src, src_scale), codes of K16 chunks of 16 bytes and scales
+// of SW words. A warp per row. The next kernel may start once every kernel before this one is done.
+__global__ void __launch_bounds__(kThreads) gather_fp4_rows_kernel(const uint4* src, const uint32_t* src_scale, int64_t T,
+                                                                   int K16, int SW, const int32_t* gather, int64_t R,
+                                                                   uint4* __restrict__ dst, uint32_t* __restrict__ dst_scale,
+                                                                   unsigned int* status) {
+  const int lane = threadIdx.x & 31;
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // src comes from the kernel before
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (r >= R) return;
+  const int64_t t = __ldcg(gather + r);
+  uint4* d = dst + r * K16;
+  uint32_t* ds = dst_scale + r * SW;
+  if (t < 0 || t >= T) {
+    for (int i = lane; i < K16; i += 32) d[i] = make_uint4(0, 0, 0, 0);
+    for (int i = lane; i < SW; i += 32) ds[i] = 0;
+    if (lane == 0) report(status, W4_ERR_SHAPE);
+    return;
+  }
+  const uint4* s = src + t * K16;
+  const uint32_t* ss = src_scale + t * SW;
+  for (int i0 = 0; i0 < K16; i0 += 128) {
+    uint4 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = i0 + 32 * j + lane;
+      if (i < K16) v[j] = ld_cg_v4(s + i);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = i0 + 32 * j + lane;
+      if (i < K16) d[i] = v[j];
+    }
+  }
+  for (int i = lane; i < SW; i += 32) ds[i] = __ldcg(ss + i);
+}
+
 }  // namespace
 
 bool quant_fp4_fits(int64_t M, int64_t K) {
@@ -271,6 +310,16 @@ cudaError_t launch_quant_fp4(const QuantFp4Args& a, cudaStream_t s) {
   if (a.silu) return a.nv ? launch<true, false, true>(a, s) : launch<false, false, true>(a, s);
   if (a.f16) return a.nv ? launch<true, true, false>(a, s) : launch<false, true, false>(a, s);
   return a.nv ? launch<true, false, false>(a, s) : launch<false, false, false>(a, s);
+}
+
+cudaError_t launch_gather_fp4_rows(const void* src, const void* src_scale, int64_t T, int64_t K, bool nv,
+                                   const int32_t* gather, int64_t R, void* dst, void* dst_scale, unsigned int* status,
+                                   cudaStream_t s) {
+  PdlLaunch pl(static_cast<unsigned>((R + kThreads / 32 - 1) / (kThreads / 32)), kThreads, 0, s);
+  return cudaLaunchKernelEx(&pl.cfg, gather_fp4_rows_kernel, static_cast<const uint4*>(src),
+                            static_cast<const uint32_t*>(src_scale), T, static_cast<int>(K / 32),
+                            static_cast<int>(K / fp4_block(nv) / 4), gather, R, static_cast<uint4*>(dst),
+                            static_cast<uint32_t*>(dst_scale), status);
 }
 
 cudaError_t launch_dequant_fp4(const void* q, const void* scale, const float* global, bool nv, bool f16, int64_t M,

@@ -198,6 +198,11 @@ bool quant_fp4_fits(int64_t M, int64_t K);
 cudaError_t launch_quant_fp4(const QuantFp4Args& a, cudaStream_t s);
 cudaError_t launch_dequant_fp4(const void* q, const void* scale, const float* global, bool nv, bool f16, int64_t M,
                                int64_t K, void* out, cudaStream_t s);
+// Rows gather[r] of quantized (src, src_scale) [T, K], which the kernel launched just before writes, as row r of (dst, dst_scale).
+// K as the products take it (whole words of scales).
+cudaError_t launch_gather_fp4_rows(const void* src, const void* src_scale, int64_t T, int64_t K, bool nv,
+                                   const int32_t* gather, int64_t R, void* dst, void* dst_scale, unsigned int* status,
+                                   cudaStream_t s);
 struct Fp4Args {
   const void *qx, *x_scale;       // e2m1 [R, K/2 bytes] and its scales
   const void *qweight, *w_scale;  // e2m1 [E, N, K/2 bytes] and its scales

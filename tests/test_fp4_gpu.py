@@ -270,3 +270,24 @@ def test_a_chain_without_synchronization_equals_the_calls_with_it(fmt):
         torch.cuda.synchronize()
         qx, sx = w4.w4_quant_fp4(x, fmt)
         check_bf16_output(bits(h), O.fp4_linear(host(qx), host(sx), host(q), host(s), fmt), "chain")
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_tokens_quantized_once_give_the_same_rows(fmt):
+    """Enough rows for the copy of the tokens' codes: as with a workspace that has no room for it."""
+    T, k, E, N, K = 700, 8, 6, 64, 2048
+    xb = act(T, K, seed=1)
+    gx = g_of(fmt, xb)
+    rows = (np.arange(T * k) * 13 % T).astype(np.int32)
+    rows[5], rows[9] = T, -3
+    off = S.offsets_from_counts([T * k // 2, 0, 100, T * k // 2 - 300, 200, 0])
+    qw, sw, _ = weights((E, N, K), fmt)
+    call = lambda **kw: w4.w4_fp4_moe_gemm_bf16in(bf16(xb), to_dev(rows), to_dev(off), to_dev(qw), to_dev(sw), fmt, scalar(gx), **kw)  # noqa: E731
+    y = call()
+    torch.cuda.synchronize()
+    assert w4.w4_device_status() == w4.W4_ERR_SHAPE
+    small = torch.empty(w4.w4_workspace_bytes(w4.W4_OP_FP4_IN, T * k, N, K, O.FP4_BLOCK[fmt]), dtype=torch.uint8, device=dev())
+    z = call(workspace=small)
+    torch.cuda.synchronize()
+    assert w4.w4_device_status() == w4.W4_ERR_SHAPE
+    assert torch.equal(y, z) and (y[[5, 9]] == 0).all()
