@@ -423,22 +423,29 @@ fp4_kernel(const __grid_constant__ Params p) {
         }
       } else {
         const int o = 32 * warp + lane, n = t.n0 + o, valid = t.row_end - t.row0;
-        const float b = p.split == 1 && p.bias != nullptr && n < p.N ? __uint_as_float(static_cast<uint32_t>(p.bias[n]) << 16) : 0.f;
-        float* mine = reinterpret_cast<float*>(ring);   // split: every copy has landed and every MMA is done
-        uint16_t* yp = p.y + static_cast<size_t>(t.row0) * p.N + n;
+        if (p.split > 1) {
+          float* mine = reinterpret_cast<float*>(ring) + o;   // every copy has landed and every MMA is done
 #pragma unroll 1
-        for (int c0 = 0; c0 < C::N; c0 += 16) {
-          if (c0 >= valid) break;
-          uint32_t v[16];
-          tc::tmem_ld16_async(ta + c0, v);
-          tc::tmem_wait_ld(v);
+          for (int c0 = 0; c0 < C::N && c0 < valid; c0 += 16) {
+            uint32_t v[16];
+            tc::tmem_ld16_async(ta + c0, v);
+            tc::tmem_wait_ld(v);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            if (c0 + j >= valid) break;
-            if (p.split > 1)
-              mine[(c0 + j) * 128 + o] = __uint_as_float(v[j]);
-            else if (n < p.N)
-              yp[static_cast<size_t>(c0 + j) * p.N] = static_cast<uint16_t>(f32_to_bf16_bits(fmaf(__uint_as_float(v[j]), alpha, b)));
+            for (int j = 0; j < 16; ++j) mine[(c0 + j) * 128] = __uint_as_float(v[j]);   // past the last token too
+          }
+        } else {
+          const float b = p.bias != nullptr && n < p.N ? __uint_as_float(static_cast<uint32_t>(p.bias[n]) << 16) : 0.f;
+          uint16_t* yp = p.y + static_cast<size_t>(t.row0) * p.N + n;
+#pragma unroll 1
+          for (int c0 = 0; c0 < C::N && c0 < valid; c0 += 16) {
+            uint32_t v[16];
+            tc::tmem_ld16_async(ta + c0, v);
+            tc::tmem_wait_ld(v);
+            if (n < p.N) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j, yp += p.N)
+                if (c0 + j < valid) *yp = static_cast<uint16_t>(f32_to_bf16_bits(fmaf(__uint_as_float(v[j]), alpha, b)));
+            }
           }
         }
         hand_back(ac);
@@ -538,7 +545,7 @@ cudaError_t run(const Fp4Args& a, Params& p, cudaStream_t s) {
   const int64_t slots = static_cast<int64_t>(current_sm_count()) * C::CTAS;
   if (kForm == kStream && a.expert_offsets == nullptr)
     for (int n = kMaxSplit; n > 1 && p.split == 1; --n)
-      if (p.KS >= 2 * n && items <= clusters_held(n, C::CTAS)) p.split = n;
+      if (p.KS >= 2 * n && items <= clusters_held(n, X > 16 ? 1 : C::CTAS)) p.split = n;
   const int64_t grid = p.split > 1 ? items * p.split : (items < slots ? items : slots);
   return start<fp4_kernel<W, X, kNv, kForm>>(p, grid, C::THREADS, C::SMEM, p.split, s);
 }
