@@ -542,7 +542,8 @@ w4_status w4_dequant_fp4(const void* q, const void* scale, int32_t format, const
  *
  * w4_fp4_gemm_bf16in: x [M, K] bf16 or fp16, quantized as w4_quant_fp4 does into the
  * workspace (at least w4_workspace_bytes(W4_OP_FP4_IN, M, N, K, 16 or 32) bytes, 16-byte
- * aligned), then w4_fp4_gemm; y equals the two calls' bit for bit.
+ * aligned; 0 bytes for few rows, where the product quantizes x itself and the
+ * workspace may be NULL), then w4_fp4_gemm; y equals the two calls' bit for bit.
  *
  * w4_fp4_moe_grouped_gemm: the product over expert-sorted rows, as
  * w4afp8_moe_grouped_gemm takes them: rows [offsets[e], offsets[e+1]) of qx [R, K/2] times

@@ -141,7 +141,7 @@ size_t w4_workspace_bytes(int32_t op, int64_t M, int64_t N, int64_t K, int32_t g
   }
   if (op == W4_OP_MOE_DECODE) return N > 0 ? w4::moe_decode_workspace_bytes(M, N, K) : 0;
   if (op == W4_OP_FP4_IN || op == W4_OP_FP4_MOE_IN) {
-    if ((group != 16 && group != 32) || K % group != 0) return 0;
+    if ((group != 16 && group != 32) || K % group != 0 || w4::fp4_fuses(M, op == W4_OP_FP4_MOE_IN)) return 0;
     // the rows, and for experts the tokens they come from when those are at most half as many
     return w4::fp4_workspace_bytes(M, K, group == 16) + (op == W4_OP_FP4_MOE_IN ? w4::fp4_workspace_bytes(M / 2, K, group == 16) : 0);
   }
@@ -670,7 +670,7 @@ static w4_status check_fp4_gemm(int32_t format, const float* x_global, const flo
 }
 
 static w4_status run_fp4(w4::Fp4Args a, void* stream) {
-  if (!a.qx || !a.x_scale || !a.qweight || !a.w_scale || !a.y) return fail(W4_ERR_NULL, "required pointer is NULL");
+  if ((!a.x && (!a.qx || !a.x_scale)) || !a.qweight || !a.w_scale || !a.y) return fail(W4_ERR_NULL, "required pointer is NULL");
   if (!aligned(a.qx, 16) || !aligned(a.qweight, 16) || !aligned(a.y, 16) || !aligned(a.x_scale, 4) || !aligned(a.w_scale, 4) ||
       !aligned(a.expert_offsets, 4) || !aligned(a.bias, 16))
     return fail(W4_ERR_ALIGN, "matrices and the bias must be 16-byte aligned, scales and offsets 4-byte aligned");
@@ -690,6 +690,11 @@ static w4_status run_fp4_act(const void* x, bool f16, int64_t T, const int32_t* 
   if (!aligned(x, 16) || !aligned(rows, 4) || !aligned(a.qweight, 16) || !aligned(a.y, 16) || !aligned(a.w_scale, 4) ||
       !aligned(a.expert_offsets, 4) || !aligned(a.bias, 16))
     return fail(W4_ERR_ALIGN, "matrices and the bias must be 16-byte aligned, scales, rows and offsets 4-byte aligned");
+  if (w4::fp4_fuses(a.R, a.expert_offsets != nullptr)) {   // few rows: the product quantizes, no workspace
+    a.x = x;
+    a.x_f16 = f16;
+    return run_fp4(a, stream);
+  }
   const size_t need = w4::fp4_workspace_bytes(a.R, a.K, a.nv);
   if (ws == nullptr || ws_bytes < need || !aligned(ws, 16))
     return fail(W4_ERR_WORKSPACE, "workspace must be 16-byte aligned and at least %zu bytes (got %zu)", need, ws_bytes);
@@ -720,7 +725,7 @@ w4_status w4_fp4_gemm(const void* qx, const void* x_scale, const float* x_global
   w4_status st = check_fp4_gemm(format, x_global, w_global, M, N, K, 1, false);
   if (st != W4_OK) return st;
   if (M == 0) return ok();
-  return run_fp4({qx, x_scale, qweight, w_scale, format == W4_FMT_NVFP4, x_global, w_global, bias, y, nullptr, 1, M, N, K, nullptr}, stream);
+  return run_fp4({qx, x_scale, qweight, w_scale, format == W4_FMT_NVFP4, x_global, w_global, bias, y, nullptr, 1, M, N, K, nullptr, false, nullptr}, stream);
 }
 
 w4_status w4_fp4_gemm_bf16in(const void* x, int32_t x_dtype, const float* x_global, const void* qweight,
@@ -731,7 +736,7 @@ w4_status w4_fp4_gemm_bf16in(const void* x, int32_t x_dtype, const float* x_glob
   if (x_dtype != W4_BF16 && x_dtype != W4_FP16) return fail(W4_ERR_DTYPE, "x_dtype must be W4_BF16 or W4_FP16");
   if (M == 0) return ok();
   return run_fp4_act(x, x_dtype == W4_FP16, M, nullptr,
-                     {nullptr, nullptr, qweight, w_scale, format == W4_FMT_NVFP4, x_global, w_global, bias, y, nullptr, 1, M, N, K, nullptr},
+                     {nullptr, nullptr, qweight, w_scale, format == W4_FMT_NVFP4, x_global, w_global, bias, y, nullptr, 1, M, N, K, nullptr, false, nullptr},
                      workspace, workspace_bytes, stream);
 }
 
@@ -743,7 +748,7 @@ w4_status w4_fp4_moe_grouped_gemm(const void* qx, const void* x_scale, const flo
   if (st != W4_OK) return st;
   if (R == 0) return ok();
   if (!expert_offsets) return fail(W4_ERR_NULL, "expert_offsets must be non-NULL");
-  return run_fp4({qx, x_scale, qweight, w_scale, format == W4_FMT_NVFP4, x_global, w_global, nullptr, y, expert_offsets, E, R, N, K, nullptr}, stream);
+  return run_fp4({qx, x_scale, qweight, w_scale, format == W4_FMT_NVFP4, x_global, w_global, nullptr, y, expert_offsets, E, R, N, K, nullptr, false, nullptr}, stream);
 }
 
 w4_status w4_fp4_moe_gemm_bf16in(const void* x, int64_t T, const float* x_global, const int32_t* row_token,
@@ -757,7 +762,7 @@ w4_status w4_fp4_moe_gemm_bf16in(const void* x, int64_t T, const float* x_global
   if (R == 0) return ok();
   if (!expert_offsets) return fail(W4_ERR_NULL, "expert_offsets must be non-NULL");
   return run_fp4_act(x, false, T, row_token,
-                     {nullptr, nullptr, qweight, w_scale, format == W4_FMT_NVFP4, x_global, w_global, nullptr, y, expert_offsets, E, R, N, K, nullptr},
+                     {nullptr, nullptr, qweight, w_scale, format == W4_FMT_NVFP4, x_global, w_global, nullptr, y, expert_offsets, E, R, N, K, nullptr, false, nullptr},
                      workspace, workspace_bytes, stream);
 }
 

@@ -29,6 +29,7 @@
 #include <cstring>
 
 #include "common.cuh"
+#include "fp4_codes.cuh"
 #include "launch.h"
 #include "tc.cuh"
 #include "tiles.cuh"
@@ -38,6 +39,9 @@ namespace {
 
 constexpr int kStageK = 256;                  // columns of a stage
 constexpr int kStageBytes = kStageK / 2;
+// Up to this many dense rows the stream form quantizes activations itself: one launch less.
+constexpr int kFuseRows = 8;
+constexpr int kQuantWarps = 4;                // that take the stages in turn
 
 enum Form { kStream, kTile, kPair };
 
@@ -48,6 +52,8 @@ struct Params {
   CUtensorMap tm_ws;
   const uint8_t* x_scale;
   const uint8_t* w_scale;
+  const uint4* x;          // 16-bit activations [rows, K] to quantize, or null
+  bool x_f16, x_wide;      // x_wide: 32-byte aligned
   const float* x_global;   // or null
   const float* w_global;   // [E], or null
   const uint16_t* bias;    // bf16 [N] or null
@@ -74,7 +80,7 @@ W4_DEV void seg_bounds(const Segments& p, int e, int& a, int& b) {
 }
 
 // W: weight rows of a tile, X: tokens of a CTA's tile.
-template <int W, int X, bool kNv, Form kForm>
+template <int W, int X, bool kNv, Form kForm, bool kQuant = false>
 struct Shape {
   static constexpr bool PAIR = kForm == kPair;
   static constexpr int WORDS = kNv ? 4 : 2;                    // 32-bit scale words of a row's stage
@@ -94,7 +100,7 @@ struct Shape {
   static constexpr int USED = ACCS * N + 2 * S_COLS;
   static constexpr int TMEM_COLS = USED <= 128 ? 128 : USED <= 256 ? 256 : 512;
   static constexpr int EPI = PAIR ? 8 : 4;                     // epilogue warps: a quarter of the lanes, a half or all of the columns
-  static constexpr int THREADS = 32 * (EPI + 4 + AW + AX);
+  static constexpr int THREADS = 32 * (EPI + 4 + AW + AX + (kQuant ? kQuantWarps - 2 : 0));   // quantizers for a copying and a transposing warp
   static constexpr int OUT = kForm != kStream ? EPI * 2048 : 0;
   static constexpr int BARS = 2 * STAGES + 2 * RAWS + 2 * ACCS;
   static constexpr int STARTS = (kForm != kStream ? 2 : 1) * (kMaxExperts + 1) + 16;   // words
@@ -104,6 +110,9 @@ struct Shape {
   static_assert(BARS * 8 + 8 <= 256, "barriers");
   static_assert(STAGE % 1024 == 0 && W_BYTES % 1024 == 0, "swizzle atoms");
   static_assert(kForm != kStream || X * 512 <= STAGES * STAGE, "part sums of a cluster fit the ring");
+  // A quantizer sees every fourth phase of a stage's barrier; what it waited for before is at
+  // most one phase back, so that a parity names one phase.
+  static_assert(!kQuant || STAGES >= kQuantWarps, "see above");
 };
 
 // By all lanes: 32 bytes of scales of `rows` rows from byte `at` of the row on, those below
@@ -116,12 +125,13 @@ W4_DEV void copy_scale_words(uint32_t to, const uint8_t* src, int SB, int at, in
   }
 }
 
-template <int W, int X, bool kNv, Form kForm>
-__global__ void __launch_bounds__(Shape<W, X, kNv, kForm>::THREADS, Shape<W, X, kNv, kForm>::CTAS)
+template <int W, int X, bool kNv, Form kForm, bool kQuant = false>
+__global__ void __launch_bounds__(Shape<W, X, kNv, kForm, kQuant>::THREADS, Shape<W, X, kNv, kForm, kQuant>::CTAS)
 fp4_kernel(const __grid_constant__ Params p) {
-  using C = Shape<W, X, kNv, kForm>;
-  // warps; below kMma: epilogue; kTurn ..: a warp per scale atom
-  constexpr int kMma = C::EPI, kLoadW = kMma + 1, kLoadX = kMma + 2, kLoadS = kMma + 3, kTurn = kMma + 4;
+  using C = Shape<W, X, kNv, kForm, kQuant>;
+  // warps; below kMma: epilogue; kTurn ..: one per scale atom
+  constexpr int kMma = C::EPI, kLoadW = kMma + 1, kLoadX = kQuant ? -1 : kMma + 2, kLoadS = kMma + 2 + !kQuant, kTurn = kLoadS + 1;
+  constexpr int kQuant0 = kTurn + C::AW;   // kQuant: in the place of kLoadX and the activations' kTurn
   constexpr bool P = C::PAIR;
   constexpr int kRowsPer = P ? 2 * X : X;
   extern __shared__ uint8_t smem_dyn[];
@@ -146,12 +156,12 @@ fp4_kernel(const __grid_constant__ Params p) {
   const uint32_t rank = P ? cluster_rank() : 0;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
-      mbar_init(&full[i], P ? 1 + 2 * (C::AW + C::AX) : 2 + C::AW + C::AX);   // operands; scale warps
+      mbar_init(&full[i], P ? 1 + 2 * (C::AW + C::AX) : kQuant ? 2 + C::AW : 2 + C::AW + C::AX);   // operands; scale warps
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < C::RAWS; ++i) {
       mbar_init(&raw_full[i], p.tma_scales ? 1 : 32);
-      mbar_init(&raw_empty[i], C::AW + C::AX);
+      mbar_init(&raw_empty[i], kQuant ? C::AW : C::AW + C::AX);
     }
     for (int i = 0; i < C::ACCS; ++i) {
       mbar_init(&acc_full[i], 1);
@@ -170,7 +180,7 @@ fp4_kernel(const __grid_constant__ Params p) {
   if (warp == kLoadX && lane == 0) tc::prefetch_tmap(&p.tm_x);
   if (warp == kLoadS && lane == 0 && p.tma_scales) {
     tc::prefetch_tmap(&p.tm_ws);
-    tc::prefetch_tmap(&p.tm_xs);
+    if (!kQuant) tc::prefetch_tmap(&p.tm_xs);
   }
   Segments seg{p.offsets, p.E, p.rows, p.n_tiles};
   if (p.offsets != nullptr) {
@@ -248,7 +258,7 @@ fp4_kernel(const __grid_constant__ Params p) {
         const int at = ks / C::SUPER * 32;
         if (p.tma_scales) {
           if (elect_one()) {
-            mbar_arrive_expect_tx(&raw_full[rs], 32 * (W + X));
+            mbar_arrive_expect_tx(&raw_full[rs], 32 * (kQuant ? W : W + X));
             tc::tma_load_3d(to, &p.tm_ws, &raw_full[rs], at, t.n0, t.expert);
           }
           __syncwarp();
@@ -258,19 +268,64 @@ fp4_kernel(const __grid_constant__ Params p) {
         if (!waited) grid_dependency_wait();   // the activations' come from the kernel before
         waited = true;
         if (p.tma_scales) {
-          if (elect_one()) tc::tma_load_2d(to + C::RAW_W, &p.tm_xs, &raw_full[rs], at, row0);
+          if (!kQuant && elect_one()) tc::tma_load_2d(to + C::RAW_W, &p.tm_xs, &raw_full[rs], at, row0);
           __syncwarp();
         } else {
-          copy_scale_words(smem_addr(to + C::RAW_W), p.x_scale + static_cast<size_t>(row0 < t.row_end ? row0 : t.row0) * p.SB, p.SB, at, X, t.row_end - row0);
+          if (!kQuant) copy_scale_words(smem_addr(to + C::RAW_W), p.x_scale + static_cast<size_t>(row0 < t.row_end ? row0 : t.row0) * p.SB, p.SB, at, X, t.row_end - row0);
           tc::copy_async_arrive(&raw_full[rs]);
         }
         if (++rs == C::RAWS) rs = 0, rph ^= 1;
       }
     }
+  } else if (kQuant && warp >= kQuant0) {
+    // Quantizer w takes stages w, w + 4, ... of this CTA's sequence: lane l 16 columns, l % 16,
+    // of rows l / 16 + 2 u. The next stage's columns are loaded as soon as this one's are used.
+    if constexpr (kQuant) {
+      const int h = lane >> 4, i = lane & 15, nks = ks1 - ks0;
+      const int total = first < items ? (items - first + step - 1) / step * nks : 0;
+      uint4 x[kFuseRows / 2][2];
+      auto load = [&](int g) {
+        const int c = (ks0 + g % nks) * 16 + i;   // in 16 columns
+#pragma unroll
+        for (int u = 0; u < kFuseRows / 2; ++u) {
+          const int r = h + 2 * u;
+          if (r < p.rows && 16 * c < p.K && g < total)
+            load32(p.x + static_cast<size_t>(r) * (p.K / 8) + 2 * c, p.x_wide, x[u]);
+          else
+            x[u][0] = x[u][1] = make_uint4(0, 0, 0, 0);
+        }
+      };
+      grid_dependency_wait();   // x comes from the kernel before
+      const float gx = kNv && p.x_global != nullptr ? *p.x_global : 1.f;
+      load(warp - kQuant0);
+      for (int g = warp - kQuant0; g < total; g += kQuantWarps) {
+        const int st = g % C::STAGES;
+        if (!wait_warp(&empty[st], ((g / C::STAGES) & 1) ^ 1, abort_flag, p.status)) break;
+        uint8_t* to = ring + st * C::STAGE + C::W_BYTES + (i & 1) * 8;
+        uint8_t* sc = scales + st * C::SSTAGE + C::SW_BYTES;
+#pragma unroll
+        for (int u = 0; u < kFuseRows / 2; ++u) {
+          if (2 * u >= p.rows) break;
+          const int r = h + 2 * u;   // a row past the last one fills a column that is never stored
+          float f[2][8];
+          uint32_t bits = p.x_f16 ? widen16<true>(x[u], f) : widen16<false>(x[u], f);
+          if constexpr (!kNv) bits = max(bits, __shfl_xor_sync(0xFFFFFFFFu, bits, 1));
+          uint2 code;
+          const uint32_t s = block_codes<kNv>(f, bits, gx, code);
+          *reinterpret_cast<uint2*>(to + r * 128 + (((i >> 1) ^ r) << 4)) = code;
+          const int b = kNv ? i : i >> 1;   // byte of the stage's scales
+          if (kNv || (i & 1) == 0) sc[(b >> 2) * 512 + r * 16 + (b & 3)] = static_cast<uint8_t>(s);
+        }
+        load(g + kQuantWarps);
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[st]);
+      }
+    }
   } else if (warp >= kTurn) {
     // Lane l holds the words of rows l, l + 32, l + 64 and l + 96 of this warp's 128.
     const int a = warp - kTurn;
-    const bool is_w = a < C::AW;
+    const bool is_w = kQuant || a < C::AW;
     constexpr int kBlocksX = X < 128 ? (X + 31) / 32 : 4;
     const int blocks = is_w ? 4 : kBlocksX;
     const uint8_t* from = raw + (is_w ? a * 4096 : C::RAW_W + (a - C::AW) * 4096) + lane * 32;
@@ -524,12 +579,12 @@ int64_t row_tiles(const Fp4Args& a, int per) {
   return a.expert_offsets == nullptr ? whole : (a.R < whole + a.E ? a.R : whole + a.E);
 }
 
-template <int W, int X, bool kNv, Form kForm>
+template <int W, int X, bool kNv, Form kForm, bool kQuant = false>
 cudaError_t run(const Fp4Args& a, Params& p, cudaStream_t s) {
-  using C = Shape<W, X, kNv, kForm>;
-  cudaError_t e = encode(&p.tm_x, a.qx, a.K / 2, a.R, 0, X);
+  using C = Shape<W, X, kNv, kForm, kQuant>;
+  cudaError_t e = kQuant ? cudaSuccess : encode(&p.tm_x, a.qx, a.K / 2, a.R, 0, X);
   if (e == cudaSuccess) e = encode(&p.tm_w, a.qweight, a.K / 2, a.N, a.E, C::W_LOAD);
-  if (e == cudaSuccess && p.tma_scales) e = encode(&p.tm_xs, a.x_scale, p.SB, a.R, 0, X, 1, 32);
+  if (e == cudaSuccess && p.tma_scales && !kQuant) e = encode(&p.tm_xs, a.x_scale, p.SB, a.R, 0, X, 1, 32);
   if (e == cudaSuccess && p.tma_scales) e = encode(&p.tm_ws, a.w_scale, p.SB, a.N, a.E, W, 1, 32);
   if (e != cudaSuccess) return e;
   p.n_tiles = static_cast<int>((a.N + W - 1) / W);
@@ -540,20 +595,21 @@ cudaError_t run(const Fp4Args& a, Params& p, cudaStream_t s) {
   if (C::PAIR) {
     const int64_t pairs = clusters_held(2, 1);
     if (pairs < 1) return cudaErrorInvalidConfiguration;
-    return start<fp4_kernel<W, X, kNv, kForm>>(p, 2 * (items < pairs ? items : pairs), C::THREADS, C::SMEM, 2, s);
+    return start<fp4_kernel<W, X, kNv, kForm, kQuant>>(p, 2 * (items < pairs ? items : pairs), C::THREADS, C::SMEM, 2, s);
   }
   const int64_t slots = static_cast<int64_t>(current_sm_count()) * C::CTAS;
   if (kForm == kStream && a.expert_offsets == nullptr)
     for (int n = kMaxSplit; n > 1 && p.split == 1; --n)
       if (p.KS >= 2 * n && items <= clusters_held(n, X > 16 ? 1 : C::CTAS)) p.split = n;
   const int64_t grid = p.split > 1 ? items * p.split : (items < slots ? items : slots);
-  return start<fp4_kernel<W, X, kNv, kForm>>(p, grid, C::THREADS, C::SMEM, p.split, s);
+  return start<fp4_kernel<W, X, kNv, kForm, kQuant>>(p, grid, C::THREADS, C::SMEM, p.split, s);
 }
 
 template <bool kNv>
 cudaError_t launch(const Fp4Args& a, Params& p, cudaStream_t s) {
   const bool experts = a.expert_offsets != nullptr;
   const int64_t rows = (a.R + a.E - 1) / a.E;
+  if (a.x != nullptr) return run<128, 16, kNv, kStream, true>(a, p, s);
   if (rows <= 16) return run<128, 16, kNv, kStream>(a, p, s);
   if (rows <= 32) return run<128, 32, kNv, kStream>(a, p, s);
   if (rows <= 64) return run<128, 64, kNv, kStream>(a, p, s);
@@ -564,9 +620,14 @@ cudaError_t launch(const Fp4Args& a, Params& p, cudaStream_t s) {
 
 }  // namespace
 
+bool fp4_fuses(int64_t R, bool experts) { return !experts && R <= kFuseRows; }
+
 cudaError_t launch_fp4(const Fp4Args& a, cudaStream_t s) {
   Params p;
   memset(&p, 0, sizeof(p));
+  p.x = static_cast<const uint4*>(a.x);
+  p.x_f16 = a.x_f16;
+  p.x_wide = (reinterpret_cast<uintptr_t>(a.x) & 31) == 0;
   p.x_scale = static_cast<const uint8_t*>(a.x_scale);
   p.w_scale = static_cast<const uint8_t*>(a.w_scale);
   p.x_global = a.x_global;

@@ -213,8 +213,12 @@ struct Fp4Args {
   const int32_t* expert_offsets;  // device [E + 1], or null: dense, E = 1
   int32_t E;
   int64_t R, N, K;
+  const void* x;                  // where fp4_fuses: 16-bit activations [R, K] in place of qx and x_scale
+  bool x_f16;
   unsigned int* status;
 };
+// Whether launch_fp4 takes 16-bit activations.
+bool fp4_fuses(int64_t R, bool experts);
 inline int64_t fp4_block(bool nv) { return nv ? 16 : 32; }
 // Quantized rows of the 16-bit-input forms: codes [R, K/2], then scales, each padded to 16 bytes.
 inline size_t fp4_code_bytes(int64_t R, int64_t K) { return (static_cast<size_t>(R) * (K / 2) + 15) / 16 * 16; }
