@@ -30,6 +30,7 @@
 
 #include "common.cuh"
 #include "fp4_codes.cuh"
+#include "fp4_scales.cuh"
 #include "launch.h"
 #include "tc.cuh"
 #include "tiles.cuh"
@@ -37,8 +38,6 @@
 namespace w4 {
 namespace {
 
-constexpr int kStageK = 256;                  // columns of a stage
-constexpr int kStageBytes = kStageK / 2;
 // Up to this many dense rows the stream form quantizes activations itself: one launch less.
 constexpr int kFuseRows = 8;
 constexpr int kQuantWarps = 4;                // that take the stages in turn
@@ -114,16 +113,6 @@ struct Shape {
   // most one phase back, so that a parity names one phase.
   static_assert(!kQuant || STAGES >= kQuantWarps, "see above");
 };
-
-// By all lanes: 32 bytes of scales of `rows` rows from byte `at` of the row on, those below
-// `valid` and SB; zeros elsewhere.
-W4_DEV void copy_scale_words(uint32_t to, const uint8_t* src, int SB, int at, int rows, int valid) {
-  for (int i = threadIdx.x & 31; i < rows * 8; i += 32) {
-    const int r = i >> 3, b = at + 4 * (i & 7);
-    const bool in = r < valid && b < SB;
-    tc::copy4_async(to + i * 4, in ? src + static_cast<size_t>(r) * SB + b : src, in);
-  }
-}
 
 template <int W, int X, bool kNv, Form kForm, bool kQuant = false>
 __global__ void __launch_bounds__(Shape<W, X, kNv, kForm, kQuant>::THREADS, Shape<W, X, kNv, kForm, kQuant>::CTAS)
@@ -342,26 +331,14 @@ fp4_kernel(const __grid_constant__ Params p) {
           if (!(ok = wait_warp(&raw_full[rs], rph, abort_flag, p.status))) break;
         }
         uint32_t v[4][C::WORDS];
-        const uint8_t* f = from + rs * C::RAW + sub * C::WORDS * 4;
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          if constexpr (kNv) {
-            const uint4 x = b < blocks ? *reinterpret_cast<const uint4*>(f + b * 1024) : make_uint4(0, 0, 0, 0);
-            v[b][0] = x.x, v[b][1] = x.y, v[b][2] = x.z, v[b][3] = x.w;
-          } else {
-            const uint2 x = b < blocks ? *reinterpret_cast<const uint2*>(f + b * 1024) : make_uint2(0, 0);
-            v[b][0] = x.x, v[b][1] = x.y;
-          }
-        }
+        load_scale_words<kNv>(from + rs * C::RAW + sub * C::WORDS * 4, blocks, v);
         if (ks == ks1 - 1 || sub == C::SUPER - 1) {
           __syncwarp();
           if (lane == 0) mbar_arrive(&raw_empty[rs]);
           if (++rs == C::RAWS) rs = 0, rph ^= 1;
         }
         if (!(ok = wait_warp(&empty[st], ph, abort_flag, p.status))) break;
-#pragma unroll
-        for (int j = 0; j < C::WORDS; ++j)
-          *reinterpret_cast<uint4*>(to + st * C::SSTAGE + j * pitch) = make_uint4(v[0][j], v[1][j], v[2][j], v[3][j]);
+        store_scale_atoms<kNv>(to + st * C::SSTAGE, pitch, v);
         tc::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {

@@ -32,7 +32,7 @@
 // Every sum has a fixed order: outputs are the same every time.
 #include "common.cuh"
 #include "launch.h"
-#include "route.cuh"
+#include "moe_chosen.cuh"
 #include "tc.cuh"
 #include "tiles.cuh"
 
@@ -46,7 +46,6 @@ constexpr int kPer = kChunkSteps / kGroupWarps;      // a warp's of them
 constexpr int kRows = 32;                            // weight rows of a unit
 constexpr int kBox = kRows * 128;                    // 8 steps of them, 128-byte swizzle: 16-byte chunk c of row r at c ^ r % 8
 constexpr int kSlot = kChunkSteps / 8 * kBox;
-constexpr int kMaxT = kMoeDecodeTokens, kMaxE = kMoeDecodeExperts, kMaxK = kMoeDecodeTopK, kMaxPairs = kMaxT * kMaxK;
 
 struct Params {
   CUtensorMap tm_w;        // up: [2E, I, K/2 bytes] in boxes of 16 rows of two matrices; down: [E, H, K/2 bytes], 32 rows
@@ -98,83 +97,7 @@ W4_DEV void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint3
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// What routing leaves in shared memory, the same in every CTA. Rows of the activations
-// are the chosen pairs by expert, then token.
-struct Routed {
-  uint32_t mask[kMaxE];        // tokens of an expert
-  int32_t ids[kMaxPairs];
-  float wts[kMaxPairs];
-  float weight[kMaxPairs];     // of a row
-  uint8_t token[kMaxPairs];    // of a row
-  int16_t expert[kMaxE];       // the chosen experts in ascending order
-  int16_t first[kMaxE + 1];    // their first rows
-  int32_t part[8];
-  int n;                       // how many
-  int x_exp[kMaxT];            // up: exponent taken out of x_t
-};
-
 W4_DEV void group_sync(int group) { asm volatile("bar.sync %0, %1;" :: "r"(group + 1), "r"(kGroupThreads) : "memory"); }
-
-// All threads. scratch: 16 x 8 x 33 words of shared memory. Warps call also(warp) on the way.
-template <class Also>
-W4_DEV void route_all(const Params& p, Routed& s, uint32_t* scratch, Also also) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int T = static_cast<int>(p.route.T), E = p.route.E, k = p.route.k;
-  for (int e = threadIdx.x; e < kMaxE; e += kThreads) s.mask[e] = 0;
-  __syncthreads();
-  if (warp < T) {
-    MoeRouteArgs a = p.route;
-    a.ids = s.ids;
-    a.wts = s.wts;
-    int mine[2];
-    if (E <= 64) {
-      float v[2];
-      load_logits<2>(a, warp, v);
-      route_token<2>(a, warp, v, scratch + warp * 8 * 33, mine);
-    } else {
-      float v[8];
-      load_logits<8>(a, warp, v);
-      route_token<8>(a, warp, v, scratch + warp * 8 * 33, mine);
-    }
-    if (lane < k) atomicOr(&s.mask[mine[0]], 1u << warp);
-  }
-  also(warp);
-  __syncthreads();
-  // the chosen experts and their first rows: a scan of (rows, experts) over 256 threads
-  int v = 0, inc = 0;
-  if (warp < 8) {
-    const uint32_t m = s.mask[threadIdx.x];
-    v = inc = m != 0 ? (__popc(m) << 16) | 1 : 0;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(kFull, inc, o);
-      if (lane >= o) inc += u;
-    }
-    if (lane == 31) s.part[warp] = inc;
-  }
-  __syncthreads();
-  if (warp < 8) {
-    int before = inc - v;
-    for (int w = 0; w < warp; ++w) before += s.part[w];
-    if (v != 0) {
-      s.expert[before & 0xFFFF] = static_cast<int16_t>(threadIdx.x);
-      s.first[before & 0xFFFF] = static_cast<int16_t>(before >> 16);
-      s.mask[threadIdx.x] |= (before >> 16) << 16;   // first row beside the tokens, for the rows below
-    }
-    if (threadIdx.x == 255) {
-      s.n = (before + v) & 0xFFFF;
-      s.first[s.n] = static_cast<int16_t>((before + v) >> 16);
-    }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < T * k; i += kThreads) {
-    const uint32_t m = s.mask[s.ids[i]];
-    const int t = i / k, r = static_cast<int>(m >> 16) + __popc(m & 0xFFFFu & ((1u << t) - 1u));
-    s.token[r] = static_cast<uint8_t>(t);
-    s.weight[r] = s.wts[i];
-  }
-  __syncthreads();
-}
 
 // x_t as fp16 times a power of two, by one warp; returns the exponent taken out.
 template <int kFmt>
@@ -382,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_decode_kernel(const __grid_co
   if (!kDown) grid_dependency_wait();
   launch_dependents();
   const int x_pitch = 2 * p.H + 64;   // two tokens' pieces lie in different banks
-  route_all(p, r, reinterpret_cast<uint32_t*>(ring), [&](int w) {
+  route_all<kThreads>(p.route, r, reinterpret_cast<uint32_t*>(ring), [&](int w) {
     const int t = T <= 8 ? w - 8 : w;   // by warps that route no token, where there are
     if (!kDown && t >= 0 && t < T) {
       const int e = widen_row<kFmt>(p, t, rest + t * x_pitch);
@@ -666,7 +589,13 @@ bool moe_decode_fits(const MoeDecodeArgs& a) {
   return true;
 }
 
+size_t moe_decode_workspace_bytes(int64_t T, int64_t k, int64_t I) {
+  const size_t halves = static_cast<size_t>(T * k) * static_cast<size_t>(2 * I + I / 8), sums = moe_decode_fp4_workspace_bytes(T, k, I);
+  return ((halves > sums ? halves : sums) + 15) / 16 * 16;
+}
+
 cudaError_t launch_moe_decode(const MoeDecodeArgs& a, cudaStream_t s) {
+  if (moe_decode_fp4_fits(a)) return launch_moe_decode_fp4(a, s);
   if (a.format == W4_FMT_INT4) return run_both<W4_FMT_INT4>(a, s);
   return a.format == W4_FMT_NVFP4 ? run_both<W4_FMT_NVFP4>(a, s) : run_both<W4_FMT_MXFP4>(a, s);
 }

@@ -1,0 +1,695 @@
+// The few-token expert layer on 4-bit floating point weights (mxfp4, nvfp4), on the
+// block-scaled tensor cores: routing, then in two kernels
+//
+//   up:     h = W_gu[e] x_t                         for every chosen (t, e)
+//   down:   a = silu(h_gate) h_up;  y_t = bf16( sum_e w_te W_d[e] a_te ).
+//
+// The chosen experts' weights are nearly all there is to read: they stream through shared
+// memory by TMA and are multiplied as they are (tcgen05 kind::mxf4 and mxf4nvf4, weights on
+// the MMA's 128 rows), so that no thread ever unpacks one. For that the activations have to
+// be 4-bit floats too: 16-bit numbers become sums of kTerms of them, each with its own block
+// scale 2^e,
+//
+//   x = sum_j 2^(e - 3 j) q_j + r,   q_j = e2m1(rest / 2^(e - 3 j)),   e = floor(log2 amax) - 1.
+//
+// With amax in [2, 4) 2^e the rest after a term is at most half a step, 2^(e - 1) = 4 2^(e - 3),
+// so that every term fits the next one's range and adds three bits: |r| <= 2^(e - 13) after
+// five, 2^-14 of the block's largest value. A bf16 number down to 2^-6 of that comes out exactly. The
+// terms are columns of the MMA's other operand, and their products are added in fp32. Terms of
+// up to 16 tokens are 80 columns; with memory as the bound the tensor core has time for them.
+// (e4m3 holds powers of two from 2^-9 to 2^8: a token's largest value is brought to [2^8,
+// 2^9), and what falls below 2^-20 of it is lost.)
+//
+// up: the stages of 256 columns of all (expert, tile of 64 gate and 64 up rows) form one list,
+// of which every CTA takes an equal share; a tile lies in at most kParts shares, and their
+// fp32 sums are added by the down kernel. down: a CTA has 128 outputs and every split-th
+// chosen expert, builds the activations' terms while the weights before are multiplied, and
+// adds the experts' outputs in order; the CTAs of a cluster add theirs by token. Every sum
+// has a fixed order. The down kernel routes for itself and starts its weights while the up
+// kernel still runs.
+#include <cstring>
+
+#include "common.cuh"
+#include "fp4_codes.cuh"
+#include "fp4_scales.cuh"
+#include "launch.h"
+#include "moe_chosen.cuh"
+#include "tc.cuh"
+#include "tiles.cuh"
+
+namespace w4 {
+namespace {
+
+constexpr int kTerms = 5;
+constexpr int kParts = 3;                     // shares that a tile of the up kernel can lie in
+constexpr int kStage = 128 * kStageBytes;     // 128 weight rows
+constexpr int kMaxStages = 6;
+constexpr int kRaw = 128 * 32, kRaws = 2;
+constexpr int kUpThreads = 256, kDownThreads = 384;
+constexpr int kMaxI = 4096;                   // two items of 16 columns a thread of the down kernel
+constexpr int kTmem = 256, kAccCols = 80;     // two accumulators of up to 80 columns, then scales
+
+struct Params {
+  CUtensorMap tm_w;        // up: [2E, I, K/2 bytes] in boxes of 64 rows of two matrices; down: [E, H, K/2 bytes], 128 rows
+  CUtensorMap tm_ws;       // the scales alike, 32 bytes a row
+  MoeRouteArgs route;      // ids and wts unset
+  const uint8_t* w_scale;
+  const float* up_global;  // [E] or null
+  const float* down_global;
+  const uint4* x;          // bf16 [T, H]
+  float* part;             // [kParts][rows][2I]: rows of a tile together, 64 gate and 64 up
+  uint16_t* y;             // bf16 [T, H]
+  int H, I, K, KS, SB;     // of the kernel's weights: columns, stages, scale bytes a row
+  int up_ks, up_ctas;      // the up kernel's stages a tile, and CTAs
+  int NC, rows, stages, split;
+  bool tma_scales;
+  unsigned int* status;
+};
+
+// The up kernel's list of stages: `total` of them, shares for `n` CTAs.
+struct Shares {
+  long long total;
+  int n;
+  W4_DEV Shares(const Params& p, int experts) {
+    const int tiles = experts * (p.I / 64);
+    total = static_cast<long long>(tiles) * p.up_ks;
+    n = min(p.up_ctas, 2 * tiles);   // at least half a tile each: a tile lies in three at most
+  }
+  W4_DEV int start(int c) const { return c >= n ? static_cast<int>(total) : static_cast<int>(total * c / n); }
+  W4_DEV int owner(long long s) const { return static_cast<int>(((s + 1) * n - 1) / total); }
+};
+
+struct Bars {
+  uint64_t full[kMaxStages], empty[kMaxStages], raw_full[kRaws], raw_empty[kRaws];
+  uint64_t acc_full[2], acc_empty[2], b_full[2], b_empty[2];
+  uint32_t tmem;
+  int abort_flag;
+};
+
+// 2^e as an e4m3 or e8m0 code; e4m3: e in [-9, 8].
+template <bool kNv>
+W4_DEV uint32_t power_code(int e) {
+  if constexpr (!kNv) return static_cast<uint32_t>(e + 127);
+  return e >= -6 ? static_cast<uint32_t>(e + 7) << 3 : 1u << (e + 9);
+}
+
+// The terms of 16 values, block maximum `bits`: codes and scale bytes into rows row ..
+// row + kTerms - 1 of the operand. b, bs: the stage's operand and scale atoms; i: which 16 of
+// its 256 columns.
+template <bool kNv>
+W4_DEV void store_terms(float (&f)[2][8], uint32_t bits, uint8_t* b, uint8_t* bs, int row, int i) {
+  constexpr int kMin = kNv ? -9 : -126;
+  int e = max(static_cast<int>(bits >> 23) - 128, kMin);   // floor(log2) - 1
+  const int byte = kNv ? i : i >> 1;
+#pragma unroll
+  for (int j = 0; j < kTerms; ++j) {
+    const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23), neg = -__uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+    uint2 code;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; k += 2) mul2(v[k], v[k + 1], f[h][k], f[h][k + 1], inv);
+      const uint32_t c = e2m1x8(v);
+      (h ? code.y : code.x) = c;
+      if (j + 1 < kTerms) {
+        uint32_t w[4];
+        e2m1x8_to_f16(c, w);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          fma2(f[h][2 * k], f[h][2 * k + 1], neg, half_bits_to_f32(w[k] & 0xFFFFu), half_bits_to_f32(w[k] >> 16));
+      }
+    }
+    const int r = row + j;
+    *reinterpret_cast<uint2*>(b + r * 128 + (((i >> 1) ^ (r & 7)) << 4) + (i & 1) * 8) = code;
+    if (kNv || (i & 1) == 0) bs[(byte >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (byte & 3)] = static_cast<uint8_t>(power_code<kNv>(e));
+    e = max(e - 3, kMin);
+  }
+}
+
+// What brings a maximum (magnitude bits) to [2^8, 2^9), and its inverse; NaN for what is not finite.
+W4_DEV float norm_of(uint32_t bits) {
+  const int e = min(max(static_cast<int>(bits >> 23), 9), 254);
+  return __uint_as_float(static_cast<uint32_t>(min(262 - e, 254)) << 23);   // 2^(8 - (e - 127))
+}
+W4_DEV float inverse_norm_of(uint32_t bits) {
+  if (bits >= kInfBits) return __uint_as_float(0x7FC00000u);
+  return __fdiv_rn(1.f, norm_of(bits));
+}
+
+// Warps that bring weights in: both kernels walk the same way over (expert, first row, stages
+// k0 .. k1) that next() gives.
+template <class Next>
+W4_DEV void load_weights(const Params& p, Bars& bar, uint8_t* ring, Next next, bool late) {
+  int st = 0, ph = 1, mat, row, k0, k1;
+  bool ok = true, waited = !late;
+  while (ok && next(mat, row, k0, k1))
+    for (int ks = k0; ks < k1; ++ks) {
+      if (!waited && ph == 0) {   // the ring is full, and is emptied only after the kernel before
+        grid_dependency_wait();
+        waited = true;
+      }
+      if (!(ok = wait_warp(&bar.empty[st], ph, &bar.abort_flag, p.status))) break;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&bar.full[st], kStage);
+        tc::tma_load_3d(ring + st * kStage, &p.tm_w, &bar.full[st], ks * kStageBytes, row, mat);
+      }
+      __syncwarp();
+      if (++st == p.stages) st = 0, ph ^= 1;
+    }
+}
+template <bool kNv, bool kDown, class Next>
+W4_DEV void load_scales(const Params& p, Bars& bar, uint8_t* raw, Next next, bool late) {
+  constexpr int kSuper = kNv ? 2 : 4;
+  int rs = 0, rph = 1, mat, row, k0, k1;
+  bool ok = true, waited = !late;
+  while (ok && next(mat, row, k0, k1))
+    for (int ks = k0; ks < k1; ks = (ks / kSuper + 1) * kSuper) {
+      if (!waited && rph == 0) {
+        grid_dependency_wait();
+        waited = true;
+      }
+      if (!(ok = wait_warp(&bar.raw_empty[rs], rph, &bar.abort_flag, p.status))) break;
+      uint8_t* to = raw + rs * kRaw;
+      const int at = ks / kSuper * 32;
+      if (p.tma_scales) {
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&bar.raw_full[rs], kRaw);
+          tc::tma_load_3d(to, &p.tm_ws, &bar.raw_full[rs], at, row, mat);
+        }
+        __syncwarp();
+      } else {
+        if constexpr (kDown) {
+          copy_scale_words(smem_addr(to), p.w_scale + (static_cast<size_t>(mat) * p.H + row) * p.SB, p.SB, at, 128, p.H - row);
+        } else {
+          const uint8_t* src = p.w_scale + (static_cast<size_t>(mat) * p.I + row) * p.SB;
+          copy_scale_words(smem_addr(to), src, p.SB, at, 64, 64);
+          copy_scale_words(smem_addr(to) + kRaw / 2, src + static_cast<size_t>(p.I) * p.SB, p.SB, at, 64, 64);
+        }
+        tc::copy_async_arrive(&bar.raw_full[rs]);
+      }
+      if (++rs == kRaws) rs = 0, rph ^= 1;
+    }
+}
+template <bool kNv, class Next>
+W4_DEV void turn_scales(const Params& p, Bars& bar, const uint8_t* raw, uint8_t* atoms, Next next, bool late) {
+  constexpr int kWords = kNv ? 4 : 2, kSuper = 8 / kWords;
+  const int lane = threadIdx.x & 31;
+  int st = 0, ph = 1, rs = 0, rph = 0, mat, row, k0, k1;
+  bool ok = true, waited = !late;
+  while (ok && next(mat, row, k0, k1))
+    for (int ks = k0; ks < k1; ++ks) {
+      const int sub = ks % kSuper;
+      if ((ks == k0 || sub == 0) && !(ok = wait_warp(&bar.raw_full[rs], rph, &bar.abort_flag, p.status))) break;
+      uint32_t v[4][kWords];
+      load_scale_words<kNv>(raw + rs * kRaw + lane * 32 + sub * kWords * 4, 4, v);
+      if (ks == k1 - 1 || sub == kSuper - 1) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.raw_empty[rs]);
+        if (++rs == kRaws) rs = 0, rph ^= 1;
+      }
+      if (!waited && ph == 0) {
+        grid_dependency_wait();
+        waited = true;
+      }
+      if (!(ok = wait_warp(&bar.empty[st], ph, &bar.abort_flag, p.status))) break;
+      store_scale_atoms<kNv>(atoms + st * kWords * 512 + lane * 16, 512, v);
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.full[st]);
+      if (++st == p.stages) st = 0, ph ^= 1;
+    }
+}
+
+// One stage's MMAs: weights of ring slot st on the rows, `cols` columns of operand b.
+template <bool kNv>
+W4_DEV void issue_stage(const Params& p, uint32_t tmem, int acc, int buf, uint32_t ring, uint32_t atoms, uint32_t b,
+                        uint32_t bs, int ks, int cols, bool first) {
+  constexpr int kWords = kNv ? 4 : 2, kCols = 4 * kWords;
+  const uint32_t sw = tmem + 2 * kAccCols + buf * 2 * kCols, sx = sw + kCols;
+  const uint64_t wsd = tc::sdesc_scales(atoms), xsd = tc::sdesc_scales(bs);
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) {
+    tc::copy_scales<false>(sw + 4 * i, wsd + 32 * i);
+    tc::copy_scales<false>(sx + 4 * i, xsd + 32 * i);
+  }
+  const uint64_t wd = tc::sdesc_sw128(ring), xd = tc::sdesc_sw128(b);
+  const uint32_t idesc = tc::idesc_fp4<kNv>(128, 0) | static_cast<uint32_t>(cols >> 3) << 17;
+  const int left = p.K - ks * kStageK;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (64 * j >= left) break;
+    const int word = kNv ? j : j >> 1;
+    const uint32_t id = idesc | (kNv || !(j & 1) ? 0u : (2u << 29) | (2u << 4));
+    tc::mma_fp4<kNv, false>(tmem + acc * kAccCols, wd + 2 * j, xd + 2 * j, id, sw + 4 * word, sx + 4 * word, !first || j > 0 ? 1u : 0u);
+  }
+}
+
+// The sum of a token's terms: columns col .. col + 4 of the accumulator.
+W4_DEV float sum_terms(uint32_t taddr) {
+  uint32_t v[8];
+  tc::tmem_ld8(taddr, v);
+  return ((__uint_as_float(v[0]) + __uint_as_float(v[1])) + (__uint_as_float(v[2]) + __uint_as_float(v[3]))) + __uint_as_float(v[4]);
+}
+
+W4_DEV void init_bars(const Params& p, Bars& bar) {
+  for (int i = 0; i < p.stages; ++i) {
+    mbar_init(&bar.full[i], 2);   // the weights, the transposing warp
+    mbar_init(&bar.empty[i], 1);
+  }
+  for (int i = 0; i < kRaws; ++i) {
+    mbar_init(&bar.raw_full[i], p.tma_scales ? 1 : 32);
+    mbar_init(&bar.raw_empty[i], 1);
+  }
+  for (int i = 0; i < 2; ++i) {
+    mbar_init(&bar.acc_full[i], 1);
+    mbar_init(&bar.acc_empty[i], 4);
+    mbar_init(&bar.b_full[i], 4);
+    mbar_init(&bar.b_empty[i], 1 + 4);
+  }
+  bar.abort_flag = 0;
+  fence_mbar_init();
+}
+
+W4_DEV void finish(Bars& bar, int mma_warp) {
+  if (*const_cast<volatile int*>(&bar.abort_flag)) {   // let copies and MMAs in flight land before the shared memory goes away
+    const uint64_t t0 = tc::globaltimer_ns();
+    while (tc::globaltimer_ns() - t0 < 1000000ull) {
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (static_cast<int>(threadIdx.x >> 5) == mma_warp) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(bar.tmem, kTmem);
+  }
+}
+
+// Shared memory: Bars and Routed, then (1024-byte aligned) the ring, the activations' operand,
+// its scale atoms, the weights' scale atoms and scales as they are in memory.
+constexpr int kHead = (sizeof(Bars) + sizeof(Routed) + 16 + 1023) / 1024 * 1024;
+
+// Warps 0-3 epilogue, 4 MMA issuer and TMEM owner, 5 weights, 6 their scales, 7 their
+// transposition; 0-4 first turn x into terms.
+template <bool kNv>
+__global__ void __launch_bounds__(kUpThreads) up_kernel(const __grid_constant__ Params p) {
+  constexpr int kWords = kNv ? 4 : 2;
+  extern __shared__ uint8_t smem_dyn[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
+  Bars& bar = *reinterpret_cast<Bars*>(smem);
+  Routed& r = *reinterpret_cast<Routed*>(smem + (sizeof(Bars) + 15) / 16 * 16);
+  uint8_t* ring = smem + kHead;
+  uint8_t* b = ring + p.stages * kStage;
+  uint8_t* bs = b + p.KS * p.NC * 128;
+  uint8_t* atoms = bs + p.KS * kWords * 512;
+  uint8_t* raw = atoms + p.stages * kWords * 512;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int T = static_cast<int>(p.route.T);
+  if (threadIdx.x == 0) init_bars(p, bar);
+  if (warp == 4) tc::tmem_alloc(&bar.tmem, kTmem);
+  if (warp == 5 && lane == 0) {
+    tc::prefetch_tmap(&p.tm_w);
+    if (p.tma_scales) tc::prefetch_tmap(&p.tm_ws);
+  }
+  grid_dependency_wait();
+  launch_dependents();
+  route_all<kUpThreads>(p.route, r, reinterpret_cast<uint32_t*>(ring), [&](int w) {
+    for (int t = kUpThreads / 32 - 1 - w; t < T; t += kUpThreads / 32) {   // the largest magnitude of a token
+      const uint4* xr = p.x + static_cast<size_t>(t) * (p.H / 8);
+      uint32_t m = 0;
+      for (int i = lane; i < p.H / 8; i += 32) {
+        const uint4 v = ld_cg_v4(xr + i);
+        m = __vmaxu2(__vmaxu2(m, v.x & 0x7FFF7FFFu), v.y & 0x7FFF7FFFu);
+        m = __vmaxu2(__vmaxu2(m, v.z & 0x7FFF7FFFu), v.w & 0x7FFF7FFFu);
+      }
+      m = __reduce_max_sync(kFull, max(m & 0xFFFFu, m >> 16));
+      if (lane == 0) r.x_exp[t] = static_cast<int>(m << 16);   // as fp32 bits
+    }
+  });
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = bar.tmem;
+  const Shares shares(p, r.n);
+  const int tiles = p.I / 64, s_end = shares.start(blockIdx.x + 1);
+  // a role's walk over this CTA's share
+  auto walk = [&, s = shares.start(blockIdx.x)](int& mat, int& row, int& k0, int& k1) mutable {
+    if (s >= s_end) return false;
+    const int tile = s / p.KS, a = tile / tiles;
+    k0 = s - tile * p.KS;
+    k1 = min(p.KS, k0 + s_end - s);
+    s += k1 - k0;
+    mat = 2 * r.expert[a];
+    row = (tile - a * tiles) * 64;
+    return true;
+  };
+
+  if (warp == 5) {
+    tc::fence_proxy_async_smem();   // the ring held the routing's scratch
+    load_weights(p, bar, ring, walk, false);
+  } else if (warp == 6) {
+    load_scales<kNv, false>(p, bar, raw, walk, false);
+  } else if (warp == 7) {
+    turn_scales<kNv>(p, bar, raw, atoms, walk, false);
+  } else {
+    // x in terms: 16 columns a thread
+    for (int it = threadIdx.x; it < T * (p.H / 16); it += 160) {
+      const int t = it / (p.H / 16), c = it - t * (p.H / 16);
+      const uint4* xr = p.x + static_cast<size_t>(t) * (p.H / 8) + 2 * c;
+      const uint4 v[2] = {ld_cg_v4(xr), ld_cg_v4(xr + 1)};
+      float f[2][8];
+      widen16<false>(v, f);
+      const float norm = norm_of(static_cast<uint32_t>(r.x_exp[t]));
+      uint32_t bits = 0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          f[h][k] *= norm;
+          bits = max(bits, __float_as_uint(f[h][k]) & 0x7FFFFFFFu);
+        }
+      if constexpr (!kNv) bits = max(bits, __shfl_xor_sync(__activemask(), bits, 1));   // pairs of lanes come and go together
+      const int ks = c >> 4;
+      store_terms<kNv>(f, min(bits, 0x43FFFFFFu), b + ks * p.NC * 128, bs + ks * kWords * 512, t * kTerms, c & 15);
+    }
+    tc::fence_proxy_async_smem();
+    asm volatile("bar.sync 1, 160;" ::: "memory");
+    if (warp == 4) {
+      int st = 0, ph = 0, ac = 0, aph = 1, buf = 0, mat, row, k0, k1;
+      bool ok = true;
+      while (ok && walk(mat, row, k0, k1)) {
+        if (!(ok = wait_warp(&bar.acc_empty[ac], aph, &bar.abort_flag, p.status))) break;
+        for (int ks = k0; ks < k1; ++ks) {
+          if (!(ok = wait_warp(&bar.full[st], ph, &bar.abort_flag, p.status))) break;
+          tc::fence_after_sync();
+          if (elect_one()) {
+            issue_stage<kNv>(p, tmem, ac, buf, smem_addr(ring) + st * kStage, smem_addr(atoms) + st * kWords * 512,
+                             smem_addr(b) + ks * p.NC * 128, smem_addr(bs) + ks * kWords * 512, ks, p.NC, ks == k0);
+            tc::commit(&bar.empty[st]);
+            if (ks == k1 - 1) tc::commit(&bar.acc_full[ac]);
+          }
+          __syncwarp();
+          buf ^= 1;
+          if (++st == p.stages) st = 0, ph ^= 1;
+        }
+        if (++ac == 2) ac = 0, aph ^= 1;
+      }
+    } else {
+      const int o = 32 * warp + lane;
+      int ac = 0, aph = 0, mat, row, k0, k1;
+      bool ok = true;
+      int s = shares.start(blockIdx.x);
+      while (ok && walk(mat, row, k0, k1)) {
+        const int tile = s / p.KS, a = tile / tiles, e = mat >> 1;
+        s += k1 - k0;
+        const int part = static_cast<int>(blockIdx.x) - shares.owner(static_cast<long long>(tile) * p.KS);
+        const float g = p.up_global != nullptr ? __ldcg(p.up_global + e) : 1.f;
+        float* out = p.part + (static_cast<size_t>(part) * p.rows + r.first[a]) * (2 * p.I) + 2 * row + o;
+        if (!(ok = wait_warp(&bar.acc_full[ac], aph, &bar.abort_flag, p.status))) break;
+        tc::fence_after_sync();
+        const uint32_t ta = tmem + (static_cast<uint32_t>(32 * warp) << 16) + ac * kAccCols;
+        const int n = r.first[a + 1] - r.first[a];
+        for (int i = 0; i < n; ++i) {
+          const int t = r.token[r.first[a] + i];
+          out[static_cast<size_t>(i) * (2 * p.I)] = sum_terms(ta + t * kTerms) * inverse_norm_of(static_cast<uint32_t>(r.x_exp[t])) * g;
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.acc_empty[ac]);
+        if (++ac == 2) ac = 0, aph ^= 1;
+      }
+    }
+  }
+  __syncwarp();
+  finish(bar, 4);
+}
+
+// Warps as in up_kernel, and 8-11: activations.
+template <bool kNv>
+__global__ void __launch_bounds__(kDownThreads) down_kernel(const __grid_constant__ Params p) {
+  constexpr int kWords = kNv ? 4 : 2;
+  extern __shared__ uint8_t smem_dyn[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
+  Bars& bar = *reinterpret_cast<Bars*>(smem);
+  Routed& r = *reinterpret_cast<Routed*>(smem + (sizeof(Bars) + 15) / 16 * 16);
+  uint8_t* ring = smem + kHead;
+  uint8_t* b = ring + p.stages * kStage;             // two
+  uint8_t* bs = b + 2 * p.KS * p.NC * 128;
+  uint8_t* atoms = bs + 2 * p.KS * kWords * 512;
+  uint8_t* raw = atoms + p.stages * kWords * 512;
+  const int T = static_cast<int>(p.route.T);
+  float* sums = reinterpret_cast<float*>(raw + kRaws * kRaw);   // [T][128]
+  float* b_scale = sums + T * 128;                              // [2][T]
+  uint32_t* maxima = reinterpret_cast<uint32_t*>(b_scale + 2 * kMaxT);   // [2][4]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) init_bars(p, bar);
+  if (warp == 4) tc::tmem_alloc(&bar.tmem, kTmem);
+  if (warp == 5 && lane == 0) {
+    tc::prefetch_tmap(&p.tm_w);
+    if (p.tma_scales) tc::prefetch_tmap(&p.tm_ws);
+  }
+  // the up kernel lets this one go when all before it are done, so the logits are there
+  launch_dependents();
+  route_all<kDownThreads>(p.route, r, reinterpret_cast<uint32_t*>(ring), [](int) {});
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = bar.tmem;
+  const int rank = p.split > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int n0 = static_cast<int>(blockIdx.x) / p.split * 128;
+  auto walk = [&, a = rank](int& mat, int& row, int& k0, int& k1) mutable {
+    if (a >= r.n) return false;
+    mat = r.expert[a];
+    row = n0, k0 = 0, k1 = p.KS;
+    a += p.split;
+    return true;
+  };
+
+  if (warp == 5) {
+    tc::fence_proxy_async_smem();
+    load_weights(p, bar, ring, walk, true);
+  } else if (warp == 6) {
+    load_scales<kNv, true>(p, bar, raw, walk, true);
+  } else if (warp == 7) {
+    turn_scales<kNv>(p, bar, raw, atoms, walk, true);
+  } else if (warp == 4) {
+    grid_dependency_wait();
+    int st = 0, ph = 0, ac = 0, aph = 1, bph = 0, buf = 0;
+    bool ok = true;
+    for (int a = rank; ok && a < r.n; a += p.split) {
+      const int cols = ((r.first[a + 1] - r.first[a]) * kTerms + 15) / 16 * 16;
+      if (!(ok = wait_warp(&bar.acc_empty[ac], aph, &bar.abort_flag, p.status))) break;
+      if (!(ok = wait_warp(&bar.b_full[ac], bph, &bar.abort_flag, p.status))) break;
+      const uint32_t bo = smem_addr(b) + ac * p.KS * p.NC * 128, bso = smem_addr(bs) + ac * p.KS * kWords * 512;
+      for (int ks = 0; ks < p.KS; ++ks) {
+        if (!(ok = wait_warp(&bar.full[st], ph, &bar.abort_flag, p.status))) break;
+        tc::fence_after_sync();
+        if (elect_one()) {
+          issue_stage<kNv>(p, tmem, ac, buf, smem_addr(ring) + st * kStage, smem_addr(atoms) + st * kWords * 512,
+                           bo + ks * p.NC * 128, bso + ks * kWords * 512, ks, cols, ks == 0);
+          tc::commit(&bar.empty[st]);
+          if (ks == p.KS - 1) {
+            tc::commit(&bar.acc_full[ac]);
+            tc::commit(&bar.b_empty[ac]);
+          }
+        }
+        __syncwarp();
+        buf ^= 1;
+        if (++st == p.stages) st = 0, ph ^= 1;
+      }
+      if (++ac == 2) ac = 0, aph ^= 1, bph ^= 1;
+    }
+  } else if (warp >= 8) {
+    // silu(gate) * up of a token's row, 16 columns an item, two items a thread; then its terms
+    grid_dependency_wait();
+    const Shares shares(p, r.n);
+    const int tid = threadIdx.x - 256, tiles = p.I / 64, all = p.I / 16;
+    int buf = 0, ph = 1, turn = 0;
+    bool ok = true;
+    for (int a = rank; a < r.n; a += p.split) {
+      // after a time-out the warps go on without waiting, so that they still meet
+      ok = ok && wait_warp(&bar.b_empty[buf], ph, &bar.abort_flag, p.status);
+      uint8_t* bo = b + buf * p.KS * p.NC * 128;
+      uint8_t* bso = bs + buf * p.KS * kWords * 512;
+      const int n = r.first[a + 1] - r.first[a];
+      for (int t = 0; t < n; ++t) {
+        const size_t at = static_cast<size_t>(r.first[a] + t) * (2 * p.I);
+        float f[2][2][8];
+        uint32_t bits[2] = {0, 0};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int i = tid + 128 * k;
+          if (i < all) {
+            const int tile = i >> 2;
+            const long long s = (static_cast<long long>(a) * tiles + tile) * p.up_ks;
+            const int parts = shares.owner(s + p.up_ks - 1) - shares.owner(s) + 1;
+            const float* h = p.part + at + tile * 128 + (i & 3) * 16;
+#pragma unroll
+            for (int j = 0; j < 16; j += 4) {
+              float4 g = __ldcg(reinterpret_cast<const float4*>(h + j)), u = __ldcg(reinterpret_cast<const float4*>(h + 64 + j));
+              for (int q = 1; q < parts; ++q) {
+                const float* hq = h + static_cast<size_t>(q) * p.rows * (2 * p.I) + j;
+                const float4 g2 = __ldcg(reinterpret_cast<const float4*>(hq)), u2 = __ldcg(reinterpret_cast<const float4*>(hq + 64));
+                g.x += g2.x, g.y += g2.y, g.z += g2.z, g.w += g2.w;
+                u.x += u2.x, u.y += u2.y, u.z += u2.z, u.w += u2.w;
+              }
+              float* to = f[k][j >> 3] + (j & 7);
+              to[0] = __fdividef(g.x, 1.f + __expf(-g.x)) * u.x, to[1] = __fdividef(g.y, 1.f + __expf(-g.y)) * u.y;
+              to[2] = __fdividef(g.z, 1.f + __expf(-g.z)) * u.z, to[3] = __fdividef(g.w, 1.f + __expf(-g.w)) * u.w;
+#pragma unroll
+              for (int c = 0; c < 4; ++c) bits[k] = max(bits[k], __float_as_uint(to[c]) & 0x7FFFFFFFu);
+            }
+          }
+        }
+        // the row's largest magnitude
+        uint32_t m = __reduce_max_sync(kFull, max(bits[0], bits[1]));
+        if (lane == 0) maxima[turn * 4 + warp - 8] = m;
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        m = max(max(maxima[turn * 4], maxima[turn * 4 + 1]), max(maxima[turn * 4 + 2], maxima[turn * 4 + 3]));
+        turn ^= 1;
+        if (tid == 0) b_scale[buf * kMaxT + t] = inverse_norm_of(m);
+        const float norm = norm_of(m);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int i = tid + 128 * k;
+          uint32_t top = __float_as_uint(__uint_as_float(bits[k]) * norm);
+          if constexpr (!kNv) top = max(top, __shfl_xor_sync(kFull, top, 1));
+          if (i < all) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int c = 0; c < 8; ++c) f[k][h][c] *= norm;
+            store_terms<kNv>(f[k], min(top, 0x43FFFFFFu), bo + (i >> 4) * p.NC * 128, bso + (i >> 4) * kWords * 512, t * kTerms, i & 15);
+          }
+        }
+      }
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.b_full[buf]);
+      if (++buf == 2) buf = 0, ph ^= 1;
+    }
+  } else {
+    const int o = 32 * warp + lane;
+    for (int t = 0; t < T; ++t) sums[t * 128 + o] = 0.f;   // this thread's outputs
+    grid_dependency_wait();
+    int ac = 0, aph = 0;
+    bool ok = true;
+    for (int a = rank; ok && a < r.n; a += p.split) {
+      const float g = p.down_global != nullptr ? __ldcg(p.down_global + r.expert[a]) : 1.f;
+      if (!(ok = wait_warp(&bar.acc_full[ac], aph, &bar.abort_flag, p.status))) break;
+      tc::fence_after_sync();
+      const uint32_t ta = tmem + (static_cast<uint32_t>(32 * warp) << 16) + ac * kAccCols;
+      const int first = r.first[a], n = r.first[a + 1] - first;
+      for (int i = 0; i < n; ++i) {
+        float& at = sums[r.token[first + i] * 128 + o];
+        at = fmaf(sum_terms(ta + i * kTerms) * b_scale[ac * kMaxT + i], g * r.weight[first + i], at);
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&bar.acc_empty[ac]);
+        mbar_arrive(&bar.b_empty[ac]);
+      }
+      if (++ac == 2) ac = 0, aph ^= 1;
+    }
+  }
+  __syncwarp();
+  __syncthreads();
+  if (p.split > 1) {
+    cluster_arrive();
+    cluster_wait();
+  }
+  // tokens rank, rank + split, ...: a warp a token, four outputs a lane, the CTAs in order
+  for (int t = rank + warp * p.split; t < T; t += kDownThreads / 32 * p.split) {
+    const uint32_t at = smem_addr(sums + t * 128 + 4 * lane);
+    float4 v[kMaxSplit];
+#pragma unroll
+    for (int k = 0; k < kMaxSplit; ++k)
+      if (k < p.split) v[k] = p.split > 1 ? ld_cluster_f32x4(at, k) : *reinterpret_cast<const float4*>(sums + t * 128 + 4 * lane);
+    float4 s = v[0];
+#pragma unroll
+    for (int k = 1; k < kMaxSplit; ++k)
+      if (k < p.split) s.x += v[k].x, s.y += v[k].y, s.z += v[k].z, s.w += v[k].w;
+    if (n0 + 4 * lane < p.H)
+      *reinterpret_cast<uint2*>(p.y + static_cast<size_t>(t) * p.H + n0 + 4 * lane) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+  }
+  if (p.split > 1) {
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+  }
+  finish(bar, 4);
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+int columns(int64_t T) { return static_cast<int>((T * kTerms + 15) / 16 * 16); }
+int64_t smem_bytes(const MoeDecodeArgs& a, bool down, int stages) {
+  const int words = a.format == W4_FMT_NVFP4 ? 4 : 2;
+  const int64_t ks = ((down ? a.I : a.H) + kStageK - 1) / kStageK;
+  return 1024 + kHead + static_cast<int64_t>(stages) * (kStage + words * 512) + (down ? 2 : 1) * ks * (columns(a.route.T) * 128 + words * 512) +
+         kRaws * kRaw + (down ? a.route.T * 512 + 2 * kMaxT * 4 + 32 : 0);
+}
+
+template <bool kNv>
+cudaError_t run(const MoeDecodeArgs& a, bool down, cudaStream_t s) {
+  Params p;
+  memset(&p, 0, sizeof(p));
+  p.route = a.route;
+  p.K = static_cast<int>(down ? a.I : a.H);
+  p.H = static_cast<int>(a.H);
+  p.I = static_cast<int>(a.I);
+  p.KS = (p.K + kStageK - 1) / kStageK;
+  p.SB = p.K / static_cast<int>(fp4_block(kNv));
+  p.up_ks = static_cast<int>((a.H + kStageK - 1) / kStageK);
+  p.up_ctas = current_sm_count();
+  p.w_scale = static_cast<const uint8_t*>(down ? a.down_scale : a.gate_up_scale);
+  p.up_global = a.gate_up_global;
+  p.down_global = a.down_global;
+  p.x = static_cast<const uint4*>(a.x);
+  p.part = static_cast<float*>(a.workspace);
+  p.y = static_cast<uint16_t*>(a.y);
+  p.NC = columns(a.route.T);
+  p.rows = static_cast<int>(a.route.T) * a.route.k;
+  p.tma_scales = p.SB % 16 == 0;
+  p.status = a.status;
+  const void* w = down ? a.down : a.gate_up;
+  const int64_t rows = down ? a.H : a.I, mats = down ? a.route.E : 2 * a.route.E;
+  const int box = down ? 128 : 64, pair = down ? 1 : 2;
+  cudaError_t e = encode(&p.tm_w, w, p.K / 2, rows, mats, box, pair);
+  if (e == cudaSuccess && p.tma_scales) e = encode(&p.tm_ws, p.w_scale, p.SB, rows, mats, box, pair, 32);
+  if (e != cudaSuccess) return e;
+  for (p.stages = kMaxStages; smem_bytes(a, down, p.stages) > 232448; --p.stages) {
+  }
+  p.split = 1;
+  const int smem = static_cast<int>(smem_bytes(a, down, p.stages));
+  if (!down) return start<up_kernel<kNv>>(p, p.up_ctas, kUpThreads, smem, 1, s);
+  const int64_t slices = (a.H + 127) / 128;
+  for (int n = kMaxSplit; n > 1 && p.split == 1; n /= 2)
+    if (slices * n <= current_sm_count() && n <= p.rows) p.split = n;
+  return start<down_kernel<kNv>>(p, slices * p.split, kDownThreads, smem, p.split, s);
+}
+
+}  // namespace
+
+size_t moe_decode_fp4_workspace_bytes(int64_t T, int64_t k, int64_t I) {
+  return static_cast<size_t>(kParts) * static_cast<size_t>(T * k) * static_cast<size_t>(2 * I) * sizeof(float);
+}
+
+// Whole words of scales a row, room for three stages beside the activations.
+bool moe_decode_fp4_fits(const MoeDecodeArgs& a) {
+  if (a.format == W4_FMT_INT4 || a.I > kMaxI) return false;
+  const int64_t unit = a.format == W4_FMT_NVFP4 ? 64 : 128;
+  return a.H % unit == 0 && a.I % unit == 0 && smem_bytes(a, false, 3) <= 232448 && smem_bytes(a, true, 3) <= 232448;
+}
+
+cudaError_t launch_moe_decode_fp4(const MoeDecodeArgs& a, cudaStream_t s) {
+  const bool nv = a.format == W4_FMT_NVFP4;
+  const cudaError_t e = nv ? run<true>(a, false, s) : run<false>(a, false, s);
+  if (e != cudaSuccess) return e;
+  return nv ? run<true>(a, true, s) : run<false>(a, true, s);
+}
+
+}  // namespace w4

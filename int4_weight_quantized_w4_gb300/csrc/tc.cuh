@@ -292,6 +292,15 @@ W4_DEV void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
       : "r"(taddr) : "memory");
 }
 
+// The same of 8 columns.
+W4_DEV void tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+      : "r"(taddr) : "memory");
+}
+
 // The same load of 16 columns without the wait. tmem_wait_ld, given the
 // registers, makes them usable (its operands keep the uses behind it).
 W4_DEV void tmem_ld16_async(uint32_t taddr, uint32_t (&v)[16]) {
