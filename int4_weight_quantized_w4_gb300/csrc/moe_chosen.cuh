@@ -21,16 +21,24 @@ struct Routed {
   uint8_t token[kMaxPairs];    // of a row
   int16_t expert[kMaxE];       // the chosen experts in ascending order
   int16_t first[kMaxE + 1];    // their first rows
-  int32_t part[8];
   int n;                       // how many
   int x_exp[kMaxT];            // exponent taken out of x_t
 };
 
-// All kThreads (at least 256) threads. scratch: 8 x 33 words of shared memory a warp. Warps
-// call also(warp) on the way.
+template <int kEPL>
+W4_DEV void choose(const MoeRouteArgs& a, int t, Routed& s, uint32_t* scratch) {
+  int mine[2];
+  float v[kEPL];
+  load_logits<kEPL>(a, t, v);
+  route_token<kEPL>(a, t, v, scratch, mine);
+  if (static_cast<int>(threadIdx.x & 31) < a.k) atomicOr(&s.mask[mine[0]], 1u << t);
+}
+
+// All kThreads threads. scratch: 8 x 33 words of shared memory a warp. Warps call also(warp) on
+// the way. Each CTA does this once, with its instructions not in the cache yet, so that loops
+// off the choice itself stay loops.
 template <int kThreads, class Also>
 W4_DEV void route_all(const MoeRouteArgs& route, Routed& s, uint32_t* scratch, Also also) {
-  static_assert(kThreads >= 256, "a thread to an expert");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int T = static_cast<int>(route.T), E = route.E, k = route.k;
   for (int e = threadIdx.x; e < kMaxE; e += kThreads) s.mask[e] = 0;
@@ -39,47 +47,45 @@ W4_DEV void route_all(const MoeRouteArgs& route, Routed& s, uint32_t* scratch, A
     MoeRouteArgs a = route;
     a.ids = s.ids;
     a.wts = s.wts;
-    int mine[2];
-    if (E <= 64) {
-      float v[2];
-      load_logits<2>(a, t, v);
-      route_token<2>(a, t, v, scratch + warp * 8 * 33, mine);
-    } else {
-      float v[8];
-      load_logits<8>(a, t, v);
-      route_token<8>(a, t, v, scratch + warp * 8 * 33, mine);
-    }
-    if (lane < k) atomicOr(&s.mask[mine[0]], 1u << t);
+    if (E <= 64)
+      choose<2>(a, t, s, scratch + warp * 8 * 33);
+    else if (E <= 128)
+      choose<4>(a, t, s, scratch + warp * 8 * 33);
+    else
+      choose<8>(a, t, s, scratch + warp * 8 * 33);
   }
   also(warp);
   __syncthreads();
-  // the chosen experts and their first rows: a scan of (rows, experts) over 256 threads
-  int v = 0, inc = 0;
-  if (warp < 8) {
-    const uint32_t m = s.mask[threadIdx.x];
-    v = inc = m != 0 ? (__popc(m) << 16) | 1 : 0;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(kFull, inc, o);
-      if (lane >= o) inc += u;
+  // the chosen experts and their first rows, 32 experts at a time
+  if (warp == 0) {
+    int n = 0, rows = 0;
+#pragma unroll 1
+    for (int e0 = 0; e0 < E; e0 += 32) {
+      const uint32_t m = s.mask[e0 + lane];
+      const uint32_t some = __ballot_sync(kFull, m != 0);
+      int inc = __popc(m);
+#pragma unroll 1
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(kFull, inc, o);
+        if (lane >= o) inc += u;
+      }
+      const int first = rows + inc - __popc(m);
+      if (m != 0) {
+        const int i = n + __popc(some & ((1u << lane) - 1u));
+        s.expert[i] = static_cast<int16_t>(e0 + lane);
+        s.first[i] = static_cast<int16_t>(first);
+        s.mask[e0 + lane] = m | static_cast<uint32_t>(first) << 16;   // for the rows below
+      }
+      n += __popc(some);
+      rows += __shfl_sync(kFull, inc, 31);
     }
-    if (lane == 31) s.part[warp] = inc;
+    if (lane == 0) {
+      s.n = n;
+      s.first[n] = static_cast<int16_t>(rows);
+    }
   }
   __syncthreads();
-  if (warp < 8) {
-    int before = inc - v;
-    for (int w = 0; w < warp; ++w) before += s.part[w];
-    if (v != 0) {
-      s.expert[before & 0xFFFF] = static_cast<int16_t>(threadIdx.x);
-      s.first[before & 0xFFFF] = static_cast<int16_t>(before >> 16);
-      s.mask[threadIdx.x] |= (before >> 16) << 16;   // first row beside the tokens, for the rows below
-    }
-    if (threadIdx.x == 255) {
-      s.n = (before + v) & 0xFFFF;
-      s.first[s.n] = static_cast<int16_t>((before + v) >> 16);
-    }
-  }
-  __syncthreads();
+#pragma unroll 1
   for (int i = threadIdx.x; i < T * k; i += kThreads) {
     const uint32_t m = s.mask[s.ids[i]];
     const int t = i / k, r = static_cast<int>(m >> 16) + __popc(m & 0xFFFFu & ((1u << t) - 1u));

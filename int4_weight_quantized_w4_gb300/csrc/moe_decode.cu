@@ -329,6 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_decode_kernel(const __grid_co
   {
     const int group = warp / kGroupWarps, w = warp % kGroupWarps, tid = threadIdx.x % kGroupThreads;
     const int g = lane >> 2, q = lane & 3;
+    const uint64_t policy = tc::evict_first_policy();   // weights are read once
     // A whole warp: starts the copies of the group's piece number `count`, its unit's scales
     // with the first piece of the unit.
     auto fill = [&](int count) {
@@ -341,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_decode_kernel(const __grid_co
       if (elect_one()) {
         mbar_arrive_expect_tx(bar, boxes * kBox);
         for (int i = 0; i < boxes; ++i)
-          tc::tma_load_3d(ring + (group * p.slots + slot) * kSlot + i * kBox, &p.tm_w, bar, (s0 + 8 * i) * 16, t.n0, t.mat);
+          tc::tma_load_3d_hint(ring + (group * p.slots + slot) * kSlot + i * kBox, &p.tm_w, bar, (s0 + 8 * i) * 16, t.n0, t.mat, policy);
       }
       __syncwarp();
       if (ch == 0) {

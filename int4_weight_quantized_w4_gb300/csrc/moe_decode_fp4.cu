@@ -7,18 +7,22 @@
 // The chosen experts' weights are nearly all there is to read: they stream through shared
 // memory by TMA and are multiplied as they are (tcgen05 kind::mxf4 and mxf4nvf4, weights on
 // the MMA's 128 rows), so that no thread ever unpacks one. For that the activations have to
-// be 4-bit floats too: 16-bit numbers become sums of kTerms of them, each with its own block
-// scale 2^e,
+// be 4-bit floats too: a number becomes a sum of kTerms of them, the digits of a balanced
+// octal fraction,
 //
-//   x = sum_j 2^(e - 3 j) q_j + r,   q_j = e2m1(rest / 2^(e - 3 j)),   e = floor(log2 amax) - 1.
+//   x = 2^e sum_j d_j 8^-j + r,   d_j in -4 .. 3,
 //
-// With amax in [2, 4) 2^e the rest after a term is at most half a step, 2^(e - 1) = 4 2^(e - 3),
-// so that every term fits the next one's range and adds three bits: |r| <= 2^(e - 13) after
-// five, 2^-14 of the block's largest value. A bf16 number down to 2^-6 of that comes out exactly. The
-// terms are columns of the MMA's other operand, and their products are added in fp32. Terms of
-// up to 16 tokens are 80 columns; with memory as the bound the tensor core has time for them.
-// (e4m3 holds powers of two from 2^-9 to 2^8: a token's largest value is brought to [2^8,
-// 2^9), and what falls below 2^-20 of it is lost.)
+// as e2m1 codes 0, 0.5, 1, 1.5, 2 and their negatives, whose magnitude bits count the halves, with
+// a block scale 2^(e + 1 - 3 j) per digit. e is chosen per block of columns so that the
+// largest magnitude lies in [1.713, 3.427) 2^e, which leaves the first digit within its range,
+// and |r| <= 2^(e - 13), 2^-13 of that magnitude: a bf16 number down to 2^-6 of it comes out
+// exactly. All digits come from one fp32 addition that aligns the number as an integer and
+// adds 4 at every digit, and a few bit operations on eight numbers at a time (the conversion
+// instruction for e2m1 takes some 16 cycles a warp). Digits are columns of the MMA's other
+// operand, and their products are added in fp32. Those of up to 16 tokens are 80 columns; with
+// memory as the bound the tensor core has time for them. (e4m3 holds powers of two from 2^-9
+// to 2^8: a token's largest value is brought to [2^7, 2^8), and what falls below 2^-17 of it
+// is lost.)
 //
 // up: the stages of 256 columns of all (expert, tile of 64 gate and 64 up rows) form one list,
 // of which every CTA takes an equal share; a tile lies in at most kParts shares, and their
@@ -45,8 +49,11 @@ constexpr int kParts = 3;                     // shares that a tile of the up ke
 constexpr int kStage = 128 * kStageBytes;     // 128 weight rows
 constexpr int kMaxStages = 6;
 constexpr int kRaw = 128 * 32, kRaws = 2;
-constexpr int kUpThreads = 256, kDownThreads = 384;
-constexpr int kMaxI = 4096;                   // two items of 16 columns a thread of the down kernel
+constexpr int kThreads = 512;
+constexpr int kActWarps = 8, kActThreads = 32 * kActWarps;
+constexpr int kBlock = 8;                     // tokens of an expert that the down kernel takes at once
+constexpr int kMaxI = 4096;                   // two items of 8 columns a thread of the down kernel's kActWarps
+constexpr int kMaxH = 8192;
 constexpr int kTmem = 256, kAccCols = 80;     // two accumulators of up to 80 columns, then scales
 
 struct Params {
@@ -62,21 +69,21 @@ struct Params {
   int H, I, K, KS, SB;     // of the kernel's weights: columns, stages, scale bytes a row
   int up_ks, up_ctas;      // the up kernel's stages a tile, and CTAs
   int NC, rows, stages, split;
+  int raw;                 // bytes of a slot of scales as they are in memory
   bool tma_scales;
   unsigned int* status;
 };
 
 // The up kernel's list of stages: `total` of them, shares for `n` CTAs.
 struct Shares {
-  long long total;
-  int n;
+  unsigned total, n;   // total n fits 32 bits: at most 256 experts, 64 tiles, 32 stages and n = 256
   W4_DEV Shares(const Params& p, int experts) {
     const int tiles = experts * (p.I / 64);
-    total = static_cast<long long>(tiles) * p.up_ks;
-    n = min(p.up_ctas, 2 * tiles);   // at least half a tile each: a tile lies in three at most
+    total = static_cast<unsigned>(tiles * p.up_ks);
+    n = static_cast<unsigned>(min(p.up_ctas, 2 * tiles));   // at least half a tile each: a tile lies in three at most
   }
-  W4_DEV int start(int c) const { return c >= n ? static_cast<int>(total) : static_cast<int>(total * c / n); }
-  W4_DEV int owner(long long s) const { return static_cast<int>(((s + 1) * n - 1) / total); }
+  W4_DEV int start(unsigned c) const { return static_cast<int>(c >= n ? total : total * c / n); }
+  W4_DEV int owner(int s) const { return static_cast<int>(((static_cast<unsigned>(s) + 1) * n - 1) / total); }
 };
 
 struct Bars {
@@ -93,44 +100,44 @@ W4_DEV uint32_t power_code(int e) {
   return e >= -6 ? static_cast<uint32_t>(e + 7) << 3 : 1u << (e + 9);
 }
 
-// The terms of 16 values, block maximum `bits`: codes and scale bytes into rows row ..
-// row + kTerms - 1 of the operand. b, bs: the stage's operand and scale atoms; i: which 16 of
-// its 256 columns.
+// The digits of 8 values, whose block's largest magnitude has bits `bits`: codes into rows row
+// .. row + kTerms - 1 of the operand, and by the block's first lane the scales. b, bs: the stage's
+// operand and scale atoms; i: which 8 of its 256 columns.
 template <bool kNv>
-W4_DEV void store_terms(float (&f)[2][8], uint32_t bits, uint8_t* b, uint8_t* bs, int row, int i) {
+W4_DEV void store_terms(const float (&f)[8], uint32_t bits, uint8_t* b, uint8_t* bs, int row, int i) {
+  static_assert(kTerms == 5, "digits of 3 bits in 16");
   constexpr int kMin = kNv ? -9 : -126;
-  int e = max(static_cast<int>(bits >> 23) - 128, kMin);   // floor(log2) - 1
-  const int byte = kNv ? i : i >> 1;
+  const int e = max(static_cast<int>((bits + 0x24A000u) >> 23) - 128, -120);   // the next one for mantissas from 1.713 on
+  const float s = __uint_as_float(static_cast<uint32_t>(127 + 12 - e) << 23);   // 8^4 2^-e
+  constexpr float kMagic = 12582912.f + 4.f * (1 + 8 + 64 + 512 + 4096);        // 1.5 2^23 and 4 at every digit
+  uint32_t y[8], w[4];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) y[k] = __float_as_uint(fmaf(f[k], s, kMagic));    // digit j + 4 at bits 3 (4 - j)
+#pragma unroll
+  for (int k = 0; k < 4; ++k) w[k] = prmt(y[k], y[k + 4], 0x5410u);
+  const int blk = kNv ? i >> 1 : i >> 2;   // of the stage's scales
+  const bool first = kNv ? (i & 1) == 0 : (i & 3) == 0;
 #pragma unroll
   for (int j = 0; j < kTerms; ++j) {
-    const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23), neg = -__uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-    uint2 code;
+    const int at = 3 * (4 - j);
+    // the eight digits, 4 more than they are, in nibbles
+    uint32_t z = (w[0] >> at) & 0x00070007u;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float v[8];
-#pragma unroll
-      for (int k = 0; k < 8; k += 2) mul2(v[k], v[k + 1], f[h][k], f[h][k + 1], inv);
-      const uint32_t c = e2m1x8(v);
-      (h ? code.y : code.x) = c;
-      if (j + 1 < kTerms) {
-        uint32_t w[4];
-        e2m1x8_to_f16(c, w);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          fma2(f[h][2 * k], f[h][2 * k + 1], neg, half_bits_to_f32(w[k] & 0xFFFFu), half_bits_to_f32(w[k] >> 16));
-      }
-    }
+    for (int k = 1; k < 4; ++k) z = and_or(at > 4 * k ? w[k] >> (at > 4 * k ? at - 4 * k : 0) : w[k] << (at > 4 * k ? 0 : 4 * k - at), 0x00070007u << (4 * k), z);
+    // to sign and magnitude: below 4, 4 - z is (z & 3 flipped) + 1
+    const uint32_t n = ~z & 0x44444444u, one = n >> 2;
+    const uint32_t code = (((z & 0x33333333u) ^ (one | one << 1)) + one) | n << 1;
     const int r = row + j;
-    *reinterpret_cast<uint2*>(b + r * 128 + (((i >> 1) ^ (r & 7)) << 4) + (i & 1) * 8) = code;
-    if (kNv || (i & 1) == 0) bs[(byte >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (byte & 3)] = static_cast<uint8_t>(power_code<kNv>(e));
-    e = max(e - 3, kMin);
+    *reinterpret_cast<uint32_t*>(b + r * 128 + (((i >> 2) ^ (r & 7)) << 4) + (i & 3) * 4) = code;
+    const int power = e + 1 - 3 * j;
+    if (first) bs[(blk >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (blk & 3)] = static_cast<uint8_t>(power < kMin ? 0 : power_code<kNv>(power));
   }
 }
 
-// What brings a maximum (magnitude bits) to [2^8, 2^9), and its inverse; NaN for what is not finite.
+// What brings a maximum (magnitude bits) to [2^7, 2^8), and its inverse; NaN for what is not finite.
 W4_DEV float norm_of(uint32_t bits) {
-  const int e = min(max(static_cast<int>(bits >> 23), 9), 254);
-  return __uint_as_float(static_cast<uint32_t>(min(262 - e, 254)) << 23);   // 2^(8 - (e - 127))
+  const int e = min(max(static_cast<int>(bits >> 23), 8), 254);
+  return __uint_as_float(static_cast<uint32_t>(min(261 - e, 254)) << 23);   // 2^(7 - (e - 127))
 }
 W4_DEV float inverse_norm_of(uint32_t bits) {
   if (bits >= kInfBits) return __uint_as_float(0x7FC00000u);
@@ -139,8 +146,12 @@ W4_DEV float inverse_norm_of(uint32_t bits) {
 
 // Warps that bring weights in: both kernels walk the same way over (expert, first row, stages
 // k0 .. k1) that next() gives.
+W4_DEV float silu_mul(float g, float u) { return __fdividef(g, 1.f + __expf(-g)) * u; }
+
 template <class Next>
 W4_DEV void load_weights(const Params& p, Bars& bar, uint8_t* ring, Next next, bool late) {
+  // weights are read once, and 200 MB of them would push the kernels' own instructions out of L2
+  const uint64_t policy = tc::evict_first_policy();
   int st = 0, ph = 1, mat, row, k0, k1;
   bool ok = true, waited = !late;
   while (ok && next(mat, row, k0, k1))
@@ -152,40 +163,40 @@ W4_DEV void load_weights(const Params& p, Bars& bar, uint8_t* ring, Next next, b
       if (!(ok = wait_warp(&bar.empty[st], ph, &bar.abort_flag, p.status))) break;
       if (elect_one()) {
         mbar_arrive_expect_tx(&bar.full[st], kStage);
-        tc::tma_load_3d(ring + st * kStage, &p.tm_w, &bar.full[st], ks * kStageBytes, row, mat);
+        tc::tma_load_3d_hint(ring + st * kStage, &p.tm_w, &bar.full[st], ks * kStageBytes, row, mat, policy);
       }
       __syncwarp();
       if (++st == p.stages) st = 0, ph ^= 1;
     }
 }
+// Scales: 32 bytes a row at a time by TMA, or, where a row's are no whole 16 bytes, all of a
+// tile's rows as they lie in memory (p.raw bytes a slot).
 template <bool kNv, bool kDown, class Next>
 W4_DEV void load_scales(const Params& p, Bars& bar, uint8_t* raw, Next next, bool late) {
   constexpr int kSuper = kNv ? 2 : 4;
+  const int lane = threadIdx.x & 31;
   int rs = 0, rph = 1, mat, row, k0, k1;
   bool ok = true, waited = !late;
   while (ok && next(mat, row, k0, k1))
-    for (int ks = k0; ks < k1; ks = (ks / kSuper + 1) * kSuper) {
+    for (int ks = k0; ks < k1; ks = p.tma_scales ? (ks / kSuper + 1) * kSuper : k1) {
       if (!waited && rph == 0) {
         grid_dependency_wait();
         waited = true;
       }
       if (!(ok = wait_warp(&bar.raw_empty[rs], rph, &bar.abort_flag, p.status))) break;
-      uint8_t* to = raw + rs * kRaw;
-      const int at = ks / kSuper * 32;
+      uint8_t* to = raw + rs * p.raw;
       if (p.tma_scales) {
         if (elect_one()) {
           mbar_arrive_expect_tx(&bar.raw_full[rs], kRaw);
-          tc::tma_load_3d(to, &p.tm_ws, &bar.raw_full[rs], at, row, mat);
+          tc::tma_load_3d(to, &p.tm_ws, &bar.raw_full[rs], ks / kSuper * 32, row, mat);
         }
         __syncwarp();
       } else {
-        if constexpr (kDown) {
-          copy_scale_words(smem_addr(to), p.w_scale + (static_cast<size_t>(mat) * p.H + row) * p.SB, p.SB, at, 128, p.H - row);
-        } else {
-          const uint8_t* src = p.w_scale + (static_cast<size_t>(mat) * p.I + row) * p.SB;
-          copy_scale_words(smem_addr(to), src, p.SB, at, 64, 64);
-          copy_scale_words(smem_addr(to) + kRaw / 2, src + static_cast<size_t>(p.I) * p.SB, p.SB, at, 64, 64);
-        }
+        const uint8_t* src = p.w_scale + (static_cast<size_t>(mat) * (kDown ? p.H : p.I) + row) * p.SB;
+        const int half = 64 * p.SB;   // rows come and go in blocks of 64: whole 16 bytes
+        const bool two = !kDown || row + 64 < p.H;
+        for (int i = lane * 16; i < (two ? 2 * half : half); i += 512)
+          tc::copy16_async(smem_addr(to) + i, src + (kDown || i < half ? i : i - half + static_cast<size_t>(p.I) * p.SB));
         tc::copy_async_arrive(&bar.raw_full[rs]);
       }
       if (++rs == kRaws) rs = 0, rph ^= 1;
@@ -200,10 +211,18 @@ W4_DEV void turn_scales(const Params& p, Bars& bar, const uint8_t* raw, uint8_t*
   while (ok && next(mat, row, k0, k1))
     for (int ks = k0; ks < k1; ++ks) {
       const int sub = ks % kSuper;
-      if ((ks == k0 || sub == 0) && !(ok = wait_warp(&bar.raw_full[rs], rph, &bar.abort_flag, p.status))) break;
+      if ((ks == k0 || (p.tma_scales && sub == 0)) && !(ok = wait_warp(&bar.raw_full[rs], rph, &bar.abort_flag, p.status))) break;
       uint32_t v[4][kWords];
-      load_scale_words<kNv>(raw + rs * kRaw + lane * 32 + sub * kWords * 4, 4, v);
-      if (ks == k1 - 1 || sub == kSuper - 1) {
+      if (p.tma_scales) {
+        load_scale_words<kNv>(raw + rs * p.raw + lane * 32 + sub * kWords * 4, 4, v);
+      } else {   // rows of an even number of bytes; past their ends the next rows', which meet no column
+        const uint16_t* f = reinterpret_cast<const uint16_t*>(raw + rs * p.raw + lane * p.SB + ks * kWords * 4);
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+          for (int j = 0; j < kWords; ++j) v[b][j] = f[b * 16 * p.SB + 2 * j] | static_cast<uint32_t>(f[b * 16 * p.SB + 2 * j + 1]) << 16;
+      }
+      if (ks == k1 - 1 || (p.tma_scales && sub == kSuper - 1)) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.raw_empty[rs]);
         if (++rs == kRaws) rs = 0, rph ^= 1;
@@ -264,7 +283,7 @@ W4_DEV void init_bars(const Params& p, Bars& bar) {
   for (int i = 0; i < 2; ++i) {
     mbar_init(&bar.acc_full[i], 1);
     mbar_init(&bar.acc_empty[i], 4);
-    mbar_init(&bar.b_full[i], 4);
+    mbar_init(&bar.b_full[i], kActWarps);
     mbar_init(&bar.b_empty[i], 1 + 4);
   }
   bar.abort_flag = 0;
@@ -290,9 +309,9 @@ W4_DEV void finish(Bars& bar, int mma_warp) {
 constexpr int kHead = (sizeof(Bars) + sizeof(Routed) + 16 + 1023) / 1024 * 1024;
 
 // Warps 0-3 epilogue, 4 MMA issuer and TMEM owner, 5 weights, 6 their scales, 7 their
-// transposition; 0-4 first turn x into terms.
+// transposition; the others turn x into digits.
 template <bool kNv>
-__global__ void __launch_bounds__(kUpThreads) up_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, 2) up_kernel(const __grid_constant__ Params p) {
   constexpr int kWords = kNv ? 4 : 2;
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
@@ -313,8 +332,8 @@ __global__ void __launch_bounds__(kUpThreads) up_kernel(const __grid_constant__ 
   }
   grid_dependency_wait();
   launch_dependents();
-  route_all<kUpThreads>(p.route, r, reinterpret_cast<uint32_t*>(ring), [&](int w) {
-    for (int t = kUpThreads / 32 - 1 - w; t < T; t += kUpThreads / 32) {   // the largest magnitude of a token
+  route_all<kThreads>(p.route, r, reinterpret_cast<uint32_t*>(ring), [&](int w) {
+    for (int t = kThreads / 32 - 1 - w; t < T; t += kThreads / 32) {   // the largest magnitude of a token
       const uint4* xr = p.x + static_cast<size_t>(t) * (p.H / 8);
       uint32_t m = 0;
       for (int i = lane; i < p.H / 8; i += 32) {
@@ -352,28 +371,34 @@ __global__ void __launch_bounds__(kUpThreads) up_kernel(const __grid_constant__ 
   } else if (warp == 7) {
     turn_scales<kNv>(p, bar, raw, atoms, walk, false);
   } else {
-    // x in terms: 16 columns a thread
-    for (int it = threadIdx.x; it < T * (p.H / 16); it += 160) {
-      const int t = it / (p.H / 16), c = it - t * (p.H / 16);
-      const uint4* xr = p.x + static_cast<size_t>(t) * (p.H / 8) + 2 * c;
-      const uint4 v[2] = {ld_cg_v4(xr), ld_cg_v4(xr + 1)};
-      float f[2][8];
-      widen16<false>(v, f);
+    // x in digits: a warp takes a token's stage, 8 columns a lane, the next one's on their way
+    constexpr int kMakerWarps = kThreads / 32 - 3, kMakers = 32 * kMakerWarps;
+    const int units = T * p.KS;
+    auto load = [&](int u) {
+      const int t = u / p.KS, c = (u - t * p.KS) * 32 + lane;
+      return u < units && c < p.H / 8 ? ld_cg_v4(p.x + static_cast<size_t>(t) * (p.H / 8) + c) : make_uint4(0, 0, 0, 0);
+    };
+    int u = warp < 5 ? warp : warp - 3;
+    uint4 next = load(u);
+    for (; u < units; u += kMakerWarps) {
+      const uint4 v = next;
+      next = load(u + kMakerWarps);
+      const int t = u / p.KS, ks = u - t * p.KS;
       const float norm = norm_of(static_cast<uint32_t>(r.x_exp[t]));
+      float f[8];
+      chunk_f32<false>(v, f);
       uint32_t bits = 0;
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          f[h][k] *= norm;
-          bits = max(bits, __float_as_uint(f[h][k]) & 0x7FFFFFFFu);
-        }
-      if constexpr (!kNv) bits = max(bits, __shfl_xor_sync(__activemask(), bits, 1));   // pairs of lanes come and go together
-      const int ks = c >> 4;
-      store_terms<kNv>(f, min(bits, 0x43FFFFFFu), b + ks * p.NC * 128, bs + ks * kWords * 512, t * kTerms, c & 15);
+      for (int k = 0; k < 8; ++k) {
+        f[k] *= norm;
+        bits = max(bits, __float_as_uint(f[k]) & 0x7FFFFFFFu);
+      }
+      bits = max(bits, __shfl_xor_sync(kFull, bits, 1));
+      if constexpr (!kNv) bits = max(bits, __shfl_xor_sync(kFull, bits, 2));
+      store_terms<kNv>(f, min(bits, 0x437FFFFFu), b + ks * p.NC * 128, bs + ks * kWords * 512, t * kTerms, lane);
     }
     tc::fence_proxy_async_smem();
-    asm volatile("bar.sync 1, 160;" ::: "memory");
+    asm volatile("bar.sync 1, %0;" :: "n"(kMakers) : "memory");
     if (warp == 4) {
       int st = 0, ph = 0, ac = 0, aph = 1, buf = 0, mat, row, k0, k1;
       bool ok = true;
@@ -394,7 +419,7 @@ __global__ void __launch_bounds__(kUpThreads) up_kernel(const __grid_constant__ 
         }
         if (++ac == 2) ac = 0, aph ^= 1;
       }
-    } else {
+    } else if (warp < 4) {
       const int o = 32 * warp + lane;
       int ac = 0, aph = 0, mat, row, k0, k1;
       bool ok = true;
@@ -402,7 +427,7 @@ __global__ void __launch_bounds__(kUpThreads) up_kernel(const __grid_constant__ 
       while (ok && walk(mat, row, k0, k1)) {
         const int tile = s / p.KS, a = tile / tiles, e = mat >> 1;
         s += k1 - k0;
-        const int part = static_cast<int>(blockIdx.x) - shares.owner(static_cast<long long>(tile) * p.KS);
+        const int part = static_cast<int>(blockIdx.x) - shares.owner(tile * p.KS);
         const float g = p.up_global != nullptr ? __ldcg(p.up_global + e) : 1.f;
         float* out = p.part + (static_cast<size_t>(part) * p.rows + r.first[a]) * (2 * p.I) + 2 * row + o;
         if (!(ok = wait_warp(&bar.acc_full[ac], aph, &bar.abort_flag, p.status))) break;
@@ -424,9 +449,9 @@ __global__ void __launch_bounds__(kUpThreads) up_kernel(const __grid_constant__ 
   finish(bar, 4);
 }
 
-// Warps as in up_kernel, and 8-11: activations.
+// Warps as in up_kernel, 8-15: activations.
 template <bool kNv>
-__global__ void __launch_bounds__(kDownThreads) down_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, 2) down_kernel(const __grid_constant__ Params p) {
   constexpr int kWords = kNv ? 4 : 2;
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
@@ -438,9 +463,9 @@ __global__ void __launch_bounds__(kDownThreads) down_kernel(const __grid_constan
   uint8_t* atoms = bs + 2 * p.KS * kWords * 512;
   uint8_t* raw = atoms + p.stages * kWords * 512;
   const int T = static_cast<int>(p.route.T);
-  float* sums = reinterpret_cast<float*>(raw + kRaws * kRaw);   // [T][128]
-  float* b_scale = sums + T * 128;                              // [2][T]
-  uint32_t* maxima = reinterpret_cast<uint32_t*>(b_scale + 2 * kMaxT);   // [2][4]
+  float* sums = reinterpret_cast<float*>(raw + kRaws * p.raw);   // [T][128]
+  float* b_scale = sums + T * 128;                              // [2][kBlock]
+  uint32_t* maxima = reinterpret_cast<uint32_t*>(b_scale + 2 * kBlock);   // [2][kActWarps]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) init_bars(p, bar);
   if (warp == 4) tc::tmem_alloc(&bar.tmem, kTmem);
@@ -450,18 +475,20 @@ __global__ void __launch_bounds__(kDownThreads) down_kernel(const __grid_constan
   }
   // the up kernel lets this one go when all before it are done, so the logits are there
   launch_dependents();
-  route_all<kDownThreads>(p.route, r, reinterpret_cast<uint32_t*>(ring), [](int) {});
+  route_all<kThreads>(p.route, r, reinterpret_cast<uint32_t*>(ring), [](int) {});
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = bar.tmem;
   const int rank = p.split > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int n0 = static_cast<int>(blockIdx.x) / p.split * 128;
-  auto walk = [&, a = rank](int& mat, int& row, int& k0, int& k1) mutable {
+  // every split-th chosen expert, its tokens kBlock at a time (the weights once for each)
+  auto blocks = [&](int a) { return (r.first[a + 1] - r.first[a] + kBlock - 1) / kBlock; };
+  auto walk = [&, a = rank, i = 0](int& mat, int& row, int& k0, int& k1) mutable {
     if (a >= r.n) return false;
     mat = r.expert[a];
     row = n0, k0 = 0, k1 = p.KS;
-    a += p.split;
+    if (++i == blocks(a)) i = 0, a += p.split;
     return true;
   };
 
@@ -476,8 +503,8 @@ __global__ void __launch_bounds__(kDownThreads) down_kernel(const __grid_constan
     grid_dependency_wait();
     int st = 0, ph = 0, ac = 0, aph = 1, bph = 0, buf = 0;
     bool ok = true;
-    for (int a = rank; ok && a < r.n; a += p.split) {
-      const int cols = ((r.first[a + 1] - r.first[a]) * kTerms + 15) / 16 * 16;
+    for (int a = rank, i = 0; ok && a < r.n; ++i == blocks(a) ? i = 0, a += p.split : 0) {
+      const int cols = (min(r.first[a + 1] - r.first[a] - i * kBlock, kBlock) * kTerms + 15) / 16 * 16;
       if (!(ok = wait_warp(&bar.acc_empty[ac], aph, &bar.abort_flag, p.status))) break;
       if (!(ok = wait_warp(&bar.b_full[ac], bph, &bar.abort_flag, p.status))) break;
       const uint32_t bo = smem_addr(b) + ac * p.KS * p.NC * 128, bso = smem_addr(bs) + ac * p.KS * kWords * 512;
@@ -500,66 +527,71 @@ __global__ void __launch_bounds__(kDownThreads) down_kernel(const __grid_constan
       if (++ac == 2) ac = 0, aph ^= 1, bph ^= 1;
     }
   } else if (warp >= 8) {
-    // silu(gate) * up of a token's row, 16 columns an item, two items a thread; then its terms
+    // silu(gate) * up of a token's row, 8 columns an item, two items a thread; then its digits
     grid_dependency_wait();
     const Shares shares(p, r.n);
-    const int tid = threadIdx.x - 256, tiles = p.I / 64, all = p.I / 16;
+    const int tid = threadIdx.x - 256, tiles = p.I / 64, all = p.I / 8;
     int buf = 0, ph = 1, turn = 0;
     bool ok = true;
-    for (int a = rank; a < r.n; a += p.split) {
+    for (int a = rank, blk = 0; a < r.n; ++blk == blocks(a) ? blk = 0, a += p.split : 0) {
       // after a time-out the warps go on without waiting, so that they still meet
       ok = ok && wait_warp(&bar.b_empty[buf], ph, &bar.abort_flag, p.status);
       uint8_t* bo = b + buf * p.KS * p.NC * 128;
       uint8_t* bso = bs + buf * p.KS * kWords * 512;
-      const int n = r.first[a + 1] - r.first[a];
+      const int first = r.first[a] + blk * kBlock, n = min(r.first[a + 1] - first, kBlock);
+      // the parts of this thread's columns
+      int parts[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int s = (a * tiles + ((tid + kActThreads * k) >> 3)) * p.up_ks;
+        parts[k] = tid + kActThreads * k < all ? shares.owner(s + p.up_ks - 1) - shares.owner(s) + 1 : 0;
+      }
       for (int t = 0; t < n; ++t) {
-        const size_t at = static_cast<size_t>(r.first[a] + t) * (2 * p.I);
-        float f[2][2][8];
+        const float* row = p.part + static_cast<size_t>(first + t) * (2 * p.I);
+        float f[2][8];
         uint32_t bits[2] = {0, 0};
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const int i = tid + 128 * k;
-          if (i < all) {
-            const int tile = i >> 2;
-            const long long s = (static_cast<long long>(a) * tiles + tile) * p.up_ks;
-            const int parts = shares.owner(s + p.up_ks - 1) - shares.owner(s) + 1;
-            const float* h = p.part + at + tile * 128 + (i & 3) * 16;
+          const int i = tid + kActThreads * k;
+          const float* h = row + (i >> 3) * 128 + (i & 7) * 8;
+          float4 g[2] = {}, u[2] = {};
+          for (int q = 0; q < parts[k]; ++q) {
+            const float* hq = h + static_cast<size_t>(q) * p.rows * (2 * p.I);
+            const float4 g0 = __ldcg(reinterpret_cast<const float4*>(hq)), g1 = __ldcg(reinterpret_cast<const float4*>(hq + 4));
+            const float4 u0 = __ldcg(reinterpret_cast<const float4*>(hq + 64)), u1 = __ldcg(reinterpret_cast<const float4*>(hq + 68));
+            g[0].x += g0.x, g[0].y += g0.y, g[0].z += g0.z, g[0].w += g0.w;
+            g[1].x += g1.x, g[1].y += g1.y, g[1].z += g1.z, g[1].w += g1.w;
+            u[0].x += u0.x, u[0].y += u0.y, u[0].z += u0.z, u[0].w += u0.w;
+            u[1].x += u1.x, u[1].y += u1.y, u[1].z += u1.z, u[1].w += u1.w;
+          }
 #pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-              float4 g = __ldcg(reinterpret_cast<const float4*>(h + j)), u = __ldcg(reinterpret_cast<const float4*>(h + 64 + j));
-              for (int q = 1; q < parts; ++q) {
-                const float* hq = h + static_cast<size_t>(q) * p.rows * (2 * p.I) + j;
-                const float4 g2 = __ldcg(reinterpret_cast<const float4*>(hq)), u2 = __ldcg(reinterpret_cast<const float4*>(hq + 64));
-                g.x += g2.x, g.y += g2.y, g.z += g2.z, g.w += g2.w;
-                u.x += u2.x, u.y += u2.y, u.z += u2.z, u.w += u2.w;
-              }
-              float* to = f[k][j >> 3] + (j & 7);
-              to[0] = __fdividef(g.x, 1.f + __expf(-g.x)) * u.x, to[1] = __fdividef(g.y, 1.f + __expf(-g.y)) * u.y;
-              to[2] = __fdividef(g.z, 1.f + __expf(-g.z)) * u.z, to[3] = __fdividef(g.w, 1.f + __expf(-g.w)) * u.w;
+          for (int j = 0; j < 2; ++j) {
+            float* to = f[k] + 4 * j;
+            to[0] = silu_mul(g[j].x, u[j].x), to[1] = silu_mul(g[j].y, u[j].y);
+            to[2] = silu_mul(g[j].z, u[j].z), to[3] = silu_mul(g[j].w, u[j].w);
 #pragma unroll
-              for (int c = 0; c < 4; ++c) bits[k] = max(bits[k], __float_as_uint(to[c]) & 0x7FFFFFFFu);
-            }
+            for (int c = 0; c < 4; ++c) bits[k] = max(bits[k], __float_as_uint(to[c]) & 0x7FFFFFFFu);
           }
         }
         // the row's largest magnitude
         uint32_t m = __reduce_max_sync(kFull, max(bits[0], bits[1]));
-        if (lane == 0) maxima[turn * 4 + warp - 8] = m;
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        m = max(max(maxima[turn * 4], maxima[turn * 4 + 1]), max(maxima[turn * 4 + 2], maxima[turn * 4 + 3]));
+        if (lane == 0) maxima[turn * kActWarps + warp - 8] = m;
+        asm volatile("bar.sync 1, %0;" :: "n"(kActThreads) : "memory");
+#pragma unroll
+        for (int k = 0; k < kActWarps; ++k) m = max(m, maxima[turn * kActWarps + k]);
         turn ^= 1;
-        if (tid == 0) b_scale[buf * kMaxT + t] = inverse_norm_of(m);
+        if (tid == 0) b_scale[buf * kBlock + t] = inverse_norm_of(m);
         const float norm = norm_of(m);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const int i = tid + 128 * k;
+          const int i = tid + kActThreads * k;
           uint32_t top = __float_as_uint(__uint_as_float(bits[k]) * norm);
-          if constexpr (!kNv) top = max(top, __shfl_xor_sync(kFull, top, 1));
+          top = max(top, __shfl_xor_sync(kFull, top, 1));
+          if constexpr (!kNv) top = max(top, __shfl_xor_sync(kFull, top, 2));
           if (i < all) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int c = 0; c < 8; ++c) f[k][h][c] *= norm;
-            store_terms<kNv>(f[k], min(top, 0x43FFFFFFu), bo + (i >> 4) * p.NC * 128, bso + (i >> 4) * kWords * 512, t * kTerms, i & 15);
+            for (int c = 0; c < 8; ++c) f[k][c] *= norm;
+            store_terms<kNv>(f[k], min(top, 0x437FFFFFu), bo + (i >> 5) * p.NC * 128, bso + (i >> 5) * kWords * 512, t * kTerms, i & 31);
           }
         }
       }
@@ -574,15 +606,15 @@ __global__ void __launch_bounds__(kDownThreads) down_kernel(const __grid_constan
     grid_dependency_wait();
     int ac = 0, aph = 0;
     bool ok = true;
-    for (int a = rank; ok && a < r.n; a += p.split) {
+    for (int a = rank, blk = 0; ok && a < r.n; ++blk == blocks(a) ? blk = 0, a += p.split : 0) {
       const float g = p.down_global != nullptr ? __ldcg(p.down_global + r.expert[a]) : 1.f;
       if (!(ok = wait_warp(&bar.acc_full[ac], aph, &bar.abort_flag, p.status))) break;
       tc::fence_after_sync();
       const uint32_t ta = tmem + (static_cast<uint32_t>(32 * warp) << 16) + ac * kAccCols;
-      const int first = r.first[a], n = r.first[a + 1] - first;
+      const int first = r.first[a] + blk * kBlock, n = min(r.first[a + 1] - first, kBlock);
       for (int i = 0; i < n; ++i) {
         float& at = sums[r.token[first + i] * 128 + o];
-        at = fmaf(sum_terms(ta + i * kTerms) * b_scale[ac * kMaxT + i], g * r.weight[first + i], at);
+        at = fmaf(sum_terms(ta + i * kTerms) * b_scale[ac * kBlock + i], g * r.weight[first + i], at);
       }
       tc::fence_before_sync();
       __syncwarp();
@@ -600,7 +632,7 @@ __global__ void __launch_bounds__(kDownThreads) down_kernel(const __grid_constan
     cluster_wait();
   }
   // tokens rank, rank + split, ...: a warp a token, four outputs a lane, the CTAs in order
-  for (int t = rank + warp * p.split; t < T; t += kDownThreads / 32 * p.split) {
+  for (int t = rank + warp * p.split; t < T; t += kThreads / 32 * p.split) {
     const uint32_t at = smem_addr(sums + t * 128 + 4 * lane);
     float4 v[kMaxSplit];
 #pragma unroll
@@ -625,12 +657,17 @@ __global__ void __launch_bounds__(kDownThreads) down_kernel(const __grid_constan
 // host side
 // ---------------------------------------------------------------------------
 
+// A slot of scales: 32 bytes of 128 rows, or all of theirs and what a read past the last row's end may touch.
+int raw_bytes(const MoeDecodeArgs& a, bool down) {
+  const int64_t SB = (down ? a.I : a.H) / (a.format == W4_FMT_NVFP4 ? 16 : 32);
+  return SB % 16 == 0 ? kRaw : static_cast<int>((128 * SB + 32 + 127) / 128 * 128);
+}
 int columns(int64_t T) { return static_cast<int>((T * kTerms + 15) / 16 * 16); }
 int64_t smem_bytes(const MoeDecodeArgs& a, bool down, int stages) {
   const int words = a.format == W4_FMT_NVFP4 ? 4 : 2;
-  const int64_t ks = ((down ? a.I : a.H) + kStageK - 1) / kStageK;
-  return 1024 + kHead + static_cast<int64_t>(stages) * (kStage + words * 512) + (down ? 2 : 1) * ks * (columns(a.route.T) * 128 + words * 512) +
-         kRaws * kRaw + (down ? a.route.T * 512 + 2 * kMaxT * 4 + 32 : 0);
+  const int64_t ks = ((down ? a.I : a.H) + kStageK - 1) / kStageK, T = down && a.route.T > kBlock ? kBlock : a.route.T;
+  return 1024 + kHead + static_cast<int64_t>(stages) * (kStage + words * 512) + (down ? 2 : 1) * ks * (columns(T) * 128 + words * 512) +
+         kRaws * raw_bytes(a, down) + (down ? a.route.T * 512 + 2 * kBlock * 4 + 2 * kActWarps * 4 : 0);
 }
 
 template <bool kNv>
@@ -644,16 +681,17 @@ cudaError_t run(const MoeDecodeArgs& a, bool down, cudaStream_t s) {
   p.KS = (p.K + kStageK - 1) / kStageK;
   p.SB = p.K / static_cast<int>(fp4_block(kNv));
   p.up_ks = static_cast<int>((a.H + kStageK - 1) / kStageK);
-  p.up_ctas = current_sm_count();
+  p.up_ctas = current_sm_count() < 256 ? current_sm_count() : 256;
   p.w_scale = static_cast<const uint8_t*>(down ? a.down_scale : a.gate_up_scale);
   p.up_global = a.gate_up_global;
   p.down_global = a.down_global;
   p.x = static_cast<const uint4*>(a.x);
   p.part = static_cast<float*>(a.workspace);
   p.y = static_cast<uint16_t*>(a.y);
-  p.NC = columns(a.route.T);
+  p.NC = columns(down && a.route.T > kBlock ? kBlock : a.route.T);
   p.rows = static_cast<int>(a.route.T) * a.route.k;
   p.tma_scales = p.SB % 16 == 0;
+  p.raw = raw_bytes(a, down);
   p.status = a.status;
   const void* w = down ? a.down : a.gate_up;
   const int64_t rows = down ? a.H : a.I, mats = down ? a.route.E : 2 * a.route.E;
@@ -661,15 +699,25 @@ cudaError_t run(const MoeDecodeArgs& a, bool down, cudaStream_t s) {
   cudaError_t e = encode(&p.tm_w, w, p.K / 2, rows, mats, box, pair);
   if (e == cudaSuccess && p.tma_scales) e = encode(&p.tm_ws, p.w_scale, p.SB, rows, mats, box, pair, 32);
   if (e != cudaSuccess) return e;
-  for (p.stages = kMaxStages; smem_bytes(a, down, p.stages) > 232448; --p.stages) {
+  // Where both kernels fit an SM together, the second one's first stages arrive while the
+  // first still runs: the up kernel gets what the down kernel leaves with three stages.
+  const int64_t both = 233472 - 2 * 1024;
+  int up = kMaxStages, dn = kMaxStages;
+  if (smem_bytes(a, false, 3) + smem_bytes(a, true, 3) <= both) {
+    while (smem_bytes(a, false, up) + smem_bytes(a, true, 3) > both) --up;
+    while (smem_bytes(a, false, up) + smem_bytes(a, true, dn) > both) --dn;
+  } else {
+    while (smem_bytes(a, false, up) > 232448) --up;
+    while (smem_bytes(a, true, dn) > 232448) --dn;
   }
+  p.stages = down ? dn : up;
   p.split = 1;
   const int smem = static_cast<int>(smem_bytes(a, down, p.stages));
-  if (!down) return start<up_kernel<kNv>>(p, p.up_ctas, kUpThreads, smem, 1, s);
+  if (!down) return start<up_kernel<kNv>>(p, p.up_ctas, kThreads, smem, 1, s);
   const int64_t slices = (a.H + 127) / 128;
   for (int n = kMaxSplit; n > 1 && p.split == 1; n /= 2)
     if (slices * n <= current_sm_count() && n <= p.rows) p.split = n;
-  return start<down_kernel<kNv>>(p, slices * p.split, kDownThreads, smem, p.split, s);
+  return start<down_kernel<kNv>>(p, slices * p.split, kThreads, smem, p.split, s);
 }
 
 }  // namespace
@@ -678,11 +726,10 @@ size_t moe_decode_fp4_workspace_bytes(int64_t T, int64_t k, int64_t I) {
   return static_cast<size_t>(kParts) * static_cast<size_t>(T * k) * static_cast<size_t>(2 * I) * sizeof(float);
 }
 
-// Whole words of scales a row, room for three stages beside the activations.
+// Room for three stages beside the activations.
 bool moe_decode_fp4_fits(const MoeDecodeArgs& a) {
-  if (a.format == W4_FMT_INT4 || a.I > kMaxI) return false;
-  const int64_t unit = a.format == W4_FMT_NVFP4 ? 64 : 128;
-  return a.H % unit == 0 && a.I % unit == 0 && smem_bytes(a, false, 3) <= 232448 && smem_bytes(a, true, 3) <= 232448;
+  if (a.format == W4_FMT_INT4 || a.I > kMaxI || a.H > kMaxH) return false;
+  return smem_bytes(a, false, 3) <= 232448 && smem_bytes(a, true, 3) <= 232448;
 }
 
 cudaError_t launch_moe_decode_fp4(const MoeDecodeArgs& a, cudaStream_t s) {

@@ -125,6 +125,18 @@ W4_DEV void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "mem
 template <int kPending>
 W4_DEV void copy_async_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(kPending) : "memory"); }
 
+// L2 policy for data that is read once: it makes room before anything else does.
+W4_DEV uint64_t evict_first_policy() {
+  uint64_t p;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+W4_DEV void tma_load_3d_hint(void* smem_dst, const void* tmap, uint64_t* bar, int c0, int c1, int c2, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;"
+      :: "r"(smem_addr(smem_dst)), "l"(tmap), "r"(smem_addr(bar)), "r"(c0), "r"(c1), "r"(c2), "l"(policy) : "memory");
+}
+
 // Contiguous global -> shared copy of `bytes` (a multiple of 16; both
 // addresses 16-byte aligned), completion counted on `bar`.
 W4_DEV void bulk_load(void* smem_dst, const void* src, uint32_t bytes, uint64_t* bar) {
