@@ -69,6 +69,7 @@ struct Params {
   int H, I, K, KS, SB;     // of the kernel's weights: columns, stages, scale bytes a row
   int up_ks, up_ctas;      // the up kernel's stages a tile, and CTAs
   int NC, rows, stages, split;
+  int token_rows;          // up: rows of the operand a digit, 8 or 16
   int raw;                 // bytes of a slot of scales as they are in memory
   bool tma_scales;
   unsigned int* status;
@@ -93,21 +94,21 @@ struct Bars {
   int abort_flag;
 };
 
-// 2^e as an e4m3 or e8m0 code; e4m3: e in [-9, 8].
-template <bool kNv>
-W4_DEV uint32_t power_code(int e) {
-  if constexpr (!kNv) return static_cast<uint32_t>(e + 127);
-  return e >= -6 ? static_cast<uint32_t>(e + 7) << 3 : 1u << (e + 9);
+// Rows of the operand: digit j of token t is row j * rows + t, rows = 8 or 16, so that a token's
+// digits have the same place in the swizzle. Where row r's scale lies in its atom: 16 (r % 32)
+// + 4 (r / 32).
+template <int kRows>
+W4_DEV constexpr int scale_at(int j) {
+  return (j * kRows & 31) * 16 + (j * kRows >> 5) * 4;
 }
 
-// The digits of 8 values, whose block's largest magnitude has bits `bits`: codes into rows row
-// .. row + kTerms - 1 of the operand, and by the block's first lane the scales. b, bs: the stage's
-// operand and scale atoms; i: which 8 of its 256 columns.
-template <bool kNv>
-W4_DEV void store_terms(const float (&f)[8], uint32_t bits, uint8_t* b, uint8_t* bs, int row, int i) {
+// The digits of 8 values of token t, whose block's largest magnitude has bits `bits`: codes, and by
+// the block's first lane the scales. b, bs: the stage's operand and scale atoms; i: which 8 of
+// its 256 columns.
+template <bool kNv, int kRows>
+W4_DEV void store_digits(const float (&f)[8], uint32_t bits, uint8_t* b, uint8_t* bs, int t, int i) {
   static_assert(kTerms == 5, "digits of 3 bits in 16");
-  constexpr int kMin = kNv ? -9 : -126;
-  const int e = max(static_cast<int>((bits + 0x24A000u) >> 23) - 128, -120);   // the next one for mantissas from 1.713 on
+  const int e = max(static_cast<int>((bits + 0x24A000u) >> 23) - 128, -110);   // the next one for mantissas from 1.713 on
   const float s = __uint_as_float(static_cast<uint32_t>(127 + 12 - e) << 23);   // 8^4 2^-e
   constexpr float kMagic = 12582912.f + 4.f * (1 + 8 + 64 + 512 + 4096);        // 1.5 2^23 and 4 at every digit
   uint32_t y[8], w[4];
@@ -115,8 +116,7 @@ W4_DEV void store_terms(const float (&f)[8], uint32_t bits, uint8_t* b, uint8_t*
   for (int k = 0; k < 8; ++k) y[k] = __float_as_uint(fmaf(f[k], s, kMagic));    // digit j + 4 at bits 3 (4 - j)
 #pragma unroll
   for (int k = 0; k < 4; ++k) w[k] = prmt(y[k], y[k + 4], 0x5410u);
-  const int blk = kNv ? i >> 1 : i >> 2;   // of the stage's scales
-  const bool first = kNv ? (i & 1) == 0 : (i & 3) == 0;
+  uint8_t* code_at = b + t * 128 + (((i >> 2) ^ (t & 7)) << 4) + (i & 3) * 4;
 #pragma unroll
   for (int j = 0; j < kTerms; ++j) {
     const int at = 3 * (4 - j);
@@ -126,11 +126,23 @@ W4_DEV void store_terms(const float (&f)[8], uint32_t bits, uint8_t* b, uint8_t*
     for (int k = 1; k < 4; ++k) z = and_or(at > 4 * k ? w[k] >> (at > 4 * k ? at - 4 * k : 0) : w[k] << (at > 4 * k ? 0 : 4 * k - at), 0x00070007u << (4 * k), z);
     // to sign and magnitude: below 4, 4 - z is (z & 3 flipped) + 1
     const uint32_t n = ~z & 0x44444444u, one = n >> 2;
-    const uint32_t code = (((z & 0x33333333u) ^ (one | one << 1)) + one) | n << 1;
-    const int r = row + j;
-    *reinterpret_cast<uint32_t*>(b + r * 128 + (((i >> 2) ^ (r & 7)) << 4) + (i & 3) * 4) = code;
-    const int power = e + 1 - 3 * j;
-    if (first) bs[(blk >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (blk & 3)] = static_cast<uint8_t>(power < kMin ? 0 : power_code<kNv>(power));
+    *reinterpret_cast<uint32_t*>(code_at + j * kRows * 128) = (((z & 0x33333333u) ^ (one | one << 1)) + one) | n << 1;
+  }
+  // scales 2^(e + 1 - 3 j): e4m3 by its conversion, which gives 0 below 2^-10, where the digit is given up
+  uint32_t c[kTerms];
+  if constexpr (kNv) {
+    const float p0 = __uint_as_float(static_cast<uint32_t>(127 + 1 + e) << 23);
+    const uint32_t c01 = e4m3x2_rn(p0, p0 * 0.125f), c23 = e4m3x2_rn(p0 * 0.015625f, p0 * 0.001953125f);
+    c[0] = c01, c[1] = c01 >> 8, c[2] = c23, c[3] = c23 >> 8, c[4] = e4m3x2_rn(p0 * 0.000244140625f, 0.f);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kTerms; ++j) c[j] = static_cast<uint32_t>(127 + 1 + e - 3 * j);   // e >= -110
+  }
+  const int blk = kNv ? i >> 1 : i >> 2;   // of the stage's scales
+  if (kNv ? (i & 1) == 0 : (i & 3) == 0) {
+    uint8_t* to = bs + (blk >> 2) * 512 + t * 16 + (blk & 3);
+#pragma unroll
+    for (int j = 0; j < kTerms; ++j) to[scale_at<kRows>(j)] = static_cast<uint8_t>(c[j]);
   }
 }
 
@@ -264,11 +276,13 @@ W4_DEV void issue_stage(const Params& p, uint32_t tmem, int acc, int buf, uint32
   }
 }
 
-// The sum of a token's terms: columns col .. col + 4 of the accumulator.
-W4_DEV float sum_terms(uint32_t taddr) {
-  uint32_t v[8];
-  tc::tmem_ld8(taddr, v);
-  return ((__uint_as_float(v[0]) + __uint_as_float(v[1])) + (__uint_as_float(v[2]) + __uint_as_float(v[3]))) + __uint_as_float(v[4]);
+// The sum of token t's digits: columns t + `rows` j of the accumulator.
+W4_DEV float sum_digits(uint32_t taddr, int t, int rows) {
+  float v[kTerms];
+#pragma unroll
+  for (int j = 0; j < kTerms; ++j) v[j] = tc::tmem_ld1_async(taddr + t + rows * j);
+  tc::tmem_wait_ld(v);
+  return ((v[0] + v[1]) + (v[2] + v[3])) + v[4];
 }
 
 W4_DEV void init_bars(const Params& p, Bars& bar) {
@@ -310,7 +324,7 @@ constexpr int kHead = (sizeof(Bars) + sizeof(Routed) + 16 + 1023) / 1024 * 1024;
 
 // Warps 0-3 epilogue, 4 MMA issuer and TMEM owner, 5 weights, 6 their scales, 7 their
 // transposition; the others turn x into digits.
-template <bool kNv>
+template <bool kNv, int kRows>
 __global__ void __launch_bounds__(kThreads, 2) up_kernel(const __grid_constant__ Params p) {
   constexpr int kWords = kNv ? 4 : 2;
   extern __shared__ uint8_t smem_dyn[];
@@ -395,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 2) up_kernel(const __grid_constant__
       }
       bits = max(bits, __shfl_xor_sync(kFull, bits, 1));
       if constexpr (!kNv) bits = max(bits, __shfl_xor_sync(kFull, bits, 2));
-      store_terms<kNv>(f, min(bits, 0x437FFFFFu), b + ks * p.NC * 128, bs + ks * kWords * 512, t * kTerms, lane);
+      store_digits<kNv, kRows>(f, min(bits, 0x437FFFFFu), b + ks * p.NC * 128, bs + ks * kWords * 512, t, lane);
     }
     tc::fence_proxy_async_smem();
     asm volatile("bar.sync 1, %0;" :: "n"(kMakers) : "memory");
@@ -436,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 2) up_kernel(const __grid_constant__
         const int n = r.first[a + 1] - r.first[a];
         for (int i = 0; i < n; ++i) {
           const int t = r.token[r.first[a] + i];
-          out[static_cast<size_t>(i) * (2 * p.I)] = sum_terms(ta + t * kTerms) * inverse_norm_of(static_cast<uint32_t>(r.x_exp[t])) * g;
+          out[static_cast<size_t>(i) * (2 * p.I)] = sum_digits(ta, t, p.token_rows) * inverse_norm_of(static_cast<uint32_t>(r.x_exp[t])) * g;
         }
         tc::fence_before_sync();
         __syncwarp();
@@ -504,7 +518,6 @@ __global__ void __launch_bounds__(kThreads, 2) down_kernel(const __grid_constant
     int st = 0, ph = 0, ac = 0, aph = 1, bph = 0, buf = 0;
     bool ok = true;
     for (int a = rank, i = 0; ok && a < r.n; ++i == blocks(a) ? i = 0, a += p.split : 0) {
-      const int cols = (min(r.first[a + 1] - r.first[a] - i * kBlock, kBlock) * kTerms + 15) / 16 * 16;
       if (!(ok = wait_warp(&bar.acc_empty[ac], aph, &bar.abort_flag, p.status))) break;
       if (!(ok = wait_warp(&bar.b_full[ac], bph, &bar.abort_flag, p.status))) break;
       const uint32_t bo = smem_addr(b) + ac * p.KS * p.NC * 128, bso = smem_addr(bs) + ac * p.KS * kWords * 512;
@@ -513,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 2) down_kernel(const __grid_constant
         tc::fence_after_sync();
         if (elect_one()) {
           issue_stage<kNv>(p, tmem, ac, buf, smem_addr(ring) + st * kStage, smem_addr(atoms) + st * kWords * 512,
-                           bo + ks * p.NC * 128, bso + ks * kWords * 512, ks, cols, ks == 0);
+                           bo + ks * p.NC * 128, bso + ks * kWords * 512, ks, p.NC, ks == 0);
           tc::commit(&bar.empty[st]);
           if (ks == p.KS - 1) {
             tc::commit(&bar.acc_full[ac]);
@@ -591,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 2) down_kernel(const __grid_constant
           if (i < all) {
 #pragma unroll
             for (int c = 0; c < 8; ++c) f[k][c] *= norm;
-            store_terms<kNv>(f[k], min(top, 0x437FFFFFu), bo + (i >> 5) * p.NC * 128, bso + (i >> 5) * kWords * 512, t * kTerms, i & 31);
+            store_digits<kNv, kBlock>(f[k], min(top, 0x437FFFFFu), bo + (i >> 5) * p.NC * 128, bso + (i >> 5) * kWords * 512, t, i & 31);
           }
         }
       }
@@ -614,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 2) down_kernel(const __grid_constant
       const int first = r.first[a] + blk * kBlock, n = min(r.first[a + 1] - first, kBlock);
       for (int i = 0; i < n; ++i) {
         float& at = sums[r.token[first + i] * 128 + o];
-        at = fmaf(sum_terms(ta + i * kTerms) * b_scale[ac * kBlock + i], g * r.weight[first + i], at);
+        at = fmaf(sum_digits(ta, i, kBlock) * b_scale[ac * kBlock + i], g * r.weight[first + i], at);
       }
       tc::fence_before_sync();
       __syncwarp();
@@ -662,10 +675,11 @@ int raw_bytes(const MoeDecodeArgs& a, bool down) {
   const int64_t SB = (down ? a.I : a.H) / (a.format == W4_FMT_NVFP4 ? 16 : 32);
   return SB % 16 == 0 ? kRaw : static_cast<int>((128 * SB + 32 + 127) / 128 * 128);
 }
-int columns(int64_t T) { return static_cast<int>((T * kTerms + 15) / 16 * 16); }
+// Columns of a stage's operand: kTerms times 8 or 16 rows, in whole 16.
+int columns(int64_t T) { return T <= 8 ? 48 : 80; }
 int64_t smem_bytes(const MoeDecodeArgs& a, bool down, int stages) {
   const int words = a.format == W4_FMT_NVFP4 ? 4 : 2;
-  const int64_t ks = ((down ? a.I : a.H) + kStageK - 1) / kStageK, T = down && a.route.T > kBlock ? kBlock : a.route.T;
+  const int64_t ks = ((down ? a.I : a.H) + kStageK - 1) / kStageK, T = down ? kBlock : a.route.T;
   return 1024 + kHead + static_cast<int64_t>(stages) * (kStage + words * 512) + (down ? 2 : 1) * ks * (columns(T) * 128 + words * 512) +
          kRaws * raw_bytes(a, down) + (down ? a.route.T * 512 + 2 * kBlock * 4 + 2 * kActWarps * 4 : 0);
 }
@@ -688,7 +702,8 @@ cudaError_t run(const MoeDecodeArgs& a, bool down, cudaStream_t s) {
   p.x = static_cast<const uint4*>(a.x);
   p.part = static_cast<float*>(a.workspace);
   p.y = static_cast<uint16_t*>(a.y);
-  p.NC = columns(down && a.route.T > kBlock ? kBlock : a.route.T);
+  p.NC = columns(down ? kBlock : a.route.T);
+  p.token_rows = a.route.T <= 8 ? 8 : 16;
   p.rows = static_cast<int>(a.route.T) * a.route.k;
   p.tma_scales = p.SB % 16 == 0;
   p.raw = raw_bytes(a, down);
@@ -713,7 +728,7 @@ cudaError_t run(const MoeDecodeArgs& a, bool down, cudaStream_t s) {
   p.stages = down ? dn : up;
   p.split = 1;
   const int smem = static_cast<int>(smem_bytes(a, down, p.stages));
-  if (!down) return start<up_kernel<kNv>>(p, p.up_ctas, kThreads, smem, 1, s);
+  if (!down) return a.route.T <= 8 ? start<up_kernel<kNv, 8>>(p, p.up_ctas, kThreads, smem, 1, s) : start<up_kernel<kNv, 16>>(p, p.up_ctas, kThreads, smem, 1, s);
   const int64_t slices = (a.H + 127) / 128;
   for (int n = kMaxSplit; n > 1 && p.split == 1; n /= 2)
     if (slices * n <= current_sm_count() && n <= p.rows) p.split = n;
