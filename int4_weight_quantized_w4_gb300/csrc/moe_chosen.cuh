@@ -22,7 +22,10 @@ struct Routed {
   int16_t expert[kMaxE];       // the chosen experts in ascending order
   int16_t first[kMaxE + 1];    // their first rows
   int n;                       // how many
-  int x_exp[kMaxT];            // exponent taken out of x_t
+  union {
+    int x_exp[kMaxT];          // exponent taken out of x_t
+    float x_scale[kMaxT];      // or what its numbers are to be multiplied with
+  };
 };
 
 template <int kEPL>
@@ -34,6 +37,13 @@ W4_DEV void choose(const MoeRouteArgs& a, int t, Routed& s, uint32_t* scratch) {
   if (static_cast<int>(threadIdx.x & 31) < a.k) atomicOr(&s.mask[mine[0]], 1u << t);
 }
 
+// Before route_all, and before what it reads is there.
+template <int kThreads>
+W4_DEV void route_prepare(Routed& s) {
+  for (int e = threadIdx.x; e < kMaxE; e += kThreads) s.mask[e] = 0;
+  __syncthreads();
+}
+
 // All kThreads threads. scratch: 8 x 33 words of shared memory a warp. Warps call also(warp) on
 // the way. Each CTA does this once, with its instructions not in the cache yet, so that loops
 // off the choice itself stay loops.
@@ -41,8 +51,6 @@ template <int kThreads, class Also>
 W4_DEV void route_all(const MoeRouteArgs& route, Routed& s, uint32_t* scratch, Also also) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int T = static_cast<int>(route.T), E = route.E, k = route.k;
-  for (int e = threadIdx.x; e < kMaxE; e += kThreads) s.mask[e] = 0;
-  __syncthreads();
   for (int t = warp; t < T; t += kThreads / 32) {
     MoeRouteArgs a = route;
     a.ids = s.ids;

@@ -301,6 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_decode_kernel(const __grid_co
     c.abort_flag = 0;
     fence_mbar_init();
   }
+  route_prepare<kThreads>(r);
   // down: the up kernel lets this one go when all before it are done, so the logits are there
   if (!kDown) grid_dependency_wait();
   launch_dependents();

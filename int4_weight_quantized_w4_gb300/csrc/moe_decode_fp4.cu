@@ -50,9 +50,9 @@ constexpr int kStage = 128 * kStageBytes;     // 128 weight rows
 constexpr int kMaxStages = 6;
 constexpr int kRaw = 128 * 32, kRaws = 2;
 constexpr int kThreads = 512;
-constexpr int kActWarps = 8, kActThreads = 32 * kActWarps;
+constexpr int kTeamWarps = 4, kTeam = 32 * kTeamWarps;   // of two teams
 constexpr int kBlock = 8;                     // tokens of an expert that the down kernel takes at once
-constexpr int kMaxI = 4096;                   // two items of 8 columns a thread of the down kernel's kActWarps
+constexpr int kMaxI = 2 * 8 * kTeam;         // two items of 8 columns a thread of a team
 constexpr int kMaxH = 8192;
 constexpr int kTmem = 256, kAccCols = 80;     // two accumulators of up to 80 columns, then scales
 
@@ -297,7 +297,7 @@ W4_DEV void init_bars(const Params& p, Bars& bar) {
   for (int i = 0; i < 2; ++i) {
     mbar_init(&bar.acc_full[i], 1);
     mbar_init(&bar.acc_empty[i], 4);
-    mbar_init(&bar.b_full[i], kActWarps);
+    mbar_init(&bar.b_full[i], kTeamWarps);
     mbar_init(&bar.b_empty[i], 1 + 4);
   }
   bar.abort_flag = 0;
@@ -323,7 +323,7 @@ W4_DEV void finish(Bars& bar, int mma_warp) {
 constexpr int kHead = (sizeof(Bars) + sizeof(Routed) + 16 + 1023) / 1024 * 1024;
 
 // Warps 0-3 epilogue, 4 MMA issuer and TMEM owner, 5 weights, 6 their scales, 7 their
-// transposition; the others turn x into digits.
+// transposition.
 template <bool kNv, int kRows>
 __global__ void __launch_bounds__(kThreads, 2) up_kernel(const __grid_constant__ Params p) {
   constexpr int kWords = kNv ? 4 : 2;
@@ -344,20 +344,43 @@ __global__ void __launch_bounds__(kThreads, 2) up_kernel(const __grid_constant__
     tc::prefetch_tmap(&p.tm_w);
     if (p.tma_scales) tc::prefetch_tmap(&p.tm_ws);
   }
+  route_prepare<kThreads>(r);
   grid_dependency_wait();
   launch_dependents();
   route_all<kThreads>(p.route, r, reinterpret_cast<uint32_t*>(ring), [&](int w) {
-    for (int t = kThreads / 32 - 1 - w; t < T; t += kThreads / 32) {   // the largest magnitude of a token
-      const uint4* xr = p.x + static_cast<size_t>(t) * (p.H / 8);
-      uint32_t m = 0;
-      for (int i = lane; i < p.H / 8; i += 32) {
-        const uint4 v = ld_cg_v4(xr + i);
-        m = __vmaxu2(__vmaxu2(m, v.x & 0x7FFF7FFFu), v.y & 0x7FFF7FFFu);
-        m = __vmaxu2(__vmaxu2(m, v.z & 0x7FFF7FFFu), v.w & 0x7FFF7FFFu);
-      }
-      m = __reduce_max_sync(kFull, max(m & 0xFFFFu, m >> 16));
-      if (lane == 0) r.x_exp[t] = static_cast<int>(m << 16);   // as fp32 bits
+    // a token's x in digits, by a warp that routes none where there are
+    const int t = T <= 8 ? w - 8 : w;
+    if (t < 0 || t >= T) return;
+    const uint4* xr = p.x + static_cast<size_t>(t) * (p.H / 8);
+    uint32_t m = 0;
+#pragma unroll 4
+    for (int i = lane; i < p.H / 8; i += 32) {
+      const uint4 v = ld_cg_v4(xr + i);
+      m = __vmaxu2(__vmaxu2(m, v.x & 0x7FFF7FFFu), v.y & 0x7FFF7FFFu);
+      m = __vmaxu2(__vmaxu2(m, v.z & 0x7FFF7FFFu), v.w & 0x7FFF7FFFu);
     }
+    m = __reduce_max_sync(kFull, max(m & 0xFFFFu, m >> 16)) << 16;   // as fp32 bits
+    if (lane == 0) r.x_scale[t] = inverse_norm_of(m);
+    const float norm = norm_of(m);
+    uint4 next = lane < p.H / 8 ? ld_cg_v4(xr + lane) : make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+    for (int ks = 0; ks < p.KS; ++ks) {   // a stage, 8 columns a lane, the next one's on their way
+      const uint4 v = next;
+      const int i = (ks + 1) * 32 + lane;
+      next = i < p.H / 8 ? ld_cg_v4(xr + i) : make_uint4(0, 0, 0, 0);
+      float f[8];
+      chunk_f32<false>(v, f);
+      uint32_t bits = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        f[k] *= norm;
+        bits = max(bits, __float_as_uint(f[k]) & 0x7FFFFFFFu);
+      }
+      bits = max(bits, __shfl_xor_sync(kFull, bits, 1));
+      if constexpr (!kNv) bits = max(bits, __shfl_xor_sync(kFull, bits, 2));
+      store_digits<kNv, kRows>(f, min(bits, 0x437FFFFFu), b + ks * p.NC * 128, bs + ks * kWords * 512, t, lane);
+    }
+    tc::fence_proxy_async_smem();
   });
   tc::fence_before_sync();
   __syncthreads();
@@ -385,34 +408,6 @@ __global__ void __launch_bounds__(kThreads, 2) up_kernel(const __grid_constant__
   } else if (warp == 7) {
     turn_scales<kNv>(p, bar, raw, atoms, walk, false);
   } else {
-    // x in digits: a warp takes a token's stage, 8 columns a lane, the next one's on their way
-    constexpr int kMakerWarps = kThreads / 32 - 3, kMakers = 32 * kMakerWarps;
-    const int units = T * p.KS;
-    auto load = [&](int u) {
-      const int t = u / p.KS, c = (u - t * p.KS) * 32 + lane;
-      return u < units && c < p.H / 8 ? ld_cg_v4(p.x + static_cast<size_t>(t) * (p.H / 8) + c) : make_uint4(0, 0, 0, 0);
-    };
-    int u = warp < 5 ? warp : warp - 3;
-    uint4 next = load(u);
-    for (; u < units; u += kMakerWarps) {
-      const uint4 v = next;
-      next = load(u + kMakerWarps);
-      const int t = u / p.KS, ks = u - t * p.KS;
-      const float norm = norm_of(static_cast<uint32_t>(r.x_exp[t]));
-      float f[8];
-      chunk_f32<false>(v, f);
-      uint32_t bits = 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        f[k] *= norm;
-        bits = max(bits, __float_as_uint(f[k]) & 0x7FFFFFFFu);
-      }
-      bits = max(bits, __shfl_xor_sync(kFull, bits, 1));
-      if constexpr (!kNv) bits = max(bits, __shfl_xor_sync(kFull, bits, 2));
-      store_digits<kNv, kRows>(f, min(bits, 0x437FFFFFu), b + ks * p.NC * 128, bs + ks * kWords * 512, t, lane);
-    }
-    tc::fence_proxy_async_smem();
-    asm volatile("bar.sync 1, %0;" :: "n"(kMakers) : "memory");
     if (warp == 4) {
       int st = 0, ph = 0, ac = 0, aph = 1, buf = 0, mat, row, k0, k1;
       bool ok = true;
@@ -450,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 2) up_kernel(const __grid_constant__
         const int n = r.first[a + 1] - r.first[a];
         for (int i = 0; i < n; ++i) {
           const int t = r.token[r.first[a] + i];
-          out[static_cast<size_t>(i) * (2 * p.I)] = sum_digits(ta, t, p.token_rows) * inverse_norm_of(static_cast<uint32_t>(r.x_exp[t])) * g;
+          out[static_cast<size_t>(i) * (2 * p.I)] = sum_digits(ta, t, p.token_rows) * r.x_scale[t] * g;
         }
         tc::fence_before_sync();
         __syncwarp();
@@ -479,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 2) down_kernel(const __grid_constant
   const int T = static_cast<int>(p.route.T);
   float* sums = reinterpret_cast<float*>(raw + kRaws * p.raw);   // [T][128]
   float* b_scale = sums + T * 128;                              // [2][kBlock]
-  uint32_t* maxima = reinterpret_cast<uint32_t*>(b_scale + 2 * kBlock);   // [2][kActWarps]
+  uint32_t* maxima = reinterpret_cast<uint32_t*>(b_scale + 2 * kBlock);   // [team][2][kTeamWarps]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) init_bars(p, bar);
   if (warp == 4) tc::tmem_alloc(&bar.tmem, kTmem);
@@ -487,6 +482,7 @@ __global__ void __launch_bounds__(kThreads, 2) down_kernel(const __grid_constant
     tc::prefetch_tmap(&p.tm_w);
     if (p.tma_scales) tc::prefetch_tmap(&p.tm_ws);
   }
+  route_prepare<kThreads>(r);
   // the up kernel lets this one go when all before it are done, so the logits are there
   launch_dependents();
   route_all<kThreads>(p.route, r, reinterpret_cast<uint32_t*>(ring), [](int) {});
@@ -540,24 +536,25 @@ __global__ void __launch_bounds__(kThreads, 2) down_kernel(const __grid_constant
       if (++ac == 2) ac = 0, aph ^= 1, bph ^= 1;
     }
   } else if (warp >= 8) {
-    // silu(gate) * up of a token's row, 8 columns an item, two items a thread; then its digits
+    // Two teams of four warps take the blocks of tokens in turn, each with an operand of its
+    // own: silu(gate) * up of a token's row, 8 columns an item, two items a thread, then its digits.
     grid_dependency_wait();
     const Shares shares(p, r.n);
-    const int tid = threadIdx.x - 256, tiles = p.I / 64, all = p.I / 8;
-    int buf = 0, ph = 1, turn = 0;
+    const int team = (warp - 8) / kTeamWarps, tid = threadIdx.x % kTeam, tiles = p.I / 64, all = p.I / 8;
+    uint8_t* bo = b + team * p.KS * p.NC * 128;
+    uint8_t* bso = bs + team * p.KS * kWords * 512;
+    uint32_t* top_of = maxima + team * 2 * kTeamWarps;
+    int ph = 1, turn = 0, number = 0;
     bool ok = true;
     for (int a = rank, blk = 0; a < r.n; ++blk == blocks(a) ? blk = 0, a += p.split : 0) {
-      // after a time-out the warps go on without waiting, so that they still meet
-      ok = ok && wait_warp(&bar.b_empty[buf], ph, &bar.abort_flag, p.status);
-      uint8_t* bo = b + buf * p.KS * p.NC * 128;
-      uint8_t* bso = bs + buf * p.KS * kWords * 512;
+      if ((number++ & 1) != team) continue;
       const int first = r.first[a] + blk * kBlock, n = min(r.first[a + 1] - first, kBlock);
       // the parts of this thread's columns
       int parts[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int s = (a * tiles + ((tid + kActThreads * k) >> 3)) * p.up_ks;
-        parts[k] = tid + kActThreads * k < all ? shares.owner(s + p.up_ks - 1) - shares.owner(s) + 1 : 0;
+        const int s = (a * tiles + ((tid + kTeam * k) >> 3)) * p.up_ks;
+        parts[k] = tid + kTeam * k < all ? shares.owner(s + p.up_ks - 1) - shares.owner(s) + 1 : 0;
       }
       for (int t = 0; t < n; ++t) {
         const float* row = p.part + static_cast<size_t>(first + t) * (2 * p.I);
@@ -565,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 2) down_kernel(const __grid_constant
         uint32_t bits[2] = {0, 0};
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const int i = tid + kActThreads * k;
+          const int i = tid + kTeam * k;
           const float* h = row + (i >> 3) * 128 + (i & 7) * 8;
           float4 g[2] = {}, u[2] = {};
           for (int q = 0; q < parts[k]; ++q) {
@@ -588,16 +585,20 @@ __global__ void __launch_bounds__(kThreads, 2) down_kernel(const __grid_constant
         }
         // the row's largest magnitude
         uint32_t m = __reduce_max_sync(kFull, max(bits[0], bits[1]));
-        if (lane == 0) maxima[turn * kActWarps + warp - 8] = m;
-        asm volatile("bar.sync 1, %0;" :: "n"(kActThreads) : "memory");
+        if (lane == 0) top_of[turn * kTeamWarps + warp % kTeamWarps] = m;
+        asm volatile("bar.sync %0, %1;" :: "r"(team + 1), "n"(kTeam) : "memory");
 #pragma unroll
-        for (int k = 0; k < kActWarps; ++k) m = max(m, maxima[turn * kActWarps + k]);
+        for (int k = 0; k < kTeamWarps; ++k) m = max(m, top_of[turn * kTeamWarps + k]);
         turn ^= 1;
-        if (tid == 0) b_scale[buf * kBlock + t] = inverse_norm_of(m);
+        if (t == 0) {   // the operand is needed from here on; after a time-out the warps go on without waiting, so that they still meet
+          ok = ok && wait_warp(&bar.b_empty[team], ph, &bar.abort_flag, p.status);
+          ph ^= 1;
+        }
+        if (tid == 0) b_scale[team * kBlock + t] = inverse_norm_of(m);
         const float norm = norm_of(m);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const int i = tid + kActThreads * k;
+          const int i = tid + kTeam * k;
           uint32_t top = __float_as_uint(__uint_as_float(bits[k]) * norm);
           top = max(top, __shfl_xor_sync(kFull, top, 1));
           if constexpr (!kNv) top = max(top, __shfl_xor_sync(kFull, top, 2));
@@ -610,8 +611,7 @@ __global__ void __launch_bounds__(kThreads, 2) down_kernel(const __grid_constant
       }
       tc::fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.b_full[buf]);
-      if (++buf == 2) buf = 0, ph ^= 1;
+      if (lane == 0) mbar_arrive(&bar.b_full[team]);
     }
   } else {
     const int o = 32 * warp + lane;
@@ -681,7 +681,7 @@ int64_t smem_bytes(const MoeDecodeArgs& a, bool down, int stages) {
   const int words = a.format == W4_FMT_NVFP4 ? 4 : 2;
   const int64_t ks = ((down ? a.I : a.H) + kStageK - 1) / kStageK, T = down ? kBlock : a.route.T;
   return 1024 + kHead + static_cast<int64_t>(stages) * (kStage + words * 512) + (down ? 2 : 1) * ks * (columns(T) * 128 + words * 512) +
-         kRaws * raw_bytes(a, down) + (down ? a.route.T * 512 + 2 * kBlock * 4 + 2 * kActWarps * 4 : 0);
+         kRaws * raw_bytes(a, down) + (down ? a.route.T * 512 + 2 * kBlock * 4 + 4 * kTeamWarps * 4 : 0);
 }
 
 template <bool kNv>
