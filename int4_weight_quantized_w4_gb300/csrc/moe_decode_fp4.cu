@@ -459,8 +459,9 @@ __global__ void __launch_bounds__(kThreads, 2) up_kernel(const __grid_constant__
 }
 
 // Warps as in up_kernel, 8-15: activations.
-template <bool kNv>
-__global__ void __launch_bounds__(kThreads, 2) down_kernel(const __grid_constant__ Params p) {
+// kTogether: few enough registers for an SM to hold a CTA of the up kernel beside.
+template <bool kNv, bool kTogether>
+__global__ void __launch_bounds__(kThreads, kTogether ? 2 : 1) down_kernel(const __grid_constant__ Params p) {
   constexpr int kWords = kNv ? 4 : 2;
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
@@ -544,45 +545,77 @@ __global__ void __launch_bounds__(kThreads, 2) down_kernel(const __grid_constant
     uint8_t* bo = b + team * p.KS * p.NC * 128;
     uint8_t* bso = bs + team * p.KS * kWords * 512;
     uint32_t* top_of = maxima + team * 2 * kTeamWarps;
-    int ph = 1, turn = 0, number = 0;
+    // sums of gate and up of eight of this thread's columns: the first parts, to which the rest is added
+    struct Sums {
+      float4 g[2], u[2];
+    };
+    auto fetch = [&](int row, int k, Sums& v) {
+      const int i = tid + kTeam * k;
+      const float* h = p.part + static_cast<size_t>(row) * (2 * p.I) + (i >> 3) * 128 + (i & 7) * 8;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        v.g[j] = i < all ? __ldcg(reinterpret_cast<const float4*>(h + 4 * j)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        v.u[j] = i < all ? __ldcg(reinterpret_cast<const float4*>(h + 64 + 4 * j)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    };
+    int ph = 1, turn = 0, count = 0;
     bool ok = true;
-    for (int a = rank, blk = 0; a < r.n; ++blk == blocks(a) ? blk = 0, a += p.split : 0) {
-      if ((number++ & 1) != team) continue;
+    int a = rank, blk = 0;
+    auto skip = [&]() {   // to this team's next block
+      while (a < r.n && (count & 1) != team) {
+        ++count;
+        if (++blk == blocks(a)) blk = 0, a += p.split;
+      }
+    };
+    skip();
+    // With the registers of a whole SM a token's sums are fetched while the digits of the one before
+    // are made (16 tokens, 64 experts of 2048 x 1408, 8 chosen: 126 -> 108 us); with half of them
+    // that spills, and the other kernel's CTA fills the time (5 tokens, 96 experts of 1024 x 704,
+    // 6 chosen: 24.7 us, 27.4 with it).
+    constexpr bool kAhead = !kTogether;
+    Sums v[2];
+    if (kAhead && a < r.n) fetch(r.first[a] + blk * kBlock, 0, v[0]), fetch(r.first[a] + blk * kBlock, 1, v[1]);
+    while (a < r.n) {
       const int first = r.first[a] + blk * kBlock, n = min(r.first[a + 1] - first, kBlock);
-      // the parts of this thread's columns
-      int parts[2];
+      int parts[2];   // the other parts of this thread's columns
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int s = (a * tiles + ((tid + kTeam * k) >> 3)) * p.up_ks;
-        parts[k] = tid + kTeam * k < all ? shares.owner(s + p.up_ks - 1) - shares.owner(s) + 1 : 0;
+        parts[k] = tid + kTeam * k < all ? shares.owner(s + p.up_ks - 1) - shares.owner(s) : 0;
       }
+      ++count;
+      if (++blk == blocks(a)) blk = 0, a += p.split;
+      skip();
+      const int after = a < r.n ? r.first[a] + blk * kBlock : -1;   // first row of the block after this one
       for (int t = 0; t < n; ++t) {
-        const float* row = p.part + static_cast<size_t>(first + t) * (2 * p.I);
         float f[2][8];
         uint32_t bits[2] = {0, 0};
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int i = tid + kTeam * k;
-          const float* h = row + (i >> 3) * 128 + (i & 7) * 8;
-          float4 g[2] = {}, u[2] = {};
-          for (int q = 0; q < parts[k]; ++q) {
-            const float* hq = h + static_cast<size_t>(q) * p.rows * (2 * p.I);
-            const float4 g0 = __ldcg(reinterpret_cast<const float4*>(hq)), g1 = __ldcg(reinterpret_cast<const float4*>(hq + 4));
-            const float4 u0 = __ldcg(reinterpret_cast<const float4*>(hq + 64)), u1 = __ldcg(reinterpret_cast<const float4*>(hq + 68));
-            g[0].x += g0.x, g[0].y += g0.y, g[0].z += g0.z, g[0].w += g0.w;
-            g[1].x += g1.x, g[1].y += g1.y, g[1].z += g1.z, g[1].w += g1.w;
-            u[0].x += u0.x, u[0].y += u0.y, u[0].z += u0.z, u[0].w += u0.w;
-            u[1].x += u1.x, u[1].y += u1.y, u[1].z += u1.z, u[1].w += u1.w;
+          Sums& c = v[kAhead ? k : 0];
+          if (!kAhead) fetch(first + t, k, c);
+          const float* h = p.part + static_cast<size_t>(first + t) * (2 * p.I) + (i >> 3) * 128 + (i & 7) * 8;
+          for (int q = parts[k]; q > 0; --q) {
+            h += static_cast<size_t>(p.rows) * (2 * p.I);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float4 g = __ldcg(reinterpret_cast<const float4*>(h + 4 * j)), u = __ldcg(reinterpret_cast<const float4*>(h + 64 + 4 * j));
+              c.g[j].x += g.x, c.g[j].y += g.y, c.g[j].z += g.z, c.g[j].w += g.w;
+              c.u[j].x += u.x, c.u[j].y += u.y, c.u[j].z += u.z, c.u[j].w += u.w;
+            }
           }
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             float* to = f[k] + 4 * j;
-            to[0] = silu_mul(g[j].x, u[j].x), to[1] = silu_mul(g[j].y, u[j].y);
-            to[2] = silu_mul(g[j].z, u[j].z), to[3] = silu_mul(g[j].w, u[j].w);
+            to[0] = silu_mul(c.g[j].x, c.u[j].x), to[1] = silu_mul(c.g[j].y, c.u[j].y);
+            to[2] = silu_mul(c.g[j].z, c.u[j].z), to[3] = silu_mul(c.g[j].w, c.u[j].w);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) bits[k] = max(bits[k], __float_as_uint(to[c]) & 0x7FFFFFFFu);
+            for (int e = 0; e < 4; ++e) bits[k] = max(bits[k], __float_as_uint(to[e]) & 0x7FFFFFFFu);
           }
         }
+        const int next = t + 1 < n ? first + t + 1 : after;
+        if (kAhead && next >= 0) fetch(next, 0, v[0]), fetch(next, 1, v[1]);
         // the row's largest magnitude
         uint32_t m = __reduce_max_sync(kFull, max(bits[0], bits[1]));
         if (lane == 0) top_of[turn * kTeamWarps + warp % kTeamWarps] = m;
@@ -718,7 +751,8 @@ cudaError_t run(const MoeDecodeArgs& a, bool down, cudaStream_t s) {
   // first still runs: the up kernel gets what the down kernel leaves with three stages.
   const int64_t both = 233472 - 2 * 1024;
   int up = kMaxStages, dn = kMaxStages;
-  if (smem_bytes(a, false, 3) + smem_bytes(a, true, 3) <= both) {
+  const bool together = smem_bytes(a, false, 3) + smem_bytes(a, true, 3) <= both;
+  if (together) {
     while (smem_bytes(a, false, up) + smem_bytes(a, true, 3) > both) --up;
     while (smem_bytes(a, false, up) + smem_bytes(a, true, dn) > both) --dn;
   } else {
@@ -732,7 +766,8 @@ cudaError_t run(const MoeDecodeArgs& a, bool down, cudaStream_t s) {
   const int64_t slices = (a.H + 127) / 128;
   for (int n = kMaxSplit; n > 1 && p.split == 1; n /= 2)
     if (slices * n <= current_sm_count() && n <= p.rows) p.split = n;
-  return start<down_kernel<kNv>>(p, slices * p.split, kThreads, smem, p.split, s);
+  return together ? start<down_kernel<kNv, true>>(p, slices * p.split, kThreads, smem, p.split, s)
+                  : start<down_kernel<kNv, false>>(p, slices * p.split, kThreads, smem, p.split, s);
 }
 
 }  // namespace
