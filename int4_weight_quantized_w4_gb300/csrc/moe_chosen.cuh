@@ -22,10 +22,7 @@ struct Routed {
   int16_t expert[kMaxE];       // the chosen experts in ascending order
   int16_t first[kMaxE + 1];    // their first rows
   int n;                       // how many
-  union {
-    int x_exp[kMaxT];          // exponent taken out of x_t
-    float x_scale[kMaxT];      // or what its numbers are to be multiplied with
-  };
+  float x_scale[kMaxT];        // what undoes the factor that brought x_t into range
 };
 
 template <int kEPL>

@@ -29,6 +29,12 @@
 // largest of them before it multiplies. fp16 rounds a to 11 bits where a bf16 step would
 // leave 8.
 //
+// One token, 64 experts of 2048 x 1408 in int4, 8 chosen (34.6 MB, 5.3 us at the copy rate): 30 us,
+// some 8 of them the two choices of experts, most of the rest instructions: a warp takes 1100 cycles
+// for its 16 words of a piece alone and 2000 beside three others. 16 tokens: 106 us (a floor of 37).
+// (Two groups a CTA and a CTA of either kernel on an SM, or 64 registers a thread to the same end,
+// leave too few warps or too short rings: 34 and 42 us.)
+//
 // Every sum has a fixed order: outputs are the same every time.
 #include "common.cuh"
 #include "launch.h"
@@ -39,8 +45,7 @@
 namespace w4 {
 namespace {
 
-constexpr int kGroups = 4, kGroupWarps = 4, kGroupThreads = 128;
-constexpr int kThreads = kGroups * kGroupThreads;    // 16 warps leave a thread 128 registers, a 17th would leave 96
+constexpr int kGroups = 4, kGroupWarps = 4, kGroupThreads = 128, kThreads = kGroups * kGroupThreads;
 constexpr int kChunkSteps = 16;                      // steps of 32 columns in a ring slot
 constexpr int kPer = kChunkSteps / kGroupWarps;      // a warp's of them
 constexpr int kRows = 32;                            // weight rows of a unit
@@ -57,9 +62,8 @@ struct Params {
   uint8_t* act_exp;        // [pairs, I / 8]: biased exponents
   uint16_t* y;             // down: bf16 [T, H]
   int H, I, K, rows;       // K: columns of w (up: H, down: I); rows an expert
-  int group_steps;         // int4: 32-column steps of a scale
+  int group_steps, group_shift;   // int4: 32-column steps of a scale; their logarithm, or -1
   int scale_row;           // bytes of a row's scales
-  int scale_pitch;         // the same in shared memory
   int chunks, slots, scale_slots;
   int split;               // down: CTAs of a cluster that share the experts of a slice
   unsigned int* status;
@@ -99,9 +103,9 @@ W4_DEV void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint3
 
 W4_DEV void group_sync(int group) { asm volatile("bar.sync %0, %1;" :: "r"(group + 1), "r"(kGroupThreads) : "memory"); }
 
-// x_t as fp16 times a power of two, by one warp; returns the exponent taken out.
+// x_t as fp16 times a power of two, by one warp; returns what undoes it.
 template <int kFmt>
-W4_DEV int widen_row(const Params& p, int t, uint8_t* to) {
+W4_DEV float widen_row(const Params& p, int t, uint8_t* to) {
   const int lane = threadIdx.x & 31;
   const uint4* xr = reinterpret_cast<const uint4*>(p.x) + static_cast<size_t>(t) * (p.H / 8);
   uint32_t m = 0;
@@ -112,7 +116,7 @@ W4_DEV int widen_row(const Params& p, int t, uint8_t* to) {
   }
   m = __reduce_max_sync(kFull, max(m & 0xFFFFu, m >> 16));
   const int e = max(static_cast<int>(m >> 7), 15);   // biased exponent; factors are normal numbers
-  const float f = __uint_as_float(static_cast<uint32_t>(min(268 - e, 254)) << 23);   // 2^(14 - (e - 127))
+  const float f = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);   // 2^(14 - (e - 127))
   for (int i = lane; i < p.H / 8; i += 32) {
     const uint4 v = ld_cg_v4(xr + i);
     float a[8];
@@ -125,36 +129,27 @@ W4_DEV int widen_row(const Params& p, int t, uint8_t* to) {
     }
     *reinterpret_cast<uint4*>(to + i * 16) = make_uint4(h[0], h[1], h[2], h[3]);
   }
-  return 127 - min(268 - e, 254);
+  return __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
 }
 
-// One unit's rows of weights: two blocks of 16, one behind the other (down) or gate and up.
-struct Unit {
-  int a;                 // index among the chosen experts
-  int n0, mat;           // first row and matrix of its box
-  size_t row[2];         // first row of each block, over all experts
+// Where a group is in its list of units: chosen expert and first row. A unit is two blocks
+// of 16 rows, one behind the other (down) or gate and up.
+template <bool kDown>
+struct Place {
+  int a, n0, left;   // left: units from here to the end of the CTA's list, before which it stands while positive
+  W4_DEV void skip(int I, int units) {
+    left -= units;
+    if constexpr (kDown) {
+      a += units;
+    } else {
+      n0 += 16 * units;
+      while (n0 >= I) n0 -= I, ++a;
+    }
+  }
 };
 
-template <bool kDown>
-W4_DEV Unit unit_of(const Params& p, const Routed& s, int u) {
-  Unit t;
-  if constexpr (kDown) {
-    t.a = u;
-    t.n0 = static_cast<int>(blockIdx.x) / p.split * kRows;
-    t.mat = s.expert[u];
-    t.row[0] = static_cast<size_t>(t.mat) * p.rows + t.n0;
-    t.row[1] = t.row[0] + 16;
-  } else {
-    const int per = p.I / 16;
-    t.a = u / per;
-    t.n0 = (u - t.a * per) * 16;
-    t.mat = 2 * s.expert[t.a];
-    t.row[0] = static_cast<size_t>(s.expert[t.a]) * p.rows + t.n0;
-    t.row[1] = t.row[0] + p.I;
-  }
-  return t;
-}
-
+// 2^e, -127 <= e <= 127: the least is not a normal number.
+W4_DEV float two_to(int e) { return __uint_as_float(e == -127 ? 0x00400000u : static_cast<uint32_t>(e + 127) << 23); }
 W4_DEV uint32_t e4m3_f16x2(uint32_t s8) { return e4m3x2_to_f16x2(s8 * 0x0101u); }   // twice
 W4_DEV float e8m0_f32(uint32_t s8) { return __uint_as_float(s8 << 23); }               // 0 for 2^-127, infinite for NaN
 W4_DEV float scale_int4(const uint8_t* row, int grp) { return half_bits_to_f32(reinterpret_cast<const uint16_t*>(row)[grp]); }
@@ -180,7 +175,7 @@ W4_DEV void multiply(const Params& p, const uint8_t* slot, const uint8_t* scales
 #pragma unroll
   for (int m = 0; m < 2; ++m)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) sc[m][h] = scales + (R::first(m) + h * R::kApart + g) * p.scale_pitch;
+    for (int h = 0; h < 2; ++h) sc[m][h] = scales + (R::first(m) + h * R::kApart + g) * p.scale_row;
   // one step: weights to operand registers, two products a block
   auto step = [&](int s, const uint4& v, const uint32_t (&f)[2][2], float (&d)[2][4]) {
     const uint8_t* w = w0 + ((s - c0) >> 3) * kBox + (((static_cast<uint32_t>(s) & 7u) << 4) ^ swz);
@@ -246,23 +241,34 @@ W4_DEV void multiply(const Params& p, const uint8_t* slot, const uint8_t* scales
     }
   } else {
     const uint32_t none[2][2] = {};
-    int grp = s0 / p.group_steps, left = (grp + 1) * p.group_steps - s0;
-    float d[2][4] = {};
+    float d[2][4] = {}, f[2][2];
+    auto scales_of = [&](int grp) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      if (s0 + i >= s1) break;
-      step(s0 + i, b(i), none, d);
-      if (--left == 0 || s0 + i + 1 == s1) {   // the end of a scale's columns, or of this warp's
-        float f[2][2];
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int h = 0; h < 2; ++h) f[m][h] = scale_int4(sc[m][h], grp);
+    };
+    int grp = p.group_shift >= 0 ? s0 >> p.group_shift : s0 / p.group_steps;
+    const int end = (grp + 1) * p.group_steps;
+    scales_of(grp);
+    if (s1 - s0 == kPer && s1 <= end) {   // one scale for all
 #pragma unroll
-          for (int h = 0; h < 2; ++h) f[m][h] = scale_int4(sc[m][h], grp);
-        add(f, d);
+      for (int i = 0; i < kPer; ++i) step(s0 + i, b(i), none, d);
+      add(f, d);
+    } else {
+      int left = end - s0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) d[j >> 2][j & 3] = 0.f;
-        ++grp;
-        left = p.group_steps;
+      for (int i = 0; i < kPer; ++i) {
+        if (s0 + i >= s1) break;
+        step(s0 + i, b(i), none, d);
+        if (--left == 0 || s0 + i + 1 == s1) {   // the end of a scale's columns, or of this warp's
+          add(f, d);
+          if (s0 + i + 1 == s1) break;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) d[j >> 2][j & 3] = 0.f;
+          scales_of(++grp);
+          left = p.group_steps;
+        }
       }
     }
   }
@@ -272,9 +278,9 @@ W4_DEV void multiply(const Params& p, const uint8_t* slot, const uint8_t* scales
 // of row pieces and of scales, and up: x in fp16, down: each group's outputs.
 struct Common {
   Routed r;
-  alignas(16) float red[kGroups][kGroupWarps][2][32][4];   // [group][warp][block][lane]
+  alignas(16) float red[kGroups][2][kGroupWarps][2][32][4];   // [group][in turn][warp][block][lane]
   uint64_t full[kGroups][kMoeDecodeSlots];
-  unsigned int done[kGroups][kMoeDecodeSlots];   // warps that are done with a slot, ever
+  uint64_t empty[kGroups][kMoeDecodeSlots];   // a group's warps are done with a slot
   int abort_flag;
 };
 
@@ -286,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_decode_kernel(const __grid_co
   Routed& r = c.r;
   uint8_t* ring = smem + (sizeof(Common) + 1023) / 1024 * 1024;
   uint8_t* scale_ring = ring + kGroups * p.slots * kSlot;
-  const int scale_slot = kRows * p.scale_pitch;
+  const int scale_slot = kRows * p.scale_row;
   uint8_t* rest = scale_ring + kGroups * p.scale_slots * scale_slot;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int T = static_cast<int>(p.route.T);
@@ -295,8 +301,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_decode_kernel(const __grid_co
   if (threadIdx.x == 0) {
     for (int g = 0; g < kGroups; ++g)
       for (int i = 0; i < p.slots; ++i) {
-        mbar_init(&c.full[g][i], 1 + 32);   // the weights; every lane's copies of scales
-        c.done[g][i] = 0;
+        mbar_init(&c.full[g][i], 1);
+        mbar_init(&c.empty[g][i], kGroupWarps);
       }
     c.abort_flag = 0;
     fence_mbar_init();
@@ -309,93 +315,103 @@ __global__ void __launch_bounds__(kThreads, 1) moe_decode_kernel(const __grid_co
   route_all<kThreads>(p.route, r, reinterpret_cast<uint32_t*>(ring), [&](int w) {
     const int t = T <= 8 ? w - 8 : w;   // by warps that route no token, where there are
     if (!kDown && t >= 0 && t < T) {
-      const int e = widen_row<kFmt>(p, t, rest + t * x_pitch);
-      if (lane == 0) r.x_exp[t] = e;
+      const float f = widen_row<kFmt>(p, t, rest + t * x_pitch);
+      if (lane == 0) r.x_scale[t] = f;
     }
   });
 
-  // units of this CTA: up, a share of all (expert, 16 columns) in order; down, every split-th expert
+  // units of this CTA: up, a share of all (expert, 16 columns) in order; down, every split-th expert.
+  // A group takes every kGroups-th of them.
   const int rank = kDown && p.split > 1 ? static_cast<int>(cluster_rank()) : 0;
-  int u0, u1, stride;
-  if constexpr (kDown) {
-    u0 = rank, u1 = r.n, stride = p.split;
-  } else {
-    const long long all = static_cast<long long>(r.n) * (p.I / 16);
-    u0 = static_cast<int>(all * blockIdx.x / gridDim.x);
-    u1 = static_cast<int>(all * (blockIdx.x + 1) / gridDim.x);
-    stride = 1;
-  }
-  const int steps = p.K / 32;
+  const int stride = kGroups * (kDown ? p.split : 1), steps = p.K / 32;
 
   {
     const int group = warp / kGroupWarps, w = warp % kGroupWarps, tid = threadIdx.x % kGroupThreads;
     const int g = lane >> 2, q = lane & 3;
     const uint64_t policy = tc::evict_first_policy();   // weights are read once
-    // A whole warp: starts the copies of the group's piece number `count`, its unit's scales
-    // with the first piece of the unit.
-    auto fill = [&](int count) {
-      const int round = count / p.chunks, ch = count - round * p.chunks;
-      const int u = u0 + (group + kGroups * round) * stride;
-      if (u >= u1) return;
-      const Unit t = unit_of<kDown>(p, r, u);
-      const int slot = count % p.slots, s0 = ch * kChunkSteps, boxes = (min(kChunkSteps, steps - s0) + 7) / 8;
-      uint64_t* bar = &c.full[group][slot];
-      if (elect_one()) {
-        mbar_arrive_expect_tx(bar, boxes * kBox);
+    Place<kDown> at;
+    if constexpr (kDown) {
+      at.a = rank + group * p.split, at.n0 = static_cast<int>(blockIdx.x) / p.split * kRows, at.left = r.n - at.a;
+    } else {
+      const unsigned per = p.I / 16, all = r.n * per;   // 256 experts of I / 16 units, times an SM count: below 2^32 for every I that fits
+      const unsigned u0 = all * blockIdx.x / gridDim.x + group, u1 = all * (blockIdx.x + 1) / gridDim.x;
+      at.a = u0 / per, at.n0 = (u0 - at.a * per) * 16, at.left = static_cast<int>(u1) - static_cast<int>(u0);
+    }
+    uint8_t* const my_ring = ring + group * p.slots * kSlot;
+    uint8_t* const my_scales = scale_ring + group * p.scale_slots * scale_slot;
+    // The next piece to copy. All warps of the group keep count.
+    Place<kDown> to = at;
+    int to_ch = 0, to_slot = 0, to_scale = 0;
+    // A whole warp: starts the copies of that piece, its unit's scales with the first of the unit.
+    auto fill = [&]() {
+      if (to.left > 0 && elect_one()) {
+        const int s0 = to_ch * kChunkSteps, boxes = (min(kChunkSteps, steps - s0) + 7) / 8, e = r.expert[to.a];
+        uint64_t* bar = &c.full[group][to_slot];
+        uint8_t* slot = my_ring + to_slot * kSlot;
+        mbar_arrive_expect_tx(bar, boxes * kBox + (to_ch == 0 ? scale_slot : 0));
         for (int i = 0; i < boxes; ++i)
-          tc::tma_load_3d_hint(ring + (group * p.slots + slot) * kSlot + i * kBox, &p.tm_w, bar, (s0 + 8 * i) * 16, t.n0, t.mat, policy);
-      }
-      __syncwarp();
-      if (ch == 0) {
-        // two blocks of 16 rows, 16 bytes at a time; rows of whole 16 bytes go to their pitch
-        const uint32_t to = smem_addr(scale_ring + (group * p.scale_slots + round % p.scale_slots) * scale_slot);
-        const bool pitched = p.scale_pitch != p.scale_row;
-        const int per = p.scale_row / 16;
-        for (int i = lane; i < 2 * p.scale_row; i += 32) {   // 16 rows are scale_row pieces of 16 bytes
-          const int blk = i >= p.scale_row, j = i - blk * p.scale_row;
-          const int row = pitched ? j / per : 0;
-          tc::copy16_async(to + blk * 16 * p.scale_pitch + (pitched ? row * (p.scale_pitch - p.scale_row) : 0) + j * 16,
-                           p.w_scale + t.row[blk] * p.scale_row + j * 16);
+          tc::tma_load_3d_hint(slot + i * kBox, &p.tm_w, bar, (s0 + 8 * i) * 16, to.n0, kDown ? e : 2 * e, policy);
+        if (to_ch == 0) {
+          uint8_t* sc = my_scales + to_scale * scale_slot;
+          const uint8_t* from = p.w_scale + (static_cast<size_t>(e) * p.rows + to.n0) * p.scale_row;
+          tc::bulk_load(sc, from, 16 * p.scale_row, bar);
+          tc::bulk_load(sc + 16 * p.scale_row, from + static_cast<size_t>(kDown ? 16 : p.I) * p.scale_row, 16 * p.scale_row, bar);
         }
       }
-      tc::copy_async_arrive(bar);
+      __syncwarp();
+    };
+    auto filled = [&]() {   // on to the piece after it
+      if (++to_slot == p.slots) to_slot = 0;
+      if (++to_ch == p.chunks) {
+        to_ch = 0;
+        if (++to_scale == p.scale_slots) to_scale = 0;
+        to.skip(p.I, stride);
+      }
     };
     tc::fence_proxy_async_smem();   // the ring held the routing's scratch
-    if (w < p.slots) fill(w);
+    for (int i = 0; i < p.slots; ++i) {
+      if (w == (i & (kGroupWarps - 1))) fill();
+      filled();
+    }
     float* out = reinterpret_cast<float*>(rest) + group * T * kRows;   // down: [T][32]
     if constexpr (kDown) {
       for (int i = tid; i < T * kRows; i += kGroupThreads) out[i] = 0.f;
       grid_dependency_wait();   // the activations, and y may still be read
     }
-    int count = 0, round = 0;
+    int count = 0, slot = 0, phase = 0, scale_at = 0, turn = 0;
     bool ok = true;
-    for (int u = u0 + group * stride; u < u1; u += kGroups * stride, ++round) {
-      const Unit t = unit_of<kDown>(p, r, u);
-      const int first = r.first[t.a], tokens = r.first[t.a + 1] - first;
-      const uint8_t* scales = scale_ring + (group * p.scale_slots + round % p.scale_slots) * scale_slot;
+    for (; at.left > 0; at.skip(p.I, stride)) {
+      const int first = r.first[at.a], tokens = r.first[at.a + 1] - first;
+      const uint8_t* scales = my_scales + scale_at * scale_slot;
+      const float gl = p.w_global != nullptr ? __ldcg(p.w_global + r.expert[at.a]) : 1.f;
       float y[2][2][4] = {};   // [eight tokens][block]
       for (int ch = 0; ch < p.chunks; ++ch, ++count) {
-        const int slot = count % p.slots;
-        const int c0 = ch * kChunkSteps, n = min(kChunkSteps, steps - c0);
-        const int s0 = c0 + n * w / kGroupWarps, s1 = c0 + n * (w + 1) / kGroupWarps;
-        const uint8_t* piece = ring + (group * p.slots + slot) * kSlot;
+        const int c0 = ch * kChunkSteps;
+        const int s0 = min(c0 + kPer * w, steps), s1 = min(s0 + kPer, steps);
+        const uint8_t* piece = my_ring + slot * kSlot;
+        auto row_of = [&](int nb) { return first + min(8 * nb + g, tokens - 1); };   // columns past the last token repeat it
+        uint4 v[kPer];
+        int e[kPer];
+        auto fetch = [&](int nb) {   // activations and their exponents
+          const uint16_t* ar = p.act + static_cast<size_t>(row_of(nb)) * p.K + 8 * q;
+          const uint8_t* er = p.act_exp + static_cast<size_t>(row_of(nb)) * (p.K / 8) + q;
+#pragma unroll
+          for (int i = 0; i < kPer; ++i)
+            if (s0 + i < s1) {
+              v[i] = ld_cg_v4(ar + 32 * (s0 + i));
+              e[i] = __ldcg(er + 4 * (s0 + i));
+            }
+        };
+        if constexpr (kDown) fetch(0);
         // after a time-out the group goes on without waiting, so that its warps still meet
-        ok = ok && wait_warp(&c.full[group][slot], count / p.slots & 1, abort_flag, p.status);
+        ok = ok && wait_warp(&c.full[group][slot], phase, abort_flag, p.status);
 #pragma unroll
         for (int nb = 0; nb < 2; ++nb) {
-          if (8 * nb >= tokens) break;
-          const int row = first + min(8 * nb + g, tokens - 1);   // columns past the last token repeat it
+          if (8 * nb >= tokens || s0 >= s1) break;
+          const int row = row_of(nb);
           if constexpr (kDown) {
-            const uint16_t* ar = p.act + static_cast<size_t>(row) * p.K + 8 * q;
-            const uint8_t* er = p.act_exp + static_cast<size_t>(row) * (p.K / 8) + q;
-            uint4 v[kPer];
-            int e[kPer], top = 0;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-              if (s0 + i < s1) {
-                v[i] = ld_cg_v4(ar + 32 * (s0 + i));
-                e[i] = __ldcg(er + 4 * (s0 + i));
-              }
+            int top = 0;
+            if (nb > 0) fetch(nb);
 #pragma unroll
             for (int i = 0; i < kPer; ++i)
               if (s0 + i < s1) top = max(top, e[i]);
@@ -416,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_decode_kernel(const __grid_co
             multiply<kFmt, kDown>(p, piece, scales, c0, s0, s1, [&](int i) { return v[i]; }, d);
             // a factor 2^(top - 127 - 14) for this lane's two columns
             const int t0 = __shfl_sync(kFull, top, 8 * q), t1 = __shfl_sync(kFull, top, 8 * q + 4);
-            const float f0 = ldexpf(1.f, t0 - 141), f1 = ldexpf(1.f, t1 - 141);
+            const float f0 = two_to(t0 - 141), f1 = two_to(t1 - 141);
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
               y[nb][m][0] = fmaf(d[m][0], f0, y[nb][m][0]), y[nb][m][1] = fmaf(d[m][1], f1, y[nb][m][1]);
@@ -428,22 +444,26 @@ __global__ void __launch_bounds__(kThreads, 1) moe_decode_kernel(const __grid_co
                            [&](int i) { return *reinterpret_cast<const uint4*>(xr + 64 * i); }, y[nb]);
           }
         }
-        // the last of the four warps to be done with the piece starts the copy of the next one into its place
         __syncwarp();
-        int before = 0;
-        if (lane == 0) {
-          __threadfence_block();
-          before = atomicAdd(&c.done[group][slot], 1);
-          __threadfence_block();
+        if (lane == 0) mbar_arrive(&c.empty[group][slot]);
+        // One of the warps copies the next piece into the place of the one before this, which the
+        // others left a piece ago or soon will.
+        if (count > 0) {
+          if (w == (count & (kGroupWarps - 1))) {
+            const int last = slot == 0 ? p.slots - 1 : slot - 1;
+            ok = ok && wait_warp(&c.empty[group][last], slot == 0 ? phase ^ 1 : phase, abort_flag, p.status);
+            if (ok) fill();
+          }
+          filled();
         }
-        if ((__shfl_sync(kFull, before, 0) & (kGroupWarps - 1)) == kGroupWarps - 1) fill(count + p.slots);
+        if (++slot == p.slots) slot = 0, phase ^= 1;
       }
-      const float gl = p.w_global != nullptr ? __ldcg(p.w_global + r.expert[t.a]) : 1.f;
+      if (++scale_at == p.scale_slots) scale_at = 0;
 #pragma unroll
       for (int nb = 0; nb < 2; ++nb) {
         if (8 * nb >= tokens) break;
-        float (*red)[2][32][4] = c.red[group];
-        if (round > 0 || nb > 0) group_sync(group);   // the sums before have been read
+        float (*red)[2][32][4] = c.red[group][turn];   // two in turn, so that one meeting is enough
+        turn ^= 1;
 #pragma unroll
         for (int m = 0; m < 2; ++m) *reinterpret_cast<float4*>(red[w][m][lane]) = make_float4(y[nb][m][0], y[nb][m][1], y[nb][m][2], y[nb][m][3]);
         group_sync(group);
@@ -463,8 +483,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_decode_kernel(const __grid_co
           // thread: column tid % 16 of the unit, token tid / 16
           const int i = tid & 15, n = 8 * nb + (tid >> 4);
           const int k = min(n, tokens - 1), l = (i & 7) * 4 + (k & 7) / 2, j = k & 1;
-          const int e = r.x_exp[r.token[first + k]];
-          const float gate = ldexpf(sum(i >> 3, l, j), e) * gl, up = ldexpf(sum(i >> 3, l, 2 + j), e) * gl;
+          const float f = r.x_scale[r.token[first + k]];
+          const float gate = sum(i >> 3, l, j) * f * gl, up = sum(i >> 3, l, 2 + j) * f * gl;
           const float a = __fdiv_rn(gate, 1.f + expf(-gate)) * up;
           uint32_t bits = __float_as_uint(a) & 0x7FFFFFFFu;
           bits = max(bits, __shfl_xor_sync(kFull, bits, 1));
@@ -474,8 +494,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_decode_kernel(const __grid_co
           if (n < tokens) {
             uint16_t h;
             asm("cvt.rn.f16.f32 %0, %1;" : "=h"(h) : "f"(a * __uint_as_float((268u - ex) << 23)));
-            p.act[static_cast<size_t>(first + n) * p.I + t.n0 + (i & 8) + chunk_place<kFmt>(i & 7)] = h;
-            if ((i & 7) == 0) p.act_exp[static_cast<size_t>(first + n) * (p.I / 8) + (t.n0 + i) / 8] = static_cast<uint8_t>(ex);
+            p.act[static_cast<size_t>(first + n) * p.I + at.n0 + (i & 8) + chunk_place<kFmt>(i & 7)] = h;
+            if ((i & 7) == 0) p.act_exp[static_cast<size_t>(first + n) * (p.I / 8) + (at.n0 + i) / 8] = static_cast<uint8_t>(ex);
           }
         }
       }
@@ -527,8 +547,29 @@ int scale_row_bytes(const MoeDecodeArgs& a, bool down) {
   return static_cast<int>(a.format == W4_FMT_INT4 ? 2 * (K / (down ? a.down_group : a.gate_up_group)) : a.format == W4_FMT_NVFP4 ? K / 16 : K / 32);
 }
 
+// Shared memory: `slots` ring slots a group, the most that fit; fewer than two: it does not fit.
+struct Layout {
+  int slots, chunks, scale_slots;
+  int64_t bytes;
+};
+Layout layout_of(const MoeDecodeArgs& a, bool down) {
+  const int64_t K = down ? a.I : a.H, T = a.route.T;
+  const int64_t rest = down ? kGroups * T * kRows * 4 : T * (2 * a.H + 64);
+  Layout l;
+  l.chunks = static_cast<int>((K / 32 + kChunkSteps - 1) / kChunkSteps);
+  for (l.slots = kMoeDecodeSlots; l.slots >= 2; --l.slots) {
+    l.scale_slots = (l.slots + l.chunks - 1) / l.chunks + 1;   // a unit's are in use until its last piece is done
+    l.bytes = 1024 + static_cast<int64_t>(sizeof(Common) + 1023) / 1024 * 1024 + rest +
+              static_cast<int64_t>(kGroups) * (l.slots * kSlot + static_cast<int64_t>(l.scale_slots) * kRows * scale_row_bytes(a, down));
+    if (l.bytes <= 232448) break;
+  }
+  return l;
+}
+
 template <int kFmt, bool kDown>
 cudaError_t run(const MoeDecodeArgs& a, cudaStream_t s) {
+  const Layout l = layout_of(a, kDown);
+  if (l.slots < 2) return cudaErrorInvalidConfiguration;   // refused before (moe_decode_fits)
   Params p = {};
   p.route = a.route;
   const int T = static_cast<int>(a.route.T);
@@ -545,20 +586,12 @@ cudaError_t run(const MoeDecodeArgs& a, cudaStream_t s) {
   p.K = kDown ? p.I : p.H;
   p.rows = kDown ? p.H : 2 * p.I;
   p.group_steps = kFmt == W4_FMT_INT4 ? (kDown ? a.down_group : a.gate_up_group) / 32 : 1;
+  p.group_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (p.group_steps == 1 << i) p.group_shift = i;
   p.scale_row = scale_row_bytes(a, kDown);
-  // rows of whole 16 bytes are copied one by one to a pitch that spreads eight rows over the banks
-  p.scale_pitch = p.scale_row % 16 != 0 ? p.scale_row : p.scale_row % 32 == 0 ? p.scale_row + 16 : p.scale_row + 32;
-  p.chunks = (p.K / 32 + kChunkSteps - 1) / kChunkSteps;
+  p.slots = l.slots, p.chunks = l.chunks, p.scale_slots = l.scale_slots;
   p.status = a.status;
-  const int rest = kDown ? kGroups * T * kRows * 4 : T * (2 * p.H + 64);
-  const int base = 1024 + (static_cast<int>(sizeof(Common)) + 1023) / 1024 * 1024 + rest;
-  int smem = 0;
-  for (p.slots = kMoeDecodeSlots; p.slots >= 2; --p.slots) {
-    p.scale_slots = (p.slots + p.chunks - 1) / p.chunks + 1;
-    smem = base + kGroups * (p.slots * kSlot + p.scale_slots * kRows * p.scale_pitch);
-    if (smem <= 232448) break;
-  }
-  if (p.slots < 2) return cudaErrorInvalidConfiguration;   // refused before (moe_decode_fits)
   p.split = 1;
   int64_t grid = current_sm_count();
   if (kDown) {
@@ -567,7 +600,7 @@ cudaError_t run(const MoeDecodeArgs& a, cudaStream_t s) {
       if (slices * n <= grid && n <= a.route.k * T) p.split = n;
     grid = slices * p.split;
   }
-  return start<moe_decode_kernel<kFmt, kDown>>(p, grid, kThreads, smem, p.split, s);
+  return start<moe_decode_kernel<kFmt, kDown>>(p, grid, kThreads, static_cast<int>(l.bytes), p.split, s);
 }
 
 template <int kFmt>
@@ -578,18 +611,7 @@ cudaError_t run_both(const MoeDecodeArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// Two ring slots a group beside the activations, for either kernel.
-bool moe_decode_fits(const MoeDecodeArgs& a) {
-  const int64_t common = 1024 + (static_cast<int64_t>(sizeof(Common)) + 1023) / 1024 * 1024;
-  for (bool down : {false, true}) {
-    const int64_t K = down ? a.I : a.H;
-    const int64_t chunks = (K / 32 + kChunkSteps - 1) / kChunkSteps;
-    const int64_t ring = kGroups * (2 * kSlot + ((2 + chunks - 1) / chunks + 1) * kRows * (static_cast<int64_t>(scale_row_bytes(a, down)) + 32));
-    const int64_t rest = down ? kGroups * a.route.T * kRows * 4 : a.route.T * (2 * a.H + 64);
-    if (common + ring + rest > 232448) return false;
-  }
-  return true;
-}
+bool moe_decode_fits(const MoeDecodeArgs& a) { return layout_of(a, false).slots >= 2 && layout_of(a, true).slots >= 2; }
 
 size_t moe_decode_workspace_bytes(int64_t T, int64_t k, int64_t I) {
   const size_t halves = static_cast<size_t>(T * k) * static_cast<size_t>(2 * I + I / 8), sums = moe_decode_fp4_workspace_bytes(T, k, I);
