@@ -139,7 +139,8 @@ size_t w4_workspace_bytes(int32_t op, int64_t M, int64_t N, int64_t K, int32_t g
     return w4::fp8_block_workspace_bytes(M, K) +
            (group > 0 ? w4::fp8_block_workspace_bytes(M / 2, K) : w4::fp8_block_part_bytes(M, N, K));
   }
-  if (op == W4_OP_MOE_DECODE) return N > 0 ? w4::moe_decode_workspace_bytes(M, N, K) : 0;
+  if (op == W4_OP_MOE_DECODE)
+    return (N > 0 && N <= w4::kMoeDecodeTopK && M <= w4::kMoeDecodeTokens && K <= INT32_MAX) ? w4::moe_decode_workspace_bytes(M, N, K) : 0;
   if (op == W4_OP_FP4_IN || op == W4_OP_FP4_MOE_IN) {
     if ((group != 16 && group != 32) || K % group != 0 || w4::fp4_fuses(M, op == W4_OP_FP4_MOE_IN)) return 0;
     // the rows, and for experts the tokens they come from when those are at most half as many
@@ -800,7 +801,7 @@ w4_status w4_moe_decode(const void* x, const void* logits, int32_t logits_f32, c
   w4::MoeDecodeArgs a{route, x, format, gate_up_group, down_group, gate_up, gate_up_scale, gate_up_global, down, down_scale,
                       down_global, H, I, y, workspace, nullptr};
   if (!w4::moe_decode_fp4_fits(a) && !w4::moe_decode_fits(a))
-    return fail(W4_ERR_UNSUPPORTED, "T rows of x do not fit in shared memory (T=%lld H=%lld)", (long long)T, (long long)H);
+    return fail(W4_ERR_UNSUPPORTED, "T rows of x and the copies in flight do not fit in shared memory (T=%lld H=%lld I=%lld)", (long long)T, (long long)H, (long long)I);
   if (T == 0) return ok();
   if (!x || !logits || !gate_up || !gate_up_scale || !down || !down_scale || !y)
     return fail(W4_ERR_NULL, "required pointer is NULL");

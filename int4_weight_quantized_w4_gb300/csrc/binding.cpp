@@ -601,9 +601,7 @@ PyObject* moe_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (scale == -1.0 && PyErr_Occurred()) return nullptr;
   const CallStream stream(a[18], dev);
   const at::Tensor y = output(a[16], "y", {T, H}, ScalarType::BFloat16, kBf16, dev, stream);
-  // a call that the library refuses asks for no memory first
-  const bool small = T <= 16 && k >= 1 && k <= 32;
-  const Scratch s = scratch(a[17], W4_OP_MOE_DECODE, small ? T : 0, k, I, 0, dev);
+  const Scratch s = scratch(a[17], W4_OP_MOE_DECODE, T, k, I, 0, dev);
   if (failed(w4_moe_decode(x.data_ptr(), logits.data_ptr(), logits.scalar_type() == ScalarType::Float,
                            static_cast<const float*>(data(a[10])), T, static_cast<int32_t>(E), k,
                            integer32(a[11], "n_group"), integer32(a[12], "topk_group"), integer32(a[13], "scoring"),

@@ -48,6 +48,7 @@ namespace {
 constexpr int kGroups = 4, kGroupWarps = 4, kGroupThreads = 128, kThreads = kGroups * kGroupThreads;
 constexpr int kChunkSteps = 16;                      // steps of 32 columns in a ring slot
 constexpr int kPer = kChunkSteps / kGroupWarps;      // a warp's of them
+constexpr int64_t kMaxI = 1 << 20;                   // 256 experts of I / 16 units times 152 CTAs are numbers of 32 bits
 constexpr int kRows = 32;                            // weight rows of a unit
 constexpr int kBox = kRows * 128;                    // 8 steps of them, 128-byte swizzle: 16-byte chunk c of row r at c ^ r % 8
 constexpr int kSlot = kChunkSteps / 8 * kBox;
@@ -333,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_decode_kernel(const __grid_co
     if constexpr (kDown) {
       at.a = rank + group * p.split, at.n0 = static_cast<int>(blockIdx.x) / p.split * kRows, at.left = r.n - at.a;
     } else {
-      const unsigned per = p.I / 16, all = r.n * per;   // 256 experts of I / 16 units, times an SM count: below 2^32 for every I that fits
+      const unsigned per = p.I / 16, all = r.n * per;   // times a CTA's index below 2^32: kMaxI
       const unsigned u0 = all * blockIdx.x / gridDim.x + group, u1 = all * (blockIdx.x + 1) / gridDim.x;
       at.a = u0 / per, at.n0 = (u0 - at.a * per) * 16, at.left = static_cast<int>(u1) - static_cast<int>(u0);
     }
@@ -611,7 +612,9 @@ cudaError_t run_both(const MoeDecodeArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-bool moe_decode_fits(const MoeDecodeArgs& a) { return layout_of(a, false).slots >= 2 && layout_of(a, true).slots >= 2; }
+bool moe_decode_fits(const MoeDecodeArgs& a) {
+  return a.I <= kMaxI && layout_of(a, false).slots >= 2 && layout_of(a, true).slots >= 2;
+}
 
 size_t moe_decode_workspace_bytes(int64_t T, int64_t k, int64_t I) {
   const size_t halves = static_cast<size_t>(T * k) * static_cast<size_t>(2 * I + I / 8), sums = moe_decode_fp4_workspace_bytes(T, k, I);

@@ -3,8 +3,8 @@
 Quantized codes and scales are whole numbers and have to be equal, but where silu is
 in between: there fp32 steps and float64 may put a value on different sides of a border.
 Products of codes are exact and sums are taken in fp32, so that outputs meet the bar of
-every bf16 output (tests/_compare.py: one rounding is 2^-9 of a value, the bar is two
-and the sum's error a hundredth of that)."""
+every bf16 output (tests/_compare.py: one rounding is at most 2^-8 of a value, the bar is two of
+them, and the sum's error a hundredth of one)."""
 import numpy as np
 import pytest
 import torch

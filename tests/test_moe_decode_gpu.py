@@ -1,9 +1,12 @@
 """The few-token expert layer against the float64 oracle.
 
 An output is off by its rounding to bf16 (2^-8 of it at most), by the activations'
-rounding to 11 bits (2^-11 of each, so of the sum of magnitudes `size`) and by fp32 sums: a
-chain of at most 2^10 additions a warp, 2^-23 each of what is summed, for gate, up and
-output, which silu enlarges by less than twice: 2^-11 of `size` again is ample."""
+rounding, in int4 to 11 bits (2^-11 of each, so of the sum of magnitudes `size`), in the 4-bit
+floating point formats to 2^-13 of the largest of 16 or 32 neighbours, for x and for the activations
+in between: with signs and sizes at random, 2^-13 of a few typical magnitudes each, of which a sum
+of K terms keeps a share of about K^-1/2; and by fp32 sums: a chain of at most 2^10 additions a warp,
+2^-23 each of what is summed, for gate, up and output, which silu enlarges by less than twice.
+2^-10 of `size` covers either."""
 import numpy as np
 import pytest
 import torch
@@ -168,3 +171,58 @@ def test_repeated_and_captured_calls_are_the_same(fmt):
 def test_no_tokens():
     ex = Experts(4, 128, 64, "mxfp4")
     assert ex.call(np.zeros((0, 128), np.uint16), np.zeros((0, 4), np.float32), 2).shape == (0, 128)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+def test_a_token_with_nan_or_infinity_leaves_the_others_alone_in_fp4(fmt):
+    ex = Experts(4, 128, 64, fmt)
+    xb, logits = inputs(4, 128, 4)
+    clean = ex.call(xb, logits, 3)
+    x = O.bf16_to_f64(xb).astype(np.float32)
+    x[1, 5], x[3, 100] = np.nan, np.inf
+    y = ex.call(S.to_bf16_bits(x), logits, 3)
+    assert torch.isnan(y[1].float()).all() and not torch.isfinite(y[3].float()).any()
+    assert torch.equal(y[[0, 2]], clean[[0, 2]])
+
+
+@pytest.mark.parametrize("H,I,group", [(384, 192, 96), (2048, 1408, 128), (192, 576, 192), (1088, 320, 64)])
+@pytest.mark.parametrize("T", [2, 16])
+def test_groups_of_an_int4_scale(H, I, group, T):
+    """Scales that end inside a warp's columns, and numbers of columns that are no power of two."""
+    Experts(6, H, I, "int4", group).check(*inputs(T, H, 6, seed=H + T), 3)
+
+
+@pytest.mark.parametrize("fmt,T,H,I", [("mxfp4", 3, 128, 2112), ("nvfp4", 9, 128, 2112), ("nvfp4", 2, 320, 4096), ("mxfp4", 1, 8256, 64)])
+def test_sizes_past_the_block_scaled_form(fmt, T, H, I):
+    Experts(5, H, I, fmt).check(*inputs(T, H, 5, seed=I), 2)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_bf16_logits(fmt):
+    """Choices among rounded logits: as with the same numbers in fp32."""
+    ex = Experts(24, 128, 64, fmt)
+    xb, logits = inputs(7, 128, 24)
+    lb = S.to_bf16_bits(logits)
+    want = ex.call(xb, O.bf16_to_f64(lb).astype(np.float32), 5)
+    u, us, d, ds, ug, dg = ex._dev
+    got = w4.w4_moe_decode(bf16(xb), bf16(lb), u, us, d, ds, 5, fmt, gate_up_global=ug, down_global=dg)
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_masked_logits(fmt):
+    """Experts masked by -inf or the lowest number are chosen last; a token with nothing but -inf weighs nothing."""
+    ex = Experts(12, 128, 64, fmt)
+    xb, logits = inputs(3, 128, 12)
+    logits[0, 3:] = -np.inf
+    logits[1, :] = -np.inf
+    logits[2, 4:] = np.finfo(np.float32).min
+    y = ex.call(xb, logits, 3, scoring="softmax")
+    torch.cuda.synchronize()
+    assert w4.w4_device_status() == w4.W4_OK
+    ids, wts, _ = O.moe_route_grouped(logits, 3, scoring="softmax")
+    assert sorted(ids[0].tolist()) == [0, 1, 2]
+    r, size = O.moe_decode(xb[[0, 2]], logits[[0, 2]], lambda e: ex.values(0, e), lambda e: ex.values(1, e), 3, scoring="softmax")
+    err = np.abs(y[[0, 2]].float().cpu().numpy() - r)
+    assert (err <= 2.0 ** -8 * np.abs(r) + 2.0 ** -10 * size).all()
+    assert (y[1] == 0).all()
