@@ -229,6 +229,7 @@ cudaError_t launch_fp4(const Fp4Args& a, cudaStream_t s);
 // Limits of the few-token expert layer.
 constexpr int kMoeDecodeTokens = 16, kMoeDecodeExperts = 256, kMoeDecodeTopK = 32;
 constexpr int kMoeDecodeSlots = 4;
+constexpr int kMoeChoiceBytes = 3712;   // of a workspace, in front
 struct MoeDecodeArgs {
   MoeRouteArgs route;           // logits [T, E] and how to choose; no outputs
   const void* x;                // bf16 [T, H]

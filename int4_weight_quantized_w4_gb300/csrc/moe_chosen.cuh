@@ -11,19 +11,37 @@ namespace {
 
 constexpr int kMaxT = kMoeDecodeTokens, kMaxE = kMoeDecodeExperts, kMaxK = kMoeDecodeTopK, kMaxPairs = kMaxT * kMaxK;
 
-// What routing leaves in shared memory, the same in every CTA. Rows of the activations
-// are the chosen pairs by expert, then token.
-struct Routed {
+// What routing leaves: rows of the activations are the chosen pairs by expert, then token.
+struct alignas(16) Choice {
+  float weight[kMaxPairs];     // of a row
+  float x_scale[kMaxT];        // what undoes the factor that brought x_t into range
+  int16_t expert[kMaxE];       // the chosen experts in ascending order
+  int16_t first[kMaxE + 8];    // their first rows, and behind the last one's
+  uint8_t token[kMaxPairs];    // of a row
+  int n;                       // how many experts
+  int pad[11];
+};
+static_assert(sizeof(Choice) == kMoeChoiceBytes, "a workspace begins with one");
+
+// In shared memory, the same in every CTA.
+struct Routed : Choice {
   uint32_t mask[kMaxE];        // tokens of an expert
   int32_t ids[kMaxPairs];
   float wts[kMaxPairs];
-  float weight[kMaxPairs];     // of a row
-  uint8_t token[kMaxPairs];    // of a row
-  int16_t expert[kMaxE];       // the chosen experts in ascending order
-  int16_t first[kMaxE + 1];    // their first rows
-  int n;                       // how many
-  float x_scale[kMaxT];        // what undoes the factor that brought x_t into range
 };
+
+// The choice from one kernel to the next, in global memory. All threads.
+template <int kThreads>
+W4_DEV void keep_choice(const Routed& s, uint4* to) {
+  for (int i = threadIdx.x; i < static_cast<int>(sizeof(Choice) / 16); i += kThreads)
+    to[i] = reinterpret_cast<const uint4*>(static_cast<const Choice*>(&s))[i];
+}
+template <int kThreads>
+W4_DEV void take_choice(Routed& s, const uint4* from) {
+  for (int i = threadIdx.x; i < static_cast<int>(sizeof(Choice) / 16); i += kThreads)
+    reinterpret_cast<uint4*>(static_cast<Choice*>(&s))[i] = ld_cg_v4(from + i);
+  __syncthreads();
+}
 
 template <int kEPL>
 W4_DEV void choose(const MoeRouteArgs& a, int t, Routed& s, uint32_t* scratch) {

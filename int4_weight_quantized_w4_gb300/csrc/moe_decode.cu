@@ -6,9 +6,7 @@
 //   down:   y_t = bf16( sum_e w_te W_d[e] a_te ).
 //
 // The chosen experts' weights are nearly all there is to read, each weight once: bound by
-// HBM. Both kernels route for themselves (the logits are an input), so that the second
-// one's copies of weights can start while the first still computes, and no launch lies in
-// between.
+// HBM. The first kernel routes, in every CTA, and leaves the choice to the second one.
 //
 // A unit of work is 32 weight rows of one expert: 16 gate rows and their 16 up rows
 // (up), or 32 output columns (down). Four warps take a unit together, each a quarter of
@@ -29,11 +27,12 @@
 // largest of them before it multiplies. fp16 rounds a to 11 bits where a bf16 step would
 // leave 8.
 //
-// One token, 64 experts of 2048 x 1408 in int4, 8 chosen (34.6 MB, 5.3 us at the copy rate): 30 us,
-// some 8 of them the two choices of experts, most of the rest instructions: a warp takes 1100 cycles
-// for its 16 words of a piece alone and 2000 beside three others. 16 tokens: 106 us (a floor of 37).
-// (Two groups a CTA and a CTA of either kernel on an SM, or 64 registers a thread to the same end,
-// leave too few warps or too short rings: 34 and 42 us.)
+// One token, 64 experts of 2048 x 1408 in int4, 8 chosen (34.6 MB, 5.3 us at the copy rate): 26 us,
+// of which 4 go to the choice of experts and 4 to the second kernel's start, most of the rest to
+// instructions: 31 for a lane's word of weights, 11 of them the widening and the product, at half
+// an instruction a cycle. 8 tokens (42 experts): 80 us, 16 tokens: 103. (Measured against this: a second
+// CTA on an SM, with two groups or 64 registers a thread, 34 and 42 us for the one token; a last unit
+// cut among the groups, the same, as the instructions remain.)
 //
 // Every sum has a fixed order: outputs are the same every time.
 #include "common.cuh"
@@ -59,6 +58,7 @@ struct Params {
   const uint8_t* w_scale;  // [E, rows, scale_row bytes]
   const float* w_global;   // [E] or null
   const uint16_t* x;       // up: bf16 [T, H]
+  uint4* choice;           // the up kernel's, for the down kernel
   uint16_t* act;           // fp16 [pairs, I]
   uint8_t* act_exp;        // [pairs, I / 8]: biased exponents
   uint16_t* y;             // down: bf16 [T, H]
@@ -109,26 +109,49 @@ template <int kFmt>
 W4_DEV float widen_row(const Params& p, int t, uint8_t* to) {
   const int lane = threadIdx.x & 31;
   const uint4* xr = reinterpret_cast<const uint4*>(p.x) + static_cast<size_t>(t) * (p.H / 8);
+  const int n = p.H / 8;
+  // eight chunks a lane at a time, that their loads are in flight together; those of 2048 columns stay for the second pass
+  constexpr int kAtOnce = 8;
+  uint4 v[kAtOnce];
+  auto fetch = [&](int i0) {
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int i = i0 + 32 * k + lane;
+      v[k] = i < n ? ld_cg_v4(xr + i) : make_uint4(0, 0, 0, 0);
+    }
+  };
   uint32_t m = 0;
-  for (int i = lane; i < p.H / 8; i += 32) {
-    const uint4 v = ld_cg_v4(xr + i);
-    m = __vmaxu2(__vmaxu2(m, v.x & 0x7FFF7FFFu), v.y & 0x7FFF7FFFu);
-    m = __vmaxu2(__vmaxu2(m, v.z & 0x7FFF7FFFu), v.w & 0x7FFF7FFFu);
+  int i0 = 0;
+#pragma unroll 1
+  for (;; i0 += 32 * kAtOnce) {
+    fetch(i0);
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      m = __vmaxu2(__vmaxu2(m, v[k].x & 0x7FFF7FFFu), v[k].y & 0x7FFF7FFFu);
+      m = __vmaxu2(__vmaxu2(m, v[k].z & 0x7FFF7FFFu), v[k].w & 0x7FFF7FFFu);
+    }
+    if (i0 + 32 * kAtOnce >= n) break;
   }
   m = __reduce_max_sync(kFull, max(m & 0xFFFFu, m >> 16));
   const int e = max(static_cast<int>(m >> 7), 15);   // biased exponent; factors are normal numbers
   const float f = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);   // 2^(14 - (e - 127))
-  for (int i = lane; i < p.H / 8; i += 32) {
-    const uint4 v = ld_cg_v4(xr + i);
-    float a[8];
-    chunk_f32<false>(v, a);
-    uint32_t h[4];
+#pragma unroll 1
+  for (;; i0 -= 32 * kAtOnce) {   // the last ones are here
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int lo = kFmt == W4_FMT_INT4 ? j : 2 * j, hi = kFmt == W4_FMT_INT4 ? j + 4 : 2 * j + 1;
-      asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[j]) : "f"(a[hi] * f), "f"(a[lo] * f));
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int i = i0 + 32 * k + lane;
+      float a[8];
+      chunk_f32<false>(v[k], a);
+      uint32_t h[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int lo = kFmt == W4_FMT_INT4 ? j : 2 * j, hi = kFmt == W4_FMT_INT4 ? j + 4 : 2 * j + 1;
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[j]) : "f"(a[hi] * f), "f"(a[lo] * f));
+      }
+      if (i < n) *reinterpret_cast<uint4*>(to + i * 16) = make_uint4(h[0], h[1], h[2], h[3]);
     }
-    *reinterpret_cast<uint4*>(to + i * 16) = make_uint4(h[0], h[1], h[2], h[3]);
+    if (i0 == 0) break;
+    fetch(i0 - 32 * kAtOnce);
   }
   return __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
 }
@@ -308,18 +331,24 @@ __global__ void __launch_bounds__(kThreads, 1) moe_decode_kernel(const __grid_co
     c.abort_flag = 0;
     fence_mbar_init();
   }
-  route_prepare<kThreads>(r);
-  // down: the up kernel lets this one go when all before it are done, so the logits are there
-  if (!kDown) grid_dependency_wait();
-  launch_dependents();
   const int x_pitch = 2 * p.H + 64;   // two tokens' pieces lie in different banks
-  route_all<kThreads>(p.route, r, reinterpret_cast<uint32_t*>(ring), [&](int w) {
-    const int t = T <= 8 ? w - 8 : w;   // by warps that route no token, where there are
-    if (!kDown && t >= 0 && t < T) {
-      const float f = widen_row<kFmt>(p, t, rest + t * x_pitch);
-      if (lane == 0) r.x_scale[t] = f;
-    }
-  });
+  if constexpr (kDown) {
+    launch_dependents();
+    grid_dependency_wait();
+    take_choice<kThreads>(r, p.choice);
+  } else {
+    grid_dependency_wait();
+    launch_dependents();
+    route_prepare<kThreads>(r);
+    route_all<kThreads>(p.route, r, reinterpret_cast<uint32_t*>(ring), [&](int w) {
+      const int t = T <= 8 ? w - 8 : w;   // by warps that route no token, where there are
+      if (t >= 0 && t < T) {
+        const float f = widen_row<kFmt>(p, t, rest + t * x_pitch);
+        if (lane == 0) r.x_scale[t] = f;
+      }
+    });
+    if (blockIdx.x == 0) keep_choice<kThreads>(r, p.choice);
+  }
 
   // units of this CTA: up, a share of all (expert, 16 columns) in order; down, every split-th expert.
   // A group takes every kGroups-th of them.
@@ -377,7 +406,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_decode_kernel(const __grid_co
     float* out = reinterpret_cast<float*>(rest) + group * T * kRows;   // down: [T][32]
     if constexpr (kDown) {
       for (int i = tid; i < T * kRows; i += kGroupThreads) out[i] = 0.f;
-      grid_dependency_wait();   // the activations, and y may still be read
     }
     int count = 0, slot = 0, phase = 0, scale_at = 0, turn = 0;
     bool ok = true;
@@ -579,7 +607,8 @@ cudaError_t run(const MoeDecodeArgs& a, cudaStream_t s) {
   p.w_scale = static_cast<const uint8_t*>(kDown ? a.down_scale : a.gate_up_scale);
   p.w_global = kDown ? a.down_global : a.gate_up_global;
   p.x = static_cast<const uint16_t*>(a.x);
-  p.act = static_cast<uint16_t*>(a.workspace);
+  p.choice = static_cast<uint4*>(a.workspace);
+  p.act = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(a.workspace) + kMoeChoiceBytes);
   p.act_exp = reinterpret_cast<uint8_t*>(p.act + static_cast<size_t>(T) * a.route.k * a.I);
   p.y = static_cast<uint16_t*>(a.y);
   p.H = static_cast<int>(a.H);
@@ -617,7 +646,7 @@ bool moe_decode_fits(const MoeDecodeArgs& a) {
 }
 
 size_t moe_decode_workspace_bytes(int64_t T, int64_t k, int64_t I) {
-  const size_t halves = static_cast<size_t>(T * k) * static_cast<size_t>(2 * I + I / 8), sums = moe_decode_fp4_workspace_bytes(T, k, I);
+  const size_t halves = kMoeChoiceBytes + static_cast<size_t>(T * k) * static_cast<size_t>(2 * I + I / 8), sums = moe_decode_fp4_workspace_bytes(T, k, I);
   return ((halves > sums ? halves : sums) + 15) / 16 * 16;
 }
 

@@ -29,8 +29,14 @@
 // fp32 sums are added by the down kernel. down: a CTA has 128 outputs and every split-th
 // chosen expert, builds the activations' terms while the weights before are multiplied, and
 // adds the experts' outputs in order; the CTAs of a cluster add theirs by token. Every sum
-// has a fixed order. The down kernel routes for itself and starts its weights while the up
-// kernel still runs.
+// has a fixed order. Where an SM holds a CTA of either kernel, the down kernel routes for itself
+// and starts its weights while the up kernel still runs; else it takes the up kernel's choice
+// (16 tokens: 108 us with a choice of its own, 101 without).
+//
+// 16 tokens, 64 experts of 2048 x 1408 in nvfp4, 8 chosen (some 57 of them, 280 MB, 41 us at the
+// copy rate): 101 us, the up kernel 40 (10 until the digits of x are there, 28 at the rate of
+// memory), the down kernel 60, of which the activations' digits are most. 5 tokens, 96 experts
+// of 1024 x 704 in mxfp4, 6 chosen: 25 us.
 #include <cstring>
 
 #include "common.cuh"
@@ -64,6 +70,7 @@ struct Params {
   const float* up_global;  // [E] or null
   const float* down_global;
   const uint4* x;          // bf16 [T, H]
+  uint4* choice;           // the up kernel's, for the down kernel
   float* part;             // [kParts][rows][2I]: rows of a tile together, 64 gate and 64 up
   uint16_t* y;             // bf16 [T, H]
   int H, I, K, KS, SB;     // of the kernel's weights: columns, stages, scale bytes a row
@@ -344,9 +351,9 @@ __global__ void __launch_bounds__(kThreads, 2) up_kernel(const __grid_constant__
     tc::prefetch_tmap(&p.tm_w);
     if (p.tma_scales) tc::prefetch_tmap(&p.tm_ws);
   }
-  route_prepare<kThreads>(r);
   grid_dependency_wait();
   launch_dependents();
+  route_prepare<kThreads>(r);
   route_all<kThreads>(p.route, r, reinterpret_cast<uint32_t*>(ring), [&](int w) {
     // a token's x in digits, by a warp that routes none where there are
     const int t = T <= 8 ? w - 8 : w;
@@ -382,6 +389,7 @@ __global__ void __launch_bounds__(kThreads, 2) up_kernel(const __grid_constant__
     }
     tc::fence_proxy_async_smem();
   });
+  if (blockIdx.x == 0) keep_choice<kThreads>(r, p.choice);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -483,10 +491,14 @@ __global__ void __launch_bounds__(kThreads, kTogether ? 2 : 1) down_kernel(const
     tc::prefetch_tmap(&p.tm_w);
     if (p.tma_scales) tc::prefetch_tmap(&p.tm_ws);
   }
-  route_prepare<kThreads>(r);
-  // the up kernel lets this one go when all before it are done, so the logits are there
   launch_dependents();
-  route_all<kThreads>(p.route, r, reinterpret_cast<uint32_t*>(ring), [](int) {});
+  if constexpr (kTogether) {   // while the up kernel runs, which let this one go when all before it were done: the logits are there
+    route_prepare<kThreads>(r);
+    route_all<kThreads>(p.route, r, reinterpret_cast<uint32_t*>(ring), [](int) {});
+  } else {
+    grid_dependency_wait();
+    take_choice<kThreads>(r, p.choice);
+  }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -733,7 +745,8 @@ cudaError_t run(const MoeDecodeArgs& a, bool down, cudaStream_t s) {
   p.up_global = a.gate_up_global;
   p.down_global = a.down_global;
   p.x = static_cast<const uint4*>(a.x);
-  p.part = static_cast<float*>(a.workspace);
+  p.choice = static_cast<uint4*>(a.workspace);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kMoeChoiceBytes);
   p.y = static_cast<uint16_t*>(a.y);
   p.NC = columns(down ? kBlock : a.route.T);
   p.token_rows = a.route.T <= 8 ? 8 : 16;
@@ -773,7 +786,7 @@ cudaError_t run(const MoeDecodeArgs& a, bool down, cudaStream_t s) {
 }  // namespace
 
 size_t moe_decode_fp4_workspace_bytes(int64_t T, int64_t k, int64_t I) {
-  return static_cast<size_t>(kParts) * static_cast<size_t>(T * k) * static_cast<size_t>(2 * I) * sizeof(float);
+  return kMoeChoiceBytes + static_cast<size_t>(kParts) * static_cast<size_t>(T * k) * static_cast<size_t>(2 * I) * sizeof(float);
 }
 
 // Room for three stages beside the activations.
