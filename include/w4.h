@@ -501,7 +501,7 @@ w4_status w4_fp8_block_moe_gemm_bf16in(const void* x, int64_t T, const int32_t* 
  *     W4_FMT_MXFP4: blocks of 32, scale 2^(byte - 127) (e8m0; 255 is NaN);
  *     W4_FMT_NVFP4: blocks of 16, scale e4m3 times an fp32 scale of the whole
  *                   tensor, which is a device scalar (`global`; NULL: 1; must be NULL
- *                   for mxfp4, else W4_ERR_UNSUPPORTED).
+ *                   for mxfp4, else W4_ERR_UNSUPPORTED). No block scale is negative.
  *
  * w4_quant_fp4: x [M, K] bf16 or fp16 to codes q [M, K/2] bytes and scale [M, K/32]
  * (mxfp4) or [M, K/16] (nvfp4) bytes, activations or weights alike. With amax

@@ -175,7 +175,7 @@ struct Place {
 // 2^e, -127 <= e <= 127: the least is not a normal number.
 W4_DEV float two_to(int e) { return __uint_as_float(e == -127 ? 0x00400000u : static_cast<uint32_t>(e + 127) << 23); }
 W4_DEV uint32_t e4m3_f16x2(uint32_t s8) { return e4m3x2_to_f16x2(s8 * 0x0101u); }   // twice
-W4_DEV float e8m0_f32(uint32_t s8) { return __uint_as_float(s8 << 23); }               // 0 for 2^-127, infinite for NaN
+W4_DEV float e8m0_f32(uint32_t s8) { return __uint_as_float(s8 == 0 ? 1u << 22 : s8 == 255 ? 0x7FC00000u : s8 << 23); }
 W4_DEV float scale_int4(const uint8_t* row, int grp) { return half_bits_to_f32(reinterpret_cast<const uint16_t*>(row)[grp]); }
 
 // Where this lane's two MMA blocks find their rows: block m has rows r, r + 8 of the MMA from
@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_decode_kernel(const __grid_co
               at = fmaf(v, gl * r.weight[first + n], at);
             }
           }
-        } else {
+        } else if (8 * nb + 2 * w < tokens) {   // a warp with no token has nothing to do here
           // thread: column tid % 16 of the unit, token tid / 16
           const int i = tid & 15, n = 8 * nb + (tid >> 4);
           const int k = min(n, tokens - 1), l = (i & 7) * 4 + (k & 7) / 2, j = k & 1;
