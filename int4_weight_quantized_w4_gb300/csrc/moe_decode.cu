@@ -308,7 +308,9 @@ struct Common {
   int abort_flag;
 };
 
-template <int kFmt, bool kDown>
+// kEights: of tokens, two where there are more than eight. (For fewer the code of one alone, which is read from the
+// instruction cache for every piece.)
+template <int kFmt, bool kDown, int kEights>
 __global__ void __launch_bounds__(kThreads, 1) moe_decode_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
@@ -413,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_decode_kernel(const __grid_co
       const int first = r.first[at.a], tokens = r.first[at.a + 1] - first;
       const uint8_t* scales = my_scales + scale_at * scale_slot;
       const float gl = p.w_global != nullptr ? __ldcg(p.w_global + r.expert[at.a]) : 1.f;
-      float y[2][2][4] = {};   // [eight tokens][block]
+      float y[kEights][2][4] = {};   // [eight tokens][block]
       for (int ch = 0; ch < p.chunks; ++ch, ++count) {
         const int c0 = ch * kChunkSteps;
         const int s0 = min(c0 + kPer * w, steps), s1 = min(s0 + kPer, steps);
@@ -435,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_decode_kernel(const __grid_co
         // after a time-out the group goes on without waiting, so that its warps still meet
         ok = ok && wait_warp(&c.full[group][slot], phase, abort_flag, p.status);
 #pragma unroll
-        for (int nb = 0; nb < 2; ++nb) {
+        for (int nb = 0; nb < kEights; ++nb) {
           if (8 * nb >= tokens || s0 >= s1) break;
           const int row = row_of(nb);
           if constexpr (kDown) {
@@ -489,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_decode_kernel(const __grid_co
       }
       if (++scale_at == p.scale_slots) scale_at = 0;
 #pragma unroll
-      for (int nb = 0; nb < 2; ++nb) {
+      for (int nb = 0; nb < kEights; ++nb) {
         if (8 * nb >= tokens) break;
         float (*red)[2][32][4] = c.red[group][turn];   // two in turn, so that one meeting is enough
         turn ^= 1;
@@ -595,7 +597,7 @@ Layout layout_of(const MoeDecodeArgs& a, bool down) {
   return l;
 }
 
-template <int kFmt, bool kDown>
+template <int kFmt, bool kDown, int kEights>
 cudaError_t run(const MoeDecodeArgs& a, cudaStream_t s) {
   const Layout l = layout_of(a, kDown);
   if (l.slots < 2) return cudaErrorInvalidConfiguration;   // refused before (moe_decode_fits)
@@ -630,13 +632,17 @@ cudaError_t run(const MoeDecodeArgs& a, cudaStream_t s) {
       if (slices * n <= grid && n <= a.route.k * T) p.split = n;
     grid = slices * p.split;
   }
-  return start<moe_decode_kernel<kFmt, kDown>>(p, grid, kThreads, static_cast<int>(l.bytes), p.split, s);
+  return start<moe_decode_kernel<kFmt, kDown, kEights>>(p, grid, kThreads, static_cast<int>(l.bytes), p.split, s);
 }
 
 template <int kFmt>
 cudaError_t run_both(const MoeDecodeArgs& a, cudaStream_t s) {
-  const cudaError_t e = run<kFmt, false>(a, s);
-  return e == cudaSuccess ? run<kFmt, true>(a, s) : e;
+  if (a.route.T > 8) {
+    const cudaError_t e = run<kFmt, false, 2>(a, s);
+    return e == cudaSuccess ? run<kFmt, true, 2>(a, s) : e;
+  }
+  const cudaError_t e = run<kFmt, false, 1>(a, s);
+  return e == cudaSuccess ? run<kFmt, true, 1>(a, s) : e;
 }
 
 }  // namespace
