@@ -27,12 +27,12 @@
 // largest of them before it multiplies. fp16 rounds a to 11 bits where a bf16 step would
 // leave 8.
 //
-// One token, 64 experts of 2048 x 1408 in int4, 8 chosen (34.6 MB, 5.3 us at the copy rate): 26 us,
+// One token, 64 experts of 2048 x 1408 in int4, 8 chosen (34.6 MB, 5.3 us at the copy rate): 23 us,
 // of which 4 go to the choice of experts and 4 to the second kernel's start, most of the rest to
-// instructions: 31 for a lane's word of weights, 11 of them the widening and the product, at half
-// an instruction a cycle. 8 tokens (42 experts): 80 us, 16 tokens: 103. (Measured against this: a second
-// CTA on an SM, with two groups or 64 registers a thread, 34 and 42 us for the one token; a last unit
-// cut among the groups, the same, as the instructions remain.)
+// instructions: some 26 for a lane's word of weights, 14 of them the widening and the product, at
+// half an instruction a cycle. 8 tokens (42 experts): 70 us, 16 tokens: 101. (Measured beside it: a
+// second CTA on an SM, with two groups or 64 registers a thread, 34 and 42 us where this took 26;
+// a last unit cut among the groups, the same, as the instructions remain.)
 //
 // Every sum has a fixed order: outputs are the same every time.
 #include "common.cuh"
@@ -188,7 +188,8 @@ struct RowsOf {
 
 // Adds this warp's steps [s0, s1), at most kPer, to y[block]; the slot starts at step c0. b(i)
 // are the lane's 8 activations of step s0 + i (columns 8 (lane % 4) ..) of token lane / 4.
-template <int kFmt, bool kDown, class B>
+// kWhole: int4, kPer steps that have one scale.
+template <int kFmt, bool kDown, bool kWhole, class B>
 W4_DEV void multiply(const Params& p, const uint8_t* slot, const uint8_t* scales, int c0, int s0, int s1, B b,
                      float (&y)[2][4]) {
   using R = RowsOf<kDown>;
@@ -272,27 +273,27 @@ W4_DEV void multiply(const Params& p, const uint8_t* slot, const uint8_t* scales
 #pragma unroll
         for (int h = 0; h < 2; ++h) f[m][h] = scale_int4(sc[m][h], grp);
     };
-    int grp = p.group_shift >= 0 ? s0 >> p.group_shift : s0 / p.group_steps;
-    const int end = (grp + 1) * p.group_steps;
+    int grp = kWhole || p.group_shift >= 0 ? s0 >> p.group_shift : s0 / p.group_steps;
     scales_of(grp);
-    if (s1 - s0 == kPer && s1 <= end) {   // one scale for all
+    const int end = (grp + 1) * p.group_steps;
+    if (kWhole || (s1 - s0 == kPer && s1 <= end)) {   // one scale for all
 #pragma unroll
       for (int i = 0; i < kPer; ++i) step(s0 + i, b(i), none, d);
       add(f, d);
-    } else {
-      int left = end - s0;
+      return;
+    }
+    int left = end - s0;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        if (s0 + i >= s1) break;
-        step(s0 + i, b(i), none, d);
-        if (--left == 0 || s0 + i + 1 == s1) {   // the end of a scale's columns, or of this warp's
-          add(f, d);
-          if (s0 + i + 1 == s1) break;
+    for (int i = 0; i < kPer; ++i) {
+      if (s0 + i >= s1) break;
+      step(s0 + i, b(i), none, d);
+      if (--left == 0 || s0 + i + 1 == s1) {   // the end of a scale's columns, or of this warp's
+        add(f, d);
+        if (s0 + i + 1 == s1) break;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) d[j >> 2][j & 3] = 0.f;
-          scales_of(++grp);
-          left = p.group_steps;
-        }
+        for (int j = 0; j < 8; ++j) d[j >> 2][j & 3] = 0.f;
+        scales_of(++grp);
+        left = p.group_steps;
       }
     }
   }
@@ -308,9 +309,8 @@ struct Common {
   int abort_flag;
 };
 
-// kEights: of tokens, two where there are more than eight. (For fewer the code of one alone, which is read from the
-// instruction cache for every piece.)
-template <int kFmt, bool kDown, int kEights>
+// kEights: of tokens, two where there are more than eight. kWhole: as multiply.
+template <int kFmt, bool kDown, int kEights, bool kWhole>
 __global__ void __launch_bounds__(kThreads, 1) moe_decode_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_decode_kernel(const __grid_co
           const uint8_t* er = p.act_exp + static_cast<size_t>(row_of(nb)) * (p.K / 8) + q;
 #pragma unroll
           for (int i = 0; i < kPer; ++i)
-            if (s0 + i < s1) {
+            if (kWhole ? s0 < s1 : s0 + i < s1) {
               v[i] = ld_cg_v4(ar + 32 * (s0 + i));
               e[i] = __ldcg(er + 4 * (s0 + i));
             }
@@ -445,12 +445,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_decode_kernel(const __grid_co
             if (nb > 0) fetch(nb);
 #pragma unroll
             for (int i = 0; i < kPer; ++i)
-              if (s0 + i < s1) top = max(top, e[i]);
+              if (kWhole || s0 + i < s1) top = max(top, e[i]);
             top = max(top, __shfl_xor_sync(kFull, top, 1));
             top = max(top, __shfl_xor_sync(kFull, top, 2));
 #pragma unroll
             for (int i = 0; i < kPer; ++i)
-              if (s0 + i < s1) {
+              if (kWhole || s0 + i < s1) {
                 const float f = __uint_as_float(static_cast<uint32_t>(max(127 + e[i] - top, 0)) << 23);
                 uint32_t h;
                 asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(h) : "f"(f));
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_decode_kernel(const __grid_co
                 asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(v[i].w) : "r"(h));
               }
             float d[2][4] = {};
-            multiply<kFmt, kDown>(p, piece, scales, c0, s0, s1, [&](int i) { return v[i]; }, d);
+            multiply<kFmt, kDown, kWhole>(p, piece, scales, c0, s0, s1, [&](int i) { return v[i]; }, d);
             // a factor 2^(top - 127 - 14) for this lane's two columns
             const int t0 = __shfl_sync(kFull, top, 8 * q), t1 = __shfl_sync(kFull, top, 8 * q + 4);
             const float f0 = two_to(t0 - 141), f1 = two_to(t1 - 141);
@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_decode_kernel(const __grid_co
             }
           } else {
             const uint8_t* xr = rest + r.token[row] * x_pitch + 64 * s0 + 16 * q;
-            multiply<kFmt, kDown>(p, piece, scales, c0, s0, s1,
+            multiply<kFmt, kDown, kWhole>(p, piece, scales, c0, s0, s1,
                            [&](int i) { return *reinterpret_cast<const uint4*>(xr + 64 * i); }, y[nb]);
           }
         }
@@ -597,7 +597,7 @@ Layout layout_of(const MoeDecodeArgs& a, bool down) {
   return l;
 }
 
-template <int kFmt, bool kDown, int kEights>
+template <int kFmt, bool kDown, int kEights, bool kWhole>
 cudaError_t run(const MoeDecodeArgs& a, cudaStream_t s) {
   const Layout l = layout_of(a, kDown);
   if (l.slots < 2) return cudaErrorInvalidConfiguration;   // refused before (moe_decode_fits)
@@ -632,17 +632,26 @@ cudaError_t run(const MoeDecodeArgs& a, cudaStream_t s) {
       if (slices * n <= grid && n <= a.route.k * T) p.split = n;
     grid = slices * p.split;
   }
-  return start<moe_decode_kernel<kFmt, kDown, kEights>>(p, grid, kThreads, static_cast<int>(l.bytes), p.split, s);
+  return start<moe_decode_kernel<kFmt, kDown, kEights, kWhole>>(p, grid, kThreads, static_cast<int>(l.bytes), p.split, s);
+}
+
+// A kernel's code for eight tokens and for scales of whole pieces of a warp is shorter: what is not
+// in it need not come from the instruction cache (int4, 8 tokens: 78 us for any number and group,
+// 74 for eight, 70 for both; with more tokens the latter spills registers, 111 for 101).
+template <int kFmt, bool kDown>
+cudaError_t run_fitting(const MoeDecodeArgs& a, cudaStream_t s) {
+  if constexpr (kFmt == W4_FMT_INT4) {
+    const int steps = (kDown ? a.down_group : a.gate_up_group) / 32;
+    if (a.route.T <= 8 && steps % kPer == 0 && (steps & (steps - 1)) == 0 && (kDown ? a.I : a.H) % (32 * kPer) == 0)
+      return run<kFmt, kDown, 1, true>(a, s);
+  }
+  return a.route.T > 8 ? run<kFmt, kDown, 2, false>(a, s) : run<kFmt, kDown, 1, false>(a, s);
 }
 
 template <int kFmt>
 cudaError_t run_both(const MoeDecodeArgs& a, cudaStream_t s) {
-  if (a.route.T > 8) {
-    const cudaError_t e = run<kFmt, false, 2>(a, s);
-    return e == cudaSuccess ? run<kFmt, true, 2>(a, s) : e;
-  }
-  const cudaError_t e = run<kFmt, false, 1>(a, s);
-  return e == cudaSuccess ? run<kFmt, true, 1>(a, s) : e;
+  const cudaError_t e = run_fitting<kFmt, false>(a, s);
+  return e == cudaSuccess ? run_fitting<kFmt, true>(a, s) : e;
 }
 
 }  // namespace
