@@ -18,7 +18,7 @@
 // Three forms:
 //  * stream (few rows): weights on the MMA's 128 rows, X tokens on its columns; dense
 //    products share a tile's k among the CTAs of a cluster. Bound by the weight bytes.
-//  * tile: 128 tokens on the MMA's rows, 192 outputs on its columns, with two
+//  * tile (where its waves are fewer): 128 tokens on the MMA's rows, 192 outputs on its columns, with two
 //    accumulators, so that the MMAs of a tile run while the one before leaves.
 //  * pair (many rows): two CTAs share a tile of 256 tokens and 192 outputs (cta_group::2):
 //    each copies its 128 tokens and half of the weights. What an SM takes in is what
@@ -590,8 +590,19 @@ cudaError_t launch(const Fp4Args& a, Params& p, cudaStream_t s) {
   if (rows <= 16) return run<128, 16, kNv, kStream>(a, p, s);
   if (rows <= 32) return run<128, 32, kNv, kStream>(a, p, s);
   if (rows <= 64) return run<128, 64, kNv, kStream>(a, p, s);
-  if (!experts && rows <= 128) return run<128, 128, kNv, kStream>(a, p, s);
-  if (rows <= 192) return run<192, 128, kNv, kTile>(a, p, s);
+  if (!experts) {
+    const int64_t sms = current_sm_count();
+    auto tiles = [&](int64_t x, int64_t w) { return (a.R + x - 1) / x * ((a.N + w - 1) / w); };
+    // Clusters that cut k where the weights' tiles are few: 300 x 2048 x 8192 nvfp4 10.4 us, pairs
+    // 12.7. With room for two parts only they are even (256 x 4096 x 4096 8.6 against 8.4).
+    if (rows <= 128 || 3 * tiles(128, 128) <= sms) return run<128, 128, kNv, kStream>(a, p, s);
+    // A wave of tiles takes 1.1 times one of pairs, and wastes fewer rows: 517 x 11008 x 4096 nvfp4 16.3
+    // us in two waves, 19.0 in three of pairs; 768 rows, three of either, 21.6 and 19.7.
+    const int64_t waves = (tiles(128, 192) + sms - 1) / sms, pair_waves = (tiles(256, 192) + sms / 2 - 1) / (sms / 2);
+    if (rows <= 192 || 11 * waves < 10 * pair_waves) return run<192, 128, kNv, kTile>(a, p, s);
+  } else if (rows <= 192) {
+    return run<192, 128, kNv, kTile>(a, p, s);
+  }
   return run<192, 128, kNv, kPair>(a, p, s);
 }
 

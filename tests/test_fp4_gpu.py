@@ -291,3 +291,28 @@ def test_tokens_quantized_once_give_the_same_rows(fmt):
     torch.cuda.synchronize()
     assert w4.w4_device_status() == w4.W4_ERR_SHAPE
     assert torch.equal(y, z) and (y[[5, 9]] == 0).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,N,k", [(257, 5000, 1), (513, 2696, 7), (900, 2056, 16), (1300, 1992, 3)])
+def test_linear_of_many_rows(fmt, M, N, k):
+    """Pairs of CTAs: rows and outputs that end inside a tile, a second CTA with no rows, odd numbers of stages."""
+    check_linear(M, N, k * STEP[fmt], fmt, bias=M % 2 == 0, seed=M)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_linear_of_rows_that_fill_fewer_tiles_than_pairs(fmt):
+    check_linear(517, 11008, STEP[fmt], fmt)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,N,k", [(300, 264, 33), (390, 1000, 16), (200, 2048, 20)])
+def test_linear_of_few_weight_tiles(fmt, M, N, k):
+    """Clusters that cut k among more rows than one tile holds."""
+    check_linear(M, N, k * STEP[fmt], fmt, bias=True, seed=k)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("counts", [[600, 0, 3, 470], [1, 1025], [255, 257, 129, 384]])
+def test_experts_of_many_rows(fmt, counts):
+    test_experts(fmt, counts)
