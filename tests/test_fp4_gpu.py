@@ -316,3 +316,10 @@ def test_linear_of_few_weight_tiles(fmt, M, N, k):
 @pytest.mark.parametrize("counts", [[600, 0, 3, 470], [1, 1025], [255, 257, 129, 384]])
 def test_experts_of_many_rows(fmt, counts):
     test_experts(fmt, counts)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,K", [(2101, 4064), (8193, 1024)])
+def test_quant_of_many_elements_is_bit_exact(fmt, M, K):
+    """Several blocks a thread, and a last warp with some of its threads' second ones."""
+    test_quant_is_bit_exact(fmt, M, K, False)
