@@ -632,7 +632,7 @@ cudaError_t run(const MoeDecodeArgs& a, cudaStream_t s) {
       if (slices * n <= grid && n <= a.route.k * T) p.split = n;
     grid = slices * p.split;
   }
-  return start<moe_decode_kernel<kFmt, kDown, kEights, kWhole>>(p, grid, kThreads, static_cast<int>(l.bytes), p.split, s);
+  return start<moe_decode_kernel<kFmt, kDown, kEights, kWhole>>(p, grid, kThreads, static_cast<int>(l.bytes), p.split, s, 232448);
 }
 
 // A kernel's code for eight tokens and for scales of whole pieces of a warp is shorter: what is not

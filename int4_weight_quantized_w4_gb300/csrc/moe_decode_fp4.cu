@@ -775,12 +775,12 @@ cudaError_t run(const MoeDecodeArgs& a, bool down, cudaStream_t s) {
   p.stages = down ? dn : up;
   p.split = 1;
   const int smem = static_cast<int>(smem_bytes(a, down, p.stages));
-  if (!down) return a.route.T <= 8 ? start<up_kernel<kNv, 8>>(p, p.up_ctas, kThreads, smem, 1, s) : start<up_kernel<kNv, 16>>(p, p.up_ctas, kThreads, smem, 1, s);
+  if (!down) return a.route.T <= 8 ? start<up_kernel<kNv, 8>>(p, p.up_ctas, kThreads, smem, 1, s, 232448) : start<up_kernel<kNv, 16>>(p, p.up_ctas, kThreads, smem, 1, s, 232448);
   const int64_t slices = (a.H + 127) / 128;
   for (int n = kMaxSplit; n > 1 && p.split == 1; n /= 2)
     if (slices * n <= current_sm_count() && n <= p.rows) p.split = n;
-  return together ? start<down_kernel<kNv, true>>(p, slices * p.split, kThreads, smem, p.split, s)
-                  : start<down_kernel<kNv, false>>(p, slices * p.split, kThreads, smem, p.split, s);
+  return together ? start<down_kernel<kNv, true>>(p, slices * p.split, kThreads, smem, p.split, s, 232448)
+                  : start<down_kernel<kNv, false>>(p, slices * p.split, kThreads, smem, p.split, s, 232448);
 }
 
 }  // namespace

@@ -186,9 +186,10 @@ cudaError_t encode(CUtensorMap* m, const void* base, int64_t K, int64_t rows, in
 
 // Lets a kernel use its dynamic shared memory: once per device, since the call
 // costs as much as the rest of the host path put together. A device reset takes
-// the setting back; the launch that then fails is repeated with it set again.
+// the setting back; the launch that then fails is repeated with it set again. `most`: the most
+// shared memory of any launch, where they differ: a launch that is captured must not fail first.
 template <auto kKernel, class P>
-cudaError_t start(const P& p, int64_t grid, int threads, int smem, int cluster, cudaStream_t s) {
+cudaError_t start(const P& p, int64_t grid, int threads, int smem, int cluster, cudaStream_t s, int most = 0) {
   static std::atomic<uint64_t> set{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -200,7 +201,7 @@ cudaError_t start(const P& p, int64_t grid, int threads, int smem, int cluster, 
     if (e != cudaErrorInvalidValue) return e;
     cudaGetLastError();
   }
-  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most > smem ? most : smem);
   if (e != cudaSuccess) return e;
   e = cudaLaunchKernelEx(&pl.cfg, kKernel, p);
   if (e == cudaSuccess && dev < 64) set.fetch_or(bit, std::memory_order_relaxed);

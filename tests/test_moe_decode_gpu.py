@@ -226,3 +226,23 @@ def test_masked_logits(fmt):
     err = np.abs(y[[0, 2]].float().cpu().numpy() - r)
     assert (err <= 2.0 ** -8 * np.abs(r) + 2.0 ** -10 * size).all()
     assert (y[1] == 0).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T", [3, 12])
+def test_a_larger_call_captured_after_a_smaller_one(fmt, T):
+    """Kernels whose shared memory grows with the sizes: the first larger call may be one that is captured."""
+    Experts(4, 64, 64, fmt).call(*inputs(T, 64, 4), 2)
+    ex = Experts(4, 2048, 1024, fmt, group=128)
+    xb, logits = inputs(T, 2048, 4, seed=T)
+    (u, us, ug), (d, ds, dg) = ex.parts
+    u, us, d, ds, ug, dg = (None if a is None else to_dev(a) for a in (u, us, d, ds, ug, dg))
+    x, lg = bf16(xb), to_dev(logits)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = w4.w4_moe_decode(x, lg, u, us, d, ds, 2, fmt, gate_up_global=ug, down_global=dg)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert w4.w4_device_status() == w4.W4_OK
+    assert torch.equal(y, ex.call(xb, logits, 2))
