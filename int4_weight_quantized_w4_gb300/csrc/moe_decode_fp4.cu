@@ -31,10 +31,10 @@
 // adds the experts' outputs in order; the CTAs of a cluster add theirs by token. Every sum
 // has a fixed order. Where an SM holds a CTA of either kernel, the down kernel routes for itself
 // and starts its weights while the up kernel still runs; else it takes the up kernel's choice
-// (16 tokens: 108 us with a choice of its own, 101 without).
+// (16 tokens: 108 us with a choice of its own, 102 without).
 //
 // 16 tokens, 64 experts of 2048 x 1408 in nvfp4, 8 chosen (some 57 of them, 280 MB, 41 us at the
-// copy rate): 101 us, the up kernel 40 (10 until the digits of x are there, 28 at the rate of
+// copy rate): 102 us, the up kernel 40 (10 until the digits of x are there, 28 at the rate of
 // memory), the down kernel 60, of which the activations' digits are most. 5 tokens, 96 experts
 // of 1024 x 704 in mxfp4, 6 chosen: 25 us.
 #include <cstring>
