@@ -351,9 +351,9 @@ __global__ void __launch_bounds__(kThreads, 2) up_kernel(const __grid_constant__
     tc::prefetch_tmap(&p.tm_w);
     if (p.tma_scales) tc::prefetch_tmap(&p.tm_ws);
   }
-  grid_dependency_wait();
-  launch_dependents();
   route_prepare<kThreads>(r);
+  grid_dependency_wait();
+  launch_dependents();   // this CTA has its tensor memory, which the next kernels could else take first
   route_all<kThreads>(p.route, r, reinterpret_cast<uint32_t*>(ring), [&](int w) {
     // a token's x in digits, by a warp that routes none where there are
     const int t = T <= 8 ? w - 8 : w;
@@ -491,11 +491,14 @@ __global__ void __launch_bounds__(kThreads, kTogether ? 2 : 1) down_kernel(const
     tc::prefetch_tmap(&p.tm_w);
     if (p.tma_scales) tc::prefetch_tmap(&p.tm_ws);
   }
-  launch_dependents();
+  // The next kernels may come once this CTA has its tensor memory, which they could else take first.
   if constexpr (kTogether) {   // while the up kernel runs, which let this one go when all before it were done: the logits are there
     route_prepare<kThreads>(r);
+    launch_dependents();
     route_all<kThreads>(p.route, r, reinterpret_cast<uint32_t*>(ring), [](int) {});
   } else {
+    __syncthreads();
+    launch_dependents();
     grid_dependency_wait();
     take_choice<kThreads>(r, p.choice);
   }
