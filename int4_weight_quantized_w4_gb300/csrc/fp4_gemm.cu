@@ -596,14 +596,8 @@ cudaError_t launch(const Fp4Args& a, Params& p, cudaStream_t s) {
     // Clusters that cut k where the weights' tiles are few: 300 x 2048 x 8192 nvfp4 10.4 us, pairs
     // 12.7. With room for two parts only they are even (256 x 4096 x 4096 8.6 against 8.4).
     if (rows <= 128 || 3 * tiles(128, 128) <= sms) return run<128, 128, kNv, kStream>(a, p, s);
-    // A wave of tiles takes 1.1 times one of pairs, and wastes fewer rows: 517 x 11008 x 4096 nvfp4 16.3
-    // us in two waves, 19.0 in three of pairs; 768 rows, three of either, 21.6 and 19.7.
-    const int64_t waves = (tiles(128, 192) + sms - 1) / sms, pair_waves = (tiles(256, 192) + sms / 2 - 1) / (sms / 2);
-    if (rows <= 192 || 11 * waves < 10 * pair_waves) return run<192, 128, kNv, kTile>(a, p, s);
-  } else if (rows <= 192) {
-    return run<192, 128, kNv, kTile>(a, p, s);
   }
-  return run<192, 128, kNv, kPair>(a, p, s);
+  return run<192, 128, kNv, kTile>(a, p, s);
 }
 
 }  // namespace

@@ -37,7 +37,6 @@ __global__ void __launch_bounds__(kThreads) quant_fp4_kernel(const uint4* x, int
                                                              uint8_t* __restrict__ scale, unsigned int* status) {
   const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (kThreads * kItems) + threadIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");   // x may come from the kernel before, which may still read q
-  if (signals) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   uint4 v[kItems][2], u[kItems][2];   // u: kSilu
 #pragma unroll
   for (int n = 0; n < kItems; ++n) {
@@ -171,7 +170,7 @@ __global__ void __launch_bounds__(kThreads) dequant_fp4_kernel(const uint2* q, c
 
 // Quantized rows copied to their places among the expert-sorted rows: row r of (dst,
 // dst_scale) is row gather[r] of (src, src_scale), codes of K16 chunks of 16 bytes and scales
-// of SW words. A warp per row. The next kernel may start once every kernel before this one is done.
+// of SW words. A warp per row.
 __global__ void __launch_bounds__(kThreads) gather_fp4_rows_kernel(const uint4* src, const uint32_t* src_scale, int64_t T,
                                                                    int K16, int SW, const int32_t* gather, int64_t R,
                                                                    uint4* __restrict__ dst, uint32_t* __restrict__ dst_scale,
@@ -179,7 +178,6 @@ __global__ void __launch_bounds__(kThreads) gather_fp4_rows_kernel(const uint4* 
   const int lane = threadIdx.x & 31;
   const int64_t r = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
   asm volatile("griddepcontrol.wait;" ::: "memory");   // src comes from the kernel before
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (r >= R) return;
   const int64_t t = __ldcg(gather + r);
   uint4* d = dst + r * K16;

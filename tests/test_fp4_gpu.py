@@ -323,3 +323,24 @@ def test_experts_of_many_rows(fmt, counts):
 def test_quant_of_many_elements_is_bit_exact(fmt, M, K):
     """Several blocks a thread, and a last warp with some of its threads' second ones."""
     test_quant_is_bit_exact(fmt, M, K, False)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,N,K", [(4096, 11008, 4096), (700, 4096, 4096), (100, 4096, 2048), (5, 4096, 4096)])
+def test_chains_of_calls_give_the_same_bits(fmt, M, N, K):
+    """A product that starts while its quantizer still runs finds its first stages all there at once."""
+    qw, sw, gw = weights((N, K), fmt)
+    qw, sw, gw = to_dev(qw), to_dev(sw), scalar(gw)
+    xs = [torch.randn((M, K), device=dev(), generator=torch.Generator(dev()).manual_seed(i)).to(torch.bfloat16) for i in range(3)]
+    gx = scalar(np.float32(6.0 / (6 * 448))) if fmt == "nvfp4" else None
+    ref = []
+    for x in xs:
+        q, s = w4.w4_quant_fp4(x, fmt, gx)
+        torch.cuda.synchronize()
+        ref.append(w4.w4_fp4_gemm(q, s, qw, sw, fmt, gx, gw))
+        torch.cuda.synchronize()
+    for _ in range(40):
+        ys = [w4.w4_fp4_gemm_bf16in(xs[i % 3], qw, sw, fmt, gx, gw) for i in range(6)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, ref[i % 3]) for i, y in enumerate(ys))
+    assert w4.w4_device_status() == w4.W4_OK
