@@ -332,11 +332,6 @@ fp4_kernel(const __grid_constant__ Params p) {
         }
         uint32_t v[4][C::WORDS];
         load_scale_words<kNv>(from + rs * C::RAW + sub * C::WORDS * 4, blocks, v);
-        if (ks == ks1 - 1 || sub == C::SUPER - 1) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&raw_empty[rs]);
-          if (++rs == C::RAWS) rs = 0, rph ^= 1;
-        }
         if (!(ok = wait_warp(&empty[st], ph, abort_flag, p.status))) break;
         store_scale_atoms<kNv>(to + st * C::SSTAGE, pitch, v);
         tc::fence_proxy_async_smem();
@@ -346,6 +341,11 @@ fp4_kernel(const __grid_constant__ Params p) {
             tc::cluster_arrive_on(tc::cluster_addr(&full[st], 0));
           else
             mbar_arrive(&full[st]);
+        }
+        // the slot goes back once its words have arrived in registers and the fence lies between them and the next copy
+        if (ks == ks1 - 1 || sub == C::SUPER - 1) {
+          if (lane == 0) mbar_arrive(&raw_empty[rs]);
+          if (++rs == C::RAWS) rs = 0, rph ^= 1;
         }
         if (++st == C::STAGES) st = 0, ph ^= 1;
       }
