@@ -241,11 +241,6 @@ W4_DEV void turn_scales(const Params& p, Bars& bar, const uint8_t* raw, uint8_t*
 #pragma unroll
           for (int j = 0; j < kWords; ++j) v[b][j] = f[b * 16 * p.SB + 2 * j] | static_cast<uint32_t>(f[b * 16 * p.SB + 2 * j + 1]) << 16;
       }
-      if (ks == k1 - 1 || (p.tma_scales && sub == kSuper - 1)) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.raw_empty[rs]);
-        if (++rs == kRaws) rs = 0, rph ^= 1;
-      }
       if (!waited && ph == 0) {
         grid_dependency_wait();
         waited = true;
@@ -255,6 +250,11 @@ W4_DEV void turn_scales(const Params& p, Bars& bar, const uint8_t* raw, uint8_t*
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.full[st]);
+      // the slot goes back once its words have arrived in registers and the fence lies between them and the next copy
+      if (ks == k1 - 1 || (p.tma_scales && sub == kSuper - 1)) {
+        if (lane == 0) mbar_arrive(&bar.raw_empty[rs]);
+        if (++rs == kRaws) rs = 0, rph ^= 1;
+      }
       if (++st == p.stages) st = 0, ph ^= 1;
     }
 }
