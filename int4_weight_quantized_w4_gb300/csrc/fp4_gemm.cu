@@ -20,7 +20,8 @@
 //    products share a tile's k among the CTAs of a cluster. Bound by the weight bytes.
 //  * tile (where its waves are fewer): 128 tokens on the MMA's rows, 192 outputs on its columns, with two
 //    accumulators, so that the MMAs of a tile run while the one before leaves.
-//  * pair (many rows): two CTAs share a tile of 256 tokens and 192 outputs (cta_group::2):
+//  * pair (reached by no call: its arrivals on the other CTA's barriers would have to release at
+//    cluster scope, 204 us where tiles take 92): two CTAs share a tile of 256 tokens and 192 outputs (cta_group::2):
 //    each copies its 128 tokens and half of the weights. What an SM takes in is what
 //    bounds tiles of 4-bit operands, and a CTA of a pair takes in 33 KB a stage, one alone 45.
 //
