@@ -15,15 +15,13 @@
 // four stages' mxfp4), a warp per 128 rows transposes a stage's words in registers, and the
 // MMA warp sends each 512-byte atom on to tensor memory ahead of the MMAs that use it.
 //
-// Three forms:
+// Two forms:
 //  * stream (few rows): weights on the MMA's 128 rows, X tokens on its columns; dense
 //    products share a tile's k among the CTAs of a cluster. Bound by the weight bytes.
-//  * tile (where its waves are fewer): 128 tokens on the MMA's rows, 192 outputs on its columns, with two
+//  * tile (many rows): 128 tokens on the MMA's rows, 192 outputs on its columns, with two
 //    accumulators, so that the MMAs of a tile run while the one before leaves.
-//  * pair (reached by no call: its arrivals on the other CTA's barriers would have to release at
-//    cluster scope, 204 us where tiles take 92): two CTAs share a tile of 256 tokens and 192 outputs (cta_group::2):
-//    each copies its 128 tokens and half of the weights. What an SM takes in is what
-//    bounds tiles of 4-bit operands, and a CTA of a pair takes in 33 KB a stage, one alone 45.
+//    (Pairs of CTAs with cta_group::2 take in fewer bytes a stage, 33 KB for 45, but their arrivals on the
+//    other CTA's barriers have to release at cluster scope: 204 us where tiles take 92.)
 //
 // All are launched as programmatic dependents and let their own dependents go early: the
 // weights and their scales start while the kernels before finish, everything else waits.
@@ -43,7 +41,7 @@ namespace {
 constexpr int kFuseRows = 8;
 constexpr int kQuantWarps = 4;                // that take the stages in turn
 
-enum Form { kStream, kTile, kPair };
+enum Form { kStream, kTile };
 
 struct Params {
   CUtensorMap tm_x;        // codes [rows, K/2 bytes]
@@ -82,13 +80,11 @@ W4_DEV void seg_bounds(const Segments& p, int e, int& a, int& b) {
 // W: weight rows of a tile, X: tokens of a CTA's tile.
 template <int W, int X, bool kNv, Form kForm, bool kQuant = false>
 struct Shape {
-  static constexpr bool PAIR = kForm == kPair;
   static constexpr int WORDS = kNv ? 4 : 2;                    // 32-bit scale words of a row's stage
   static constexpr int SUPER = 8 / WORDS;                      // stages of a row's 32 bytes of scales
   static constexpr int N = kForm == kStream ? X : W;           // MMA columns
-  static constexpr int W_LOAD = PAIR ? W / 2 : W;              // weight rows that this CTA copies
   static constexpr int AW = (W + 127) / 128, AX = (X + 127) / 128;   // atoms of 128 rows
-  static constexpr int W_BYTES = W_LOAD * kStageBytes, X_BYTES = X * kStageBytes;
+  static constexpr int W_BYTES = W * kStageBytes, X_BYTES = X * kStageBytes;
   static constexpr int STAGE = W_BYTES + X_BYTES;
   static constexpr int SW_BYTES = AW * WORDS * 512, SSTAGE = SW_BYTES + AX * WORDS * 512;
   static constexpr int RAW_W = 128 * AW * 32, RAW = RAW_W + (X + 31) / 32 * 32 * 32;   // scales as they are in memory
@@ -99,7 +95,7 @@ struct Shape {
   static constexpr int S_COLS = 4 * WORDS * (AW + AX);         // tensor memory columns of a stage's scales
   static constexpr int USED = ACCS * N + 2 * S_COLS;
   static constexpr int TMEM_COLS = USED <= 128 ? 128 : USED <= 256 ? 256 : 512;
-  static constexpr int EPI = PAIR ? 8 : 4;                     // epilogue warps: a quarter of the lanes, a half or all of the columns
+  static constexpr int EPI = 4;                                // epilogue warps: a quarter of the lanes each
   static constexpr int THREADS = 32 * (EPI + 4 + AW + AX + (kQuant ? kQuantWarps - 2 : 0));   // quantizers for a copying and a transposing warp
   static constexpr int OUT = kForm != kStream ? EPI * 2048 : 0;
   static constexpr int BARS = 2 * STAGES + 2 * RAWS + 2 * ACCS;
@@ -122,20 +118,18 @@ fp4_kernel(const __grid_constant__ Params p) {
   // warps; below kMma: epilogue; kTurn ..: one per scale atom
   constexpr int kMma = C::EPI, kLoadW = kMma + 1, kLoadX = kQuant ? -1 : kMma + 2, kLoadS = kMma + 2 + !kQuant, kTurn = kLoadS + 1;
   constexpr int kQuant0 = kTurn + C::AW;   // kQuant: in the place of kLoadX and the activations' kTurn
-  constexpr bool P = C::PAIR;
-  constexpr int kRowsPer = P ? 2 * X : X;
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
   uint8_t* ring = smem;                               // per stage: weights, activations
   uint8_t* scales = ring + C::STAGES * C::STAGE;      // per stage: weights', activations'
   uint8_t* raw = scales + C::STAGES * C::SSTAGE;      // per slot: weights', activations'
   uint4* out_base = reinterpret_cast<uint4*>(raw + C::RAWS * C::RAW);
-  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(out_base) + C::OUT);   // pair: the first CTA's
+  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(out_base) + C::OUT);
   uint64_t* empty = full + C::STAGES;
   uint64_t* raw_full = empty + C::STAGES;
   uint64_t* raw_empty = raw_full + C::RAWS;
   uint64_t* acc_full = raw_empty + C::RAWS;
-  uint64_t* acc_empty = acc_full + C::ACCS;                                                      // pair: the first CTA's
+  uint64_t* acc_empty = acc_full + C::ACCS;                                                   
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(acc_empty + C::ACCS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int32_t* starts = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(full) + 256);
@@ -143,10 +137,9 @@ fp4_kernel(const __grid_constant__ Params p) {
   int32_t* offsets = warp_sum + 16;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = P ? cluster_rank() : 0;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
-      mbar_init(&full[i], P ? 1 + 2 * (C::AW + C::AX) : kQuant ? 2 + C::AW : 2 + C::AW + C::AX);   // operands; scale warps
+      mbar_init(&full[i], kQuant ? 2 + C::AW : 2 + C::AW + C::AX);   // operands; scale warps
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < C::RAWS; ++i) {
@@ -155,17 +148,12 @@ fp4_kernel(const __grid_constant__ Params p) {
     }
     for (int i = 0; i < C::ACCS; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], P ? 2 * C::EPI : C::EPI);
+      mbar_init(&acc_empty[i], C::EPI);
     }
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kMma) {
-    if constexpr (P)
-      tc::tmem_alloc_pair(tmem_holder, C::TMEM_COLS);
-    else
-      tc::tmem_alloc(tmem_holder, C::TMEM_COLS);
-  }
+  if (warp == kMma) tc::tmem_alloc(tmem_holder, C::TMEM_COLS);
   if (warp == kLoadW && lane == 0) tc::prefetch_tmap(&p.tm_w);
   if (warp == kLoadX && lane == 0) tc::prefetch_tmap(&p.tm_x);
   if (warp == kLoadS && lane == 0 && p.tma_scales) {
@@ -180,14 +168,10 @@ fp4_kernel(const __grid_constant__ Params p) {
       seg.offsets = offsets;
       __syncthreads();
     }
-    tile_starts<C::THREADS>(seg, kRowsPer, starts, warp_sum);
+    tile_starts<C::THREADS>(seg, X, starts, warp_sum);
   }
   tc::fence_before_sync();
   __syncthreads();
-  if constexpr (P) {   // the other CTA's barriers are set up
-    cluster_arrive();
-    cluster_wait();
-  }
   tc::fence_after_sync();
   launch_dependents();
   const uint32_t tmem = *tmem_holder;
@@ -195,19 +179,17 @@ fp4_kernel(const __grid_constant__ Params p) {
   // this CTA's part of the stages (the same for every item)
   const int part = p.split > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int ks0 = p.KS * part / p.split, ks1 = p.KS * (part + 1) / p.split;
-  const int ctas = P ? 2 : p.split;   // of one item
-  const int first = blockIdx.x / ctas, step = gridDim.x / ctas;
+  const int first = blockIdx.x / p.split, step = gridDim.x / p.split;
   const int items = p.offsets == nullptr ? p.items : min(p.items, starts[p.E] * p.n_tiles);
 
   if (warp == kLoadW || warp == kLoadX) {
-    // An operand. Pair: all four copies of a stage count on the first CTA's barrier, and its
-    // weights' warp announces them.
+    // An operand.
     const bool is_w = warp == kLoadW;
     int st = 0, ph = 1, e = 0;
     bool ok = true, waited = !is_w;
     Tile t;
     if (!is_w) grid_dependency_wait();   // the codes come from the kernel before
-    for (int it = first; ok && it < items && decode(seg, it, kRowsPer, W, starts, t, e); it += step)
+    for (int it = first; ok && it < items && decode(seg, it, X, W, starts, t, e); it += step)
       for (int ks = ks0; ks < ks1; ++ks) {
         if (!waited && ph == 0) {   // the ring is full, and is emptied only after the kernels before
           grid_dependency_wait();
@@ -216,21 +198,11 @@ fp4_kernel(const __grid_constant__ Params p) {
         if (!(ok = wait_warp(&empty[st], ph, abort_flag, p.status))) break;
         if (elect_one()) {
           uint8_t* to = ring + st * C::STAGE + (is_w ? 0 : C::W_BYTES);
-          if constexpr (P) {
-            const uint32_t bar = tc::cluster_addr(&full[st], 0);
-            if (is_w) {
-              if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * C::STAGE);
-              tc::tma_load_3d_pair(to, &p.tm_w, bar, ks * kStageBytes, t.n0 + static_cast<int>(rank) * C::W_LOAD, t.expert);
-            } else {
-              tc::tma_load_2d_pair(to, &p.tm_x, bar, ks * kStageBytes, t.row0 + static_cast<int>(rank) * X);
-            }
-          } else {
-            mbar_arrive_expect_tx(&full[st], is_w ? C::W_BYTES : C::X_BYTES);
-            if (is_w)
-              tc::tma_load_3d(to, &p.tm_w, &full[st], ks * kStageBytes, t.n0, t.expert);
-            else
-              tc::tma_load_2d(to, &p.tm_x, &full[st], ks * kStageBytes, t.row0);
-          }
+          mbar_arrive_expect_tx(&full[st], is_w ? C::W_BYTES : C::X_BYTES);
+          if (is_w)
+            tc::tma_load_3d(to, &p.tm_w, &full[st], ks * kStageBytes, t.n0, t.expert);
+          else
+            tc::tma_load_2d(to, &p.tm_x, &full[st], ks * kStageBytes, t.row0);
         }
         __syncwarp();
         if (++st == C::STAGES) st = 0, ph ^= 1;
@@ -240,8 +212,8 @@ fp4_kernel(const __grid_constant__ Params p) {
     int rs = 0, rph = 1, e = 0;
     bool ok = true, waited = false;
     Tile t;
-    for (int it = first; ok && it < items && decode(seg, it, kRowsPer, W, starts, t, e); it += step) {
-      const int row0 = t.row0 + static_cast<int>(rank) * X;
+    for (int it = first; ok && it < items && decode(seg, it, X, W, starts, t, e); it += step) {
+      const int row0 = t.row0;
       for (int ks = ks0; ks < ks1; ks = (ks / C::SUPER + 1) * C::SUPER) {
         if (!(ok = wait_warp(&raw_empty[rs], rph, abort_flag, p.status))) break;
         uint8_t* to = raw + rs * C::RAW;
@@ -325,7 +297,7 @@ fp4_kernel(const __grid_constant__ Params p) {
     bool ok = true;
     grid_dependency_wait();   // what it waits for depends on the kernels before
     Tile t;
-    for (int it = first; ok && it < items && decode(seg, it, kRowsPer, W, starts, t, e); it += step)
+    for (int it = first; ok && it < items && decode(seg, it, X, W, starts, t, e); it += step)
       for (int ks = ks0; ks < ks1; ++ks) {
         const int sub = ks % C::SUPER;
         if (ks == ks0 || sub == 0) {
@@ -337,12 +309,7 @@ fp4_kernel(const __grid_constant__ Params p) {
         store_scale_atoms<kNv>(to + st * C::SSTAGE, pitch, v);
         tc::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          if constexpr (P)
-            tc::cluster_arrive_on(tc::cluster_addr(&full[st], 0));
-          else
-            mbar_arrive(&full[st]);
-        }
+        if (lane == 0) mbar_arrive(&full[st]);
         // the slot goes back once its words have arrived in registers and the fence lies between them and the next copy
         if (ks == ks1 - 1 || sub == C::SUPER - 1) {
           if (lane == 0) mbar_arrive(&raw_empty[rs]);
@@ -352,52 +319,45 @@ fp4_kernel(const __grid_constant__ Params p) {
       }
   } else if (warp == kMma) {
     grid_dependency_wait();
-    if (rank == 0) {
-      constexpr uint32_t idesc = tc::idesc_fp4<kNv>(P ? 256 : 128, C::N);
-      const uint64_t wd0 = tc::sdesc_sw128(smem_addr(ring)), xd0 = wd0 + (C::W_BYTES >> 4);
-      const uint64_t sd0 = tc::sdesc_scales(smem_addr(scales));
-      int st = 0, ph = 0, ac = 0, aph = 1, buf = 0;
-      bool ok = true;
-      for (int it = first; ok && it < items; it += step) {
-        if (!(ok = wait_warp(&acc_empty[ac], aph, abort_flag, p.status))) break;
-        for (int ks = ks0; ks < ks1; ++ks) {
-          if (!(ok = wait_warp(&full[st], ph, abort_flag, p.status))) break;
-          tc::fence_after_sync();
-          if (elect_one()) {
-            // weights' scales, then the activations': [word][atom][4 columns] each
-            const uint32_t sw = tmem + C::ACCS * C::N + buf * C::S_COLS, sx = sw + 4 * C::WORDS * C::AW;
-            const uint64_t sd = sd0 + static_cast<uint64_t>((st * C::SSTAGE) >> 4);
+    constexpr uint32_t idesc = tc::idesc_fp4<kNv>(128, C::N);
+    const uint64_t wd0 = tc::sdesc_sw128(smem_addr(ring)), xd0 = wd0 + (C::W_BYTES >> 4);
+    const uint64_t sd0 = tc::sdesc_scales(smem_addr(scales));
+    int st = 0, ph = 0, ac = 0, aph = 1, buf = 0;
+    bool ok = true;
+    for (int it = first; ok && it < items; it += step) {
+      if (!(ok = wait_warp(&acc_empty[ac], aph, abort_flag, p.status))) break;
+      for (int ks = ks0; ks < ks1; ++ks) {
+        if (!(ok = wait_warp(&full[st], ph, abort_flag, p.status))) break;
+        tc::fence_after_sync();
+        if (elect_one()) {
+          // weights' scales, then the activations': [word][atom][4 columns] each
+          const uint32_t sw = tmem + C::ACCS * C::N + buf * C::S_COLS, sx = sw + 4 * C::WORDS * C::AW;
+          const uint64_t sd = sd0 + static_cast<uint64_t>((st * C::SSTAGE) >> 4);
 #pragma unroll
-            for (int i = 0; i < C::WORDS * (C::AW + C::AX); ++i) tc::copy_scales<P>(sw + 4 * i, sd + 32 * i);
-            const uint64_t wd = wd0 + static_cast<uint64_t>((st * C::STAGE) >> 4);
-            const uint64_t xd = xd0 + static_cast<uint64_t>((st * C::STAGE) >> 4);
-            const int left = p.K - ks * kStageK;
+          for (int i = 0; i < C::WORDS * (C::AW + C::AX); ++i) tc::copy_scales(sw + 4 * i, sd + 32 * i);
+          const uint64_t wd = wd0 + static_cast<uint64_t>((st * C::STAGE) >> 4);
+          const uint64_t xd = xd0 + static_cast<uint64_t>((st * C::STAGE) >> 4);
+          const int left = p.K - ks * kStageK;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {   // 64 columns, 32 bytes, at a time
-              if (64 * j >= left) break;
-              const int word = kNv ? j : j >> 1;
-              const uint32_t id = idesc | (kNv || !(j & 1) ? 0u : (2u << 29) | (2u << 4));
-              const uint32_t fw = sw + 4 * C::AW * word, fx = sx + 4 * C::AX * word;
-              const uint32_t acc = ks > ks0 || j > 0 ? 1u : 0u;
-              if constexpr (kForm != kStream)
-                tc::mma_fp4<kNv, P>(tmem + ac * C::N, xd + 2 * j, wd + 2 * j, id, fx, fw, acc);
-              else
-                tc::mma_fp4<kNv, P>(tmem + ac * C::N, wd + 2 * j, xd + 2 * j, id, fw, fx, acc);
-            }
-            if constexpr (P) {
-              tc::commit_pair(&empty[st]);
-              if (ks == ks1 - 1) tc::commit_pair(&acc_full[ac]);
-            } else {
-              tc::commit(&empty[st]);
-              if (ks == ks1 - 1) tc::commit(&acc_full[ac]);
-            }
+          for (int j = 0; j < 4; ++j) {   // 64 columns, 32 bytes, at a time
+            if (64 * j >= left) break;
+            const int word = kNv ? j : j >> 1;
+            const uint32_t id = idesc | (kNv || !(j & 1) ? 0u : (2u << 29) | (2u << 4));
+            const uint32_t fw = sw + 4 * C::AW * word, fx = sx + 4 * C::AX * word;
+            const uint32_t acc = ks > ks0 || j > 0 ? 1u : 0u;
+            if constexpr (kForm != kStream)
+              tc::mma_fp4<kNv>(tmem + ac * C::N, xd + 2 * j, wd + 2 * j, id, fx, fw, acc);
+            else
+              tc::mma_fp4<kNv>(tmem + ac * C::N, wd + 2 * j, xd + 2 * j, id, fw, fx, acc);
           }
-          __syncwarp();
-          buf ^= 1;
-          if (++st == C::STAGES) st = 0, ph ^= 1;
+          tc::commit(&empty[st]);
+          if (ks == ks1 - 1) tc::commit(&acc_full[ac]);
         }
-        if (++ac == C::ACCS) ac = 0, aph ^= 1;
+        __syncwarp();
+        buf ^= 1;
+        if (++st == C::STAGES) st = 0, ph ^= 1;
       }
+      if (++ac == C::ACCS) ac = 0, aph ^= 1;
     }
     __syncwarp();
   } else {
@@ -409,30 +369,23 @@ fp4_kernel(const __grid_constant__ Params p) {
     auto hand_back = [&](int acc) {   // the accumulator is read
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) {
-        if constexpr (P)
-          tc::cluster_arrive_on(tc::cluster_addr(&acc_empty[acc], 0));
-        else
-          mbar_arrive(&acc_empty[acc]);
-      }
+      if (lane == 0) mbar_arrive(&acc_empty[acc]);
     };
-    for (int it = first; ok && it < items && decode(seg, it, kRowsPer, W, starts, t, e); it += step) {
+    for (int it = first; ok && it < items && decode(seg, it, X, W, starts, t, e); it += step) {
       const float alpha = p.w_global != nullptr ? gx * __ldcg(p.w_global + t.expert) : gx;
       if (!(ok = wait_warp(&acc_full[ac], aph, abort_flag, p.status))) break;
       tc::fence_after_sync();
       const int q = warp & 3;
       const uint32_t ta = tmem + (static_cast<uint32_t>(32 * q) << 16) + ac * C::N;
       if constexpr (kForm != kStream) {
-        constexpr int kCols = C::N / (C::EPI / 4);   // of a warp
-        const int col0 = (warp >> 2) * kCols;
-        const int row0 = t.row0 + static_cast<int>(rank) * X + 32 * q;
+        const int row0 = t.row0 + 32 * q;
         uint4* buf = out_base + warp * 128;
         uint16_t* yp = p.y + static_cast<size_t>(row0) * p.N + t.n0;
 #pragma unroll 1
-        for (int c0 = col0; c0 < col0 + kCols; c0 += 32) {
+        for (int c0 = 0; c0 < C::N; c0 += 32) {
           uint32_t v[32];
           tc::tmem_ld32(ta + c0, v);
-          if (c0 + 32 == col0 + kCols) hand_back(ac);
+          if (c0 + 32 == C::N) hand_back(ac);
           if (t.n0 + c0 >= p.N) continue;
           uint4 o[4];
 #pragma unroll
@@ -534,16 +487,9 @@ fp4_kernel(const __grid_constant__ Params p) {
   }
   tc::fence_before_sync();
   __syncthreads();
-  if constexpr (P) {   // nothing of the other CTA's is on its way here any more
-    cluster_arrive();
-    cluster_wait();
-  }
   if (warp == kMma) {
     tc::fence_after_sync();
-    if constexpr (P)
-      tc::tmem_dealloc_pair(tmem, C::TMEM_COLS);
-    else
-      tc::tmem_dealloc(tmem, C::TMEM_COLS);
+    tc::tmem_dealloc(tmem, C::TMEM_COLS);
   }
 }
 
@@ -561,20 +507,15 @@ template <int W, int X, bool kNv, Form kForm, bool kQuant = false>
 cudaError_t run(const Fp4Args& a, Params& p, cudaStream_t s) {
   using C = Shape<W, X, kNv, kForm, kQuant>;
   cudaError_t e = kQuant ? cudaSuccess : encode(&p.tm_x, a.qx, a.K / 2, a.R, 0, X);
-  if (e == cudaSuccess) e = encode(&p.tm_w, a.qweight, a.K / 2, a.N, a.E, C::W_LOAD);
+  if (e == cudaSuccess) e = encode(&p.tm_w, a.qweight, a.K / 2, a.N, a.E, W);
   if (e == cudaSuccess && p.tma_scales && !kQuant) e = encode(&p.tm_xs, a.x_scale, p.SB, a.R, 0, X, 1, 32);
   if (e == cudaSuccess && p.tma_scales) e = encode(&p.tm_ws, a.w_scale, p.SB, a.N, a.E, W, 1, 32);
   if (e != cudaSuccess) return e;
   p.n_tiles = static_cast<int>((a.N + W - 1) / W);
-  const int64_t items = row_tiles(a, C::PAIR ? 2 * X : X) * p.n_tiles;
+  const int64_t items = row_tiles(a, X) * p.n_tiles;
   if (items > kMaxItems) return cudaErrorInvalidConfiguration;
   p.items = static_cast<int>(items);
   p.split = 1;
-  if (C::PAIR) {
-    const int64_t pairs = clusters_held(2, 1);
-    if (pairs < 1) return cudaErrorInvalidConfiguration;
-    return start<fp4_kernel<W, X, kNv, kForm, kQuant>>(p, 2 * (items < pairs ? items : pairs), C::THREADS, C::SMEM, 2, s);
-  }
   const int64_t slots = static_cast<int64_t>(current_sm_count()) * C::CTAS;
   if (kForm == kStream && a.expert_offsets == nullptr)
     for (int n = kMaxSplit; n > 1 && p.split == 1; --n)
@@ -594,8 +535,8 @@ cudaError_t launch(const Fp4Args& a, Params& p, cudaStream_t s) {
   if (!experts) {
     const int64_t sms = current_sm_count();
     auto tiles = [&](int64_t x, int64_t w) { return (a.R + x - 1) / x * ((a.N + w - 1) / w); };
-    // Clusters that cut k where the weights' tiles are few: 300 x 2048 x 8192 nvfp4 10.4 us, pairs
-    // 12.7. With room for two parts only they are even (256 x 4096 x 4096 8.6 against 8.4).
+    // Clusters that cut k where the weights' tiles are few: 300 x 2048 x 8192 nvfp4 10.4 us, tiles
+    // 14.0. Without room for three parts tiles are as good (517 x 4096 x 4096 9.6 against 12.0).
     if (rows <= 128 || 3 * tiles(128, 128) <= sms) return run<128, 128, kNv, kStream>(a, p, s);
   }
   return run<192, 128, kNv, kTile>(a, p, s);

@@ -268,8 +268,8 @@ W4_DEV void issue_stage(const Params& p, uint32_t tmem, int acc, int buf, uint32
   const uint64_t wsd = tc::sdesc_scales(atoms), xsd = tc::sdesc_scales(bs);
 #pragma unroll
   for (int i = 0; i < kWords; ++i) {
-    tc::copy_scales<false>(sw + 4 * i, wsd + 32 * i);
-    tc::copy_scales<false>(sx + 4 * i, xsd + 32 * i);
+    tc::copy_scales(sw + 4 * i, wsd + 32 * i);
+    tc::copy_scales(sx + 4 * i, xsd + 32 * i);
   }
   const uint64_t wd = tc::sdesc_sw128(ring), xd = tc::sdesc_sw128(b);
   const uint32_t idesc = tc::idesc_fp4<kNv>(128, 0) | static_cast<uint32_t>(cols >> 3) << 17;
@@ -279,7 +279,7 @@ W4_DEV void issue_stage(const Params& p, uint32_t tmem, int acc, int buf, uint32
     if (64 * j >= left) break;
     const int word = kNv ? j : j >> 1;
     const uint32_t id = idesc | (kNv || !(j & 1) ? 0u : (2u << 29) | (2u << 4));
-    tc::mma_fp4<kNv, false>(tmem + acc * kAccCols, wd + 2 * j, xd + 2 * j, id, sw + 4 * word, sx + 4 * word, !first || j > 0 ? 1u : 0u);
+    tc::mma_fp4<kNv>(tmem + acc * kAccCols, wd + 2 * j, xd + 2 * j, id, sw + 4 * word, sx + 4 * word, !first || j > 0 ? 1u : 0u);
   }
 }
 

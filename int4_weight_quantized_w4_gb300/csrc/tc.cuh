@@ -68,48 +68,6 @@ W4_DEV void tma_load_3d(void* smem_dst, const void* tmap, uint64_t* bar, int c0,
       :: "r"(smem_addr(smem_dst)), "l"(tmap), "r"(smem_addr(bar)), "r"(c0), "r"(c1), "r"(c2) : "memory");
 }
 
-// ---------------------------------------------------------------------------
-// pairs of CTAs (a cluster of two whose tensor cores work on one tile)
-// ---------------------------------------------------------------------------
-
-// Address of `p` in CTA `rank` of the cluster.
-W4_DEV uint32_t cluster_addr(const void* p, uint32_t rank) {
-  uint32_t a;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
-  return a;
-}
-// Arrival on a barrier of any CTA of the cluster, given by cluster_addr. It orders what a
-// thread did for its own CTA (with release at cluster scope it takes some 1500 cycles): the
-// one that waits issues MMAs, whose reads of either CTA's shared memory are its own SM's.
-W4_DEV void cluster_arrive_on(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
-}
-// Copies into this CTA's shared memory whose bytes count on a barrier of either CTA.
-W4_DEV void tma_load_2d_pair(void* smem_dst, const void* tmap, uint32_t bar, int c0, int c1) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, %4}], [%2];"
-      :: "r"(smem_addr(smem_dst)), "l"(tmap), "r"(bar), "r"(c0), "r"(c1) : "memory");
-}
-W4_DEV void tma_load_3d_pair(void* smem_dst, const void* tmap, uint32_t bar, int c0, int c1, int c2) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, %4, %5}], [%2];"
-      :: "r"(smem_addr(smem_dst)), "l"(tmap), "r"(bar), "r"(c0), "r"(c1), "r"(c2) : "memory");
-}
-// One warp of each CTA of the pair.
-W4_DEV void tmem_alloc_pair(uint32_t* dst, uint32_t ncols) {
-  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
-               :: "r"(smem_addr(dst)), "r"(ncols) : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-}
-W4_DEV void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
-  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(taddr), "r"(ncols) : "memory");
-}
-// Arrives on `bar` of both CTAs when every tcgen05 op this thread issued so far is done.
-W4_DEV void commit_pair(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-               :: "r"(smem_addr(bar)), "h"(static_cast<uint16_t>(3)) : "memory");
-}
-
 // Asynchronous copy of 4 bytes, or zeros where `in` is false (then nothing is read).
 W4_DEV void copy4_async(uint32_t smem_dst, const void* src, bool in) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" :: "r"(smem_dst), "l"(src), "r"(in ? 4 : 0) : "memory");
@@ -241,23 +199,19 @@ constexpr uint32_t idesc_fp4(int M, int N) {
 
 // M x N x 64 per instruction. Scales come from tensor memory, a 32-bit column word per
 // row: four e4m3 of 16 k each (kNv), or two powers of two of 32 k each in the half that
-// the descriptor's scale ids (bits 29 and 4, 0 or 2) name. kPair: M is both CTAs' rows.
-#define W4_MMA_FP4(group, kind)                                                                          \
+// the descriptor's scale ids (bits 29 and 4, 0 or 2) name.
+#define W4_MMA_FP4(kind)                                                                                 \
   asm volatile("{.reg .pred p; setp.ne.b32 p, %6, 0; "                                                   \
-               "tcgen05.mma.cta_group::" group ".kind::" kind " [%0], %1, %2, %3, [%4], [%5], p;}"       \
+               "tcgen05.mma.cta_group::1.kind::" kind " [%0], %1, %2, %3, [%4], [%5], p;}"               \
                :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) \
                : "memory")
-template <bool kNv, bool kPair>
+template <bool kNv>
 W4_DEV void mma_fp4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t sfa, uint32_t sfb,
                     uint32_t accumulate) {
-  if constexpr (kNv && kPair)
-    W4_MMA_FP4("2", "mxf4nvf4.block_scale.scale_vec::4X");
-  else if constexpr (kNv)
-    W4_MMA_FP4("1", "mxf4nvf4.block_scale.scale_vec::4X");
-  else if constexpr (kPair)
-    W4_MMA_FP4("2", "mxf4.block_scale.scale_vec::2X");
+  if constexpr (kNv)
+    W4_MMA_FP4("mxf4nvf4.block_scale.scale_vec::4X");
   else
-    W4_MMA_FP4("1", "mxf4.block_scale.scale_vec::2X");
+    W4_MMA_FP4("mxf4.block_scale.scale_vec::2X");
 }
 #undef W4_MMA_FP4
 
@@ -272,15 +226,10 @@ W4_DEV uint64_t sdesc_scales(uint32_t saddr) {
   return d;
 }
 
-// A scale atom into four columns of tensor memory, the same in all four lane quadrants
-// (kPair: in both CTAs, each from its own shared memory). It is executed in order with the
-// MMAs that the thread issues.
-template <bool kPair>
+// A scale atom into four columns of tensor memory, the same in all four lane quadrants.
+// It is executed in order with the MMAs that the thread issues.
 W4_DEV void copy_scales(uint32_t taddr, uint64_t sdesc) {
-  if constexpr (kPair)
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" :: "r"(taddr), "l"(sdesc) : "memory");
-  else
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" :: "r"(taddr), "l"(sdesc) : "memory");
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" :: "r"(taddr), "l"(sdesc) : "memory");
 }
 
 // Arrive (once) on `bar` when every tcgen05 op this thread issued so far is done.
