@@ -475,6 +475,13 @@ __global__ void __launch_bounds__(kThreads, 1) moe_decode_kernel(const __grid_co
                            [&](int i) { return *reinterpret_cast<const uint4*>(xr + 64 * i); }, y[nb]);
           }
         }
+        // the slot goes back behind the products that used its words and the scales, with a fence
+        // between them and the next copy
+#pragma unroll
+        for (int nb = 0; nb < kEights; ++nb)
+#pragma unroll
+          for (int m = 0; m < 2; ++m) asm volatile("" : "+f"(y[nb][m][0]), "+f"(y[nb][m][1]), "+f"(y[nb][m][2]), "+f"(y[nb][m][3]) :: "memory");
+        tc::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&c.empty[group][slot]);
         // One of the warps copies the next piece into the place of the one before this, which the
