@@ -19,11 +19,13 @@ W4_DEV uint32_t e2m1x8(const float (&x)[8]) {
 }
 
 // Codes of fl(x / d), with r = fl(1 / d): the quotient by multiply-add refinement as
-// quotient2_e4m3, where d takes it (scale_refines). A quotient below 2^-3 has code 0 or -0
-// either way, so the bounds of the e4m3 form are ample.
-W4_DEV uint32_t quotients_e2m1(const float (&x)[8], float d, float r) {
+// quotient2_e4m3, where `refines`: d takes it (scale_refines) and no quotient is beyond 4096,
+// as where the block's scale was held at 448 (one that overflows would come out of the
+// refinement as NaN, which has lost its sign). A quotient below 2^-3 has code 0 or -0 either
+// way, so the lower bounds of the e4m3 form are ample.
+W4_DEV uint32_t quotients_e2m1(const float (&x)[8], float d, float r, bool refines) {
   float q[8];
-  if (scale_refines(d)) {
+  if (refines) {
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
       float q0, q1, e0, e1;
@@ -76,8 +78,9 @@ W4_DEV uint32_t block_codes(const float (&x)[2][8], uint32_t bits, float g, uint
     const float d = s * g;
     if (d > 0.f) {
       const float r = __frcp_rn(d);
-      code.x = quotients_e2m1(x[0], d, r);
-      code.y = quotients_e2m1(x[1], d, r);
+      const bool refines = scale_refines(d) && __uint_as_float(bits) * r < 4096.f;
+      code.x = quotients_e2m1(x[0], d, r, refines);
+      code.y = quotients_e2m1(x[1], d, r, refines);
     } else {
       code = make_uint2(0, 0);
     }
