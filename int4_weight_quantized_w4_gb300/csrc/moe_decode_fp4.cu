@@ -230,6 +230,11 @@ W4_DEV void turn_scales(const Params& p, Bars& bar, const uint8_t* raw, uint8_t*
   while (ok && next(mat, row, k0, k1))
     for (int ks = k0; ks < k1; ++ks) {
       const int sub = ks % kSuper;
+      // A ring that comes around holds what was copied after the kernel before: either may be the first to.
+      if (!waited && (rph == 1 || ph == 0)) {
+        grid_dependency_wait();
+        waited = true;
+      }
       if ((ks == k0 || (p.tma_scales && sub == 0)) && !(ok = wait_warp(&bar.raw_full[rs], rph, &bar.abort_flag, p.status))) break;
       uint32_t v[4][kWords];
       if (p.tma_scales) {
@@ -240,10 +245,6 @@ W4_DEV void turn_scales(const Params& p, Bars& bar, const uint8_t* raw, uint8_t*
         for (int b = 0; b < 4; ++b)
 #pragma unroll
           for (int j = 0; j < kWords; ++j) v[b][j] = f[b * 16 * p.SB + 2 * j] | static_cast<uint32_t>(f[b * 16 * p.SB + 2 * j + 1]) << 16;
-      }
-      if (!waited && ph == 0) {
-        grid_dependency_wait();
-        waited = true;
       }
       if (!(ok = wait_warp(&bar.empty[st], ph, &bar.abort_flag, p.status))) break;
       store_scale_atoms<kNv>(atoms + st * kWords * 512 + lane * 16, 512, v);
