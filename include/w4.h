@@ -584,14 +584,10 @@ w4_status w4_fp4_moe_gemm_bf16in(const void* x, int64_t T, const float* x_global
  *     experts e and weights w of token t as w4_moe_route_grouped gives them (bias,
  *     top_k, n_group, topk_group, scoring, renormalize, scale as there);
  *     h = gate_up[e] x_t;  a = silu(h[0 .. I)) h[I .. 2I);  y_t = bf16( sum_e w down[e] a ).
- * Activations stay 16-bit (the W4A16 form of the experts); sums are fp32. In int4 x is taken as
+ * Activations stay 16-bit (the W4A16 form of the experts); sums are fp32. x is taken as
  * fp16 times a power of two per token (a bf16 loses nothing down to 2^-29 of the token's largest
- * number) and a is rounded to 11 bits (fp16 with an exponent of its own per eight columns). In the
- * 4-bit floating point formats both become sums of five e2m1 terms, off by at most 2^-13 of the
- * largest magnitude among the 32 (mxfp4) or 16 (nvfp4) columns of a block, and in nvfp4 what lies
- * below 2^-17 of a row's largest number is lost; past the sizes of that form (H 8192, I 2048, or
- * what shared memory holds) they take the int4 form's way. A token that holds a NaN or an infinity gives no
- * finite numbers and leaves the others alone. Outputs are the same every time.
+ * number) and a is rounded to 11 bits (fp16 with an exponent of its own per eight columns). A token that
+ * holds a NaN or an infinity gives no finite numbers and leaves the others alone. Outputs are the same every time.
  *   format   W4_FMT_INT4: gate_up [E, 2I, H/8] int32, gate_up_scale [E, 2I, H/group] fp16
  *            (the layout of w4afp8_moe_grouped_gemm); group: gate_up_group and
  *            down_group, multiples of 32 that divide H and I, or -1;
@@ -602,7 +598,9 @@ w4_status w4_fp4_moe_gemm_bf16in(const void* x, int64_t T, const float* x_global
  *   y        [T, H] bf16
  * Limits (W4_ERR_UNSUPPORTED): T <= 16, E <= 256, top_k <= 32, H and I multiples of 64, and
  * shared memory for T rows of x beside the copies in flight: with I up to 7168, 16 tokens fit at H
- * up to 2560 and 7 at H = 4096; int4 groups of 128 and mxfp4 leave room for more. For more tokens w4_moe_route_grouped and the grouped products.
+ * up to 2560 and 7 at H = 4096; int4 groups of 128 leave room for more. Where rows of scales can be copied 512
+ * columns at a time (H and I multiples of 512 in mxfp4, of 256 in nvfp4 and int4 groups of 32, of 512 in groups of 64), 14 fit
+ * at H = 4096 and 8 at H = 7168, whatever I. For more tokens w4_moe_route_grouped and the grouped products.
  * Matrices, scales and the workspace are 16-byte aligned. workspace: at least
  * w4_workspace_bytes(W4_OP_MOE_DECODE, T, top_k, I, 0) bytes. x, logits, bias and weights are
  * read after the kernels before are done; its own dependents may start early, as those

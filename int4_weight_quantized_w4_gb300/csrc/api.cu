@@ -800,7 +800,7 @@ w4_status w4_moe_decode(const void* x, const void* logits, int32_t logits_f32, c
                                renormalize != 0, scale, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr};
   w4::MoeDecodeArgs a{route, x, format, gate_up_group, down_group, gate_up, gate_up_scale, gate_up_global, down, down_scale,
                       down_global, H, I, y, workspace, nullptr};
-  if (!w4::moe_decode_fp4_fits(a) && !w4::moe_decode_fits(a))
+  if (!w4::moe_decode_fits(a))
     return fail(W4_ERR_UNSUPPORTED, "T rows of x and the copies in flight do not fit in shared memory (T=%lld H=%lld I=%lld)", (long long)T, (long long)H, (long long)I);
   if (T == 0) return ok();
   if (!x || !logits || !gate_up || !gate_up_scale || !down || !down_scale || !y)

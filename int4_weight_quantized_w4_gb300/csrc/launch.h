@@ -243,15 +243,11 @@ struct MoeDecodeArgs {
   void* workspace;              // moe_decode_workspace_bytes
   unsigned int* status;
 };
-// The largest of what the two forms keep: fp16 activations of every chosen (token, expert) and an exponent per eight
-// of them, or fp32 sums.
+// fp16 activations of every chosen (token, expert) and an exponent per eight of them.
 size_t moe_decode_workspace_bytes(int64_t T, int64_t k, int64_t I);
-// The 4-bit floating point form, where it fits: fp32 sums of gate_up, in up to three parts.
-size_t moe_decode_fp4_workspace_bytes(int64_t T, int64_t k, int64_t I);
-bool moe_decode_fp4_fits(const MoeDecodeArgs& a);
-cudaError_t launch_moe_decode_fp4(const MoeDecodeArgs& a, cudaStream_t s);
 bool moe_decode_fits(const MoeDecodeArgs& a);
 cudaError_t launch_moe_decode(const MoeDecodeArgs& a, cudaStream_t s);
+cudaError_t launch_moe_decode_fp4(const MoeDecodeArgs& a, cudaStream_t s);   // of it, mxfp4 and nvfp4
 cudaError_t launch_bounded_wait_selftest(long long limit, unsigned int* status, cudaStream_t s);
 
 }  // namespace w4

@@ -72,16 +72,10 @@ W4_DEV void tma_load_3d(void* smem_dst, const void* tmap, uint64_t* bar, int c0,
 W4_DEV void copy4_async(uint32_t smem_dst, const void* src, bool in) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" :: "r"(smem_dst), "l"(src), "r"(in ? 4 : 0) : "memory");
 }
-W4_DEV void copy16_async(uint32_t smem_dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(smem_dst), "l"(src) : "memory");
-}
 // Arrives on `bar`, which counts it, when this thread's copies so far have landed.
 W4_DEV void copy_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" :: "r"(smem_addr(bar)) : "memory");
 }
-W4_DEV void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kPending>
-W4_DEV void copy_async_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(kPending) : "memory"); }
 
 // L2 policy for data that is read once: it makes room before anything else does.
 W4_DEV uint64_t evict_first_policy() {
@@ -251,16 +245,6 @@ W4_DEV void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
         "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
         "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
       : "r"(taddr) : "memory");
-}
-
-// One column without the wait. tmem_wait_ld, given the values, makes five of them usable.
-W4_DEV float tmem_ld1_async(uint32_t taddr) {
-  uint32_t v;
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(v) : "r"(taddr) : "memory");
-  return __uint_as_float(v);
-}
-W4_DEV void tmem_wait_ld(float (&v)[5]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]) :: "memory");
 }
 
 // The same load of 16 columns without the wait. tmem_wait_ld, given the

@@ -10,7 +10,7 @@ import pytest
 from int4_weight_quantized_w4_gb300 import _build
 
 ARRIVAL = re.compile(r"mbar_arrive\(&(?:\w+\.)*(?:raw_)?empty\[")
-UNITS = sorted(os.path.basename(f) for f in glob.glob(os.path.join(_build.CSRC, "*.cu")))
+UNITS = sorted(os.path.basename(f) for f in glob.glob(os.path.join(_build.CSRC, "*.cu*")))
 
 
 def hand_backs(unit):
@@ -21,7 +21,7 @@ def hand_backs(unit):
 
 
 def test_there_are_such_slots():
-    assert {u for u in UNITS if hand_backs(u)} >= {"fp4_gemm.cu", "moe_decode.cu", "w4a8.cu"}
+    assert {u for u in UNITS if hand_backs(u)} >= {"fp4_gemm.cu", "moe_decode.cuh", "w4a8.cu"}
 
 
 @pytest.mark.parametrize("unit", UNITS)
