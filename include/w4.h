@@ -586,8 +586,9 @@ w4_status w4_fp4_moe_gemm_bf16in(const void* x, int64_t T, const float* x_global
  *     h = gate_up[e] x_t;  a = silu(h[0 .. I)) h[I .. 2I);  y_t = bf16( sum_e w down[e] a ).
  * Activations stay 16-bit (the W4A16 form of the experts); sums are fp32. x is taken as
  * fp16 times a power of two per token (a bf16 loses nothing down to 2^-29 of the token's largest
- * number) and a is rounded to 11 bits (fp16 with an exponent of its own per eight columns). A token that
- * holds a NaN or an infinity gives no finite numbers and leaves the others alone. Outputs are the same every time.
+ * number) and a to 22 bits (two fp16 numbers with an exponent per eight columns), down to 2^-29 of the
+ * largest among 128 columns. A token that holds a NaN or an infinity gives no finite numbers and leaves the
+ * others alone. Outputs are the same every time.
  *   format   W4_FMT_INT4: gate_up [E, 2I, H/8] int32, gate_up_scale [E, 2I, H/group] fp16
  *            (the layout of w4afp8_moe_grouped_gemm); group: gate_up_group and
  *            down_group, multiples of 32 that divide H and I, or -1;

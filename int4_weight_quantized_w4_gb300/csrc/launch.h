@@ -243,7 +243,7 @@ struct MoeDecodeArgs {
   void* workspace;              // moe_decode_workspace_bytes
   unsigned int* status;
 };
-// fp16 activations of every chosen (token, expert) and an exponent per eight of them.
+// Two fp16 numbers per activation of every chosen (token, expert) and an exponent per eight of them.
 size_t moe_decode_workspace_bytes(int64_t T, int64_t k, int64_t I);
 bool moe_decode_fits(const MoeDecodeArgs& a);
 cudaError_t launch_moe_decode(const MoeDecodeArgs& a, cudaStream_t s);

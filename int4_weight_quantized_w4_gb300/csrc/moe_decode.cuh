@@ -25,9 +25,10 @@
 //
 // Activations are fp16 numbers times a power of two: x_t with its largest magnitude in
 // [2^14, 2^15) (a bf16 keeps all its bits down to 2^-29 of that), a_te the same over every
-// eight columns. Those exponents differ along k; a warp brings its columns to the
-// largest of them before it multiplies. fp16 rounds a to 11 bits where a bf16 step would
-// leave 8.
+// eight columns, in two halves: fp16 rounds a to 11 bits, and a second number takes the next 11. The
+// halves are columns of the product side by side, which costs nothing up to four tokens an expert.
+// Those exponents differ along k; a warp brings its columns to the
+// largest of them before it multiplies, which takes bits only from what lies below 2^-29 of it.
 //
 // One token, 64 experts of 2048 x 1408 in int4, 8 chosen (34.6 MB, 5.3 us at the copy rate): 23 us,
 // of which 4 go to the choice of experts and 4 to the second kernel's start, most of the rest to
@@ -64,7 +65,7 @@ struct Params {
   const float* w_global;   // [E] or null
   const uint16_t* x;       // up: bf16 [T, H]
   uint4* choice;           // the up kernel's, for the down kernel
-  uint16_t* act;           // fp16 [pairs, I]
+  uint16_t* act;           // fp16 [pairs, 2, I]
   uint8_t* act_exp;        // [pairs, I / 8]: biased exponents
   uint16_t* y;             // down: bf16 [T, H]
   int H, I, K, rows;       // K: columns of w (up: H, down: I); rows an expert
@@ -206,7 +207,7 @@ struct RowsOf {
 };
 
 // Adds this warp's steps [s0, s1), at most kPer, to y[block]; the slot starts at step c0, the scales at step z0. b(i)
-// are the lane's 8 activations of step s0 + i (columns 8 (lane % 4) ..) of token lane / 4.
+// are the lane's 8 activations of step s0 + i (columns 8 (lane % 4) ..) of column lane / 4 of the block.
 // kWhole: int4, kPer steps that have one scale.
 template <int kFmt, bool kDown, bool kWhole, class B>
 W4_DEV void multiply(const Params& p, const uint8_t* slot, const uint8_t* scales, int c0, int z0, int s0, int s1, B b,
@@ -375,10 +376,12 @@ W4_DEV void prepare(const Params& p, Common& c) {
   }
 }
 
-// A kernel behind that wait. kEights: of tokens, two where there are more than eight. kWhole: as multiply.
-template <int kFmt, bool kDown, int kEights, bool kWhole>
+// A kernel behind that wait. kBlocks: of an expert's tokens, 8 of them (up) or 4 (down, whose
+// activations are pairs of columns). kWhole: as multiply.
+template <int kFmt, bool kDown, int kBlocks, bool kWhole>
 W4_DEV void layer(const Params& p, Common& c) {
   uint8_t* smem = reinterpret_cast<uint8_t*>(&c);
+  constexpr int kTokens = kDown ? 4 : 8, kSums = kDown ? 2 : 4;   // of a block, a lane's sums of 16 rows
   Routed& r = c.r;
   uint8_t* ring = smem + (sizeof(Common) + 1023) / 1024 * 1024;
   uint8_t* scale_ring = ring + kGroups * p.slots * kSlot;
@@ -467,18 +470,19 @@ W4_DEV void layer(const Params& p, Common& c) {
     for (; at.left > 0; at.skip(p.I, stride)) {
       const int first = r.first[at.a], tokens = r.first[at.a + 1] - first;
       const float gl = p.w_global != nullptr ? __ldcg(p.w_global + r.expert[at.a]) : 1.f;
-      float y[kEights][2][4] = {};   // [eight tokens][block]
+      float y[kBlocks][2][kSums] = {};   // [block of tokens][16 rows]
       for (int ch = 0; ch < p.chunks; ++ch, ++count) {
         const int c0 = ch * kChunkSteps;
         const int s0 = min(c0 + kPer * w, steps), s1 = min(s0 + kPer, steps);
         const uint8_t* piece = my_ring + slot * kSlot;
         const uint8_t* scales = my_scales + (p.by_piece ? slot : scale_at) * scale_slot;
         const int z0 = p.by_piece ? c0 : 0;
-        auto row_of = [&](int nb) { return first + min(8 * nb + g, tokens - 1); };   // columns past the last token repeat it
+        // this lane's column of a block: a token, or half of its activations; columns past the last token repeat it
+        auto row_of = [&](int nb) { return first + min(kTokens * nb + (kDown ? g >> 1 : g), tokens - 1); };
         uint4 v[kPer];
         int e[kPer];
         auto fetch = [&](int nb) {   // activations and their exponents
-          const uint16_t* ar = p.act + static_cast<size_t>(row_of(nb)) * p.K + 8 * q;
+          const uint16_t* ar = p.act + (2 * static_cast<size_t>(row_of(nb)) + (g & 1)) * p.K + 8 * q;
           const uint8_t* er = p.act_exp + static_cast<size_t>(row_of(nb)) * (p.K / 8) + q;
 #pragma unroll
           for (int i = 0; i < kPer; ++i)
@@ -490,51 +494,76 @@ W4_DEV void layer(const Params& p, Common& c) {
         if constexpr (kDown) fetch(0);
         // after a time-out the group goes on without waiting, so that its warps still meet
         ok = ok && wait_warp(&c.full[group][slot], phase, abort_flag, p.status);
+        auto held = [](float& v) { asm volatile("" : "+f"(v) :: "memory"); };
+        // one block of tokens: fold(m, h, v, f) takes this lane's sums
+        auto block = [&](int nb, auto fold) {
+          int top = 0, low = 255;
 #pragma unroll
-        for (int nb = 0; nb < kEights; ++nb) {
-          if (8 * nb >= tokens || s0 >= s1) break;
-          const int row = row_of(nb);
-          if constexpr (kDown) {
-            int top = 0;
-            if (nb > 0) fetch(nb);
+          for (int i = 0; i < kPer; ++i)
+            if (kWhole || s0 + i < s1) top = max(top, e[i]), low = min(low, e[i]);
+          top = max(top, __shfl_xor_sync(kFull, top, 1));
+          top = max(top, __shfl_xor_sync(kFull, top, 2));
+          auto shift = [&](uint4& a, int by) {   // times 2^by, from 2^-24 on
+            const float f = __uint_as_float(static_cast<uint32_t>(max(127 + by, 0)) << 23);
+            uint32_t h;
+            asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(h) : "f"(f));
+            asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(a.x) : "r"(h));
+            asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(a.y) : "r"(h));
+            asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(a.z) : "r"(h));
+            asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(a.w) : "r"(h));
+          };
+          if (__any_sync(kFull, top - low > 24)) {   // far apart: in two steps
 #pragma unroll
             for (int i = 0; i < kPer; ++i)
-              if (kWhole || s0 + i < s1) top = max(top, e[i]);
-            top = max(top, __shfl_xor_sync(kFull, top, 1));
-            top = max(top, __shfl_xor_sync(kFull, top, 2));
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-              if (kWhole || s0 + i < s1) {
-                const float f = __uint_as_float(static_cast<uint32_t>(max(127 + e[i] - top, 0)) << 23);
-                uint32_t h;
-                asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(h) : "f"(f));
-                asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(v[i].x) : "r"(h));
-                asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(v[i].y) : "r"(h));
-                asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(v[i].z) : "r"(h));
-                asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(v[i].w) : "r"(h));
+              if ((kWhole || s0 + i < s1) && top - e[i] > 24) {
+                shift(v[i], -24);
+                e[i] += 24;
               }
-            float d[2][4] = {};
-            multiply<kFmt, kDown, kWhole>(p, piece, scales, c0, z0, s0, s1, [&](int i) { return v[i]; }, d);
-            // a factor 2^(top - 127 - 14) for this lane's two columns
-            const int t0 = __shfl_sync(kFull, top, 8 * q), t1 = __shfl_sync(kFull, top, 8 * q + 4);
-            const float f0 = two_to(t0 - 141), f1 = two_to(t1 - 141);
+          }
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-              y[nb][m][0] = fmaf(d[m][0], f0, y[nb][m][0]), y[nb][m][1] = fmaf(d[m][1], f1, y[nb][m][1]);
-              y[nb][m][2] = fmaf(d[m][2], f0, y[nb][m][2]), y[nb][m][3] = fmaf(d[m][3], f1, y[nb][m][3]);
+          for (int i = 0; i < kPer; ++i)
+            if (kWhole || s0 + i < s1) shift(v[i], e[i] - top);
+          float d[2][4] = {};
+          multiply<kFmt, kDown, kWhole>(p, piece, scales, c0, z0, s0, s1, [&](int i) { return v[i]; }, d);
+          // the lane's two columns are a token's halves: a factor 2^(top - 127 - 14), and 2^-11 of the second
+          const float f = two_to(__shfl_sync(kFull, top, 8 * q) - 141);
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float a = fmaf(d[m][2 * h + 1], 1.f / 2048.f, d[m][2 * h]);
+              held(a);
+              fold(m, h, a, f);
             }
-          } else {
-            const uint8_t* xr = rest + r.token[row] * x_pitch + 64 * s0 + 16 * q;
+        };
+        if constexpr (kDown) {
+          if (s0 < s1) {
+            block(0, [&](int m, int h, float a, float f) { y[0][m][h] = fmaf(a, f, y[0][m][h]); });
+            if constexpr (kBlocks > 1) {
+#pragma unroll 1
+              for (int nb = 1; kTokens * nb < tokens; ++nb) {   // few experts have more
+                fetch(nb);
+                block(nb, [&](int m, int h, float a, float f) {
+#pragma unroll
+                  for (int j = 1; j < kBlocks; ++j)
+                    if (j == nb) y[j][m][h] = fmaf(a, f, y[j][m][h]);
+                });
+              }
+            }
+          }
+        } else {
+#pragma unroll
+          for (int nb = 0; nb < kBlocks; ++nb) {
+            if (kTokens * nb >= tokens || s0 >= s1) break;
+            const uint8_t* xr = rest + r.token[row_of(nb)] * x_pitch + 64 * s0 + 16 * q;
             multiply<kFmt, kDown, kWhole>(p, piece, scales, c0, z0, s0, s1,
-                           [&](int i) { return *reinterpret_cast<const uint4*>(xr + 64 * i); }, y[nb]);
+                                          [&](int i) { return *reinterpret_cast<const uint4*>(xr + 64 * i); }, y[nb]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) held(y[nb][k >> 2][k & 3]);
           }
         }
-        // the slot goes back behind the products that used its words and the scales, with a fence
-        // between them and the next copy
-#pragma unroll
-        for (int nb = 0; nb < kEights; ++nb)
-#pragma unroll
-          for (int m = 0; m < 2; ++m) asm volatile("" : "+f"(y[nb][m][0]), "+f"(y[nb][m][1]), "+f"(y[nb][m][2]), "+f"(y[nb][m][3]) :: "memory");
+        // the slot goes back behind the products that used its words and the scales (taken in `held`), with
+        // a fence between them and the next copy
         tc::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&c.empty[group][slot]);
@@ -552,24 +581,25 @@ W4_DEV void layer(const Params& p, Common& c) {
       }
       if (++scale_at == p.scale_slots) scale_at = 0;
 #pragma unroll
-      for (int nb = 0; nb < kEights; ++nb) {
-        if (8 * nb >= tokens) break;
+      for (int nb = 0; nb < kBlocks; ++nb) {
+        if (kTokens * nb >= tokens) break;
         float (*red)[2][32][4] = c.red[group][turn];   // two in turn, so that one meeting is enough
         turn ^= 1;
+        if constexpr (kDown) {
+          *reinterpret_cast<float4*>(red[w][0][lane]) = make_float4(y[nb][0][0], y[nb][0][1], y[nb][1][0], y[nb][1][1]);
+        } else {
 #pragma unroll
-        for (int m = 0; m < 2; ++m) *reinterpret_cast<float4*>(red[w][m][lane]) = make_float4(y[nb][m][0], y[nb][m][1], y[nb][m][2], y[nb][m][3]);
+          for (int m = 0; m < 2; ++m) *reinterpret_cast<float4*>(red[w][m][lane]) = make_float4(y[nb][m][0], y[nb][m][1], y[nb][m][2], y[nb][m][3]);
+        }
         group_sync(group);
         auto sum = [&](int m, int l, int j) { return ((red[0][m][l][j] + red[1][m][l][j]) + red[2][m][l][j]) + red[3][m][l][j]; };
         if constexpr (kDown) {
-          const int o = tid & 31;
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int n = 8 * nb + 4 * k + (tid >> 5);
-            if (n < tokens) {
-              const float v = sum(o >> 4, (o & 7) * 4 + (n & 7) / 2, (o >> 3 & 1) * 2 + (n & 1));
-              float& at = out[r.token[first + n] * kRows + o];
-              at = fmaf(v, gl * r.weight[first + n], at);
-            }
+          // thread: column tid % 32 of the unit, token tid / 32, a warp's own
+          const int o = lane, n = 4 * nb + w;
+          if (n < tokens) {
+            const float v = sum(0, (o & 7) * 4 + w, o >> 3);
+            float& at = out[r.token[first + n] * kRows + o];
+            at = fmaf(v, gl * r.weight[first + n], at);
           }
         } else if (8 * nb + 2 * w < tokens) {   // a warp with no token has nothing to do here
           // thread: column tid % 16 of the unit, token tid / 16
@@ -584,9 +614,13 @@ W4_DEV void layer(const Params& p, Common& c) {
           bits = max(bits, __shfl_xor_sync(kFull, bits, 4));
           const uint32_t ex = max(bits >> 23, 14u);   // a 2^(14 - (ex - 127)): the largest in [2^14, 2^15)
           if (n < tokens) {
-            uint16_t h;
-            asm("cvt.rn.f16.f32 %0, %1;" : "=h"(h) : "f"(a * __uint_as_float((268u - ex) << 23)));
-            p.act[static_cast<size_t>(first + n) * p.I + at.n0 + (i & 8) + chunk_place<kFmt>(i & 7)] = h;
+            // in two halves of 11 bits, the second 2^11 times what the first left
+            const float f16 = a * __uint_as_float((268u - ex) << 23);
+            uint16_t hi, lo;
+            asm("cvt.rn.f16.f32 %0, %1;" : "=h"(hi) : "f"(f16));
+            asm("cvt.rn.f16.f32 %0, %1;" : "=h"(lo) : "f"((f16 - half_bits_to_f32(hi)) * 2048.f));
+            uint16_t* to = p.act + 2 * static_cast<size_t>(first + n) * p.I + at.n0 + (i & 8) + chunk_place<kFmt>(i & 7);
+            to[0] = hi, to[p.I] = lo;
             if ((i & 7) == 0) p.act_exp[static_cast<size_t>(first + n) * (p.I / 8) + (at.n0 + i) / 8] = static_cast<uint8_t>(ex);
           }
         }
@@ -688,7 +722,7 @@ cudaError_t run(const MoeDecodeArgs& a, cudaStream_t s) {
   p.x = static_cast<const uint16_t*>(a.x);
   p.choice = static_cast<uint4*>(a.workspace);
   p.act = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(a.workspace) + kMoeChoiceBytes);
-  p.act_exp = reinterpret_cast<uint8_t*>(p.act + static_cast<size_t>(T) * a.route.k * a.I);
+  p.act_exp = reinterpret_cast<uint8_t*>(p.act + 2 * static_cast<size_t>(T) * a.route.k * a.I);
   p.y = static_cast<uint16_t*>(a.y);
   p.H = static_cast<int>(a.H);
   p.I = static_cast<int>(a.I);

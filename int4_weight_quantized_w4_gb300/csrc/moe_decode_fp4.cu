@@ -10,7 +10,7 @@
 namespace w4 {
 namespace {
 
-template <bool kNv, bool kDown, int kEights>
+template <bool kNv, bool kDown, int kBlocks>
 __global__ void __launch_bounds__(kThreads, 1) moe_decode_fp4_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_dyn[];
   Common& c = common_of(smem_dyn);
@@ -18,13 +18,15 @@ __global__ void __launch_bounds__(kThreads, 1) moe_decode_fp4_kernel(const __gri
   if (kDown) launch_dependents();
   grid_dependency_wait();
   if (!kDown) launch_dependents();
-  layer<kNv ? W4_FMT_NVFP4 : W4_FMT_MXFP4, kDown, kEights, false>(p, c);
+  layer<kNv ? W4_FMT_NVFP4 : W4_FMT_MXFP4, kDown, kBlocks, false>(p, c);
 }
 
 template <bool kNv, bool kDown>
 cudaError_t run_fitting(const MoeDecodeArgs& a, cudaStream_t s) {
   constexpr int kFmt = kNv ? W4_FMT_NVFP4 : W4_FMT_MXFP4;
-  return a.route.T > 8 ? run<moe_decode_fp4_kernel<kNv, kDown, 2>, kFmt, kDown>(a, s) : run<moe_decode_fp4_kernel<kNv, kDown, 1>, kFmt, kDown>(a, s);
+  if (a.route.T > 8) return run<moe_decode_fp4_kernel<kNv, kDown, kDown ? 4 : 2>, kFmt, kDown>(a, s);
+  if (kDown && a.route.T > 4) return run<moe_decode_fp4_kernel<kNv, kDown, kDown ? 2 : 1>, kFmt, kDown>(a, s);
+  return run<moe_decode_fp4_kernel<kNv, kDown, 1>, kFmt, kDown>(a, s);
 }
 
 template <bool kNv>

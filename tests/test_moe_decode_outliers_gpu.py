@@ -69,3 +69,21 @@ def test_a_scale_that_is_no_number():
     assert np.isnan(y[2, 200])
     y[2, 200] = clean[2, 200]
     np.testing.assert_array_equal(y, clean)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T", [1, 9])
+def test_an_activation_that_counts_for_nothing(fmt, T):
+    """One gate and up row of far larger weights, and none in that column of the down weights: its
+    neighbours lie up to 2^-30 below it, and have an exponent of their own."""
+    H, I, c = 512, 320, 77
+    ex = Experts(8, H, I, fmt)
+    q, s, g = ex.parts[0]
+    s = s.copy()
+    s[:, [c, I + c]] = {"int4": 8.0, "mxfp4": 118 + 16, "nvfp4": 0x7E}[fmt]          # 2^7, 448
+    ex.parts[0] = q, s, g
+    ex.parts[1] = without(ex.parts[1], c, fmt)
+    x = S.normal(3, T, T * H).reshape(T, H)
+    h = ex.values(0, 0) @ x[0]
+    assert np.abs(h[[c, I + c]]).min() > 10 * np.median(np.abs(h))
+    ex.check(S.to_bf16_bits(x), S.router_logits(T, 8, seed=5), 3, scoring="softmax")
