@@ -2,8 +2,8 @@
 
 The experts' weights are e2m1 codes with block scales (``mxfp4`` or ``nvfp4``), quantized by the
 library. Up to sixteen tokens take the few-token layer (16-bit activations, routing and both
-products in one call); more are routed, quantized to the weights' format and multiplied on the
-block-scaled tensor cores. Run it on a GPU::
+products in one call) where that is the faster way and takes their sizes; others are routed, quantized to the
+weights' format and multiplied on the block-scaled tensor cores. Run it on a GPU::
 
     python examples/fp4_moe_layer.py --tokens 64 --format nvfp4
 
@@ -23,6 +23,10 @@ if __package__ in (None, ""):
 import int4_weight_quantized_w4_gb300 as w4
 
 DECODE_TOKENS = 16
+# Bytes of the chosen experts' weights up to which the few-token call is the faster one. On a GB300, it and the
+# separate calls: 8 experts of 2048 x 1408 in mxfp4 (37 MB) 24 and 29 us, 15 of them 34 and 32; 39 of 1024 x 704 in
+# nvfp4 (47 MB) 32 and 34; 8 of 4096 x 1536 (80 MB) 40 and 33.
+DECODE_BYTES = 50e6
 
 
 @dataclasses.dataclass
@@ -46,7 +50,20 @@ class Fp4MoeLayer:
     def __call__(self, x: torch.Tensor) -> torch.Tensor:
         """bf16 ``[T, H]`` -> bf16 ``[T, H]``."""
         logits = x.float() @ self.router.T
-        return self.decode(x, logits) if x.shape[0] <= DECODE_TOKENS else self.prefill(x, logits)
+        if self.few(x.shape[0]):
+            try:
+                return self.decode(x, logits)
+            except w4.W4Error as e:
+                if e.status != w4.W4_ERR_UNSUPPORTED:
+                    raise
+        return self.prefill(x, logits)
+
+    def few(self, tokens: int) -> bool:
+        """Whether the few-token call is the faster one."""
+        E = self.router.shape[0]
+        chosen = E * (1 - (1 - self.top_k / E) ** tokens)      # experts that get a token, on average
+        parts = (self.gate_up.codes, self.gate_up.scale, self.down.codes, self.down.scale)
+        return tokens <= DECODE_TOKENS and chosen / E * sum(t.numel() for t in parts) <= DECODE_BYTES
 
     def decode(self, x, logits):
         u, d = self.gate_up, self.down
