@@ -233,8 +233,9 @@ w4_status w4a8_gemm_bf16in(const void* x, const void* qweight, const void* w_sca
  * does not, or a synchronization, stands between the two on the stream (one
  * early signaller after another lets this kernel start while the first still
  * runs). Early signallers are this kernel, those of the fp8 block-scaled
- * layer and those of the 4-bit floating point products; every other kernel of this
- * library, and ordinary library kernels, are waited for in full.
+ * layer and its grouped router, those of the 4-bit floating point products and those of
+ * w4_moe_decode; every other kernel of this library, and ordinary library kernels, are waited
+ * for in full.
  */
 w4_status w4a16_gemm(const void* x, const void* qweight, const void* w_scale, int32_t w_scale_dtype,
                      const void* zeros, int32_t group, const void* bias, void* y,
@@ -602,6 +603,10 @@ w4_status w4_fp4_moe_gemm_bf16in(const void* x, int64_t T, const float* x_global
  * up to 2560 and 7 at H = 4096; int4 groups of 128 leave room for more. Where rows of scales can be copied 512
  * columns at a time (H and I multiples of 512 in mxfp4, of 256 in nvfp4 and int4 groups of 32, of 512 in groups of 64), 14 fit
  * at H = 4096 and 8 at H = 7168, whatever I. For more tokens w4_moe_route_grouped and the grouped products.
+ * In int4 it takes a third to a quarter of these calls' time at any number of tokens. In the 4-bit floating point
+ * formats those, whose activations have 4 bits, are faster from some 50 MB of chosen experts' weights on (64 experts of
+ * 2048 x 1408, 8 chosen, mxfp4: 1 token 24 us and 29, 2 34 and 32, 16 100 and 60; 96 of 1024 x 704, 6 chosen, nvfp4: 8 tokens
+ * 32 and 34, 16 47 and 37).
  * Matrices, scales and the workspace are 16-byte aligned. workspace: at least
  * w4_workspace_bytes(W4_OP_MOE_DECODE, T, top_k, I, 0) bytes. x, logits, bias and weights are
  * read after the kernels before are done; its own dependents may start early, as those

@@ -680,8 +680,9 @@ static w4_status run_fp4(w4::Fp4Args a, void* stream) {
   return from_cuda(w4::launch_fp4(a, static_cast<cudaStream_t>(stream)), "fp4 product launch");
 }
 
-// Elements of expert rows from which on tokens are quantized once and their codes copied, as
-// kCopyElements.
+// Elements of expert rows from which on tokens are quantized once and their codes copied: the extra launch against
+// the rows' own quantization (64 experts, top 8, N 2816, K 2048, by row / copied, nvfp4: 256 tokens, 4 M elements, 41.3 /
+// 43.6 us; 512, 8 M, 46.2 / 45.8, 768 51.9 / 48.5, 4096 148 / 120; mxfp4: 512 42.4 / 43.4, 768 46.5 / 46.7, 4096 128 / 112).
 constexpr int64_t kCopyFp4 = int64_t{1} << 23;
 
 // Quantizes rows of x (gathered by `rows` when given) into the workspace, then multiplies (a.qx, a.x_scale unset).

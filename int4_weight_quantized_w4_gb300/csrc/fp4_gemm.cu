@@ -213,7 +213,6 @@ fp4_kernel(const __grid_constant__ Params p) {
     bool ok = true, waited = false;
     Tile t;
     for (int it = first; ok && it < items && decode(seg, it, X, W, starts, t, e); it += step) {
-      const int row0 = t.row0;
       for (int ks = ks0; ks < ks1; ks = (ks / C::SUPER + 1) * C::SUPER) {
         if (!(ok = wait_warp(&raw_empty[rs], rph, abort_flag, p.status))) break;
         uint8_t* to = raw + rs * C::RAW;
@@ -230,10 +229,10 @@ fp4_kernel(const __grid_constant__ Params p) {
         if (!waited) grid_dependency_wait();   // the activations' come from the kernel before
         waited = true;
         if (p.tma_scales) {
-          if (!kQuant && elect_one()) tc::tma_load_2d(to + C::RAW_W, &p.tm_xs, &raw_full[rs], at, row0);
+          if (!kQuant && elect_one()) tc::tma_load_2d(to + C::RAW_W, &p.tm_xs, &raw_full[rs], at, t.row0);
           __syncwarp();
         } else {
-          if (!kQuant) copy_scale_words(smem_addr(to + C::RAW_W), p.x_scale + static_cast<size_t>(row0 < t.row_end ? row0 : t.row0) * p.SB, p.SB, at, X, t.row_end - row0);
+          if (!kQuant) copy_scale_words(smem_addr(to + C::RAW_W), p.x_scale + static_cast<size_t>(t.row0) * p.SB, p.SB, at, X, t.row_end - t.row0);
           tc::copy_async_arrive(&raw_full[rs]);
         }
         if (++rs == C::RAWS) rs = 0, rph ^= 1;
@@ -527,6 +526,8 @@ cudaError_t run(const Fp4Args& a, Params& p, cudaStream_t s) {
 template <bool kNv>
 cudaError_t launch(const Fp4Args& a, Params& p, cudaStream_t s) {
   const bool experts = a.expert_offsets != nullptr;
+  // Experts' rows on average, as only the device knows each one's. Where they are uneven the tile form may be a little
+  // better: 256 tokens, half of whose 8 choices are the same four of 64 experts, N 2816, K 2048 nvfp4 45.7 us, 43.6 in tiles.
   const int64_t rows = (a.R + a.E - 1) / a.E;
   if (a.x != nullptr) return run<128, 16, kNv, kStream, true>(a, p, s);
   if (rows <= 16) return run<128, 16, kNv, kStream>(a, p, s);
