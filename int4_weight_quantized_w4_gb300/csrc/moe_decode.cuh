@@ -618,7 +618,8 @@ W4_DEV void layer(const Params& p, Common& c) {
             const float f16 = a * __uint_as_float((268u - ex) << 23);
             uint16_t hi, lo;
             asm("cvt.rn.f16.f32 %0, %1;" : "=h"(hi) : "f"(f16));
-            asm("cvt.rn.f16.f32 %0, %1;" : "=h"(lo) : "f"((f16 - half_bits_to_f32(hi)) * 2048.f));
+            const float left = f16 - half_bits_to_f32(hi);
+            asm("cvt.rn.f16.f32 %0, %1;" : "=h"(lo) : "f"(left == left ? left * 2048.f : 0.f));   // of an infinity nothing
             uint16_t* to = p.act + 2 * static_cast<size_t>(first + n) * p.I + at.n0 + (i & 8) + chunk_place<kFmt>(i & 7);
             to[0] = hi, to[p.I] = lo;
             if ((i & 7) == 0) p.act_exp[static_cast<size_t>(first + n) * (p.I / 8) + (at.n0 + i) / 8] = static_cast<uint8_t>(ex);

@@ -6,6 +6,7 @@ magnitudes. x is exact down to 2^-29 of a row's largest number."""
 import numpy as np
 import pytest
 
+import oracle as O
 import synthetic as S
 from _gpu import requires_cuda
 from test_moe_decode_gpu import Experts
@@ -87,3 +88,33 @@ def test_an_activation_that_counts_for_nothing(fmt, T):
     h = ex.values(0, 0) @ x[0]
     assert np.abs(h[[c, I + c]]).min() > 10 * np.median(np.abs(h))
     ex.check(S.to_bf16_bits(x), S.router_logits(T, 8, seed=5), 3, scoring="softmax")
+
+
+@pytest.mark.parametrize("T", [6, 16])
+def test_an_activation_past_the_largest_number(T):
+    """It is infinite in fp32, and so are the outputs that it counts for, with their sign; the others of the same token are none
+    the worse."""
+    H, I, c, E = 512, 320, 77, 2
+    ex = Experts(E, H, I, "mxfp4")
+    q, s, g = ex.parts[0]
+    s = s.copy()
+    s[:, [c, I + c]] = 127 + 60
+    ex.parts[0] = q, s, g
+    q, s, g = ex.parts[1]
+    q = q.copy()
+    q[:, :100, c // 2] = 0x55          # 3 in the first 100 rows
+    q[:, 100:, c // 2] = 0xDD          # -3 in the others
+    ex.parts[1] = q, s, g
+    xb, logits = S.activations_bf16(T, H, seed=2), S.router_logits(T, E, seed=5)
+    logits[:, 0], logits[:, 1] = 5.0, -5.0
+    y = ex.call(xb, logits, 1).float().cpu().numpy()
+    h = O.bf16_to_f64(xb) @ ex.values(0, 0).T
+    with np.errstate(over="ignore"):
+        a = h[:, c] / (1 + np.exp(-h[:, c])) * h[:, I + c]
+    large, small = np.abs(a) > 4e38, np.abs(a) < 3e38      # fp32 ends at 3.4e38
+    assert large.any() and small.any()
+    for t in range(T):
+        if large[t]:
+            assert (y[t, :100] == np.sign(a[t]) * np.inf).all() and (y[t, 100:] == -np.sign(a[t]) * np.inf).all()
+        elif small[t]:
+            assert np.isfinite(y[t]).all()
