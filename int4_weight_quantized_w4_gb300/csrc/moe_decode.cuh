@@ -470,7 +470,15 @@ W4_DEV void layer(const Params& p, Common& c) {
     for (; at.left > 0; at.skip(p.I, stride)) {
       const int first = r.first[at.a], tokens = r.first[at.a + 1] - first;
       const float gl = p.w_global != nullptr ? __ldcg(p.w_global + r.expert[at.a]) : 1.f;
-      float y[kBlocks][2][kSums] = {};   // [block of tokens][16 rows]
+      float y[kDown ? 1 : kBlocks][2][kSums] = {};   // [block of tokens][16 rows]
+      // down: of the blocks behind the first, which few experts have (in local memory)
+      float more[kDown && kBlocks > 1 ? kBlocks - 1 : 1][2][kSums];
+      if constexpr (kDown && kBlocks > 1) {
+        if (tokens > kTokens) {
+#pragma unroll
+          for (int i = 0; i < (kBlocks - 1) * 2 * kSums; ++i) more[i / (2 * kSums)][i / kSums % 2][i % kSums] = 0.f;
+        }
+      }
       for (int ch = 0; ch < p.chunks; ++ch, ++count) {
         const int c0 = ch * kChunkSteps;
         const int s0 = min(c0 + kPer * w, steps), s1 = min(s0 + kPer, steps);
@@ -541,13 +549,9 @@ W4_DEV void layer(const Params& p, Common& c) {
             block(0, [&](int m, int h, float a, float f) { y[0][m][h] = fmaf(a, f, y[0][m][h]); });
             if constexpr (kBlocks > 1) {
 #pragma unroll 1
-              for (int nb = 1; kTokens * nb < tokens; ++nb) {   // few experts have more
+              for (int nb = 1; kTokens * nb < tokens; ++nb) {
                 fetch(nb);
-                block(nb, [&](int m, int h, float a, float f) {
-#pragma unroll
-                  for (int j = 1; j < kBlocks; ++j)
-                    if (j == nb) y[j][m][h] = fmaf(a, f, y[j][m][h]);
-                });
+                block(nb, [&](int m, int h, float a, float f) { more[nb - 1][m][h] = fmaf(a, f, more[nb - 1][m][h]); });
               }
             }
           }
@@ -580,16 +584,15 @@ W4_DEV void layer(const Params& p, Common& c) {
         if (++slot == p.slots) slot = 0, phase ^= 1;
       }
       if (++scale_at == p.scale_slots) scale_at = 0;
-#pragma unroll
-      for (int nb = 0; nb < kBlocks; ++nb) {
-        if (kTokens * nb >= tokens) break;
+      // the warps' sums z of a block of tokens meet
+      auto meet = [&](int nb, const float (&z)[2][kSums]) {
         float (*red)[2][32][4] = c.red[group][turn];   // two in turn, so that one meeting is enough
         turn ^= 1;
         if constexpr (kDown) {
-          *reinterpret_cast<float4*>(red[w][0][lane]) = make_float4(y[nb][0][0], y[nb][0][1], y[nb][1][0], y[nb][1][1]);
+          *reinterpret_cast<float4*>(red[w][0][lane]) = make_float4(z[0][0], z[0][1], z[1][0], z[1][1]);
         } else {
 #pragma unroll
-          for (int m = 0; m < 2; ++m) *reinterpret_cast<float4*>(red[w][m][lane]) = make_float4(y[nb][m][0], y[nb][m][1], y[nb][m][2], y[nb][m][3]);
+          for (int m = 0; m < 2; ++m) *reinterpret_cast<float4*>(red[w][m][lane]) = make_float4(z[m][0], z[m][1], z[m][2], z[m][3]);
         }
         group_sync(group);
         auto sum = [&](int m, int l, int j) { return ((red[0][m][l][j] + red[1][m][l][j]) + red[2][m][l][j]) + red[3][m][l][j]; };
@@ -624,6 +627,19 @@ W4_DEV void layer(const Params& p, Common& c) {
             to[0] = hi, to[p.I] = lo;
             if ((i & 7) == 0) p.act_exp[static_cast<size_t>(first + n) * (p.I / 8) + (at.n0 + i) / 8] = static_cast<uint8_t>(ex);
           }
+        }
+      };
+      if constexpr (kDown) {
+        meet(0, y[0]);
+        if constexpr (kBlocks > 1) {
+#pragma unroll 1
+          for (int nb = 1; kTokens * nb < tokens; ++nb) meet(nb, more[nb - 1]);
+        }
+      } else {
+#pragma unroll
+        for (int nb = 0; nb < kBlocks; ++nb) {
+          if (kTokens * nb >= tokens) break;
+          meet(nb, y[nb]);
         }
       }
     }
