@@ -17,11 +17,12 @@
 // weights into operand registers. A word is 8 consecutive columns of a row, and a lane's
 // words are its operands as they lie: columns 8 c .. 8 c + 7 of 32 belong to lane c of a
 // quad for weights and activations alike, so that no shuffle is needed. int4 codes become
-// q - 8 by (q | 1024) - 1032 (exact in fp16, four words of five steps), e2m1 codes by
-// the
-// conversion instruction (byte permutations of a table and the sign apart, 15 instructions a word, take
-// 129 us for 16 tokens in nvfp4 where this takes 103); nvfp4 block scales are multiplied in (six mantissa bits, exact), the others scale fp32 sums of their group. A piece's scales come with it where rows of them are
-// whole 16 bytes for TMA, else a unit's with its first piece.
+// q - 8 by (q | 1024) - 1032 (exact in fp16, four words of five steps), e2m1 codes by the
+// conversion instruction (byte permutations of a table and the sign apart, 15 instructions a word, took
+// 129 us for 16 tokens in nvfp4 where this took 103); nvfp4 block scales are multiplied in (six
+// mantissa bits, exact), the others scale fp32 sums of their group. A piece's scales come with it where
+// rows of them are whole 16 bytes for TMA, else a unit's with its first piece (16 tokens in nvfp4 103 us by the
+// piece, 120 by the unit).
 //
 // Activations are fp16 numbers times a power of two: x_t with its largest magnitude in
 // [2^14, 2^15) (a bf16 keeps all its bits down to 2^-29 of that), a_te the same over every
@@ -30,12 +31,14 @@
 // Those exponents differ along k; a warp brings its columns to the
 // largest of them before it multiplies, which takes bits only from what lies below 2^-29 of it.
 //
-// One token, 64 experts of 2048 x 1408 in int4, 8 chosen (34.6 MB, 5.3 us at the copy rate): 23 us,
+// One token, 64 experts of 2048 x 1408 in int4, 8 chosen (34.6 MB, 5.3 us at the copy rate): 24 us,
 // of which 4 go to the choice of experts and 4 to the second kernel's start, most of the rest to
 // instructions: some 26 for a lane's word of weights, 14 of them the widening and the product, at
-// half an instruction a cycle. 8 tokens (42 experts): 70 us, 16 tokens: 101. (Measured beside it: a
+// half an instruction a cycle. 8 tokens (42 experts): 71 us, 16 tokens: 101; in nvfp4 26, 80 and 107 to 115 (280 MB,
+// 41 us), in mxfp4 24.5 for one and 102 for 16. (Measured beside it: a
 // second CTA on an SM, with two groups or 64 registers a thread, 34 and 42 us where this took 26;
-// a last unit cut among the groups, the same, as the instructions remain.)
+// a last unit cut among the groups, the same, as the instructions remain; the next piece's activations
+// fetched behind this one's products, the same.)
 //
 // Every sum has a fixed order: outputs are the same every time.
 #pragma once

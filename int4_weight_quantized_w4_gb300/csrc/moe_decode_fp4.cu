@@ -4,7 +4,7 @@
 // needs the activations as 4-bit floats too, sums of several with scales per block. Five terms left 2^-13 of a
 // block's largest magnitude, so that a column of 4096 cost the numbers of size 1 beside it 2 %, and nvfp4's
 // scales lost all below 2^-17 of a row's. Its times, and this form's: 5 tokens, 96 experts of 1024 x 704 in mxfp4
-// 25.6 us, 23.1; 16 tokens, 64 of 2048 x 1408 in nvfp4 104.7, 104; 8 tokens, 32 of 4096 x 1536 in mxfp4 76, 95.)
+// 25.6 us, 24.3; 16 tokens, 64 of 2048 x 1408 in nvfp4 104.7, 107 to 115; 8 tokens, 32 of 4096 x 1536 in mxfp4 76, 98.)
 #include "moe_decode.cuh"
 
 namespace w4 {
